@@ -80,6 +80,8 @@ typedef enum pkv_status {
 #define PKV_DEV_TABLE_RANGE   0x20u /* a position past the end of its table row */
 #define PKV_DEV_PREFIX        0x40u /* cascade: a table that does not begin with the
                                        shared prefix blocks */
+#define PKV_DEV_QUERY_RANGE   0x80u /* chunk attention: cu_q_lens decreases, or leaves
+                                       [0, num_tokens] */
 
 /* Shape of one layer's paged KV cache. */
 typedef struct pkv_cache_desc {
@@ -176,6 +178,64 @@ int pkv_kv_append_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
 int pkv_copy_blocks_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
                          const int32_t *src, const int32_t *dst, int32_t num_pairs,
                          pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_rope_append -- rotary positions of the new tokens, fused with the
+ * append.  For token t at position m = positions[t] and pair i <
+ * rotary_dim / 2 of a head's rotary part (its elements rotary_offset ..
+ * rotary_offset + rotary_dim - 1), with angle = m * inv_freq[i]:
+ *     (x1, x2) -> amplitude * (x1 cos(angle) - x2 sin(angle),
+ *                              x2 cos(angle) + x1 sin(angle))
+ * where (x1, x2) are elements i and i + rotary_dim / 2 of the part (half
+ * layout, the default), or 2i and 2i + 1 (PKV_ROPE_INTERLEAVED).  The other
+ * elements pass through.  Every query head of q [T][num_q_heads][head_dim_k]
+ * (bf16) goes to q_out (bf16, which may be q itself; fp32 with
+ * PKV_ROPE_Q_FP32, as the decode calls take it); every rotated key row of
+ * k_new and every (unrotated) value row of v_new goes to the token's slot of
+ * the pools, as pkv_kv_append places them.  Arithmetic is fp32, each output
+ * rounded once; the angle keeps its fraction of a turn exactly to
+ * m * 2^-53 turns, so far positions lose nothing.
+ *  - inv_freq: [rotary_dim / 2] binary64 on the device, radians per token
+ *    (pkv_rope_frequencies makes the usual tables).
+ *  - rotary_dim even, 2 .. head_dim_k; vectors of 16 bytes rotate when
+ *    rotary_dim is a multiple of 16 (interleaved: 8) and rotary_offset of 8,
+ *    else an element-wise form runs.
+ *  - A negative position is padding: that token is skipped, its q_out rows
+ *    left as they were.  A negative slot writes no key or value; a slot past
+ *    the pool sets PKV_DEV_SLOT (the token's q_out is written in both cases).
+ *    Two tokens with the same slot race.
+ *  - v_pool and v_new both NULL: values inside the keys, as pkv_kv_append.
+ *  - num_q_heads + num_kv_heads <= 4096 (PKV_ERR_SHAPE).
+ * pkv_rope_append_e4m3: the same into E4M3 pools; the rotated key is
+ * quantised as pkv_kv_append_e4m3 quantises, from fp32 (no bf16 in between).
+ *
+ * pkv_rope_frequencies (host): inv_freq[i] for a base theta, i <
+ * rotary_dim / 2.  With f_i = theta^(-2i / rotary_dim):
+ *   original_len == 0: inv_freq[i] = f_i / factor (factor 1: plain; above 1:
+ *     positions interpolated).
+ *   original_len > 0: by parts, for a context `factor` times original_len.  A
+ *     pair that makes at least high_turns turns within original_len keeps
+ *     f_i, one of low_turns or fewer gets f_i / factor, linear in the turns
+ *     between (0 < low_turns < high_turns).
+ * ------------------------------------------------------------------------- */
+#define PKV_ROPE_INTERLEAVED 0x1
+#define PKV_ROPE_Q_FP32 0x2
+
+int pkv_rope_frequencies(int32_t rotary_dim, double theta, double factor, double original_len,
+                         double low_turns, double high_turns, double *inv_freq);
+
+int pkv_rope_append(const pkv_cache_desc *cache, void *k_pool, void *v_pool, const void *q,
+                    int32_t num_q_heads, const void *k_new, const void *v_new,
+                    const int64_t *positions, const int64_t *slot_mapping, int64_t num_tokens,
+                    const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
+                    float amplitude, int32_t flags, void *q_out, pkv_stream_t stream);
+
+int pkv_rope_append_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool, const void *q,
+                         int32_t num_q_heads, const void *k_new, const void *v_new,
+                         const float *k_scale, const float *v_scale, const int64_t *positions,
+                         const int64_t *slot_mapping, int64_t num_tokens, const double *inv_freq,
+                         int32_t rotary_dim, int32_t rotary_offset, float amplitude,
+                         int32_t flags, void *q_out, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * pkv_interleave_slot_mapping -- [DCP] interleaved assignment: the KV of token i
@@ -486,6 +546,77 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
                                   const int32_t *seq_lens, float scale, int32_t prefix_splits,
                                   int32_t suffix_splits, void *workspace, size_t workspace_bytes,
                                   float *out, float *lse, int32_t flags, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_chunk_attn -- attention of chunks of new tokens over the paged
+ * cache: prompts, the next chunk of a long prompt, or a batch that mixes
+ * both with single-token sequences.  [KVB] counts the prompt's step beside
+ * the decode steps; [PA] continuous batching runs them together.
+ * Sequence b brings n_b = cu_q_lens[b + 1] - cu_q_lens[b] >= 0 new tokens, the
+ * last n_b of its seq_lens[b] stored ones (already appended); its token i is
+ * row t = cu_q_lens[b] + i of q and sits at position p = seq_lens[b] - n_b + i.
+ * It attends to the stored positions j with
+ *     0 <= j <= p  and  (window == 0 or j > p - window or j < sink_tokens):
+ * causally, within a sliding window of the last `window` positions (its own
+ * among them) and the first sink_tokens positions, which stay visible.  Over
+ * those, with K_j, V_j and the KV head of h as in pkv_paged_decode_attn:
+ *     s_j = scale * sum_d q[t][h][d] * K_j[d]
+ *     out[t][h][:] = sum_j e^{s_j} V_j / sum_j e^{s_j},  lse[t][h] = ln sum_j e^{s_j}
+ * q [num_tokens][num_q_heads][head_dim_k] bf16, cu_q_lens [batch + 1] int32,
+ * out [num_tokens][num_q_heads][head_dim_v] bf16, lse [num_tokens][num_q_heads]
+ * fp32 (or NULL: not wanted).  scale > 0 and finite; window >= 0 (0: none);
+ * sink_tokens >= 0 (without a window it changes nothing).  Probabilities are
+ * rounded to bf16 for the value product (E4M3 caches: to two E4M3 terms, as
+ * the query is), sums and statistics are fp32, out is rounded once.
+ *  - Rows of q outside [cu_q_lens[0], cu_q_lens[batch]) are padding: their out
+ *    and lse are left as they were.
+ *  - Table entries of blocks that no new token sees (between the sinks and
+ *    the window) are not read and may be stale.
+ *  - A sequence with fewer stored than new tokens sets PKV_DEV_SEQ_LEN and its
+ *    rows with p < 0 give out = 0, lse = -inf; so does a seq_len outside
+ *    [0, max_blocks * block_size], which counts as 0.  A table entry outside
+ *    the pool is handled as in pkv_paged_decode_attn.  A cu_q_lens that
+ *    decreases or leaves [0, num_tokens] sets PKV_DEV_QUERY_RANGE; which rows
+ *    are then written is unspecified.
+ *  - What lies past a sequence's end in its last block is never used, whatever
+ *    its bits.  A stored key or value of the sequence itself that is infinite
+ *    or NaN reaches the rows that see it, and may reach rows of the same
+ *    sequence that do not.
+ *  - v_pool NULL: values inside the keys, as pkv_paged_decode_attn.
+ * Head dims 64 or 128 (equal for K and V), query groups up to 128 and
+ * power-of-two block sizes 8..256 (E4M3: head dim 128, 16..256) run on the
+ * tcgen05 tensor cores; other shapes (head dims multiples of 8 up to 1024),
+ * and flags PKV_DECODE_GENERIC or PKV_DECODE_NO_TCGEN05, on CUDA cores.
+ * workspace: at least pkv_chunk_workspace_size(...) bytes (0: may be NULL),
+ * 16-byte aligned, contents on entry do not matter; calls that may overlap
+ * on the GPU need one each.  A row whose kernel gave up on a pipeline wait
+ * (PKV_DEV_TIMEOUT) is NaN.  batch <= 65535, num_tokens * num_q_heads < 2^31.
+ * ------------------------------------------------------------------------- */
+size_t pkv_chunk_workspace_size(const pkv_cache_desc *cache, int64_t num_tokens, int32_t batch,
+                                int32_t num_q_heads, int32_t max_blocks, int32_t flags);
+
+int pkv_paged_chunk_attn(const pkv_cache_desc *cache, const void *q, int64_t num_tokens,
+                         int32_t num_q_heads, const int32_t *cu_q_lens, int32_t batch,
+                         const void *k_pool, const void *v_pool, const int32_t *block_tables,
+                         int32_t max_blocks, const int32_t *seq_lens, float scale,
+                         int32_t window, int32_t sink_tokens, void *workspace,
+                         size_t workspace_bytes, void *out, float *lse, int32_t flags,
+                         pkv_stream_t stream);
+
+/* pkv_paged_chunk_attn over E4M3 pools (the FP8 cache above; its workspace
+ * size is pkv_chunk_workspace_size_e4m3's). */
+size_t pkv_chunk_workspace_size_e4m3(const pkv_cache_desc *cache, int64_t num_tokens,
+                                     int32_t batch, int32_t num_q_heads, int32_t max_blocks,
+                                     int32_t flags);
+
+int pkv_paged_chunk_attn_e4m3(const pkv_cache_desc *cache, const void *q, int64_t num_tokens,
+                              int32_t num_q_heads, const int32_t *cu_q_lens, int32_t batch,
+                              const void *k_pool, const void *v_pool, const float *k_scale,
+                              const float *v_scale, const int32_t *block_tables,
+                              int32_t max_blocks, const int32_t *seq_lens, float scale,
+                              int32_t window, int32_t sink_tokens, void *workspace,
+                              size_t workspace_bytes, void *out, float *lse, int32_t flags,
+                              pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * pkv_lse_merge -- [DCP] decode step, stage 3: correct each partial output

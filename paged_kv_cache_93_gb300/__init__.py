@@ -21,7 +21,8 @@ import torch
 from . import _lib
 from ._lib import (DECODE_GENERIC, DECODE_NO_TCGEN05, DECODE_TEST_WITHHOLD, DEV_BLOCK_ID,
                    DEV_COPY_CONFLICT, DEV_PREFIX, DEV_SEQ_LEN, DEV_SLOT, DEV_TABLE_RANGE,
-                   DEV_TIMEOUT, CacheDesc, PkvError)
+                   DEV_QUERY_RANGE, DEV_TIMEOUT, ROPE_INTERLEAVED, ROPE_Q_FP32, CacheDesc,
+                   PkvError)
 
 __all__ = [
     "CacheDesc", "PkvError", "ValuesInKeys", "cache_desc", "kv_append", "slot_mapping", "copy_blocks",
@@ -30,7 +31,9 @@ __all__ = [
     "paged_decode_attn_multi", "lse_merge", "kv_append_e4m3", "copy_blocks_e4m3",
     "paged_decode_attn_e4m3", "paged_decode_attn_partial_e4m3", "paged_decode_attn_multi_e4m3",
     "paged_decode_attn_cascade",
-    "decode_cascade_splits", "DEV_PREFIX",
+    "decode_cascade_splits", "DEV_PREFIX", "rope_frequencies", "rope_append", "rope_append_e4m3",
+    "chunk_workspace_size", "paged_chunk_attn", "paged_chunk_attn_e4m3", "DEV_QUERY_RANGE",
+    "ROPE_INTERLEAVED", "ROPE_Q_FP32",
     "device_status", "BlockManager", "library_path", "DECODE_GENERIC", "DECODE_NO_TCGEN05",
     "DECODE_TEST_WITHHOLD", "DEV_BLOCK_ID",
     "DEV_SLOT", "DEV_SEQ_LEN", "DEV_COPY_CONFLICT", "DEV_TIMEOUT", "DEV_TABLE_RANGE",
@@ -188,6 +191,95 @@ def copy_blocks_e4m3(k_pool, v_pool, src, dst, stream=None) -> None:
     _check("pkv_copy_blocks_e4m3", lib.pkv_copy_blocks_e4m3(
         ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(src), _ptr(dst), src.numel(),
         _stream(stream)))
+
+
+def rope_frequencies(rotary_dim: int, theta: float = 10000.0, factor: float = 1.0,
+                     original_len: float = 0, low_turns: float = 1.0, high_turns: float = 4.0,
+                     device=None) -> torch.Tensor:
+    """Radians per token of each rotary pair, [rotary_dim / 2] float64:
+    theta^(-2i / rotary_dim), divided by `factor` (positions interpolated), or
+    with original_len > 0 scaled by parts (pairs of at least high_turns turns
+    within original_len keep their frequency, those of low_turns or fewer are
+    divided by `factor`, linear between)."""
+    host = torch.empty(max(0, int(rotary_dim) // 2), dtype=torch.float64)
+    _check("pkv_rope_frequencies", lib.pkv_rope_frequencies(
+        int(rotary_dim), float(theta), float(factor), float(original_len), float(low_turns),
+        float(high_turns), _ptr(host)))
+    return host.to("cuda" if device is None else device)
+
+
+def _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq, interleaved, q_dtype,
+               q_out):
+    """Checks of the rope_append calls -> (q_out, flags)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_new, "k_new", torch.bfloat16, 3)
+    _need(positions, "positions", torch.int64, 1)
+    _need(slots, "slot_mapping", torch.int64, 1)
+    _need(inv_freq, "inv_freq", torch.float64, 1)
+    T = positions.numel()
+    if slots.numel() != T or q.shape[0] != T:
+        raise ValueError("q, positions and slots disagree on the number of tokens")
+    if q.shape[2] != desc.head_dim_k:
+        raise ValueError(f"q must have head dim {desc.head_dim_k}, got {q.shape[2]}")
+    if tuple(k_new.shape) != (T, desc.num_kv_heads, desc.head_dim_k):
+        raise ValueError("k_new must be [tokens, Hkv, Dk] of the cache")
+    if isinstance(v_pool, ValuesInKeys):
+        if v_new is not None:
+            raise ValueError("v_new must be None when the values are inside the keys")
+    else:
+        _need(v_new, "v_new", torch.bfloat16, 3)
+        if tuple(v_new.shape) != (T, desc.num_kv_heads, desc.head_dim_v):
+            raise ValueError("v_new must be [tokens, Hkv, Dv] of the cache")
+    if q_out is None:
+        if q_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"q_dtype must be torch.bfloat16 or torch.float32, got {q_dtype}")
+        q_out = torch.empty(q.shape, dtype=q_dtype, device=q.device)
+    else:
+        if q_out.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"q_out must be torch.bfloat16 or torch.float32, got {q_out.dtype}")
+        _need(q_out, "q_out", q_out.dtype, 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    flags = (ROPE_INTERLEAVED if interleaved else 0) | \
+        (ROPE_Q_FP32 if q_out.dtype == torch.float32 else 0)
+    return q_out, flags
+
+
+def rope_append(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq,
+                interleaved: bool = False, rotary_offset: int = 0, amplitude: float = 1.0,
+                q_dtype: torch.dtype = torch.bfloat16, q_out=None, stream=None):
+    """Rotate q [T, Hq, Dk] and k_new [T, Hkv, Dk] (bf16) by their tokens'
+    positions [T] (int64; negative: padding, skipped) and write k_new and
+    v_new [T, Hkv, Dv] at slots [T] -> the rotated q (bf16, or fp32 as the
+    decode calls take it; q_out may be q itself).  inv_freq: [rotary_dim / 2]
+    float64 radians per token (see rope_frequencies); pairs are the halves of
+    the rotary part, or neighbours with `interleaved`; amplitude multiplies the
+    rotary part."""
+    desc = _bf16_desc(k_pool, v_pool)
+    q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
+                              interleaved, q_dtype, q_out)
+    _check("pkv_rope_append", lib.pkv_rope_append(
+        ctypes.byref(desc), _ptr(k_pool), _v_ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
+        _ptr(v_new), _ptr(positions), _ptr(slots), positions.numel(), _ptr(inv_freq),
+        2 * inv_freq.numel(), int(rotary_offset), float(amplitude), flags, _ptr(q_out),
+        _stream(stream)))
+    return q_out
+
+
+def rope_append_e4m3(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq, k_scale,
+                     v_scale, interleaved: bool = False, rotary_offset: int = 0,
+                     amplitude: float = 1.0, q_dtype: torch.dtype = torch.bfloat16, q_out=None,
+                     stream=None):
+    """rope_append into E4M3 pools (uint8 codes, fp32 scales per KV head)."""
+    desc = _e4m3_desc(k_pool, v_pool, k_scale, v_scale)
+    q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
+                              interleaved, q_dtype, q_out)
+    _check("pkv_rope_append_e4m3", lib.pkv_rope_append_e4m3(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
+        _ptr(v_new), _ptr(k_scale), _ptr(v_scale), _ptr(positions), _ptr(slots),
+        positions.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), int(rotary_offset),
+        float(amplitude), flags, _ptr(q_out), _stream(stream)))
+    return q_out
 
 
 def interleave_slot_mapping(k_pool, v_pool, first_token: int, num_tokens: int, num_parts: int,
@@ -418,6 +510,86 @@ def paged_decode_attn_multi(q, k_pool, v_pool, block_tables, seq_lens, scale: fl
         _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), float(scale), S,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
         int(flags), _stream(stream)))
+    return out, lse
+
+
+def chunk_workspace_size(k_pool, v_pool, num_tokens: int, batch: int, num_q_heads: int,
+                         max_blocks: int, flags: int = 0) -> int:
+    """Workspace bytes of paged_chunk_attn (bf16 pools) or paged_chunk_attn_e4m3."""
+    desc = cache_desc(k_pool, v_pool)
+    size = (lib.pkv_chunk_workspace_size_e4m3 if k_pool.dtype == torch.uint8
+            else lib.pkv_chunk_workspace_size)
+    return int(size(ctypes.byref(desc), num_tokens, batch, num_q_heads, max_blocks, int(flags)))
+
+
+def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out, lse, flags):
+    """Checks of the chunk attention calls -> (workspace, its bytes, out, lse)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    T, Hq, Dk = q.shape
+    B = seq_lens.numel()
+    if Dk != desc.head_dim_k:
+        raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
+    if cu_q_lens.numel() != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("cu_q_lens must have one entry more, block_tables one row per seq_len")
+    if out is None:
+        out = torch.empty(T, Hq, desc.head_dim_v, dtype=torch.bfloat16, device=q.device)
+    else:
+        _need(out, "out", torch.bfloat16, 3)
+        if tuple(out.shape) != (T, Hq, desc.head_dim_v):
+            raise ValueError("out must be [tokens, Hq, Dv]")
+    if lse is None:
+        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+    else:
+        _need(lse, "lse", torch.float32, 2)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError("lse must be [tokens, Hq]")
+    need = int(size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags))
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, ws_bytes, out, lse
+
+
+def paged_chunk_attn(q, cu_q_lens, k_pool, v_pool, block_tables, seq_lens, scale: float,
+                     window: int = 0, sink_tokens: int = 0, workspace=None, out=None, lse=None,
+                     flags: int = 0, stream=None):
+    """Attention of ragged chunks of new tokens over the paged cache.
+
+    q [T, Hq, Dk] bf16 holds the chunks one after another: sequence b's are
+    rows cu_q_lens[b] .. cu_q_lens[b + 1] (int32 [B + 1]), the last tokens of
+    its seq_lens[b] stored ones.  Causal; with window > 0 a token sees the last
+    `window` positions (its own among them) and the first `sink_tokens`.
+    -> (out [T, Hq, Dv] bf16, lse [T, Hq] fp32); rows past the last sequence
+    are left as they were."""
+    desc = _bf16_desc(k_pool, v_pool)
+    workspace, ws_bytes, out, lse = _chunk_args(
+        desc, lib.pkv_chunk_workspace_size, q, cu_q_lens, block_tables, seq_lens, workspace, out,
+        lse, int(flags))
+    _check("pkv_paged_chunk_attn", lib.pkv_paged_chunk_attn(
+        ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
+        _ptr(k_pool), _v_ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+        float(scale), int(window), int(sink_tokens), _ptr(workspace), ws_bytes, _ptr(out),
+        _ptr(lse), int(flags), _stream(stream)))
+    return out, lse
+
+
+def paged_chunk_attn_e4m3(q, cu_q_lens, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
+                          scale: float, window: int = 0, sink_tokens: int = 0, workspace=None,
+                          out=None, lse=None, flags: int = 0, stream=None):
+    """paged_chunk_attn over an E4M3 cache (uint8 code pools, fp32 scales per
+    KV head) -> (out, lse)."""
+    desc = _e4m3_desc(k_pool, v_pool, k_scale, v_scale)
+    workspace, ws_bytes, out, lse = _chunk_args(
+        desc, lib.pkv_chunk_workspace_size_e4m3, q, cu_q_lens, block_tables, seq_lens, workspace,
+        out, lse, int(flags))
+    _check("pkv_paged_chunk_attn_e4m3", lib.pkv_paged_chunk_attn_e4m3(
+        ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
+        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), float(scale), int(window), int(sink_tokens),
+        _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse), int(flags), _stream(stream)))
     return out, lse
 
 

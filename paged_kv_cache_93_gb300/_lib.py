@@ -24,8 +24,11 @@ DEV_COPY_CONFLICT = 0x8
 DEV_TIMEOUT = 0x10
 DEV_TABLE_RANGE = 0x20
 DEV_PREFIX = 0x40
+DEV_QUERY_RANGE = 0x80
 DECODE_GENERIC = 0x1
 DECODE_NO_TCGEN05 = 0x2
+ROPE_INTERLEAVED = 0x1
+ROPE_Q_FP32 = 0x2
 DECODE_TEST_WITHHOLD = 0x100      # test control of the failure path (see pkv.h)
 
 
@@ -38,7 +41,7 @@ class CacheDesc(ctypes.Structure):
 # name -> (restype, argtypes); mirrors include/pkv.h
 _P = ctypes.c_void_p
 _i32, _i64, _u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
-_f32, _sz = ctypes.c_float, ctypes.c_size_t
+_f32, _sz, _f64 = ctypes.c_float, ctypes.c_size_t, ctypes.c_double
 _DESC = ctypes.POINTER(CacheDesc)
 SIGNATURES = {
     "pkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -48,6 +51,18 @@ SIGNATURES = {
     "pkv_copy_blocks": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _i32, _P]),
     "pkv_kv_append_e4m3": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _P, _P, _P, _i64, _P]),
     "pkv_copy_blocks_e4m3": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _i32, _P]),
+    "pkv_rope_frequencies": (ctypes.c_int, [_i32, _f64, _f64, _f64, _f64, _f64, _P]),
+    "pkv_rope_append": (ctypes.c_int, [_DESC, _P, _P, _P, _i32, _P, _P, _P, _P, _i64, _P, _i32,
+                                       _i32, _f32, _i32, _P, _P]),
+    "pkv_rope_append_e4m3": (ctypes.c_int, [_DESC, _P, _P, _P, _i32, _P, _P, _P, _P, _P, _P,
+                                            _i64, _P, _i32, _i32, _f32, _i32, _P, _P]),
+    "pkv_chunk_workspace_size": (_sz, [_DESC, _i64, _i32, _i32, _i32, _i32]),
+    "pkv_chunk_workspace_size_e4m3": (_sz, [_DESC, _i64, _i32, _i32, _i32, _i32]),
+    "pkv_paged_chunk_attn": (ctypes.c_int, [_DESC, _P, _i64, _i32, _P, _i32, _P, _P, _P, _i32, _P,
+                                            _f32, _i32, _i32, _P, _sz, _P, _P, _i32, _P]),
+    "pkv_paged_chunk_attn_e4m3": (ctypes.c_int, [_DESC, _P, _i64, _i32, _P, _i32, _P, _P, _P, _P,
+                                                 _P, _i32, _P, _f32, _i32, _i32, _P, _sz, _P, _P,
+                                                 _i32, _P]),
     "pkv_decode_auto_splits_e4m3": (_i32, [_DESC, _i32, _i32, _i32]),
     "pkv_paged_decode_attn_e4m3": (ctypes.c_int, [_DESC, _P, _i32, _i32, _P, _P, _P, _P, _P,
                                                   _i32, _P, _f32, _i32, _P, _sz, _P, _P, _i32,

@@ -1,0 +1,122 @@
+// chunk.cu -- C ABI entry points of the attention of ragged chunks of new
+// tokens: argument checks and kernel choice.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "pkv.h"
+#include "pkv_host.h"
+
+namespace pkv {
+namespace {
+
+// The host checks both entry points share; fills all of `a` but the scales.
+// *done: nothing to launch.
+int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64_t num_tokens,
+            int32_t hq, const int32_t *cu_q_lens, int32_t batch, const void *k_pool,
+            const void *v_pool, const int32_t *block_tables, int32_t max_blocks,
+            const int32_t *seq_lens, float scale, int32_t window, int32_t sink_tokens, void *out,
+            float *lse, int32_t flags, cudaStream_t stream, bool *done) {
+    *done = false;
+    if (!c || num_tokens < 0 || batch < 0 || hq <= 0 || max_blocks < 0 || window < 0 ||
+        sink_tokens < 0 || !(scale > 0.f) || !std::isfinite(scale) ||
+        (flags & ~(PKV_DECODE_GENERIC | PKV_DECODE_NO_TCGEN05)) != 0)
+        return PKV_ERR_INVALID_ARG;
+    if (c->num_blocks <= 0 || c->block_size < 1 || c->block_size > 256 || c->num_kv_heads <= 0 ||
+        c->head_dim_k <= 0 || c->head_dim_v <= 0)
+        return PKV_ERR_INVALID_ARG;
+    if (hq % c->num_kv_heads != 0 || c->head_dim_k % 8 != 0 || c->head_dim_v % 8 != 0 ||
+        c->head_dim_k > 1024 || c->head_dim_v > 1024 || batch > 65535 || hq > 65535 ||
+        num_tokens * hq >= (int64_t(1) << 31))
+        return PKV_ERR_SHAPE;
+    if (num_tokens == 0 || batch == 0) {
+        *done = true;
+        return PKV_OK;
+    }
+    if (!q || !cu_q_lens || !k_pool || !block_tables || !seq_lens || !out || (e4 && !v_pool))
+        return PKV_ERR_INVALID_ARG;
+    if (!v_pool && c->head_dim_v > c->head_dim_k) return PKV_ERR_SHAPE;   // values inside the keys
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || (v_pool && !aligned16(v_pool)))
+        return PKV_ERR_ALIGNMENT;
+    a.status = status_word();
+    if (!a.status) return PKV_ERR_CUDA;
+    a.cache = *c;
+    a.q = q;
+    a.num_tokens = int32_t(num_tokens);
+    a.batch = batch;
+    a.num_q_heads = hq;
+    a.cu_q_lens = cu_q_lens;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool ? v_pool : k_pool;
+    a.v_stride = v_pool ? c->head_dim_v : c->head_dim_k;
+    a.block_tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.seq_lens = seq_lens;
+    a.scale = scale;
+    a.window = window;
+    a.sinks = sink_tokens;
+    a.out = out;
+    a.lse = lse;
+    a.stream = stream;
+    return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" size_t pkv_chunk_workspace_size(const pkv_cache_desc *cache, int64_t num_tokens,
+                                           int32_t batch, int32_t num_q_heads, int32_t max_blocks,
+                                           int32_t flags) {
+    (void)cache, (void)num_tokens, (void)batch, (void)num_q_heads, (void)max_blocks, (void)flags;
+    return 0;
+}
+
+extern "C" size_t pkv_chunk_workspace_size_e4m3(const pkv_cache_desc *cache, int64_t num_tokens,
+                                                int32_t batch, int32_t num_q_heads,
+                                                int32_t max_blocks, int32_t flags) {
+    (void)cache, (void)num_tokens, (void)batch, (void)num_q_heads, (void)max_blocks, (void)flags;
+    return 0;
+}
+
+extern "C" int pkv_paged_chunk_attn(const pkv_cache_desc *cache, const void *q,
+                                    int64_t num_tokens, int32_t num_q_heads,
+                                    const int32_t *cu_q_lens, int32_t batch, const void *k_pool,
+                                    const void *v_pool, const int32_t *block_tables,
+                                    int32_t max_blocks, const int32_t *seq_lens, float scale,
+                                    int32_t window, int32_t sink_tokens, void *workspace,
+                                    size_t workspace_bytes, void *out, float *lse, int32_t flags,
+                                    pkv_stream_t stream) {
+    (void)workspace, (void)workspace_bytes;
+    ChunkArgs a = {};
+    bool done;
+    const int rc = prepare(a, false, cache, q, num_tokens, num_q_heads, cu_q_lens, batch, k_pool,
+                           v_pool, block_tables, max_blocks, seq_lens, scale, window, sink_tokens,
+                           out, lse, flags, reinterpret_cast<cudaStream_t>(stream), &done);
+    if (rc != PKV_OK || done) return rc;
+    return launch_chunk_generic(a);
+}
+
+extern "C" int pkv_paged_chunk_attn_e4m3(const pkv_cache_desc *cache, const void *q,
+                                         int64_t num_tokens, int32_t num_q_heads,
+                                         const int32_t *cu_q_lens, int32_t batch,
+                                         const void *k_pool, const void *v_pool,
+                                         const float *k_scale, const float *v_scale,
+                                         const int32_t *block_tables, int32_t max_blocks,
+                                         const int32_t *seq_lens, float scale, int32_t window,
+                                         int32_t sink_tokens, void *workspace,
+                                         size_t workspace_bytes, void *out, float *lse,
+                                         int32_t flags, pkv_stream_t stream) {
+    (void)workspace, (void)workspace_bytes;
+    ChunkArgs a = {};
+    bool done;
+    const int rc = prepare(a, true, cache, q, num_tokens, num_q_heads, cu_q_lens, batch, k_pool,
+                           v_pool, block_tables, max_blocks, seq_lens, scale, window, sink_tokens,
+                           out, lse, flags, reinterpret_cast<cudaStream_t>(stream), &done);
+    if (rc != PKV_OK || done) return rc;
+    if (!k_scale || !v_scale) return PKV_ERR_INVALID_ARG;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    return launch_chunk_generic_e4m3(a);
+}

@@ -152,6 +152,31 @@ int run_decode_split_kernel(const DecodeArgs &a, int32_t flags);
 int launch_decode_generic(const DecodeArgs &a);
 // The same over E4M3 pools (a.k_scale, a.v_scale set).
 int launch_decode_generic_e4m3(const DecodeArgs &a);
+// Attention of ragged chunks of new tokens (pkv_paged_chunk_attn).  Arguments
+// are already validated.
+struct ChunkArgs {
+    pkv_cache_desc cache;
+    const void *q;                       // bf16 [num_tokens][num_q_heads][head_dim_k]
+    int32_t num_tokens, batch, num_q_heads;
+    const int32_t *cu_q_lens;
+    const void *k_pool, *v_pool;
+    const int32_t *block_tables;
+    int32_t max_blocks;
+    const int32_t *seq_lens;
+    float scale;
+    int32_t window, sinks;
+    void *out;                           // bf16
+    float *lse;                          // may be nullptr
+    uint32_t *status;
+    cudaStream_t stream;
+    // elements from one V row to the next (head_dim_k when the values are
+    // inside the keys; v_pool then points at the K pool)
+    int32_t v_stride;
+    const float *k_scale, *v_scale;      // E4M3 pools only
+};
+int launch_chunk_generic(const ChunkArgs &a);
+int launch_chunk_generic_e4m3(const ChunkArgs &a);
+
 int launch_lse_merge(int32_t num_parts, const float *out_part, const float *lse_part,
                      int64_t rows, int32_t head_dim_v, float *out, float *lse,
                      cudaStream_t stream);
