@@ -590,7 +590,7 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  * workspace: at least pkv_chunk_workspace_size(...) bytes (0: may be NULL),
  * 16-byte aligned, contents on entry do not matter; calls that may overlap
  * on the GPU need one each.  A row whose kernel gave up on a pipeline wait
- * (PKV_DEV_TIMEOUT) is NaN.  batch <= 65535, num_tokens * num_q_heads < 2^31.
+ * (PKV_DEV_TIMEOUT) is NaN.  batch <= 65535, num_tokens * num_q_heads < 2^29.
  * ------------------------------------------------------------------------- */
 size_t pkv_chunk_workspace_size(const pkv_cache_desc *cache, int64_t num_tokens, int32_t batch,
                                 int32_t num_q_heads, int32_t max_blocks, int32_t flags);

@@ -10,6 +10,39 @@
 namespace pkv {
 namespace {
 
+// Whether a call of this shape runs on the tensor cores.
+bool on_tensor_cores(const pkv_cache_desc &c, int32_t hq, int32_t max_blocks, int32_t flags,
+                     bool e4, bool values_in_keys) {
+    return flags == 0 && !values_in_keys && chunk_tc_supports(c, hq, max_blocks, e4);
+}
+
+size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch, int32_t hq,
+                      int32_t max_blocks, int32_t flags, bool e4) {
+    if (!c || num_tokens <= 0 || batch <= 0 || hq <= 0 || max_blocks < 0 ||
+        c->num_kv_heads <= 0 || hq % c->num_kv_heads != 0 || c->num_blocks <= 0 ||
+        num_tokens * hq >= (int64_t(1) << 29) ||
+        !on_tensor_cores(*c, hq, max_blocks, flags, e4, false))
+        return 0;
+    return chunk_tc_workspace(*c, num_tokens, batch, hq, max_blocks);
+}
+
+// Runs a checked call.
+int run(ChunkArgs &a, bool e4, bool values_in_keys, void *workspace, size_t workspace_bytes,
+        int32_t flags) {
+    const bool tc = on_tensor_cores(a.cache, a.num_q_heads, a.max_blocks, flags, e4,
+                                    values_in_keys);
+    if (tc) {
+        const size_t need =
+            chunk_tc_workspace(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks);
+        if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned16(workspace)) return PKV_ERR_ALIGNMENT;
+    }
+    a.status = status_word();
+    if (!a.status) return PKV_ERR_CUDA;
+    if (tc) return launch_chunk_tc(a, workspace);
+    return e4 ? launch_chunk_generic_e4m3(a) : launch_chunk_generic(a);
+}
+
 // The host checks both entry points share; fills all of `a` but the scales.
 // *done: nothing to launch.
 int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64_t num_tokens,
@@ -27,7 +60,7 @@ int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64
         return PKV_ERR_INVALID_ARG;
     if (hq % c->num_kv_heads != 0 || c->head_dim_k % 8 != 0 || c->head_dim_v % 8 != 0 ||
         c->head_dim_k > 1024 || c->head_dim_v > 1024 || batch > 65535 || hq > 65535 ||
-        num_tokens * hq >= (int64_t(1) << 31))
+        num_tokens * hq >= (int64_t(1) << 29))
         return PKV_ERR_SHAPE;
     if (num_tokens == 0 || batch == 0) {
         *done = true;
@@ -38,8 +71,6 @@ int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64
     if (!v_pool && c->head_dim_v > c->head_dim_k) return PKV_ERR_SHAPE;   // values inside the keys
     if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || (v_pool && !aligned16(v_pool)))
         return PKV_ERR_ALIGNMENT;
-    a.status = status_word();
-    if (!a.status) return PKV_ERR_CUDA;
     a.cache = *c;
     a.q = q;
     a.num_tokens = int32_t(num_tokens);
@@ -69,15 +100,13 @@ using namespace pkv;
 extern "C" size_t pkv_chunk_workspace_size(const pkv_cache_desc *cache, int64_t num_tokens,
                                            int32_t batch, int32_t num_q_heads, int32_t max_blocks,
                                            int32_t flags) {
-    (void)cache, (void)num_tokens, (void)batch, (void)num_q_heads, (void)max_blocks, (void)flags;
-    return 0;
+    return workspace_size(cache, num_tokens, batch, num_q_heads, max_blocks, flags, false);
 }
 
 extern "C" size_t pkv_chunk_workspace_size_e4m3(const pkv_cache_desc *cache, int64_t num_tokens,
                                                 int32_t batch, int32_t num_q_heads,
                                                 int32_t max_blocks, int32_t flags) {
-    (void)cache, (void)num_tokens, (void)batch, (void)num_q_heads, (void)max_blocks, (void)flags;
-    return 0;
+    return workspace_size(cache, num_tokens, batch, num_q_heads, max_blocks, flags, true);
 }
 
 extern "C" int pkv_paged_chunk_attn(const pkv_cache_desc *cache, const void *q,
@@ -88,14 +117,13 @@ extern "C" int pkv_paged_chunk_attn(const pkv_cache_desc *cache, const void *q,
                                     int32_t window, int32_t sink_tokens, void *workspace,
                                     size_t workspace_bytes, void *out, float *lse, int32_t flags,
                                     pkv_stream_t stream) {
-    (void)workspace, (void)workspace_bytes;
     ChunkArgs a = {};
     bool done;
     const int rc = prepare(a, false, cache, q, num_tokens, num_q_heads, cu_q_lens, batch, k_pool,
                            v_pool, block_tables, max_blocks, seq_lens, scale, window, sink_tokens,
                            out, lse, flags, reinterpret_cast<cudaStream_t>(stream), &done);
     if (rc != PKV_OK || done) return rc;
-    return launch_chunk_generic(a);
+    return run(a, false, !v_pool, workspace, workspace_bytes, flags);
 }
 
 extern "C" int pkv_paged_chunk_attn_e4m3(const pkv_cache_desc *cache, const void *q,
@@ -108,7 +136,6 @@ extern "C" int pkv_paged_chunk_attn_e4m3(const pkv_cache_desc *cache, const void
                                          int32_t sink_tokens, void *workspace,
                                          size_t workspace_bytes, void *out, float *lse,
                                          int32_t flags, pkv_stream_t stream) {
-    (void)workspace, (void)workspace_bytes;
     ChunkArgs a = {};
     bool done;
     const int rc = prepare(a, true, cache, q, num_tokens, num_q_heads, cu_q_lens, batch, k_pool,
@@ -118,5 +145,5 @@ extern "C" int pkv_paged_chunk_attn_e4m3(const pkv_cache_desc *cache, const void
     if (!k_scale || !v_scale) return PKV_ERR_INVALID_ARG;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    return launch_chunk_generic_e4m3(a);
+    return run(a, true, false, workspace, workspace_bytes, flags);
 }

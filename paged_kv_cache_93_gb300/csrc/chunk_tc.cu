@@ -1,0 +1,1219 @@
+// chunk_tc.cu -- attention of ragged chunks of new tokens over the paged cache
+// on the 5th-generation tensor cores of sm_103a: bf16 caches with head dims 64
+// or 128, E4M3 caches with head dim 128.
+//
+// The rows of one KV head -- (token, query head of the group) pairs, token
+// major -- are packed into tiles of 128 (tokens_per_tile = 128 / group, so an odd
+// group wastes the remainder).  With m the running row maximum,
+//   S[128 rows x 128 keys] = Q_tile . K_tile^T             (tcgen05, fp32 in TMEM)
+//   P = 2^((S - m) scale log2 e), l += row sums of P       (CUDA cores, one thread a row)
+//   O[128 rows x D]       += P . V_tile                    (tcgen05, P read from TMEM)
+// and out = O / l, lse = m scale + ln l.  P is rounded to bf16 for the second
+// product (its sum is taken before the rounding, in fp32): one bf16 term is
+// what the bf16 output resolves.  E4M3 caches: Q and P go as two E4M3 terms
+// each, the second the rounding residual of the first (bf16 queries fit two
+// terms exactly; P keeps 2^-8 relative and 2^-17 of the row's largest), so the
+// stored codes feed the tensor cores as they are.
+//
+// Work item = (block of up to 2 tiles' tokens of a sequence, KV head, run of
+// key tiles), made by plan_kernel:
+//  - a pair item has two row tiles A and B that read the same keys: while the
+//    tensor cores work for one, the CUDA cores take the softmax of the other;
+//  - a block of at most one tile's tokens is a split item: A and B are the
+//    same rows over the first and second half of the item's key tiles.
+// Long runs of keys are cut into items of near-equal length when that
+// shortens the whole (few rows over a long context); their partial (O / l, lse)
+// go to the workspace and chunk_merge_kernel joins them.
+//
+// Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
+// warps 4-7 of B, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
+// S_B O_A O_B, P over S.  The MMAs of one thread run in order, so S may be
+// overwritten by the next score product once the value product that reads P
+// there is issued.  A row's m rises only when a score exceeds it by more than
+// kSlack (log2): then that warp rescales its rows of O in TMEM.  Every wait is
+// bounded.
+//
+// Keys are walked in absolute 128-key tiles.  Under a window the tiles
+// between the sinks and the first row's window are skipped; in a tile only
+// the blocks that some row of the item sees are copied, and the value rows of
+// keys no row sees are zeroed in shared memory, so stale bits (0 * NaN) never
+// reach O.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "pkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_math.cuh"
+#include "pkv_pipeline.cuh"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kRows = 128;               // query rows per tile (TMEM lanes)
+constexpr int kKeys = 128;               // keys per tile
+constexpr int kThreads = 384;             // three warp groups
+// Registers a thread: launched with 168 (384 x 168 = 64,512), the softmax
+// groups then take 216, the issuing group keeps 72 (256 x 216 + 128 x 72).
+constexpr int kSoftRegs = 216, kIssueRegs = 72;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D, bool E4>
+struct Cfg {
+    static_assert(D == 64 || D == 128, "head dims of one or two 128-byte column blocks");
+    static_assert(!E4 || D == 128, "E4M3 rows fill a 128-byte swizzle row");
+    static constexpr int kElem = E4 ? 1 : 2;
+    static constexpr int kTerms = E4 ? 2 : 1;                       // of Q and of P
+    static constexpr uint32_t kHalfTile = kRows * 128;              // [128 rows][128 B]
+    static constexpr uint32_t kQTile = E4 ? 2 * kHalfTile : kRows * D * 2;
+    static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
+    static constexpr int kStages = kStage == 32768 ? 5 : 10;
+    static constexpr uint32_t kOffQ = 1024;
+    static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
+    static constexpr uint32_t kSmem = 1024 + kOffRing + kStages * kStage;
+    // The running maximum may be exceeded by 2^kSlack; E4M3 probabilities are
+    // kept 2^kShift larger, so that their second term's smallest step (2^-9)
+    // is 2^-16 of the row's largest (2^kShift .. 2^(kShift + kSlack) <= 448).
+    static constexpr float kSlack = E4 ? 1.f : 8.f;
+    static constexpr float kShift = E4 ? 7.f : 0.f;
+    static constexpr uint32_t kIdS = E4 ? tc::idesc_e4m3_f32(kRows, kKeys, 0, 0)
+                                        : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
+    static constexpr uint32_t kIdO = E4 ? tc::idesc_e4m3_f32(kRows, D, 0, 1)
+                                        : tc::idesc_bf16_f32(kRows, D, 0, 1);
+};
+
+// mbarrier slots
+constexpr int kBarFull = 0;              // + stage (at most 10)
+constexpr int kBarEmpty = 10;            // + stage
+constexpr int kBarQFull = 20;
+constexpr int kBarQEmpty = 21;           // commit: the item's score products are done
+constexpr int kBarSFull = 22;            // + half: scores written (commit)
+constexpr int kBarPFull = 24;            // + half: probabilities written (128 arrivals)
+constexpr int kBarPvDone = 26;           // + half: value product done (commit)
+constexpr int kBarOEmpty = 28;           // + half: O read out (128 arrivals)
+constexpr int kBarDrain = 30;
+constexpr uint32_t kOffSlot = 31 * 8;
+constexpr uint32_t kOffFlag = kOffSlot + 4;
+
+struct __align__(16) Item {
+    int32_t b, qrow, pos, ntok;          // sequence; row of q and position of its first token
+    int32_t v0, na, nb, prow;            // first key tile, tiles of A and B; partial row or -1
+    int32_t gstride, split, pad0, pad1;  // partial rows per KV head
+};
+struct __align__(16) Merge {
+    int32_t qrow, ntok, prow, count;     // tokens; first partial row; partials
+};
+struct Plan {                            // device pointers into the workspace
+    int32_t *header;                     // units, merges
+    Item *items;
+    Merge *merges;
+    int4 *blocks;                        // per query block: sequence, first token, tiles, tokens
+    int32_t *first;                      // [batch + 1] query blocks before a sequence
+    float *o_part, *lse_part;            // [partial rows][D], [partial rows]
+    int32_t max_units, max_rows;
+};
+
+struct Shape {
+    int32_t group, tokens_per_tile;
+};
+
+// The key tiles a query block sees: virtual tiles 0 .. count - 1, of which
+// the first `sink_tiles` are tiles 0.., the others shifted by `gap`.
+struct Tiles {
+    int32_t count, sink_tiles, gap, lo;  // lo: first key in the window of the first token
+};
+__device__ __forceinline__ Tiles tiles_of(int32_t pos, int32_t ntok, int32_t window,
+                                          int32_t sinks) {
+    Tiles t;
+    const int32_t last = pos + ntok - 1;
+    const int32_t end = last < 0 ? 0 : last / kKeys + 1;
+    t.lo = window > 0 ? max(0, pos - window + 1) : 0;
+    const int32_t w0 = t.lo / kKeys;
+    t.sink_tiles = min((sinks + kKeys - 1) / kKeys, w0);
+    t.gap = w0 - t.sink_tiles;
+    t.count = max(0, end - t.gap);
+    return t;
+}
+
+// ------------------------------------------------------------------- the plan
+constexpr int kPlanThreads = 1024;
+
+// Inclusive scan over the CTA's 1024 threads; `total` gets the sum.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warp_sums, int64_t &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    total = warp_sums[31];
+    return x + (warp ? warp_sums[warp - 1] : 0);
+}
+
+// Steps of an item: a pair item takes one key tile a step, a split item two.
+__device__ __forceinline__ int32_t steps_of(const int4 &q, int32_t tpt) {
+    return q.w <= tpt ? (q.z + 1) >> 1 : q.z;
+}
+
+// One CTA: query blocks of every sequence, the items' length, the item list.
+// Item lengths: with C steps an item, block i of steps_i steps becomes
+// ceil(steps_i / C) items of near-equal length.  Of 32 values of C (the
+// longest block's fractions and the even share's multiples) the one with the
+// least estimated time is taken: the smaller of two bounds on `ctas` CTAs,
+// waves of the longest item, and the even share plus one item; an item costs
+// kItemCost steps beside its own, one with partial results kPartCost more.
+constexpr int kItemCost = 2, kPartCost = 1;
+
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh, int32_t ctas) {
+    __shared__ int64_t warp_sums[32];
+    __shared__ int64_t red[32];
+    __shared__ int32_t s_max, s_c, s_cost;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t hkv = a.cache.num_kv_heads, tpt = sh.tokens_per_tile, per = 2 * tpt;
+    int64_t total;
+
+    // ---- query blocks before each sequence
+    bool bad = false;
+    int32_t carry = 0;
+    for (int base = 0; base < a.batch; base += kPlanThreads) {
+        const int b = base + tid;
+        int32_t nq = 0;
+        if (b < a.batch) {
+            const int32_t x = a.cu_q_lens[b], y = a.cu_q_lens[b + 1];
+            if (x < 0 || y < x || y > a.num_tokens) bad = true;
+            else nq = (y - x + per - 1) / per;
+        }
+        const int64_t incl = block_scan(nq, warp_sums, total);
+        if (b < a.batch) plan.first[b] = carry + int32_t(incl) - nq;
+        carry += int32_t(total);
+        if (__syncthreads_or(bad)) break;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            raise_status(a.status, PKV_DEV_QUERY_RANGE);
+            plan.header[0] = plan.header[1] = 0;
+        }
+        return;
+    }
+    const int32_t nblocks = carry;
+    if (tid == 0) {
+        plan.first[a.batch] = nblocks;
+        s_max = 0;
+        s_cost = INT_MAX;
+        s_c = 1;
+    }
+    __syncthreads();
+
+    // ---- each block's keys
+    int64_t sum = 0;
+    int32_t longest = 0;
+    for (int i = tid; i < nblocks; i += kPlanThreads) {
+        int lo = 0, hi = a.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (plan.first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int b = lo;
+        const int32_t q0 = a.cu_q_lens[b], n = a.cu_q_lens[b + 1] - q0;
+        const int32_t t0 = (i - plan.first[b]) * per;
+        int32_t L = a.seq_lens[b];
+        if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) {
+            raise_status(a.status, PKV_DEV_SEQ_LEN);
+            L = 0;
+        } else if (L < n) {
+            raise_status(a.status, PKV_DEV_SEQ_LEN);
+        }
+        const int32_t ntok = min(per, n - t0);
+        const Tiles t = tiles_of(L - n + t0, ntok, a.window, a.sinks);
+        const int4 q = make_int4(b, t0, t.count, ntok);
+        plan.blocks[i] = q;
+        const int32_t steps = steps_of(q, tpt);
+        sum += steps;
+        longest = max(longest, steps);
+    }
+    atomicMax(&s_max, longest);
+    block_scan(sum, warp_sums, total);
+    const int64_t steps_all = total * hkv;
+
+    // ---- the items' length: warp w tries one
+    {
+        int64_t c = warp < 16 ? (s_max + warp) / (warp + 1)
+                              : (steps_all * (warp - 15) + int64_t(ctas) * 8 - 1) / (int64_t(ctas) * 8);
+        c = max(int64_t(1), min(c, int64_t(max(1, s_max))));
+        int64_t units = 0, rows = 0, parts = 0;
+        for (int i = lane; i < nblocks; i += 32) {
+            const int4 q = plan.blocks[i];
+            const int32_t steps = steps_of(q, tpt);
+            const int32_t k = max(1, int32_t((steps + c - 1) / c));
+            const bool split = q.w <= tpt;
+            units += k;
+            if (k > 1 || (split && q.z > 1)) {
+                parts += k;
+                rows += int64_t(k) * (split ? 2 : 1) * q.w * sh.group;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            units += __shfl_xor_sync(0xffffffffu, units, o);
+            rows += __shfl_xor_sync(0xffffffffu, rows, o);
+            parts += __shfl_xor_sync(0xffffffffu, parts, o);
+        }
+        const bool fits = units <= plan.max_units && rows * hkv <= plan.max_rows;
+        const int64_t extra = units * hkv * kItemCost + parts * hkv * kPartCost;
+        const int64_t waves =
+            (units * hkv + ctas - 1) / ctas * (c + kItemCost + (parts ? kPartCost : 0));
+        const int64_t share = (steps_all + extra) / ctas + c + kItemCost;
+        int64_t cost = min(waves, share);
+        if (cost > (1 << 25)) cost = (1 << 25) + (cost >> 20);
+        if (lane == 0) {
+            red[warp] = c;
+            if (fits) atomicMin(&s_cost, int32_t(min(cost, int64_t(INT_MAX >> 5))) * 32 + warp);
+        }
+    }
+    __syncthreads();
+    // (the longest block whole always fits: its rows are what max_rows holds)
+    const int64_t c = s_cost == INT_MAX ? max(1, s_max) : red[s_cost & 31];
+
+    // ---- the items
+    int64_t unit0 = 0, row0 = 0, merge0 = 0;
+    for (int base = 0; base < nblocks; base += kPlanThreads) {
+        const int i = base + tid;
+        int4 q = make_int4(0, 0, 0, 0);
+        int32_t k = 0, steps = 0, count = 0;
+        bool split = false;
+        if (i < nblocks) {
+            q = plan.blocks[i];
+            steps = steps_of(q, tpt);
+            split = q.w <= tpt;
+            k = max(1, int32_t((steps + c - 1) / c));
+            count = k > 1 || (split && q.z > 1) ? k * (split ? 2 : 1) : 0;
+        }
+        const int64_t rows = int64_t(count) * q.w * sh.group * hkv;
+        const int64_t u = block_scan(k, warp_sums, total) - k + unit0;
+        unit0 += total;
+        const int64_t r = block_scan(rows, warp_sums, total) - rows + row0;
+        row0 += total;
+        const int64_t m = block_scan(count > 0, warp_sums, total) - (count > 0) + merge0;
+        merge0 += total;
+        if (i < nblocks) {
+            const int32_t q0 = a.cu_q_lens[q.x], n = a.cu_q_lens[q.x + 1] - q0;
+            int32_t L = a.seq_lens[q.x];
+            if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) L = 0;
+            if (count) plan.merges[m] = {q0 + q.y, q.w, int32_t(r), count};
+            const int32_t tile_rows = q.w * sh.group;
+            for (int j = 0; j < k; ++j) {
+                const int32_t s0 = int32_t(int64_t(steps) * j / k);
+                const int32_t s1 = int32_t(int64_t(steps) * (j + 1) / k);
+                Item it = {};
+                it.b = q.x;
+                it.qrow = q0 + q.y;
+                it.pos = L - n + q.y;
+                it.ntok = q.w;
+                it.split = split;
+                if (split) {
+                    // tiles 2 s0 .. 2 s1 (the last may be missing): A the first half
+                    it.v0 = 2 * s0;
+                    const int32_t tiles = min(q.z, 2 * s1) - 2 * s0;
+                    it.na = (tiles + 1) >> 1;
+                    it.nb = tiles >> 1;
+                } else {
+                    it.v0 = s0;
+                    it.na = it.nb = s1 - s0;
+                }
+                it.prow = count ? int32_t(r) + j * (split ? 2 : 1) * tile_rows : -1;
+                it.gstride = count * tile_rows;
+                plan.items[u + j] = it;
+            }
+        }
+    }
+    if (tid == 0) {
+        plan.header[0] = int32_t(unit0);
+        plan.header[1] = int32_t(merge0);
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+// Ring positions of an item's tiles, from its first: pair items K0 V0 K1 V1 ..,
+// split items KA0 KB0 VA0 VB0 KA1 .. (the last step may have A alone).
+struct Order {
+    uint32_t base;
+    int32_t split, nb;
+    __device__ __forceinline__ uint32_t k(int h, int i) const {
+        return base + (split ? 4 * i + (h ? 1 : 0) : 2 * i);
+    }
+    __device__ __forceinline__ uint32_t v(int h, int i) const {
+        return base + (split ? 4 * i + (i < nb ? 2 + h : 1) : 2 * i + 1);
+    }
+    __device__ __forceinline__ uint32_t total(int na) const {
+        return split ? 2 * (na + nb) : 2 * na;
+    }
+};
+
+// Bits c < x of the 32 columns from 32 w on.
+__device__ __forceinline__ uint32_t below(int32_t x, int w) {
+    const int32_t n = min(32, max(0, x - 32 * w));
+    return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// d = a * b + c on two fp32 pairs.
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+    asm("{ .reg .b64 a, b, c, d; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; "
+        "fma.rn.f32x2 d, a, b, c; mov.b64 {%0, %1}, d; }"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
+    asm("{ .reg .b64 a, d; mov.b64 a, {%2, %3}; mov.b64 d, {%0, %1}; "
+        "add.rn.f32x2 d, d, a; mov.b64 {%0, %1}, d; }"
+        : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
+}
+// Makes what follows depend on registers a TMEM load has filled (their values
+// are there only after the wait that precedes this).
+__device__ __forceinline__ void pin32(uint32_t *r) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
+                          "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+// Four probabilities -> their E4M3 codes and those of the rounding residuals.
+// Through fp16 (2^-11 relative, below what two terms resolve).
+__device__ __forceinline__ void e4m3_terms(float p0, float p1, float p2, float p3, uint32_t &t0,
+                                           uint32_t &t1) {
+    const uint32_t a = pack_f16x2(p0, p1), b = pack_f16x2(p2, p3);
+    asm("{ .reg .b16 x, y; .reg .b32 u, v;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 x, %2; cvt.rn.satfinite.e4m3x2.f16x2 y, %3;\n\t"
+        "mov.b32 %0, {x, y};\n\t"
+        "cvt.rn.f16x2.e4m3x2 u, x; cvt.rn.f16x2.e4m3x2 v, y;\n\t"
+        "sub.rn.f16x2 u, %2, u; sub.rn.f16x2 v, %3, v;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 x, u; cvt.rn.satfinite.e4m3x2.f16x2 y, v;\n\t"
+        "mov.b32 %1, {x, y}; }"
+        : "=&r"(t0), "=r"(t1) : "r"(a), "r"(b));
+}
+
+template <int D, bool E4>
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v, const ChunkArgs a, const Plan plan,
+                const Shape sh) {
+    using C = Cfg<D, E4>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_addr(base);
+    volatile uint32_t *tslot = reinterpret_cast<volatile uint32_t *>(base + kOffSlot);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(base + kOffFlag);
+    auto bar = [&](int i) { return sb + 8u * uint32_t(i); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hkv = a.cache.num_kv_heads, bs = a.cache.block_size;
+    const int G = sh.group, tpt = sh.tokens_per_tile;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar(kBarFull + s), 1);
+            mbar_init(bar(kBarEmpty + s), 1);
+        }
+        mbar_init(bar(kBarQFull), E4 ? 256 : 1);
+        mbar_init(bar(kBarQEmpty), 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(bar(kBarSFull + h), 1);
+            mbar_init(bar(kBarPFull + h), 128);
+            mbar_init(bar(kBarPvDone + h), 1);
+            mbar_init(bar(kBarOEmpty + h), 128);
+        }
+        mbar_init(bar(kBarDrain), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tc::alloc(sb + kOffSlot, kTmemCols);
+        tc::fence_before_sync();
+    }
+    if (threadIdx.x == kLoadWarp * 32) {
+        if (!E4) tma_prefetch_desc(&tmap_q);
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tslot;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int num_items = plan.header[0] * hkv;
+    auto read_item = [&](int it) {
+        Item r;
+        const int4 *p = reinterpret_cast<const int4 *>(plan.items + it / hkv);
+        int4 *d = reinterpret_cast<int4 *>(&r);
+        d[0] = p[0];
+        d[1] = p[1];
+        d[2] = p[2];
+        return r;
+    };
+
+    if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ producer
+        const int box = min(bs, kKeys);
+        const int nbox = kKeys / box;
+        uint32_t ring = 0, items_done = 0;
+        uint32_t armed = 0, armed_parity = 0;
+        uint32_t q_armed = 0, q_parity = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
+            const Item r = read_item(it);
+            if (r.na == 0) continue;
+            const int g = it % hkv;
+            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+            const int32_t pmax = r.pos + r.ntok - 1;
+            const int32_t *table = a.block_tables + int64_t(r.b) * a.max_blocks;
+            // lane's box of virtual tile v: its pool row, or -1 (nothing to copy)
+            auto lookup = [&](int v) -> int32_t {
+                if (lane >= nbox) return -1;
+                const int32_t key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + lane * box;
+                if (key > pmax || (key + box - 1 < tl.lo && key >= a.sinks)) return -1;
+                const int32_t phys = table[key / bs];
+                if (phys < 0 || phys >= a.cache.num_blocks) {
+                    raise_status(a.status, PKV_DEV_BLOCK_ID);
+                    return g * bs;                  // some block's rows stand in
+                }
+                return (phys * hkv + g) * bs + key % bs;
+            };
+            auto load = [&](const CUtensorMap *map, int32_t y) -> bool {
+                const uint32_t stage = ring % C::kStages, phase = (ring / C::kStages) & 1u;
+                if (!__all_sync(0xffffffffu, pipe_wait(bar(kBarEmpty + stage), phase ^ 1u,
+                                                       a.status, abort_flag)))
+                    return false;
+                const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar(kBarFull + stage),
+                                          __popc(live) * uint32_t(box) * D * C::kElem);
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                __syncwarp();
+                if (y >= 0) {
+                    const uint32_t dst = sb + C::kOffRing + stage * C::kStage +
+                                         uint32_t(lane * box) * D * C::kElem;
+                    if constexpr (D * C::kElem == 256)
+                        tma_load_4d(dst, map, 0, 0, 0, y >> 3, bar(kBarFull + stage));
+                    else
+                        tma_load_2d(dst, map, 0, y, bar(kBarFull + stage));
+                }
+                ++ring;
+                return true;
+            };
+            int32_t ya = lookup(r.v0);
+            if constexpr (!E4) {
+                // the item's query tiles, once the last item's are no longer read
+                if (!(ok = __all_sync(0xffffffffu,
+                                      pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
+                                                abort_flag))))
+                    break;
+                if (lane == 0) {
+                    const int tiles = r.split ? 1 : 2;
+                    mbar_arrive_expect_tx(bar(kBarQFull), tiles * uint32_t(tpt * G) * D * 2);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int half = 0; half < D / 64; ++half)
+                            tma_load_3d(sb + C::kOffQ + t * C::kQTile + half * C::kHalfTile,
+                                        &tmap_q, half * 64, g * G, r.qrow + t * tpt,
+                                        bar(kBarQFull));
+                }
+                q_armed = 1;
+                q_parity = items_done & 1u;
+            }
+            ++items_done;
+            if (!r.split) {
+                for (int i = 0; i < r.na && ok; ++i) {
+                    const int32_t y = ya;
+                    ok = load(&tmap_k, y);
+                    if (i + 1 < r.na) ya = lookup(r.v0 + i + 1);
+                    ok = ok && load(&tmap_v, y);
+                }
+            } else {
+                int32_t yb = r.nb > 0 ? lookup(r.v0 + r.na) : -1;
+                for (int i = 0; i < r.na && ok; ++i) {
+                    const int32_t y0 = ya, y1 = yb;
+                    const bool both = i < r.nb;
+                    ok = load(&tmap_k, y0) && (!both || load(&tmap_k, y1));
+                    if (i + 1 < r.na) ya = lookup(r.v0 + i + 1);
+                    if (i + 1 < r.nb) yb = lookup(r.v0 + r.na + i + 1);
+                    ok = ok && load(&tmap_v, y0) && (!both || load(&tmap_v, y1));
+                }
+            }
+        }
+        // Do not leave while copies may still land in this CTA's shared memory.
+        if (lane == 0) {
+            for (int s = 0; s < C::kStages; ++s)
+                if (armed & (1u << s))
+                    mbar_wait(bar(kBarFull + s), (armed_parity >> s) & 1u, a.status);
+            if (q_armed) mbar_wait(bar(kBarQFull), q_parity, a.status);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        uint32_t ring = 0, items_done = 0;
+        uint32_t np[2] = {0, 0};                 // value products issued
+        uint32_t nitem[2] = {0, 0};              // items begun, by half
+        bool ok = true;
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, pipe_wait(b, parity, a.status, abort_flag));
+        };
+        for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
+            const Item r = read_item(it);
+            if (r.na == 0) continue;
+            const Order ord{ring, r.split, r.nb};
+            if (!(ok = wait_all(bar(kBarQFull), items_done & 1u))) break;
+            auto scores = [&](int h, int i) -> bool {
+                const uint32_t pos = ord.k(h, i), stage = pos % C::kStages;
+                if (!wait_all(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
+                    const uint32_t qb = sb + C::kOffQ + (r.split ? 0 : h) * C::kQTile;
+                    const uint32_t d = tmem + kKeys * h;
+                    if constexpr (E4) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_e4m3(d,
+                                             tc::smem_desc(qb + t * C::kHalfTile + 32 * kk, 16, 1024),
+                                             tc::smem_desc(kb + 32 * kk, 16, 1024), C::kIdS,
+                                             (t | kk) != 0);
+                    } else {
+#pragma unroll
+                        for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_bf16(
+                                    d, tc::smem_desc(qb + half * C::kHalfTile + 32 * kk, 16, 1024),
+                                    tc::smem_desc(kb + half * 1024 + 32 * kk, 16,
+                                                  D == 128 ? 2048 : 1024),
+                                    C::kIdS, (half | kk) != 0);
+                    }
+                    tc::commit(bar(kBarSFull + h));
+                    if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
+                    // the item's last score product frees its queries
+                    if (h == (r.split && r.nb < r.na ? 0 : 1) && i == r.na - 1)
+                        tc::commit(bar(kBarQEmpty));
+                }
+                __syncwarp();
+                return true;
+            };
+            auto product = [&](int h, int i) -> bool {
+                if (!wait_all(bar(kBarPFull + h), np[h] & 1u)) return false;
+                if (i == 0 && !wait_all(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
+                const uint32_t pos = ord.v(h, i), stage = pos % C::kStages;
+                if (!wait_all(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
+                    const uint32_t d = tmem + kColO + 128 * h, p = tmem + kKeys * h;
+                    if constexpr (E4) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk,
+                                                tc::smem_desc(vb + 4096 * kk, 16384, 1024),
+                                                C::kIdO, (i | t | kk) != 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_bf16_ts(d, p + 8 * kk,
+                                            D == 128 ? tc::smem_desc(vb + 4096 * kk, 1024, 2048)
+                                                     : tc::smem_desc(vb + 2048 * kk, 16384, 1024),
+                                            C::kIdO, (i | kk) != 0);
+                    }
+                    tc::commit(bar(kBarPvDone + h));
+                    if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
+                }
+                __syncwarp();
+                if (i == 0) ++nitem[h];
+                ++np[h];
+                return true;
+            };
+            ok = scores(0, 0) && (r.nb == 0 || scores(1, 0));
+            for (int i = 0; i < r.na && ok; ++i) {
+                ok = product(0, i) && (i + 1 >= r.na || scores(0, i + 1));
+                if (ok && i < r.nb) ok = product(1, i) && (i + 1 >= r.nb || scores(1, i + 1));
+            }
+            ring += ord.total(r.na);
+            ++items_done;
+        }
+        if (lane == 0) {
+            tc::commit(bar(kBarDrain));
+            mbar_wait(bar(kBarDrain), 0, a.status);
+        }
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // -------------------------------------------- softmax and epilogue
+        const int h = warp >> 2;                         // half
+        const int row = threadIdx.x & 127;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + kKeys * h + lanes;    // S, P
+        const uint32_t to = tmem + kColO + 128 * h + lanes;
+        const int tok_row = row / G, head_row = row - tok_row * G;
+        uint32_t ring = 0, np = 0, items_done = 0;
+        bool ok = true;
+        for (int it = blockIdx.x; it < num_items; it += gridDim.x) {
+            const Item r = read_item(it);
+            const int g = it % hkv;
+            const int n = h ? r.nb : r.na;
+            const int tok0 = r.split ? 0 : h * tpt;      // the half's first token
+            const int tok = tok0 + tok_row;
+            const bool live = tok_row < tpt && tok < r.ntok;
+            const int32_t pos = r.pos + tok;
+            const Order ord{ring, r.split, r.nb};
+            float sc = a.scale * kLog2e;
+            float m = -INFINITY, l = 0.f;
+            if constexpr (E4) {
+                sc *= a.k_scale[g];
+                if (r.na > 0) {
+                    // this half's query rows as two E4M3 terms, scaled by a power
+                    // of two that puts the row's largest element in [128, 256)
+                    if (ok) ok = pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
+                                           abort_flag);
+                    if (ok && (h == 0 || !r.split)) {
+                        const uint4 *src = static_cast<const uint4 *>(a.q) +
+                            (int64_t(r.qrow + min(tok, r.ntok - 1)) * a.num_q_heads + g * G +
+                             head_row) * (D / 8);
+                        uint4 x[D / 8];
+                        float big = 0.f;
+                        bool finite = true;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float u = fabsf(bf16_lo_to_f32(w[e]));
+                                const float v = fabsf(bf16_hi_to_f32(w[e]));
+                                finite = finite && u < INFINITY && v < INFINITY;
+                                big = fmaxf(big, fmaxf(u, v));
+                            }
+                        }
+                        // big = 1.f 2^e: 2^(7 - e), within the normal range
+                        const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
+                        const float up = __uint_as_float(uint32_t(134 - e) << 23);
+                        sc *= __uint_as_float(uint32_t(max(1, 120 + e)) << 23);
+                        if (!finite) sc = __int_as_float(0x7fc00000);   // inf or NaN: a NaN row
+                        uint8_t *q0 = base + C::kOffQ + h * C::kQTile + row * 128;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            uint32_t t0[4], t1[4];
+#pragma unroll
+                            for (int e2 = 0; e2 < 4; ++e2) {
+                                const uint4 &xx = x[2 * i + (e2 >> 1)];
+                                const uint32_t w0 = e2 & 1 ? xx.z : xx.x, w1 = e2 & 1 ? xx.w : xx.y;
+                                e4m3_terms(bf16_lo_to_f32(w0) * up, bf16_hi_to_f32(w0) * up,
+                                           bf16_lo_to_f32(w1) * up, bf16_hi_to_f32(w1) * up,
+                                           t0[e2], t1[e2]);
+                            }
+                            const int off = ((i ^ row) & 7) << 4;
+                            *reinterpret_cast<uint4 *>(q0 + off) =
+                                make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                            *reinterpret_cast<uint4 *>(q0 + C::kHalfTile + off) =
+                                make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    if (r.split && h == 1) {
+                        // the same rows' scale (their terms are the other half's)
+                        const uint4 *src = static_cast<const uint4 *>(a.q) +
+                            (int64_t(r.qrow + min(tok, r.ntok - 1)) * a.num_q_heads + g * G +
+                             head_row) * (D / 8);
+                        float big = 0.f;
+                        bool finite = true;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 x = src[i];
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float u = fabsf(bf16_lo_to_f32(w[e]));
+                                const float v = fabsf(bf16_hi_to_f32(w[e]));
+                                finite = finite && u < INFINITY && v < INFINITY;
+                                big = fmaxf(big, fmaxf(u, v));
+                            }
+                        }
+                        const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
+                        sc *= __uint_as_float(uint32_t(max(1, 120 + e)) << 23);
+                        if (!finite) sc = __int_as_float(0x7fc00000);
+                    }
+                    mbar_arrive(bar(kBarQFull));
+                }
+            }
+            if (r.na > 0) ++items_done;
+            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+            const int32_t pmax = r.pos + r.ntok - 1;
+            // positions of the half's first and last row
+            const int32_t hmin = r.pos + tok0, hmax = r.pos + min(r.ntok - 1, tok0 + tpt - 1);
+            const int v0 = r.v0 + (r.split && h ? r.na : 0);
+            for (int i = 0; i < n && ok; ++i) {
+                const int v = v0 + i;
+                const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
+                ok = pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                uint32_t s[kKeys];
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 32) tc::ld32(ts + j, s + j);
+                tc::wait_ld();
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 32) pin32(s + j);
+                // ---- keys this row does not see
+                const bool all_seen =
+                    k0 + kKeys - 1 <= hmin &&
+                    (a.window == 0 || k0 > hmax - a.window || k0 + kKeys - 1 < a.sinks);
+                if (!all_seen) {
+                    const int32_t rel = pos - k0;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t see = pos >= 0 ? below(rel + 1, w) : 0u;
+                        if (a.window > 0)
+                            see &= ~below(rel - a.window + 1, w) | below(a.sinks - k0, w);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!((see >> j) & 1u)) s[32 * w + j] = 0xff800000u;
+                    }
+                }
+                // ---- row maximum
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[j + e])),
+                                      __uint_as_float(s[j + 4 + e]));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (i == 0) {
+                    m = mt;
+                } else if (__any_sync(0xffffffffu, (mt - m) * sc > C::kSlack)) {
+                    // rescale: the last value product into these rows is done first
+                    ok = pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const float mn = fmaxf(m, mt);
+                    const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
+                    l *= f;
+                    m = mn;
+#pragma unroll
+                    for (int j = 0; j < D; j += 32) {
+                        uint32_t o[32];
+                        tc::ld32(to + j, o);
+                        tc::wait_ld();
+                        pin32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::st32(to + j, o);
+                    }
+                }
+                const float neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
+                // ---- probabilities, their sum, and their terms into S's columns
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < kKeys; j += 4) {
+                    float p[4];
+                    fma2(p[0], p[1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]), sc, sc, neg,
+                         neg);
+                    fma2(p[2], p[3], __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]), sc, sc,
+                         neg, neg);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
+                    add2(sum[0], sum[1], p[0], p[1]);
+                    add2(sum[2], sum[3], p[2], p[3]);
+                    if constexpr (E4) {
+                        // terms t of keys j.. at register 32 t + j / 4: the scores of
+                        // those registers are consumed by then (32 t + j / 4 <= j) only
+                        // for t = 0; the second term waits in the register of key j
+                        uint32_t t0, t1;
+                        e4m3_terms(p[0], p[1], p[2], p[3], t0, t1);
+                        s[j] = t0;
+                        s[j + 1] = t1;
+                    } else {
+                        s[j / 2] = pack_bf16x2(p[0], p[1]);
+                        s[j / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                    }
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if constexpr (E4) {
+                    uint32_t t[64];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        t[j] = s[4 * j];
+                        t[32 + j] = s[4 * j + 1];
+                    }
+                    tc::st32(ts, t);
+                    tc::st32(ts + 32, t + 32);
+                } else {
+                    tc::st32(ts, s);
+                    tc::st32(ts + 32, s + 32);
+                }
+                // ---- value rows no row of the item sees: zeroed, thread = key
+                const bool stale = k0 + kKeys - 1 > pmax ||
+                                   (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys));
+                if (stale) {
+                    const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
+                    ok = pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u, a.status,
+                                   abort_flag);
+                    const int32_t key = k0 + row;
+                    if (ok && (key > pmax || (key < tl.lo && key >= a.sinks))) {
+                        uint8_t *vt = base + C::kOffRing + stage * C::kStage;
+                        if constexpr (D * C::kElem == 256) {
+                            vt += (row >> 3) * 2048 + (row & 7) * 128;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                *reinterpret_cast<uint4 *>(vt + (c >> 3) * 1024 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        } else {
+                            vt += row * 128;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                *reinterpret_cast<uint4 *>(vt + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
+                mbar_arrive(bar(kBarPFull + h));
+                ++np;
+            }
+            ring += ord.total(r.na);
+
+            // ---- epilogue
+            if (n > 0 && ok) {
+                ok = pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
+                tc::fence_after_sync();
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            const float nan = __int_as_float(0x7fc00000);
+            float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+            if constexpr (E4) inv *= a.v_scale[g];
+            float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kShift)) * kLn2 : -INFINITY;
+            if (!ok) lse = nan;
+            const bool direct = r.prow < 0;
+            const int64_t orow = int64_t(r.qrow + tok) * a.num_q_heads + g * G + head_row;
+            const int64_t prow = int64_t(r.prow) + int64_t(g) * r.gstride +
+                                 (r.split ? h * r.ntok * G : 0) + tok * G + head_row;
+            // half B of a split item without a tile of its own adds nothing to a direct row
+            const bool writes = live && !(direct && r.split && h == 1);
+#pragma unroll
+            for (int j = 0; j < D; j += 32) {
+                uint32_t o[32];
+                if (n > 0 && ok) {
+                    tc::ld32(to + j, o);
+                    tc::wait_ld();
+                    pin32(o);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = ok ? 0u : 0x7fc00000u;
+                }
+                if (writes && direct) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
+                                                           orow * D + j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv,
+                                               __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (writes) {
+                    float4 *dst = reinterpret_cast<float4 *>(plan.o_part + prow * D + j);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv,
+                                             __uint_as_float(o[4 * e + 1]) * inv,
+                                             __uint_as_float(o[4 * e + 2]) * inv,
+                                             __uint_as_float(o[4 * e + 3]) * inv);
+                }
+            }
+            if (n > 0) {
+                tc::fence_before_sync();
+                mbar_arrive(bar(kBarOEmpty + h));
+            }
+            if (writes) {
+                if (!direct) plan.lse_part[prow] = lse;
+                else if (a.lse) a.lse[orow] = lse;
+            }
+        }
+    }
+
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------- the merge
+// One row per D / 4 lanes: out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M}
+// over the row's partials, each already divided by its own sum.  A NaN partial
+// makes the row NaN; empty ones (lse = -inf) weigh nothing.
+constexpr int kMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
+    constexpr int kLanes = D / 4, kRowsPerCta = kMergeThreads / kLanes;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int hkv = a.cache.num_kv_heads, G = sh.group;
+    const int chunks = (2 * kRows + kRowsPerCta - 1) / kRowsPerCta;
+    const int64_t total = int64_t(plan.header[1]) * hkv * chunks;
+    const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const int64_t mg = w / chunks;
+        const Merge m = plan.merges[mg / hkv];
+        const int g = int(mg % hkv), rows = m.ntok * G;
+        const int row = int(w % chunks) * kRowsPerCta + sub;
+        if (row >= rows) continue;
+        const int64_t first = int64_t(m.prow) + int64_t(g) * m.count * rows + row;
+        const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + first * kLanes + c;
+        float M = -INFINITY, W = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool broken = false;
+        for (int p0 = 0; p0 < m.count; p0 += 8) {
+            float l[8];
+            float4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const bool in = p0 + u < m.count;
+                const int64_t at = int64_t(p0 + u) * rows;
+                l[u] = in ? plan.lse_part[first + at] : -INFINITY;
+                x[u] = in ? op[at * kLanes] : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float mc = M;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                broken |= l[u] != l[u];
+                mc = fmaxf(mc, l[u]);
+            }
+            if (mc == -INFINITY) continue;
+            const float f = expf(M - mc);
+            W *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float wt = expf(l[u] - mc);
+                if (wt != 0.f) {
+                    W += wt;
+                    acc.x = fmaf(wt, x[u].x, acc.x); acc.y = fmaf(wt, x[u].y, acc.y);
+                    acc.z = fmaf(wt, x[u].z, acc.z); acc.w = fmaf(wt, x[u].w, acc.w);
+                }
+            }
+            M = mc;
+        }
+        const int64_t orow = (int64_t(m.qrow) + row / G) * a.num_q_heads + g * G + row % G;
+        float inv = W > 0.f ? 1.f / W : 0.f;
+        float lse = W > 0.f ? M + logf(W) : -INFINITY;
+        if (broken) inv = lse = __int_as_float(0x7fc00000);
+        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + orow * D)[c] =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (c == 0 && a.lse) a.lse[orow] = lse;
+    }
+}
+
+// ------------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 chunk_encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+bool encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *at,
+            const cuuint64_t *dim, const cuuint64_t *stride, const cuuint32_t *box) {
+    auto fn = chunk_encode_fn();
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return fn && fn(map, type, cuuint32_t(rank), const_cast<void *>(at), dim, stride, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A pool as rows of D elements; one box is `box` whole rows.  256-byte rows land
+// as [8-row group][128-byte half][8 rows][128 B], 128-byte rows as they are.
+template <int D, bool E4>
+bool pool_map(CUtensorMap *map, const void *pool, int64_t rows, int box) {
+    const auto type = E4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if constexpr (!E4 && D == 128) {
+        const cuuint64_t dim[4] = {64, 8, 2, cuuint64_t(rows / 8)}, stride[3] = {256, 128, 2048};
+        const cuuint32_t b[4] = {64, 8, 2, cuuint32_t(box / 8)};
+        return encode(map, type, 4, pool, dim, stride, b);
+    } else {
+        const cuuint64_t dim[2] = {D, cuuint64_t(rows)}, stride[1] = {128};
+        const cuuint32_t b[2] = {D, cuuint32_t(box)};
+        return encode(map, type, 2, pool, dim, stride, b);
+    }
+}
+
+Shape shape_of(int32_t hq, int32_t hkv) {
+    const int group = hq / hkv;
+    return {group, kRows / group};
+}
+
+struct Sizes {
+    int64_t blocks, units, rows;
+    size_t items, merges, blocks_at, first, o_part, lse_part, total;
+};
+
+// Most query blocks: every sequence's last one may be short.  Partial rows:
+// every token of a split item gives two partials (its block is its sequence's
+// only or last, at most tokens_per_tile of them), and kSpare CTAs' worth of
+// full blocks may be cut further.
+constexpr int kSpare = 4;
+
+Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32_t hq,
+               int32_t max_blocks) {
+    const Shape sh = shape_of(hq, c.num_kv_heads);
+    Sizes s;
+    const int64_t per = 2 * sh.tokens_per_tile;
+    s.blocks = std::min(num_tokens, num_tokens / per + batch);
+    const int64_t tiles = (int64_t(max_blocks) * c.block_size + kKeys - 1) / kKeys + 1;
+    // items of all KV heads that cutting may add
+    const int64_t spare = int64_t(sm_count()) * kSpare;
+    s.units = s.blocks + std::min(spare, s.blocks * tiles);
+    const int64_t split_rows = 2 * std::min(num_tokens, int64_t(batch) * sh.tokens_per_tile) * hq;
+    const int64_t most = num_tokens * hq * tiles;          // one partial per row and tile
+    s.rows = std::min(split_rows + spare * 2 * kRows, std::max<int64_t>(most, 1));
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    s.items = 256;
+    s.merges = up(s.items + s.units * sizeof(Item));
+    s.blocks_at = up(s.merges + s.blocks * sizeof(Merge));
+    s.first = up(s.blocks_at + s.blocks * sizeof(int4));
+    s.lse_part = up(s.first + (size_t(batch) + 1) * 4);
+    s.o_part = up(s.lse_part + s.rows * 4);
+    s.total = up(s.o_part + size_t(s.rows) * c.head_dim_v * 4);
+    return s;
+}
+
+template <int D, bool E4>
+int launch(const ChunkArgs &a, uint8_t *ws) {
+    using C = Cfg<D, E4>;
+    auto kernel = chunk_tc_kernel<D, E4>;
+    const Shape sh = shape_of(a.num_q_heads, a.cache.num_kv_heads);
+    const Sizes sz = sizes_of(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks);
+    const Plan plan{reinterpret_cast<int32_t *>(ws),
+                    reinterpret_cast<Item *>(ws + sz.items),
+                    reinterpret_cast<Merge *>(ws + sz.merges),
+                    reinterpret_cast<int4 *>(ws + sz.blocks_at),
+                    reinterpret_cast<int32_t *>(ws + sz.first),
+                    reinterpret_cast<float *>(ws + sz.o_part),
+                    reinterpret_cast<float *>(ws + sz.lse_part),
+                    int32_t(sz.units), int32_t(sz.rows)};
+    const int64_t rows = int64_t(a.cache.num_blocks) * a.cache.num_kv_heads * a.cache.block_size;
+    const int box = std::min(a.cache.block_size, kKeys);
+    CUtensorMap tq = {}, tk, tv;
+    if (!pool_map<D, E4>(&tk, a.k_pool, rows, box) || !pool_map<D, E4>(&tv, a.v_pool, rows, box))
+        return PKV_ERR_CUDA;
+    if constexpr (!E4) {
+        // boxes of one 128-byte column block of tokens_per_tile tokens' group heads
+        const cuuint64_t dim[3] = {D, cuuint64_t(a.num_q_heads), cuuint64_t(a.num_tokens)};
+        const cuuint64_t stride[2] = {D * 2, cuuint64_t(a.num_q_heads) * D * 2};
+        const cuuint32_t b[3] = {64, cuuint32_t(sh.group), cuuint32_t(sh.tokens_per_tile)};
+        if (!encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dim, stride, b))
+            return PKV_ERR_CUDA;
+    }
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (configured_dev != dev) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(C::kSmem)) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured_dev = dev;
+    }
+    const int ctas = sm_count();
+    int rc = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, plan, sh,
+                        int32_t(ctas));
+    if (rc != PKV_OK) return rc;
+    const int grid =
+        int(std::min<int64_t>(ctas, std::max<int64_t>(1, sz.units * a.cache.num_kv_heads)));
+    rc = launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
+                    sh);
+    if (rc != PKV_OK) return rc;
+    const int64_t merge_work = sz.blocks * a.cache.num_kv_heads * (2 * kRows * D / 4 / kMergeThreads);
+    return launch_pdl(chunk_merge_kernel<D>,
+                      dim3(unsigned(std::min<int64_t>(merge_work, int64_t(ctas) * 8))),
+                      dim3(kMergeThreads), 0, a.stream, a, plan, sh);
+}
+
+}  // namespace
+
+bool chunk_tc_supports(const pkv_cache_desc &c, int32_t num_q_heads, int32_t max_blocks, bool e4) {
+    const int group = num_q_heads / c.num_kv_heads;
+    const int least = e4 ? 16 : 8;
+    const bool pow2 = c.block_size >= least && (c.block_size & (c.block_size - 1)) == 0;
+    const int64_t rows = int64_t(c.num_blocks) * c.num_kv_heads * c.block_size;
+    return c.head_dim_k == c.head_dim_v && (c.head_dim_k == 128 || (c.head_dim_k == 64 && !e4)) &&
+           group <= kRows && pow2 && rows < (int64_t(1) << 31) - 1 &&
+           int64_t(max_blocks) * c.block_size <= (int64_t(1) << 30);
+}
+
+size_t chunk_tc_workspace(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch,
+                          int32_t num_q_heads, int32_t max_blocks) {
+    return sizes_of(c, num_tokens, batch, num_q_heads, max_blocks).total;
+}
+
+int launch_chunk_tc(const ChunkArgs &in, void *workspace) {
+    ChunkArgs a = in;
+    // a window no sequence outgrows is none; positions stay below 2^30
+    if (a.window >= int64_t(a.max_blocks) * a.cache.block_size) a.window = 0;
+    a.sinks = std::min(a.sinks, 1 << 30);
+    if (a.window == 0) a.sinks = 0;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (a.k_scale) return launch<128, true>(a, ws);
+    return a.cache.head_dim_k == 128 ? launch<128, false>(a, ws) : launch<64, false>(a, ws);
+}
+
+}  // namespace pkv
