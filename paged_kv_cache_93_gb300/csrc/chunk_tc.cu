@@ -579,97 +579,92 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMA issuer
-        uint32_t ring = 0, items_done = 0;
-        uint32_t np[2] = {0, 0};                 // value products issued
-        uint32_t nitem[2] = {0, 0};              // items begun, by half
-        bool ok = true;
-        auto wait_all = [&](uint32_t b, uint32_t parity) {
-            return __all_sync(0xffffffffu, pipe_wait(b, parity, a.status, abort_flag));
-        };
-        for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
-            const Item r = read_item(it);
-            if (r.na == 0) continue;
-            const Order ord{ring, r.split, r.nb};
-            if (!(ok = wait_all(bar(kBarQFull), items_done & 1u))) break;
-            auto scores = [&](int h, int i) -> bool {
-                const uint32_t pos = ord.k(h, i), stage = pos % C::kStages;
-                if (!wait_all(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
-                tc::fence_after_sync();
-                if (lane == 0) {
+        // One thread runs the whole role: a wait that is already satisfied costs
+        // it a few tens of cycles, where warp-wide votes and re-elections cost
+        // some 250 each (five of them per tile bound the kernel).
+        if (tc::elect_one()) {
+            uint32_t ring = 0, items_done = 0;
+            uint32_t np[2] = {0, 0};             // value products issued
+            uint32_t nitem[2] = {0, 0};          // items begun, by half
+            bool ok = true;
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                return pipe_wait(b, parity, a.status, abort_flag);
+            };
+            for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
+                const Item r = read_item(it);
+                if (r.na == 0) continue;
+                const Order ord{ring, r.split, r.nb};
+                if (!(ok = wait(bar(kBarQFull), items_done & 1u))) break;
+                auto scores = [&](int h, int i) -> bool {
+                    const uint32_t pos = ord.k(h, i), stage = pos % C::kStages;
+                    if (!wait(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
+                    tc::fence_after_sync();
                     const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
                     const uint32_t qb = sb + C::kOffQ + (r.split ? 0 : h) * C::kQTile;
                     const uint32_t d = tmem + kKeys * h;
+                    const uint64_t qd = tc::smem_desc(qb, 16, 1024);
+                    const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
                     if constexpr (E4) {
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_e4m3(d,
-                                             tc::smem_desc(qb + t * C::kHalfTile + 32 * kk, 16, 1024),
-                                             tc::smem_desc(kb + 32 * kk, 16, 1024), C::kIdS,
-                                             (t | kk) != 0);
+                                tc::mma_e4m3(d, qd + ((t * C::kHalfTile + 32 * kk) >> 4),
+                                             kd + ((32 * kk) >> 4), C::kIdS, (t | kk) != 0);
                     } else {
 #pragma unroll
                         for (int half = 0; half < D / 64; ++half)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_bf16(
-                                    d, tc::smem_desc(qb + half * C::kHalfTile + 32 * kk, 16, 1024),
-                                    tc::smem_desc(kb + half * 1024 + 32 * kk, 16,
-                                                  D == 128 ? 2048 : 1024),
-                                    C::kIdS, (half | kk) != 0);
+                                tc::mma_bf16(d, qd + ((half * C::kHalfTile + 32 * kk) >> 4),
+                                             kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
+                                             (half | kk) != 0);
                     }
                     tc::commit(bar(kBarSFull + h));
                     if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
                     // the item's last score product frees its queries
                     if (h == (r.split && r.nb < r.na ? 0 : 1) && i == r.na - 1)
                         tc::commit(bar(kBarQEmpty));
-                }
-                __syncwarp();
-                return true;
-            };
-            auto product = [&](int h, int i) -> bool {
-                if (!wait_all(bar(kBarPFull + h), np[h] & 1u)) return false;
-                if (i == 0 && !wait_all(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
-                const uint32_t pos = ord.v(h, i), stage = pos % C::kStages;
-                if (!wait_all(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
-                tc::fence_after_sync();
-                if (lane == 0) {
+                    return true;
+                };
+                auto product = [&](int h, int i) -> bool {
+                    const uint32_t pos = ord.v(h, i), stage = pos % C::kStages;
+                    if (!wait(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
+                    if (i == 0 && !wait(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
+                    if (!wait(bar(kBarPFull + h), np[h] & 1u)) return false;
+                    tc::fence_after_sync();
                     const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
                     const uint32_t d = tmem + kColO + 128 * h, p = tmem + kKeys * h;
                     if constexpr (E4) {
+                        const uint64_t vd = tc::smem_desc(vb, 16384, 1024);
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk,
-                                                tc::smem_desc(vb + 4096 * kk, 16384, 1024),
+                                tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
                                                 C::kIdO, (i | t | kk) != 0);
                     } else {
+                        const uint64_t vd = D == 128 ? tc::smem_desc(vb, 1024, 2048)
+                                                     : tc::smem_desc(vb, 16384, 1024);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_bf16_ts(d, p + 8 * kk,
-                                            D == 128 ? tc::smem_desc(vb + 4096 * kk, 1024, 2048)
-                                                     : tc::smem_desc(vb + 2048 * kk, 16384, 1024),
+                            tc::mma_bf16_ts(d, p + 8 * kk, vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
                                             C::kIdO, (i | kk) != 0);
                     }
                     tc::commit(bar(kBarPvDone + h));
                     if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
+                    if (i == 0) ++nitem[h];
+                    ++np[h];
+                    return true;
+                };
+                ok = scores(0, 0) && (r.nb == 0 || scores(1, 0));
+                for (int i = 0; i < r.na && ok; ++i) {
+                    ok = product(0, i) && (i + 1 >= r.na || scores(0, i + 1));
+                    if (ok && i < r.nb) ok = product(1, i) && (i + 1 >= r.nb || scores(1, i + 1));
                 }
-                __syncwarp();
-                if (i == 0) ++nitem[h];
-                ++np[h];
-                return true;
-            };
-            ok = scores(0, 0) && (r.nb == 0 || scores(1, 0));
-            for (int i = 0; i < r.na && ok; ++i) {
-                ok = product(0, i) && (i + 1 >= r.na || scores(0, i + 1));
-                if (ok && i < r.nb) ok = product(1, i) && (i + 1 >= r.nb || scores(1, i + 1));
+                ring += ord.total(r.na);
+                ++items_done;
             }
-            ring += ord.total(r.na);
-            ++items_done;
-        }
-        if (lane == 0) {
             tc::commit(bar(kBarDrain));
             mbar_wait(bar(kBarDrain), 0, a.status);
         }

@@ -83,6 +83,15 @@ __device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
 }
 
+// True in one lane of the (converged) warp.  Issuing MMAs under this rather than
+// under a lane comparison tells the compiler that one thread runs them, so
+// their operands go to uniform registers directly.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r = 0;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
+
 // Arrive once on the mbarrier when every tcgen05 operation this thread has
 // issued so far has completed.
 __device__ __forceinline__ void commit(uint32_t bar) {
