@@ -26,7 +26,7 @@
 // go to the workspace and chunk_merge_kernel joins them.
 //
 // Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
-// warps 4-7 of B, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
+// warps 4-7 of B, one thread a row, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
 // S_B O_A O_B, P over S.  The MMAs of one thread run in order, so S may be
 // overwritten by the next score product once the value product that reads P
 // there is issued.  A row's m rises only when a score exceeds it by more than
@@ -97,11 +97,12 @@ constexpr int kBarEmpty = 10;            // + stage
 constexpr int kBarQFull = 20;
 constexpr int kBarQEmpty = 21;           // commit: the item's score products are done
 constexpr int kBarSFull = 22;            // + half: scores written (commit)
-constexpr int kBarPFull = 24;            // + half: probabilities written (128 arrivals)
-constexpr int kBarPvDone = 26;           // + half: value product done (commit)
-constexpr int kBarOEmpty = 28;           // + half: O read out (128 arrivals)
-constexpr int kBarDrain = 30;
-constexpr uint32_t kOffSlot = 31 * 8;
+constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64 keys written
+                                         // (128 arrivals)
+constexpr int kBarPvDone = 28;           // + half: value product done (commit)
+constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
+constexpr int kBarDrain = 32;
+constexpr uint32_t kOffSlot = 33 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 struct __align__(16) Item {
@@ -394,11 +395,17 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1) {
         "add.rn.f32x2 d, d, a; mov.b64 {%0, %1}, d; }"
         : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1));
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
 // Makes what follows depend on registers a TMEM load has filled (their values
 // are there only after the wait that precedes this).
-__device__ __forceinline__ void pin32(uint32_t *r) {
+template <int N>
+__device__ __forceinline__ void pin(uint32_t *r) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
+    for (int i = 0; i < N; i += 8)
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
                           "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
@@ -446,6 +453,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int h = 0; h < 2; ++h) {
             mbar_init(bar(kBarSFull + h), 1);
             mbar_init(bar(kBarPFull + h), 128);
+            mbar_init(bar(kBarPFull + 2 + h), 128);
             mbar_init(bar(kBarPvDone + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
         }
@@ -631,25 +639,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const uint32_t pos = ord.v(h, i), stage = pos % C::kStages;
                     if (!wait(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
                     if (i == 0 && !wait(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
-                    if (!wait(bar(kBarPFull + h), np[h] & 1u)) return false;
-                    tc::fence_after_sync();
                     const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
                     const uint32_t d = tmem + kColO + 128 * h, p = tmem + kKeys * h;
-                    if constexpr (E4) {
-                        const uint64_t vd = tc::smem_desc(vb, 16384, 1024);
+                    const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
+                                                            : tc::smem_desc(vb, 16384, 1024);
+                    // the first 64 keys' product while the others' softmax goes on
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                    for (int part = 0; part < 2; ++part) {
+                        if (!wait(bar(kBarPFull + 2 * part + h), np[h] & 1u)) return false;
+                        tc::fence_after_sync();
+                        if constexpr (E4) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
-                                                C::kIdO, (i | t | kk) != 0);
-                    } else {
-                        const uint64_t vd = D == 128 ? tc::smem_desc(vb, 1024, 2048)
-                                                     : tc::smem_desc(vb, 16384, 1024);
+                            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_bf16_ts(d, p + 8 * kk, vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
-                                            C::kIdO, (i | kk) != 0);
+                                for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                                    tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk,
+                                                    vd + ((4096 * kk) >> 4), C::kIdO,
+                                                    (i | part | t | (kk & 1)) != 0);
+                        } else {
+#pragma unroll
+                            for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                                tc::mma_bf16_ts(d, p + 8 * kk,
+                                                vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
+                                                C::kIdO, (i | kk) != 0);
+                        }
                     }
                     tc::commit(bar(kBarPvDone + h));
                     if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
@@ -686,10 +699,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int g = it % hkv;
             const int n = h ? r.nb : r.na;
             const int tok0 = r.split ? 0 : h * tpt;      // the half's first token
-            const int tok = tok0 + tok_row;
-            const bool live = tok_row < tpt && tok < r.ntok;
-            const int32_t pos = r.pos + tok;
-            const Order ord{ring, r.split, r.nb};
             float sc = a.scale * kLog2e;
             float m = -INFINITY, l = 0.f;
             if constexpr (E4) {
@@ -697,45 +706,43 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (r.na > 0) {
                     // this half's query rows as two E4M3 terms, scaled by a power
                     // of two that puts the row's largest element in [128, 256)
-                    if (ok) ok = pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
-                                           abort_flag);
-                    if (ok && (h == 0 || !r.split)) {
-                        const uint4 *src = static_cast<const uint4 *>(a.q) +
-                            (int64_t(r.qrow + min(tok, r.ntok - 1)) * a.num_q_heads + g * G +
-                             head_row) * (D / 8);
-                        uint4 x[D / 8];
-                        float big = 0.f;
-                        bool finite = true;
+                    ok = ok && pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
+                                         abort_flag);
+                    const uint4 *src = static_cast<const uint4 *>(a.q) +
+                        (int64_t(r.qrow + min(tok0 + tok_row, r.ntok - 1)) * a.num_q_heads + g * G +
+                         head_row) * (D / 8);
+                    float big = 0.f;
+                    bool finite = true;
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i) x[i] = src[i];
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 x = src[i];
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float u = fabsf(bf16_lo_to_f32(w[e]));
-                                const float v = fabsf(bf16_hi_to_f32(w[e]));
-                                finite = finite && u < INFINITY && v < INFINITY;
-                                big = fmaxf(big, fmaxf(u, v));
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = fabsf(bf16_lo_to_f32(w[e]));
+                            const float v = fabsf(bf16_hi_to_f32(w[e]));
+                            finite = finite && u < INFINITY && v < INFINITY;
+                            big = fmaxf(big, fmaxf(u, v));
                         }
-                        // big = 1.f 2^e: 2^(7 - e), within the normal range
-                        const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
-                        const float up = __uint_as_float(uint32_t(134 - e) << 23);
-                        sc *= __uint_as_float(uint32_t(max(1, 120 + e)) << 23);
-                        if (!finite) sc = __int_as_float(0x7fc00000);   // inf or NaN: a NaN row
+                    }
+                    // big = 1.f 2^e: 2^(7 - e), within the normal range
+                    const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
+                    const float up = __uint_as_float(uint32_t(134 - e) << 23);
+                    sc *= __uint_as_float(uint32_t(120 + e) << 23);
+                    if (!finite) sc = __int_as_float(0x7fc00000);       // inf or NaN: a NaN row
+                    if (ok && (h == 0 || !r.split)) {
                         uint8_t *q0 = base + C::kOffQ + h * C::kQTile + row * 128;
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
+                            const uint4 x0 = src[2 * i], x1 = src[2 * i + 1];
+                            const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
                             uint32_t t0[4], t1[4];
 #pragma unroll
-                            for (int e2 = 0; e2 < 4; ++e2) {
-                                const uint4 &xx = x[2 * i + (e2 >> 1)];
-                                const uint32_t w0 = e2 & 1 ? xx.z : xx.x, w1 = e2 & 1 ? xx.w : xx.y;
-                                e4m3_terms(bf16_lo_to_f32(w0) * up, bf16_hi_to_f32(w0) * up,
-                                           bf16_lo_to_f32(w1) * up, bf16_hi_to_f32(w1) * up,
-                                           t0[e2], t1[e2]);
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                e4m3_terms(bf16_lo_to_f32(w[2 * k]) * up,
+                                           bf16_hi_to_f32(w[2 * k]) * up,
+                                           bf16_lo_to_f32(w[2 * k + 1]) * up,
+                                           bf16_hi_to_f32(w[2 * k + 1]) * up, t0[k], t1[k]);
                             const int off = ((i ^ row) & 7) << 4;
                             *reinterpret_cast<uint4 *>(q0 + off) =
                                 make_uint4(t0[0], t0[1], t0[2], t0[3]);
@@ -744,180 +751,161 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                         fence_proxy_async_smem();
                     }
-                    if (r.split && h == 1) {
-                        // the same rows' scale (their terms are the other half's)
-                        const uint4 *src = static_cast<const uint4 *>(a.q) +
-                            (int64_t(r.qrow + min(tok, r.ntok - 1)) * a.num_q_heads + g * G +
-                             head_row) * (D / 8);
-                        float big = 0.f;
-                        bool finite = true;
-#pragma unroll
-                        for (int i = 0; i < D / 8; ++i) {
-                            const uint4 x = src[i];
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float u = fabsf(bf16_lo_to_f32(w[e]));
-                                const float v = fabsf(bf16_hi_to_f32(w[e]));
-                                finite = finite && u < INFINITY && v < INFINITY;
-                                big = fmaxf(big, fmaxf(u, v));
-                            }
-                        }
-                        const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
-                        sc *= __uint_as_float(uint32_t(max(1, 120 + e)) << 23);
-                        if (!finite) sc = __int_as_float(0x7fc00000);
-                    }
                     mbar_arrive(bar(kBarQFull));
                 }
             }
             if (r.na > 0) ++items_done;
-            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
-            const int32_t pmax = r.pos + r.ntok - 1;
-            // positions of the half's first and last row
-            const int32_t hmin = r.pos + tok0, hmax = r.pos + min(r.ntok - 1, tok0 + tpt - 1);
             const int v0 = r.v0 + (r.split && h ? r.na : 0);
-            for (int i = 0; i < n && ok; ++i) {
+            // Virtual tiles [clear0, clear1): every row of the half sees every key.
+            // Only the others look at positions; they read the item again, so that
+            // the common tiles keep few values in registers.
+            int clear0, clear1;
+            {
+                const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+                const int32_t hmin = r.pos + tok0, hmax = r.pos + min(r.ntok, tok0 + tpt) - 1;
+                clear0 = a.window > 0 && hmax >= a.window ? (hmax - a.window) / kKeys + 1 : 0;
+                clear0 = max(clear0 - tl.gap, tl.sink_tiles);
+                clear1 = max(hmin + 1, 0) / kKeys - tl.gap;
+            }
+            for (int i = 0; i < n; ++i) {
                 const int v = v0 + i;
-                const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                ok = pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                const bool clear = v >= clear0 && v < clear1;
+                ok = ok && pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
+                __syncwarp();
                 tc::fence_after_sync();
                 uint32_t s[kKeys];
 #pragma unroll
                 for (int j = 0; j < kKeys; j += 32) tc::ld32(ts + j, s + j);
                 tc::wait_ld();
 #pragma unroll
-                for (int j = 0; j < kKeys; j += 32) pin32(s + j);
+                for (int j = 0; j < kKeys; j += 32) pin<32>(s + j);
                 // ---- keys this row does not see
-                const bool all_seen =
-                    k0 + kKeys - 1 <= hmin &&
-                    (a.window == 0 || k0 > hmax - a.window || k0 + kKeys - 1 < a.sinks);
-                if (!all_seen) {
-                    const int32_t rel = pos - k0;
+                if (!clear) {
+                    const Item q = read_item(it);
+                    const Tiles tl = tiles_of(q.pos, q.ntok, a.window, a.sinks);
+                    const int32_t p = q.pos + (q.split ? 0 : h * tpt) + tok_row;
+                    const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t see = pos >= 0 ? below(rel + 1, w) : 0u;
+                    for (int w = 0; w < kKeys / 32; ++w) {
+                        uint32_t see = p >= 0 ? below(p - k0 + 1, w) : 0u;
                         if (a.window > 0)
-                            see &= ~below(rel - a.window + 1, w) | below(a.sinks - k0, w);
+                            see &= ~below(p - k0 - a.window + 1, w) | below(a.sinks - k0, w);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!((see >> j) & 1u)) s[32 * w + j] = 0xff800000u;
                     }
                 }
+                // ---- value rows no row of the item sees: zeroed, thread = key
+                if (!clear) {
+                    const Item q = read_item(it);
+                    const Tiles tl = tiles_of(q.pos, q.ntok, a.window, a.sinks);
+                    const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
+                    const int32_t pmax = q.pos + q.ntok - 1;
+                    if (k0 + kKeys - 1 > pmax ||
+                        (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
+                        const Order ord{ring, q.split, q.nb};
+                        const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
+                        ok = ok && pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
+                                             a.status, abort_flag);
+                        const int32_t key = k0 + row;
+                        if (ok && (key > pmax || (key < tl.lo && key >= a.sinks))) {
+                            uint8_t *vt = base + C::kOffRing + stage * C::kStage;
+                            if constexpr (D * C::kElem == 256)
+                                vt += (row >> 3) * 2048 + (row & 7) * 128;
+                            else
+                                vt += row * 128;
+#pragma unroll
+                            for (int c = 0; c < D * C::kElem / 16; ++c)
+                                *reinterpret_cast<uint4 *>(vt + (c >> 3) * 1024 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
                 // ---- row maximum
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float mx[8];
 #pragma unroll
-                for (int j = 0; j < kKeys; j += 8)
+                for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(s[e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(s[j + e])),
-                                      __uint_as_float(s[j + 4 + e]));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int j = 8; j < kKeys; j += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        mx[e] = j + 8 < kKeys ? max3(mx[e], __uint_as_float(s[j + e]),
+                                                     __uint_as_float(s[(j + 8 + e) % kKeys]))
+                                              : fmaxf(mx[e], __uint_as_float(s[j + e]));
+                const float mt = fmaxf(max3(mx[0], mx[1], mx[2]),
+                                       max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
                 if (i == 0) {
                     m = mt;
                 } else if (__any_sync(0xffffffffu, (mt - m) * sc > C::kSlack)) {
-                    // rescale: the last value product into these rows is done first
-                    ok = pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
-                        break;
-                    }
+                    // rescale, once the last value product into these rows is done
+                    ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status,
+                                         abort_flag);
+                    __syncwarp();
                     tc::fence_after_sync();
                     const float mn = fmaxf(m, mt);
                     const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
                     l *= f;
                     m = mn;
 #pragma unroll
-                    for (int j = 0; j < D; j += 32) {
-                        uint32_t o[32];
-                        tc::ld32(to + j, o);
+                    for (int j = 0; j < D; j += 16) {
+                        uint32_t o[16];
+                        tc::ld16(to + j, o);
                         tc::wait_ld();
-                        pin32(o);
+                        pin<16>(o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::st32(to + j, o);
+                        tc::st16(to + j, o);
                     }
                 }
                 const float neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
-                // ---- probabilities, their sum, and their terms into S's columns
+                // ---- probabilities, their sum, and their terms over S's columns,
+                // 64 keys at a time
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < kKeys; j += 4) {
-                    float p[4];
-                    fma2(p[0], p[1], __uint_as_float(s[j]), __uint_as_float(s[j + 1]), sc, sc, neg,
-                         neg);
-                    fma2(p[2], p[3], __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]), sc, sc,
-                         neg, neg);
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t t0[32], t1[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
-                    add2(sum[0], sum[1], p[0], p[1]);
-                    add2(sum[2], sum[3], p[2], p[3]);
-                    if constexpr (E4) {
-                        // terms t of keys j.. at register 32 t + j / 4: the scores of
-                        // those registers are consumed by then (32 t + j / 4 <= j) only
-                        // for t = 0; the second term waits in the register of key j
-                        uint32_t t0, t1;
-                        e4m3_terms(p[0], p[1], p[2], p[3], t0, t1);
-                        s[j] = t0;
-                        s[j + 1] = t1;
-                    } else {
-                        s[j / 2] = pack_bf16x2(p[0], p[1]);
-                        s[j / 2 + 1] = pack_bf16x2(p[2], p[3]);
-                    }
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                if constexpr (E4) {
-                    uint32_t t[64];
+                    for (int j = 0; j < 64; j += 4) {
+                        const uint32_t *x = s + 64 * part + j;
+                        float p[4];
+                        fma2(p[0], p[1], __uint_as_float(x[0]), __uint_as_float(x[1]), sc, sc, neg,
+                             neg);
+                        fma2(p[2], p[3], __uint_as_float(x[2]), __uint_as_float(x[3]), sc, sc, neg,
+                             neg);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        t[j] = s[4 * j];
-                        t[32 + j] = s[4 * j + 1];
-                    }
-                    tc::st32(ts, t);
-                    tc::st32(ts + 32, t + 32);
-                } else {
-                    tc::st32(ts, s);
-                    tc::st32(ts + 32, s + 32);
-                }
-                // ---- value rows no row of the item sees: zeroed, thread = key
-                const bool stale = k0 + kKeys - 1 > pmax ||
-                                   (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys));
-                if (stale) {
-                    const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
-                    ok = pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u, a.status,
-                                   abort_flag);
-                    const int32_t key = k0 + row;
-                    if (ok && (key > pmax || (key < tl.lo && key >= a.sinks))) {
-                        uint8_t *vt = base + C::kOffRing + stage * C::kStage;
-                        if constexpr (D * C::kElem == 256) {
-                            vt += (row >> 3) * 2048 + (row & 7) * 128;
-#pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                *reinterpret_cast<uint4 *>(vt + (c >> 3) * 1024 + (c & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
+                        add2(sum[0], sum[1], p[0], p[1]);
+                        add2(sum[2], sum[3], p[2], p[3]);
+                        if constexpr (E4) {
+                            e4m3_terms(p[0], p[1], p[2], p[3], t0[j / 4], t1[j / 4]);
                         } else {
-                            vt += row * 128;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                *reinterpret_cast<uint4 *>(vt + c * 16) = make_uint4(0, 0, 0, 0);
+                            t0[j / 2] = pack_bf16x2(p[0], p[1]);
+                            t0[j / 2 + 1] = pack_bf16x2(p[2], p[3]);
                         }
                     }
-                    fence_proxy_async_smem();
+                    if constexpr (E4) {
+                        uint32_t u0[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) u0[j] = t0[j];
+                        tc::st16(ts + 16 * part, u0);
+                        tc::st16(ts + 32 + 16 * part, t1);
+                    } else {
+                        tc::st32(ts + 32 * part, t0);
+                    }
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    mbar_arrive(bar(kBarPFull + 2 * part + h));
                 }
-                tc::wait_st();
-                tc::fence_before_sync();
-                mbar_arrive(bar(kBarPFull + h));
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 ++np;
             }
-            ring += ord.total(r.na);
 
             // ---- epilogue
-            if (n > 0 && ok) {
-                ok = pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
+            if (n > 0) {
+                ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
+                __syncwarp();
                 tc::fence_after_sync();
             }
             ok = __all_sync(0xffffffffu, ok);
@@ -925,23 +913,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             if constexpr (E4) inv *= a.v_scale[g];
             float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kShift)) * kLn2 : -INFINITY;
-            if (!ok) lse = nan;
-            const bool direct = r.prow < 0;
-            const int64_t orow = int64_t(r.qrow + tok) * a.num_q_heads + g * G + head_row;
-            const int64_t prow = int64_t(r.prow) + int64_t(g) * r.gstride +
-                                 (r.split ? h * r.ntok * G : 0) + tok * G + head_row;
+            if (!ok) inv = lse = nan;
+            const Item q = read_item(it);
+            ring += Order{ring, q.split, q.nb}.total(q.na);
+            const int tok = (q.split ? 0 : h * tpt) + tok_row;
+            const bool live = tok_row < tpt && tok < q.ntok;
+            const bool direct = q.prow < 0;
+            const int64_t orow = int64_t(q.qrow + tok) * a.num_q_heads + g * G + head_row;
+            const int64_t prow = int64_t(q.prow) + int64_t(g) * q.gstride +
+                                 (q.split ? h * q.ntok * G : 0) + tok * G + head_row;
             // half B of a split item without a tile of its own adds nothing to a direct row
-            const bool writes = live && !(direct && r.split && h == 1);
+            const bool writes = live && !(direct && q.split && h == 1);
 #pragma unroll
             for (int j = 0; j < D; j += 32) {
                 uint32_t o[32];
-                if (n > 0 && ok) {
+                if (n > 0) {
                     tc::ld32(to + j, o);
                     tc::wait_ld();
-                    pin32(o);
+                    pin<32>(o);
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = ok ? 0u : 0x7fc00000u;
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
                 }
                 if (writes && direct) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
@@ -956,7 +948,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 } else if (writes) {
-                    float4 *dst = reinterpret_cast<float4 *>(plan.o_part + prow * D + j);
+                    float4 *dst =
+                        reinterpret_cast<float4 *>(plan.o_part + prow * D + j);
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv,
