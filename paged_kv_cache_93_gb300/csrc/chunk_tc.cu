@@ -26,7 +26,7 @@
 // go to the workspace and chunk_merge_kernel joins them.
 //
 // Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
-// warps 4-7 of B, one thread a row, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
+// warps 4-7 of B, one thread a row, warps 8 and 9 MMA issue, warp 10 TMA.  TMEM, all 512 columns: S_A
 // S_B O_A O_B, P over S.  The MMAs of one thread run in order, so S may be
 // overwritten by the next score product once the value product that reads P
 // there is issued.  A row's m rises only when a score exceeds it by more than
@@ -61,7 +61,7 @@ constexpr int kThreads = 384;             // three warp groups
 // Registers a thread: launched with 168 (384 x 168 = 64,512), the softmax
 // groups then take 216, the issuing group keeps 72 (256 x 216 + 128 x 72).
 constexpr int kSoftRegs = 216, kIssueRegs = 72;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMmaWarp = 8, kLoadWarp = 10;   // kMmaWarp + half
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
@@ -101,8 +101,9 @@ constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64
                                          // (128 arrivals)
 constexpr int kBarPvDone = 28;           // + half: value product done (commit)
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
-constexpr int kBarDrain = 32;
-constexpr uint32_t kOffSlot = 33 * 8;
+constexpr int kBarDrain = 32;            // + half
+constexpr int kBarTurn = 34;             // + half: the other half's block is issued
+constexpr uint32_t kOffSlot = 36 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 struct __align__(16) Item {
@@ -424,6 +425,59 @@ __device__ __forceinline__ void e4m3_terms(float p0, float p1, float p2, float p
         : "=&r"(t0), "=r"(t1) : "r"(a), "r"(b));
 }
 
+// 2^(s sc + neg) of 64 scores: their sums onto `sum`, their terms in t0 (t1).
+// extra(j) is called once for each four scores j .. j + 3.
+template <bool E4, typename F>
+__device__ __forceinline__ void exponentials(const uint32_t *s, float sc, float neg,
+                                             float (&sum)[4], uint32_t (&t0)[32],
+                                             uint32_t (&t1)[16], F extra) {
+    constexpr int kLag = 2;              // groups between an exponential and its use
+    float p[4 * (kLag + 1)];
+#pragma unroll
+    for (int g = 0; g < 16 + kLag; ++g) {
+        if (g < 16) {
+            float *x = p + 4 * (g % (kLag + 1));
+            fma2(x[0], x[1], __uint_as_float(s[4 * g]), __uint_as_float(s[4 * g + 1]), sc, sc, neg,
+                 neg);
+            fma2(x[2], x[3], __uint_as_float(s[4 * g + 2]), __uint_as_float(s[4 * g + 3]), sc, sc,
+                 neg, neg);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e]);
+            extra(4 * g);
+        }
+        if (g >= kLag) {
+            const int d = g - kLag;
+            const float *x = p + 4 * (d % (kLag + 1));
+            add2(sum[0], sum[1], x[0], x[1]);
+            add2(sum[2], sum[3], x[2], x[3]);
+            if constexpr (E4) {
+                e4m3_terms(x[0], x[1], x[2], x[3], t0[d], t1[d]);
+            } else {
+                t0[2 * d] = pack_bf16x2(x[0], x[1]);
+                t0[2 * d + 1] = pack_bf16x2(x[2], x[3]);
+            }
+        }
+    }
+}
+
+// The terms of 64 keys (part 0 or 1 of the tile) to their columns at `ts`, ready
+// for the value product.
+template <bool E4>
+__device__ __forceinline__ void store_terms(uint32_t ts, int part, const uint32_t (&t0)[32],
+                                            const uint32_t (&t1)[16]) {
+    if constexpr (E4) {
+        uint32_t u0[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u0[j] = t0[j];
+        tc::st16(ts + 16 * part, u0);
+        tc::st16(ts + 32 + 16 * part, t1);
+    } else {
+        tc::st32(ts + 32 * part, t0);
+    }
+    tc::wait_st();
+    tc::fence_before_sync();
+}
+
 template <int D, bool E4>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -446,18 +500,19 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), 1);
+            mbar_init(bar(kBarEmpty + s), 2);
         }
         mbar_init(bar(kBarQFull), E4 ? 256 : 1);
-        mbar_init(bar(kBarQEmpty), 1);
+        mbar_init(bar(kBarQEmpty), 2);
         for (int h = 0; h < 2; ++h) {
             mbar_init(bar(kBarSFull + h), 1);
             mbar_init(bar(kBarPFull + h), 128);
             mbar_init(bar(kBarPFull + 2 + h), 128);
             mbar_init(bar(kBarPvDone + h), 1);
+            mbar_init(bar(kBarDrain + h), 1);
+            mbar_init(bar(kBarTurn + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
         }
-        mbar_init(bar(kBarDrain), 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -585,16 +640,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (q_armed) mbar_wait(bar(kBarQFull), q_parity, a.status);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------- MMA issuer
-        // One thread runs the whole role: a wait that is already satisfied costs
-        // it a few tens of cycles, where warp-wide votes and re-elections cost
-        // some 250 each (five of them per tile bound the kernel).
+    } else if (warp < kMmaWarp + 2) {
+        // ---------------------------------------------------------- MMA issuers
+        // One thread for each half.  A thread is held up until its last product
+        // has been taken up and then needs some 200 cycles for commits and waits,
+        // which the other half's products fill: the two take turns (tokens) with
+        // blocks of [value product of step i, score product of step i + 1], so
+        // that one half's softmax runs under the other's products.  (One thread
+        // for both left a quarter of the time idle; without the turns the halves
+        // fall into step and idle together.)
+        const int h = warp - kMmaWarp;
         if (tc::elect_one()) {
             uint32_t ring = 0, items_done = 0;
-            uint32_t np[2] = {0, 0};             // value products issued
-            uint32_t nitem[2] = {0, 0};          // items begun, by half
+            uint32_t np = 0, nitem = 0;          // value products issued, items begun
+            uint32_t turn = 0;                   // blocks issued, or passed over
             bool ok = true;
+            const uint32_t ds = tmem + kKeys * h, dO = tmem + kColO + 128 * h;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return pipe_wait(b, parity, a.status, abort_flag);
             };
@@ -602,84 +663,108 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const Item r = read_item(it);
                 if (r.na == 0) continue;
                 const Order ord{ring, r.split, r.nb};
+                const int n = h ? r.nb : r.na;
+                ring += ord.total(r.na);
                 if (!(ok = wait(bar(kBarQFull), items_done & 1u))) break;
-                auto scores = [&](int h, int i) -> bool {
-                    const uint32_t pos = ord.k(h, i), stage = pos % C::kStages;
-                    if (!wait(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
-                    tc::fence_after_sync();
+                ++items_done;
+                if (n == 0) mbar_arrive(bar(kBarQEmpty));
+                const uint64_t qd =
+                    tc::smem_desc(sb + C::kOffQ + (r.split ? 0 : h) * C::kQTile, 16, 1024);
+                // a tile has two readers; the one of a split item counts twice
+                auto release = [&](uint32_t stage) {
+                    tc::commit(bar(kBarEmpty + stage));
+                    if (r.split) tc::commit(bar(kBarEmpty + stage));
+                };
+                auto take_turn = [&]() {
+                    return wait(bar(kBarTurn + h), (turn & 1u) ^ (h ? 0u : 1u));
+                };
+                auto pass_turn = [&]() {
+                    mbar_arrive(bar(kBarTurn + (h ^ 1)));
+                    ++turn;
+                };
+                auto scores = [&](uint32_t stage) {
                     const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
-                    const uint32_t qb = sb + C::kOffQ + (r.split ? 0 : h) * C::kQTile;
-                    const uint32_t d = tmem + kKeys * h;
-                    const uint64_t qd = tc::smem_desc(qb, 16, 1024);
                     const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
                     if constexpr (E4) {
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_e4m3(d, qd + ((t * C::kHalfTile + 32 * kk) >> 4),
+                                tc::mma_e4m3(ds, qd + ((t * C::kHalfTile + 32 * kk) >> 4),
                                              kd + ((32 * kk) >> 4), C::kIdS, (t | kk) != 0);
                     } else {
 #pragma unroll
                         for (int half = 0; half < D / 64; ++half)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_bf16(d, qd + ((half * C::kHalfTile + 32 * kk) >> 4),
+                                tc::mma_bf16(ds, qd + ((half * C::kHalfTile + 32 * kk) >> 4),
                                              kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
                                              (half | kk) != 0);
                     }
-                    tc::commit(bar(kBarSFull + h));
-                    if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
-                    // the item's last score product frees its queries
-                    if (h == (r.split && r.nb < r.na ? 0 : 1) && i == r.na - 1)
-                        tc::commit(bar(kBarQEmpty));
-                    return true;
                 };
-                auto product = [&](int h, int i) -> bool {
-                    const uint32_t pos = ord.v(h, i), stage = pos % C::kStages;
-                    if (!wait(bar(kBarFull + stage), (pos / C::kStages) & 1u)) return false;
-                    if (i == 0 && !wait(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
-                    const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
-                    const uint32_t d = tmem + kColO + 128 * h, p = tmem + kKeys * h;
-                    const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
-                                                            : tc::smem_desc(vb, 16384, 1024);
-                    // the first 64 keys' product while the others' softmax goes on
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        if (!wait(bar(kBarPFull + 2 * part + h), np[h] & 1u)) return false;
-                        tc::fence_after_sync();
-                        if constexpr (E4) {
-#pragma unroll
-                            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                                    tc::mma_e4m3_ts(d, p + 32 * t + 8 * kk,
-                                                    vd + ((4096 * kk) >> 4), C::kIdO,
-                                                    (i | part | t | (kk & 1)) != 0);
-                        } else {
-#pragma unroll
-                            for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
-                                tc::mma_bf16_ts(d, p + 8 * kk,
-                                                vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
-                                                C::kIdO, (i | kk) != 0);
-                        }
+                // step -1: the first score product; step i: value product i and
+                // score product i + 1
+                for (int i = -1; i < r.na && ok; ++i) {
+                    const bool pv = i >= 0 && i < n, qk = i + 1 < n;
+                    const uint32_t kpos = ord.k(h, i + 1), ks = kpos % C::kStages;
+                    const uint32_t vpos = ord.v(h, max(i, 0)), vs = vpos % C::kStages;
+                    // everything that can be waited for before the turn
+                    ok = !qk || wait(bar(kBarFull + ks), (kpos / C::kStages) & 1u);
+                    if (pv) {
+                        ok = ok && wait(bar(kBarFull + vs), (vpos / C::kStages) & 1u) &&
+                             (i > 0 || wait(bar(kBarOEmpty + h), (nitem & 1u) ^ 1u)) &&
+                             wait(bar(kBarPFull + h), np & 1u);
                     }
-                    tc::commit(bar(kBarPvDone + h));
-                    if (r.split || h == 1) tc::commit(bar(kBarEmpty + stage));
-                    if (i == 0) ++nitem[h];
-                    ++np[h];
-                    return true;
-                };
-                ok = scores(0, 0) && (r.nb == 0 || scores(1, 0));
-                for (int i = 0; i < r.na && ok; ++i) {
-                    ok = product(0, i) && (i + 1 >= r.na || scores(0, i + 1));
-                    if (ok && i < r.nb) ok = product(1, i) && (i + 1 >= r.nb || scores(1, i + 1));
+                    if (!(ok = ok && take_turn())) break;
+                    tc::fence_after_sync();
+                    if (pv) {
+                        const uint32_t vb = sb + C::kOffRing + vs * C::kStage;
+                        const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
+                                                                : tc::smem_desc(vb, 16384, 1024);
+                        // the first 64 keys' product while the others' softmax goes on
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            if (part) {
+                                if (!(ok = wait(bar(kBarPFull + 2 + h), np & 1u))) break;
+                                tc::fence_after_sync();
+                            }
+                            if constexpr (E4) {
+#pragma unroll
+                                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                    for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                                        tc::mma_e4m3_ts(dO, ds + 32 * t + 8 * kk,
+                                                        vd + ((4096 * kk) >> 4), C::kIdO,
+                                                        (i | part | t | (kk & 1)) != 0);
+                            } else {
+#pragma unroll
+                                for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                                    tc::mma_bf16_ts(dO, ds + 8 * kk,
+                                                    vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
+                                                    C::kIdO, (i | kk) != 0);
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                    if (qk) scores(ks);
+                    pass_turn();
+                    // (the value product's end is told with the score product's: a
+                    // rescale needs it only after the next scores)
+                    if (qk) {
+                        tc::commit(bar(kBarSFull + h));
+                        release(ks);
+                        if (i + 1 == n - 1) tc::commit(bar(kBarQEmpty));
+                    }
+                    if (pv) {
+                        tc::commit(bar(kBarPvDone + h));
+                        release(vs);
+                        ++np;
+                    }
                 }
-                ring += ord.total(r.na);
-                ++items_done;
+                if (n > 0) ++nitem;
             }
-            tc::commit(bar(kBarDrain));
-            mbar_wait(bar(kBarDrain), 0, a.status);
+            tc::commit(bar(kBarDrain + h));
+            mbar_wait(bar(kBarDrain + h), 0, a.status);
         }
         __syncwarp();
     }
@@ -773,7 +858,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 ok = ok && pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
-                uint32_t s[kKeys];
+                uint32_t s[kKeys], t0[32], t1[16];
 #pragma unroll
                 for (int j = 0; j < kKeys; j += 32) tc::ld32(ts + j, s + j);
                 tc::wait_ld();
@@ -822,82 +907,53 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         fence_proxy_async_smem();
                     }
                 }
-                // ---- row maximum
-                float mx[8];
+                // ---- probabilities and their terms over S's columns, 64 keys at a
+                // time.  The first 64 are taken with the maximum so far while the
+                // tile's own maximum is found (its instructions fill the gaps of the
+                // exponentials); only if some row's then rises are they taken again.
+                float mt = -INFINITY, neg;
+                float sum[4];
+                for (bool again = false;; again = true) {
+                    neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
+                    sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    exponentials<E4>(s, sc, neg, sum, t0, t1, [&](int j) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx[e] = __uint_as_float(s[e]);
-#pragma unroll
-                for (int j = 8; j < kKeys; j += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mx[e] = j + 8 < kKeys ? max3(mx[e], __uint_as_float(s[j + e]),
-                                                     __uint_as_float(s[(j + 8 + e) % kKeys]))
-                                              : fmaxf(mx[e], __uint_as_float(s[j + e]));
-                const float mt = fmaxf(max3(mx[0], mx[1], mx[2]),
-                                       max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-                if (i == 0) {
-                    m = mt;
-                } else if (__any_sync(0xffffffffu, (mt - m) * sc > C::kSlack)) {
-                    // rescale, once the last value product into these rows is done
-                    ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status,
-                                         abort_flag);
-                    __syncwarp();
-                    tc::fence_after_sync();
+                        for (int e = 0; e < 4; ++e)
+                            mx[e] = max3(mx[e], __uint_as_float(s[j + e]),
+                                         __uint_as_float(s[64 + j + e]));
+                    });
+                    if (again) break;
+                    mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    if (!__any_sync(0xffffffffu, i == 0 || (mt - m) * sc > C::kSlack)) break;
                     const float mn = fmaxf(m, mt);
-                    const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
-                    l *= f;
-                    m = mn;
+                    if (i > 0) {
+                        // rescale, once the last value product into these rows is done
+                        ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status,
+                                             abort_flag);
+                        __syncwarp();
+                        tc::fence_after_sync();
+                        const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
+                        l *= f;
 #pragma unroll
-                    for (int j = 0; j < D; j += 16) {
-                        uint32_t o[16];
-                        tc::ld16(to + j, o);
-                        tc::wait_ld();
-                        pin<16>(o);
+                        for (int j = 0; j < D; j += 16) {
+                            uint32_t o[16];
+                            tc::ld16(to + j, o);
+                            tc::wait_ld();
+                            pin<16>(o);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::st16(to + j, o);
-                    }
-                }
-                const float neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
-                // ---- probabilities, their sum, and their terms over S's columns,
-                // 64 keys at a time
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    uint32_t t0[32], t1[16];
-#pragma unroll
-                    for (int j = 0; j < 64; j += 4) {
-                        const uint32_t *x = s + 64 * part + j;
-                        float p[4];
-                        fma2(p[0], p[1], __uint_as_float(x[0]), __uint_as_float(x[1]), sc, sc, neg,
-                             neg);
-                        fma2(p[2], p[3], __uint_as_float(x[2]), __uint_as_float(x[3]), sc, sc, neg,
-                             neg);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
-                        add2(sum[0], sum[1], p[0], p[1]);
-                        add2(sum[2], sum[3], p[2], p[3]);
-                        if constexpr (E4) {
-                            e4m3_terms(p[0], p[1], p[2], p[3], t0[j / 4], t1[j / 4]);
-                        } else {
-                            t0[j / 2] = pack_bf16x2(p[0], p[1]);
-                            t0[j / 2 + 1] = pack_bf16x2(p[2], p[3]);
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tc::st16(to + j, o);
                         }
                     }
-                    if constexpr (E4) {
-                        uint32_t u0[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) u0[j] = t0[j];
-                        tc::st16(ts + 16 * part, u0);
-                        tc::st16(ts + 32 + 16 * part, t1);
-                    } else {
-                        tc::st32(ts + 32 * part, t0);
-                    }
-                    tc::wait_st();
-                    tc::fence_before_sync();
-                    mbar_arrive(bar(kBarPFull + 2 * part + h));
+                    m = mn;
                 }
+                store_terms<E4>(ts, 0, t0, t1);
+                mbar_arrive(bar(kBarPFull + h));
+                exponentials<E4>(s + 64, sc, neg, sum, t0, t1, [](int) {});
+                store_terms<E4>(ts, 1, t0, t1);
+                mbar_arrive(bar(kBarPFull + 2 + h));
                 l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 ++np;
             }
