@@ -682,24 +682,26 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     mbar_arrive(bar(kBarTurn + (h ^ 1)));
                     ++turn;
                 };
-                auto scores = [&](uint32_t stage) {
+                // part 0 or 1 of the eight products of a tile's scores
+                auto scores = [&](uint32_t stage, int part) {
                     const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
                     const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
                     if constexpr (E4) {
 #pragma unroll
-                        for (int t = 0; t < 2; ++t)
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_e4m3(ds, qd + ((part * C::kHalfTile + 32 * kk) >> 4),
+                                         kd + ((32 * kk) >> 4), C::kIdS, (part | kk) != 0);
+                    } else if constexpr (D == 128) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_e4m3(ds, qd + ((t * C::kHalfTile + 32 * kk) >> 4),
-                                             kd + ((32 * kk) >> 4), C::kIdS, (t | kk) != 0);
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_bf16(ds, qd + ((part * C::kHalfTile + 32 * kk) >> 4),
+                                         kd + ((part * 1024 + 32 * kk) >> 4), C::kIdS,
+                                         (part | kk) != 0);
                     } else {
 #pragma unroll
-                        for (int half = 0; half < D / 64; ++half)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_bf16(ds, qd + ((half * C::kHalfTile + 32 * kk) >> 4),
-                                             kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
-                                             (half | kk) != 0);
+                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                            tc::mma_bf16(ds, qd + ((32 * kk) >> 4), kd + ((32 * kk) >> 4), C::kIdS,
+                                         kk != 0);
                     }
                 };
                 // step -1: the first score product; step i: value product i and
@@ -708,14 +710,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const bool pv = i >= 0 && i < n, qk = i + 1 < n;
                     const uint32_t kpos = ord.k(h, i + 1), ks = kpos % C::kStages;
                     const uint32_t vpos = ord.v(h, max(i, 0)), vs = vpos % C::kStages;
-                    // everything that can be waited for before the turn
+                    // the probabilities come last, so they are waited for last
                     ok = !qk || wait(bar(kBarFull + ks), (kpos / C::kStages) & 1u);
-                    if (pv) {
+                    if (pv)
                         ok = ok && wait(bar(kBarFull + vs), (vpos / C::kStages) & 1u) &&
-                             (i > 0 || wait(bar(kBarOEmpty + h), (nitem & 1u) ^ 1u)) &&
-                             wait(bar(kBarPFull + h), np & 1u);
-                    }
-                    if (!(ok = ok && take_turn())) break;
+                             (i > 0 || wait(bar(kBarOEmpty + h), (nitem & 1u) ^ 1u));
+                    ok = ok && take_turn();
+                    if (pv) ok = ok && wait(bar(kBarPFull + h), np & 1u);
+                    if (!ok) break;
                     tc::fence_after_sync();
                     if (pv) {
                         const uint32_t vb = sb + C::kOffRing + vs * C::kStage;
@@ -746,8 +748,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                         if (!ok) break;
                     }
-                    if (qk) scores(ks);
+                    // (the turn is passed with half of the scores still to issue:
+                    // the other thread needs as long to take it up)
+                    if (qk) scores(ks, 0);
                     pass_turn();
+                    if (qk) scores(ks, 1);
                     // (the value product's end is told with the score product's: a
                     // rescale needs it only after the next scores)
                     if (qk) {
