@@ -23,7 +23,7 @@ size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch
         num_tokens * hq >= (int64_t(1) << 29) ||
         !on_tensor_cores(*c, hq, max_blocks, flags, e4, false))
         return 0;
-    return chunk_tc_workspace(*c, num_tokens, batch, hq, max_blocks);
+    return chunk_tc_workspace(*c, num_tokens, batch, hq);
 }
 
 // Runs a checked call.
@@ -33,7 +33,7 @@ int run(ChunkArgs &a, bool e4, bool values_in_keys, void *workspace, size_t work
                                     values_in_keys);
     if (tc) {
         const size_t need =
-            chunk_tc_workspace(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks);
+            chunk_tc_workspace(a.cache, a.num_tokens, a.batch, a.num_q_heads);
         if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned16(workspace)) return PKV_ERR_ALIGNMENT;
     }

@@ -15,15 +15,14 @@
 // terms exactly; P keeps 2^-8 relative and 2^-17 of the row's largest), so the
 // stored codes feed the tensor cores as they are.
 //
-// Work item = (block of up to 2 tiles' tokens of a sequence, KV head, run of
-// key tiles), made by plan_kernel:
+// Work item = (block of up to 2 tiles' tokens of a sequence, KV head, all of its
+// key tiles or a run of them), given out by plan_kernel:
 //  - a pair item has two row tiles A and B that read the same keys: while the
 //    tensor cores work for one, the CUDA cores take the softmax of the other;
 //  - a block of at most one tile's tokens is a split item: A and B are the
 //    same rows over the first and second half of the item's key tiles.
-// Long runs of keys are cut into items of near-equal length when that
-// shortens the whole (few rows over a long context); their partial (O / l, lse)
-// go to the workspace and chunk_merge_kernel joins them.
+// A cut item's partial (O / l, lse), and the two halves' of a split item, go to
+// the workspace and chunk_merge_kernel joins them.
 //
 // Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
 // warps 4-7 of B, one thread a row, warps 8 and 9 MMA issue, warp 10 TMA.  TMEM, all 512 columns: S_A
@@ -106,23 +105,41 @@ constexpr int kBarTurn = 34;             // + half: the other half's block is is
 constexpr uint32_t kOffSlot = 36 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
-struct __align__(16) Item {
+// A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
+struct __align__(16) Block {
     int32_t b, qrow, pos, ntok;          // sequence; row of q and position of its first token
-    int32_t v0, na, nb, prow;            // first key tile, tiles of A and B; partial row or -1
-    int32_t gstride, split, pad0, pad1;  // partial rows per KV head
+    int32_t tiles, steps, prow, pad;     // key tiles; steps of the whole; partial rows of KV
+                                         // head 0 when taken whole as a split item, or -1
 };
-struct __align__(16) Merge {
-    int32_t qrow, ntok, prow, count;     // tokens; first partial row; partials
+// What a CTA does at a time: some steps of a (block, KV head).
+struct __align__(16) Item {
+    int32_t b, qrow, pos, ntok;
+    int32_t v0, na, nb, prow;            // first key tile, tiles of A and B; partial row or -1
+    int32_t g, split, pad0, pad1;
+};
+// A (block, KV head) cut over several CTAs: its first piece's partials are in slot
+// ctas + cta, the others' in the slots of the `more` CTAs that follow.
+struct __align__(16) Cut {
+    int32_t block, g, cta, more;
 };
 struct Plan {                            // device pointers into the workspace
-    int32_t *header;                     // units, merges
-    Item *items;
-    Merge *merges;
-    int4 *blocks;                        // per query block: sequence, first token, tiles, tokens
+    int32_t *header;
+    Block *blocks;                       // in the order of the work
+    int64_t *before;                     // cost of the blocks before each
     int32_t *first;                      // [batch + 1] query blocks before a sequence
+    int32_t *split;                      // blocks taken as split items with partials
+    uint8_t *is_cut;                     // [(block, KV head)] of the second part of the work
+    Cut *cuts;                           // [ctas]
+    int32_t *piece0;                     // [ctas + 1] first piece of a CTA
+    Item *pieces;
     float *o_part, *lse_part;            // [partial rows][D], [partial rows]
-    int32_t max_units, max_rows;
+    int32_t ctas, slot_rows;             // rows of a slot; slots come first, 2 for each CTA
 };
+constexpr int kHdrBlocks = 0;            // query blocks
+constexpr int kHdrRounds = 1;            // whole items of every CTA
+constexpr int kHdrByHead = 2;            // work order: KV head major
+constexpr int kHdrSplit = 3;             // entries of `split`
+constexpr int kHdrCuts = 4;              // entries of `cuts`
 
 struct Shape {
     int32_t group, tokens_per_tile;
@@ -146,8 +163,57 @@ __device__ __forceinline__ Tiles tiles_of(int32_t pos, int32_t ntok, int32_t win
     return t;
 }
 
+// Steps s0 .. s1 - 1 of a block: a pair item takes one key tile a step, a split
+// item two, its half A the first of its tiles.
+__device__ __forceinline__ Item item_of(const Block &q, int32_t g, int32_t s0, int32_t s1,
+                                        int32_t tpt, int32_t prow) {
+    Item r;
+    r.b = q.b;
+    r.qrow = q.qrow;
+    r.pos = q.pos;
+    r.ntok = q.ntok;
+    r.g = g;
+    r.prow = prow;
+    r.split = q.ntok <= tpt;
+    if (r.split) {
+        r.v0 = 2 * s0;
+        const int32_t tiles = min(q.tiles, 2 * s1) - 2 * s0;
+        r.na = (tiles + 1) >> 1;
+        r.nb = tiles >> 1;
+    } else {
+        r.v0 = s0;
+        r.na = r.nb = s1 - s0;
+    }
+    r.pad0 = r.pad1 = 0;
+    return r;
+}
+
+// Work order: (block r, KV head g) <-> index.
+__device__ __forceinline__ void item_at(int64_t idx, bool by_head, int32_t nblocks, int32_t hkv,
+                                        int32_t &r, int32_t &g) {
+    if (by_head) {
+        g = int32_t(idx / nblocks);
+        r = int32_t(idx - int64_t(g) * nblocks);
+    } else {
+        r = int32_t(idx / hkv);
+        g = int32_t(idx - int64_t(r) * hkv);
+    }
+}
+// The whole item CTA `cta` takes in round k: forth and back, so that the CTAs'
+// sums of a falling sequence stay near.
+__device__ __forceinline__ int64_t round_item(int32_t k, int32_t cta, int32_t ctas) {
+    return int64_t(k) * ctas + (k & 1 ? ctas - 1 - cta : cta);
+}
+
 // ------------------------------------------------------------------- the plan
 constexpr int kPlanThreads = 1024;
+constexpr int kMaxCtas = 512;
+constexpr int kSortBlocks = 2048;        // at most so many query blocks are sorted
+// Costs in steps of an item beside its own, measured (2,048 tokens over 32K
+// keys): an item's start and end, and those of a piece of a cut item, whose
+// partial results (128 KB) go through memory; pieces of fewer steps than
+// kSnap are left to the neighbour.
+constexpr int kItemCost = 3, kPieceCost = 6, kSnap = 6;
 
 // Inclusive scan over the CTA's 1024 threads; `total` gets the sum.
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warp_sums, int64_t &total) {
@@ -174,34 +240,29 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warp_sums, int
     return x + (warp ? warp_sums[warp - 1] : 0);
 }
 
-// Steps of an item: a pair item takes one key tile a step, a split item two.
-__device__ __forceinline__ int32_t steps_of(const int4 &q, int32_t tpt) {
-    return q.w <= tpt ? (q.z + 1) >> 1 : q.z;
-}
-
-// One CTA: query blocks of every sequence, the items' length, the item list.
-// Item lengths: with C steps an item, block i of steps_i steps becomes
-// ceil(steps_i / C) items of near-equal length.  Of 32 values of C (the
-// longest block's fractions and the even share's multiples) the one with the
-// least estimated time is taken: the smaller of two bounds on `ctas` CTAs,
-// waves of the longest item, and the even share plus one item; an item costs
-// kItemCost steps beside its own, one with partial results kPartCost more.
-constexpr int kItemCost = 2, kPartCost = 1;
-
+// One CTA makes the plan.  The work -- every (query block, KV head), longest
+// first unless they are nearly alike -- is given out in two parts: rounds of
+// whole items, one to each CTA, as long as no CTA passes its even share T; then
+// the rest, laid end to end, cut at the points where the CTAs' remaining
+// capacities T - load end.  So few blocks over long contexts are cut over all
+// CTAs evenly, and many blocks are mostly whole.  Nearly alike blocks are
+// ordered by KV head, which keeps the keys that are read at one time few.
 __global__ void __launch_bounds__(kPlanThreads)
-plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh, int32_t ctas) {
+plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     __shared__ int64_t warp_sums[32];
-    __shared__ int64_t red[32];
-    __shared__ int32_t s_max, s_c, s_cost;
+    __shared__ uint32_t keys[kSortBlocks];
+    __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
+    __shared__ int32_t s_max, s_min;
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int32_t hkv = a.cache.num_kv_heads, tpt = sh.tokens_per_tile, per = 2 * tpt;
+    const int32_t ctas = plan.ctas;
     int64_t total;
 
     // ---- query blocks before each sequence
     bool bad = false;
-    int32_t carry = 0;
+    int32_t nblocks = 0;
     for (int base = 0; base < a.batch; base += kPlanThreads) {
         const int b = base + tid;
         int32_t nq = 0;
@@ -211,152 +272,231 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh, int32_t ctas) {
             else nq = (y - x + per - 1) / per;
         }
         const int64_t incl = block_scan(nq, warp_sums, total);
-        if (b < a.batch) plan.first[b] = carry + int32_t(incl) - nq;
-        carry += int32_t(total);
+        if (b < a.batch) plan.first[b] = nblocks + int32_t(incl) - nq;
+        nblocks += int32_t(total);
         if (__syncthreads_or(bad)) break;
+    }
+    if (tid == 0) {
+        s_max = 0;
+        s_min = INT_MAX;
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             raise_status(a.status, PKV_DEV_QUERY_RANGE);
-            plan.header[0] = plan.header[1] = 0;
+            plan.header[kHdrBlocks] = plan.header[kHdrRounds] = plan.header[kHdrSplit] =
+                plan.header[kHdrCuts] = 0;
         }
+        for (int j = tid; j <= ctas; j += kPlanThreads) plan.piece0[j] = 0;
         return;
     }
-    const int32_t nblocks = carry;
-    if (tid == 0) {
-        plan.first[a.batch] = nblocks;
-        s_max = 0;
-        s_cost = INT_MAX;
-        s_c = 1;
-    }
-    __syncthreads();
+    if (tid == 0) plan.first[a.batch] = nblocks;
 
-    // ---- each block's keys
-    int64_t sum = 0;
-    int32_t longest = 0;
-    for (int i = tid; i < nblocks; i += kPlanThreads) {
+    auto block_of = [&](int i) {
         int lo = 0, hi = a.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (plan.first[mid] <= i) lo = mid;
             else hi = mid;
         }
-        const int b = lo;
-        const int32_t q0 = a.cu_q_lens[b], n = a.cu_q_lens[b + 1] - q0;
-        const int32_t t0 = (i - plan.first[b]) * per;
-        int32_t L = a.seq_lens[b];
+        Block q;
+        q.b = lo;
+        const int32_t q0 = a.cu_q_lens[lo], n = a.cu_q_lens[lo + 1] - q0;
+        const int32_t t0 = (i - plan.first[lo]) * per;
+        int32_t L = a.seq_lens[lo];
         if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) {
             raise_status(a.status, PKV_DEV_SEQ_LEN);
             L = 0;
         } else if (L < n) {
             raise_status(a.status, PKV_DEV_SEQ_LEN);
         }
-        const int32_t ntok = min(per, n - t0);
-        const Tiles t = tiles_of(L - n + t0, ntok, a.window, a.sinks);
-        const int4 q = make_int4(b, t0, t.count, ntok);
-        plan.blocks[i] = q;
-        const int32_t steps = steps_of(q, tpt);
-        sum += steps;
-        longest = max(longest, steps);
-    }
-    atomicMax(&s_max, longest);
-    block_scan(sum, warp_sums, total);
-    const int64_t steps_all = total * hkv;
+        q.qrow = q0 + t0;
+        q.pos = L - n + t0;
+        q.ntok = min(per, n - t0);
+        q.tiles = tiles_of(q.pos, q.ntok, a.window, a.sinks).count;
+        q.steps = q.ntok <= tpt ? (q.tiles + 1) >> 1 : q.tiles;
+        q.prow = -1;
+        q.pad = 0;
+        return q;
+    };
+    __syncthreads();
 
-    // ---- the items' length: warp w tries one
-    {
-        int64_t c = warp < 16 ? (s_max + warp) / (warp + 1)
-                              : (steps_all * (warp - 15) + int64_t(ctas) * 8 - 1) / (int64_t(ctas) * 8);
-        c = max(int64_t(1), min(c, int64_t(max(1, s_max))));
-        int64_t units = 0, rows = 0, parts = 0;
-        for (int i = lane; i < nblocks; i += 32) {
-            const int4 q = plan.blocks[i];
-            const int32_t steps = steps_of(q, tpt);
-            const int32_t k = max(1, int32_t((steps + c - 1) / c));
-            const bool split = q.w <= tpt;
-            units += k;
-            if (k > 1 || (split && q.z > 1)) {
-                parts += k;
-                rows += int64_t(k) * (split ? 2 : 1) * q.w * sh.group;
+    // ---- the blocks in order
+    const bool sortable = nblocks <= kSortBlocks;
+    int32_t most = 0, least = INT_MAX;
+    for (int i = tid; i < nblocks; i += kPlanThreads) {
+        const Block q = block_of(i);
+        if (sortable) keys[i] = uint32_t((1 << 20) - 1 - min(q.steps, (1 << 20) - 1)) << 11 | i;
+        most = max(most, q.steps);
+        least = min(least, q.steps);
+    }
+    atomicMax(&s_max, most);
+    atomicMin(&s_min, least);
+    __syncthreads();
+    const bool alike = s_max - s_min <= s_max / 4;
+    const bool by_head = alike;
+    if (sortable && !alike) {
+        int n = 1;
+        while (n < nblocks) n <<= 1;
+        for (int i = nblocks + tid; i < n; i += kPlanThreads) keys[i] = 0xffffffffu;
+        for (int k = 2; k <= n; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                __syncthreads();
+                for (int i = tid; i < n; i += kPlanThreads) {
+                    const int x = i ^ j;
+                    if (x > i) {
+                        const uint32_t u = keys[i], v = keys[x];
+                        if ((u > v) == ((i & k) == 0)) {
+                            keys[i] = v;
+                            keys[x] = u;
+                        }
+                    }
+                }
             }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            units += __shfl_xor_sync(0xffffffffu, units, o);
-            rows += __shfl_xor_sync(0xffffffffu, rows, o);
-            parts += __shfl_xor_sync(0xffffffffu, parts, o);
-        }
-        const bool fits = units <= plan.max_units && rows * hkv <= plan.max_rows;
-        const int64_t extra = units * hkv * kItemCost + parts * hkv * kPartCost;
-        const int64_t waves =
-            (units * hkv + ctas - 1) / ctas * (c + kItemCost + (parts ? kPartCost : 0));
-        const int64_t share = (steps_all + extra) / ctas + c + kItemCost;
-        int64_t cost = min(waves, share);
-        if (cost > (1 << 25)) cost = (1 << 25) + (cost >> 20);
-        if (lane == 0) {
-            red[warp] = c;
-            if (fits) atomicMin(&s_cost, int32_t(min(cost, int64_t(INT_MAX >> 5))) * 32 + warp);
-        }
     }
     __syncthreads();
-    // (the longest block whole always fits: its rows are what max_rows holds)
-    const int64_t c = s_cost == INT_MAX ? max(1, s_max) : red[s_cost & 31];
-
-    // ---- the items
-    int64_t unit0 = 0, row0 = 0, merge0 = 0;
+    int64_t cost_all = 0, nsplit = 0, part_rows = int64_t(2) * ctas * plan.slot_rows;
     for (int base = 0; base < nblocks; base += kPlanThreads) {
         const int i = base + tid;
-        int4 q = make_int4(0, 0, 0, 0);
-        int32_t k = 0, steps = 0, count = 0;
-        bool split = false;
-        if (i < nblocks) {
-            q = plan.blocks[i];
-            steps = steps_of(q, tpt);
-            split = q.w <= tpt;
-            k = max(1, int32_t((steps + c - 1) / c));
-            count = k > 1 || (split && q.z > 1) ? k * (split ? 2 : 1) : 0;
+        Block q = {};
+        const bool in = i < nblocks;
+        if (in) q = block_of(sortable ? int(keys[i] & (kSortBlocks - 1)) : i);
+        const bool halves = in && q.ntok <= tpt && q.tiles > 1;
+        const int64_t cost = in ? q.steps + kItemCost : 0;
+        const int64_t c = block_scan(cost, warp_sums, total);
+        if (in) plan.before[i] = cost_all + c - cost;
+        cost_all += total;
+        const int64_t s = block_scan(halves, warp_sums, total);
+        if (halves) plan.split[nsplit + s - 1] = i;
+        nsplit += total;
+        const int64_t rows = halves ? int64_t(2) * q.ntok * sh.group * hkv : 0;
+        const int64_t r = block_scan(rows, warp_sums, total);
+        if (halves) q.prow = int32_t(part_rows + r - rows);
+        part_rows += total;
+        if (in) plan.blocks[i] = q;
+    }
+    if (tid == 0) plan.before[nblocks] = cost_all;
+    __syncthreads();
+
+    // ---- whole rounds
+    const int64_t n_items = int64_t(nblocks) * hkv;
+    const int64_t share = (cost_all * hkv + int64_t(ctas) * kPieceCost + ctas - 1) / ctas;
+    int64_t load = 0;
+    int32_t rounds = 0;
+    while ((rounds + 1) * int64_t(ctas) <= n_items) {
+        int64_t next = load;
+        if (tid < ctas) {
+            int32_t r, g;
+            item_at(round_item(rounds, tid, ctas), by_head, nblocks, hkv, r, g);
+            next += plan.blocks[r].steps + kItemCost;
         }
-        const int64_t rows = int64_t(count) * q.w * sh.group * hkv;
-        const int64_t u = block_scan(k, warp_sums, total) - k + unit0;
-        unit0 += total;
-        const int64_t r = block_scan(rows, warp_sums, total) - rows + row0;
-        row0 += total;
-        const int64_t m = block_scan(count > 0, warp_sums, total) - (count > 0) + merge0;
-        merge0 += total;
-        if (i < nblocks) {
-            const int32_t q0 = a.cu_q_lens[q.x], n = a.cu_q_lens[q.x + 1] - q0;
-            int32_t L = a.seq_lens[q.x];
-            if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) L = 0;
-            if (count) plan.merges[m] = {q0 + q.y, q.w, int32_t(r), count};
-            const int32_t tile_rows = q.w * sh.group;
-            for (int j = 0; j < k; ++j) {
-                const int32_t s0 = int32_t(int64_t(steps) * j / k);
-                const int32_t s1 = int32_t(int64_t(steps) * (j + 1) / k);
-                Item it = {};
-                it.b = q.x;
-                it.qrow = q0 + q.y;
-                it.pos = L - n + q.y;
-                it.ntok = q.w;
-                it.split = split;
-                if (split) {
-                    // tiles 2 s0 .. 2 s1 (the last may be missing): A the first half
-                    it.v0 = 2 * s0;
-                    const int32_t tiles = min(q.z, 2 * s1) - 2 * s0;
-                    it.na = (tiles + 1) >> 1;
-                    it.nb = tiles >> 1;
-                } else {
-                    it.v0 = s0;
-                    it.na = it.nb = s1 - s0;
-                }
-                it.prow = count ? int32_t(r) + j * (split ? 2 : 1) * tile_rows : -1;
-                it.gstride = count * tile_rows;
-                plan.items[u + j] = it;
+        if (__syncthreads_or(next > share)) break;
+        load = next;
+        ++rounds;
+    }
+
+    // ---- the rest, cut by the capacities left
+    const int64_t idx0 = int64_t(rounds) * ctas;
+    int32_t r0 = 0, g0 = 0;
+    if (idx0 < n_items) item_at(idx0, by_head, nblocks, hkv, r0, g0);
+    const int64_t done =
+        idx0 >= n_items ? cost_all * hkv
+        : by_head       ? g0 * cost_all + plan.before[r0]
+                        : plan.before[r0] * hkv + g0 * int64_t(plan.blocks[r0].steps + kItemCost);
+    const int64_t rest = cost_all * hkv - done;
+    for (int64_t i = idx0 + tid; i < n_items; i += kPlanThreads) plan.is_cut[i - idx0] = 0;
+    const int64_t cap = tid < ctas ? max(int64_t(0), share - kPieceCost - load) : 0;
+    const int64_t upto = block_scan(cap, warp_sums, total);
+    if (tid == 0) {
+        cut_idx[0] = int32_t(idx0);
+        cut_step[0] = 0;
+    }
+    if (tid < ctas) {
+        // the end of CTA tid's part: position x of the rest
+        int64_t idx = n_items;
+        int32_t step = 0;
+        if (rest > 0 && tid < ctas - 1 && total > 0) {
+            const int64_t x = done + int64_t(double(rest) * (double(upto) / double(total)));
+            int64_t y = x;
+            int32_t g = 0;
+            if (by_head) {
+                g = int32_t(min(x / cost_all, int64_t(hkv - 1)));
+                y = x - g * cost_all;
+            } else {
+                y = x / hkv;
+            }
+            int lo = 0, hi = nblocks;            // before[lo] <= y < before[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan.before[mid] <= y) lo = mid;
+                else hi = mid;
+            }
+            const int32_t steps = plan.blocks[lo].steps;
+            int64_t off = y - plan.before[lo];
+            if (!by_head) {
+                off = x - plan.before[lo] * hkv;
+                g = int32_t(min(off / (steps + kItemCost), int64_t(hkv - 1)));
+                off -= g * int64_t(steps + kItemCost);
+            }
+            idx = by_head ? int64_t(g) * nblocks + lo : int64_t(lo) * hkv + g;
+            step = int32_t(min(max(off - kItemCost, int64_t(0)), int64_t(steps)));
+            if (step < kSnap) step = 0;
+            else if (steps - step < kSnap) {
+                step = 0;
+                ++idx;
+            }
+            if (idx < idx0) {
+                idx = idx0;
+                step = 0;
+            }
+        }
+        cut_idx[tid + 1] = int32_t(idx);
+        cut_step[tid + 1] = step;
+    }
+    __syncthreads();
+    int32_t i0 = 0, i1 = 0, s0 = 0, s1 = 0, count = 0, cut = 0;
+    if (tid < ctas) {
+        i0 = cut_idx[tid];
+        s0 = cut_step[tid];
+        i1 = cut_idx[tid + 1];
+        s1 = cut_step[tid + 1];
+        // (a part inside one item may be empty: its zero steps still fill its slot)
+        count = i1 - i0 + (s1 > 0);
+        // this part begins an item that goes on
+        cut = s1 > 0 && (i1 > i0 || s0 == 0);
+    }
+    const int64_t p1 = block_scan(count, warp_sums, total);
+    const int64_t npieces = total;
+    const int64_t c1 = block_scan(cut, warp_sums, total);
+    if (tid < ctas) {
+        plan.piece0[tid] = int32_t(p1 - count);
+        for (int k = 0; k < count; ++k) {
+            const int32_t idx = i0 + k, from = k ? 0 : s0;
+            int32_t r, g;
+            item_at(idx, by_head, nblocks, hkv, r, g);
+            const Block q = plan.blocks[r];
+            const int32_t to = idx == i1 ? s1 : q.steps;
+            int32_t prow;
+            if (from > 0) prow = tid * plan.slot_rows;
+            else if (to < q.steps) prow = (ctas + tid) * plan.slot_rows;
+            else prow = q.prow < 0 ? -1 : q.prow + g * 2 * q.ntok * sh.group;
+            plan.pieces[p1 - count + k] = item_of(q, g, from, to, tpt, prow);
+            if (from == 0 && to < q.steps) {
+                int more = 0;
+                while (tid + 1 + more < ctas && cut_idx[tid + 1 + more] == idx &&
+                       cut_step[tid + 1 + more] > 0)
+                    ++more;
+                plan.cuts[c1 - 1] = {r, g, tid, more};
+                plan.is_cut[idx - idx0] = 1;
             }
         }
     }
     if (tid == 0) {
-        plan.header[0] = int32_t(unit0);
-        plan.header[1] = int32_t(merge0);
+        plan.piece0[ctas] = int32_t(npieces);
+        plan.header[kHdrBlocks] = nblocks;
+        plan.header[kHdrRounds] = rounds;
+        plan.header[kHdrByHead] = by_head;
+        plan.header[kHdrSplit] = int32_t(nsplit);
+        plan.header[kHdrCuts] = int32_t(total);
     }
 }
 
@@ -530,14 +670,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint32_t tmem = *tslot;
     pdl_launch_dependents();
     pdl_wait();
-    const int num_items = plan.header[0] * hkv;
+    const int rounds = plan.header[kHdrRounds], piece0 = plan.piece0[blockIdx.x];
+    const int num_items = rounds + plan.piece0[blockIdx.x + 1] - piece0;
+    // this CTA's item `it`: whole ones first, then its pieces
     auto read_item = [&](int it) {
         Item r;
-        const int4 *p = reinterpret_cast<const int4 *>(plan.items + it / hkv);
-        int4 *d = reinterpret_cast<int4 *>(&r);
-        d[0] = p[0];
-        d[1] = p[1];
-        d[2] = p[2];
+        if (it >= rounds) {
+            const int4 *p = reinterpret_cast<const int4 *>(plan.pieces + piece0 + it - rounds);
+            int4 *d = reinterpret_cast<int4 *>(&r);
+            d[0] = p[0];
+            d[1] = p[1];
+            d[2] = p[2];
+        } else {
+            int32_t blk, g;
+            item_at(round_item(it, blockIdx.x, plan.ctas), plan.header[kHdrByHead] != 0,
+                    plan.header[kHdrBlocks], hkv, blk, g);
+            Block q;
+            const int4 *p = reinterpret_cast<const int4 *>(plan.blocks + blk);
+            int4 *d = reinterpret_cast<int4 *>(&q);
+            d[0] = p[0];
+            d[1] = p[1];
+            r = item_of(q, g, 0, q.steps, tpt, q.prow < 0 ? -1 : q.prow + g * 2 * q.ntok * G);
+        }
         return r;
     };
 
@@ -551,10 +705,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         uint32_t armed = 0, armed_parity = 0;
         uint32_t q_armed = 0, q_parity = 0;
         bool ok = true;
-        for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
+        for (int it = 0; it < num_items && ok; ++it) {
             const Item r = read_item(it);
             if (r.na == 0) continue;
-            const int g = it % hkv;
+            const int g = r.g;
             const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
             const int32_t pmax = r.pos + r.ntok - 1;
             const int32_t *table = a.block_tables + int64_t(r.b) * a.max_blocks;
@@ -659,7 +813,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return pipe_wait(b, parity, a.status, abort_flag);
             };
-            for (int it = blockIdx.x; it < num_items && ok; it += gridDim.x) {
+            for (int it = 0; it < num_items && ok; ++it) {
                 const Item r = read_item(it);
                 if (r.na == 0) continue;
                 const Order ord{ring, r.split, r.nb};
@@ -784,9 +938,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int tok_row = row / G, head_row = row - tok_row * G;
         uint32_t ring = 0, np = 0, items_done = 0;
         bool ok = true;
-        for (int it = blockIdx.x; it < num_items; it += gridDim.x) {
+        for (int it = 0; it < num_items; ++it) {
             const Item r = read_item(it);
-            const int g = it % hkv;
+            const int g = r.g;
             const int n = h ? r.nb : r.na;
             const int tok0 = r.split ? 0 : h * tpt;      // the half's first token
             float sc = a.scale * kLog2e;
@@ -981,8 +1135,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const bool live = tok_row < tpt && tok < q.ntok;
             const bool direct = q.prow < 0;
             const int64_t orow = int64_t(q.qrow + tok) * a.num_q_heads + g * G + head_row;
-            const int64_t prow = int64_t(q.prow) + int64_t(g) * q.gstride +
-                                 (q.split ? h * q.ntok * G : 0) + tok * G + head_row;
+            const int64_t prow = int64_t(q.prow) + (q.split ? h * q.ntok * G : 0) + tok * G + head_row;
             // half B of a split item without a tile of its own adds nothing to a direct row
             const bool writes = live && !(direct && q.split && h == 1);
 #pragma unroll
@@ -1050,29 +1203,63 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     pdl_wait();
     pdl_launch_dependents();
     const int hkv = a.cache.num_kv_heads, G = sh.group;
-    const int chunks = (2 * kRows + kRowsPerCta - 1) / kRowsPerCta;
-    const int64_t total = int64_t(plan.header[1]) * hkv * chunks;
+    // the split items taken whole (two partials of at most kRows rows each), then the cuts
+    constexpr int kHalfChunks = kRows / kRowsPerCta, kChunks = 2 * kHalfChunks;
+    const int64_t n_half = int64_t(plan.header[kHdrSplit]) * hkv * kHalfChunks;
+    const int64_t total = n_half + int64_t(plan.header[kHdrCuts]) * kChunks;
     const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    const int nblocks = plan.header[kHdrBlocks];
+    const int64_t idx0 = int64_t(plan.header[kHdrRounds]) * plan.ctas;
     for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-        const int64_t mg = w / chunks;
-        const Merge m = plan.merges[mg / hkv];
-        const int g = int(mg % hkv), rows = m.ntok * G;
-        const int row = int(w % chunks) * kRowsPerCta + sub;
+        int blk, g, row, count, halves = 2;
+        int64_t first, next;                 // rows of the first piece, and of the others'
+        if (w < n_half) {
+            const int64_t sg = w / kHalfChunks;
+            blk = plan.split[sg / hkv];
+            g = int(sg % hkv);
+            row = int(w % kHalfChunks) * kRowsPerCta + sub;
+            const int64_t idx =
+                plan.header[kHdrByHead] ? int64_t(g) * nblocks + blk : int64_t(blk) * hkv + g;
+            if (idx >= idx0 && plan.is_cut[idx - idx0]) continue;
+            count = 2;
+            first = next = 0;
+        } else {
+            const Cut cut = plan.cuts[(w - n_half) / kChunks];
+            blk = cut.block;
+            g = cut.g;
+            row = int((w - n_half) % kChunks) * kRowsPerCta + sub;
+            count = 1 + cut.more;
+            first = int64_t(plan.ctas + cut.cta) * plan.slot_rows;
+            next = int64_t(cut.cta) * plan.slot_rows;
+        }
+        const Block m = plan.blocks[blk];
+        const int rows = m.ntok * G;
         if (row >= rows) continue;
-        const int64_t first = int64_t(m.prow) + int64_t(g) * m.count * rows + row;
-        const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + first * kLanes + c;
+        if (w < n_half) {
+            first = next = m.prow + int64_t(g) * 2 * rows;
+        } else {
+            halves = m.ntok <= sh.tokens_per_tile ? 2 : 1;
+            count *= halves;
+        }
+        // partial p: piece p / halves, half p % halves
+        auto at = [&](int p) {
+            const int piece = halves == 2 ? p >> 1 : p;
+            return (piece ? next + int64_t(piece) * plan.slot_rows : first) +
+                   (halves == 2 ? (p & 1) * rows : 0) + row;
+        };
+        const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + c;
         float M = -INFINITY, W = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         bool broken = false;
-        for (int p0 = 0; p0 < m.count; p0 += 8) {
+        for (int p0 = 0; p0 < count; p0 += 8) {
             float l[8];
             float4 x[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const bool in = p0 + u < m.count;
-                const int64_t at = int64_t(p0 + u) * rows;
-                l[u] = in ? plan.lse_part[first + at] : -INFINITY;
-                x[u] = in ? op[at * kLanes] : make_float4(0.f, 0.f, 0.f, 0.f);
+                const bool in = p0 + u < count;
+                const int64_t r = in ? at(p0 + u) : 0;
+                l[u] = in ? plan.lse_part[r] : -INFINITY;
+                x[u] = in ? op[r * kLanes] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
             float mc = M;
 #pragma unroll
@@ -1152,37 +1339,41 @@ Shape shape_of(int32_t hq, int32_t hkv) {
 }
 
 struct Sizes {
-    int64_t blocks, units, rows;
-    size_t items, merges, blocks_at, first, o_part, lse_part, total;
+    int64_t blocks, rows, slot_rows;
+    int32_t ctas;
+    size_t blocks_at, before, first, split, is_cut, cuts, piece0, pieces, o_part, lse_part, total;
 };
 
-// Most query blocks: every sequence's last one may be short.  Partial rows:
-// every token of a split item gives two partials (its block is its sequence's
-// only or last, at most tokens_per_tile of them), and kSpare CTAs' worth of
-// full blocks may be cut further.
-constexpr int kSpare = 4;
-
-Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32_t hq,
-               int32_t max_blocks) {
+// Most query blocks: every sequence's last one may be short.  Partial rows: two
+// slots for each CTA, and two partials for every token of a block taken as a
+// split item (its sequence's only or last block, at most tokens_per_tile of it).
+Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32_t hq) {
     const Shape sh = shape_of(hq, c.num_kv_heads);
     Sizes s;
-    const int64_t per = 2 * sh.tokens_per_tile;
-    s.blocks = std::min(num_tokens, num_tokens / per + batch);
-    const int64_t tiles = (int64_t(max_blocks) * c.block_size + kKeys - 1) / kKeys + 1;
-    // items of all KV heads that cutting may add
-    const int64_t spare = int64_t(sm_count()) * kSpare;
-    s.units = s.blocks + std::min(spare, s.blocks * tiles);
-    const int64_t split_rows = 2 * std::min(num_tokens, int64_t(batch) * sh.tokens_per_tile) * hq;
-    const int64_t most = num_tokens * hq * tiles;          // one partial per row and tile
-    s.rows = std::min(split_rows + spare * 2 * kRows, std::max<int64_t>(most, 1));
-    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    s.items = 256;
-    s.merges = up(s.items + s.units * sizeof(Item));
-    s.blocks_at = up(s.merges + s.blocks * sizeof(Merge));
-    s.first = up(s.blocks_at + s.blocks * sizeof(int4));
-    s.lse_part = up(s.first + (size_t(batch) + 1) * 4);
-    s.o_part = up(s.lse_part + s.rows * 4);
-    s.total = up(s.o_part + size_t(s.rows) * c.head_dim_v * 4);
+    s.ctas = std::min(sm_count(), kMaxCtas);
+    s.blocks = std::min(num_tokens, num_tokens / (2 * sh.tokens_per_tile) + batch);
+    s.slot_rows = std::min<int64_t>(2 * kRows, 2 * num_tokens * sh.group);
+    s.rows = 2 * s.ctas * s.slot_rows +
+             2 * std::min(num_tokens, int64_t(batch) * sh.tokens_per_tile) * hq;
+    const size_t items = size_t(s.blocks) * c.num_kv_heads;
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at = (at + bytes + 255) & ~size_t(255);
+        return here;
+    };
+    s.blocks_at = take(s.blocks * sizeof(Block));
+    s.before = take((s.blocks + 1) * sizeof(int64_t));
+    s.first = take((size_t(batch) + 1) * sizeof(int32_t));
+    s.split = take(s.blocks * sizeof(int32_t));
+    s.is_cut = take(items);
+    s.cuts = take(s.ctas * sizeof(Cut));
+    s.piece0 = take((s.ctas + 1) * sizeof(int32_t));
+    // pieces: the rest's items (all of them when no round fits) and one more per cut
+    s.pieces = take((items + s.ctas) * sizeof(Item));
+    s.lse_part = take(s.rows * sizeof(float));
+    s.o_part = take(size_t(s.rows) * c.head_dim_v * sizeof(float));
+    s.total = at;
     return s;
 }
 
@@ -1191,15 +1382,19 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
     using C = Cfg<D, E4>;
     auto kernel = chunk_tc_kernel<D, E4>;
     const Shape sh = shape_of(a.num_q_heads, a.cache.num_kv_heads);
-    const Sizes sz = sizes_of(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks);
+    const Sizes sz = sizes_of(a.cache, a.num_tokens, a.batch, a.num_q_heads);
     const Plan plan{reinterpret_cast<int32_t *>(ws),
-                    reinterpret_cast<Item *>(ws + sz.items),
-                    reinterpret_cast<Merge *>(ws + sz.merges),
-                    reinterpret_cast<int4 *>(ws + sz.blocks_at),
+                    reinterpret_cast<Block *>(ws + sz.blocks_at),
+                    reinterpret_cast<int64_t *>(ws + sz.before),
                     reinterpret_cast<int32_t *>(ws + sz.first),
+                    reinterpret_cast<int32_t *>(ws + sz.split),
+                    ws + sz.is_cut,
+                    reinterpret_cast<Cut *>(ws + sz.cuts),
+                    reinterpret_cast<int32_t *>(ws + sz.piece0),
+                    reinterpret_cast<Item *>(ws + sz.pieces),
                     reinterpret_cast<float *>(ws + sz.o_part),
                     reinterpret_cast<float *>(ws + sz.lse_part),
-                    int32_t(sz.units), int32_t(sz.rows)};
+                    sz.ctas, int32_t(sz.slot_rows)};
     const int64_t rows = int64_t(a.cache.num_blocks) * a.cache.num_kv_heads * a.cache.block_size;
     const int box = std::min(a.cache.block_size, kKeys);
     CUtensorMap tq = {}, tk, tv;
@@ -1222,18 +1417,15 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
             return PKV_ERR_CUDA;
         configured_dev = dev;
     }
-    const int ctas = sm_count();
-    int rc = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, plan, sh,
-                        int32_t(ctas));
+    int rc = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, plan, sh);
     if (rc != PKV_OK) return rc;
-    const int grid =
-        int(std::min<int64_t>(ctas, std::max<int64_t>(1, sz.units * a.cache.num_kv_heads)));
-    rc = launch_pdl(kernel, dim3(grid), dim3(kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
+    rc = launch_pdl(kernel, dim3(sz.ctas), dim3(kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
                     sh);
     if (rc != PKV_OK) return rc;
-    const int64_t merge_work = sz.blocks * a.cache.num_kv_heads * (2 * kRows * D / 4 / kMergeThreads);
+    const int64_t merge_rows = std::min<int64_t>(sz.rows, int64_t(a.num_tokens) * a.num_q_heads);
+    const int64_t merge_work = (merge_rows * (D / 4) + kMergeThreads - 1) / kMergeThreads;
     return launch_pdl(chunk_merge_kernel<D>,
-                      dim3(unsigned(std::min<int64_t>(merge_work, int64_t(ctas) * 8))),
+                      dim3(unsigned(std::min<int64_t>(merge_work, int64_t(sz.ctas) * 8))),
                       dim3(kMergeThreads), 0, a.stream, a, plan, sh);
 }
 
@@ -1250,8 +1442,8 @@ bool chunk_tc_supports(const pkv_cache_desc &c, int32_t num_q_heads, int32_t max
 }
 
 size_t chunk_tc_workspace(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch,
-                          int32_t num_q_heads, int32_t max_blocks) {
-    return sizes_of(c, num_tokens, batch, num_q_heads, max_blocks).total;
+                          int32_t num_q_heads) {
+    return sizes_of(c, num_tokens, batch, num_q_heads).total;
 }
 
 int launch_chunk_tc(const ChunkArgs &in, void *workspace) {

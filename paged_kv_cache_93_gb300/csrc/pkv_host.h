@@ -179,7 +179,7 @@ int launch_chunk_generic_e4m3(const ChunkArgs &a);
 // The tensor-core form (E4M3 when a.k_scale is set), its shapes and workspace.
 bool chunk_tc_supports(const pkv_cache_desc &c, int32_t num_q_heads, int32_t max_blocks, bool e4);
 size_t chunk_tc_workspace(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch,
-                          int32_t num_q_heads, int32_t max_blocks);
+                          int32_t num_q_heads);
 int launch_chunk_tc(const ChunkArgs &a, void *workspace);
 
 int launch_lse_merge(int32_t num_parts, const float *out_part, const float *lse_part,
