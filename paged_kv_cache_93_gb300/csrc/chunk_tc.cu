@@ -25,7 +25,7 @@
 // the workspace and chunk_merge_kernel joins them.
 //
 // Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
-// warps 4-7 of B, one thread a row, warps 8 and 9 MMA issue, warp 10 TMA.  TMEM, all 512 columns: S_A
+// warps 4-7 of B, one thread a row, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
 // S_B O_A O_B, P over S.  The MMAs of one thread run in order, so S may be
 // overwritten by the next score product once the value product that reads P
 // there is issued.  A row's m rises only when a score exceeds it by more than
@@ -58,9 +58,9 @@ constexpr int kRows = 128;               // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kThreads = 384;             // three warp groups
 // Registers a thread: launched with 168 (384 x 168 = 64,512), the softmax
-// groups then take 216, the issuing group keeps 72 (256 x 216 + 128 x 72).
-constexpr int kSoftRegs = 216, kIssueRegs = 72;
-constexpr int kMmaWarp = 8, kLoadWarp = 10;   // kMmaWarp + half
+// groups then take 200, the issuing group keeps 104 (256 x 200 + 128 x 104).
+constexpr int kSoftRegs = 200, kIssueRegs = 104;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
@@ -100,9 +100,8 @@ constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64
                                          // (128 arrivals)
 constexpr int kBarPvDone = 28;           // + half: value product done (commit)
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
-constexpr int kBarDrain = 32;            // + half
-constexpr int kBarTurn = 34;             // + half: the other half's block is issued
-constexpr uint32_t kOffSlot = 36 * 8;
+constexpr int kBarDrain = 32;
+constexpr uint32_t kOffSlot = 33 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -640,17 +639,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), 2);
+            mbar_init(bar(kBarEmpty + s), 1);
         }
         mbar_init(bar(kBarQFull), E4 ? 256 : 1);
-        mbar_init(bar(kBarQEmpty), 2);
+        mbar_init(bar(kBarQEmpty), 1);
+        mbar_init(bar(kBarDrain), 1);
         for (int h = 0; h < 2; ++h) {
             mbar_init(bar(kBarSFull + h), 1);
             mbar_init(bar(kBarPFull + h), 128);
             mbar_init(bar(kBarPFull + 2 + h), 128);
             mbar_init(bar(kBarPvDone + h), 1);
-            mbar_init(bar(kBarDrain + h), 1);
-            mbar_init(bar(kBarTurn + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
         }
         *abort_flag = 0;
@@ -794,22 +792,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (q_armed) mbar_wait(bar(kBarQFull), q_parity, a.status);
         }
         __syncwarp();
-    } else if (warp < kMmaWarp + 2) {
-        // ---------------------------------------------------------- MMA issuers
-        // One thread for each half.  A thread is held up until its last product
-        // has been taken up and then needs some 200 cycles for commits and waits,
-        // which the other half's products fill: the two take turns (tokens) with
-        // blocks of [value product of step i, score product of step i + 1], so
-        // that one half's softmax runs under the other's products.  (One thread
-        // for both left a quarter of the time idle; without the turns the halves
-        // fall into step and idle together.)
-        const int h = warp - kMmaWarp;
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        // One thread issues blocks of [value product of step i, score product of
+        // step i + 1], half A's and half B's in turn, so that one half's softmax
+        // runs under the other's products.  The thread is held up until its last
+        // product has been taken up; what it then does before the next one
+        // (commits, waits of some 50 cycles even when satisfied) would leave the
+        // tensor cores idle.  So the next block's waits are tried before the last
+        // four products of a block are issued, and the commits follow the block.
         if (tc::elect_one()) {
             uint32_t ring = 0, items_done = 0;
-            uint32_t np = 0, nitem = 0;          // value products issued, items begun
-            uint32_t turn = 0;                   // blocks issued, or passed over
+            uint32_t np[2] = {0, 0};             // value products issued
+            uint32_t nitem[2] = {0, 0};          // items begun, by half
             bool ok = true;
-            const uint32_t ds = tmem + kKeys * h, dO = tmem + kColO + 128 * h;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return pipe_wait(b, parity, a.status, abort_flag);
             };
@@ -817,113 +813,125 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const Item r = read_item(it);
                 if (r.na == 0) continue;
                 const Order ord{ring, r.split, r.nb};
-                const int n = h ? r.nb : r.na;
-                ring += ord.total(r.na);
                 if (!(ok = wait(bar(kBarQFull), items_done & 1u))) break;
-                ++items_done;
-                if (n == 0) mbar_arrive(bar(kBarQEmpty));
-                const uint64_t qd =
-                    tc::smem_desc(sb + C::kOffQ + (r.split ? 0 : h) * C::kQTile, 16, 1024);
-                // a tile has two readers; the one of a split item counts twice
-                auto release = [&](uint32_t stage) {
-                    tc::commit(bar(kBarEmpty + stage));
-                    if (r.split) tc::commit(bar(kBarEmpty + stage));
-                };
-                auto take_turn = [&]() {
-                    return wait(bar(kBarTurn + h), (turn & 1u) ^ (h ? 0u : 1u));
-                };
-                auto pass_turn = [&]() {
-                    mbar_arrive(bar(kBarTurn + (h ^ 1)));
-                    ++turn;
-                };
-                // part 0 or 1 of the eight products of a tile's scores
-                auto scores = [&](uint32_t stage, int part) {
+                const uint64_t qd = tc::smem_desc(sb + C::kOffQ, 16, 1024);
+                // part 0 or 1 of the products of a tile's scores
+                auto scores = [&](int h, uint32_t stage, int part) {
+                    const uint32_t ds = tmem + kKeys * h;
                     const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
                     const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
+                    const uint64_t q = qd + (r.split || h == 0 ? 0 : C::kQTile >> 4);
                     if constexpr (E4) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_e4m3(ds, qd + ((part * C::kHalfTile + 32 * kk) >> 4),
+                            tc::mma_e4m3(ds, q + ((part * C::kHalfTile + 32 * kk) >> 4),
                                          kd + ((32 * kk) >> 4), C::kIdS, (part | kk) != 0);
                     } else if constexpr (D == 128) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_bf16(ds, qd + ((part * C::kHalfTile + 32 * kk) >> 4),
+                            tc::mma_bf16(ds, q + ((part * C::kHalfTile + 32 * kk) >> 4),
                                          kd + ((part * 1024 + 32 * kk) >> 4), C::kIdS,
                                          (part | kk) != 0);
                     } else {
 #pragma unroll
                         for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                            tc::mma_bf16(ds, qd + ((32 * kk) >> 4), kd + ((32 * kk) >> 4), C::kIdS,
+                            tc::mma_bf16(ds, q + ((32 * kk) >> 4), kd + ((32 * kk) >> 4), C::kIdS,
                                          kk != 0);
                     }
                 };
-                // step -1: the first score product; step i: value product i and
-                // score product i + 1
-                for (int i = -1; i < r.na && ok; ++i) {
-                    const bool pv = i >= 0 && i < n, qk = i + 1 < n;
-                    const uint32_t kpos = ord.k(h, i + 1), ks = kpos % C::kStages;
-                    const uint32_t vpos = ord.v(h, max(i, 0)), vs = vpos % C::kStages;
-                    // the probabilities come last, so they are waited for last
-                    ok = !qk || wait(bar(kBarFull + ks), (kpos / C::kStages) & 1u);
-                    if (pv)
-                        ok = ok && wait(bar(kBarFull + vs), (vpos / C::kStages) & 1u) &&
-                             (i > 0 || wait(bar(kBarOEmpty + h), (nitem & 1u) ^ 1u));
-                    ok = ok && take_turn();
-                    if (pv) ok = ok && wait(bar(kBarPFull + h), np & 1u);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    if (pv) {
-                        const uint32_t vb = sb + C::kOffRing + vs * C::kStage;
-                        const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
-                                                                : tc::smem_desc(vb, 16384, 1024);
-                        // the first 64 keys' product while the others' softmax goes on
+                // part 0 or 1 (64 keys) of a value product
+                auto values = [&](int h, int i, uint32_t stage, int part) {
+                    const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
+                    const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
+                    const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
+                                                            : tc::smem_desc(vb, 16384, 1024);
+                    if constexpr (E4) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            if (part) {
-                                if (!(ok = wait(bar(kBarPFull + 2 + h), np & 1u))) break;
-                                tc::fence_after_sync();
-                            }
-                            if constexpr (E4) {
+                        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                                for (int t = 0; t < 2; ++t)
+                            for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                                tc::mma_e4m3_ts(dO, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
+                                                C::kIdO, (i | part | t | (kk & 1)) != 0);
+                    } else {
 #pragma unroll
-                                    for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                                        tc::mma_e4m3_ts(dO, ds + 32 * t + 8 * kk,
-                                                        vd + ((4096 * kk) >> 4), C::kIdO,
-                                                        (i | part | t | (kk & 1)) != 0);
-                            } else {
+                        for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                            tc::mma_bf16_ts(dO, p + 8 * kk,
+                                            vd + (((D == 128 ? 4096 : 2048) * kk) >> 4), C::kIdO,
+                                            (i | kk) != 0);
+                    }
+                };
+                // What block (h, i) waits for: the key tile of its scores, the value
+                // tile, O read out by the last item's epilogue, the probabilities.
+                auto each_wait = [&](int h, int i, auto &&one) -> bool {
+                    const int n = h ? r.nb : r.na;
+                    if (i + 1 < n) {
+                        const uint32_t pos = ord.k(h, i + 1);
+                        if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
+                            return false;
+                    }
+                    if (i >= 0) {
+                        const uint32_t pos = ord.v(h, i);
+                        if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
+                            return false;
+                        if (i == 0 && !one(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
+                        if (!one(bar(kBarPFull + h), np[h] & 1u)) return false;
+                    }
+                    return true;
+                };
+                bool ready = false;              // the next block's waits are known to be over
+                // step -1: the first score products
+                for (int i = -1; i < r.na && ok; ++i)
 #pragma unroll
-                                for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
-                                    tc::mma_bf16_ts(dO, ds + 8 * kk,
-                                                    vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
-                                                    C::kIdO, (i | kk) != 0);
-                            }
+                    for (int h = 0; h < 2; ++h) {
+                        const int n = h ? r.nb : r.na;
+                        const bool pv = i >= 0 && i < n, qk = i + 1 < n;
+                        if (!ok || !(pv || qk)) continue;
+                        if (!ready && !(ok = each_wait(h, i, wait))) continue;
+                        tc::fence_after_sync();
+                        const uint32_t ks = ord.k(h, i + 1) % C::kStages;
+                        const uint32_t vs = pv ? ord.v(h, i) % C::kStages : 0u;
+                        if (pv) {
+                            // the first 64 keys' product while the others' softmax goes on
+                            values(h, i, vs, 0);
+                            if (!(ok = wait(bar(kBarPFull + 2 + h), np[h] & 1u))) continue;
+                            tc::fence_after_sync();
+                            values(h, i, vs, 1);
                         }
-                        if (!ok) break;
+                        // the next block that this item has: (1, i), else (0, i + 1)
+                        const bool b_next = h == 0 && i < r.nb && (i >= 0 || r.nb > 0);
+                        const int hn = b_next ? 1 : 0, in = b_next ? i : i + 1;
+                        auto probe = [&]() {
+                            return in < r.na && each_wait(hn, in, [&](uint32_t b, uint32_t ph) {
+                                       return mbar_try_wait(b, ph);
+                                   });
+                        };
+                        ready = false;
+                        if (qk) {
+                            scores(h, ks, 0);
+                            if (hn != h) ready = probe();
+                            scores(h, ks, 1);
+                        }
+                        // (the value product's end is told with the score product's: a
+                        // rescale needs it only after the next scores)
+                        if (qk) {
+                            tc::commit(bar(kBarSFull + h));
+                            if (r.split || h == 1) tc::commit(bar(kBarEmpty + ks));
+                            // the item's last score product frees its queries
+                            if (h == (r.split && r.nb < r.na ? 0 : 1) && i + 1 == r.na - 1)
+                                tc::commit(bar(kBarQEmpty));
+                        }
+                        if (pv) {
+                            tc::commit(bar(kBarPvDone + h));
+                            if (r.split || h == 1) tc::commit(bar(kBarEmpty + vs));
+                            if (i == 0) ++nitem[h];
+                            ++np[h];
+                        }
                     }
-                    // (the turn is passed with half of the scores still to issue:
-                    // the other thread needs as long to take it up)
-                    if (qk) scores(ks, 0);
-                    pass_turn();
-                    if (qk) scores(ks, 1);
-                    // (the value product's end is told with the score product's: a
-                    // rescale needs it only after the next scores)
-                    if (qk) {
-                        tc::commit(bar(kBarSFull + h));
-                        release(ks);
-                        if (i + 1 == n - 1) tc::commit(bar(kBarQEmpty));
-                    }
-                    if (pv) {
-                        tc::commit(bar(kBarPvDone + h));
-                        release(vs);
-                        ++np;
-                    }
-                }
-                if (n > 0) ++nitem;
+                ring += ord.total(r.na);
+                ++items_done;
             }
-            tc::commit(bar(kBarDrain + h));
-            mbar_wait(bar(kBarDrain + h), 0, a.status);
+            tc::commit(bar(kBarDrain));
+            mbar_wait(bar(kBarDrain), 0, a.status);
         }
         __syncwarp();
     }
@@ -1065,6 +1073,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                         fence_proxy_async_smem();
                     }
+                    __syncwarp();
                 }
                 // ---- probabilities and their terms over S's columns, 64 keys at a
                 // time.  The first 64 are taken with the maximum so far while the
@@ -1108,6 +1117,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                     m = mn;
                 }
+                __syncwarp();
                 store_terms<E4>(ts, 0, t0, t1);
                 mbar_arrive(bar(kBarPFull + h));
                 exponentials<E4>(s + 64, sc, neg, sum, t0, t1, [](int) {});
@@ -1138,43 +1148,40 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int64_t prow = int64_t(q.prow) + (q.split ? h * q.ntok * G : 0) + tok * G + head_row;
             // half B of a split item without a tile of its own adds nothing to a direct row
             const bool writes = live && !(direct && q.split && h == 1);
-#pragma unroll
-            for (int j = 0; j < D; j += 32) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tc::ld32(to + j, o);
-                    tc::wait_ld();
-                    pin<32>(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-                if (writes && direct) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) +
-                                                           orow * D + j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv,
-                                               __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else if (writes) {
-                    float4 *dst =
-                        reinterpret_cast<float4 *>(plan.o_part + prow * D + j);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv,
-                                             __uint_as_float(o[4 * e + 1]) * inv,
-                                             __uint_as_float(o[4 * e + 2]) * inv,
-                                             __uint_as_float(o[4 * e + 3]) * inv);
-                }
-            }
+            // All of the row into registers, by converged warps, before the rows
+            // part ways (the warp-wide loads are only defined for a whole warp).
+            uint32_t o[D];
             if (n > 0) {
+#pragma unroll
+                for (int j = 0; j < D; j += 32) tc::ld32(to + j, o + j);
+                tc::wait_ld();
+#pragma unroll
+                for (int j = 0; j < D; j += 32) pin<32>(o + j);
                 tc::fence_before_sync();
                 mbar_arrive(bar(kBarOEmpty + h));
+            } else {
+#pragma unroll
+                for (int e = 0; e < D; ++e) o[e] = 0u;
+            }
+            if (writes && direct) {
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * D);
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv,
+                                           __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
+                    dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else if (writes) {
+                float4 *dst = reinterpret_cast<float4 *>(plan.o_part + prow * D);
+#pragma unroll
+                for (int e = 0; e < D / 4; ++e)
+                    dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv,
+                                         __uint_as_float(o[4 * e + 1]) * inv,
+                                         __uint_as_float(o[4 * e + 2]) * inv,
+                                         __uint_as_float(o[4 * e + 3]) * inv);
             }
             if (writes) {
                 if (!direct) plan.lse_part[prow] = lse;
