@@ -214,29 +214,39 @@ constexpr int kSortBlocks = 2048;        // at most so many query blocks are sor
 // kSnap are left to the neighbour.
 constexpr int kItemCost = 3, kPieceCost = 6, kSnap = 6;
 
-// Inclusive scan over the CTA's 1024 threads; `total` gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warp_sums, int64_t &total) {
+// Inclusive scans of two numbers over the CTA's 1024 threads, in place; the sums
+// go to `total`.
+struct Two {
+    int64_t x, y;
+};
+__device__ __forceinline__ Two block_scan(Two v, Two *warp_sums, Two &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t s = warp_sums[lane];
+    auto warp_scan = [&](Two &u) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+            const int64_t x = __shfl_up_sync(0xffffffffu, u.x, o);
+            const int64_t y = __shfl_up_sync(0xffffffffu, u.y, o);
+            if (lane >= o) {
+                u.x += x;
+                u.y += y;
+            }
         }
-        warp_sums[lane] = s;
-    }
+    };
+    warp_scan(v);
     __syncthreads();
-    total = warp_sums[31];
-    return x + (warp ? warp_sums[warp - 1] : 0);
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    Two s = warp_sums[lane];
+    warp_scan(s);                        // by every warp: no barrier after it
+    total.x = __shfl_sync(0xffffffffu, s.x, 31);
+    total.y = __shfl_sync(0xffffffffu, s.y, 31);
+    const int64_t x = __shfl_sync(0xffffffffu, s.x, (warp + 31) & 31);
+    const int64_t y = __shfl_sync(0xffffffffu, s.y, (warp + 31) & 31);
+    if (warp) {
+        v.x += x;
+        v.y += y;
+    }
+    return v;
 }
 
 // One CTA makes the plan.  The work -- every (query block, KV head), longest
@@ -246,10 +256,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *warp_sums, int
 // capacities T - load end.  So few blocks over long contexts are cut over all
 // CTAs evenly, and many blocks are mostly whole.  Nearly alike blocks are
 // ordered by KV head, which keeps the keys that are read at one time few.
+//
+// Up to kInShared sequences and query blocks its tables are kept in shared
+// memory: a dependent load from L2 costs more than a scan.
+constexpr int kInShared = 1024;
+
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
-    __shared__ int64_t warp_sums[32];
+    __shared__ Two warp_sums[32];
     __shared__ uint32_t keys[kSortBlocks];
+    __shared__ int32_t s_first[kInShared + 1], s_cu[kInShared + 1], s_len[kInShared];
+    __shared__ int64_t s_before[kInShared + 1];
+    __shared__ int32_t s_steps[kInShared], s_prow[kInShared];
     __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
     __shared__ int32_t s_max, s_min;
     pdl_wait();
@@ -257,57 +275,73 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     const int tid = threadIdx.x;
     const int32_t hkv = a.cache.num_kv_heads, tpt = sh.tokens_per_tile, per = 2 * tpt;
     const int32_t ctas = plan.ctas;
-    int64_t total;
+    Two total;
 
     // ---- query blocks before each sequence
+    const bool few_seqs = a.batch <= kInShared;
     bool bad = false;
     int32_t nblocks = 0;
-    for (int base = 0; base < a.batch; base += kPlanThreads) {
-        const int b = base + tid;
-        int32_t nq = 0;
-        if (b < a.batch) {
-            const int32_t x = a.cu_q_lens[b], y = a.cu_q_lens[b + 1];
-            if (x < 0 || y < x || y > a.num_tokens) bad = true;
-            else nq = (y - x + per - 1) / per;
-        }
-        const int64_t incl = block_scan(nq, warp_sums, total);
-        if (b < a.batch) plan.first[b] = nblocks + int32_t(incl) - nq;
-        nblocks += int32_t(total);
-        if (__syncthreads_or(bad)) break;
-    }
     if (tid == 0) {
         s_max = 0;
         s_min = INT_MAX;
     }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) {
-            raise_status(a.status, PKV_DEV_QUERY_RANGE);
-            plan.header[kHdrBlocks] = plan.header[kHdrRounds] = plan.header[kHdrSplit] =
-                plan.header[kHdrCuts] = 0;
+    for (int base = 0; base < a.batch; base += kPlanThreads) {
+        const int b = base + tid;
+        int32_t nq = 0, x = 0, y = 0, L = 0;
+        if (b < a.batch) {
+            x = a.cu_q_lens[b];
+            y = a.cu_q_lens[b + 1];
+            L = a.seq_lens[b];
+            if (x < 0 || y < x || y > a.num_tokens) bad = true;
+            else nq = (y - x + per - 1) / per;
+            if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) {
+                raise_status(a.status, PKV_DEV_SEQ_LEN);
+                L = 0;
+            } else if (!bad && L < y - x) {
+                raise_status(a.status, PKV_DEV_SEQ_LEN);
+            }
         }
-        for (int j = tid; j <= ctas; j += kPlanThreads) plan.piece0[j] = 0;
-        return;
+        const Two incl = block_scan({nq, 0}, warp_sums, total);
+        if (b < a.batch) {
+            const int32_t before = nblocks + int32_t(incl.x) - nq;
+            if (few_seqs) {
+                s_first[b] = before;
+                s_cu[b] = x;
+                s_cu[b + 1] = y;
+                s_len[b] = L;
+            } else {
+                plan.first[b] = before;
+            }
+        }
+        nblocks += int32_t(total.x);
+        if (__syncthreads_or(bad)) {
+            if (tid == 0) {
+                raise_status(a.status, PKV_DEV_QUERY_RANGE);
+                plan.header[kHdrBlocks] = plan.header[kHdrRounds] = plan.header[kHdrSplit] =
+                    plan.header[kHdrCuts] = 0;
+            }
+            for (int j = tid; j <= ctas; j += kPlanThreads) plan.piece0[j] = 0;
+            return;
+        }
     }
-    if (tid == 0) plan.first[a.batch] = nblocks;
+    if (tid == 0) (few_seqs ? s_first : plan.first)[a.batch] = nblocks;
+    __syncthreads();
+    const bool few_blocks = nblocks <= kInShared, sortable = nblocks <= kSortBlocks;
 
     auto block_of = [&](int i) {
+        const int32_t *first = few_seqs ? s_first : plan.first;
         int lo = 0, hi = a.batch;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (plan.first[mid] <= i) lo = mid;
+            if (first[mid] <= i) lo = mid;
             else hi = mid;
         }
         Block q;
         q.b = lo;
-        const int32_t q0 = a.cu_q_lens[lo], n = a.cu_q_lens[lo + 1] - q0;
-        const int32_t t0 = (i - plan.first[lo]) * per;
-        int32_t L = a.seq_lens[lo];
-        if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) {
-            raise_status(a.status, PKV_DEV_SEQ_LEN);
-            L = 0;
-        } else if (L < n) {
-            raise_status(a.status, PKV_DEV_SEQ_LEN);
-        }
+        const int32_t *cu = few_seqs ? s_cu : a.cu_q_lens;
+        const int32_t q0 = cu[lo], n = cu[lo + 1] - q0, t0 = (i - first[lo]) * per;
+        int32_t L = few_seqs ? s_len[lo] : a.seq_lens[lo];
+        if (!few_seqs && (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size)) L = 0;
         q.qrow = q0 + t0;
         q.pos = L - n + t0;
         q.ntok = min(per, n - t0);
@@ -317,10 +351,8 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         q.pad = 0;
         return q;
     };
-    __syncthreads();
 
     // ---- the blocks in order
-    const bool sortable = nblocks <= kSortBlocks;
     int32_t most = 0, least = INT_MAX;
     for (int i = tid; i < nblocks; i += kPlanThreads) {
         const Block q = block_of(i);
@@ -328,8 +360,12 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         most = max(most, q.steps);
         least = min(least, q.steps);
     }
-    atomicMax(&s_max, most);
-    atomicMin(&s_min, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if ((tid & 31) == 0) {
+        atomicMax(&s_max, most);
+        atomicMin(&s_min, least);
+    }
     __syncthreads();
     const bool alike = s_max - s_min <= s_max / 4;
     const bool by_head = alike;
@@ -351,30 +387,45 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
                     }
                 }
             }
+        __syncthreads();
     }
-    __syncthreads();
+    auto ordered = [&](int r) {
+        return block_of(sortable ? int(keys[r] & (kSortBlocks - 1)) : r);
+    };
     int64_t cost_all = 0, nsplit = 0, part_rows = int64_t(2) * ctas * plan.slot_rows;
     for (int base = 0; base < nblocks; base += kPlanThreads) {
         const int i = base + tid;
         Block q = {};
         const bool in = i < nblocks;
-        if (in) q = block_of(sortable ? int(keys[i] & (kSortBlocks - 1)) : i);
+        if (in) q = ordered(i);
         const bool halves = in && q.ntok <= tpt && q.tiles > 1;
         const int64_t cost = in ? q.steps + kItemCost : 0;
-        const int64_t c = block_scan(cost, warp_sums, total);
-        if (in) plan.before[i] = cost_all + c - cost;
-        cost_all += total;
-        const int64_t s = block_scan(halves, warp_sums, total);
-        if (halves) plan.split[nsplit + s - 1] = i;
-        nsplit += total;
         const int64_t rows = halves ? int64_t(2) * q.ntok * sh.group * hkv : 0;
-        const int64_t r = block_scan(rows, warp_sums, total);
-        if (halves) q.prow = int32_t(part_rows + r - rows);
-        part_rows += total;
-        if (in) plan.blocks[i] = q;
+        // costs beside the count of split blocks: both below 2^31
+        const Two v = block_scan({cost << 24 | halves, rows}, warp_sums, total);
+        if (in) {
+            const int64_t before = cost_all + (v.x >> 24) - cost;
+            if (halves) {
+                plan.split[nsplit + (v.x & 0xffffff) - 1] = i;
+                q.prow = int32_t(part_rows + v.y - rows);
+            }
+            plan.blocks[i] = q;
+            if (few_blocks) {
+                s_before[i] = before;
+                s_steps[i] = q.steps;
+                s_prow[i] = q.prow;
+            } else {
+                plan.before[i] = before;
+            }
+        }
+        cost_all += total.x >> 24;
+        nsplit += total.x & 0xffffff;
+        part_rows += total.y;
     }
-    if (tid == 0) plan.before[nblocks] = cost_all;
+    if (tid == 0) (few_blocks ? s_before : plan.before)[nblocks] = cost_all;
     __syncthreads();
+    const int64_t *before = few_blocks ? s_before : plan.before;
+    auto steps_at = [&](int r) { return few_blocks ? s_steps[r] : plan.blocks[r].steps; };
 
     // ---- whole rounds
     const int64_t n_items = int64_t(nblocks) * hkv;
@@ -386,7 +437,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         if (tid < ctas) {
             int32_t r, g;
             item_at(round_item(rounds, tid, ctas), by_head, nblocks, hkv, r, g);
-            next += plan.blocks[r].steps + kItemCost;
+            next += steps_at(r) + kItemCost;
         }
         if (__syncthreads_or(next > share)) break;
         load = next;
@@ -397,14 +448,13 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     const int64_t idx0 = int64_t(rounds) * ctas;
     int32_t r0 = 0, g0 = 0;
     if (idx0 < n_items) item_at(idx0, by_head, nblocks, hkv, r0, g0);
-    const int64_t done =
-        idx0 >= n_items ? cost_all * hkv
-        : by_head       ? g0 * cost_all + plan.before[r0]
-                        : plan.before[r0] * hkv + g0 * int64_t(plan.blocks[r0].steps + kItemCost);
+    const int64_t done = idx0 >= n_items ? cost_all * hkv
+                         : by_head       ? g0 * cost_all + before[r0]
+                                   : before[r0] * hkv + g0 * int64_t(steps_at(r0) + kItemCost);
     const int64_t rest = cost_all * hkv - done;
     for (int64_t i = idx0 + tid; i < n_items; i += kPlanThreads) plan.is_cut[i - idx0] = 0;
     const int64_t cap = tid < ctas ? max(int64_t(0), share - kPieceCost - load) : 0;
-    const int64_t upto = block_scan(cap, warp_sums, total);
+    const int64_t upto = block_scan({cap, 0}, warp_sums, total).x;
     if (tid == 0) {
         cut_idx[0] = int32_t(idx0);
         cut_step[0] = 0;
@@ -413,8 +463,8 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         // the end of CTA tid's part: position x of the rest
         int64_t idx = n_items;
         int32_t step = 0;
-        if (rest > 0 && tid < ctas - 1 && total > 0) {
-            const int64_t x = done + int64_t(double(rest) * (double(upto) / double(total)));
+        if (rest > 0 && tid < ctas - 1 && total.x > 0) {
+            const int64_t x = done + int64_t(double(rest) * (double(upto) / double(total.x)));
             int64_t y = x;
             int32_t g = 0;
             if (by_head) {
@@ -426,13 +476,13 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
             int lo = 0, hi = nblocks;            // before[lo] <= y < before[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (plan.before[mid] <= y) lo = mid;
+                if (before[mid] <= y) lo = mid;
                 else hi = mid;
             }
-            const int32_t steps = plan.blocks[lo].steps;
-            int64_t off = y - plan.before[lo];
+            const int32_t steps = steps_at(lo);
+            int64_t off = y - before[lo];
             if (!by_head) {
-                off = x - plan.before[lo] * hkv;
+                off = x - before[lo] * hkv;
                 g = int32_t(min(off / (steps + kItemCost), int64_t(hkv - 1)));
                 off -= g * int64_t(steps + kItemCost);
             }
@@ -463,39 +513,39 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         // this part begins an item that goes on
         cut = s1 > 0 && (i1 > i0 || s0 == 0);
     }
-    const int64_t p1 = block_scan(count, warp_sums, total);
-    const int64_t npieces = total;
-    const int64_t c1 = block_scan(cut, warp_sums, total);
+    const Two at = block_scan({count, cut}, warp_sums, total);
     if (tid < ctas) {
-        plan.piece0[tid] = int32_t(p1 - count);
+        const int64_t p0 = at.x - count;
+        plan.piece0[tid] = int32_t(p0);
         for (int k = 0; k < count; ++k) {
             const int32_t idx = i0 + k, from = k ? 0 : s0;
             int32_t r, g;
             item_at(idx, by_head, nblocks, hkv, r, g);
-            const Block q = plan.blocks[r];
+            Block q = few_blocks ? ordered(r) : plan.blocks[r];
+            if (few_blocks) q.prow = s_prow[r];
             const int32_t to = idx == i1 ? s1 : q.steps;
             int32_t prow;
             if (from > 0) prow = tid * plan.slot_rows;
             else if (to < q.steps) prow = (ctas + tid) * plan.slot_rows;
             else prow = q.prow < 0 ? -1 : q.prow + g * 2 * q.ntok * sh.group;
-            plan.pieces[p1 - count + k] = item_of(q, g, from, to, tpt, prow);
+            plan.pieces[p0 + k] = item_of(q, g, from, to, tpt, prow);
             if (from == 0 && to < q.steps) {
                 int more = 0;
                 while (tid + 1 + more < ctas && cut_idx[tid + 1 + more] == idx &&
                        cut_step[tid + 1 + more] > 0)
                     ++more;
-                plan.cuts[c1 - 1] = {r, g, tid, more};
+                plan.cuts[at.y - 1] = {r, g, tid, more};
                 plan.is_cut[idx - idx0] = 1;
             }
         }
     }
     if (tid == 0) {
-        plan.piece0[ctas] = int32_t(npieces);
+        plan.piece0[ctas] = int32_t(total.x);
         plan.header[kHdrBlocks] = nblocks;
         plan.header[kHdrRounds] = rounds;
         plan.header[kHdrByHead] = by_head;
         plan.header[kHdrSplit] = int32_t(nsplit);
-        plan.header[kHdrCuts] = int32_t(total);
+        plan.header[kHdrCuts] = int32_t(total.y);
     }
 }
 
@@ -539,6 +589,18 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+// 32 bytes, a whole sector (in one store where the buffer's alignment allows it).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool aligned) {
+    if (!aligned) {
+        uint4 *q = static_cast<uint4 *>(p);
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 // Makes what follows depend on registers a TMEM load has filled (their values
 // are there only after the wait that precedes this).
@@ -710,10 +772,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
             const int32_t pmax = r.pos + r.ntok - 1;
             const int32_t *table = a.block_tables + int64_t(r.b) * a.max_blocks;
-            // lane's box of virtual tile v: its pool row, or -1 (nothing to copy)
-            auto lookup = [&](int v) -> int32_t {
-                if (lane >= nbox) return -1;
-                const int32_t key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + lane * box;
+            // pool row of box `bx` of virtual tile v, or -1 (nothing to copy)
+            auto row_of = [&](int v, int bx) -> int32_t {
+                const int32_t key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + bx * box;
                 if (key > pmax || (key + box - 1 < tl.lo && key >= a.sinks)) return -1;
                 const int32_t phys = table[key / bs];
                 if (phys < 0 || phys >= a.cache.num_blocks) {
@@ -721,6 +782,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     return g * bs;                  // some block's rows stand in
                 }
                 return (phys * hkv + g) * bs + key % bs;
+            };
+            auto lookup = [&](int v) { return lane < nbox ? row_of(v, lane) : -1; };
+            auto lookup2 = [&](int v, int w, bool second) {
+                const int bx = lane & 15;
+                return bx < nbox && (lane < 16 || second) ? row_of(lane < 16 ? v : w, bx) : -1;
             };
             auto load = [&](const CUtensorMap *map, int32_t y) -> bool {
                 const uint32_t stage = ring % C::kStages, phase = (ring / C::kStages) & 1u;
@@ -745,42 +811,52 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 ++ring;
                 return true;
             };
-            int32_t ya = lookup(r.v0);
-            if constexpr (!E4) {
-                // the item's query tiles, once the last item's are no longer read
-                if (!(ok = __all_sync(0xffffffffu,
-                                      pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
-                                                abort_flag))))
-                    break;
-                if (lane == 0) {
-                    const int tiles = r.split ? 1 : 2;
-                    mbar_arrive_expect_tx(bar(kBarQFull), tiles * uint32_t(tpt * G) * D * 2);
-                    for (int t = 0; t < tiles; ++t)
-                        for (int half = 0; half < D / 64; ++half)
-                            tma_load_3d(sb + C::kOffQ + t * C::kQTile + half * C::kHalfTile,
-                                        &tmap_q, half * 64, g * G, r.qrow + t * tpt,
-                                        bar(kBarQFull));
+            // the item's query tiles, once the last item's are no longer read
+            auto load_q = [&]() -> bool {
+                if constexpr (!E4) {
+                    if (!__all_sync(0xffffffffu,
+                                    pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
+                                              abort_flag)))
+                        return false;
+                    if (lane == 0) {
+                        const int tiles = r.split ? 1 : 2;
+                        mbar_arrive_expect_tx(bar(kBarQFull), tiles * uint32_t(tpt * G) * D * 2);
+                        for (int t = 0; t < tiles; ++t)
+                            for (int half = 0; half < D / 64; ++half)
+                                tma_load_3d(sb + C::kOffQ + t * C::kQTile + half * C::kHalfTile,
+                                            &tmap_q, half * 64, g * G, r.qrow + t * tpt,
+                                            bar(kBarQFull));
+                    }
+                    __syncwarp();
+                    q_armed = 1;
+                    q_parity = items_done & 1u;
                 }
-                q_armed = 1;
-                q_parity = items_done & 1u;
-            }
-            ++items_done;
+                ++items_done;
+                return true;
+            };
+            // Blocks are looked up a step ahead, so that the next copies need not wait
+            // for the table; the queries' buffer frees late, so the item's first keys
+            // go before them.
             if (!r.split) {
+                int32_t y = lookup(r.v0);
                 for (int i = 0; i < r.na && ok; ++i) {
-                    const int32_t y = ya;
-                    ok = load(&tmap_k, y);
-                    if (i + 1 < r.na) ya = lookup(r.v0 + i + 1);
-                    ok = ok && load(&tmap_v, y);
+                    const int32_t yn = i + 1 < r.na ? lookup(r.v0 + i + 1) : -1;
+                    ok = load(&tmap_k, y) && (i > 0 || load_q()) && load(&tmap_v, y);
+                    y = yn;
                 }
             } else {
-                int32_t yb = r.nb > 0 ? lookup(r.v0 + r.na) : -1;
+                // lanes 0 .. 15: half A's boxes, 16 .. 31: half B's
+                int32_t y = lookup2(r.v0, r.v0 + r.na, r.nb > 0);
                 for (int i = 0; i < r.na && ok; ++i) {
-                    const int32_t y0 = ya, y1 = yb;
+                    const int32_t yn =
+                        i + 1 < r.na ? lookup2(r.v0 + i + 1, r.v0 + r.na + i + 1, i + 1 < r.nb) : -1;
+                    const int32_t y1 = __shfl_down_sync(0xffffffffu, y, 16);
+                    const int32_t y0 = lane < 16 ? y : -1;
                     const bool both = i < r.nb;
-                    ok = load(&tmap_k, y0) && (!both || load(&tmap_k, y1));
-                    if (i + 1 < r.na) ya = lookup(r.v0 + i + 1);
-                    if (i + 1 < r.nb) yb = lookup(r.v0 + r.na + i + 1);
-                    ok = ok && load(&tmap_v, y0) && (!both || load(&tmap_v, y1));
+                    ok = load(&tmap_k, y0) && (!both || load(&tmap_k, lane < 16 ? y1 : -1)) &&
+                         (i > 0 || load_q()) && load(&tmap_v, y0) &&
+                         (!both || load(&tmap_v, lane < 16 ? y1 : -1));
+                    y = yn;
                 }
             }
         }
@@ -944,6 +1020,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const uint32_t ts = tmem + kKeys * h + lanes;    // S, P
         const uint32_t to = tmem + kColO + 128 * h + lanes;
         const int tok_row = row / G, head_row = row - tok_row * G;
+        const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         uint32_t ring = 0, np = 0, items_done = 0;
         bool ok = true;
         for (int it = 0; it < num_items; ++it) {
@@ -1009,11 +1086,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (r.na > 0) ++items_done;
             const int v0 = r.v0 + (r.split && h ? r.na : 0);
             // Virtual tiles [clear0, clear1): every row of the half sees every key.
-            // Only the others look at positions; they read the item again, so that
-            // the common tiles keep few values in registers.
+            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+            const int32_t pmax = r.pos + r.ntok - 1, pos = r.pos + tok0 + tok_row;
+            const Order ord{ring, r.split, r.nb};
             int clear0, clear1;
             {
-                const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
                 const int32_t hmin = r.pos + tok0, hmax = r.pos + min(r.ntok, tok0 + tpt) - 1;
                 clear0 = a.window > 0 && hmax >= a.window ? (hmax - a.window) / kKeys + 1 : 0;
                 clear0 = max(clear0 - tl.gap, tl.sink_tiles);
@@ -1033,15 +1110,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 for (int j = 0; j < kKeys; j += 32) pin<32>(s + j);
                 // ---- keys this row does not see
                 if (!clear) {
-                    const Item q = read_item(it);
-                    const Tiles tl = tiles_of(q.pos, q.ntok, a.window, a.sinks);
-                    const int32_t p = q.pos + (q.split ? 0 : h * tpt) + tok_row;
                     const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
 #pragma unroll
                     for (int w = 0; w < kKeys / 32; ++w) {
-                        uint32_t see = p >= 0 ? below(p - k0 + 1, w) : 0u;
+                        uint32_t see = pos >= 0 ? below(pos - k0 + 1, w) : 0u;
                         if (a.window > 0)
-                            see &= ~below(p - k0 - a.window + 1, w) | below(a.sinks - k0, w);
+                            see &= ~below(pos - k0 - a.window + 1, w) | below(a.sinks - k0, w);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!((see >> j) & 1u)) s[32 * w + j] = 0xff800000u;
@@ -1049,13 +1123,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
                 // ---- value rows no row of the item sees: zeroed, thread = key
                 if (!clear) {
-                    const Item q = read_item(it);
-                    const Tiles tl = tiles_of(q.pos, q.ntok, a.window, a.sinks);
                     const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                    const int32_t pmax = q.pos + q.ntok - 1;
                     if (k0 + kKeys - 1 > pmax ||
                         (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
-                        const Order ord{ring, q.split, q.nb};
                         const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
                         ok = ok && pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
                                              a.status, abort_flag);
@@ -1139,15 +1209,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if constexpr (E4) inv *= a.v_scale[g];
             float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kShift)) * kLn2 : -INFINITY;
             if (!ok) inv = lse = nan;
-            const Item q = read_item(it);
-            ring += Order{ring, q.split, q.nb}.total(q.na);
-            const int tok = (q.split ? 0 : h * tpt) + tok_row;
-            const bool live = tok_row < tpt && tok < q.ntok;
-            const bool direct = q.prow < 0;
-            const int64_t orow = int64_t(q.qrow + tok) * a.num_q_heads + g * G + head_row;
-            const int64_t prow = int64_t(q.prow) + (q.split ? h * q.ntok * G : 0) + tok * G + head_row;
+            ring += ord.total(r.na);
+            const int tok = (r.split ? 0 : h * tpt) + tok_row;
+            const bool live = tok_row < tpt && tok < r.ntok;
+            const bool direct = r.prow < 0;
+            const int64_t orow = int64_t(r.qrow + tok) * a.num_q_heads + g * G + head_row;
+            const int64_t prow = int64_t(r.prow) + (r.split ? h * r.ntok * G : 0) + tok * G + head_row;
             // half B of a split item without a tile of its own adds nothing to a direct row
-            const bool writes = live && !(direct && q.split && h == 1);
+            const bool writes = live && !(direct && r.split && h == 1);
             // All of the row into registers, by converged warps, before the rows
             // part ways (the warp-wide loads are only defined for a whole warp).
             uint32_t o[D];
@@ -1164,24 +1233,26 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 for (int e = 0; e < D; ++e) o[e] = 0u;
             }
             if (writes && direct) {
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + orow * D);
+                uint16_t *dst = static_cast<uint16_t *>(a.out) + orow * D;
 #pragma unroll
-                for (int e = 0; e < D / 8; ++e) {
-                    uint32_t w[4];
+                for (int e = 0; e < D; e += 16) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * inv,
-                                           __uint_as_float(o[8 * e + 2 * x + 1]) * inv);
-                    dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int x = 0; x < 8; ++x)
+                        w[x] = pack_bf16x2(__uint_as_float(o[e + 2 * x]) * inv,
+                                           __uint_as_float(o[e + 2 * x + 1]) * inv);
+                    store32(dst + e, w, out32);
                 }
             } else if (writes) {
-                float4 *dst = reinterpret_cast<float4 *>(plan.o_part + prow * D);
+                float *dst = plan.o_part + prow * D;
 #pragma unroll
-                for (int e = 0; e < D / 4; ++e)
-                    dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv,
-                                         __uint_as_float(o[4 * e + 1]) * inv,
-                                         __uint_as_float(o[4 * e + 2]) * inv,
-                                         __uint_as_float(o[4 * e + 3]) * inv);
+                for (int e = 0; e < D; e += 8) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        w[x] = __float_as_uint(__uint_as_float(o[e + x]) * inv);
+                    store32(dst + e, w, true);
+                }
             }
             if (writes) {
                 if (!direct) plan.lse_part[prow] = lse;
@@ -1198,104 +1269,111 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 }
 
 // ------------------------------------------------------------------- the merge
-// One row per D / 4 lanes: out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M}
+// D / 4 lanes a row: out = sum_c e^{lse_c - M} o_c / sum_c e^{lse_c - M}
 // over the row's partials, each already divided by its own sum.  A NaN partial
 // makes the row NaN; empty ones (lse = -inf) weigh nothing.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 16;           // rows of a warp's unit of work
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
 chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
-    constexpr int kLanes = D / 4, kRowsPerCta = kMergeThreads / kLanes;
+    constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;
     pdl_wait();
     pdl_launch_dependents();
     const int hkv = a.cache.num_kv_heads, G = sh.group;
     // the split items taken whole (two partials of at most kRows rows each), then the cuts
-    constexpr int kHalfChunks = kRows / kRowsPerCta, kChunks = 2 * kHalfChunks;
-    const int64_t n_half = int64_t(plan.header[kHdrSplit]) * hkv * kHalfChunks;
-    const int64_t total = n_half + int64_t(plan.header[kHdrCuts]) * kChunks;
-    const int sub = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+    constexpr int kHalfUnits = kRows / kMergeRows, kUnits = 2 * kHalfUnits;
+    const int64_t n_half = int64_t(plan.header[kHdrSplit]) * hkv * kHalfUnits;
+    const int64_t total = n_half + int64_t(plan.header[kHdrCuts]) * kUnits;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
     const int nblocks = plan.header[kHdrBlocks];
     const int64_t idx0 = int64_t(plan.header[kHdrRounds]) * plan.ctas;
-    for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-        int blk, g, row, count, halves = 2;
+    const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + c;
+    constexpr int kWarps = kMergeThreads / 32;
+    for (int64_t w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < total; w += gridDim.x * kWarps) {
+        int blk, g, row0, count, halves = 2;
         int64_t first, next;                 // rows of the first piece, and of the others'
         if (w < n_half) {
-            const int64_t sg = w / kHalfChunks;
+            // (unit-major, so that the units past a short item's rows end up in other warps)
+            const int64_t sg = w % (n_half / kHalfUnits);
+            row0 = int(w / (n_half / kHalfUnits)) * kMergeRows;
             blk = plan.split[sg / hkv];
             g = int(sg % hkv);
-            row = int(w % kHalfChunks) * kRowsPerCta + sub;
-            const int64_t idx =
-                plan.header[kHdrByHead] ? int64_t(g) * nblocks + blk : int64_t(blk) * hkv + g;
-            if (idx >= idx0 && plan.is_cut[idx - idx0]) continue;
             count = 2;
             first = next = 0;
         } else {
-            const Cut cut = plan.cuts[(w - n_half) / kChunks];
+            const Cut cut = plan.cuts[(w - n_half) / kUnits];
             blk = cut.block;
             g = cut.g;
-            row = int((w - n_half) % kChunks) * kRowsPerCta + sub;
+            row0 = int((w - n_half) % kUnits) * kMergeRows;
             count = 1 + cut.more;
             first = int64_t(plan.ctas + cut.cta) * plan.slot_rows;
             next = int64_t(cut.cta) * plan.slot_rows;
         }
         const Block m = plan.blocks[blk];
         const int rows = m.ntok * G;
-        if (row >= rows) continue;
+        if (row0 >= rows) continue;
         if (w < n_half) {
+            const int64_t idx =
+                plan.header[kHdrByHead] ? int64_t(g) * nblocks + blk : int64_t(blk) * hkv + g;
+            if (idx >= idx0 && plan.is_cut[idx - idx0]) continue;
             first = next = m.prow + int64_t(g) * 2 * rows;
         } else {
             halves = m.ntok <= sh.tokens_per_tile ? 2 : 1;
             count *= halves;
         }
-        // partial p: piece p / halves, half p % halves
-        auto at = [&](int p) {
-            const int piece = halves == 2 ? p >> 1 : p;
-            return (piece ? next + int64_t(piece) * plan.slot_rows : first) +
-                   (halves == 2 ? (p & 1) * rows : 0) + row;
-        };
-        const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + c;
-        float M = -INFINITY, W = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        bool broken = false;
-        for (int p0 = 0; p0 < count; p0 += 8) {
-            float l[8];
-            float4 x[8];
+        const int end = min(rows, row0 + kMergeRows);
+#pragma unroll 2
+        for (int row = row0 + sub; row < end; row += kAtOnce) {
+            // partial p: piece p / halves, half p % halves
+            auto at = [&](int p) {
+                const int piece = halves == 2 ? p >> 1 : p;
+                return (piece ? next + int64_t(piece) * plan.slot_rows : first) +
+                       (halves == 2 ? (p & 1) * rows : 0) + row;
+            };
+            float M = -INFINITY, W = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            bool broken = false;
+            for (int p0 = 0; p0 < count; p0 += 4) {
+                float l[4];
+                float4 x[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const bool in = p0 + u < count;
-                const int64_t r = in ? at(p0 + u) : 0;
-                l[u] = in ? plan.lse_part[r] : -INFINITY;
-                x[u] = in ? op[r * kLanes] : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            float mc = M;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                broken |= l[u] != l[u];
-                mc = fmaxf(mc, l[u]);
-            }
-            if (mc == -INFINITY) continue;
-            const float f = expf(M - mc);
-            W *= f;
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float wt = expf(l[u] - mc);
-                if (wt != 0.f) {
-                    W += wt;
-                    acc.x = fmaf(wt, x[u].x, acc.x); acc.y = fmaf(wt, x[u].y, acc.y);
-                    acc.z = fmaf(wt, x[u].z, acc.z); acc.w = fmaf(wt, x[u].w, acc.w);
+                for (int u = 0; u < 4; ++u) {
+                    const bool in = p0 + u < count;
+                    const int64_t r = in ? at(p0 + u) : 0;
+                    l[u] = in ? plan.lse_part[r] : -INFINITY;
+                    x[u] = in ? op[r * kLanes] : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
+                float mc = M;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    broken |= l[u] != l[u];
+                    mc = fmaxf(mc, l[u]);
+                }
+                if (mc == -INFINITY) continue;
+                const float f = expf(M - mc);
+                W *= f;
+                acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float wt = expf(l[u] - mc);
+                    if (wt != 0.f) {
+                        W += wt;
+                        acc.x = fmaf(wt, x[u].x, acc.x); acc.y = fmaf(wt, x[u].y, acc.y);
+                        acc.z = fmaf(wt, x[u].z, acc.z); acc.w = fmaf(wt, x[u].w, acc.w);
+                    }
+                }
+                M = mc;
             }
-            M = mc;
+            const int64_t orow = (int64_t(m.qrow) + row / G) * a.num_q_heads + g * G + row % G;
+            float inv = W > 0.f ? 1.f / W : 0.f;
+            float lse = W > 0.f ? M + logf(W) : -INFINITY;
+            if (broken) inv = lse = __int_as_float(0x7fc00000);
+            reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + orow * D)[c] = make_uint2(
+                pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+            if (c == 0 && a.lse) a.lse[orow] = lse;
         }
-        const int64_t orow = (int64_t(m.qrow) + row / G) * a.num_q_heads + g * G + row % G;
-        float inv = W > 0.f ? 1.f / W : 0.f;
-        float lse = W > 0.f ? M + logf(W) : -INFINITY;
-        if (broken) inv = lse = __int_as_float(0x7fc00000);
-        reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + orow * D)[c] =
-            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (c == 0 && a.lse) a.lse[orow] = lse;
     }
 }
 
@@ -1380,7 +1458,7 @@ Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32
     s.pieces = take((items + s.ctas) * sizeof(Item));
     s.lse_part = take(s.rows * sizeof(float));
     s.o_part = take(size_t(s.rows) * c.head_dim_v * sizeof(float));
-    s.total = at;
+    s.total = at + 256;                  // the workspace may begin on any 16 bytes
     return s;
 }
 
@@ -1429,10 +1507,11 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
     rc = launch_pdl(kernel, dim3(sz.ctas), dim3(kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
                     sh);
     if (rc != PKV_OK) return rc;
-    const int64_t merge_rows = std::min<int64_t>(sz.rows, int64_t(a.num_tokens) * a.num_q_heads);
-    const int64_t merge_work = (merge_rows * (D / 4) + kMergeThreads - 1) / kMergeThreads;
+    const int64_t merge_units = sz.blocks * a.cache.num_kv_heads * (kRows / kMergeRows) +
+                                int64_t(sz.ctas) * (2 * kRows / kMergeRows);
+    const int64_t merge_ctas = (merge_units + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
     return launch_pdl(chunk_merge_kernel<D>,
-                      dim3(unsigned(std::min<int64_t>(merge_work, int64_t(sz.ctas) * 8))),
+                      dim3(unsigned(std::min<int64_t>(merge_ctas, int64_t(sz.ctas) * 8))),
                       dim3(kMergeThreads), 0, a.stream, a, plan, sh);
 }
 
@@ -1459,7 +1538,8 @@ int launch_chunk_tc(const ChunkArgs &in, void *workspace) {
     if (a.window >= int64_t(a.max_blocks) * a.cache.block_size) a.window = 0;
     a.sinks = std::min(a.sinks, 1 << 30);
     if (a.window == 0) a.sinks = 0;
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    uint8_t *ws = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
     if (a.k_scale) return launch<128, true>(a, ws);
     return a.cache.head_dim_k == 128 ? launch<128, false>(a, ws) : launch<64, false>(a, ws);
 }
