@@ -49,15 +49,26 @@ def _check(where: str, status: int) -> None:
 
 
 def _ptr(t: torch.Tensor | None):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # (a plain address: ctypes converts it for a c_void_p argument at a third of
+    # the cost of building the object here)
+    return None if t is None else t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    # the current stream's handle, without the Stream object around it
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dim: int | None = None):
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and (dim is None or t.dim() == dim):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -209,7 +220,7 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, factor: float = 1.
 
 
 def _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq, interleaved, q_dtype,
-               q_out):
+               q_out, stream):
     """Checks of the rope_append calls -> (q_out, flags)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(k_new, "k_new", torch.bfloat16, 3)
@@ -217,23 +228,28 @@ def _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq, interl
     _need(slots, "slot_mapping", torch.int64, 1)
     _need(inv_freq, "inv_freq", torch.float64, 1)
     T = positions.numel()
-    if slots.numel() != T or q.shape[0] != T:
+    Tq, Hq, Dk = q.shape
+    if slots.numel() != T or Tq != T:
         raise ValueError("q, positions and slots disagree on the number of tokens")
-    if q.shape[2] != desc.head_dim_k:
-        raise ValueError(f"q must have head dim {desc.head_dim_k}, got {q.shape[2]}")
-    if tuple(k_new.shape) != (T, desc.num_kv_heads, desc.head_dim_k):
+    if Dk != desc.head_dim_k:
+        raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
+    if k_new.shape != (T, desc.num_kv_heads, Dk):
         raise ValueError("k_new must be [tokens, Hkv, Dk] of the cache")
     if isinstance(v_pool, ValuesInKeys):
         if v_new is not None:
             raise ValueError("v_new must be None when the values are inside the keys")
     else:
         _need(v_new, "v_new", torch.bfloat16, 3)
-        if tuple(v_new.shape) != (T, desc.num_kv_heads, desc.head_dim_v):
+        if v_new.shape != (T, desc.num_kv_heads, desc.head_dim_v):
             raise ValueError("v_new must be [tokens, Hkv, Dv] of the cache")
     if q_out is None:
         if q_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"q_dtype must be torch.bfloat16 or torch.float32, got {q_dtype}")
-        q_out = torch.empty(q.shape, dtype=q_dtype, device=q.device)
+        if stream is None:
+            q_out = torch.empty_like(q, dtype=q_dtype)
+        else:                    # it is written on that stream: let it belong to it
+            with torch.cuda.stream(stream):
+                q_out = torch.empty_like(q, dtype=q_dtype)
     else:
         if q_out.dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"q_out must be torch.bfloat16 or torch.float32, got {q_out.dtype}")
@@ -257,7 +273,7 @@ def rope_append(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq,
     rotary part."""
     desc = _bf16_desc(k_pool, v_pool)
     q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
-                              interleaved, q_dtype, q_out)
+                              interleaved, q_dtype, q_out, stream)
     _check("pkv_rope_append", lib.pkv_rope_append(
         ctypes.byref(desc), _ptr(k_pool), _v_ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(positions), _ptr(slots), positions.numel(), _ptr(inv_freq),
@@ -273,7 +289,7 @@ def rope_append_e4m3(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq
     """rope_append into E4M3 pools (uint8 codes, fp32 scales per KV head)."""
     desc = _e4m3_desc(k_pool, v_pool, k_scale, v_scale)
     q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
-                              interleaved, q_dtype, q_out)
+                              interleaved, q_dtype, q_out, stream)
     _check("pkv_rope_append_e4m3", lib.pkv_rope_append_e4m3(
         ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(k_scale), _ptr(v_scale), _ptr(positions), _ptr(slots),
@@ -522,7 +538,14 @@ def chunk_workspace_size(k_pool, v_pool, num_tokens: int, batch: int, num_q_head
     return int(size(ctypes.byref(desc), num_tokens, batch, num_q_heads, max_blocks, int(flags)))
 
 
-def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out, lse, flags):
+# Workspaces of the chunk attention calls that bring none: one for each device
+# and stream, kept, as calls on a stream follow one another.  A capture gets
+# one of its own (graphs may run beside anything).
+_chunk_scratch: dict = {}
+
+
+def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out, lse, flags,
+                stream):
     """Checks of the chunk attention calls -> (workspace, its bytes, out, lse)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
@@ -530,26 +553,40 @@ def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out
     _need(seq_lens, "seq_lens", torch.int32, 1)
     T, Hq, Dk = q.shape
     B = seq_lens.numel()
+    Dv = desc.head_dim_v
     if Dk != desc.head_dim_k:
         raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
     if cu_q_lens.numel() != B + 1 or block_tables.shape[0] != B:
         raise ValueError("cu_q_lens must have one entry more, block_tables one row per seq_len")
+    if stream is not None and (out is None or lse is None or workspace is None):
+        # what is allocated here is used on that stream: let it belong to it
+        with torch.cuda.stream(stream):
+            return _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out,
+                               lse, flags, None)
     if out is None:
-        out = torch.empty(T, Hq, desc.head_dim_v, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, Dv), dtype=torch.bfloat16, device=q.device)
     else:
         _need(out, "out", torch.bfloat16, 3)
-        if tuple(out.shape) != (T, Hq, desc.head_dim_v):
+        if out.shape != (T, Hq, Dv):
             raise ValueError("out must be [tokens, Hq, Dv]")
     if lse is None:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     else:
         _need(lse, "lse", torch.float32, 2)
-        if tuple(lse.shape) != (T, Hq):
+        if lse.shape != (T, Hq):
             raise ValueError("lse must be [tokens, Hq]")
-    need = int(size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags))
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    need = size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if ws_bytes < need:
+        if torch.cuda.is_current_stream_capturing():
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:
+            key = (q.device.index, _stream())
+            workspace = _chunk_scratch.get(key)
+            if workspace is None or workspace.numel() < need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+                _chunk_scratch[key] = workspace
+        ws_bytes = workspace.numel()
     return workspace, ws_bytes, out, lse
 
 
@@ -567,7 +604,7 @@ def paged_chunk_attn(q, cu_q_lens, k_pool, v_pool, block_tables, seq_lens, scale
     desc = _bf16_desc(k_pool, v_pool)
     workspace, ws_bytes, out, lse = _chunk_args(
         desc, lib.pkv_chunk_workspace_size, q, cu_q_lens, block_tables, seq_lens, workspace, out,
-        lse, int(flags))
+        lse, int(flags), stream)
     _check("pkv_paged_chunk_attn", lib.pkv_paged_chunk_attn(
         ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
         _ptr(k_pool), _v_ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
@@ -584,7 +621,7 @@ def paged_chunk_attn_e4m3(q, cu_q_lens, k_pool, v_pool, k_scale, v_scale, block_
     desc = _e4m3_desc(k_pool, v_pool, k_scale, v_scale)
     workspace, ws_bytes, out, lse = _chunk_args(
         desc, lib.pkv_chunk_workspace_size_e4m3, q, cu_q_lens, block_tables, seq_lens, workspace,
-        out, lse, int(flags))
+        out, lse, int(flags), stream)
     _check("pkv_paged_chunk_attn_e4m3", lib.pkv_paged_chunk_attn_e4m3(
         ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
         _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),

@@ -124,7 +124,7 @@ struct __align__(16) Cut {
 struct Plan {                            // device pointers into the workspace
     int32_t *header;
     Block *blocks;                       // in the order of the work
-    int64_t *before;                     // cost of the blocks before each
+    int32_t *before;                     // cost of the blocks before each
     int32_t *first;                      // [batch + 1] query blocks before a sequence
     int32_t *split;                      // blocks taken as split items with partials
     uint8_t *is_cut;                     // [(block, KV head)] of the second part of the work
@@ -188,47 +188,42 @@ __device__ __forceinline__ Item item_of(const Block &q, int32_t g, int32_t s0, i
 }
 
 // Work order: (block r, KV head g) <-> index.
-__device__ __forceinline__ void item_at(int64_t idx, bool by_head, int32_t nblocks, int32_t hkv,
+__device__ __forceinline__ void item_at(int32_t idx, bool by_head, int32_t nblocks, int32_t hkv,
                                         int32_t &r, int32_t &g) {
-    if (by_head) {
-        g = int32_t(idx / nblocks);
-        r = int32_t(idx - int64_t(g) * nblocks);
-    } else {
-        r = int32_t(idx / hkv);
-        g = int32_t(idx - int64_t(r) * hkv);
-    }
+    const uint32_t n = by_head ? nblocks : hkv, q = uint32_t(idx) / n;
+    g = by_head ? q : idx - q * n;
+    r = by_head ? idx - q * n : q;
 }
 // The whole item CTA `cta` takes in round k: forth and back, so that the CTAs'
 // sums of a falling sequence stay near.
-__device__ __forceinline__ int64_t round_item(int32_t k, int32_t cta, int32_t ctas) {
-    return int64_t(k) * ctas + (k & 1 ? ctas - 1 - cta : cta);
+__device__ __forceinline__ int32_t round_item(int32_t k, int32_t cta, int32_t ctas) {
+    return k * ctas + (k & 1 ? ctas - 1 - cta : cta);
 }
 
 // ------------------------------------------------------------------- the plan
-constexpr int kPlanThreads = 1024;
-constexpr int kMaxCtas = 512;
-constexpr int kSortBlocks = 2048;        // at most so many query blocks are sorted
+constexpr int kPlanThreads = 256;        // all of them run every step: more only slow it
+                                         // down (1,024: twice the time)
+constexpr int kMaxCtas = kPlanThreads;
 // Costs in steps of an item beside its own, measured (2,048 tokens over 32K
 // keys): an item's start and end, and those of a piece of a cut item, whose
 // partial results (128 KB) go through memory; pieces of fewer steps than
 // kSnap are left to the neighbour.
 constexpr int kItemCost = 3, kPieceCost = 6, kSnap = 6;
 
-// Inclusive scans of two numbers over the CTA's 1024 threads, in place; the sums
-// go to `total`.
-struct Two {
-    int64_t x, y;
-};
-__device__ __forceinline__ Two block_scan(Two v, Two *warp_sums, Two &total) {
+// Inclusive scans of three numbers over the CTA's threads; the sums go to
+// `total`.
+__device__ __forceinline__ int3 block_scan(int3 v, int3 *warp_sums, int3 &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto warp_scan = [&](Two &u) {
+    auto warp_scan = [&](int3 &u) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, u.x, o);
-            const int64_t y = __shfl_up_sync(0xffffffffu, u.y, o);
+            const int x = __shfl_up_sync(0xffffffffu, u.x, o);
+            const int y = __shfl_up_sync(0xffffffffu, u.y, o);
+            const int z = __shfl_up_sync(0xffffffffu, u.z, o);
             if (lane >= o) {
                 u.x += x;
                 u.y += y;
+                u.z += z;
             }
         }
     };
@@ -236,17 +231,14 @@ __device__ __forceinline__ Two block_scan(Two v, Two *warp_sums, Two &total) {
     __syncthreads();
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    Two s = warp_sums[lane];
+    int3 s = lane < kPlanThreads / 32 ? warp_sums[lane] : make_int3(0, 0, 0);
     warp_scan(s);                        // by every warp: no barrier after it
-    total.x = __shfl_sync(0xffffffffu, s.x, 31);
-    total.y = __shfl_sync(0xffffffffu, s.y, 31);
-    const int64_t x = __shfl_sync(0xffffffffu, s.x, (warp + 31) & 31);
-    const int64_t y = __shfl_sync(0xffffffffu, s.y, (warp + 31) & 31);
-    if (warp) {
-        v.x += x;
-        v.y += y;
-    }
-    return v;
+    total = make_int3(__shfl_sync(0xffffffffu, s.x, 31), __shfl_sync(0xffffffffu, s.y, 31),
+                      __shfl_sync(0xffffffffu, s.z, 31));
+    const int from = (warp + 31) & 31;
+    const int x = __shfl_sync(0xffffffffu, s.x, from), y = __shfl_sync(0xffffffffu, s.y, from);
+    const int z = __shfl_sync(0xffffffffu, s.z, from);
+    return warp ? make_int3(v.x + x, v.y + y, v.z + z) : v;
 }
 
 // One CTA makes the plan.  The work -- every (query block, KV head), longest
@@ -258,16 +250,16 @@ __device__ __forceinline__ Two block_scan(Two v, Two *warp_sums, Two &total) {
 // ordered by KV head, which keeps the keys that are read at one time few.
 //
 // Up to kInShared sequences and query blocks its tables are kept in shared
-// memory: a dependent load from L2 costs more than a scan.
-constexpr int kInShared = 1024;
+// memory (a dependent load from L2 costs more than a scan); more blocks than
+// that are not sorted: the capacities even out what is left.
+constexpr int kInShared = 1024;          // (s_key: ten bits)
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
-    __shared__ Two warp_sums[32];
-    __shared__ uint32_t keys[kSortBlocks];
+    __shared__ int3 warp_sums[32];
     __shared__ int32_t s_first[kInShared + 1], s_cu[kInShared + 1], s_len[kInShared];
-    __shared__ int64_t s_before[kInShared + 1];
-    __shared__ int32_t s_steps[kInShared], s_prow[kInShared];
+    __shared__ int32_t s_before[kInShared + 1], s_steps[kInShared], s_prow[kInShared];
+    __shared__ uint32_t s_key[kInShared];            // low 10 bits: the block at a place
     __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
     __shared__ int32_t s_max, s_min;
     pdl_wait();
@@ -275,7 +267,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     const int tid = threadIdx.x;
     const int32_t hkv = a.cache.num_kv_heads, tpt = sh.tokens_per_tile, per = 2 * tpt;
     const int32_t ctas = plan.ctas;
-    Two total;
+    int3 total;
 
     // ---- query blocks before each sequence
     const bool few_seqs = a.batch <= kInShared;
@@ -293,7 +285,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
             y = a.cu_q_lens[b + 1];
             L = a.seq_lens[b];
             if (x < 0 || y < x || y > a.num_tokens) bad = true;
-            else nq = (y - x + per - 1) / per;
+            else nq = uint32_t(y - x + per - 1) / uint32_t(per);
             if (L < 0 || L > int64_t(a.max_blocks) * a.cache.block_size) {
                 raise_status(a.status, PKV_DEV_SEQ_LEN);
                 L = 0;
@@ -301,19 +293,6 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
                 raise_status(a.status, PKV_DEV_SEQ_LEN);
             }
         }
-        const Two incl = block_scan({nq, 0}, warp_sums, total);
-        if (b < a.batch) {
-            const int32_t before = nblocks + int32_t(incl.x) - nq;
-            if (few_seqs) {
-                s_first[b] = before;
-                s_cu[b] = x;
-                s_cu[b + 1] = y;
-                s_len[b] = L;
-            } else {
-                plan.first[b] = before;
-            }
-        }
-        nblocks += int32_t(total.x);
         if (__syncthreads_or(bad)) {
             if (tid == 0) {
                 raise_status(a.status, PKV_DEV_QUERY_RANGE);
@@ -323,10 +302,23 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
             for (int j = tid; j <= ctas; j += kPlanThreads) plan.piece0[j] = 0;
             return;
         }
+        const int3 incl = block_scan(make_int3(nq, 0, 0), warp_sums, total);
+        if (b < a.batch) {
+            const int32_t before = nblocks + incl.x - nq;
+            if (few_seqs) {
+                s_first[b] = before;
+                s_cu[b] = x;
+                s_cu[b + 1] = y;
+                s_len[b] = L;
+            } else {
+                plan.first[b] = before;
+            }
+        }
+        nblocks += total.x;
     }
     if (tid == 0) (few_seqs ? s_first : plan.first)[a.batch] = nblocks;
     __syncthreads();
-    const bool few_blocks = nblocks <= kInShared, sortable = nblocks <= kSortBlocks;
+    const bool few_blocks = nblocks <= kInShared;
 
     auto block_of = [&](int i) {
         const int32_t *first = few_seqs ? s_first : plan.first;
@@ -356,7 +348,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     int32_t most = 0, least = INT_MAX;
     for (int i = tid; i < nblocks; i += kPlanThreads) {
         const Block q = block_of(i);
-        if (sortable) keys[i] = uint32_t((1 << 20) - 1 - min(q.steps, (1 << 20) - 1)) << 11 | i;
+        if (few_blocks) s_key[i] = uint32_t((1 << 20) - 1 - min(q.steps, (1 << 20) - 1)) << 10 | i;
         most = max(most, q.steps);
         least = min(least, q.steps);
     }
@@ -367,47 +359,49 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         atomicMin(&s_min, least);
     }
     __syncthreads();
-    const bool alike = s_max - s_min <= s_max / 4;
-    const bool by_head = alike;
-    if (sortable && !alike) {
+    const bool by_head = s_max - s_min <= s_max / 4;       // nearly alike
+    const int32_t n_items = nblocks * hkv;       // below 2^29 as the query rows are
+    // costs in units of 2^shift steps, so that their sum stays below 2^30
+    int32_t shift = 0;
+    while (float(s_max + kItemCost) * float(n_items) > float(1 << 30) * float(1u << shift)) ++shift;
+    auto cost_of = [&](int32_t steps) { return ((steps + kItemCost) >> shift) + (shift > 0); };
+    const int32_t item_cost = cost_of(0), piece_cost = (kPieceCost >> shift) + (shift > 0);
+    if (few_blocks && !by_head && n_items > ctas) {
         int n = 1;
         while (n < nblocks) n <<= 1;
-        for (int i = nblocks + tid; i < n; i += kPlanThreads) keys[i] = 0xffffffffu;
+        for (int i = nblocks + tid; i < n; i += kPlanThreads) s_key[i] = 0xffffffffu;
         for (int k = 2; k <= n; k <<= 1)
             for (int j = k >> 1; j > 0; j >>= 1) {
                 __syncthreads();
                 for (int i = tid; i < n; i += kPlanThreads) {
                     const int x = i ^ j;
                     if (x > i) {
-                        const uint32_t u = keys[i], v = keys[x];
+                        const uint32_t u = s_key[i], v = s_key[x];
                         if ((u > v) == ((i & k) == 0)) {
-                            keys[i] = v;
-                            keys[x] = u;
+                            s_key[i] = v;
+                            s_key[x] = u;
                         }
                     }
                 }
             }
         __syncthreads();
     }
-    auto ordered = [&](int r) {
-        return block_of(sortable ? int(keys[r] & (kSortBlocks - 1)) : r);
-    };
-    int64_t cost_all = 0, nsplit = 0, part_rows = int64_t(2) * ctas * plan.slot_rows;
+    auto ordered = [&](int r) { return block_of(few_blocks ? int(s_key[r] & 1023u) : r); };
+    int32_t cost_all = 0, nsplit = 0, part_rows = 2 * ctas * plan.slot_rows;
     for (int base = 0; base < nblocks; base += kPlanThreads) {
         const int i = base + tid;
         Block q = {};
         const bool in = i < nblocks;
         if (in) q = ordered(i);
         const bool halves = in && q.ntok <= tpt && q.tiles > 1;
-        const int64_t cost = in ? q.steps + kItemCost : 0;
-        const int64_t rows = halves ? int64_t(2) * q.ntok * sh.group * hkv : 0;
-        // costs beside the count of split blocks: both below 2^31
-        const Two v = block_scan({cost << 24 | halves, rows}, warp_sums, total);
+        const int32_t cost = in ? cost_of(q.steps) : 0;
+        const int32_t rows = halves ? 2 * q.ntok * sh.group * hkv : 0;
+        const int3 v = block_scan(make_int3(cost, halves, rows), warp_sums, total);
         if (in) {
-            const int64_t before = cost_all + (v.x >> 24) - cost;
+            const int32_t before = cost_all + v.x - cost;
             if (halves) {
-                plan.split[nsplit + (v.x & 0xffffff) - 1] = i;
-                q.prow = int32_t(part_rows + v.y - rows);
+                plan.split[nsplit + v.y - 1] = i;
+                q.prow = part_rows + v.z - rows;
             }
             plan.blocks[i] = q;
             if (few_blocks) {
@@ -418,26 +412,24 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
                 plan.before[i] = before;
             }
         }
-        cost_all += total.x >> 24;
-        nsplit += total.x & 0xffffff;
-        part_rows += total.y;
+        cost_all += total.x;
+        nsplit += total.y;
+        part_rows += total.z;
     }
     if (tid == 0) (few_blocks ? s_before : plan.before)[nblocks] = cost_all;
     __syncthreads();
-    const int64_t *before = few_blocks ? s_before : plan.before;
+    const int32_t *before = few_blocks ? s_before : plan.before;
     auto steps_at = [&](int r) { return few_blocks ? s_steps[r] : plan.blocks[r].steps; };
 
     // ---- whole rounds
-    const int64_t n_items = int64_t(nblocks) * hkv;
-    const int64_t share = (cost_all * hkv + int64_t(ctas) * kPieceCost + ctas - 1) / ctas;
-    int64_t load = 0;
-    int32_t rounds = 0;
-    while ((rounds + 1) * int64_t(ctas) <= n_items) {
-        int64_t next = load;
+    const int32_t share = uint32_t(cost_all * hkv) / uint32_t(ctas) + 1 + piece_cost;
+    int32_t load = 0, rounds = 0;
+    while ((rounds + 1) * ctas <= n_items) {
+        int32_t next = load;
         if (tid < ctas) {
             int32_t r, g;
             item_at(round_item(rounds, tid, ctas), by_head, nblocks, hkv, r, g);
-            next += steps_at(r) + kItemCost;
+            next += cost_of(steps_at(r));
         }
         if (__syncthreads_or(next > share)) break;
         load = next;
@@ -445,49 +437,48 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     }
 
     // ---- the rest, cut by the capacities left
-    const int64_t idx0 = int64_t(rounds) * ctas;
+    const int32_t idx0 = rounds * ctas;
     int32_t r0 = 0, g0 = 0;
     if (idx0 < n_items) item_at(idx0, by_head, nblocks, hkv, r0, g0);
-    const int64_t done = idx0 >= n_items ? cost_all * hkv
+    const int32_t done = idx0 >= n_items ? cost_all * hkv
                          : by_head       ? g0 * cost_all + before[r0]
-                                   : before[r0] * hkv + g0 * int64_t(steps_at(r0) + kItemCost);
-    const int64_t rest = cost_all * hkv - done;
-    for (int64_t i = idx0 + tid; i < n_items; i += kPlanThreads) plan.is_cut[i - idx0] = 0;
-    const int64_t cap = tid < ctas ? max(int64_t(0), share - kPieceCost - load) : 0;
-    const int64_t upto = block_scan({cap, 0}, warp_sums, total).x;
+                                         : before[r0] * hkv + g0 * cost_of(steps_at(r0));
+    const int32_t rest = cost_all * hkv - done;
+    for (int32_t i = idx0 + tid; i < n_items; i += kPlanThreads) plan.is_cut[i - idx0] = 0;
+    const int32_t cap = tid < ctas ? max(0, share - piece_cost - load) : 0;
+    const int32_t upto = block_scan(make_int3(cap, 0, 0), warp_sums, total).x;
     if (tid == 0) {
-        cut_idx[0] = int32_t(idx0);
+        cut_idx[0] = idx0;
         cut_step[0] = 0;
     }
     if (tid < ctas) {
-        // the end of CTA tid's part: position x of the rest
-        int64_t idx = n_items;
-        int32_t step = 0;
+        // the end of CTA tid's part: position x of the rest (in binary32: only its
+        // order counts)
+        int32_t idx = n_items, step = 0;
         if (rest > 0 && tid < ctas - 1 && total.x > 0) {
-            const int64_t x = done + int64_t(double(rest) * (double(upto) / double(total.x)));
-            int64_t y = x;
-            int32_t g = 0;
+            const int32_t x =
+                done + min(rest, int32_t(float(rest) * (float(upto) / float(total.x))));
+            int32_t g = 0, y = x;
             if (by_head) {
-                g = int32_t(min(x / cost_all, int64_t(hkv - 1)));
+                g = min(int32_t(uint32_t(x) / uint32_t(cost_all)), hkv - 1);
                 y = x - g * cost_all;
-            } else {
-                y = x / hkv;
             }
-            int lo = 0, hi = nblocks;            // before[lo] <= y < before[hi]
+            const int32_t times = by_head ? 1 : hkv;
+            int lo = 0, hi = nblocks;            // before[lo] <= y / times < before[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (before[mid] <= y) lo = mid;
+                if (before[mid] * times <= y) lo = mid;
                 else hi = mid;
             }
             const int32_t steps = steps_at(lo);
-            int64_t off = y - before[lo];
+            int32_t off = y - before[lo] * times;
             if (!by_head) {
-                off = x - before[lo] * hkv;
-                g = int32_t(min(off / (steps + kItemCost), int64_t(hkv - 1)));
-                off -= g * int64_t(steps + kItemCost);
+                const int32_t c = cost_of(steps);
+                g = min(int32_t(uint32_t(off) / uint32_t(c)), hkv - 1);
+                off -= g * c;
             }
-            idx = by_head ? int64_t(g) * nblocks + lo : int64_t(lo) * hkv + g;
-            step = int32_t(min(max(off - kItemCost, int64_t(0)), int64_t(steps)));
+            idx = by_head ? g * nblocks + lo : lo * hkv + g;
+            step = min(max(off - item_cost, 0) << shift, steps);
             if (step < kSnap) step = 0;
             else if (steps - step < kSnap) {
                 step = 0;
@@ -498,7 +489,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
                 step = 0;
             }
         }
-        cut_idx[tid + 1] = int32_t(idx);
+        cut_idx[tid + 1] = idx;
         cut_step[tid + 1] = step;
     }
     __syncthreads();
@@ -513,10 +504,10 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         // this part begins an item that goes on
         cut = s1 > 0 && (i1 > i0 || s0 == 0);
     }
-    const Two at = block_scan({count, cut}, warp_sums, total);
+    const int3 at = block_scan(make_int3(count, cut, 0), warp_sums, total);
     if (tid < ctas) {
-        const int64_t p0 = at.x - count;
-        plan.piece0[tid] = int32_t(p0);
+        const int32_t p0 = at.x - count;
+        plan.piece0[tid] = p0;
         for (int k = 0; k < count; ++k) {
             const int32_t idx = i0 + k, from = k ? 0 : s0;
             int32_t r, g;
@@ -540,12 +531,12 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         }
     }
     if (tid == 0) {
-        plan.piece0[ctas] = int32_t(total.x);
+        plan.piece0[ctas] = total.x;
         plan.header[kHdrBlocks] = nblocks;
         plan.header[kHdrRounds] = rounds;
         plan.header[kHdrByHead] = by_head;
-        plan.header[kHdrSplit] = int32_t(nsplit);
-        plan.header[kHdrCuts] = int32_t(total.y);
+        plan.header[kHdrSplit] = nsplit;
+        plan.header[kHdrCuts] = total.y;
     }
 }
 
@@ -1284,29 +1275,29 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     const int hkv = a.cache.num_kv_heads, G = sh.group;
     // the split items taken whole (two partials of at most kRows rows each), then the cuts
     constexpr int kHalfUnits = kRows / kMergeRows, kUnits = 2 * kHalfUnits;
-    const int64_t n_half = int64_t(plan.header[kHdrSplit]) * hkv * kHalfUnits;
-    const int64_t total = n_half + int64_t(plan.header[kHdrCuts]) * kUnits;
+    const int32_t n_short = plan.header[kHdrSplit] * hkv, n_half = n_short * kHalfUnits;
+    const int32_t total = n_half + plan.header[kHdrCuts] * kUnits;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
     const int nblocks = plan.header[kHdrBlocks];
-    const int64_t idx0 = int64_t(plan.header[kHdrRounds]) * plan.ctas;
+    const int32_t idx0 = plan.header[kHdrRounds] * plan.ctas;
     const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + c;
     constexpr int kWarps = kMergeThreads / 32;
-    for (int64_t w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < total; w += gridDim.x * kWarps) {
+    for (int32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < total; w += gridDim.x * kWarps) {
         int blk, g, row0, count, halves = 2;
         int64_t first, next;                 // rows of the first piece, and of the others'
         if (w < n_half) {
             // (unit-major, so that the units past a short item's rows end up in other warps)
-            const int64_t sg = w % (n_half / kHalfUnits);
-            row0 = int(w / (n_half / kHalfUnits)) * kMergeRows;
+            const int32_t unit = w / n_short, sg = w - unit * n_short;
+            row0 = unit * kMergeRows;
             blk = plan.split[sg / hkv];
-            g = int(sg % hkv);
+            g = sg % hkv;
             count = 2;
             first = next = 0;
         } else {
             const Cut cut = plan.cuts[(w - n_half) / kUnits];
             blk = cut.block;
             g = cut.g;
-            row0 = int((w - n_half) % kUnits) * kMergeRows;
+            row0 = (w - n_half) % kUnits * kMergeRows;
             count = 1 + cut.more;
             first = int64_t(plan.ctas + cut.cta) * plan.slot_rows;
             next = int64_t(cut.cta) * plan.slot_rows;
@@ -1315,8 +1306,7 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         const int rows = m.ntok * G;
         if (row0 >= rows) continue;
         if (w < n_half) {
-            const int64_t idx =
-                plan.header[kHdrByHead] ? int64_t(g) * nblocks + blk : int64_t(blk) * hkv + g;
+            const int32_t idx = plan.header[kHdrByHead] ? g * nblocks + blk : blk * hkv + g;
             if (idx >= idx0 && plan.is_cut[idx - idx0]) continue;
             first = next = m.prow + int64_t(g) * 2 * rows;
         } else {
@@ -1448,7 +1438,7 @@ Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32
         return here;
     };
     s.blocks_at = take(s.blocks * sizeof(Block));
-    s.before = take((s.blocks + 1) * sizeof(int64_t));
+    s.before = take((s.blocks + 1) * sizeof(int32_t));
     s.first = take((size_t(batch) + 1) * sizeof(int32_t));
     s.split = take(s.blocks * sizeof(int32_t));
     s.is_cut = take(items);
@@ -1470,7 +1460,7 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
     const Sizes sz = sizes_of(a.cache, a.num_tokens, a.batch, a.num_q_heads);
     const Plan plan{reinterpret_cast<int32_t *>(ws),
                     reinterpret_cast<Block *>(ws + sz.blocks_at),
-                    reinterpret_cast<int64_t *>(ws + sz.before),
+                    reinterpret_cast<int32_t *>(ws + sz.before),
                     reinterpret_cast<int32_t *>(ws + sz.first),
                     reinterpret_cast<int32_t *>(ws + sz.split),
                     ws + sz.is_cut,
