@@ -47,6 +47,8 @@ struct RopeArgs {
     int32_t rot, off;                    // rotary_dim, rotary_offset
     int32_t q_units, v_units;            // work units of a q/k row and of a v row
     uint32_t q_magic, v_magic;           // ceil(2^32 / units): index -> row
+    uint32_t tok_magic;                  // of a token's units, where tokens are grouped
+    int32_t group, parts;                // tokens of a work item; items of a token
     float amplitude;
     int32_t q_fp32, in_place;
 };
@@ -246,17 +248,420 @@ rope_append_kernel(const RopeArgs a) {
     }
 }
 
+// The form for rows that split into units of 16 elements (head dims, rotary_dim and
+// rotary_offset multiples of 16).  A unit is two 16-byte vectors: of the two halves
+// of the rotary part (half layout), or neighbours.  A thread keeps one unit
+// position and walks rows (a token's query heads, key heads, value heads, then the
+// next token's), so that only the row is left to be worked out for each unit; the
+// instructions, not the bytes, are what a simpler mapping was bound by.  A CTA takes
+// `group` tokens, or 1 / parts of one with many heads, at a time; kAhead units of
+// the next rows are loaded while the last ones are turned and stored.
+constexpr int kAhead = 2;
+constexpr int kWideCtas = 3;             // per SM
+constexpr int kItemUnits = 2048;         // units of a work item, about
+constexpr int kTable = 1024;             // entries of a table of cosines and sines
+
+template <bool INTER, bool E4>
+__global__ void __launch_bounds__(kThreads, kWideCtas)
+rope_append_wide_kernel(const RopeArgs a) {
+    __shared__ __align__(16) float2 cs[2][kTable];   // (cos, sin) * amplitude
+    __shared__ uint64_t step[kMaxPairs];
+    __shared__ int64_t s_slot[2][8];             // slot of a token's rows, or -1: not stored
+    __shared__ int32_t s_live[2][8];
+    const int npairs = a.rot >> 1;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < npairs; i += kThreads) step[i] = turn_step(a.inv_freq[i]);
+    __syncthreads();
+    // this thread's unit of a row, and the row it takes first
+    const int r0 = fast_div(threadIdx.x, a.q_magic, a.q_units), c = threadIdx.x - r0 * a.q_units;
+    const int rows_pass = kThreads / a.q_units;      // rows a pass of the CTA covers
+    const bool works = r0 < rows_pass;
+    const int rows_qk = a.hq + a.hkv, rows_tok = rows_qk + (a.dv ? a.hkv : 0);
+    bool turned;
+    int ea, eb;
+    if constexpr (INTER) {
+        ea = 16 * c;
+        eb = ea + 8;
+        turned = ea >= a.off && ea < a.off + a.rot;
+    } else {
+        turned = c < (a.rot >> 4);
+        ea = turned ? a.off + 8 * c : 16 * (c - (a.rot >> 4));
+        if (!turned && ea >= a.off) ea += a.rot;
+        eb = turned ? ea + (a.rot >> 1) : ea + 8;
+    }
+    // A unit's eight pairs are four 16-byte entries of the table, kept so that
+    // neighbouring units' entries are neighbours (no bank conflicts): entry i of
+    // unit u at i * (rotary units) + u.
+    const int nr = a.rot >> 4, unit = INTER ? c - (a.off >> 4) : c;
+    const int64_t groups = (a.num_tokens + a.group - 1) / a.group;
+    int buf = 0;
+    for (int64_t w = blockIdx.x; w < groups * a.parts; w += gridDim.x) {
+        const int64_t grp = a.parts > 1 ? w / a.parts : w;
+        const int part = a.parts > 1 ? int(w - grp * a.parts) : 0;
+        const int64_t t0 = grp * a.group;
+        const int ntok = int(a.num_tokens - t0 < a.group ? a.num_tokens - t0 : a.group);
+        const int per = (rows_tok + a.parts - 1) / a.parts;
+        const int begin = part * per;
+        const int end = a.parts > 1 ? min(rows_tok, begin + per) : ntok * rows_tok;
+        auto load = [&](int row, uint4 &va, uint4 &vb) {
+            if (!works || row >= end) return;
+            const int tk = a.group > 1 ? fast_div(row, a.tok_magic, rows_tok) : 0;
+            row -= tk * rows_tok;
+            const int64_t t = t0 + tk;
+            const uint16_t *src;
+            int e0 = ea, e1 = eb;
+            if (row < a.hq) {
+                src = a.q + (t * a.hq + row) * a.dk;
+            } else if (row < rows_qk) {
+                src = a.k_new + (t * a.hkv + row - a.hq) * a.dk;
+            } else {
+                if (16 * c >= a.dv) return;
+                src = a.v_new + (t * a.hkv + row - rows_qk) * a.dv;
+                e0 = 16 * c;
+                e1 = e0 + 8;
+            }
+            va = *reinterpret_cast<const uint4 *>(src + e0);
+            vb = *reinterpret_cast<const uint4 *>(src + e1);
+        };
+        auto finish = [&](int row, const uint4 &va, const uint4 &vb) {
+            if (!works || row >= end) return;
+            const int tk = a.group > 1 ? fast_div(row, a.tok_magic, rows_tok) : 0;
+            row -= tk * rows_tok;
+            const int64_t slot = s_slot[buf][tk];
+            const bool is_q = row < a.hq;
+            if (is_q ? !s_live[buf][tk] || (a.in_place && !turned) : slot < 0) return;
+            float x[8], y[8];
+            unpack8(va, x);
+            unpack8(vb, y);
+            if (turned && row < rows_qk) {
+                const float4 *r =
+                    reinterpret_cast<const float4 *>(cs[buf] + tk * npairs) + unit;
+                if constexpr (INTER) {
+                    auto turn = [](float (&v)[8], int i, const float4 &q) {
+                        float p = v[4 * i], s = v[4 * i + 1];
+                        v[4 * i] = p * q.x - s * q.y;
+                        v[4 * i + 1] = s * q.x + p * q.y;
+                        p = v[4 * i + 2], s = v[4 * i + 3];
+                        v[4 * i + 2] = p * q.z - s * q.w;
+                        v[4 * i + 3] = s * q.z + p * q.w;
+                    };
+                    turn(x, 0, r[0]);
+                    turn(x, 1, r[nr]);
+                    turn(y, 0, r[2 * nr]);
+                    turn(y, 1, r[3 * nr]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 q = r[i * nr];
+                        float p = x[2 * i], s = y[2 * i];
+                        x[2 * i] = p * q.x - s * q.y;
+                        y[2 * i] = s * q.x + p * q.y;
+                        p = x[2 * i + 1], s = y[2 * i + 1];
+                        x[2 * i + 1] = p * q.z - s * q.w;
+                        y[2 * i + 1] = s * q.z + p * q.w;
+                    }
+                }
+            }
+            if (is_q) {
+                const int64_t dst = ((t0 + tk) * a.hq + row) * a.dk;
+                if (a.q_fp32) {
+                    store8_f32(a.q_out, dst + ea, x);
+                    store8_f32(a.q_out, dst + eb, y);
+                } else {
+                    store8_bf16(a.q_out, dst + ea, x);
+                    store8_bf16(a.q_out, dst + eb, y);
+                }
+                return;
+            }
+            const bool is_k = row < rows_qk;
+            const int g = is_k ? row - a.hq : row - rows_qk, d = is_k ? a.dk : a.dv;
+            if (!is_k && 16 * c >= a.dv) return;
+            const int e0 = is_k ? ea : 16 * c, e1 = is_k ? eb : 16 * c + 8;
+            void *pool = is_k ? a.k_pool : a.v_pool;
+            // s_slot holds the row of KV head 0
+            const int64_t dst = (slot + int64_t(g) * a.block_size) * d;
+            if constexpr (E4) {
+                const float s = (is_k ? a.k_scale : a.v_scale)[g];
+                store8_e4m3(pool, dst + e0, x, s);
+                store8_e4m3(pool, dst + e1, y, s);
+            } else {
+                store8_bf16(pool, dst + e0, x);
+                store8_bf16(pool, dst + e1, y);
+            }
+        };
+        uint4 va[2][kAhead], vb[2][kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            load(begin + k * rows_pass + r0, va[0][k], vb[0][k]);
+        // the tokens' slots and angles, while the first units come in
+        if (threadIdx.x < ntok) {
+            const int64_t slot = a.slots[t0 + threadIdx.x];
+            const int64_t pos = a.positions[t0 + threadIdx.x];
+            const bool stored = pos >= 0 && slot >= 0 && slot < a.num_slots;
+            if (pos >= 0 && slot >= a.num_slots) raise_status(a.status, PKV_DEV_SLOT);
+            const int64_t block = stored ? slot / a.block_size : 0;
+            s_slot[buf][threadIdx.x] =
+                stored ? block * a.hkv * a.block_size + (slot - block * a.block_size) : -1;
+            s_live[buf][threadIdx.x] = pos >= 0;
+        }
+        for (int i = threadIdx.x; i < ntok * npairs; i += kThreads) {
+            const int tk = a.group > 1 ? i / npairs : 0, pr = i - tk * npairs;
+            const uint64_t turn = step[pr] * uint64_t(a.positions[t0 + tk]);
+            // signed 2^-32 turns; sincospif takes half turns
+            const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
+            float s, co;
+            sincospif(x, &s, &co);
+            const int entry = ((pr >> 1) & 3) * nr + (pr >> 3);
+            cs[buf][tk * npairs + 2 * entry + (pr & 1)] =
+                make_float2(co * a.amplitude, s * a.amplitude);
+        }
+        __syncthreads();
+        const int pass = rows_pass * kAhead;
+        for (int row = begin + r0; row < end + r0; row += 2 * pass) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int here = row + half * pass;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    load(here + pass + k * rows_pass, va[half ^ 1][k], vb[half ^ 1][k]);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    finish(here + k * rows_pass, va[half][k], vb[half][k]);
+            }
+        }
+        buf ^= 1;      // the other table: this one may still be read by slower warps
+    }
+}
+
+// The form for the common heads: head_dim_k = head_dim_v (or values inside the keys)
+// of 64, 128, 256 or 512 and at most 128 rotary elements.  A warp takes a token, or one
+// of its `parts`: 32 / U rows at a time (U = head_dim / 16 units a row), each lane the
+// same unit of every row, with the cosines and sines of its eight pairs in
+// registers -- two pairs a lane are computed, then handed round by shuffles -- so
+// that rows need neither table nor barrier, and the rows AHEAD passes on are on
+// their way.  Many tokens: 4 ahead on two CTAs an SM (8,191 tokens of 32 + 8 heads
+// of 128: 36.9 us, 5.5 TB/s, against 41.3 us for 2 ahead on three CTAs); a few
+// thousand: 2 ahead on three CTAs, whose warps take all of them at once (2,500
+// tokens into an FP8 cache: 25.6 us against 30.3 us).
+
+template <bool INTER, bool E4, int AHEAD, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS)
+rope_append_warp_kernel(const RopeArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int U = a.q_units, shift = 31 - __clz(U), rpp = 32 >> shift;
+    const int c = lane & (U - 1), r0 = lane >> shift, nr = a.rot >> 4, npairs = a.rot >> 1;
+    bool turned;
+    int ea, eb, unit;
+    if constexpr (INTER) {
+        unit = c - (a.off >> 4);
+        turned = unit >= 0 && unit < nr;
+        ea = 16 * c;
+        eb = ea + 8;
+    } else {
+        unit = c;
+        turned = c < nr;
+        ea = turned ? a.off + 8 * c : 16 * (c - nr);
+        if (!turned && ea >= a.off) ea += a.rot;
+        eb = turned ? ea + (a.rot >> 1) : ea + 8;
+    }
+    // this lane's pairs: lane and lane + 32
+    uint64_t step[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        step[i] = lane + 32 * i < npairs ? turn_step(a.inv_freq[lane + 32 * i]) : 0;
+    const int pq = (a.hq + rpp - 1) >> (5 - shift), pk = (a.hkv + rpp - 1) >> (5 - shift);
+    const int passes = pq + pk + (a.dv ? pk : 0), per = (passes + a.parts - 1) / a.parts;
+    const int64_t items = a.num_tokens * a.parts;
+    const int warps = gridDim.x * (kThreads / 32);
+    for (int64_t w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < items; w += warps) {
+        const int64_t t = a.parts > 1 ? w / a.parts : w;
+        const int begin = a.parts > 1 ? int(w - t * a.parts) * per : 0;
+        const int end = min(passes, begin + per);
+        const int64_t pos = a.positions[t], slot = a.slots[t];
+        uint4 va[AHEAD], vb[AHEAD];
+        // pass p: rows of queries, keys, then values
+        auto load = [&](int p, uint4 &x, uint4 &y) {
+            if (p >= end) return;
+            const uint16_t *src;
+            int row, heads, e0 = ea, e1 = eb;
+            if (p < pq) {
+                row = (p << (5 - shift)) + r0;
+                heads = a.hq;
+                src = a.q;
+            } else {
+                const bool is_k = p < pq + pk;
+                row = ((p - pq - (is_k ? 0 : pk)) << (5 - shift)) + r0;
+                heads = a.hkv;
+                src = is_k ? a.k_new : a.v_new;
+                if (!is_k) {
+                    e0 = 16 * c;
+                    e1 = e0 + 8;
+                }
+            }
+            if (row >= heads) return;
+            src += (t * heads + row) * a.dk;
+            x = *reinterpret_cast<const uint4 *>(src + e0);
+            y = *reinterpret_cast<const uint4 *>(src + e1);
+        };
+        if (pos < 0) continue;                       // padding (the whole warp)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) load(begin + k, va[k], vb[k]);
+        // ---- the angles
+        float co[8], si[8];
+        {
+            float c2[2], s2[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint64_t turn = step[i] * uint64_t(pos);
+                // signed 2^-32 turns; sincospif takes half turns
+                sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s2[i], &c2[i]);
+                c2[i] *= a.amplitude;
+                s2[i] *= a.amplitude;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int pr = (8 * unit + j) & 63;
+                const float cl = __shfl_sync(0xffffffffu, c2[0], pr & 31);
+                const float ch = __shfl_sync(0xffffffffu, c2[1], pr & 31);
+                const float sl = __shfl_sync(0xffffffffu, s2[0], pr & 31);
+                const float sh = __shfl_sync(0xffffffffu, s2[1], pr & 31);
+                co[j] = pr < 32 ? cl : ch;
+                si[j] = pr < 32 ? sl : sh;
+            }
+        }
+        if (slot >= a.num_slots && lane == 0 && begin == 0) raise_status(a.status, PKV_DEV_SLOT);
+        const bool stored = slot >= 0 && slot < a.num_slots;
+        const int64_t block = stored ? slot / a.block_size : 0;
+        const int64_t row0 = block * a.hkv * a.block_size + (stored ? slot - block * a.block_size : 0);
+        auto finish = [&](int p, const uint4 &va, const uint4 &vb) {
+            if (p >= end) return;
+            const bool is_q = p < pq, is_k = !is_q && p < pq + pk;
+            const int row = ((p - (is_q ? 0 : is_k ? pq : pq + pk)) << (5 - shift)) + r0;
+            if (row >= (is_q ? a.hq : a.hkv)) return;
+            if (is_q ? a.in_place && !turned : !stored) return;
+            float x[8], y[8];
+            unpack8(va, x);
+            unpack8(vb, y);
+            if (turned && (is_q || is_k)) {
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = x[2 * i], s0 = x[2 * i + 1];
+                        x[2 * i] = p0 * co[i] - s0 * si[i];
+                        x[2 * i + 1] = s0 * co[i] + p0 * si[i];
+                        const float p1 = y[2 * i], s1 = y[2 * i + 1];
+                        y[2 * i] = p1 * co[4 + i] - s1 * si[4 + i];
+                        y[2 * i + 1] = s1 * co[4 + i] + p1 * si[4 + i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 = x[i], s0 = y[i];
+                        x[i] = p0 * co[i] - s0 * si[i];
+                        y[i] = s0 * co[i] + p0 * si[i];
+                    }
+                }
+            }
+            if (is_q) {
+                const int64_t dst = (t * a.hq + row) * a.dk;
+                if (a.q_fp32) {
+                    store8_f32(a.q_out, dst + ea, x);
+                    store8_f32(a.q_out, dst + eb, y);
+                } else {
+                    store8_bf16(a.q_out, dst + ea, x);
+                    store8_bf16(a.q_out, dst + eb, y);
+                }
+                return;
+            }
+            const int e0 = is_k ? ea : 16 * c, e1 = is_k ? eb : 16 * c + 8;
+            void *pool = is_k ? a.k_pool : a.v_pool;
+            const int64_t dst = (row0 + int64_t(row) * a.block_size) * a.dk;
+            if constexpr (E4) {
+                const float s = (is_k ? a.k_scale : a.v_scale)[row];
+                store8_e4m3(pool, dst + e0, x, s);
+                store8_e4m3(pool, dst + e1, y, s);
+            } else {
+                store8_bf16(pool, dst + e0, x);
+                store8_bf16(pool, dst + e1, y);
+            }
+        };
+        for (int p = begin; p < end; p += AHEAD)
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const uint4 x = va[k], y = vb[k];
+                load(p + AHEAD + k, va[k], vb[k]);
+                finish(p + k, x, y);
+            }
+    }
+}
+
 uint32_t magic_of(int n) { return n > 1 ? uint32_t(((uint64_t(1) << 32) + n - 1) / n) : 0; }
+
+template <bool E4, int AHEAD, int CTAS>
+int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
+    // Parts of a token: the fewest rounds of warps x (passes of a part + 2 for its
+    // angles), so that few tokens spread over the device and the last round of
+    // many is not mostly empty.
+    constexpr int per_cta = kThreads / 32;
+    const int64_t warps = int64_t(sm_count()) * CTAS * per_cta;
+    const int rpp = 32 / a.q_units;
+    const int passes = (a.hq + rpp - 1) / rpp + (a.dv ? 2 : 1) * ((a.hkv + rpp - 1) / rpp);
+    a.parts = 1;
+    int64_t least = INT64_MAX;
+    for (int parts = 1; parts <= std::min(passes, 32); ++parts) {
+        const int64_t cost = (a.num_tokens * parts + warps - 1) / warps *
+                             ((passes + parts - 1) / parts + 2);
+        if (cost < least) {
+            least = cost;
+            a.parts = parts;
+        }
+    }
+    const int64_t items = a.num_tokens * a.parts;
+    const dim3 grid(unsigned(std::min<int64_t>((items + per_cta - 1) / per_cta,
+                                               int64_t(sm_count()) * CTAS)));
+    return launch_pdl(interleaved ? rope_append_warp_kernel<true, E4, AHEAD, CTAS>
+                                  : rope_append_warp_kernel<false, E4, AHEAD, CTAS>,
+                      grid, dim3(kThreads), 0, stream, a);
+}
 
 template <bool E4>
 int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
+    const int64_t units16 =
+        (int64_t(a.hq) + a.hkv) * (a.dk / 16) + int64_t(a.hkv) * (a.dv / 16);
+    const int units = a.dk / 16;
+    if (a.dk % 64 == 0 && (units & (units - 1)) == 0 && units <= 32 &&
+        (a.dv == 0 || a.dv == a.dk) && a.rot % 16 == 0 && a.off % 16 == 0 && a.rot <= 128) {
+        a.q_units = units;
+        // (more tokens than twice the warps that are resident with two CTAs an SM)
+        return a.num_tokens > int64_t(sm_count()) * 32 ? launch_warp<E4, 4, 2>(a, interleaved, stream)
+                                                       : launch_warp<E4, 2, 3>(a, interleaved, stream);
+    }
+    if (a.dk % 16 == 0 && a.dv % 16 == 0 && a.dv <= a.dk && a.rot % 16 == 0 && a.off % 16 == 0) {
+        a.q_units = a.dk / 16;
+        a.q_magic = magic_of(a.q_units);
+        a.tok_magic = magic_of(a.hq + a.hkv + (a.dv ? a.hkv : 0));
+        // few tokens: one each, over as many CTAs as there are; more: groups of
+        // about kItemUnits units, as many tokens as the table holds at most
+        const int64_t ctas = int64_t(sm_count()) * kWideCtas;
+        int64_t group = std::min<int64_t>(
+            {int64_t(8), kItemUnits / units16, int64_t(kTable / (a.rot / 2)), a.num_tokens / ctas});
+        a.group = int32_t(std::max<int64_t>(1, group));
+        a.parts = a.group > 1 ? 1 : int32_t((units16 + kItemUnits - 1) / kItemUnits);
+        const int64_t items = (a.num_tokens + a.group - 1) / a.group * a.parts;
+        const dim3 grid(unsigned(std::min(items, ctas)));
+        return launch_pdl(interleaved ? rope_append_wide_kernel<true, E4>
+                                      : rope_append_wide_kernel<false, E4>,
+                          grid, dim3(kThreads), 0, stream, a);
+    }
     const bool vec = interleaved ? (a.rot % 8 == 0 && a.off % 8 == 0)
                                  : (a.rot % 16 == 0 && a.off % 8 == 0);
     a.q_units = !vec          ? a.rot / 2 + (a.dk - a.rot)
                 : interleaved ? a.dk / 8
                               : a.rot / 16 + (a.dk - a.rot) / 8;
-    a.v_units = std::max(1, a.dv / 8);
-    if (a.dv == 0) a.v_units = 0;
+    a.v_units = a.dv / 8;
     a.q_magic = magic_of(a.q_units);
     a.v_magic = magic_of(std::max(1, a.v_units));
     const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, int64_t(sm_count()) * 8)));
