@@ -63,6 +63,9 @@ constexpr int kSoftRegs = 200, kIssueRegs = 104;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
+// The sum of 64 probabilities past which a row's reference rises: far below
+// overflow of the sums over 2^30 keys and of products with values up to 2^70.
+constexpr float kMost = 1048576.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -79,10 +82,10 @@ struct Cfg {
     static constexpr uint32_t kOffQ = 1024;
     static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
     static constexpr uint32_t kSmem = 1024 + kOffRing + kStages * kStage;
-    // The running maximum may be exceeded by 2^kSlack; E4M3 probabilities are
+    // E4M3 probabilities: the reference may be exceeded by 2^kSlack, and they are
     // kept 2^kShift larger, so that their second term's smallest step (2^-9)
     // is 2^-16 of the row's largest (2^kShift .. 2^(kShift + kSlack) <= 448).
-    static constexpr float kSlack = E4 ? 1.f : 8.f;
+    static constexpr float kSlack = 1.f;
     static constexpr float kShift = E4 ? 7.f : 0.f;
     static constexpr uint32_t kIdS = E4 ? tc::idesc_e4m3_f32(kRows, kKeys, 0, 0)
                                         : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
@@ -98,10 +101,11 @@ constexpr int kBarQEmpty = 21;           // commit: the item's score products ar
 constexpr int kBarSFull = 22;            // + half: scores written (commit)
 constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64 keys written
                                          // (128 arrivals)
-constexpr int kBarPvDone = 28;           // + half: value product done (commit)
+constexpr int kBarPvDone = 28;           // + half: the item's value products done (commit)
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
 constexpr int kBarDrain = 32;
-constexpr uint32_t kOffSlot = 33 * 8;
+constexpr int kBarP0Done = 33;           // + half: value product of a tile's first 64 keys done
+constexpr uint32_t kOffSlot = 35 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -593,6 +597,11 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool al
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
+// Two of four maxima raised by four scores (two chains in flight).
+__device__ __forceinline__ void raise4(float (&mx)[4], const uint32_t *x) {
+    mx[0] = max3(mx[0], __uint_as_float(x[0]), __uint_as_float(x[1]));
+    mx[2] = max3(mx[2], __uint_as_float(x[2]), __uint_as_float(x[3]));
+}
 // Makes what follows depend on registers a TMEM load has filled (their values
 // are there only after the wait that precedes this).
 template <int N>
@@ -702,6 +711,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(bar(kBarPFull + h), 128);
             mbar_init(bar(kBarPFull + 2 + h), 128);
             mbar_init(bar(kBarPvDone + h), 1);
+            mbar_init(bar(kBarP0Done + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
         }
         *abort_flag = 0;
@@ -927,25 +937,29 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                             (i | kk) != 0);
                     }
                 };
-                // What block (h, i) waits for: the key tile of its scores, the value
-                // tile, O read out by the last item's epilogue, the probabilities.
-                auto each_wait = [&](int h, int i, auto &&one) -> bool {
-                    const int n = h ? r.nb : r.na;
-                    if (i + 1 < n) {
-                        const uint32_t pos = ord.k(h, i + 1);
-                        if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
-                            return false;
+                // What block (h, i) waits for: the probabilities (of `parts`: 2 when all,
+                // 1 when the first 64 keys' do), the key tile of its scores and the value
+                // tile (half B of a pair item reads A's), O read out by the last item's
+                // epilogue.
+                auto each_wait = [&](int h, int i, int parts, auto &&one) -> bool {
+                    if (i >= 0 && !one(bar(kBarPFull + 2 * (parts - 1) + h), np[h] & 1u))
+                        return false;
+                    if (r.split || h == 0) {
+                        if (i + 1 < (h ? r.nb : r.na)) {
+                            const uint32_t pos = ord.k(h, i + 1);
+                            if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
+                                return false;
+                        }
+                        if (i >= 0) {
+                            const uint32_t pos = ord.v(h, i);
+                            if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
+                                return false;
+                        }
                     }
-                    if (i >= 0) {
-                        const uint32_t pos = ord.v(h, i);
-                        if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
-                            return false;
-                        if (i == 0 && !one(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u)) return false;
-                        if (!one(bar(kBarPFull + h), np[h] & 1u)) return false;
-                    }
-                    return true;
+                    return i != 0 || one(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u);
                 };
                 bool ready = false;              // the next block's waits are known to be over
+                int32_t used = -1;               // a key tile's stage still to be released
                 // step -1: the first score products
                 for (int i = -1; i < r.na && ok; ++i)
 #pragma unroll
@@ -953,47 +967,51 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const int n = h ? r.nb : r.na;
                         const bool pv = i >= 0 && i < n, qk = i + 1 < n;
                         if (!ok || !(pv || qk)) continue;
-                        if (!ready && !(ok = each_wait(h, i, wait))) continue;
+                        if (!ready && !(ok = each_wait(h, i, 1, wait))) continue;
                         tc::fence_after_sync();
-                        const uint32_t ks = ord.k(h, i + 1) % C::kStages;
-                        const uint32_t vs = pv ? ord.v(h, i) % C::kStages : 0u;
                         if (pv) {
                             // the first 64 keys' product while the others' softmax goes on
+                            const uint32_t vs = ord.v(h, i) % C::kStages;
                             values(h, i, vs, 0);
-                            if (!(ok = wait(bar(kBarPFull + 2 + h), np[h] & 1u))) continue;
-                            tc::fence_after_sync();
+                            tc::commit(bar(kBarP0Done + h));
+                            if (!ready) {
+                                if (!(ok = wait(bar(kBarPFull + 2 + h), np[h] & 1u))) continue;
+                                tc::fence_after_sync();
+                            }
                             values(h, i, vs, 1);
-                        }
-                        // the next block that this item has: (1, i), else (0, i + 1)
-                        const bool b_next = h == 0 && i < r.nb && (i >= 0 || r.nb > 0);
-                        const int hn = b_next ? 1 : 0, in = b_next ? i : i + 1;
-                        auto probe = [&]() {
-                            return in < r.na && each_wait(hn, in, [&](uint32_t b, uint32_t ph) {
-                                       return mbar_try_wait(b, ph);
-                                   });
-                        };
-                        ready = false;
-                        if (qk) {
-                            scores(h, ks, 0);
-                            if (hn != h) ready = probe();
-                            scores(h, ks, 1);
-                        }
-                        // (the value product's end is told with the score product's: a
-                        // rescale needs it only after the next scores)
-                        if (qk) {
-                            tc::commit(bar(kBarSFull + h));
-                            if (r.split || h == 1) tc::commit(bar(kBarEmpty + ks));
-                            // the item's last score product frees its queries
-                            if (h == (r.split && r.nb < r.na ? 0 : 1) && i + 1 == r.na - 1)
-                                tc::commit(bar(kBarQEmpty));
-                        }
-                        if (pv) {
-                            tc::commit(bar(kBarPvDone + h));
+                            // (commits cost the thread some 75 cycles each: what need not
+                            // be told at once is told here, with products queued)
                             if (r.split || h == 1) tc::commit(bar(kBarEmpty + vs));
                             if (i == 0) ++nitem[h];
                             ++np[h];
                         }
+                        if (used >= 0) {
+                            tc::commit(bar(kBarEmpty + used));
+                            used = -1;
+                        }
+                        ready = false;
+                        if (qk) {
+                            const uint32_t ks = ord.k(h, i + 1) % C::kStages;
+                            scores(h, ks, 0);
+                            // the next block, if the other half's: (1, i), else (0, i + 1)
+                            const bool to_b = h == 0 && i < r.nb && (i >= 0 || r.nb > 0);
+                            const int in = to_b ? i : i + 1;
+                            if (to_b || (h == 1 && in < r.na))
+                                ready = each_wait(h ^ 1, in, 2, [&](uint32_t b, uint32_t ph) {
+                                    return mbar_try_wait(b, ph);
+                                });
+                            scores(h, ks, 1);
+                            tc::commit(bar(kBarSFull + h));
+                            if (r.split || h == 1) used = int32_t(ks);
+                            // the item's last score product frees its queries
+                            if (h == (r.split && r.nb < r.na ? 0 : 1) && i + 1 == r.na - 1)
+                                tc::commit(bar(kBarQEmpty));
+                        } else {
+                            // (the other value products' end is told with the next scores')
+                            tc::commit(bar(kBarPvDone + h));
+                        }
                     }
+                if (used >= 0) tc::commit(bar(kBarEmpty + used));
                 ring += ord.total(r.na);
                 ++items_done;
             }
@@ -1012,7 +1030,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const uint32_t to = tmem + kColO + 128 * h + lanes;
         const int tok_row = row / G, head_row = row - tok_row * G;
         const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
-        uint32_t ring = 0, np = 0, items_done = 0;
+        uint32_t ring = 0, np = 0, nitem = 0, items_done = 0;
         bool ok = true;
         for (int it = 0; it < num_items; ++it) {
             const Item r = read_item(it);
@@ -1020,7 +1038,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int n = h ? r.nb : r.na;
             const int tok0 = r.split ? 0 : h * tpt;      // the half's first token
             float sc = a.scale * kLog2e;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;            // reference, sum against it
+            if (tok_row >= tpt || tok0 + tok_row >= r.ntok) sc = m = 0.f;    // no row: any bits
             if constexpr (E4) {
                 sc *= a.k_scale[g];
                 if (r.na > 0) {
@@ -1093,25 +1112,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 ok = ok && pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
-                uint32_t s[kKeys], t0[32], t1[16];
-#pragma unroll
-                for (int j = 0; j < kKeys; j += 32) tc::ld32(ts + j, s + j);
-                tc::wait_ld();
-#pragma unroll
-                for (int j = 0; j < kKeys; j += 32) pin<32>(s + j);
-                // ---- keys this row does not see
-                if (!clear) {
-                    const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-#pragma unroll
-                    for (int w = 0; w < kKeys / 32; ++w) {
-                        uint32_t see = pos >= 0 ? below(pos - k0 + 1, w) : 0u;
-                        if (a.window > 0)
-                            see &= ~below(pos - k0 - a.window + 1, w) | below(a.sinks - k0, w);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((see >> j) & 1u)) s[32 * w + j] = 0xff800000u;
-                    }
-                }
                 // ---- value rows no row of the item sees: zeroed, thread = key
                 if (!clear) {
                     const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
@@ -1137,60 +1137,89 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     __syncwarp();
                 }
                 // ---- probabilities and their terms over S's columns, 64 keys at a
-                // time.  The first 64 are taken with the maximum so far while the
-                // tile's own maximum is found (its instructions fill the gaps of the
-                // exponentials); only if some row's then rises are they taken again.
-                float mt = -INFINITY, neg;
-                float sum[4];
-                for (bool again = false;; again = true) {
-                    neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
-                    sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    exponentials<E4>(s, sc, neg, sum, t0, t1, [&](int j) {
+                // time, against the row's reference m.  m need not be the maximum:
+                // numbers with 8 bits of exponent hold 2^(score - m) as exactly
+                // whatever m is, short of overflow.  So bf16 terms are taken against
+                // the first maximum, and the reference rises only when the sum of a
+                // row's 64 probabilities passes kMost (E4M3 terms: when a score
+                // passes it by kSlack); they are then taken again.  A loop, not
+                // unrolled: the code of one part stays in the instruction cache beside
+                // the issuing thread's.
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    uint32_t x[64], t0[32], t1[16];
+                    tc::ld32(ts + 64 * part, x);
+                    tc::ld32(ts + 64 * part + 32, x + 32);
+                    tc::wait_ld();
+                    pin<32>(x);
+                    pin<32>(x + 32);
+                    if (!clear) {
+                        // keys this row does not see
+                        const int32_t k0 =
+                            (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + 64 * part;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            mx[e] = max3(mx[e], __uint_as_float(s[j + e]),
-                                         __uint_as_float(s[64 + j + e]));
-                    });
-                    if (again) break;
-                    mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    if (!__any_sync(0xffffffffu, i == 0 || (mt - m) * sc > C::kSlack)) break;
-                    const float mn = fmaxf(m, mt);
-                    if (i > 0) {
-                        // rescale, once the last value product into these rows is done
-                        ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status,
-                                             abort_flag);
-                        __syncwarp();
-                        tc::fence_after_sync();
-                        const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
-                        l *= f;
+                        for (int w = 0; w < 2; ++w) {
+                            uint32_t see = pos >= 0 ? below(pos - k0 + 1, w) : 0u;
+                            if (a.window > 0)
+                                see &= ~below(pos - k0 - a.window + 1, w) | below(a.sinks - k0, w);
 #pragma unroll
-                        for (int j = 0; j < D; j += 16) {
-                            uint32_t o[16];
-                            tc::ld16(to + j, o);
-                            tc::wait_ld();
-                            pin<16>(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::st16(to + j, o);
+                            for (int j = 0; j < 32; ++j)
+                                if (!((see >> j) & 1u)) x[32 * w + j] = 0xff800000u;
                         }
                     }
-                    m = mn;
+                    float total;
+                    for (bool again = false;; again = true) {
+                        const float neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        exponentials<E4>(x, sc, neg, sum, t0, t1, [&](int j) {
+                            if constexpr (E4) raise4(mx, x + j);
+                        });
+                        total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        const bool rise =
+                            E4 ? (fmaxf(mx[0], mx[2]) - m) * sc > C::kSlack
+                               : total > kMost || m == -INFINITY;
+                        if (!__any_sync(0xffffffffu, rise && !again)) break;
+                        if constexpr (!E4) {
+#pragma unroll
+                            for (int j = 0; j < 64; j += 4) raise4(mx, x + j);
+                        }
+                        const float mn = fmaxf(m, fmaxf(mx[0], mx[2]));
+                        const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
+                        if (part || i > 0) {
+                            // rescale.  These scores were told after the last tile's value
+                            // product; that of this tile's first keys has to be waited for.
+                            ok = ok && (part == 0 || pipe_wait(bar(kBarP0Done + h), np & 1u,
+                                                               a.status, abort_flag));
+                            __syncwarp();
+                            tc::fence_after_sync();
+#pragma unroll
+                            for (int j = 0; j < D; j += 16) {
+                                uint32_t o[16];
+                                tc::ld16(to + j, o);
+                                tc::wait_ld();
+                                pin<16>(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::st16(to + j, o);
+                            }
+                        }
+                        l *= f;
+                        m = mn;
+                    }
+                    __syncwarp();
+                    store_terms<E4>(ts, part, t0, t1);
+                    mbar_arrive(bar(kBarPFull + 2 * part + h));
+                    l += total;
                 }
-                __syncwarp();
-                store_terms<E4>(ts, 0, t0, t1);
-                mbar_arrive(bar(kBarPFull + h));
-                exponentials<E4>(s + 64, sc, neg, sum, t0, t1, [](int) {});
-                store_terms<E4>(ts, 1, t0, t1);
-                mbar_arrive(bar(kBarPFull + 2 + h));
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 ++np;
             }
 
             // ---- epilogue
             if (n > 0) {
-                ok = ok && pipe_wait(bar(kBarPvDone + h), (np - 1) & 1u, a.status, abort_flag);
+                ok = ok && pipe_wait(bar(kBarPvDone + h), nitem & 1u, a.status, abort_flag);
+                ++nitem;
                 __syncwarp();
                 tc::fence_after_sync();
             }
