@@ -873,147 +873,148 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // ---------------------------------------------------------- MMA issuer
         // One thread issues blocks of [value product of step i, score product of
         // step i + 1], half A's and half B's in turn, so that one half's softmax
-        // runs under the other's products.  The thread is held up until its last
-        // product has been taken up; what it then does before the next one
-        // (commits, waits of some 50 cycles even when satisfied) would leave the
-        // tensor cores idle.  So the next block's waits are tried before the last
-        // four products of a block are issued, and the commits follow the block.
+        // runs under the other's products.  What the thread does between two
+        // products leaves the tensor cores idle, so it does little: ring positions
+        // are counted, not divided, and nothing is kept that spills.
         if (tc::elect_one()) {
-            uint32_t ring = 0, items_done = 0;
-            uint32_t np[2] = {0, 0};             // value products issued
-            uint32_t nitem[2] = {0, 0};          // items begun, by half
+            uint32_t slot = 0, lap = 0;          // ring position: stage and lap parity
+            uint32_t item_bit = 0;               // items done, mod 2
+            uint32_t np[2] = {0, 0};             // tiles whose probabilities were taken, mod 2
+            uint32_t nitem[2] = {0, 0};          // items begun, by half, mod 2
             bool ok = true;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return pipe_wait(b, parity, a.status, abort_flag);
             };
+            // the ring entry `off` positions on: its stage, waited for
+            auto entry = [&](uint32_t off, uint32_t &stage) {
+                stage = slot + off;
+                uint32_t l = lap;
+                if (stage >= C::kStages) {
+                    stage -= C::kStages;
+                    l ^= 1u;
+                }
+                return wait(bar(kBarFull) + 8u * stage, l);
+            };
+            auto advance = [&](uint32_t n) {
+                slot += n;
+                if (slot >= C::kStages) {
+                    slot -= C::kStages;
+                    lap ^= 1u;
+                }
+            };
+            auto scores = [&](int h, bool second_q, uint32_t stage) {
+                const uint32_t ds = tmem + kKeys * h;
+                const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
+                const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
+                const uint64_t q =
+                    tc::smem_desc(sb + C::kOffQ + (second_q ? C::kQTile : 0u), 16, 1024);
+                if constexpr (E4) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_e4m3(ds, q + ((t * C::kHalfTile + 32 * kk) >> 4),
+                                         kd + ((32 * kk) >> 4), C::kIdS, (t | kk) != 0);
+                } else {
+#pragma unroll
+                    for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc::mma_bf16(ds, q + ((half * C::kHalfTile + 32 * kk) >> 4),
+                                         kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
+                                         (half | kk) != 0);
+                }
+            };
+            // part 0 or 1 (64 keys) of a value product; `first`: O begins
+            auto values = [&](int h, bool first, uint32_t stage, int part) {
+                const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
+                const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
+                const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
+                                                        : tc::smem_desc(vb, 16384, 1024);
+                if constexpr (E4) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
+                            tc::mma_e4m3_ts(dO, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
+                                            C::kIdO, part || t || (kk & 1) || !first);
+                } else {
+#pragma unroll
+                    for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                        tc::mma_bf16_ts(dO, p + 8 * kk,
+                                        vd + (((D == 128 ? 4096 : 2048) * kk) >> 4), C::kIdO,
+                                        kk || !first);
+                }
+            };
             for (int it = 0; it < num_items && ok; ++it) {
                 const Item r = read_item(it);
                 if (r.na == 0) continue;
-                const Order ord{ring, r.split, r.nb};
-                if (!(ok = wait(bar(kBarQFull), items_done & 1u))) break;
-                const uint64_t qd = tc::smem_desc(sb + C::kOffQ, 16, 1024);
-                // part 0 or 1 of the products of a tile's scores
-                auto scores = [&](int h, uint32_t stage, int part) {
-                    const uint32_t ds = tmem + kKeys * h;
-                    const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
-                    const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
-                    const uint64_t q = qd + (r.split || h == 0 ? 0 : C::kQTile >> 4);
-                    if constexpr (E4) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_e4m3(ds, q + ((part * C::kHalfTile + 32 * kk) >> 4),
-                                         kd + ((32 * kk) >> 4), C::kIdS, (part | kk) != 0);
-                    } else if constexpr (D == 128) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma_bf16(ds, q + ((part * C::kHalfTile + 32 * kk) >> 4),
-                                         kd + ((part * 1024 + 32 * kk) >> 4), C::kIdS,
-                                         (part | kk) != 0);
-                    } else {
-#pragma unroll
-                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                            tc::mma_bf16(ds, q + ((32 * kk) >> 4), kd + ((32 * kk) >> 4), C::kIdS,
-                                         kk != 0);
-                    }
-                };
-                // part 0 or 1 (64 keys) of a value product
-                auto values = [&](int h, int i, uint32_t stage, int part) {
-                    const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
-                    const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
-                    const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
-                                                            : tc::smem_desc(vb, 16384, 1024);
-                    if constexpr (E4) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t)
-#pragma unroll
-                            for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                                tc::mma_e4m3_ts(dO, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
-                                                C::kIdO, (i | part | t | (kk & 1)) != 0);
-                    } else {
-#pragma unroll
-                        for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
-                            tc::mma_bf16_ts(dO, p + 8 * kk,
-                                            vd + (((D == 128 ? 4096 : 2048) * kk) >> 4), C::kIdO,
-                                            (i | kk) != 0);
-                    }
-                };
-                // What block (h, i) waits for: the probabilities (of `parts`: 2 when all,
-                // 1 when the first 64 keys' do), the key tile of its scores and the value
-                // tile (half B of a pair item reads A's), O read out by the last item's
-                // epilogue.
-                auto each_wait = [&](int h, int i, int parts, auto &&one) -> bool {
-                    if (i >= 0 && !one(bar(kBarPFull + 2 * (parts - 1) + h), np[h] & 1u))
-                        return false;
-                    if (r.split || h == 0) {
-                        if (i + 1 < (h ? r.nb : r.na)) {
-                            const uint32_t pos = ord.k(h, i + 1);
-                            if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
-                                return false;
-                        }
-                        if (i >= 0) {
-                            const uint32_t pos = ord.v(h, i);
-                            if (!one(bar(kBarFull + pos % C::kStages), (pos / C::kStages) & 1u))
-                                return false;
-                        }
-                    }
-                    return i != 0 || one(bar(kBarOEmpty + h), (nitem[h] & 1u) ^ 1u);
-                };
-                bool ready = false;              // the next block's waits are known to be over
-                int32_t used = -1;               // a key tile's stage still to be released
-                // step -1: the first score products
-                for (int i = -1; i < r.na && ok; ++i)
+                const int na = r.na, nb = r.nb;
+                const bool split = r.split;
+                if (!(ok = wait(bar(kBarQFull), item_bit))) break;
+                item_bit ^= 1u;
+                uint32_t st;
+                // ---- the first scores
+                if (!(ok = entry(0, st))) break;
+                tc::fence_after_sync();
+                scores(0, false, st);
+                tc::commit(bar(kBarSFull));
+                if (split) tc::commit(bar(kBarEmpty) + 8u * st);
+                if (nb > 0) {
+                    if (split && !(ok = entry(1, st))) break;
+                    tc::fence_after_sync();
+                    scores(1, !split, st);
+                    tc::commit(bar(kBarSFull + 1));
+                    tc::commit(bar(kBarEmpty) + 8u * st);
+                }
+                if (na == 1) tc::commit(bar(kBarQEmpty));
+                // entries of step 0 from here: pair items V0 K1, split items VA0 VB0 KA1 KB1
+                advance(split && nb > 0 ? 2 : 1);
+                for (int i = 0; i < na && ok; ++i) {
+                    const bool more = i + 1 < na;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int n = h ? r.nb : r.na;
-                        const bool pv = i >= 0 && i < n, qk = i + 1 < n;
-                        if (!ok || !(pv || qk)) continue;
-                        if (!ready && !(ok = each_wait(h, i, 1, wait))) continue;
+                        if (h && i >= nb) continue;
+                        const bool scores_too = h ? i + 1 < nb : more;
+                        uint32_t vs = 0, ks = 0;
+                        // (half B of a pair item: its tiles are A's, waited for there)
+                        if (h == 0 || split) {
+                            const bool both = split && i < nb;
+                            ok = entry(both ? h : 0, vs);
+                            if (ok && scores_too) ok = entry(both ? 2 + h : 1, ks);
+                        } else {
+                            vs = slot;
+                            ks = slot + 1 == C::kStages ? 0 : slot + 1;
+                        }
+                        if (ok && i == 0) {
+                            ok = wait(bar(kBarOEmpty + h), nitem[h] ^ 1u);
+                            nitem[h] ^= 1u;
+                        }
+                        ok = ok && wait(bar(kBarPFull + h), np[h]);
+                        if (!ok) break;
                         tc::fence_after_sync();
-                        if (pv) {
-                            // the first 64 keys' product while the others' softmax goes on
-                            const uint32_t vs = ord.v(h, i) % C::kStages;
-                            values(h, i, vs, 0);
-                            tc::commit(bar(kBarP0Done + h));
-                            if (!ready) {
-                                if (!(ok = wait(bar(kBarPFull + 2 + h), np[h] & 1u))) continue;
-                                tc::fence_after_sync();
-                            }
-                            values(h, i, vs, 1);
-                            // (commits cost the thread some 75 cycles each: what need not
-                            // be told at once is told here, with products queued)
-                            if (r.split || h == 1) tc::commit(bar(kBarEmpty + vs));
-                            if (i == 0) ++nitem[h];
-                            ++np[h];
-                        }
-                        if (used >= 0) {
-                            tc::commit(bar(kBarEmpty + used));
-                            used = -1;
-                        }
-                        ready = false;
-                        if (qk) {
-                            const uint32_t ks = ord.k(h, i + 1) % C::kStages;
-                            scores(h, ks, 0);
-                            // the next block, if the other half's: (1, i), else (0, i + 1)
-                            const bool to_b = h == 0 && i < r.nb && (i >= 0 || r.nb > 0);
-                            const int in = to_b ? i : i + 1;
-                            if (to_b || (h == 1 && in < r.na))
-                                ready = each_wait(h ^ 1, in, 2, [&](uint32_t b, uint32_t ph) {
-                                    return mbar_try_wait(b, ph);
-                                });
-                            scores(h, ks, 1);
+                        // the first 64 keys' product while the others' softmax goes on
+                        values(h, i == 0, vs, 0);
+                        tc::commit(bar(kBarP0Done + h));
+                        if (!(ok = wait(bar(kBarPFull + 2 + h), np[h]))) break;
+                        tc::fence_after_sync();
+                        values(h, i == 0, vs, 1);
+                        np[h] ^= 1u;
+                        if (scores_too) {
+                            scores(h, h && !split, ks);
                             tc::commit(bar(kBarSFull + h));
-                            if (r.split || h == 1) used = int32_t(ks);
-                            // the item's last score product frees its queries
-                            if (h == (r.split && r.nb < r.na ? 0 : 1) && i + 1 == r.na - 1)
-                                tc::commit(bar(kBarQEmpty));
+                            if (split || h) tc::commit(bar(kBarEmpty) + 8u * ks);
                         } else {
                             // (the other value products' end is told with the next scores')
                             tc::commit(bar(kBarPvDone + h));
                         }
+                        if (split || h) tc::commit(bar(kBarEmpty) + 8u * vs);
                     }
-                if (used >= 0) tc::commit(bar(kBarEmpty + used));
-                ring += ord.total(r.na);
-                ++items_done;
+                    // the item's last score product frees its queries
+                    if (i + 2 == na) tc::commit(bar(kBarQEmpty));
+                    advance(split ? (i < nb ? 2 : 1) + (more ? 1 : 0) + (i + 1 < nb ? 1 : 0)
+                                  : 1 + (more ? 1 : 0));
+                }
             }
             tc::commit(bar(kBarDrain));
             mbar_wait(bar(kBarDrain), 0, a.status);
