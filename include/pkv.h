@@ -567,7 +567,9 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  * fp32 (or NULL: not wanted).  scale > 0 and finite; window >= 0 (0: none);
  * sink_tokens >= 0 (without a window it changes nothing).  Probabilities are
  * rounded to bf16 for the value product (E4M3 caches: to two E4M3 terms, as
- * the query is), sums and statistics are fp32, out is rounded once.
+ * the query is: 2^-8 relative, and 2^-17 of the row's largest); sums and
+ * statistics are fp32, out is rounded once.  Values of magnitude 2^80 and
+ * above may overflow the sums.
  *  - Rows of q outside [cu_q_lens[0], cu_q_lens[batch]) are padding: their out
  *    and lse are left as they were.
  *  - Table entries of blocks that no new token sees (between the sinks and

@@ -2,6 +2,7 @@
 // tokens: argument checks and kernel choice.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "pkv.h"
@@ -84,8 +85,11 @@ int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64
     a.max_blocks = max_blocks;
     a.seq_lens = seq_lens;
     a.scale = scale;
-    a.window = window;
-    a.sinks = sink_tokens;
+    // no position reaches the table's capacity: a wider window masks nothing, more
+    // sinks add none, and the kernels' differences of positions stay in range
+    const int64_t capacity = int64_t(max_blocks) * c->block_size;
+    a.window = window >= capacity ? 0 : window;
+    a.sinks = int32_t(std::min<int64_t>(sink_tokens, capacity));
     a.out = out;
     a.lse = lse;
     a.stream = stream;

@@ -1185,7 +1185,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
                             for (int j = 0; j < 64; j += 4) raise4(mx, x + j);
                         }
-                        const float mn = fmaxf(m, fmaxf(mx[0], mx[2]));
+                        // (a row that need not rise keeps m and, to the bit, its terms:
+                        // what a row gives does not depend on its neighbours)
+                        const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[2])) : m;
                         const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
                         if (part || i > 0) {
                             // rescale.  These scores were told after the last tile's value

@@ -84,15 +84,17 @@ def values(pool, scale):
 
 
 def reference(case):
-    """out, lse, and the bounds' ingredients: sum_j p_j |v_j| (absv) and the
-    largest scale * sum_d |q_d k_d| of a row (mag).  Rows of padding are NaN."""
+    """out, lse, and the bounds' ingredients: sum_j p_j |v_j| (absv), the largest
+    scale * sum_d |q_d k_d| of a row (mag), sum_j |v_j| over the sum of the
+    probabilities taken against the row's largest (low), and the largest
+    scale * max_d |q_d| * sum_d |k_d| (qlow).  Rows of padding are NaN."""
     T, hq, dk = case.q.shape
     hkv, bs = case.k_pool.shape[1], case.k_pool.shape[2]
     kp = values(case.k_pool, case.k_scale)
     vp = kp[..., :case.dv] if case.v_pool is None else values(case.v_pool, case.v_scale)
     out = torch.full((T, hq, case.dv), math.nan, dtype=torch.float64)
     absv, lse = out.clone(), torch.full((T, hq), math.nan, dtype=torch.float64)
-    mag = lse.clone()
+    mag, qlow, low = lse.clone(), lse.clone(), out.clone()
     for b in range(case.lens.numel()):
         lo, hi = int(case.cu[b]), int(case.cu[b + 1])
         n, L = hi - lo, int(case.lens[b])
@@ -120,9 +122,12 @@ def reference(case):
             out[lo:hi, h] = pr @ v
             absv[lo:hi, h] = pr @ v.abs()
             lse[lo:hi, h] = (m + l.log())[:, 0]
+            low[lo:hi, h] = seen.double() @ v.abs() / l.clamp(min=1)
             a = (qh.abs() @ k.abs().T * case.scale).masked_fill(~seen, 0)
             mag[lo:hi, h] = a.amax(-1) if L else 0
-    return out, lse, absv, mag
+            a = (qh.abs().amax(-1)[:, None] * k.abs().sum(-1) * case.scale).masked_fill(~seen, 0)
+            qlow[lo:hi, h] = a.amax(-1) if L else 0
+    return out, lse, absv, mag, low, qlow
 
 
 def run(pkv, case, dev="cuda", flags=0, out=None, lse=None, workspace=None, stream=None):
@@ -145,11 +150,14 @@ def check(case, out, lse):
     product (bf16; two E4M3 terms of 2^-4 each), which moves out by at most
     2^-8 sum p |v|; the result is rounded by at most 2^-8 of itself; fp32
     sums, and probabilities from scores that are off as below, are covered by
-    the score term.  Probabilities under 2^-18 of the largest may vanish from
-    the E4M3 terms: at most 2^-18 |v| each, over at most 600 keys here.
+    the score term.  The second E4M3 term of a probability steps by 2^-9 where
+    the row's largest is 2^7 or more, so it is off by up to 2^-17 of the largest
+    however small the probability is: 2^-17 sum |v|.
     lse, and each score: dk products summed in fp32, (dk + 2) 2^-24 of the sum
-    of their magnitudes; the sum of probabilities 2^-17 relative."""
-    ref, ref_lse, absv, mag = reference(case)
+    of their magnitudes; the sum of probabilities 2^-17 relative.  E4M3: the
+    second term of a query element steps by 2^-9 where the row's largest is 2^7
+    or more, an element is off by up to 2^-17 of that."""
+    ref, ref_lse, absv, mag, low, qlow = reference(case)
     out, lse = out.cpu().double(), lse.cpu().double()
     real = ~torch.isnan(ref_lse)
     empty = ref_lse == -math.inf
@@ -158,9 +166,11 @@ def check(case, out, lse):
     rows = real & ~empty
     dk = case.q.shape[2]
     score = (dk + 2) * 2.0 ** -24 * mag[rows] + 2.0 ** -17
+    if case.k_scale is not None:
+        score = score + 2.0 ** -17 * qlow[rows]
     d_lse = (lse[rows] - ref_lse[rows]).abs()
     assert torch.all(d_lse <= score), float((d_lse - score).max())
-    vanish = 600 * 2.0 ** -18 * 4 if case.k_scale is not None else 0.0
+    vanish = 2.0 ** -17 * low[rows] if case.k_scale is not None else 0.0
     tol = (2.0 ** -8 + 2 * score[:, None]) * absv[rows] + 2.0 ** -8 * ref[rows].abs() + vanish
     d = (out[rows] - ref[rows]).abs()
     assert torch.all(d <= tol), float((d - tol).max())

@@ -289,3 +289,45 @@ def test_a_served_sequence(pkv, e4m3):
                                 ks.cpu() if e4m3 else None, vs.cpu() if e4m3 else None)
         want = _chunk.reference(case)
         _chunk.check(case, torch.cat(outs[b]), want[1])
+
+
+# enough tokens that every form works through several tokens and parts a thread
+@pytest.mark.parametrize("T,shape,rot,off,interleaved", [
+    (6000, (8, 2, 128, 128, 16), 128, 0, False), (5003, (8, 2, 64, 64, 16), 32, 0, True),
+    (5001, (4, 2, 256, 256, 16), 64, 64, False), (9000, (5, 1, 128, 64, 8), 64, 0, False),
+    (20000, (3, 1, 64, 128, 8), 16, 8, True), (1300, (64, 2, 128, 128, 16), 128, 0, True),
+    (5000, (2, 1, 72, 40, 5), 24, 3, False), (5500, (2, 2, 512, 512, 16), 128, 128, True)])
+def test_many_tokens(pkv, T, shape, rot, off, interleaved):
+    hq, hkv, dk, dv, bs = shape
+    t = make(T, T, hq, hkv, dk, dv, bs)
+    inv = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    for fp32 in (False, True):
+        got = call(pkv, t, inv, rotary_offset=off, interleaved=interleaved,
+                   q_dtype=torch.float32 if fp32 else torch.bfloat16)
+        check(t, inv, got, off, interleaved, fp32=fp32)
+
+
+@pytest.mark.parametrize("T,shape,rot,off", [(6000, (4, 2, 128, 128, 16), 128, 0),
+                                             (7000, (4, 2, 128, 64, 16), 64, 64),
+                                             (5100, (3, 1, 72, 40, 16), 8, 0)])
+def test_many_tokens_e4m3(pkv, T, shape, rot, off):
+    hq, hkv, dk, dv, bs = shape
+    t = make(T, T, hq, hkv, dk, dv, bs, e4m3=True)
+    inv = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    check(t, inv, call(pkv, t, inv, rotary_offset=off), off)
+
+
+@pytest.mark.parametrize("T,interleaved", [(700, True), (2500, False)])
+def test_many_latent_rows(pkv, T, interleaved):
+    t = make(T, T, 32, 1, 576, None, 64)
+    inv = 10000.0 ** (-torch.arange(0, 64, 2, dtype=torch.float64) / 64)
+    check(t, inv, call(pkv, t, inv, latent_dv=512, rotary_offset=512, interleaved=interleaved),
+          512, interleaved)
+
+
+def test_a_stream_of_ones_own(pkv):
+    t = make(9, 40, 8, 2, 128, 128, 16)
+    inv = pkv.rope_frequencies(128)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    check(t, inv.cpu(), call(pkv, t, inv, stream=s))
