@@ -61,11 +61,9 @@ constexpr int kThreads = 384;             // three warp groups
 // groups then take 200, the issuing group keeps 104 (256 x 200 + 128 x 104).
 constexpr int kSoftRegs = 200, kIssueRegs = 104;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kWidenThreads = 64;        // warps 10 and 11 (E4M3)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
-// The sum of 64 probabilities past which a row's reference rises: far below
-// overflow of the sums over 2^30 keys and of products with values up to 2^70.
-constexpr float kMost = 1048576.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -74,28 +72,30 @@ struct Cfg {
     static_assert(D == 64 || D == 128, "head dims of one or two 128-byte column blocks");
     static_assert(!E4 || D == 128, "E4M3 rows fill a 128-byte swizzle row");
     static constexpr int kElem = E4 ? 1 : 2;
-    static constexpr int kTerms = E4 ? 2 : 1;                       // of Q and of P
     static constexpr uint32_t kHalfTile = kRows * 128;              // [128 rows][128 B]
     static constexpr uint32_t kQTile = E4 ? 2 * kHalfTile : kRows * D * 2;
     static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
-    static constexpr int kStages = kStage == 32768 ? 5 : 10;
+    static constexpr int kStages = E4 ? 6 : kStage == 32768 ? 5 : 10;
+    static constexpr uint32_t kWide = kKeys * D * 2;                // a V tile in 16 bits
     static constexpr uint32_t kOffQ = 1024;
     static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
-    static constexpr uint32_t kSmem = 1024 + kOffRing + kStages * kStage;
-    // E4M3 probabilities: the reference may be exceeded by 2^kSlack, and they are
-    // kept 2^kShift larger, so that their second term's smallest step (2^-9)
-    // is 2^-16 of the row's largest (2^kShift .. 2^(kShift + kSlack) <= 448).
-    static constexpr float kSlack = 1.f;
-    static constexpr float kShift = E4 ? 7.f : 0.f;
+    static constexpr uint32_t kOffWide = kOffRing + kStages * kStage;
+    static constexpr uint32_t kSmem = 1024 + kOffWide + (E4 ? 2 * kWide : 0);
+    // The sum of 64 probabilities past which a row's reference rises.  bf16: far
+    // below overflow of the sums over 2^30 keys and of products with values up to
+    // 2^80.  fp16: none of them reaches 65,504.
+    static constexpr float kMost = E4 ? 16384.f : 1048576.f;
     static constexpr uint32_t kIdS = E4 ? tc::idesc_e4m3_f32(kRows, kKeys, 0, 0)
                                         : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
-    static constexpr uint32_t kIdO = E4 ? tc::idesc_e4m3_f32(kRows, D, 0, 1)
+    static constexpr uint32_t kIdO = E4 ? tc::idesc_f16_f32(kRows, D, 0, 1)
                                         : tc::idesc_bf16_f32(kRows, D, 0, 1);
 };
 
 // mbarrier slots
 constexpr int kBarFull = 0;              // + stage (at most 10)
-constexpr int kBarEmpty = 10;            // + stage
+constexpr int kBarEmpty = 10;            // + stage.  E4M3: two arrivals, of a value tile the
+                                         // widening warps', of a key tile the producer's
+                                         // own and the commit
 constexpr int kBarQFull = 20;
 constexpr int kBarQEmpty = 21;           // commit: the item's score products are done
 constexpr int kBarSFull = 22;            // + half: scores written (commit)
@@ -105,7 +105,9 @@ constexpr int kBarPvDone = 28;           // + half: the item's value products do
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
 constexpr int kBarDrain = 32;
 constexpr int kBarP0Done = 33;           // + half: value product of a tile's first 64 keys done
-constexpr uint32_t kOffSlot = 35 * 8;
+constexpr int kBarWideFull = 35;         // + buffer: values widened (kWidenThreads arrivals)
+constexpr int kBarWideEmpty = 37;        // + buffer: their value products done (commit)
+constexpr uint32_t kOffSlot = 39 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -626,12 +628,11 @@ __device__ __forceinline__ void e4m3_terms(float p0, float p1, float p2, float p
         : "=&r"(t0), "=r"(t1) : "r"(a), "r"(b));
 }
 
-// 2^(s sc + neg) of 64 scores: their sums onto `sum`, their terms in t0 (t1).
-// extra(j) is called once for each four scores j .. j + 3.
-template <bool E4, typename F>
+// p = 2^(s sc + neg) of 64 scores: their sums onto `sum`, the pairs rounded to
+// bf16 (E4M3 caches: fp16) in t.
+template <bool E4>
 __device__ __forceinline__ void exponentials(const uint32_t *s, float sc, float neg,
-                                             float (&sum)[4], uint32_t (&t0)[32],
-                                             uint32_t (&t1)[16], F extra) {
+                                             float (&sum)[4], uint32_t (&t)[32]) {
     constexpr int kLag = 2;              // groups between an exponential and its use
     float p[4 * (kLag + 1)];
 #pragma unroll
@@ -644,39 +645,16 @@ __device__ __forceinline__ void exponentials(const uint32_t *s, float sc, float 
                  neg, neg);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = ex2_approx(x[e]);
-            extra(4 * g);
         }
         if (g >= kLag) {
             const int d = g - kLag;
             const float *x = p + 4 * (d % (kLag + 1));
             add2(sum[0], sum[1], x[0], x[1]);
             add2(sum[2], sum[3], x[2], x[3]);
-            if constexpr (E4) {
-                e4m3_terms(x[0], x[1], x[2], x[3], t0[d], t1[d]);
-            } else {
-                t0[2 * d] = pack_bf16x2(x[0], x[1]);
-                t0[2 * d + 1] = pack_bf16x2(x[2], x[3]);
-            }
+            t[2 * d] = E4 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
+            t[2 * d + 1] = E4 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
         }
     }
-}
-
-// The terms of 64 keys (part 0 or 1 of the tile) to their columns at `ts`, ready
-// for the value product.
-template <bool E4>
-__device__ __forceinline__ void store_terms(uint32_t ts, int part, const uint32_t (&t0)[32],
-                                            const uint32_t (&t1)[16]) {
-    if constexpr (E4) {
-        uint32_t u0[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) u0[j] = t0[j];
-        tc::st16(ts + 16 * part, u0);
-        tc::st16(ts + 32 + 16 * part, t1);
-    } else {
-        tc::st32(ts + 32 * part, t0);
-    }
-    tc::wait_st();
-    tc::fence_before_sync();
 }
 
 template <int D, bool E4>
@@ -701,7 +679,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), 1);
+            mbar_init(bar(kBarEmpty + s), E4 ? 2 : 1);
         }
         mbar_init(bar(kBarQFull), E4 ? 256 : 1);
         mbar_init(bar(kBarQEmpty), 1);
@@ -713,6 +691,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(bar(kBarPvDone + h), 1);
             mbar_init(bar(kBarP0Done + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
+            mbar_init(bar(kBarWideFull + h), kWidenThreads);
+            mbar_init(bar(kBarWideEmpty + h), 1);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -795,9 +775,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                                        a.status, abort_flag)))
                     return false;
                 const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
-                if (lane == 0)
+                if (lane == 0) {
+                    if (E4 && map == &tmap_k) mbar_arrive(bar(kBarEmpty + stage));
                     mbar_arrive_expect_tx(bar(kBarFull + stage),
                                           __popc(live) * uint32_t(box) * D * C::kElem);
+                }
                 armed |= 1u << stage;
                 armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                 __syncwarp();
@@ -881,6 +863,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             uint32_t item_bit = 0;               // items done, mod 2
             uint32_t np[2] = {0, 0};             // tiles whose probabilities were taken, mod 2
             uint32_t nitem[2] = {0, 0};          // items begun, by half, mod 2
+            uint32_t wide = 0, wide_lap = 0;     // next buffer of widened values (E4M3)
             bool ok = true;
             auto wait = [&](uint32_t b, uint32_t parity) {
                 return pipe_wait(b, parity, a.status, abort_flag);
@@ -928,23 +911,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             // part 0 or 1 (64 keys) of a value product; `first`: O begins
             auto values = [&](int h, bool first, uint32_t stage, int part) {
                 const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
-                const uint32_t vb = sb + C::kOffRing + stage * C::kStage;
-                const uint64_t vd = D * C::kElem == 256 ? tc::smem_desc(vb, 1024, 2048)
-                                                        : tc::smem_desc(vb, 16384, 1024);
-                if constexpr (E4) {
+                const uint32_t vb = sb + (E4 ? C::kOffWide + stage * C::kWide
+                                             : C::kOffRing + stage * C::kStage);
+                const uint64_t vd = D == 128 ? tc::smem_desc(vb, 1024, 2048)
+                                             : tc::smem_desc(vb, 16384, 1024);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int kk = 2 * part; kk < 2 * part + 2; ++kk)
-                            tc::mma_e4m3_ts(dO, p + 32 * t + 8 * kk, vd + ((4096 * kk) >> 4),
-                                            C::kIdO, part || t || (kk & 1) || !first);
-                } else {
-#pragma unroll
-                    for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
-                        tc::mma_bf16_ts(dO, p + 8 * kk,
-                                        vd + (((D == 128 ? 4096 : 2048) * kk) >> 4), C::kIdO,
-                                        kk || !first);
-                }
+                for (int kk = 4 * part; kk < 4 * part + 4; ++kk)
+                    tc::mma_bf16_ts(dO, p + 8 * kk, vd + (((D == 128 ? 4096 : 2048) * kk) >> 4),
+                                    C::kIdO, kk || !first);
             };
             for (int it = 0; it < num_items && ok; ++it) {
                 const Item r = read_item(it);
@@ -980,12 +954,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         // (half B of a pair item: its tiles are A's, waited for there)
                         if (h == 0 || split) {
                             const bool both = split && i < nb;
-                            ok = entry(both ? h : 0, vs);
+                            ok = E4 ? wait(bar(kBarWideFull) + 8u * wide, wide_lap)
+                                    : entry(both ? h : 0, vs);
                             if (ok && scores_too) ok = entry(both ? 2 + h : 1, ks);
                         } else {
                             vs = slot;
                             ks = slot + 1 == C::kStages ? 0 : slot + 1;
                         }
+                        if (E4) vs = wide;
                         if (ok && i == 0) {
                             ok = wait(bar(kBarOEmpty + h), nitem[h] ^ 1u);
                             nitem[h] ^= 1u;
@@ -1008,7 +984,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             // (the other value products' end is told with the next scores')
                             tc::commit(bar(kBarPvDone + h));
                         }
-                        if (split || h) tc::commit(bar(kBarEmpty) + 8u * vs);
+                        if (split || h) {
+                            tc::commit(bar(E4 ? kBarWideEmpty : kBarEmpty) + 8u * vs);
+                            wide_lap ^= wide;
+                            wide ^= 1u;
+                        }
                     }
                     // the item's last score product frees its queries
                     if (i + 2 == na) tc::commit(bar(kBarQEmpty));
@@ -1020,6 +1000,74 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_wait(bar(kBarDrain), 0, a.status);
         }
         __syncwarp();
+    } else if (E4) {
+        // ------------------------------------------------- values widened to fp16
+        // Every code is an fp16 number.  Eight lanes take a key's 128 codes (16
+        // each, the chunks of a row in turn: no bank twice), a pass 8 keys; keys that
+        // no row of the item sees become 0.
+        uint32_t ring = 0, wide = 0, lap = 1;
+        bool ok = true;
+        const int c = lane & 7, r0 = (warp - kLoadWarp - 1) * 4 + (lane >> 3);
+        const uint32_t from = uint32_t(r0 * 128 + ((c ^ r0) << 4));
+        const int half = c >> 2, chunk = (c & 3) * 2;
+        const uint32_t to0 = uint32_t(half * 1024 + r0 * 128 + (((chunk + half) ^ r0) << 4));
+        const uint32_t to1 = uint32_t(half * 1024 + r0 * 128 + (((chunk + 1 - half) ^ r0) << 4));
+        for (int it = 0; it < num_items && ok; ++it) {
+            const Item r = read_item(it);
+            if (r.na == 0) continue;
+            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+            const int32_t pmax = r.pos + r.ntok - 1;
+            const Order ord{ring, r.split, r.nb};
+            for (int j = 0; j < r.na + (r.split ? r.nb : 0) && ok; ++j) {
+                const int h = r.split ? (j < 2 * r.nb ? j & 1 : 0) : 0;
+                const int i = r.split ? (j < 2 * r.nb ? j >> 1 : r.na - 1) : j;
+                const int v = r.v0 + (h ? r.na : 0) + i;
+                const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
+                ok = __all_sync(0xffffffffu,
+                                pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u, a.status,
+                                          abort_flag) &&
+                                    pipe_wait(bar(kBarWideEmpty + wide), lap, a.status,
+                                              abort_flag));
+                if (!ok) break;
+                const uint8_t *src = base + C::kOffRing + stage * C::kStage + from;
+                uint8_t *dst = base + C::kOffWide + wide * C::kWide;
+                const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
+                const bool some = k0 + kKeys - 1 > pmax ||
+                                  (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = *reinterpret_cast<const uint4 *>(src + (4 * q + e) * 1024);
+                    if (some) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int32_t key = k0 + r0 + 8 * (4 * q + e);
+                            if (key > pmax || (key < tl.lo && key >= a.sinks))
+                                x[e] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint2 a0 = e4m3x4_to_f16x4(x[e].x), a1 = e4m3x4_to_f16x4(x[e].y);
+                        const uint2 b0 = e4m3x4_to_f16x4(x[e].z), b1 = e4m3x4_to_f16x4(x[e].w);
+                        const uint4 lo = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                        const uint4 hi = make_uint4(b0.x, b0.y, b1.x, b1.y);
+                        uint8_t *d = dst + (4 * q + e) * 2048;
+                        *reinterpret_cast<uint4 *>(d + to0) = half ? hi : lo;
+                        *reinterpret_cast<uint4 *>(d + to1) = half ? lo : hi;
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kBarWideFull + wide));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(kBarEmpty + stage));
+                lap ^= wide;
+                wide ^= 1u;
+            }
+            ring += ord.total(r.na);
+        }
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
@@ -1114,7 +1162,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key
-                if (!clear) {
+                // (E4M3: where they are widened)
+                if (!E4 && !clear) {
                     const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
                     if (k0 + kKeys - 1 > pmax ||
                         (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
@@ -1124,12 +1173,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const int32_t key = k0 + row;
                         if (ok && (key > pmax || (key < tl.lo && key >= a.sinks))) {
                             uint8_t *vt = base + C::kOffRing + stage * C::kStage;
-                            if constexpr (D * C::kElem == 256)
-                                vt += (row >> 3) * 2048 + (row & 7) * 128;
-                            else
-                                vt += row * 128;
+                            vt += D == 128 ? (row >> 3) * 2048 + (row & 7) * 128 : row * 128;
 #pragma unroll
-                            for (int c = 0; c < D * C::kElem / 16; ++c)
+                            for (int c = 0; c < D / 8; ++c)
                                 *reinterpret_cast<uint4 *>(vt + (c >> 3) * 1024 + (c & 7) * 16) =
                                     make_uint4(0, 0, 0, 0);
                         }
@@ -1137,18 +1183,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                     __syncwarp();
                 }
-                // ---- probabilities and their terms over S's columns, 64 keys at a
-                // time, against the row's reference m.  m need not be the maximum:
-                // numbers with 8 bits of exponent hold 2^(score - m) as exactly
-                // whatever m is, short of overflow.  So bf16 terms are taken against
-                // the first maximum, and the reference rises only when the sum of a
-                // row's 64 probabilities passes kMost (E4M3 terms: when a score
-                // passes it by kSlack); they are then taken again.  A loop, not
-                // unrolled: the code of one part stays in the instruction cache beside
-                // the issuing thread's.
+                // ---- probabilities, rounded to 16 bits over S's columns, 64 keys at a
+                // time, against the row's reference m.  m need not be the maximum: a
+                // number with a full exponent holds 2^(score - m) as exactly whatever m
+                // is, short of overflow.  So they are taken against the first maximum,
+                // and the reference rises only when the sum of a row's 64 passes kMost;
+                // they are then taken again.  A loop, not unrolled: the code of one part
+                // stays in the instruction cache beside the issuing thread's.
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
-                    uint32_t x[64], t0[32], t1[16];
+                    uint32_t x[64], t[32];
                     tc::ld32(ts + 64 * part, x);
                     tc::ld32(ts + 64 * part + 32, x + 32);
                     tc::wait_ld();
@@ -1170,21 +1214,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                     float total;
                     for (bool again = false;; again = true) {
-                        const float neg = (m == -INFINITY ? 0.f : -m * sc) + C::kShift;
+                        const float neg = m == -INFINITY ? 0.f : -m * sc;
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        exponentials<E4>(x, sc, neg, sum, t0, t1, [&](int j) {
-                            if constexpr (E4) raise4(mx, x + j);
-                        });
+                        exponentials<E4>(x, sc, neg, sum, t);
                         total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        const bool rise =
-                            E4 ? (fmaxf(mx[0], mx[2]) - m) * sc > C::kSlack
-                               : total > kMost || m == -INFINITY;
+                        const bool rise = total > C::kMost || m == -INFINITY;
                         if (!__any_sync(0xffffffffu, rise && !again)) break;
-                        if constexpr (!E4) {
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 64; j += 4) raise4(mx, x + j);
-                        }
+                        for (int j = 0; j < 64; j += 4) raise4(mx, x + j);
                         // (a row that need not rise keeps m and, to the bit, its terms:
                         // what a row gives does not depend on its neighbours)
                         const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[2])) : m;
@@ -1212,7 +1250,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         m = mn;
                     }
                     __syncwarp();
-                    store_terms<E4>(ts, part, t0, t1);
+                    tc::st32(ts + 32 * part, t);
+                    tc::wait_st();
+                    tc::fence_before_sync();
                     mbar_arrive(bar(kBarPFull + 2 * part + h));
                     l += total;
                 }
@@ -1230,7 +1270,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const float nan = __int_as_float(0x7fc00000);
             float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             if constexpr (E4) inv *= a.v_scale[g];
-            float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kShift)) * kLn2 : -INFINITY;
+            float lse = l > 0.f || l != l ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
             if (!ok) inv = lse = nan;
             ring += ord.total(r.na);
             const int tok = (r.split ? 0 : h * tpt) + tok_row;
