@@ -56,12 +56,7 @@ namespace {
 
 constexpr int kRows = 128;               // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;               // keys per tile
-constexpr int kThreads = 384;             // three warp groups
-// Registers a thread: launched with 168 (384 x 168 = 64,512), the softmax
-// groups then take 200, the issuing group keeps 104 (256 x 200 + 128 x 104).
-constexpr int kSoftRegs = 200, kIssueRegs = 104;
-constexpr int kMmaWarp = 8, kLoadWarp = 9;
-constexpr int kWidenThreads = 64;        // warps 10 and 11 (E4M3)
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kWidenWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
@@ -72,6 +67,12 @@ struct Cfg {
     static_assert(D == 64 || D == 128, "head dims of one or two 128-byte column blocks");
     static_assert(!E4 || D == 128, "E4M3 rows fill a 128-byte swizzle row");
     static constexpr int kElem = E4 ? 1 : 2;
+    // Three warp groups, four with the one that widens values.  Registers a thread:
+    // launched with 168 (128), the softmax groups then take kSoftRegs, the others
+    // keep kOtherRegs; the sums are those of the launch or less.
+    static constexpr int kThreads = E4 ? 512 : 384;
+    static constexpr int kSoftRegs = E4 ? 184 : 200, kOtherRegs = E4 ? 72 : 104;
+    static constexpr int kWideners = 4;                             // warps
     static constexpr uint32_t kHalfTile = kRows * 128;              // [128 rows][128 B]
     static constexpr uint32_t kQTile = E4 ? 2 * kHalfTile : kRows * D * 2;
     static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
@@ -105,7 +106,7 @@ constexpr int kBarPvDone = 28;           // + half: the item's value products do
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
 constexpr int kBarDrain = 32;
 constexpr int kBarP0Done = 33;           // + half: value product of a tile's first 64 keys done
-constexpr int kBarWideFull = 35;         // + buffer: values widened (kWidenThreads arrivals)
+constexpr int kBarWideFull = 35;         // + buffer: values widened (128 arrivals)
 constexpr int kBarWideEmpty = 37;        // + buffer: their value products done (commit)
 constexpr uint32_t kOffSlot = 39 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
@@ -145,6 +146,7 @@ constexpr int kHdrRounds = 1;            // whole items of every CTA
 constexpr int kHdrByHead = 2;            // work order: KV head major
 constexpr int kHdrSplit = 3;             // entries of `split`
 constexpr int kHdrCuts = 4;              // entries of `cuts`
+constexpr int kHdrSplitRows = 5;         // most rows of an entry of `split`
 
 struct Shape {
     int32_t group, tokens_per_tile;
@@ -267,7 +269,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     __shared__ int32_t s_before[kInShared + 1], s_steps[kInShared], s_prow[kInShared];
     __shared__ uint32_t s_key[kInShared];            // low 10 bits: the block at a place
     __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
-    __shared__ int32_t s_max, s_min;
+    __shared__ int32_t s_max, s_min, s_split_rows;
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -282,6 +284,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     if (tid == 0) {
         s_max = 0;
         s_min = INT_MAX;
+        s_split_rows = 0;
     }
     for (int base = 0; base < a.batch; base += kPlanThreads) {
         const int b = base + tid;
@@ -406,6 +409,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         if (in) {
             const int32_t before = cost_all + v.x - cost;
             if (halves) {
+                atomicMax(&s_split_rows, q.ntok * sh.group);
                 plan.split[nsplit + v.y - 1] = i;
                 q.prow = part_rows + v.z - rows;
             }
@@ -543,6 +547,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         plan.header[kHdrByHead] = by_head;
         plan.header[kHdrSplit] = nsplit;
         plan.header[kHdrCuts] = total.y;
+        plan.header[kHdrSplitRows] = s_split_rows;
     }
 }
 
@@ -658,7 +663,7 @@ __device__ __forceinline__ void exponentials(const uint32_t *s, float sc, float 
 }
 
 template <int D, bool E4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, E4>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const ChunkArgs a, const Plan plan,
@@ -679,7 +684,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), E4 ? 2 : 1);
+            mbar_init(bar(kBarEmpty + s), E4 ? C::kWideners : 1);
         }
         mbar_init(bar(kBarQFull), E4 ? 256 : 1);
         mbar_init(bar(kBarQEmpty), 1);
@@ -691,7 +696,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(bar(kBarPvDone + h), 1);
             mbar_init(bar(kBarP0Done + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
-            mbar_init(bar(kBarWideFull + h), kWidenThreads);
+            mbar_init(bar(kBarWideFull + h), 32 * C::kWideners);
             mbar_init(bar(kBarWideEmpty + h), 1);
         }
         *abort_flag = 0;
@@ -737,11 +742,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     };
 
     if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ producer
         const int box = min(bs, kKeys);
-        const int nbox = kKeys / box;
+        const int nbox = kKeys / box, log_bs = 31 - __clz(bs);
         uint32_t ring = 0, items_done = 0;
         uint32_t armed = 0, armed_parity = 0;
         uint32_t q_armed = 0, q_parity = 0;
@@ -753,21 +758,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
             const int32_t pmax = r.pos + r.ntok - 1;
             const int32_t *table = a.block_tables + int64_t(r.b) * a.max_blocks;
-            // pool row of box `bx` of virtual tile v, or -1 (nothing to copy)
-            auto row_of = [&](int v, int bx) -> int32_t {
+            // This lane's box of step i -- of a pair item lanes 0 .. nbox - 1, of a split
+            // item half A's in lanes 0 .. 15 and half B's in 16 .. 31 -- as its first
+            // key, or -1: nothing to copy.
+            auto key_of = [&](int i) -> int32_t {
+                const int bx = r.split ? lane & 15 : lane, half = r.split ? lane >> 4 : 0;
+                if (bx >= nbox || i >= (half ? r.nb : r.na)) return -1;
+                const int v = r.v0 + (half ? r.na : 0) + i;
                 const int32_t key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + bx * box;
-                if (key > pmax || (key + box - 1 < tl.lo && key >= a.sinks)) return -1;
-                const int32_t phys = table[key / bs];
+                return key > pmax || (key + box - 1 < tl.lo && key >= a.sinks) ? -1 : key;
+            };
+            // The entry of its block, and the pool row that entry stands for (two
+            // functions, a step apart: the first one's load need not be waited for).
+            auto entry_of = [&](int i) -> int32_t {
+                const int32_t key = key_of(i);
+                return key < 0 ? 0 : table[key >> log_bs];
+            };
+            auto row_of = [&](int i, int32_t phys) -> int32_t {
+                const int32_t key = key_of(i);
+                if (key < 0) return -1;
                 if (phys < 0 || phys >= a.cache.num_blocks) {
                     raise_status(a.status, PKV_DEV_BLOCK_ID);
                     return g * bs;                  // some block's rows stand in
                 }
-                return (phys * hkv + g) * bs + key % bs;
-            };
-            auto lookup = [&](int v) { return lane < nbox ? row_of(v, lane) : -1; };
-            auto lookup2 = [&](int v, int w, bool second) {
-                const int bx = lane & 15;
-                return bx < nbox && (lane < 16 || second) ? row_of(lane < 16 ? v : w, bx) : -1;
+                return (phys * hkv + g) * bs + (key & (bs - 1));
             };
             auto load = [&](const CUtensorMap *map, int32_t y) -> bool {
                 const uint32_t stage = ring % C::kStages, phase = (ring / C::kStages) & 1u;
@@ -776,7 +790,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     return false;
                 const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
                 if (lane == 0) {
-                    if (E4 && map == &tmap_k) mbar_arrive(bar(kBarEmpty + stage));
+                    if (E4 && map == &tmap_k)
+                        for (int k = 1; k < C::kWideners; ++k) mbar_arrive(bar(kBarEmpty + stage));
                     mbar_arrive_expect_tx(bar(kBarFull + stage),
                                           __popc(live) * uint32_t(box) * D * C::kElem);
                 }
@@ -817,30 +832,31 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 ++items_done;
                 return true;
             };
-            // Blocks are looked up a step ahead, so that the next copies need not wait
-            // for the table; the queries' buffer frees late, so the item's first keys
-            // go before them.
-            if (!r.split) {
-                int32_t y = lookup(r.v0);
-                for (int i = 0; i < r.na && ok; ++i) {
-                    const int32_t yn = i + 1 < r.na ? lookup(r.v0 + i + 1) : -1;
-                    ok = load(&tmap_k, y) && (i > 0 || load_q()) && load(&tmap_v, y);
-                    y = yn;
-                }
-            } else {
-                // lanes 0 .. 15: half A's boxes, 16 .. 31: half B's
-                int32_t y = lookup2(r.v0, r.v0 + r.na, r.nb > 0);
-                for (int i = 0; i < r.na && ok; ++i) {
-                    const int32_t yn =
-                        i + 1 < r.na ? lookup2(r.v0 + i + 1, r.v0 + r.na + i + 1, i + 1 < r.nb) : -1;
-                    const int32_t y1 = __shfl_down_sync(0xffffffffu, y, 16);
-                    const int32_t y0 = lane < 16 ? y : -1;
+            // Rows are known kAhead steps before their copy, so that the copies wait for
+            // no table; the queries' buffer frees late, so the item's first keys go
+            // before them.  (Copies to L2 ahead of the ring's made split items slower:
+            // single tokens under a window of 4,096 228 -> 297 us.)
+            constexpr int kAhead = 3;
+            int32_t y[kAhead], phys[kAhead + 1];
+#pragma unroll
+            for (int k = 0; k <= kAhead; ++k) phys[k] = entry_of(k);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) y[k] = row_of(k, phys[k]);
+            int32_t pending = phys[kAhead];
+            for (int i = 0; i < r.na && ok; ++i) {
+                if (!r.split) {
+                    ok = load(&tmap_k, y[0]) && (i > 0 || load_q()) && load(&tmap_v, y[0]);
+                } else {
+                    const int32_t yb = __shfl_down_sync(0xffffffffu, y[0], 16);
+                    const int32_t y0 = lane < 16 ? y[0] : -1, y1 = lane < 16 ? yb : -1;
                     const bool both = i < r.nb;
-                    ok = load(&tmap_k, y0) && (!both || load(&tmap_k, lane < 16 ? y1 : -1)) &&
-                         (i > 0 || load_q()) && load(&tmap_v, y0) &&
-                         (!both || load(&tmap_v, lane < 16 ? y1 : -1));
-                    y = yn;
+                    ok = load(&tmap_k, y0) && (!both || load(&tmap_k, y1)) &&
+                         (i > 0 || load_q()) && load(&tmap_v, y0) && (!both || load(&tmap_v, y1));
                 }
+#pragma unroll
+                for (int k = 0; k + 1 < kAhead; ++k) y[k] = y[k + 1];
+                y[kAhead - 1] = row_of(i + kAhead, pending);
+                pending = entry_of(i + kAhead + 1);
             }
         }
         // Do not leave while copies may still land in this CTA's shared memory.
@@ -1000,14 +1016,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_wait(bar(kBarDrain), 0, a.status);
         }
         __syncwarp();
-    } else if (E4) {
+    } else if (E4 && warp >= kWidenWarp) {
         // ------------------------------------------------- values widened to fp16
         // Every code is an fp16 number.  Eight lanes take a key's 128 codes (16
         // each, the chunks of a row in turn: no bank twice), a pass 8 keys; keys that
         // no row of the item sees become 0.
         uint32_t ring = 0, wide = 0, lap = 1;
         bool ok = true;
-        const int c = lane & 7, r0 = (warp - kLoadWarp - 1) * 4 + (lane >> 3);
+        const int c = lane & 7, r0 = (warp & 1) * 4 + (lane >> 3), hi8 = (warp >> 1) & 1;
         const uint32_t from = uint32_t(r0 * 128 + ((c ^ r0) << 4));
         const int half = c >> 2, chunk = (c & 3) * 2;
         const uint32_t to0 = uint32_t(half * 1024 + r0 * 128 + (((chunk + half) ^ r0) << 4));
@@ -1029,29 +1045,36 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                     pipe_wait(bar(kBarWideEmpty + wide), lap, a.status,
                                               abort_flag));
                 if (!ok) break;
-                const uint8_t *src = base + C::kOffRing + stage * C::kStage + from;
-                uint8_t *dst = base + C::kOffWide + wide * C::kWide;
+                const uint8_t *src = base + C::kOffRing + stage * C::kStage + from + hi8 * 8192;
+                uint8_t *dst = base + C::kOffWide + wide * C::kWide + hi8 * 16384;
                 const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
                 const bool some = k0 + kKeys - 1 > pmax ||
                                   (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys));
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint4 x[4];
+                // four keys' chunks are fetched before the last four are written
+                uint4 x[2][4];
+                auto fetch = [&](int q) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        x[e] = *reinterpret_cast<const uint4 *>(src + (4 * q + e) * 1024);
+                        x[q & 1][e] =
+                            *reinterpret_cast<const uint4 *>(src + (4 * q + e) * 1024);
+                };
+                fetch(0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (q < 1) fetch(q + 1);
+                    uint4 (&y)[4] = x[q & 1];
                     if (some) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int32_t key = k0 + r0 + 8 * (4 * q + e);
+                            const int32_t key = k0 + r0 + 64 * hi8 + 8 * (4 * q + e);
                             if (key > pmax || (key < tl.lo && key >= a.sinks))
-                                x[e] = make_uint4(0, 0, 0, 0);
+                                y[e] = make_uint4(0, 0, 0, 0);
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const uint2 a0 = e4m3x4_to_f16x4(x[e].x), a1 = e4m3x4_to_f16x4(x[e].y);
-                        const uint2 b0 = e4m3x4_to_f16x4(x[e].z), b1 = e4m3x4_to_f16x4(x[e].w);
+                        const uint2 a0 = e4m3x4_to_f16x4(y[e].x), a1 = e4m3x4_to_f16x4(y[e].y);
+                        const uint2 b0 = e4m3x4_to_f16x4(y[e].z), b1 = e4m3x4_to_f16x4(y[e].w);
                         const uint4 lo = make_uint4(a0.x, a0.y, a1.x, a1.y);
                         const uint4 hi = make_uint4(b0.x, b0.y, b1.x, b1.y);
                         uint8_t *d = dst + (4 * q + e) * 2048;
@@ -1070,7 +1093,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         // -------------------------------------------- softmax and epilogue
         const int h = warp >> 2;                         // half
         const int row = threadIdx.x & 127;
@@ -1336,7 +1359,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 // over the row's partials, each already divided by its own sum.  A NaN partial
 // makes the row NaN; empty ones (lse = -inf) weigh nothing.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 16;           // rows of a warp's unit of work
+constexpr int kMergeRows = 4;            // rows of a warp's unit of work
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -1346,8 +1369,10 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     pdl_launch_dependents();
     const int hkv = a.cache.num_kv_heads, G = sh.group;
     // the split items taken whole (two partials of at most kRows rows each), then the cuts
-    constexpr int kHalfUnits = kRows / kMergeRows, kUnits = 2 * kHalfUnits;
-    const int32_t n_short = plan.header[kHdrSplit] * hkv, n_half = n_short * kHalfUnits;
+    constexpr int kUnits = 2 * kRows / kMergeRows;
+    const int32_t n_short = plan.header[kHdrSplit] * hkv;
+    const int32_t n_half =
+        n_short * ((plan.header[kHdrSplitRows] + kMergeRows - 1) / kMergeRows);
     const int32_t total = n_half + plan.header[kHdrCuts] * kUnits;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
     const int nblocks = plan.header[kHdrBlocks];
@@ -1566,7 +1591,7 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
     }
     int rc = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, a.stream, a, plan, sh);
     if (rc != PKV_OK) return rc;
-    rc = launch_pdl(kernel, dim3(sz.ctas), dim3(kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
+    rc = launch_pdl(kernel, dim3(sz.ctas), dim3(C::kThreads), C::kSmem, a.stream, tq, tk, tv, a, plan,
                     sh);
     if (rc != PKV_OK) return rc;
     const int64_t merge_units = sz.blocks * a.cache.num_kv_heads * (kRows / kMergeRows) +
