@@ -58,7 +58,6 @@ constexpr int kRows = 128;               // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kWidenWarp = 12;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -77,6 +76,12 @@ struct Cfg {
     static constexpr uint32_t kQTile = E4 ? 2 * kHalfTile : kRows * D * 2;
     static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
     static constexpr int kStages = E4 ? 6 : kStage == 32768 ? 5 : 10;
+    // TMEM: the buffers of S from column 0, O_A and O_B from kColO.  Head dim 64
+    // leaves room for a third S: buffers go round, and the scores of a half's next
+    // tile are there before its probabilities of this one are (one step in 8 of a
+    // window's chunk: 264 -> XXX us).
+    static constexpr bool kThree = D == 64;
+    static constexpr uint32_t kColO = kThree ? 384 : 256;
     static constexpr uint32_t kWide = kKeys * D * 2;                // a V tile in 16 bits
     static constexpr uint32_t kOffQ = 1024;
     static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
@@ -99,16 +104,18 @@ constexpr int kBarEmpty = 10;            // + stage.  E4M3: two arrivals, of a v
                                          // own and the commit
 constexpr int kBarQFull = 20;
 constexpr int kBarQEmpty = 21;           // commit: the item's score products are done
-constexpr int kBarSFull = 22;            // + half: scores written (commit)
-constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64 keys written
-                                         // (128 arrivals)
-constexpr int kBarPvDone = 28;           // + half: the item's value products done (commit)
+constexpr int kBarPvDone = 22;           // + half (+ 2 for every other tile of three S
+                                         // buffers): value products of a tile done
+                                         // (commit; two buffers: of the item's last tile)
+constexpr int kBarP0Done = 26;           // the same, of a tile's first 64 keys
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
 constexpr int kBarDrain = 32;
-constexpr int kBarP0Done = 33;           // + half: value product of a tile's first 64 keys done
-constexpr int kBarWideFull = 35;         // + buffer: values widened (128 arrivals)
-constexpr int kBarWideEmpty = 37;        // + buffer: their value products done (commit)
-constexpr uint32_t kOffSlot = 39 * 8;
+constexpr int kBarSFull = 33;            // + S buffer: scores written (commit)
+constexpr int kBarPFull = 36;            // + 3 part + S buffer: probabilities of 64 keys written
+                                         // (128 arrivals)
+constexpr int kBarWideFull = 42;         // + buffer: values widened (128 arrivals)
+constexpr int kBarWideEmpty = 44;        // + buffer: their value products done (commit)
+constexpr uint32_t kOffSlot = 46 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -690,14 +697,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         mbar_init(bar(kBarQEmpty), 1);
         mbar_init(bar(kBarDrain), 1);
         for (int h = 0; h < 2; ++h) {
-            mbar_init(bar(kBarSFull + h), 1);
-            mbar_init(bar(kBarPFull + h), 128);
-            mbar_init(bar(kBarPFull + 2 + h), 128);
-            mbar_init(bar(kBarPvDone + h), 1);
-            mbar_init(bar(kBarP0Done + h), 1);
+            for (int e = h; e < 4; e += 2) {
+                mbar_init(bar(kBarPvDone + e), 1);
+                mbar_init(bar(kBarP0Done + e), 1);
+            }
             mbar_init(bar(kBarOEmpty + h), 128);
             mbar_init(bar(kBarWideFull + h), 32 * C::kWideners);
             mbar_init(bar(kBarWideEmpty + h), 1);
+        }
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(bar(kBarSFull + s), 1);
+            mbar_init(bar(kBarPFull + s), 128);
+            mbar_init(bar(kBarPFull + 3 + s), 128);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -877,7 +888,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (tc::elect_one()) {
             uint32_t slot = 0, lap = 0;          // ring position: stage and lap parity
             uint32_t item_bit = 0;               // items done, mod 2
-            uint32_t np[2] = {0, 0};             // tiles whose probabilities were taken, mod 2
+            // S buffers: the one of the next scores and of the next value product, and
+            // how often the latter was used, mod 2 (two buffers: the halves')
+            uint32_t sq = 0, sp = 0, np[2] = {0, 0};
+            uint32_t odd[2] = {0, 0};            // three buffers: 2 for a half's odd tiles
             uint32_t nitem[2] = {0, 0};          // items begun, by half, mod 2
             uint32_t wide = 0, wide_lap = 0;     // next buffer of widened values (E4M3)
             bool ok = true;
@@ -902,7 +916,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
             };
             auto scores = [&](int h, bool second_q, uint32_t stage) {
-                const uint32_t ds = tmem + kKeys * h;
+                const uint32_t buf = C::kThree ? sq : h, ds = tmem + kKeys * buf;
+                if (C::kThree) sq = sq == 2 ? 0 : sq + 1;
                 const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
                 const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
                 const uint64_t q =
@@ -923,10 +938,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                          kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
                                          (half | kk) != 0);
                 }
+                tc::commit(bar(kBarSFull) + 8u * buf);
             };
             // part 0 or 1 (64 keys) of a value product; `first`: O begins
             auto values = [&](int h, bool first, uint32_t stage, int part) {
-                const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
+                const uint32_t dO = tmem + C::kColO + D * h, p = tmem + kKeys * (C::kThree ? sp : h);
                 const uint32_t vb = sb + (E4 ? C::kOffWide + stage * C::kWide
                                              : C::kOffRing + stage * C::kStage);
                 const uint64_t vd = D == 128 ? tc::smem_desc(vb, 1024, 2048)
@@ -948,13 +964,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if (!(ok = entry(0, st))) break;
                 tc::fence_after_sync();
                 scores(0, false, st);
-                tc::commit(bar(kBarSFull));
                 if (split) tc::commit(bar(kBarEmpty) + 8u * st);
                 if (nb > 0) {
                     if (split && !(ok = entry(1, st))) break;
                     tc::fence_after_sync();
                     scores(1, !split, st);
-                    tc::commit(bar(kBarSFull + 1));
                     tc::commit(bar(kBarEmpty) + 8u * st);
                 }
                 if (na == 1) tc::commit(bar(kBarQEmpty));
@@ -978,28 +992,42 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             ks = slot + 1 == C::kStages ? 0 : slot + 1;
                         }
                         if (E4) vs = wide;
-                        if (ok && i == 0) {
+                        auto next_scores = [&] {
+                            if (!scores_too) return;
+                            scores(h, h && !split, ks);
+                            if (split || h) tc::commit(bar(kBarEmpty) + 8u * ks);
+                        };
+                        if (!ok) break;
+                        if (C::kThree) {
+                            tc::fence_after_sync();
+                            next_scores();
+                        }
+                        if (i == 0) {
                             ok = wait(bar(kBarOEmpty + h), nitem[h] ^ 1u);
                             nitem[h] ^= 1u;
+                            if (!ok) break;
                         }
-                        ok = ok && wait(bar(kBarPFull + h), np[h]);
-                        if (!ok) break;
+                        const uint32_t pf = bar(kBarPFull) + 8u * (C::kThree ? sp : h);
+                        const uint32_t pp = np[C::kThree ? 0 : h];
+                        if (!(ok = wait(pf, pp))) break;
                         tc::fence_after_sync();
                         // the first 64 keys' product while the others' softmax goes on
                         values(h, i == 0, vs, 0);
-                        tc::commit(bar(kBarP0Done + h));
-                        if (!(ok = wait(bar(kBarPFull + 2 + h), np[h]))) break;
+                        tc::commit(bar(kBarP0Done + h) + 8u * odd[h]);
+                        if (!(ok = wait(pf + 24u, pp))) break;
                         tc::fence_after_sync();
                         values(h, i == 0, vs, 1);
-                        np[h] ^= 1u;
-                        if (scores_too) {
-                            scores(h, h && !split, ks);
-                            tc::commit(bar(kBarSFull + h));
-                            if (split || h) tc::commit(bar(kBarEmpty) + 8u * ks);
+                        if (C::kThree) {
+                            np[0] ^= sp >> 1;
+                            sp = sp == 2 ? 0 : sp + 1;
                         } else {
-                            // (the other value products' end is told with the next scores')
-                            tc::commit(bar(kBarPvDone + h));
+                            np[h] ^= 1u;
+                            next_scores();
                         }
+                        // (with two buffers the other value products' end is told with the
+                        // next scores')
+                        if (C::kThree || !scores_too) tc::commit(bar(kBarPvDone + h) + 8u * odd[h]);
+                        if (C::kThree) odd[h] ^= 2u;
                         if (split || h) {
                             tc::commit(bar(E4 ? kBarWideEmpty : kBarEmpty) + 8u * vs);
                             wide_lap ^= wide;
@@ -1098,12 +1126,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int h = warp >> 2;                         // half
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + kKeys * h + lanes;    // S, P
-        const uint32_t to = tmem + kColO + 128 * h + lanes;
+        const uint32_t to = tmem + C::kColO + D * h + lanes;
         const int tok_row = row / G, head_row = row - tok_row * G;
         const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         uint32_t ring = 0, np = 0, nitem = 0, items_done = 0;
+        uint32_t turn = 0;                               // tiles of both halves before the item
         bool ok = true;
+        // Tile (item) k of the half is done.  With three S buffers this thread may be two
+        // tiles ahead of the value products, more than a parity tells apart: odd and even
+        // tiles have a barrier each.
+        auto done = [&](int b, uint32_t k) {
+            return C::kThree ? pipe_wait(bar(b + h) + 16u * (k & 1u), k >> 1 & 1u, a.status,
+                                         abort_flag)
+                             : pipe_wait(bar(b + h), k & 1u, a.status, abort_flag);
+        };
         for (int it = 0; it < num_items; ++it) {
             const Item r = read_item(it);
             const int g = r.g;
@@ -1178,10 +1214,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 clear0 = max(clear0 - tl.gap, tl.sink_tiles);
                 clear1 = max(hmin + 1, 0) / kKeys - tl.gap;
             }
+            // S buffer of the half's next tile, and how often it was used, mod 2
+            uint32_t buf = h, used = np & 1u;
+            if (C::kThree) {
+                buf = (turn + h) % 3u;
+                used = (turn + h) / 3u & 1u;
+                turn += r.na + r.nb;
+            }
             for (int i = 0; i < n; ++i) {
                 const int v = v0 + i;
+                const uint32_t ts = tmem + kKeys * buf + lanes;      // S, P
                 const bool clear = v >= clear0 && v < clear1;
-                ok = ok && pipe_wait(bar(kBarSFull + h), np & 1u, a.status, abort_flag);
+                ok = ok && pipe_wait(bar(kBarSFull) + 8u * buf, used, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key
@@ -1251,10 +1295,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[2])) : m;
                         const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
                         if (part || i > 0) {
-                            // rescale.  These scores were told after the last tile's value
-                            // product; that of this tile's first keys has to be waited for.
-                            ok = ok && (part == 0 || pipe_wait(bar(kBarP0Done + h), np & 1u,
-                                                               a.status, abort_flag));
+                            // rescale, once the value products so far are done: that of this
+                            // tile's first keys, and the last tile's (with two buffers that was
+                            // told with these scores).
+                            if (part) ok = ok && done(kBarP0Done, np);
+                            else if (C::kThree) ok = ok && done(kBarPvDone, np - 1);
                             __syncwarp();
                             tc::fence_after_sync();
 #pragma unroll
@@ -1276,15 +1321,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     tc::st32(ts + 32 * part, t);
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(bar(kBarPFull + 2 * part + h));
+                    mbar_arrive(bar(kBarPFull + 3 * part) + 8u * buf);
                     l += total;
                 }
                 ++np;
+                buf += C::kThree ? 2u : 0u;
+                used ^= C::kThree ? buf >= 3u : 1u;
+                buf -= C::kThree && buf >= 3u ? 3u : 0u;
             }
 
             // ---- epilogue
             if (n > 0) {
-                ok = ok && pipe_wait(bar(kBarPvDone + h), nitem & 1u, a.status, abort_flag);
+                ok = ok && done(kBarPvDone, C::kThree ? np - 1 : nitem);
                 ++nitem;
                 __syncwarp();
                 tc::fence_after_sync();
