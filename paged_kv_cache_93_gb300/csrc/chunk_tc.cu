@@ -274,9 +274,9 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     __shared__ int3 warp_sums[32];
     __shared__ int32_t s_first[kInShared + 1], s_cu[kInShared + 1], s_len[kInShared];
     __shared__ int32_t s_before[kInShared + 1], s_steps[kInShared], s_prow[kInShared];
-    __shared__ uint32_t s_key[kInShared];            // low 10 bits: the block at a place
+    __shared__ __align__(16) uint32_t s_key[kInShared];          // low 10 bits: the block at a place
     __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
-    __shared__ int32_t s_max, s_min, s_split_rows;
+    __shared__ int32_t s_max, s_min, s_split_rows, s_rounds;
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
@@ -292,6 +292,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         s_max = 0;
         s_min = INT_MAX;
         s_split_rows = 0;
+        s_rounds = INT_MAX;
     }
     for (int base = 0; base < a.batch; base += kPlanThreads) {
         const int b = base + tid;
@@ -383,23 +384,29 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     auto cost_of = [&](int32_t steps) { return ((steps + kItemCost) >> shift) + (shift > 0); };
     const int32_t item_cost = cost_of(0), piece_cost = (kPieceCost >> shift) + (shift > 0);
     if (few_blocks && !by_head && n_items > ctas) {
-        int n = 1;
-        while (n < nblocks) n <<= 1;
-        for (int i = nblocks + tid; i < n; i += kPlanThreads) s_key[i] = 0xffffffffu;
-        for (int k = 2; k <= n; k <<= 1)
-            for (int j = k >> 1; j > 0; j >>= 1) {
-                __syncthreads();
-                for (int i = tid; i < n; i += kPlanThreads) {
-                    const int x = i ^ j;
-                    if (x > i) {
-                        const uint32_t u = s_key[i], v = s_key[x];
-                        if ((u > v) == ((i & k) == 0)) {
-                            s_key[i] = v;
-                            s_key[x] = u;
-                        }
-                    }
-                }
+        // a key's place is the number of smaller ones (keys differ: the block is in them)
+        for (int i = nblocks + tid; i < (nblocks + 3 & ~3); i += kPlanThreads)
+            s_key[i] = 0xffffffffu;
+        __syncthreads();
+        uint32_t key[kInShared / kPlanThreads];
+        int place[kInShared / kPlanThreads];
+#pragma unroll
+        for (int u = 0; u < kInShared / kPlanThreads; ++u) {
+            const int i = tid + u * kPlanThreads;
+            place[u] = -1;
+            if (i >= nblocks) continue;
+            key[u] = s_key[i];
+            int n = 0;
+            for (int j = 0; j < nblocks; j += 4) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(s_key + j);
+                n += (k.x < key[u]) + (k.y < key[u]) + (k.z < key[u]) + (k.w < key[u]);
             }
+            place[u] = n;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kInShared / kPlanThreads; ++u)
+            if (place[u] >= 0) s_key[place[u]] = key[u];
         __syncthreads();
     }
     auto ordered = [&](int r) { return block_of(few_blocks ? int(s_key[r] & 1023u) : r); };
@@ -440,18 +447,26 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
 
     // ---- whole rounds
     const int32_t share = uint32_t(cost_all * hkv) / uint32_t(ctas) + 1 + piece_cost;
-    int32_t load = 0, rounds = 0;
-    while ((rounds + 1) * ctas <= n_items) {
-        int32_t next = load;
-        if (tid < ctas) {
-            int32_t r, g;
-            item_at(round_item(rounds, tid, ctas), by_head, nblocks, hkv, r, g);
-            next += cost_of(steps_at(r));
+    // (each thread on its own: the most rounds its CTA takes; the least of them counts)
+    const int32_t most_rounds = n_items / ctas;
+    auto round_cost = [&](int k) {
+        int32_t r, g;
+        item_at(round_item(k, tid, ctas), by_head, nblocks, hkv, r, g);
+        return cost_of(steps_at(r));
+    };
+    if (tid < ctas) {
+        int32_t sum = 0, k = 0;
+        for (; k < most_rounds; ++k) {
+            sum += round_cost(k);
+            if (sum > share) break;
         }
-        if (__syncthreads_or(next > share)) break;
-        load = next;
-        ++rounds;
+        if (k < most_rounds) atomicMin(&s_rounds, k);
     }
+    __syncthreads();
+    const int32_t rounds = min(s_rounds, most_rounds);
+    int32_t load = 0;
+    if (tid < ctas)
+        for (int k = 0; k < rounds; ++k) load += round_cost(k);
 
     // ---- the rest, cut by the capacities left
     const int32_t idx0 = rounds * ctas;
@@ -1067,11 +1082,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int i = r.split ? (j < 2 * r.nb ? j >> 1 : r.na - 1) : j;
                 const int v = r.v0 + (h ? r.na : 0) + i;
                 const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
+                // (the buffer first: its last product came after every wait for the key
+                // tile that was in this stage before, whose phase this wait may skip)
                 ok = __all_sync(0xffffffffu,
-                                pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u, a.status,
-                                          abort_flag) &&
-                                    pipe_wait(bar(kBarWideEmpty + wide), lap, a.status,
-                                              abort_flag));
+                                pipe_wait(bar(kBarWideEmpty + wide), lap, a.status, abort_flag) &&
+                                    pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
+                                              a.status, abort_flag));
                 if (!ok) break;
                 const uint8_t *src = base + C::kOffRing + stage * C::kStage + from + hi8 * 8192;
                 uint8_t *dst = base + C::kOffWide + wide * C::kWide + hi8 * 16384;
@@ -1147,7 +1163,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int tok0 = r.split ? 0 : h * tpt;      // the half's first token
             float sc = a.scale * kLog2e;
             float m = -INFINITY, l = 0.f;            // reference, sum against it
-            if (tok_row >= tpt || tok0 + tok_row >= r.ntok) sc = m = 0.f;    // no row: any bits
+            const bool has_row = tok_row < tpt && tok0 + tok_row < r.ntok;
+            if (!has_row) sc = m = 0.f;              // any bits
             if constexpr (E4) {
                 sc *= a.k_scale[g];
                 if (r.na > 0) {
@@ -1203,17 +1220,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             if (r.na > 0) ++items_done;
             const int v0 = r.v0 + (r.split && h ? r.na : 0);
-            // Virtual tiles [clear0, clear1): every row of the half sees every key.
             const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
             const int32_t pmax = r.pos + r.ntok - 1, pos = r.pos + tok0 + tok_row;
+            // positions of the warp's rows (none: the largest below the smallest)
+            const int32_t first = __reduce_min_sync(0xffffffffu, has_row ? pos : INT_MAX);
+            const int32_t last = __reduce_max_sync(0xffffffffu, has_row ? pos : INT_MIN);
+            // Virtual tiles [clear0, clear1): each of them sees every key.
+            const int clear0 =
+                max((a.window > 0 && last >= a.window ? (last - a.window) / kKeys + 1 : 0) - tl.gap,
+                    tl.sink_tiles);
+            const int clear1 = (first == INT_MAX ? 0 : max(first + 1, 0) / kKeys) - tl.gap;
             const Order ord{ring, r.split, r.nb};
-            int clear0, clear1;
-            {
-                const int32_t hmin = r.pos + tok0, hmax = r.pos + min(r.ntok, tok0 + tpt) - 1;
-                clear0 = a.window > 0 && hmax >= a.window ? (hmax - a.window) / kKeys + 1 : 0;
-                clear0 = max(clear0 - tl.gap, tl.sink_tiles);
-                clear1 = max(hmin + 1, 0) / kKeys - tl.gap;
-            }
             // S buffer of the half's next tile, and how often it was used, mod 2
             uint32_t buf = h, used = np & 1u;
             if (C::kThree) {
@@ -1225,20 +1242,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int v = v0 + i;
                 const uint32_t ts = tmem + kKeys * buf + lanes;      // S, P
                 const bool clear = v >= clear0 && v < clear1;
+                const int32_t tile_key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
                 ok = ok && pipe_wait(bar(kBarSFull) + 8u * buf, used, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key
                 // (E4M3: where they are widened)
                 if (!E4 && !clear) {
-                    const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                    if (k0 + kKeys - 1 > pmax ||
-                        (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
+                    const int32_t key = tile_key + row;
+                    const bool unseen = key > pmax || (key < tl.lo && key >= a.sinks);
+                    if (__any_sync(0xffffffffu, unseen)) {
                         const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
                         ok = ok && pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
                                              a.status, abort_flag);
-                        const int32_t key = k0 + row;
-                        if (ok && (key > pmax || (key < tl.lo && key >= a.sinks))) {
+                        if (ok && unseen) {
                             uint8_t *vt = base + C::kOffRing + stage * C::kStage;
                             vt += D == 128 ? (row >> 3) * 2048 + (row & 7) * 128 : row * 128;
 #pragma unroll
@@ -1247,8 +1264,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                     make_uint4(0, 0, 0, 0);
                         }
                         fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 // ---- probabilities, rounded to 16 bits over S's columns, 64 keys at a
                 // time, against the row's reference m.  m need not be the maximum: a
@@ -1260,15 +1277,30 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     uint32_t x[64], t[32];
+                    const int32_t k0 = tile_key + 64 * part;
+                    // no row of the warp sees any of the keys: nothing is computed
+                    if (!clear &&
+                        (k0 > last ||
+                         (a.window > 0 && k0 + 63 <= first - a.window && k0 >= a.sinks))) {
+                        if (last != INT_MIN) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) t[j] = 0u;
+                            tc::st32(ts + 32 * part, t);
+                            tc::wait_st();
+                            tc::fence_before_sync();
+                        }
+                        mbar_arrive(bar(kBarPFull + 3 * part) + 8u * buf);
+                        continue;
+                    }
                     tc::ld32(ts + 64 * part, x);
                     tc::ld32(ts + 64 * part + 32, x + 32);
                     tc::wait_ld();
                     pin<32>(x);
                     pin<32>(x + 32);
-                    if (!clear) {
-                        // keys this row does not see
-                        const int32_t k0 =
-                            (v < tl.sink_tiles ? v : v + tl.gap) * kKeys + 64 * part;
+                    // unless every row of the warp sees all of them
+                    if (!clear &&
+                        (k0 + 63 > first ||
+                         (a.window > 0 && k0 <= last - a.window && k0 + 63 >= a.sinks))) {
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
                             uint32_t see = pos >= 0 ? below(pos - k0 + 1, w) : 0u;
