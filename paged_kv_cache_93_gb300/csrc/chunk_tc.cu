@@ -82,6 +82,11 @@ struct Cfg {
     // window's chunk: 264 -> XXX us).
     static constexpr bool kThree = D == 64;
     static constexpr uint32_t kColO = kThree ? 384 : 256;
+    // Who makes the value rows 0 that no row of an item sees.  Head dim 64, whose
+    // softmax bounds a step: the two idle warps (an 8K prompt under a window of 1,024:
+    // 250 -> 231 us); head dim 128, where a tile's way to the tensor cores counts: the
+    // softmax warps (8K prompt 388 -> 380 us); E4M3: the warps that widen.
+    static constexpr bool kTended = D == 64;
     static constexpr uint32_t kWide = kKeys * D * 2;                // a V tile in 16 bits
     static constexpr uint32_t kOffQ = 1024;
     static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
@@ -115,7 +120,9 @@ constexpr int kBarPFull = 36;            // + 3 part + S buffer: probabilities o
                                          // (128 arrivals)
 constexpr int kBarWideFull = 42;         // + buffer: values widened (128 arrivals)
 constexpr int kBarWideEmpty = 44;        // + buffer: their value products done (commit)
-constexpr uint32_t kOffSlot = 46 * 8;
+constexpr int kBarReady = 46;            // + stage: a tile is in place, the unseen rows of a V
+                                         // tile 0 (kTended; 2 arrivals)
+constexpr uint32_t kOffSlot = 56 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -579,9 +586,6 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
 struct Order {
     uint32_t base;
     int32_t split, nb;
-    __device__ __forceinline__ uint32_t k(int h, int i) const {
-        return base + (split ? 4 * i + (h ? 1 : 0) : 2 * i);
-    }
     __device__ __forceinline__ uint32_t v(int h, int i) const {
         return base + (split ? 4 * i + (i < nb ? 2 + h : 1) : 2 * i + 1);
     }
@@ -706,6 +710,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
+            mbar_init(bar(kBarReady + s), 2);
             mbar_init(bar(kBarEmpty + s), E4 ? C::kWideners : 1);
         }
         mbar_init(bar(kBarQFull), E4 ? 256 : 1);
@@ -921,7 +926,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     stage -= C::kStages;
                     l ^= 1u;
                 }
-                return wait(bar(kBarFull) + 8u * stage, l);
+                return wait(bar(C::kTended ? kBarReady : kBarFull) + 8u * stage, l);
             };
             auto advance = [&](uint32_t n) {
                 slot += n;
@@ -1059,6 +1064,63 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_wait(bar(kBarDrain), 0, a.status);
         }
         __syncwarp();
+    } else if (C::kTended) {
+        // ------------------------------------- value rows no row of the item sees
+        // Warps 10 and 11, 64 keys each: such rows become 0 before the value product
+        // reads them.  Every tile of the ring passes here, keys too: copies may land in
+        // another order than they were issued in, and a role that waited for some
+        // phases of a stage only could take one for the next.
+        uint32_t stage = 0, lap = 0;
+        bool ok = true;
+        for (int it = 0; it < num_items && ok; ++it) {
+            const Item r = read_item(it);
+            if (r.na == 0) continue;
+            const Tiles tl = tiles_of(r.pos, r.ntok, a.window, a.sinks);
+            const int32_t pmax = r.pos + r.ntok - 1;
+            const int total = r.split ? 2 * (r.na + r.nb) : 2 * r.na;
+            for (int e = 0; e < total; ++e) {
+                // entries K0 V0 K1 .., or KA0 KB0 VA0 VB0 KA1 .. KA VA
+                int v = -1;
+                if (!r.split) {
+                    if (e & 1) v = e >> 1;
+                } else if (e < 4 * r.nb) {
+                    if (e & 2) v = (e & 1 ? r.na : 0) + (e >> 2);
+                } else if (e & 1) {
+                    v = r.nb;
+                }
+                ok = __all_sync(0xffffffffu,
+                                pipe_wait(bar(kBarFull) + 8u * stage, lap, a.status, abort_flag));
+                if (!ok) break;
+                if (v >= 0) {
+                    v += r.v0;
+                    const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
+                    if (k0 + kKeys - 1 > pmax ||
+                        (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
+                        uint8_t *vt = base + C::kOffRing + stage * C::kStage;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int row = (warp - kLoadWarp - 1) * 64 + 32 * u + lane;
+                            const int32_t key = k0 + row;
+                            uint8_t *d =
+                                vt + (D == 128 ? (row >> 3) * 2048 + (row & 7) * 128 : row * 128);
+                            if (key > pmax || (key < tl.lo && key >= a.sinks)) {
+#pragma unroll
+                                for (int c = 0; c < D / 8; ++c)
+                                    *reinterpret_cast<uint4 *>(d + (c >> 3) * 1024 + (c & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (lane == 0) mbar_arrive(bar(kBarReady) + 8u * stage);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    lap ^= 1u;
+                }
+            }
+        }
     } else if (E4 && warp >= kWidenWarp) {
         // ------------------------------------------------- values widened to fp16
         // Every code is an fp16 number.  Eight lanes take a key's 128 codes (16
@@ -1247,8 +1309,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key
-                // (E4M3: where they are widened)
-                if (!E4 && !clear) {
+                if (!C::kTended && !E4 && !clear) {
                     const int32_t key = tile_key + row;
                     const bool unseen = key > pmax || (key < tl.lo && key >= a.sinks);
                     if (__any_sync(0xffffffffu, unseen)) {
