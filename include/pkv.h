@@ -566,8 +566,8 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  * out [num_tokens][num_q_heads][head_dim_v] bf16, lse [num_tokens][num_q_heads]
  * fp32 (or NULL: not wanted).  scale > 0 and finite; window >= 0 (0: none);
  * sink_tokens >= 0 (without a window it changes nothing).  Probabilities are
- * rounded to bf16 for the value product (E4M3 caches: to two E4M3 terms, as
- * the query is: 2^-8 relative, and 2^-17 of the row's largest); sums and
+ * rounded to bf16 for the value product (E4M3 caches: to fp16, and the query to
+ * two E4M3 terms, 2^-8 relative and 2^-17 of its row's largest); sums and
  * statistics are fp32, out is rounded once.  Values of magnitude 2^80 and
  * above may overflow the sums.
  *  - Rows of q outside [cu_q_lens[0], cu_q_lens[batch]) are padding: their out

@@ -4,16 +4,19 @@
 //
 // The rows of one KV head -- (token, query head of the group) pairs, token
 // major -- are packed into tiles of 128 (tokens_per_tile = 128 / group, so an odd
-// group wastes the remainder).  With m the running row maximum,
+// group wastes the remainder).  With m a reference of the row,
 //   S[128 rows x 128 keys] = Q_tile . K_tile^T             (tcgen05, fp32 in TMEM)
 //   P = 2^((S - m) scale log2 e), l += row sums of P       (CUDA cores, one thread a row)
 //   O[128 rows x D]       += P . V_tile                    (tcgen05, P read from TMEM)
 // and out = O / l, lse = m scale + ln l.  P is rounded to bf16 for the second
 // product (its sum is taken before the rounding, in fp32): one bf16 term is
-// what the bf16 output resolves.  E4M3 caches: Q and P go as two E4M3 terms
-// each, the second the rounding residual of the first (bf16 queries fit two
-// terms exactly; P keeps 2^-8 relative and 2^-17 of the row's largest), so the
-// stored codes feed the tensor cores as they are.
+// what the bf16 output resolves.  E4M3 caches: Q goes as two E4M3 terms, the
+// second the rounding residual of the first (a bf16 element fits them exactly
+// unless it is far below its row's largest), so the stored keys feed the tensor
+// cores as they are, in the time of one bf16 product; the values are widened to
+// fp16, which holds them exactly, and P is rounded to fp16 (two E4M3 terms of P
+// instead cost the softmax threads six conversions for four scores: 650 us for
+// 1,000 tokens over 17K keys, 471 so).
 //
 // Work item = (block of up to 2 tiles' tokens of a sequence, KV head, all of its
 // key tiles or a run of them), given out by plan_kernel:
@@ -24,13 +27,20 @@
 // A cut item's partial (O / l, lse), and the two halves' of a split item, go to
 // the workspace and chunk_merge_kernel joins them.
 //
-// Roles (three warp groups, one CTA an SM): warps 0-3 softmax and epilogue of A,
-// warps 4-7 of B, one thread a row, warp 8 MMA issue, warp 9 TMA.  TMEM, all 512 columns: S_A
-// S_B O_A O_B, P over S.  The MMAs of one thread run in order, so S may be
-// overwritten by the next score product once the value product that reads P
-// there is issued.  A row's m rises only when a score exceeds it by more than
-// kSlack (log2): then that warp rescales its rows of O in TMEM.  Every wait is
-// bounded.
+// Roles, one CTA an SM: warps 0-3 softmax and epilogue of A, warps 4-7 of B, one
+// thread a row, warp 8 MMA issue, warp 9 TMA; head dim 64: warps 10 and 11, E4M3:
+// warps 12-15, see to the value tiles.  TMEM, all 512 columns: S buffers and O_A
+// O_B, P over S.  The MMAs of one thread run in order, so S may be overwritten by a
+// score product once the value product that reads P there is issued.  Every wait
+// is bounded.
+//
+// What bounds it (2,048 tokens over 32K keys, 32 heads over 8, 676 us, 1.57 PFLOP/s,
+// 0.81 of the measured bf16 rate): a step of a pair item -- four products of 512
+// cycles -- takes 2,860 cycles.  The products of a half wait for its softmax, that
+// for the scores before; TMEM has no room for a third S at head dim 128, and what
+// the issuing thread does between two products (waits, commits) leaves the tensor
+// cores idle.  Single tokens read 4.8 TB/s: the ring holds little more than a
+// step of a split item.
 //
 // Keys are walked in absolute 128-key tiles.  Under a window the tiles
 // between the sinks and the first row's window are skipped; in a tile only
@@ -78,8 +88,8 @@ struct Cfg {
     static constexpr int kStages = E4 ? 6 : kStage == 32768 ? 5 : 10;
     // TMEM: the buffers of S from column 0, O_A and O_B from kColO.  Head dim 64
     // leaves room for a third S: buffers go round, and the scores of a half's next
-    // tile are there before its probabilities of this one are (one step in 8 of a
-    // window's chunk: 264 -> XXX us).
+    // tile are there before its probabilities of this one are (an 8K prompt under a
+    // window of 1,024: 264 -> 262 us, and what followed).
     static constexpr bool kThree = D == 64;
     static constexpr uint32_t kColO = kThree ? 384 : 256;
     // Who makes the value rows 0 that no row of an item sees.  Head dim 64, whose
@@ -1096,18 +1106,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const int32_t k0 = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
                     if (k0 + kKeys - 1 > pmax ||
                         (k0 < tl.lo && max(k0, a.sinks) < min(tl.lo, k0 + kKeys))) {
-                        uint8_t *vt = base + C::kOffRing + stage * C::kStage;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int row = (warp - kLoadWarp - 1) * 64 + 32 * u + lane;
                             const int32_t key = k0 + row;
-                            uint8_t *d =
-                                vt + (D == 128 ? (row >> 3) * 2048 + (row & 7) * 128 : row * 128);
                             if (key > pmax || (key < tl.lo && key >= a.sinks)) {
+                                uint4 *d = reinterpret_cast<uint4 *>(
+                                    base + C::kOffRing + stage * C::kStage + row * 128);
 #pragma unroll
-                                for (int c = 0; c < D / 8; ++c)
-                                    *reinterpret_cast<uint4 *>(d + (c >> 3) * 1024 + (c & 7) * 16) =
-                                        make_uint4(0, 0, 0, 0);
+                                for (int c = 0; c < 8; ++c) d[c] = make_uint4(0, 0, 0, 0);
                             }
                         }
                         fence_proxy_async_smem();
@@ -1144,8 +1151,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int i = r.split ? (j < 2 * r.nb ? j >> 1 : r.na - 1) : j;
                 const int v = r.v0 + (h ? r.na : 0) + i;
                 const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
-                // (the buffer first: its last product came after every wait for the key
-                // tile that was in this stage before, whose phase this wait may skip)
+                // (The buffer first: its last product came after every wait for the key
+                // tile that was in this stage before.  Copies may land in another order
+                // than they were issued in; without that this wait could take the key
+                // tile's phase for this one's.)
                 ok = __all_sync(0xffffffffu,
                                 pipe_wait(bar(kBarWideEmpty + wide), lap, a.status, abort_flag) &&
                                     pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
@@ -1308,7 +1317,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 ok = ok && pipe_wait(bar(kBarSFull) + 8u * buf, used, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
-                // ---- value rows no row of the item sees: zeroed, thread = key
+                // ---- value rows no row of the item sees: zeroed, thread = key.  (These
+                // scores came after every wait for the tile that was in the stage
+                // before, so the wait cannot take that tile's phase for this one's.)
                 if (!C::kTended && !E4 && !clear) {
                     const int32_t key = tile_key + row;
                     const bool unseen = key > pmax || (key < tl.lo && key >= a.sinks);
@@ -1318,7 +1329,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                              a.status, abort_flag);
                         if (ok && unseen) {
                             uint8_t *vt = base + C::kOffRing + stage * C::kStage;
-                            vt += D == 128 ? (row >> 3) * 2048 + (row & 7) * 128 : row * 128;
+                            vt += (row >> 3) * 2048 + (row & 7) * 128;
 #pragma unroll
                             for (int c = 0; c < D / 8; ++c)
                                 *reinterpret_cast<uint4 *>(vt + (c >> 3) * 1024 + (c & 7) * 16) =
@@ -1500,7 +1511,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 // over the row's partials, each already divided by its own sum.  A NaN partial
 // makes the row NaN; empty ones (lse = -inf) weigh nothing.
 constexpr int kMergeThreads = 256;
-constexpr int kMergeRows = 4;            // rows of a warp's unit of work
+constexpr int kMergeRows = 4;            // rows of a warp's unit of work (each row waits for
+                                         // its partials: 16 rows a warp 23 us, 4 rows 9, of
+                                         // a ragged batch of 24)
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)

@@ -147,12 +147,12 @@ def check(case, out, lse):
     """out and lse against the definition.
 
     out: each probability is rounded by at most 2^-8 of itself for the value
-    product (bf16; two E4M3 terms of 2^-4 each), which moves out by at most
+    product (bf16; E4M3 caches fp16, 2^-11), which moves out by at most
     2^-8 sum p |v|; the result is rounded by at most 2^-8 of itself; fp32
     sums, and probabilities from scores that are off as below, are covered by
-    the score term.  The second E4M3 term of a probability steps by 2^-9 where
-    the row's largest is 2^7 or more, so it is off by up to 2^-17 of the largest
-    however small the probability is: 2^-17 sum |v|.
+    the score term.  fp16 steps by 2^-24 where the row's largest probability is 1
+    or more: however small a probability, it is off by at most 2^-24 of the
+    largest, 2^-24 sum |v|.
     lse, and each score: dk products summed in fp32, (dk + 2) 2^-24 of the sum
     of their magnitudes; the sum of probabilities 2^-17 relative.  E4M3: the
     second term of a query element steps by 2^-9 where the row's largest is 2^7
@@ -170,8 +170,9 @@ def check(case, out, lse):
         score = score + 2.0 ** -17 * qlow[rows]
     d_lse = (lse[rows] - ref_lse[rows]).abs()
     assert torch.all(d_lse <= score), float((d_lse - score).max())
-    vanish = 2.0 ** -17 * low[rows] if case.k_scale is not None else 0.0
-    tol = (2.0 ** -8 + 2 * score[:, None]) * absv[rows] + 2.0 ** -8 * ref[rows].abs() + vanish
+    e4m3 = case.k_scale is not None
+    vanish = 2.0 ** -24 * low[rows] if e4m3 else 0.0
+    tol = ((2.0 ** -11 if e4m3 else 2.0 ** -8) + 2 * score[:, None]) * absv[rows] + 2.0 ** -8 * ref[rows].abs() + vanish
     d = (out[rows] - ref[rows]).abs()
     assert torch.all(d <= tol), float((d - tol).max())
     # the whole result is nearer than the worst case of every element at once
