@@ -59,7 +59,7 @@
 #include "pkv_host.h"
 #include "pkv_math.cuh"
 #include "pkv_pipeline.cuh"
-#include "pkv_tcgen05.cuh"
+#include "pkv_tcgen05_ts.cuh"
 
 namespace pkv {
 namespace {
