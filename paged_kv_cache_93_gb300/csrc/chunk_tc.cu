@@ -138,8 +138,9 @@ constexpr uint32_t kOffFlag = kOffSlot + 4;
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
 struct __align__(16) Block {
     int32_t b, qrow, pos, ntok;          // sequence; row of q and position of its first token
-    int32_t tiles, steps, prow, pad;     // key tiles; steps of the whole; partial rows of KV
-                                         // head 0 when taken whole as a split item, or -1
+    int32_t tiles, steps, prow, work;    // key tiles; steps of the whole; partial rows of KV
+                                         // head 0 when taken whole as a split item, or -1;
+                                         // steps in pair items' steps (split_work)
 };
 // What a CTA does at a time: some steps of a (block, KV head).
 struct __align__(16) Item {
@@ -241,6 +242,10 @@ constexpr int kMaxCtas = kPlanThreads;
 // partial results (128 KB) go through memory; pieces of fewer steps than
 // kSnap are left to the neighbour.
 constexpr int kItemCost = 3, kPieceCost = 6, kSnap = 6;
+// A step of a split item moves and handles two key tiles, a pair item's one: 1.5
+// times the cost (E4M3, keys in L2: 5,200 cycles against 3,250).  And back.
+__device__ __forceinline__ int32_t split_work(int32_t steps) { return steps + (steps >> 1); }
+__device__ __forceinline__ int32_t split_steps(int32_t work) { return work - work / 3; }
 
 // Inclusive scans of three numbers over the CTA's threads; the sums go to
 // `total`.
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     __shared__ int3 warp_sums[32];
     __shared__ int32_t s_first[kInShared + 1], s_cu[kInShared + 1], s_len[kInShared];
-    __shared__ int32_t s_before[kInShared + 1], s_steps[kInShared], s_prow[kInShared];
+    __shared__ int32_t s_before[kInShared + 1], s_work[kInShared], s_prow[kInShared];
     __shared__ __align__(16) uint32_t s_key[kInShared];          // low 10 bits: the block at a place
     __shared__ int32_t cut_idx[kMaxCtas + 1], cut_step[kMaxCtas + 1];
     __shared__ int32_t s_max, s_min, s_split_rows, s_rounds;
@@ -374,7 +379,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         q.tiles = tiles_of(q.pos, q.ntok, a.window, a.sinks).count;
         q.steps = q.ntok <= tpt ? (q.tiles + 1) >> 1 : q.tiles;
         q.prow = -1;
-        q.pad = 0;
+        q.work = q.ntok <= tpt ? split_work(q.steps) : q.steps;
         return q;
     };
 
@@ -382,9 +387,9 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     int32_t most = 0, least = INT_MAX;
     for (int i = tid; i < nblocks; i += kPlanThreads) {
         const Block q = block_of(i);
-        if (few_blocks) s_key[i] = uint32_t((1 << 20) - 1 - min(q.steps, (1 << 20) - 1)) << 10 | i;
-        most = max(most, q.steps);
-        least = min(least, q.steps);
+        if (few_blocks) s_key[i] = uint32_t((1 << 20) - 1 - min(q.work, (1 << 20) - 1)) << 10 | i;
+        most = max(most, q.work);
+        least = min(least, q.work);
     }
     most = __reduce_max_sync(0xffffffffu, most);
     least = __reduce_min_sync(0xffffffffu, least);
@@ -398,7 +403,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     // costs in units of 2^shift steps, so that their sum stays below 2^30
     int32_t shift = 0;
     while (float(s_max + kItemCost) * float(n_items) > float(1 << 30) * float(1u << shift)) ++shift;
-    auto cost_of = [&](int32_t steps) { return ((steps + kItemCost) >> shift) + (shift > 0); };
+    auto cost_of = [&](int32_t work) { return ((work + kItemCost) >> shift) + (shift > 0); };
     const int32_t item_cost = cost_of(0), piece_cost = (kPieceCost >> shift) + (shift > 0);
     if (few_blocks && !by_head && n_items > ctas) {
         // a key's place is the number of smaller ones (keys differ: the block is in them)
@@ -434,7 +439,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         const bool in = i < nblocks;
         if (in) q = ordered(i);
         const bool halves = in && q.ntok <= tpt && q.tiles > 1;
-        const int32_t cost = in ? cost_of(q.steps) : 0;
+        const int32_t cost = in ? cost_of(q.work) : 0;
         const int32_t rows = halves ? 2 * q.ntok * sh.group * hkv : 0;
         const int3 v = block_scan(make_int3(cost, halves, rows), warp_sums, total);
         if (in) {
@@ -447,7 +452,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
             plan.blocks[i] = q;
             if (few_blocks) {
                 s_before[i] = before;
-                s_steps[i] = q.steps;
+                s_work[i] = q.work * 2 + (q.ntok <= tpt);
                 s_prow[i] = q.prow;
             } else {
                 plan.before[i] = before;
@@ -460,7 +465,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     if (tid == 0) (few_blocks ? s_before : plan.before)[nblocks] = cost_all;
     __syncthreads();
     const int32_t *before = few_blocks ? s_before : plan.before;
-    auto steps_at = [&](int r) { return few_blocks ? s_steps[r] : plan.blocks[r].steps; };
+    auto work_at = [&](int r) { return few_blocks ? s_work[r] >> 1 : plan.blocks[r].work; };
 
     // ---- whole rounds
     const int32_t share = uint32_t(cost_all * hkv) / uint32_t(ctas) + 1 + piece_cost;
@@ -469,7 +474,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     auto round_cost = [&](int k) {
         int32_t r, g;
         item_at(round_item(k, tid, ctas), by_head, nblocks, hkv, r, g);
-        return cost_of(steps_at(r));
+        return cost_of(work_at(r));
     };
     if (tid < ctas) {
         int32_t sum = 0, k = 0;
@@ -491,7 +496,7 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     if (idx0 < n_items) item_at(idx0, by_head, nblocks, hkv, r0, g0);
     const int32_t done = idx0 >= n_items ? cost_all * hkv
                          : by_head       ? g0 * cost_all + before[r0]
-                                         : before[r0] * hkv + g0 * cost_of(steps_at(r0));
+                                         : before[r0] * hkv + g0 * cost_of(work_at(r0));
     const int32_t rest = cost_all * hkv - done;
     for (int32_t i = idx0 + tid; i < n_items; i += kPlanThreads) plan.is_cut[i - idx0] = 0;
     const int32_t cap = tid < ctas ? max(0, share - piece_cost - load) : 0;
@@ -519,15 +524,18 @@ plan_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
                 if (before[mid] * times <= y) lo = mid;
                 else hi = mid;
             }
-            const int32_t steps = steps_at(lo);
+            const int32_t work = work_at(lo);
+            const bool halves = few_blocks ? s_work[lo] & 1 : plan.blocks[lo].ntok <= tpt;
+            const int32_t steps = halves ? split_steps(work) : work;
             int32_t off = y - before[lo] * times;
             if (!by_head) {
-                const int32_t c = cost_of(steps);
+                const int32_t c = cost_of(work);
                 g = min(int32_t(uint32_t(off) / uint32_t(c)), hkv - 1);
                 off -= g * c;
             }
             idx = by_head ? g * nblocks + lo : lo * hkv + g;
-            step = min(max(off - item_cost, 0) << shift, steps);
+            step = max(off - item_cost, 0) << shift;
+            step = min(halves ? split_steps(step) : step, steps);
             if (step < kSnap) step = 0;
             else if (steps - step < kSnap) {
                 step = 0;
