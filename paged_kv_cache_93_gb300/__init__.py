@@ -15,6 +15,7 @@ pools of the same shapes, with fp32 dequantisation scales per KV head
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -538,10 +539,11 @@ def chunk_workspace_size(k_pool, v_pool, num_tokens: int, batch: int, num_q_head
     return int(size(ctypes.byref(desc), num_tokens, batch, num_q_heads, max_blocks, int(flags)))
 
 
-# Workspaces of the chunk attention calls that bring none: one for each device
-# and stream, kept, as calls on a stream follow one another.  A capture gets
-# one of its own (graphs may run beside anything).
-_chunk_scratch: dict = {}
+# Workspaces of the chunk attention calls that bring none: one for each thread,
+# device and stream, kept, as a thread's calls on a stream follow one another
+# (two threads' kernels may interleave).  A capture gets one of its own (graphs
+# may run beside anything).
+_chunk_scratch = threading.local()
 
 
 def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out, lse, flags,
@@ -581,11 +583,12 @@ def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out
         if torch.cuda.is_current_stream_capturing():
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
+            kept = _chunk_scratch.__dict__
             key = (q.device.index, _stream())
-            workspace = _chunk_scratch.get(key)
+            workspace = kept.get(key)
             if workspace is None or workspace.numel() < need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-                _chunk_scratch[key] = workspace
+                kept[key] = workspace
         ws_bytes = workspace.numel()
     return workspace, ws_bytes, out, lse
 

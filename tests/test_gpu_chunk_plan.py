@@ -184,3 +184,28 @@ def test_two_graphs_at_once(pkv):  # noqa: F811
     for c, (_, _, (out, lse), _) in zip(cases, graphs):
         _chunk.check(c, out, lse)
     assert pkv.device_status(reset=True) == 0
+
+
+def test_two_threads_on_one_stream(pkv):  # noqa: F811
+    """Calls of two threads may interleave kernel by kernel on their stream."""
+    import threading
+    cases = [_chunk.make(s, [(3000, 200), (700, 1), (0, 90)], 8, 2, 128, 16) for s in (53, 54)]
+    want = [_chunk.run(pkv, c)[0] for c in cases]
+    bufs = [{n: getattr(c, n).cuda() for n in ("q", "cu", "k_pool", "v_pool", "tables", "lens")}
+            for c in cases]
+    torch.cuda.synchronize()
+    wrong = [0, 0]
+
+    def work(k):
+        d = bufs[k]
+        for _ in range(200):
+            out, _ = pkv.paged_chunk_attn(d["q"], d["cu"], d["k_pool"], d["v_pool"], d["tables"],
+                                          d["lens"], cases[k].scale)
+            wrong[k] += int(not torch.equal(out, want[k]))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
