@@ -125,14 +125,16 @@ constexpr int kBarPvDone = 22;           // + half (+ 2 for every other tile of 
 constexpr int kBarP0Done = 26;           // the same, of a tile's first 64 keys
 constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
 constexpr int kBarDrain = 32;
-constexpr int kBarSFull = 33;            // + S buffer: scores written (commit)
-constexpr int kBarPFull = 36;            // + 3 part + S buffer: probabilities of 64 keys written
+constexpr int kBarSFull = 33;            // + half (+ 2 as above): scores written (commit).  By
+                                         // half, not by buffer: a half without tiles for some
+                                         // items runs ahead of the other's
+constexpr int kBarPFull = 37;            // + 3 part + S buffer: probabilities of 64 keys written
                                          // (128 arrivals)
-constexpr int kBarWideFull = 42;         // + buffer: values widened (128 arrivals)
-constexpr int kBarWideEmpty = 44;        // + buffer: their value products done (commit)
-constexpr int kBarReady = 46;            // + stage: a tile is in place, the unseen rows of a V
+constexpr int kBarWideFull = 43;         // + buffer: values widened (128 arrivals)
+constexpr int kBarWideEmpty = 45;        // + buffer: their value products done (commit)
+constexpr int kBarReady = 47;            // + stage: a tile is in place, the unseen rows of a V
                                          // tile 0 (kTended; 2 arrivals)
-constexpr uint32_t kOffSlot = 56 * 8;
+constexpr uint32_t kOffSlot = 58 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -736,6 +738,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         mbar_init(bar(kBarDrain), 1);
         for (int h = 0; h < 2; ++h) {
             for (int e = h; e < 4; e += 2) {
+                mbar_init(bar(kBarSFull + e), 1);
                 mbar_init(bar(kBarPvDone + e), 1);
                 mbar_init(bar(kBarP0Done + e), 1);
             }
@@ -744,7 +747,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             mbar_init(bar(kBarWideEmpty + h), 1);
         }
         for (int s = 0; s < 3; ++s) {
-            mbar_init(bar(kBarSFull + s), 1);
             mbar_init(bar(kBarPFull + s), 128);
             mbar_init(bar(kBarPFull + 3 + s), 128);
         }
@@ -929,7 +931,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             // S buffers: the one of the next scores and of the next value product, and
             // how often the latter was used, mod 2 (two buffers: the halves')
             uint32_t sq = 0, sp = 0, np[2] = {0, 0};
-            uint32_t odd[2] = {0, 0};            // three buffers: 2 for a half's odd tiles
+            // three buffers: 2 for a half's odd tiles, of the value and score products
+            uint32_t odd[2] = {0, 0}, odd_s[2] = {0, 0};
             uint32_t nitem[2] = {0, 0};          // items begun, by half, mod 2
             uint32_t wide = 0, wide_lap = 0;     // next buffer of widened values (E4M3)
             bool ok = true;
@@ -976,7 +979,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                          kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
                                          (half | kk) != 0);
                 }
-                tc::commit(bar(kBarSFull) + 8u * buf);
+                tc::commit(bar(kBarSFull + h) + 8u * odd_s[h]);
+                if (C::kThree) odd_s[h] ^= 2u;
             };
             // part 0 or 1 (64 keys) of a value product; `first`: O begins
             auto values = [&](int h, bool first, uint32_t stage, int part) {
@@ -1310,11 +1314,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     tl.sink_tiles);
             const int clear1 = (first == INT_MAX ? 0 : max(first + 1, 0) / kKeys) - tl.gap;
             const Order ord{ring, r.split, r.nb};
-            // S buffer of the half's next tile, and how often it was used, mod 2
-            uint32_t buf = h, used = np & 1u;
+            uint32_t buf = h;                            // S buffer of the half's next tile
             if (C::kThree) {
                 buf = (turn + h) % 3u;
-                used = (turn + h) / 3u & 1u;
                 turn += r.na + r.nb;
             }
             for (int i = 0; i < n; ++i) {
@@ -1322,7 +1324,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const uint32_t ts = tmem + kKeys * buf + lanes;      // S, P
                 const bool clear = v >= clear0 && v < clear1;
                 const int32_t tile_key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                ok = ok && pipe_wait(bar(kBarSFull) + 8u * buf, used, a.status, abort_flag);
+                ok = ok && done(kBarSFull, np);
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key.  (These
@@ -1438,7 +1440,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
                 ++np;
                 buf += C::kThree ? 2u : 0u;
-                used ^= C::kThree ? buf >= 3u : 1u;
                 buf -= C::kThree && buf >= 3u ? 3u : 0u;
             }
 

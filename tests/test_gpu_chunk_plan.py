@@ -209,3 +209,16 @@ def test_two_threads_on_one_stream(pkv):  # noqa: F811
     for t in threads:
         t.join()
     assert wrong == [0, 0]
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, False), (128, False), (128, True)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 3)])
+def test_short_items_in_a_row(pkv, d, e4m3, window, sinks):  # noqa: F811
+    """Items of one and of two key tiles, mixed: their second half has nothing to
+    do for some items, and must not run ahead of the first."""
+    chunks = [((i * 53) % 420, 1 + (i % 11 == 0) * (i % 30)) for i in range(144)]
+    case = _chunk.make(55, chunks, 24, 8, d, 16, window=window, sinks=sinks, poison=True, e4m3=e4m3)
+    out, lse = both(pkv, case)
+    for _ in range(20):
+        again = _chunk.run(pkv, case)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
