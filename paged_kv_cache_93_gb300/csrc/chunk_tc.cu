@@ -29,18 +29,19 @@
 //
 // Roles, one CTA an SM: warps 0-3 softmax and epilogue of A, warps 4-7 of B, one
 // thread a row, warp 8 MMA issue, warp 9 TMA; head dim 64: warps 10 and 11, E4M3:
-// warps 12-15, see to the value tiles.  TMEM, all 512 columns: S buffers and O_A
-// O_B, P over S.  The MMAs of one thread run in order, so S may be overwritten by a
+// warps 12-15, see to the value tiles.  TMEM, all 512 columns: S_A S_B O_A O_B, P
+// over S.  The MMAs of one thread run in order, so S may be overwritten by a
 // score product once the value product that reads P there is issued.  Every wait
 // is bounded.
 //
-// What bounds it (2,048 tokens over 32K keys, 32 heads over 8, 676 us, 1.57 PFLOP/s,
+// What bounds it (2,048 tokens over 32K keys, 32 heads over 8, 679 us, 1.57 PFLOP/s,
 // 0.81 of the measured bf16 rate): a step of a pair item -- four products of 512
 // cycles -- takes 2,860 cycles.  The products of a half wait for its softmax, that
-// for the scores before; TMEM has no room for a third S at head dim 128, and what
-// the issuing thread does between two products (waits, commits) leaves the tensor
-// cores idle.  Single tokens read 4.8 TB/s: the ring holds little more than a
-// step of a split item.
+// for the scores before, and what the issuing thread does between two products
+// (waits, commits) leaves the tensor cores idle.  A third S buffer, which head dim
+// 64 has room for, so that a half's next scores are there early, changed nothing
+// (241 us either way, an 8K prompt under a window of 1,024).  Single tokens read
+// 4.8 TB/s: the ring holds little more than a step of a split item.
 //
 // Keys are walked in absolute 128-key tiles.  Under a window the tiles
 // between the sinks and the first row's window are skipped; in a tile only
@@ -68,6 +69,7 @@ constexpr int kRows = 128;               // query rows per tile (TMEM lanes)
 constexpr int kKeys = 128;               // keys per tile
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kWidenWarp = 12;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -86,15 +88,9 @@ struct Cfg {
     static constexpr uint32_t kQTile = E4 ? 2 * kHalfTile : kRows * D * 2;
     static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
     static constexpr int kStages = E4 ? 6 : kStage == 32768 ? 5 : 10;
-    // TMEM: the buffers of S from column 0, O_A and O_B from kColO.  Head dim 64
-    // leaves room for a third S: buffers go round, and the scores of a half's next
-    // tile are there before its probabilities of this one are (an 8K prompt under a
-    // window of 1,024: 264 -> 262 us, and what followed).
-    static constexpr bool kThree = D == 64;
-    static constexpr uint32_t kColO = kThree ? 384 : 256;
     // Who makes the value rows 0 that no row of an item sees.  Head dim 64, whose
-    // softmax bounds a step: the two idle warps (an 8K prompt under a window of 1,024:
-    // 250 -> 231 us); head dim 128, where a tile's way to the tensor cores counts: the
+    // softmax bounds a step: the two idle warps (7% of an 8K prompt under a window of
+    // 1,024); head dim 128, where a tile's way to the tensor cores counts: the
     // softmax warps (8K prompt 388 -> 380 us); E4M3: the warps that widen.
     static constexpr bool kTended = D == 64;
     static constexpr uint32_t kWide = kKeys * D * 2;                // a V tile in 16 bits
@@ -119,22 +115,18 @@ constexpr int kBarEmpty = 10;            // + stage.  E4M3: two arrivals, of a v
                                          // own and the commit
 constexpr int kBarQFull = 20;
 constexpr int kBarQEmpty = 21;           // commit: the item's score products are done
-constexpr int kBarPvDone = 22;           // + half (+ 2 for every other tile of three S
-                                         // buffers): value products of a tile done
-                                         // (commit; two buffers: of the item's last tile)
-constexpr int kBarP0Done = 26;           // the same, of a tile's first 64 keys
-constexpr int kBarOEmpty = 30;           // + half: O read out (128 arrivals)
-constexpr int kBarDrain = 32;
-constexpr int kBarSFull = 33;            // + half (+ 2 as above): scores written (commit).  By
-                                         // half, not by buffer: a half without tiles for some
-                                         // items runs ahead of the other's
-constexpr int kBarPFull = 37;            // + 3 part + S buffer: probabilities of 64 keys written
+constexpr int kBarSFull = 22;            // + half: scores written (commit)
+constexpr int kBarPFull = 24;            // + 2 part + half: probabilities of 64 keys written
                                          // (128 arrivals)
-constexpr int kBarWideFull = 43;         // + buffer: values widened (128 arrivals)
-constexpr int kBarWideEmpty = 45;        // + buffer: their value products done (commit)
-constexpr int kBarReady = 47;            // + stage: a tile is in place, the unseen rows of a V
+constexpr int kBarPvDone = 28;           // + half: the item's value products done (commit)
+constexpr int kBarP0Done = 30;           // + half: value product of a tile's first 64 keys done
+constexpr int kBarOEmpty = 32;           // + half: O read out (128 arrivals)
+constexpr int kBarDrain = 34;
+constexpr int kBarWideFull = 35;         // + buffer: values widened (128 arrivals)
+constexpr int kBarWideEmpty = 37;        // + buffer: their value products done (commit)
+constexpr int kBarReady = 39;            // + stage: a tile is in place, the unseen rows of a V
                                          // tile 0 (kTended; 2 arrivals)
-constexpr uint32_t kOffSlot = 58 * 8;
+constexpr uint32_t kOffSlot = 49 * 8;
 constexpr uint32_t kOffFlag = kOffSlot + 4;
 
 // A query block: up to 2 tiles' tokens of a sequence (all KV heads alike).
@@ -737,18 +729,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         mbar_init(bar(kBarQEmpty), 1);
         mbar_init(bar(kBarDrain), 1);
         for (int h = 0; h < 2; ++h) {
-            for (int e = h; e < 4; e += 2) {
-                mbar_init(bar(kBarSFull + e), 1);
-                mbar_init(bar(kBarPvDone + e), 1);
-                mbar_init(bar(kBarP0Done + e), 1);
-            }
+            mbar_init(bar(kBarSFull + h), 1);
+            mbar_init(bar(kBarPFull + h), 128);
+            mbar_init(bar(kBarPFull + 2 + h), 128);
+            mbar_init(bar(kBarPvDone + h), 1);
+            mbar_init(bar(kBarP0Done + h), 1);
             mbar_init(bar(kBarOEmpty + h), 128);
             mbar_init(bar(kBarWideFull + h), 32 * C::kWideners);
             mbar_init(bar(kBarWideEmpty + h), 1);
-        }
-        for (int s = 0; s < 3; ++s) {
-            mbar_init(bar(kBarPFull + s), 128);
-            mbar_init(bar(kBarPFull + 3 + s), 128);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -928,11 +916,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (tc::elect_one()) {
             uint32_t slot = 0, lap = 0;          // ring position: stage and lap parity
             uint32_t item_bit = 0;               // items done, mod 2
-            // S buffers: the one of the next scores and of the next value product, and
-            // how often the latter was used, mod 2 (two buffers: the halves')
-            uint32_t sq = 0, sp = 0, np[2] = {0, 0};
-            // three buffers: 2 for a half's odd tiles, of the value and score products
-            uint32_t odd[2] = {0, 0}, odd_s[2] = {0, 0};
+            uint32_t np[2] = {0, 0};             // tiles whose probabilities were taken, mod 2
             uint32_t nitem[2] = {0, 0};          // items begun, by half, mod 2
             uint32_t wide = 0, wide_lap = 0;     // next buffer of widened values (E4M3)
             bool ok = true;
@@ -957,8 +941,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
             };
             auto scores = [&](int h, bool second_q, uint32_t stage) {
-                const uint32_t buf = C::kThree ? sq : h, ds = tmem + kKeys * buf;
-                if (C::kThree) sq = sq == 2 ? 0 : sq + 1;
+                const uint32_t ds = tmem + kKeys * h;
                 const uint32_t kb = sb + C::kOffRing + stage * C::kStage;
                 const uint64_t kd = tc::smem_desc(kb, 16, D * C::kElem == 256 ? 2048 : 1024);
                 const uint64_t q =
@@ -979,12 +962,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                          kd + ((half * 1024 + 32 * kk) >> 4), C::kIdS,
                                          (half | kk) != 0);
                 }
-                tc::commit(bar(kBarSFull + h) + 8u * odd_s[h]);
-                if (C::kThree) odd_s[h] ^= 2u;
+                tc::commit(bar(kBarSFull + h));
             };
             // part 0 or 1 (64 keys) of a value product; `first`: O begins
             auto values = [&](int h, bool first, uint32_t stage, int part) {
-                const uint32_t dO = tmem + C::kColO + D * h, p = tmem + kKeys * (C::kThree ? sp : h);
+                const uint32_t dO = tmem + kColO + 128 * h, p = tmem + kKeys * h;
                 const uint32_t vb = sb + (E4 ? C::kOffWide + stage * C::kWide
                                              : C::kOffRing + stage * C::kStage);
                 const uint64_t vd = D == 128 ? tc::smem_desc(vb, 1024, 2048)
@@ -1040,36 +1022,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             if (split || h) tc::commit(bar(kBarEmpty) + 8u * ks);
                         };
                         if (!ok) break;
-                        if (C::kThree) {
-                            tc::fence_after_sync();
-                            next_scores();
-                        }
                         if (i == 0) {
                             ok = wait(bar(kBarOEmpty + h), nitem[h] ^ 1u);
                             nitem[h] ^= 1u;
                             if (!ok) break;
                         }
-                        const uint32_t pf = bar(kBarPFull) + 8u * (C::kThree ? sp : h);
-                        const uint32_t pp = np[C::kThree ? 0 : h];
+                        const uint32_t pf = bar(kBarPFull) + 8u * h;
+                        const uint32_t pp = np[h];
                         if (!(ok = wait(pf, pp))) break;
                         tc::fence_after_sync();
                         // the first 64 keys' product while the others' softmax goes on
                         values(h, i == 0, vs, 0);
-                        tc::commit(bar(kBarP0Done + h) + 8u * odd[h]);
-                        if (!(ok = wait(pf + 24u, pp))) break;
+                        tc::commit(bar(kBarP0Done + h));
+                        if (!(ok = wait(pf + 16u, pp))) break;
                         tc::fence_after_sync();
                         values(h, i == 0, vs, 1);
-                        if (C::kThree) {
-                            np[0] ^= sp >> 1;
-                            sp = sp == 2 ? 0 : sp + 1;
-                        } else {
-                            np[h] ^= 1u;
-                            next_scores();
-                        }
-                        // (with two buffers the other value products' end is told with the
-                        // next scores')
-                        if (C::kThree || !scores_too) tc::commit(bar(kBarPvDone + h) + 8u * odd[h]);
-                        if (C::kThree) odd[h] ^= 2u;
+                        np[h] ^= 1u;
+                        next_scores();
+                        // (the other value products' end is told with the next scores')
+                        if (!scores_too) tc::commit(bar(kBarPvDone + h));
                         if (split || h) {
                             tc::commit(bar(E4 ? kBarWideEmpty : kBarEmpty) + 8u * vs);
                             wide_lap ^= wide;
@@ -1225,20 +1196,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int h = warp >> 2;                         // half
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t to = tmem + C::kColO + D * h + lanes;
+        const uint32_t ts = tmem + kKeys * h + lanes;    // S, P
+        const uint32_t to = tmem + kColO + 128 * h + lanes;
         const int tok_row = row / G, head_row = row - tok_row * G;
         const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
         uint32_t ring = 0, np = 0, nitem = 0, items_done = 0;
-        uint32_t turn = 0;                               // tiles of both halves before the item
+        uint32_t s_par = 0;
         bool ok = true;
-        // Tile (item) k of the half is done.  With three S buffers this thread may be two
-        // tiles ahead of the value products, more than a parity tells apart: odd and even
-        // tiles have a barrier each.
-        auto done = [&](int b, uint32_t k) {
-            return C::kThree ? pipe_wait(bar(b + h) + 16u * (k & 1u), k >> 1 & 1u, a.status,
-                                         abort_flag)
-                             : pipe_wait(bar(b + h), k & 1u, a.status, abort_flag);
-        };
         for (int it = 0; it < num_items; ++it) {
             const Item r = read_item(it);
             const int g = r.g;
@@ -1314,17 +1278,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     tl.sink_tiles);
             const int clear1 = (first == INT_MAX ? 0 : max(first + 1, 0) / kKeys) - tl.gap;
             const Order ord{ring, r.split, r.nb};
-            uint32_t buf = h;                            // S buffer of the half's next tile
-            if (C::kThree) {
-                buf = (turn + h) % 3u;
-                turn += r.na + r.nb;
-            }
             for (int i = 0; i < n; ++i) {
                 const int v = v0 + i;
-                const uint32_t ts = tmem + kKeys * buf + lanes;      // S, P
                 const bool clear = v >= clear0 && v < clear1;
                 const int32_t tile_key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                ok = ok && done(kBarSFull, np);
+                ok = ok && pipe_wait(bar(kBarSFull + h), s_par, a.status, abort_flag);
                 __syncwarp();
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key.  (These
@@ -1371,7 +1329,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             tc::wait_st();
                             tc::fence_before_sync();
                         }
-                        mbar_arrive(bar(kBarPFull + 3 * part) + 8u * buf);
+                        mbar_arrive(bar(kBarPFull + 2 * part + h));
                         continue;
                     }
                     tc::ld32(ts + 64 * part, x);
@@ -1409,11 +1367,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[2])) : m;
                         const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
                         if (part || i > 0) {
-                            // rescale, once the value products so far are done: that of this
-                            // tile's first keys, and the last tile's (with two buffers that was
-                            // told with these scores).
-                            if (part) ok = ok && done(kBarP0Done, np);
-                            else if (C::kThree) ok = ok && done(kBarPvDone, np - 1);
+                            // rescale.  These scores were told after the last tile's value
+                            // product; that of this tile's first keys has to be waited for.
+                            if (part)
+                                ok = ok && pipe_wait(bar(kBarP0Done + h), np & 1u, a.status,
+                                                     abort_flag);
                             __syncwarp();
                             tc::fence_after_sync();
 #pragma unroll
@@ -1435,17 +1393,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     tc::st32(ts + 32 * part, t);
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(bar(kBarPFull + 3 * part) + 8u * buf);
+                    mbar_arrive(bar(kBarPFull + 2 * part + h));
                     l += total;
                 }
                 ++np;
-                buf += C::kThree ? 2u : 0u;
-                buf -= C::kThree && buf >= 3u ? 3u : 0u;
+                s_par ^= 1u;
             }
 
             // ---- epilogue
             if (n > 0) {
-                ok = ok && done(kBarPvDone, C::kThree ? np - 1 : nitem);
+                ok = ok && pipe_wait(bar(kBarPvDone + h), nitem & 1u, a.status, abort_flag);
                 ++nitem;
                 __syncwarp();
                 tc::fence_after_sync();
