@@ -539,10 +539,10 @@ def chunk_workspace_size(k_pool, v_pool, num_tokens: int, batch: int, num_q_head
     return int(size(ctypes.byref(desc), num_tokens, batch, num_q_heads, max_blocks, int(flags)))
 
 
-# Workspaces of the chunk attention calls that bring none: one for each thread,
-# device and stream, kept, as a thread's calls on a stream follow one another
-# (two threads' kernels may interleave).  A capture gets one of its own (graphs
-# may run beside anything).
+# Workspaces of the chunk attention calls that bring none, or one that is too
+# small: one for each thread, device and stream that the kernels run on, kept, as
+# a thread's calls on a stream follow one another (two threads' kernels may
+# interleave).  A capture gets one of its own (graphs may run beside anything).
 _chunk_scratch = threading.local()
 
 
@@ -560,8 +560,10 @@ def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out
         raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
     if cu_q_lens.numel() != B + 1 or block_tables.shape[0] != B:
         raise ValueError("cu_q_lens must have one entry more, block_tables one row per seq_len")
-    if stream is not None and (out is None or lse is None or workspace is None):
-        # what is allocated here is used on that stream: let it belong to it
+    need = size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if stream is not None and (out is None or lse is None or ws_bytes < need):
+        # what is allocated or looked up here is used on that stream: let it belong to it
         with torch.cuda.stream(stream):
             return _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out,
                                lse, flags, None)
@@ -577,8 +579,6 @@ def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out
         _need(lse, "lse", torch.float32, 2)
         if lse.shape != (T, Hq):
             raise ValueError("lse must be [tokens, Hq]")
-    need = size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if ws_bytes < need:
         if torch.cuda.is_current_stream_capturing():
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

@@ -1,0 +1,95 @@
+"""The chunk attention binding's own work -- buffers, streams, arguments --
+without a GPU: CUDA's streams are stood in for, and no library call is made
+that would launch."""
+from __future__ import annotations
+
+import contextlib
+import threading
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+NEED = 4096
+
+
+@pytest.fixture(scope="module")
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+    import paged_kv_cache_93_gb300 as m
+    return m
+
+
+@pytest.fixture
+def pkv(built, monkeypatch):
+    """The binding on CPU tensors; `pkv.now[0]` is the current stream's handle."""
+    now, capturing = [0], set()
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, now[0] = now[0], s.cuda_stream
+        try:
+            yield
+        finally:
+            now[0] = before
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0] in capturing)
+    monkeypatch.setattr(built, "_stream", lambda s=None: now[0] if s is None else s.cuda_stream)
+    monkeypatch.setattr(built, "_need", lambda *a, **k: None)
+    monkeypatch.setattr(built, "_chunk_scratch", threading.local())
+    return SimpleNamespace(m=built, now=now, capturing=capturing)
+
+
+SIDE = SimpleNamespace(cuda_stream=7)
+
+
+def scratch(pkv, stream=None, brings="none", outputs=False, need=NEED):
+    """The workspace a call uses."""
+    q = torch.zeros(3, 8, 128, dtype=torch.bfloat16)
+    cu, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ws = {"none": None, "small": torch.empty(NEED // 2, dtype=torch.uint8),
+          "enough": torch.empty(NEED, dtype=torch.uint8)}[brings]
+    out = torch.empty(3, 8, 128, dtype=torch.bfloat16) if outputs else None
+    lse = torch.empty(3, 8) if outputs else None
+    got, size, _, _ = pkv.m._chunk_args(pkv.m.CacheDesc(4, 16, 2, 128, 128), lambda *a: need, q,
+                                        cu, torch.zeros(1, 4, dtype=torch.int32), lens, ws, out,
+                                        lse, 0, stream)
+    assert got.numel() == size >= need
+    assert (got is ws) == (brings == "enough")
+    return got
+
+
+@pytest.mark.parametrize("outputs", [False, True])
+@pytest.mark.parametrize("here", ["none", "small", "enough"])
+@pytest.mark.parametrize("there", ["none", "small", "enough"])
+def test_streams_never_share_scratch(pkv, there, here, outputs):
+    """A call on a stream of the caller's and one on the current stream may run
+    at once, whatever each brings."""
+    a = scratch(pkv, SIDE, there, outputs)
+    b = scratch(pkv, None, here, outputs)
+    assert a.data_ptr() != b.data_ptr()
+    # each stream's own is kept, and is the same whichever way the stream is named
+    if there != "enough":
+        assert scratch(pkv, SIDE, "small", True) is a
+        pkv.now[0] = SIDE.cuda_stream
+        assert scratch(pkv, None, "none", outputs) is a
+
+
+@pytest.mark.parametrize("brings", ["none", "small"])
+@pytest.mark.parametrize("outputs", [False, True])
+def test_a_capture_on_a_side_stream_gets_scratch_of_its_own(pkv, brings, outputs):
+    kept = [scratch(pkv), scratch(pkv, SIDE)]
+    pkv.capturing.add(SIDE.cuda_stream)
+    a, b = (scratch(pkv, SIDE, brings, outputs) for _ in range(2))
+    assert len({t.data_ptr() for t in (a, b, *kept)}) == 4
+    pkv.capturing.clear()
+    assert scratch(pkv) is kept[0] and scratch(pkv, SIDE) is kept[1]
+
+
+def test_scratch_grows_on_its_own_stream(pkv):
+    main, side = scratch(pkv), scratch(pkv, SIDE)
+    more = scratch(pkv, SIDE, "small", True, need=2 * NEED)
+    assert more is not side and scratch(pkv, SIDE) is more
+    assert scratch(pkv) is main
