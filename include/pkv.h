@@ -566,9 +566,11 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  * out [num_tokens][num_q_heads][head_dim_v] bf16, lse [num_tokens][num_q_heads]
  * fp32 (or NULL: not wanted).  scale > 0 and finite; window >= 0 (0: none);
  * sink_tokens >= 0 (without a window it changes nothing).  Probabilities are
- * rounded to bf16 for the value product (E4M3 caches: to fp16, and the query to
- * two E4M3 terms, 2^-8 relative and 2^-17 of its row's largest); sums and
- * statistics are fp32, out is rounded once.  Values of magnitude 2^80 and
+ * rounded to bf16 for the value product; sums and statistics are fp32, out is
+ * rounded once.  E4M3 caches: the query goes as two E4M3 terms (2^-8 relative and
+ * 2^-17 of its row's largest), probabilities to fp16: 2^-12 relative, or 2^-33 of
+ * the row's largest if that is more, so a key 22.9 or more below the row's largest
+ * s_j counts in the sum of probabilities only.  Values of magnitude 2^80 and
  * above may overflow the sums.
  *  - Rows of q outside [cu_q_lens[0], cu_q_lens[batch]) are padding: their out
  *    and lse are left as they were.

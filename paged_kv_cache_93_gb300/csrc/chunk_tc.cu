@@ -100,8 +100,13 @@ struct Cfg {
     static constexpr uint32_t kSmem = 1024 + kOffWide + (E4 ? 2 * kWide : 0);
     // The sum of 64 probabilities past which a row's reference rises.  bf16: far
     // below overflow of the sums over 2^30 keys and of products with values up to
-    // 2^80.  fp16: none of them reaches 65,504.
-    static constexpr float kMost = E4 ? 16384.f : 1048576.f;
+    // 2^80.  fp16: none of them passes 65,504, its largest number.
+    static constexpr float kMost = E4 ? 65504.f : 1048576.f;
+    // Probabilities are taken 2^kLift times as large as against the reference.  fp16
+    // steps by 2^-24 at the least, so one loses bits from 2^-14 and vanishes at 2^-25;
+    // with a lift of 8 that is 2^-22 (15.2 nats) and 2^-33 (22.9) of the row's
+    // largest, and 64 that equal it add up to 2^14, below kMost.
+    static constexpr float kLift = E4 ? 8.f : 0.f;
     static constexpr uint32_t kIdS = E4 ? tc::idesc_e4m3_f32(kRows, kKeys, 0, 0)
                                         : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
     static constexpr uint32_t kIdO = E4 ? tc::idesc_f16_f32(kRows, D, 0, 1)
@@ -1309,8 +1314,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
                 // ---- probabilities, rounded to 16 bits over S's columns, 64 keys at a
                 // time, against the row's reference m.  m need not be the maximum: a
-                // number with a full exponent holds 2^(score - m) as exactly whatever m
-                // is, short of overflow.  So they are taken against the first maximum,
+                // number with a full exponent (bf16's) holds 2^(score - m) as exactly
+                // whatever m is, short of overflow; for fp16 they are lifted as far as
+                // its range allows.  So they are taken against the first maximum,
                 // and the reference rises only when the sum of a row's 64 passes kMost;
                 // they are then taken again.  A loop, not unrolled: the code of one part
                 // stays in the instruction cache beside the issuing thread's.
@@ -1353,7 +1359,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                     float total;
                     for (bool again = false;; again = true) {
-                        const float neg = m == -INFINITY ? 0.f : -m * sc;
+                        const float neg = m == -INFINITY ? 0.f : fmaf(-m, sc, C::kLift);
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
                         exponentials<E4>(x, sc, neg, sum, t);
                         total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -1411,7 +1417,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const float nan = __int_as_float(0x7fc00000);
             float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             if constexpr (E4) inv *= a.v_scale[g];
-            float lse = l > 0.f || l != l ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
+            float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kLift)) * kLn2 : -INFINITY;
             if (!ok) inv = lse = nan;
             ring += ord.total(r.na);
             const int tok = (r.split ? 0 : h * tpt) + tok_row;

@@ -29,3 +29,42 @@ def test_small_workspaces_on_two_streams(pkv):  # noqa: F811
     torch.cuda.synchronize()
     for (out, _), w in zip(outs, want):
         assert torch.equal(out, w)
+
+
+def weigh(case, out, lse, vanish):
+    """out and lse against the definition, element by element: the bounds of
+    _chunk.check with `vanish` the most that a probability however small is off
+    by, as a part of its row's largest."""
+    ref, ref_lse, absv, mag, low, qlow = _chunk.reference(case)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    score = (case.q.shape[2] + 2) * 2.0 ** -24 * mag + 2.0 ** -17 + 2.0 ** -17 * qlow
+    assert torch.all((lse - ref_lse).abs() <= score)
+    tol = (2.0 ** -11 + 2 * score[..., None]) * absv + 2.0 ** -8 * ref.abs() + vanish * low
+    d = (out - ref).abs()
+    assert torch.all(d <= tol), float((d / tol).max())
+
+
+@pytest.mark.parametrize("gap", [12, 14, 16, 18, 20])
+@pytest.mark.parametrize("first", [0, 300])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (500, 320)])
+def test_fp8_long_tail_behind_one_key(pkv, gap, first, window, sinks):  # noqa: F811
+    """One key, whose value is 0, takes nearly all of every row: what comes out is
+    what the keys `gap` nats below it give.  Their probabilities are fp16 numbers
+    2^8 times as large as against the row's largest, off by half a step of 2^-24
+    at most: 2^-33 of the largest.  (Against a reference that the largest equals
+    they would be off by 2^-25 of it, and vanish 17.4 nats below.)"""
+    case = _chunk.make(63, [(1000, 40), (3000, 1)], 8, 2, 128, 16, window=window, sinks=sinks,
+                       e4m3=True)
+    top = 448 * case.k_scale.double()
+    case.k_pool[..., 0] = 0
+    for b in range(2):
+        rows = (case.tables[b, first // 16].long(), slice(None), first % 16)
+        case.k_pool[rows] = 0
+        case.k_pool[rows[0], :, rows[2], 0] = 0x7e          # 448
+        case.v_pool[rows] = 0
+    for h in range(8):
+        case.q[:, h, 0] = gap / case.scale / top[h // 4]
+    out, lse = _chunk.run(pkv, case)
+    torch.cuda.synchronize()
+    assert pkv.device_status(reset=True) == 0
+    weigh(case, out, lse, 2.0 ** -33)
