@@ -1245,6 +1245,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const int e = min(126, max(-118, int(__float_as_uint(big) >> 23) - 127));
                     const float up = __uint_as_float(uint32_t(134 - e) << 23);
                     sc *= __uint_as_float(uint32_t(120 + e) << 23);
+                    // Masked scores are -inf, and -inf * 0 a NaN: rows of zeros or of the
+                    // smallest numbers over a small key scale must not lose sc.  (Scores
+                    // stay below 2^25, so at the smallest normal number all are 0.)
+                    if (sc < 1.17549435e-38f) sc = 1.17549435e-38f;
                     if (!finite) sc = __int_as_float(0x7fc00000);       // inf or NaN: a NaN row
                     if (ok && (h == 0 || !r.split)) {
                         uint8_t *q0 = base + C::kOffQ + h * C::kQTile + row * 128;

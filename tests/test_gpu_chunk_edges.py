@@ -68,3 +68,18 @@ def test_fp8_long_tail_behind_one_key(pkv, gap, first, window, sinks):  # noqa: 
     torch.cuda.synchronize()
     assert pkv.device_status(reset=True) == 0
     weigh(case, out, lse, 2.0 ** -33)
+
+
+@pytest.mark.parametrize("k_scale", [1e-2, 1e-8, 1e-30])
+def test_fp8_small_queries_over_small_keys(pkv, k_scale):  # noqa: F811
+    """Rows of zeros and of the smallest numbers over a head with a small scale:
+    all scores are 0 in binary32, the rows are the mean of the values they see."""
+    case = _chunk.make(64, [(300, 20), (0, 9)], 8, 2, 128, 16, e4m3=True)
+    case.k_scale[:] = k_scale
+    case.q[::3] = 0
+    case.q[1::3] *= 2.0 ** -120
+    out, lse = _chunk.run(pkv, case)
+    torch.cuda.synchronize()
+    assert pkv.device_status(reset=True) == 0
+    _chunk.check(case, out, lse)
+    weigh(case, out, lse, 2.0 ** -24)
