@@ -188,7 +188,7 @@ int pkv_copy_blocks_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool
  *                              x2 cos(angle) + x1 sin(angle))
  * where (x1, x2) are elements i and i + rotary_dim / 2 of the part (half
  * layout, the default), or 2i and 2i + 1 (PKV_ROPE_INTERLEAVED).  The other
- * elements pass through.  Every query head of q [T][num_q_heads][head_dim_k]
+ * elements pass through (bf16 to bf16 bit by bit, as the values do).  Every query head of q [T][num_q_heads][head_dim_k]
  * (bf16) goes to q_out (bf16, which may be q itself; fp32 with
  * PKV_ROPE_Q_FP32, as the decode calls take it); every rotated key row of
  * k_new and every (unrotated) value row of v_new goes to the token's slot of

@@ -65,11 +65,17 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
     f[6] = bf16_lo_to_f32(u.w); f[7] = bf16_hi_to_f32(u.w);
 }
 
-// 8 values to elements `at`..`at`+7 (at a multiple of 8) as bf16, fp32 or codes.
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+// 8 elements to `at`..`at`+7 (at a multiple of 8) as bf16, fp32 or codes; bf16 ones that
+// are only copied go as the bytes they came in, so that a NaN keeps its bits.
+__device__ __forceinline__ void store8_raw(void *p, int64_t at, const uint4 &x) {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = x;
+}
 __device__ __forceinline__ void store8_bf16(void *p, int64_t at, const float (&f)[8]) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) =
-        make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                   pack_bf16x2(f[6], f[7]));
+    store8_raw(p, at, pack8(f));
 }
 __device__ __forceinline__ void store8_f32(void *p, int64_t at, const float (&f)[8]) {
     float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
@@ -174,6 +180,17 @@ rope_append_kernel(const RopeArgs a) {
                     store8_bf16(a.k_pool, dst + e, f);
                 }
             };
+            // elements outside the rotary part
+            auto copy8 = [&](int e) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src + e);
+                if (is_q ? a.q_fp32 != 0 : E4) {
+                    float x[8];
+                    unpack8(v, x);
+                    store8(e, x);
+                } else {
+                    store8_raw(is_q ? a.q_out : a.k_pool, dst + e, v);
+                }
+            };
             auto store1 = [&](int e, float x) {
                 if (is_q) {
                     if (a.q_fp32) static_cast<float *>(a.q_out)[dst + e] = x;
@@ -207,26 +224,23 @@ rope_append_kernel(const RopeArgs a) {
                 } else if (!(is_q && a.in_place)) {
                     int e = (c - nr) * 8;
                     if (e >= a.off) e += a.rot;
-                    float x[8];
-                    unpack8(*reinterpret_cast<const uint4 *>(src + e), x);
-                    store8(e, x);
+                    copy8(e);
                 }
             } else if constexpr (VEC) {
                 const int e = c * 8;
-                const bool turned = e >= a.off && e < a.off + a.rot;
-                if (turned || !(is_q && a.in_place)) {
+                if (e >= a.off && e < a.off + a.rot) {
                     float x[8];
                     unpack8(*reinterpret_cast<const uint4 *>(src + e), x);
-                    if (turned) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 r = tab[((e - a.off) >> 1) + i];
-                            const float p = x[2 * i], s = x[2 * i + 1];
-                            x[2 * i] = p * r.x - s * r.y;
-                            x[2 * i + 1] = s * r.x + p * r.y;
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 r = tab[((e - a.off) >> 1) + i];
+                        const float p = x[2 * i], s = x[2 * i + 1];
+                        x[2 * i] = p * r.x - s * r.y;
+                        x[2 * i + 1] = s * r.x + p * r.y;
                     }
                     store8(e, x);
+                } else if (!(is_q && a.in_place)) {
+                    copy8(e);
                 }
             } else {
                 // units: rot / 2 pairs, then the elements outside
@@ -240,7 +254,10 @@ rope_append_kernel(const RopeArgs a) {
                 } else if (!(is_q && a.in_place)) {
                     int e = c - npairs;
                     if (e >= a.off) e += a.rot;
-                    store1(e, __uint_as_float(uint32_t(src[e]) << 16));
+                    if (is_q ? a.q_fp32 != 0 : E4)
+                        store1(e, __uint_as_float(uint32_t(src[e]) << 16));
+                    else
+                        static_cast<uint16_t *>(is_q ? a.q_out : a.k_pool)[dst + e] = src[e];
                 }
             }
         }
@@ -256,7 +273,7 @@ rope_append_kernel(const RopeArgs a) {
 // instructions, not the bytes, are what a simpler mapping was bound by.  A CTA takes
 // `group` tokens, or 1 / parts of one with many heads, at a time; kAhead units of
 // the next rows are loaded while the last ones are turned and stored (1,024 latent
-// tokens of 128 heads of 576: 61 us, 5.0 TB/s).
+// tokens of 128 heads of 576: 60.5 us, 5.0 TB/s).
 constexpr int kAhead = 2;
 constexpr int kWideCtas = 3;             // per SM
 constexpr int kItemUnits = 2048;         // units of a work item, about
@@ -325,70 +342,75 @@ rope_append_wide_kernel(const RopeArgs a) {
             va = *reinterpret_cast<const uint4 *>(src + e0);
             vb = *reinterpret_cast<const uint4 *>(src + e1);
         };
-        auto finish = [&](int row, const uint4 &va, const uint4 &vb) {
+        auto turn_unit = [&](int tk, float (&x)[8], float (&y)[8]) {
+            const float4 *r =
+                reinterpret_cast<const float4 *>(cs[buf] + tk * npairs) + unit;
+            if constexpr (INTER) {
+                auto turn = [](float (&v)[8], int i, const float4 &q) {
+                    float p = v[4 * i], s = v[4 * i + 1];
+                    v[4 * i] = p * q.x - s * q.y;
+                    v[4 * i + 1] = s * q.x + p * q.y;
+                    p = v[4 * i + 2], s = v[4 * i + 3];
+                    v[4 * i + 2] = p * q.z - s * q.w;
+                    v[4 * i + 3] = s * q.z + p * q.w;
+                };
+                turn(x, 0, r[0]);
+                turn(x, 1, r[nr]);
+                turn(y, 0, r[2 * nr]);
+                turn(y, 1, r[3 * nr]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 q = r[i * nr];
+                    float p = x[2 * i], s = y[2 * i];
+                    x[2 * i] = p * q.x - s * q.y;
+                    y[2 * i] = s * q.x + p * q.y;
+                    p = x[2 * i + 1], s = y[2 * i + 1];
+                    x[2 * i + 1] = p * q.z - s * q.w;
+                    y[2 * i + 1] = s * q.z + p * q.w;
+                }
+            }
+        };
+        auto finish = [&](int row, uint4 va, uint4 vb) {
             if (!works || row >= end) return;
             const int tk = a.group > 1 ? fast_div(row, a.tok_magic, rows_tok) : 0;
             row -= tk * rows_tok;
             const int64_t slot = s_slot[buf][tk];
             const bool is_q = row < a.hq;
             if (is_q ? !s_live[buf][tk] || (a.in_place && !turned) : slot < 0) return;
+            const bool is_k = !is_q && row < rows_qk;
+            if (!is_q && !is_k && 16 * c >= a.dv) return;
+            const int g = is_k ? row - a.hq : row - rows_qk, d = is_k ? a.dk : a.dv;
+            const int e0 = is_q || is_k ? ea : 16 * c, e1 = is_q || is_k ? eb : 16 * c + 8;
+            // s_slot holds the row of KV head 0
+            const int64_t dst = is_q ? ((t0 + tk) * a.hq + row) * a.dk
+                                     : (slot + int64_t(g) * a.block_size) * d;
+            if (is_q ? !a.q_fp32 : !E4) {
+                // to bf16: copied elements as they came
+                if (turned && (is_q || is_k)) {
+                    float x[8], y[8];
+                    unpack8(va, x);
+                    unpack8(vb, y);
+                    turn_unit(tk, x, y);
+                    va = pack8(x);
+                    vb = pack8(y);
+                }
+                void *to = is_q ? a.q_out : is_k ? a.k_pool : a.v_pool;
+                store8_raw(to, dst + e0, va);
+                store8_raw(to, dst + e1, vb);
+                return;
+            }
             float x[8], y[8];
             unpack8(va, x);
             unpack8(vb, y);
-            if (turned && row < rows_qk) {
-                const float4 *r =
-                    reinterpret_cast<const float4 *>(cs[buf] + tk * npairs) + unit;
-                if constexpr (INTER) {
-                    auto turn = [](float (&v)[8], int i, const float4 &q) {
-                        float p = v[4 * i], s = v[4 * i + 1];
-                        v[4 * i] = p * q.x - s * q.y;
-                        v[4 * i + 1] = s * q.x + p * q.y;
-                        p = v[4 * i + 2], s = v[4 * i + 3];
-                        v[4 * i + 2] = p * q.z - s * q.w;
-                        v[4 * i + 3] = s * q.z + p * q.w;
-                    };
-                    turn(x, 0, r[0]);
-                    turn(x, 1, r[nr]);
-                    turn(y, 0, r[2 * nr]);
-                    turn(y, 1, r[3 * nr]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float4 q = r[i * nr];
-                        float p = x[2 * i], s = y[2 * i];
-                        x[2 * i] = p * q.x - s * q.y;
-                        y[2 * i] = s * q.x + p * q.y;
-                        p = x[2 * i + 1], s = y[2 * i + 1];
-                        x[2 * i + 1] = p * q.z - s * q.w;
-                        y[2 * i + 1] = s * q.z + p * q.w;
-                    }
-                }
-            }
+            if (turned && (is_q || is_k)) turn_unit(tk, x, y);
             if (is_q) {
-                const int64_t dst = ((t0 + tk) * a.hq + row) * a.dk;
-                if (a.q_fp32) {
-                    store8_f32(a.q_out, dst + ea, x);
-                    store8_f32(a.q_out, dst + eb, y);
-                } else {
-                    store8_bf16(a.q_out, dst + ea, x);
-                    store8_bf16(a.q_out, dst + eb, y);
-                }
-                return;
-            }
-            const bool is_k = row < rows_qk;
-            const int g = is_k ? row - a.hq : row - rows_qk, d = is_k ? a.dk : a.dv;
-            if (!is_k && 16 * c >= a.dv) return;
-            const int e0 = is_k ? ea : 16 * c, e1 = is_k ? eb : 16 * c + 8;
-            void *pool = is_k ? a.k_pool : a.v_pool;
-            // s_slot holds the row of KV head 0
-            const int64_t dst = (slot + int64_t(g) * a.block_size) * d;
-            if constexpr (E4) {
-                const float s = (is_k ? a.k_scale : a.v_scale)[g];
-                store8_e4m3(pool, dst + e0, x, s);
-                store8_e4m3(pool, dst + e1, y, s);
+                store8_f32(a.q_out, dst + e0, x);
+                store8_f32(a.q_out, dst + e1, y);
             } else {
-                store8_bf16(pool, dst + e0, x);
-                store8_bf16(pool, dst + e1, y);
+                const float s = (is_k ? a.k_scale : a.v_scale)[g];
+                store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + e0, x, s);
+                store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + e1, y, s);
             }
         };
         uint4 va[2][kAhead], vb[2][kAhead];
@@ -440,14 +462,15 @@ rope_append_wide_kernel(const RopeArgs a) {
 // of its `parts`: 32 / U rows at a time (U = head_dim / 16 units a row), each lane the
 // same unit of every row, with the cosines and sines of its eight pairs in
 // registers -- two pairs a lane are computed, then handed round by shuffles -- so
-// that rows need neither table nor barrier, and the rows AHEAD passes on are on
-// their way.  Many tokens: 4 ahead on two CTAs an SM (8,191 tokens of 32 + 8 heads
-// of 128: 36.9 us, 5.5 TB/s, against 41.3 us for 2 ahead on three CTAs); a few
-// thousand: 2 ahead on three CTAs, whose warps take all of them at once (2,500
-// tokens into an FP8 cache: 25.6 us against 30.3 us).
+// that rows need neither table nor barrier, and the rows kWarpAhead passes on are
+// on their way (8,191 tokens of 32 + 8 heads of 128: 36.9 us, 5.5 TB/s, against 37.7
+// for 4 ahead on two CTAs an SM; 2,500 tokens of 64 + 8 heads into an FP8 cache:
+// 24.8 us against 35.7).
+constexpr int kWarpAhead = 2;
+constexpr int kWarpCtas = 3;             // per SM
 
-template <bool INTER, bool E4, int AHEAD, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS)
+template <bool INTER, bool E4>
+__global__ void __launch_bounds__(kThreads, kWarpCtas)
 rope_append_warp_kernel(const RopeArgs a) {
     pdl_wait();
     pdl_launch_dependents();
@@ -482,7 +505,7 @@ rope_append_warp_kernel(const RopeArgs a) {
         const int begin = a.parts > 1 ? int(w - t * a.parts) * per : 0;
         const int end = min(passes, begin + per);
         const int64_t pos = a.positions[t], slot = a.slots[t];
-        uint4 va[AHEAD], vb[AHEAD];
+        uint4 va[kWarpAhead], vb[kWarpAhead];
         // pass p: rows of queries, keys, then values
         auto load = [&](int p, uint4 &x, uint4 &y) {
             if (p >= end) return;
@@ -509,7 +532,7 @@ rope_append_warp_kernel(const RopeArgs a) {
         };
         if (pos < 0) continue;                       // padding (the whole warp)
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) load(begin + k, va[k], vb[k]);
+        for (int k = 0; k < kWarpAhead; ++k) load(begin + k, va[k], vb[k]);
         // ---- the angles
         float co[8], si[8];
         {
@@ -537,63 +560,67 @@ rope_append_warp_kernel(const RopeArgs a) {
         const bool stored = slot >= 0 && slot < a.num_slots;
         const int64_t block = stored ? slot / a.block_size : 0;
         const int64_t row0 = block * a.hkv * a.block_size + (stored ? slot - block * a.block_size : 0);
-        auto finish = [&](int p, const uint4 &va, const uint4 &vb) {
+        auto turn = [&](float (&x)[8], float (&y)[8]) {
+            if constexpr (INTER) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p0 = x[2 * i], s0 = x[2 * i + 1];
+                    x[2 * i] = p0 * co[i] - s0 * si[i];
+                    x[2 * i + 1] = s0 * co[i] + p0 * si[i];
+                    const float p1 = y[2 * i], s1 = y[2 * i + 1];
+                    y[2 * i] = p1 * co[4 + i] - s1 * si[4 + i];
+                    y[2 * i + 1] = s1 * co[4 + i] + p1 * si[4 + i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p0 = x[i], s0 = y[i];
+                    x[i] = p0 * co[i] - s0 * si[i];
+                    y[i] = s0 * co[i] + p0 * si[i];
+                }
+            }
+        };
+        auto finish = [&](int p, uint4 va, uint4 vb) {
             if (p >= end) return;
             const bool is_q = p < pq, is_k = !is_q && p < pq + pk;
             const int row = ((p - (is_q ? 0 : is_k ? pq : pq + pk)) << (5 - shift)) + r0;
             if (row >= (is_q ? a.hq : a.hkv)) return;
             if (is_q ? a.in_place && !turned : !stored) return;
+            const int64_t dst =
+                (is_q ? t * a.hq + row : row0 + int64_t(row) * a.block_size) * a.dk;
+            if (is_q ? !a.q_fp32 : !E4) {
+                // to bf16: copied elements as they came
+                if (turned && (is_q || is_k)) {
+                    float x[8], y[8];
+                    unpack8(va, x);
+                    unpack8(vb, y);
+                    turn(x, y);
+                    va = pack8(x);
+                    vb = pack8(y);
+                }
+                void *to = is_q ? a.q_out : is_k ? a.k_pool : a.v_pool;
+                store8_raw(to, dst + (is_q || is_k ? ea : 16 * c), va);
+                store8_raw(to, dst + (is_q || is_k ? eb : 16 * c + 8), vb);
+                return;
+            }
             float x[8], y[8];
             unpack8(va, x);
             unpack8(vb, y);
-            if (turned && (is_q || is_k)) {
-                if constexpr (INTER) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = x[2 * i], s0 = x[2 * i + 1];
-                        x[2 * i] = p0 * co[i] - s0 * si[i];
-                        x[2 * i + 1] = s0 * co[i] + p0 * si[i];
-                        const float p1 = y[2 * i], s1 = y[2 * i + 1];
-                        y[2 * i] = p1 * co[4 + i] - s1 * si[4 + i];
-                        y[2 * i + 1] = s1 * co[4 + i] + p1 * si[4 + i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p0 = x[i], s0 = y[i];
-                        x[i] = p0 * co[i] - s0 * si[i];
-                        y[i] = s0 * co[i] + p0 * si[i];
-                    }
-                }
-            }
+            if (turned && (is_q || is_k)) turn(x, y);
             if (is_q) {
-                const int64_t dst = (t * a.hq + row) * a.dk;
-                if (a.q_fp32) {
-                    store8_f32(a.q_out, dst + ea, x);
-                    store8_f32(a.q_out, dst + eb, y);
-                } else {
-                    store8_bf16(a.q_out, dst + ea, x);
-                    store8_bf16(a.q_out, dst + eb, y);
-                }
-                return;
-            }
-            const int e0 = is_k ? ea : 16 * c, e1 = is_k ? eb : 16 * c + 8;
-            void *pool = is_k ? a.k_pool : a.v_pool;
-            const int64_t dst = (row0 + int64_t(row) * a.block_size) * a.dk;
-            if constexpr (E4) {
-                const float s = (is_k ? a.k_scale : a.v_scale)[row];
-                store8_e4m3(pool, dst + e0, x, s);
-                store8_e4m3(pool, dst + e1, y, s);
+                store8_f32(a.q_out, dst + ea, x);
+                store8_f32(a.q_out, dst + eb, y);
             } else {
-                store8_bf16(pool, dst + e0, x);
-                store8_bf16(pool, dst + e1, y);
+                const float s = (is_k ? a.k_scale : a.v_scale)[row];
+                store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + (is_k ? ea : 16 * c), x, s);
+                store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + (is_k ? eb : 16 * c + 8), y, s);
             }
         };
-        for (int p = begin; p < end; p += AHEAD)
+        for (int p = begin; p < end; p += kWarpAhead)
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
+            for (int k = 0; k < kWarpAhead; ++k) {
                 const uint4 x = va[k], y = vb[k];
-                load(p + AHEAD + k, va[k], vb[k]);
+                load(p + kWarpAhead + k, va[k], vb[k]);
                 finish(p + k, x, y);
             }
     }
@@ -601,13 +628,13 @@ rope_append_warp_kernel(const RopeArgs a) {
 
 uint32_t magic_of(int n) { return n > 1 ? uint32_t(((uint64_t(1) << 32) + n - 1) / n) : 0; }
 
-template <bool E4, int AHEAD, int CTAS>
+template <bool E4>
 int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     // Parts of a token: the fewest rounds of warps x (passes of a part + 2 for its
     // angles), so that few tokens spread over the device and the last round of
     // many is not mostly empty.
     constexpr int per_cta = kThreads / 32;
-    const int64_t warps = int64_t(sm_count()) * CTAS * per_cta;
+    const int64_t warps = int64_t(sm_count()) * kWarpCtas * per_cta;
     const int rpp = 32 / a.q_units;
     const int passes = (a.hq + rpp - 1) / rpp + (a.dv ? 2 : 1) * ((a.hkv + rpp - 1) / rpp);
     a.parts = 1;
@@ -622,9 +649,9 @@ int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     }
     const int64_t items = a.num_tokens * a.parts;
     const dim3 grid(unsigned(std::min<int64_t>((items + per_cta - 1) / per_cta,
-                                               int64_t(sm_count()) * CTAS)));
-    return launch_pdl(interleaved ? rope_append_warp_kernel<true, E4, AHEAD, CTAS>
-                                  : rope_append_warp_kernel<false, E4, AHEAD, CTAS>,
+                                               int64_t(sm_count()) * kWarpCtas)));
+    return launch_pdl(interleaved ? rope_append_warp_kernel<true, E4>
+                                  : rope_append_warp_kernel<false, E4>,
                       grid, dim3(kThreads), 0, stream, a);
 }
 
@@ -636,9 +663,7 @@ int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     if (a.dk % 64 == 0 && (units & (units - 1)) == 0 && units <= 32 &&
         (a.dv == 0 || a.dv == a.dk) && a.rot % 16 == 0 && a.off % 16 == 0 && a.rot <= 128) {
         a.q_units = units;
-        // (more tokens than twice the warps that are resident with two CTAs an SM)
-        return a.num_tokens > int64_t(sm_count()) * 32 ? launch_warp<E4, 4, 2>(a, interleaved, stream)
-                                                       : launch_warp<E4, 2, 3>(a, interleaved, stream);
+        return launch_warp<E4>(a, interleaved, stream);
     }
     if (a.dk % 16 == 0 && a.dv % 16 == 0 && a.dv <= a.dk && a.rot % 16 == 0 && a.off % 16 == 0) {
         a.q_units = a.dk / 16;
