@@ -55,7 +55,6 @@
 #include <algorithm>
 #include <mutex>
 
-#include "chunk_merge_units.h"
 #include "pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
@@ -1502,30 +1501,30 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
     // the split items taken whole (two partials of at most kRows rows each), then the cuts
     constexpr int kUnits = 2 * kRows / kMergeRows;
     const int32_t n_short = plan.header[kHdrSplit] * hkv;
-    const int32_t units = (plan.header[kHdrSplitRows] + kMergeRows - 1) / kMergeRows;
+    const int32_t n_half =
+        n_short * ((plan.header[kHdrSplitRows] + kMergeRows - 1) / kMergeRows);
+    const int32_t total = n_half + plan.header[kHdrCuts] * kUnits;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
     const int nblocks = plan.header[kHdrBlocks];
     const int32_t idx0 = plan.header[kHdrRounds] * plan.ctas;
     const float4 *op = reinterpret_cast<const float4 *>(plan.o_part) + c;
     constexpr int kWarps = kMergeThreads / 32;
-    MergeWalk w(blockIdx.x * kWarps + (threadIdx.x >> 5), gridDim.x * kWarps, n_short, units,
-                plan.header[kHdrCuts] * kUnits);
-    for (; !w.done(); w.next()) {
+    for (int32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < total; w += gridDim.x * kWarps) {
         int blk, g, row0, count, halves = 2;
         int64_t first, next;                 // rows of the first piece, and of the others'
-        const bool halved = w.in_entries();
-        if (halved) {
-            row0 = w.unit * kMergeRows;
-            blk = plan.split[w.entry / hkv];
-            g = w.entry % hkv;
+        if (w < n_half) {
+            // (unit-major, so that the units past a short item's rows end up in other warps)
+            const int32_t unit = w / n_short, sg = w - unit * n_short;
+            row0 = unit * kMergeRows;
+            blk = plan.split[sg / hkv];
+            g = sg % hkv;
             count = 2;
             first = next = 0;
         } else {
-            const int32_t u = w.piece();
-            const Cut cut = plan.cuts[u / kUnits];
+            const Cut cut = plan.cuts[(w - n_half) / kUnits];
             blk = cut.block;
             g = cut.g;
-            row0 = u % kUnits * kMergeRows;
+            row0 = (w - n_half) % kUnits * kMergeRows;
             count = 1 + cut.more;
             first = int64_t(plan.ctas + cut.cta) * plan.slot_rows;
             next = int64_t(cut.cta) * plan.slot_rows;
@@ -1533,7 +1532,7 @@ chunk_merge_kernel(const ChunkArgs a, const Plan plan, const Shape sh) {
         const Block m = plan.blocks[blk];
         const int rows = m.ntok * G;
         if (row0 >= rows) continue;
-        if (halved) {
+        if (w < n_half) {
             const int32_t idx = plan.header[kHdrByHead] ? g * nblocks + blk : blk * hkv + g;
             if (idx >= idx0 && plan.is_cut[idx - idx0]) continue;
             first = next = m.prow + int64_t(g) * 2 * rows;
