@@ -73,6 +73,12 @@ constexpr uint32_t kColO = 256;          // O_A, O_B; S_A, S_B at 0 and 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// E4M3 caches: probabilities are taken 2^kLift times as large as against the reference.
+// fp16 steps by 2^-24 at the least, so one loses bits from 2^-14 and vanishes at 2^-25;
+// with a lift of 8 that is 2^-22 (15.2 nats) and 2^-33 (22.9) of the row's largest, and
+// 64 that equal it add up to 2^14, below kMost.
+constexpr float kLift = 8.f;
+
 template <int D, bool E4>
 struct Cfg {
     static_assert(D == 64 || D == 128, "head dims of one or two 128-byte column blocks");
@@ -102,11 +108,6 @@ struct Cfg {
     // below overflow of the sums over 2^30 keys and of products with values up to
     // 2^80.  fp16: none of them passes 65,504, its largest number.
     static constexpr float kMost = E4 ? 65504.f : 1048576.f;
-    // Probabilities are taken 2^kLift times as large as against the reference.  fp16
-    // steps by 2^-24 at the least, so one loses bits from 2^-14 and vanishes at 2^-25;
-    // with a lift of 8 that is 2^-22 (15.2 nats) and 2^-33 (22.9) of the row's
-    // largest, and 64 that equal it add up to 2^14, below kMost.
-    static constexpr float kLift = E4 ? 8.f : 0.f;
     static constexpr uint32_t kIdS = E4 ? tc::idesc_e4m3_f32(kRows, kKeys, 0, 0)
                                         : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
     static constexpr uint32_t kIdO = E4 ? tc::idesc_f16_f32(kRows, D, 0, 1)
@@ -1363,7 +1364,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     }
                     float total;
                     for (bool again = false;; again = true) {
-                        const float neg = m == -INFINITY ? 0.f : fmaf(-m, sc, C::kLift);
+                        float neg;
+                        if constexpr (E4) neg = m == -INFINITY ? 0.f : fmaf(-m, sc, kLift);
+                        else neg = m == -INFINITY ? 0.f : -m * sc;
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
                         exponentials<E4>(x, sc, neg, sum, t);
                         total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -1421,7 +1424,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const float nan = __int_as_float(0x7fc00000);
             float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             if constexpr (E4) inv *= a.v_scale[g];
-            float lse = l > 0.f || l != l ? (m * sc + (log2f(l) - C::kLift)) * kLn2 : -INFINITY;
+            float lse = l > 0.f || l != l ? (m * sc + log2f(l)) * kLn2 : -INFINITY;
+            if constexpr (E4) lse -= kLift * kLn2;
             if (!ok) inv = lse = nan;
             ring += ord.total(r.na);
             const int tok = (r.split ? 0 : h * tpt) + tok_row;
