@@ -589,7 +589,8 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  *  - v_pool NULL: values inside the keys, as pkv_paged_decode_attn.
  * Head dims 64 or 128 (equal for K and V), query groups up to 128 and
  * power-of-two block sizes 8..256 (E4M3: head dim 128, 16..256) run on the
- * tcgen05 tensor cores; other shapes (head dims multiples of 8 up to 1024),
+ * tcgen05 tensor cores while min(batch, num_tokens) * num_kv_heads <= 2^26 - 2048;
+ * other shapes (head dims multiples of 8 up to 1024),
  * and flags PKV_DECODE_GENERIC or PKV_DECODE_NO_TCGEN05, on CUDA cores.
  * workspace: at least pkv_chunk_workspace_size(...) bytes (0: may be NULL),
  * 16-byte aligned, contents on entry do not matter; calls that may overlap

@@ -11,10 +11,15 @@
 namespace pkv {
 namespace {
 
+// (sequence, KV head) pairs up to which the merge counts its pieces in 32 bits: 32 of each
+// (128 rows, 4 a piece), 64 of each of the 256 cuts at most, and the grid's stride.
+constexpr int64_t kMostPairs = (int64_t(1) << 26) - 2048;
+
 // Whether a call of this shape runs on the tensor cores.
-bool on_tensor_cores(const pkv_cache_desc &c, int32_t hq, int32_t max_blocks, int32_t flags,
-                     bool e4, bool values_in_keys) {
-    return flags == 0 && !values_in_keys && chunk_tc_supports(c, hq, max_blocks, e4);
+bool on_tensor_cores(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32_t hq,
+                     int32_t max_blocks, int32_t flags, bool e4, bool values_in_keys) {
+    return flags == 0 && !values_in_keys && chunk_tc_supports(c, hq, max_blocks, e4) &&
+           std::min<int64_t>(num_tokens, batch) * c.num_kv_heads <= kMostPairs;
 }
 
 size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch, int32_t hq,
@@ -22,7 +27,7 @@ size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch
     if (!c || num_tokens <= 0 || batch <= 0 || hq <= 0 || max_blocks < 0 ||
         c->num_kv_heads <= 0 || hq % c->num_kv_heads != 0 || c->num_blocks <= 0 ||
         num_tokens * hq >= (int64_t(1) << 29) ||
-        !on_tensor_cores(*c, hq, max_blocks, flags, e4, false))
+        !on_tensor_cores(*c, num_tokens, batch, hq, max_blocks, flags, e4, false))
         return 0;
     return chunk_tc_workspace(*c, num_tokens, batch, hq);
 }
@@ -30,8 +35,8 @@ size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch
 // Runs a checked call.
 int run(ChunkArgs &a, bool e4, bool values_in_keys, void *workspace, size_t workspace_bytes,
         int32_t flags) {
-    const bool tc = on_tensor_cores(a.cache, a.num_q_heads, a.max_blocks, flags, e4,
-                                    values_in_keys);
+    const bool tc = on_tensor_cores(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks,
+                                    flags, e4, values_in_keys);
     if (tc) {
         const size_t need =
             chunk_tc_workspace(a.cache, a.num_tokens, a.batch, a.num_q_heads);

@@ -93,3 +93,22 @@ def test_scratch_grows_on_its_own_stream(pkv):
     more = scratch(pkv, SIDE, "small", True, need=2 * NEED)
     assert more is not side and scratch(pkv, SIDE) is more
     assert scratch(pkv) is main
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_more_pairs_than_the_merge_counts(built, e4m3):
+    """The tensor-core form numbers 32 pieces of every (sequence, KV head) pair in 32
+    bits; calls of more pairs run on CUDA cores and need no workspace."""
+    import ctypes
+    size = built.lib.pkv_chunk_workspace_size_e4m3 if e4m3 else built.lib.pkv_chunk_workspace_size
+
+    def on_tensor_cores(hkv, batch, tokens):
+        d = built.CacheDesc(1000, 16, hkv, 128, 128)
+        return size(ctypes.byref(d), tokens, batch, hkv, 64, 0) > 0
+    most = ((1 << 31) - 1 - 256 * 64 - 256 * 8 * 8) // 32
+    for hkv in (1, 8, 1023, 1024, 1025, 4096, 8191):
+        batch = min(65535, most // hkv)
+        assert on_tensor_cores(hkv, batch - 2048, batch - 2048)
+        assert on_tensor_cores(hkv, batch, 5)
+        if hkv >= 1025:
+            assert not on_tensor_cores(hkv, batch + 2, batch + 2)
