@@ -16,18 +16,17 @@ constexpr int32_t kMaxSplits = 256;
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // PKV_DECODE_TEST_WITHHOLD is accepted only while a test has enabled it.
 std::atomic<int> g_test_withhold_enabled{0};
-// Pipeline wait limit under that control: long enough for any legitimate
-// stall of a small test case, short enough to keep the test quick.
-constexpr uint64_t kTestWaitNs = 1000000ull;
 }  // namespace
 
 namespace pkv {
+bool test_withhold_enabled() { return g_test_withhold_enabled.load() != 0; }
+
 int validate_decode(const pkv_cache_desc *c, const float *q, int32_t batch, int32_t hq,
                     const void *k_pool, const void *v_pool, const int32_t *block_tables,
                     int32_t max_blocks, const int32_t *seq_lens, int32_t num_splits,
                     int32_t flags) {
     const int32_t known = PKV_DECODE_GENERIC | PKV_DECODE_NO_TCGEN05 |
-                          (g_test_withhold_enabled.load() ? PKV_DECODE_TEST_WITHHOLD : 0);
+                          (test_withhold_enabled() ? PKV_DECODE_TEST_WITHHOLD : 0);
     if (!c || batch < 0 || hq <= 0 || max_blocks < 0 || num_splits < 0 ||
         num_splits > kMaxSplits || (flags & ~known) != 0)
         return PKV_ERR_INVALID_ARG;

@@ -15,10 +15,11 @@ namespace {
 // (128 rows, 4 a piece), 64 of each of the 256 cuts at most, and the grid's stride.
 constexpr int64_t kMostPairs = (int64_t(1) << 26) - 2048;
 
-// Whether a call of this shape runs on the tensor cores.
+// Whether a call of this shape runs on the tensor cores (which alone read the test
+// control).
 bool on_tensor_cores(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32_t hq,
                      int32_t max_blocks, int32_t flags, bool e4, bool values_in_keys) {
-    return flags == 0 && !values_in_keys && chunk_tc_supports(c, hq, max_blocks, e4) &&
+    return (flags & ~PKV_DECODE_TEST_WITHHOLD) == 0 && !values_in_keys && chunk_tc_supports(c, hq, max_blocks, e4) &&
            std::min<int64_t>(num_tokens, batch) * c.num_kv_heads <= kMostPairs;
 }
 
@@ -37,6 +38,8 @@ int run(ChunkArgs &a, bool e4, bool values_in_keys, void *workspace, size_t work
         int32_t flags) {
     const bool tc = on_tensor_cores(a.cache, a.num_tokens, a.batch, a.num_q_heads, a.max_blocks,
                                     flags, e4, values_in_keys);
+    a.withhold = (flags & PKV_DECODE_TEST_WITHHOLD) != 0;
+    if (a.withhold && !tc) return PKV_ERR_INVALID_ARG;
     if (tc) {
         const size_t need =
             chunk_tc_workspace(a.cache, a.num_tokens, a.batch, a.num_q_heads);
@@ -57,9 +60,10 @@ int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64
             const int32_t *seq_lens, float scale, int32_t window, int32_t sink_tokens, void *out,
             float *lse, int32_t flags, cudaStream_t stream, bool *done) {
     *done = false;
+    const int32_t known = PKV_DECODE_GENERIC | PKV_DECODE_NO_TCGEN05 |
+                          (test_withhold_enabled() ? PKV_DECODE_TEST_WITHHOLD : 0);
     if (!c || num_tokens < 0 || batch < 0 || hq <= 0 || max_blocks < 0 || window < 0 ||
-        sink_tokens < 0 || !(scale > 0.f) || !std::isfinite(scale) ||
-        (flags & ~(PKV_DECODE_GENERIC | PKV_DECODE_NO_TCGEN05)) != 0)
+        sink_tokens < 0 || !(scale > 0.f) || !std::isfinite(scale) || (flags & ~known) != 0)
         return PKV_ERR_INVALID_ARG;
     if (c->num_blocks <= 0 || c->block_size < 1 || c->block_size > 256 || c->num_kv_heads <= 0 ||
         c->head_dim_k <= 0 || c->head_dim_v <= 0)

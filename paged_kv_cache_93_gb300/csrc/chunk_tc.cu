@@ -99,6 +99,11 @@ struct Cfg {
     // 1,024); head dim 128, where a tile's way to the tensor cores counts: the
     // softmax warps (8K prompt 388 -> 380 us); E4M3: the warps that widen.
     static constexpr bool kTended = D == 64;
+    // How a warp that gave up keeps from arriving: by a vote a tile, or by a test before
+    // each arrival (8K prompt under a window, head dim 64: 240.5 us against 243.2, and
+    // 241 without either; 8K prompt, head dim 128: 386 against 380, and 380; FP8 chunk:
+    // 439 against 434, and 431).
+    static constexpr bool kEndsItem = D == 64;
     static constexpr uint32_t kWide = kKeys * D * 2;                // a V tile in 16 bits
     static constexpr uint32_t kOffQ = 1024;
     static constexpr uint32_t kOffRing = kOffQ + 2 * kQTile;
@@ -706,13 +711,15 @@ __device__ __forceinline__ void exponentials(const uint32_t *s, float sc, float 
     }
 }
 
-template <int D, bool E4>
+// kWithhold: the test control's form -- no copy is issued, waits are short.
+template <int D, bool E4, bool kWithhold>
 __global__ void __launch_bounds__(Cfg<D, E4>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const ChunkArgs a, const Plan plan,
                 const Shape sh) {
     using C = Cfg<D, E4>;
+    constexpr uint64_t kLimit = kWithhold ? kTestWaitNs : kWaitLimitNs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -795,7 +802,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         uint32_t ring = 0, items_done = 0;
         uint32_t armed = 0, armed_parity = 0;
         uint32_t q_armed = 0, q_parity = 0;
-        bool ok = true;
+        bool ok = !kWithhold;
         for (int it = 0; it < num_items && ok; ++it) {
             const Item r = read_item(it);
             if (r.na == 0) continue;
@@ -831,7 +838,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             auto load = [&](const CUtensorMap *map, int32_t y) -> bool {
                 const uint32_t stage = ring % C::kStages, phase = (ring / C::kStages) & 1u;
                 if (!__all_sync(0xffffffffu, pipe_wait(bar(kBarEmpty + stage), phase ^ 1u,
-                                                       a.status, abort_flag)))
+                                                       a.status, abort_flag, kLimit)))
                     return false;
                 const uint32_t live = __ballot_sync(0xffffffffu, y >= 0);
                 if (lane == 0) {
@@ -859,7 +866,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 if constexpr (!E4) {
                     if (!__all_sync(0xffffffffu,
                                     pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
-                                              abort_flag)))
+                                              abort_flag, kLimit)))
                         return false;
                     if (lane == 0) {
                         const int tiles = r.split ? 1 : 2;
@@ -908,8 +915,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (lane == 0) {
             for (int s = 0; s < C::kStages; ++s)
                 if (armed & (1u << s))
-                    mbar_wait(bar(kBarFull + s), (armed_parity >> s) & 1u, a.status);
-            if (q_armed) mbar_wait(bar(kBarQFull), q_parity, a.status);
+                    mbar_wait(bar(kBarFull + s), (armed_parity >> s) & 1u, a.status, kLimit);
+            if (q_armed) mbar_wait(bar(kBarQFull), q_parity, a.status, kLimit);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -927,7 +934,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             uint32_t wide = 0, wide_lap = 0;     // next buffer of widened values (E4M3)
             bool ok = true;
             auto wait = [&](uint32_t b, uint32_t parity) {
-                return pipe_wait(b, parity, a.status, abort_flag);
+                return pipe_wait(b, parity, a.status, abort_flag, kLimit);
             };
             // the ring entry `off` positions on: its stage, waited for
             auto entry = [&](uint32_t off, uint32_t &stage) {
@@ -1060,7 +1067,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
             }
             tc::commit(bar(kBarDrain));
-            mbar_wait(bar(kBarDrain), 0, a.status);
+            mbar_wait(bar(kBarDrain), 0, a.status, kLimit);
         }
         __syncwarp();
     } else if (C::kTended) {
@@ -1088,7 +1095,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     v = r.nb;
                 }
                 ok = __all_sync(0xffffffffu,
-                                pipe_wait(bar(kBarFull) + 8u * stage, lap, a.status, abort_flag));
+                                pipe_wait(bar(kBarFull) + 8u * stage, lap, a.status, abort_flag,
+                                          kLimit));
                 if (!ok) break;
                 if (v >= 0) {
                     v += r.v0;
@@ -1145,9 +1153,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 // than they were issued in; without that this wait could take the key
                 // tile's phase for this one's.)
                 ok = __all_sync(0xffffffffu,
-                                pipe_wait(bar(kBarWideEmpty + wide), lap, a.status, abort_flag) &&
+                                pipe_wait(bar(kBarWideEmpty + wide), lap, a.status, abort_flag,
+                                          kLimit) &&
                                     pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
-                                              a.status, abort_flag));
+                                              a.status, abort_flag, kLimit));
                 if (!ok) break;
                 const uint8_t *src = base + C::kOffRing + stage * C::kStage + from + hi8 * 8192;
                 uint8_t *dst = base + C::kOffWide + wide * C::kWide + hi8 * 16384;
@@ -1199,6 +1208,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
         // -------------------------------------------- softmax and epilogue
+        // A thread whose wait gave up arrives once more for its tile's phases at most, and
+        // for none after them: its warp takes no further tiles (kEndsItem), or goes through
+        // them without arriving.  Arrivals ahead would stand for those of rows that are
+        // behind, which the tensor cores would then read unwritten, and more than a phase
+        // has pending are a fault.  So no product is issued past it, the others' waits give
+        // up too, and what rows the CTA has not finished become NaN.
         const int h = warp >> 2;                         // half
         const int row = threadIdx.x & 127;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
@@ -1224,7 +1239,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     // this half's query rows as two E4M3 terms, scaled by a power
                     // of two that puts the row's largest element in [128, 256)
                     ok = ok && pipe_wait(bar(kBarQEmpty), (items_done & 1u) ^ 1u, a.status,
-                                         abort_flag);
+                                         abort_flag, kLimit);
                     const uint4 *src = static_cast<const uint4 *>(a.q) +
                         (int64_t(r.qrow + min(tok0 + tok_row, r.ntok - 1)) * a.num_q_heads + g * G +
                          head_row) * (D / 8);
@@ -1272,7 +1287,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         }
                         fence_proxy_async_smem();
                     }
-                    mbar_arrive(bar(kBarQFull));
+                    if (ok) mbar_arrive(bar(kBarQFull));
                 }
             }
             if (r.na > 0) ++items_done;
@@ -1292,8 +1307,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const int v = v0 + i;
                 const bool clear = v >= clear0 && v < clear1;
                 const int32_t tile_key = (v < tl.sink_tiles ? v : v + tl.gap) * kKeys;
-                ok = ok && pipe_wait(bar(kBarSFull + h), s_par, a.status, abort_flag);
-                __syncwarp();
+                ok = ok && pipe_wait(bar(kBarSFull + h), s_par, a.status, abort_flag, kLimit);
+                if constexpr (C::kEndsItem) {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                } else {
+                    __syncwarp();
+                }
                 tc::fence_after_sync();
                 // ---- value rows no row of the item sees: zeroed, thread = key.  (These
                 // scores came after every wait for the tile that was in the stage
@@ -1304,7 +1324,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     if (__any_sync(0xffffffffu, unseen)) {
                         const uint32_t vp = ord.v(h, i), stage = vp % C::kStages;
                         ok = ok && pipe_wait(bar(kBarFull + stage), (vp / C::kStages) & 1u,
-                                             a.status, abort_flag);
+                                             a.status, abort_flag, kLimit);
                         if (ok && unseen) {
                             uint8_t *vt = base + C::kOffRing + stage * C::kStage;
                             vt += (row >> 3) * 2048 + (row & 7) * 128;
@@ -1340,7 +1360,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             tc::wait_st();
                             tc::fence_before_sync();
                         }
-                        mbar_arrive(bar(kBarPFull + 2 * part + h));
+                        if (C::kEndsItem || ok) mbar_arrive(bar(kBarPFull + 2 * part + h));
                         continue;
                     }
                     tc::ld32(ts + 64 * part, x);
@@ -1384,7 +1404,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                             // product; that of this tile's first keys has to be waited for.
                             if (part)
                                 ok = ok && pipe_wait(bar(kBarP0Done + h), np & 1u, a.status,
-                                                     abort_flag);
+                                                     abort_flag, kLimit);
                             __syncwarp();
                             tc::fence_after_sync();
 #pragma unroll
@@ -1406,7 +1426,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     tc::st32(ts + 32 * part, t);
                     tc::wait_st();
                     tc::fence_before_sync();
-                    mbar_arrive(bar(kBarPFull + 2 * part + h));
+                    if (C::kEndsItem || ok) mbar_arrive(bar(kBarPFull + 2 * part + h));
                     l += total;
                 }
                 ++np;
@@ -1415,7 +1435,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 
             // ---- epilogue
             if (n > 0) {
-                ok = ok && pipe_wait(bar(kBarPvDone + h), nitem & 1u, a.status, abort_flag);
+                ok = ok && pipe_wait(bar(kBarPvDone + h), nitem & 1u, a.status, abort_flag,
+                                     kLimit);
                 ++nitem;
                 __syncwarp();
                 tc::fence_after_sync();
@@ -1445,7 +1466,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
                 for (int j = 0; j < D; j += 32) pin<32>(o + j);
                 tc::fence_before_sync();
-                mbar_arrive(bar(kBarOEmpty + h));
+                if (ok) mbar_arrive(bar(kBarOEmpty + h));
             } else {
 #pragma unroll
                 for (int e = 0; e < D; ++e) o[e] = 0u;
@@ -1683,10 +1704,10 @@ Sizes sizes_of(const pkv_cache_desc &c, int64_t num_tokens, int32_t batch, int32
     return s;
 }
 
-template <int D, bool E4>
+template <int D, bool E4, bool kWithhold>
 int launch(const ChunkArgs &a, uint8_t *ws) {
     using C = Cfg<D, E4>;
-    auto kernel = chunk_tc_kernel<D, E4>;
+    auto kernel = chunk_tc_kernel<D, E4, kWithhold>;
     const Shape sh = shape_of(a.num_q_heads, a.cache.num_kv_heads);
     const Sizes sz = sizes_of(a.cache, a.num_tokens, a.batch, a.num_q_heads);
     const Plan plan{reinterpret_cast<int32_t *>(ws),
@@ -1736,6 +1757,13 @@ int launch(const ChunkArgs &a, uint8_t *ws) {
                       dim3(kMergeThreads), 0, a.stream, a, plan, sh);
 }
 
+template <bool kWithhold>
+int launch_shape(const ChunkArgs &a, uint8_t *ws) {
+    if (a.k_scale) return launch<128, true, kWithhold>(a, ws);
+    return a.cache.head_dim_k == 128 ? launch<128, false, kWithhold>(a, ws)
+                                     : launch<64, false, kWithhold>(a, ws);
+}
+
 }  // namespace
 
 bool chunk_tc_supports(const pkv_cache_desc &c, int32_t num_q_heads, int32_t max_blocks, bool e4) {
@@ -1761,8 +1789,7 @@ int launch_chunk_tc(const ChunkArgs &in, void *workspace) {
     if (a.window == 0) a.sinks = 0;
     uint8_t *ws = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
-    if (a.k_scale) return launch<128, true>(a, ws);
-    return a.cache.head_dim_k == 128 ? launch<128, false>(a, ws) : launch<64, false>(a, ws);
+    return a.withhold ? launch_shape<true>(a, ws) : launch_shape<false>(a, ws);
 }
 
 }  // namespace pkv

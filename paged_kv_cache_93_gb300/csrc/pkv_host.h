@@ -41,6 +41,12 @@ int validate_decode(const pkv_cache_desc *c, const float *q, int32_t batch, int3
                     int32_t max_blocks, const int32_t *seq_lens, int32_t num_splits,
                     int32_t flags);
 
+// Whether a test has enabled PKV_DECODE_TEST_WITHHOLD, and the limit of a pipeline wait
+// under it: long enough for any legitimate stall of a small test case, short enough
+// to keep the test quick.
+bool test_withhold_enabled();
+constexpr uint64_t kTestWaitNs = 1000000ull;
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
@@ -173,6 +179,9 @@ struct ChunkArgs {
     // inside the keys; v_pool then points at the K pool)
     int32_t v_stride;
     const float *k_scale, *v_scale;      // E4M3 pools only
+    // Test control (PKV_DECODE_TEST_WITHHOLD) of the tensor-core form: its producer issues
+    // no copies, its waits give up after kTestWaitNs.
+    bool withhold;
 };
 int launch_chunk_generic(const ChunkArgs &a);
 int launch_chunk_generic_e4m3(const ChunkArgs &a);

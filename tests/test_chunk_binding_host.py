@@ -112,3 +112,23 @@ def test_more_pairs_than_the_merge_counts(built, e4m3):
         assert on_tensor_cores(hkv, batch, 5)
         if hkv >= 1025:
             assert not on_tensor_cores(hkv, batch + 2, batch + 2)
+
+
+def test_withhold_control_is_for_the_tensor_core_form(built):
+    """Refused, before anything is launched, wherever another kernel would run."""
+    import ctypes
+    p = ctypes.c_void_p(0x1000)
+
+    def call(desc=(16, 16, 8, 128, 128), v=p, flags=0x100):
+        d = built.CacheDesc(*desc)
+        return built.lib.pkv_paged_chunk_attn(ctypes.byref(d), p, 4, 32, p, 2, p, v, p, 4, p, 1.0,
+                                              0, 0, None, 0, p, p, flags, None)
+    assert call() == -1
+    built.lib.pkv_test_enable_withhold(1)
+    try:
+        assert call(flags=0x101) == -1 and call(flags=0x102) == -1 and call(flags=0x104) == -1
+        assert call(desc=(16, 16, 8, 96, 96)) == -1 and call(v=None) == -1
+        assert call() == -4                   # taken; it brings no workspace
+    finally:
+        built.lib.pkv_test_enable_withhold(0)
+    assert call() == -1
