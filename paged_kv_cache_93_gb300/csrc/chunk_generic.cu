@@ -232,16 +232,17 @@ chunk_generic_kernel(const ChunkArgs a) {
         float mx = -INFINITY;
         for (int x = 0; x < kWarps; ++x)
             mx = fmaxf(mx, joined[(x * kHeads + h) * stride + c.head_dim_v]);
+        // (scores that are all NaN leave no maximum, but a sum that is NaN)
+        const float base = mx == -INFINITY ? 0.f : mx;
         float o = 0.f, sum = 0.f;
-        if (mx != -INFINITY)
-            for (int x = 0; x < kWarps; ++x) {
-                const float *part = joined + (x * kHeads + h) * stride;
-                const float wt = exp2f(part[c.head_dim_v] - mx);
-                sum = fmaf(wt, part[c.head_dim_v + 1], sum);
-                o = fmaf(wt, part[d], o);
-            }
+        for (int x = 0; x < kWarps; ++x) {
+            const float *part = joined + (x * kHeads + h) * stride;
+            const float wt = exp2f(part[c.head_dim_v] - base);
+            sum = fmaf(wt, part[c.head_dim_v + 1], sum);
+            o = fmaf(wt, part[d], o);
+        }
         const int64_t orow = int64_t(t) * a.num_q_heads + g * group + h0 + h;
-        const bool empty = mx == -INFINITY;
+        const bool empty = sum == 0.f;
         static_cast<uint16_t *>(a.out)[orow * c.head_dim_v + d] =
             uint16_t(f32_to_bf16_bits(empty ? 0.f : o * vscale / sum));
         if (d == 0 && a.lse) a.lse[orow] = empty ? -INFINITY : (mx + log2f(sum)) * kLn2;

@@ -83,3 +83,26 @@ def test_fp8_small_queries_over_small_keys(pkv, k_scale):  # noqa: F811
     assert pkv.device_status(reset=True) == 0
     _chunk.check(case, out, lse)
     weigh(case, out, lse, 2.0 ** -24)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_cuda_core_rows_that_are_not_numbers(pkv, e4m3):  # noqa: F811
+    """A NaN in a query or in a key a row sees: that row is NaN in the CUDA-core
+    form too, also where it has no other score."""
+    case = _chunk.make(65, [(300, 20), (0, 3)], 8, 2, 128, 16, e4m3=e4m3)
+    want = _chunk.run(pkv, case, flags=pkv.DECODE_GENERIC)
+    case.q[7, 5, 3] = float("nan")
+    case.q[20, 1, 0] = float("nan")         # sees one key
+    out, lse = _chunk.run(pkv, case, flags=pkv.DECODE_GENERIC)
+    torch.cuda.synchronize()
+    rest = torch.ones(out.shape[:2], dtype=torch.bool)
+    for t, h in ((7, 5), (20, 1)):
+        assert torch.isnan(out[t, h]).all() and torch.isnan(lse[t, h])
+        rest[t, h] = False
+    assert torch.equal(out[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
+    # every key of the second sequence's first row, which is its only one
+    case.k_pool[case.tables[1, 0].long(), :, 0] = 0x7f if e4m3 else float("nan")
+    out, lse = _chunk.run(pkv, case, flags=pkv.DECODE_GENERIC)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[20]).all() and torch.isnan(lse[20]).all()
+    assert pkv.device_status(reset=True) == 0
