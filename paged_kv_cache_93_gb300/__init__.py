@@ -80,6 +80,12 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dim: int | None = None
         raise ValueError(f"{name} must have {dim} dims, got {t.dim()}")
 
 
+def _int32(x) -> int:
+    """x as a 32-bit argument: past 2^31 - 1 it is that, negative -1 (ctypes would wrap
+    it around)."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 class ValuesInKeys:
     """Pass as `v_pool` when the cache keeps no separate value pool: the value
     of a token is the first `head_dim_v` dims of its key row (the latent
@@ -278,7 +284,7 @@ def rope_append(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq,
     _check("pkv_rope_append", lib.pkv_rope_append(
         ctypes.byref(desc), _ptr(k_pool), _v_ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(positions), _ptr(slots), positions.numel(), _ptr(inv_freq),
-        2 * inv_freq.numel(), int(rotary_offset), float(amplitude), flags, _ptr(q_out),
+        2 * inv_freq.numel(), _int32(rotary_offset), float(amplitude), flags, _ptr(q_out),
         _stream(stream)))
     return q_out
 
@@ -294,7 +300,7 @@ def rope_append_e4m3(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq
     _check("pkv_rope_append_e4m3", lib.pkv_rope_append_e4m3(
         ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(k_scale), _ptr(v_scale), _ptr(positions), _ptr(slots),
-        positions.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), int(rotary_offset),
+        positions.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), _int32(rotary_offset),
         float(amplitude), flags, _ptr(q_out), _stream(stream)))
     return q_out
 
@@ -611,7 +617,7 @@ def paged_chunk_attn(q, cu_q_lens, k_pool, v_pool, block_tables, seq_lens, scale
     _check("pkv_paged_chunk_attn", lib.pkv_paged_chunk_attn(
         ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
         _ptr(k_pool), _v_ptr(v_pool), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-        float(scale), int(window), int(sink_tokens), _ptr(workspace), ws_bytes, _ptr(out),
+        float(scale), _int32(window), _int32(sink_tokens), _ptr(workspace), ws_bytes, _ptr(out),
         _ptr(lse), int(flags), _stream(stream)))
     return out, lse
 
@@ -628,7 +634,7 @@ def paged_chunk_attn_e4m3(q, cu_q_lens, k_pool, v_pool, k_scale, v_scale, block_
     _check("pkv_paged_chunk_attn_e4m3", lib.pkv_paged_chunk_attn_e4m3(
         ctypes.byref(desc), _ptr(q), q.shape[0], q.shape[1], _ptr(cu_q_lens), seq_lens.numel(),
         _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), float(scale), int(window), int(sink_tokens),
+        block_tables.shape[1], _ptr(seq_lens), float(scale), _int32(window), _int32(sink_tokens),
         _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse), int(flags), _stream(stream)))
     return out, lse
 

@@ -132,3 +132,55 @@ def test_withhold_control_is_for_the_tensor_core_form(built):
     finally:
         built.lib.pkv_test_enable_withhold(0)
     assert call() == -1
+
+
+@pytest.fixture
+def calls(pkv, monkeypatch):
+    """The arguments that reach the C calls, as C gets them (nothing runs)."""
+    import ctypes
+    seen = {}
+
+    def stand_in(name):
+        types = pkv.m._lib.SIGNATURES[name][1]
+
+        def call(*args):
+            seen[name] = [t(x).value if t in (ctypes.c_int32, ctypes.c_int64) else x
+                          for t, x in zip(types, args)]
+            return 0
+        return call
+    lib = SimpleNamespace(**{n: stand_in(n) for n in (
+        "pkv_paged_chunk_attn", "pkv_paged_chunk_attn_e4m3", "pkv_rope_append",
+        "pkv_rope_append_e4m3", "pkv_chunk_workspace_size", "pkv_chunk_workspace_size_e4m3")})
+    monkeypatch.setattr(pkv.m, "lib", lib)
+    return pkv.m, seen
+
+
+NUMBERS = [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1),
+           (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 16, 2 ** 31 - 1), (2 ** 63 - 1, 2 ** 31 - 1),
+           (-1, -1), (-2 ** 32 + 5, -1), (-2 ** 31 - 1, -1)]
+
+
+@pytest.mark.parametrize("given,want", NUMBERS)
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_numbers_past_32_bits(calls, given, want, e4m3):
+    """A window or sinks past 2^31 see what 2^31 - 1 do, and a negative number or an
+    offset past every head stays one that the call refuses: none wraps around."""
+    m, seen = calls
+    kind = torch.uint8 if e4m3 else torch.bfloat16
+    pool = torch.zeros(4, 2, 16, 128, dtype=kind)
+    scales = (torch.ones(2), torch.ones(2)) if e4m3 else ()
+    q, cu, lens = torch.zeros(3, 8, 128, dtype=torch.bfloat16), torch.zeros(2), torch.zeros(1)
+    call = m.paged_chunk_attn_e4m3 if e4m3 else m.paged_chunk_attn
+    call(q, cu, pool, pool, *scales, torch.zeros(1, 4), lens, 1.0, window=given, sink_tokens=given)
+    args = seen["pkv_paged_chunk_attn_e4m3" if e4m3 else "pkv_paged_chunk_attn"]
+    at = 14 if e4m3 else 12
+    assert args[at:at + 2] == [want, want]
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    i64 = torch.zeros(3, dtype=torch.int64)
+    if e4m3:
+        m.rope_append_e4m3(pool, pool, q, k, k, i64, i64, torch.zeros(4), *scales,
+                           rotary_offset=given)
+    else:
+        m.rope_append(pool, pool, q, k, k, i64, i64, torch.zeros(4), rotary_offset=given)
+    args = seen["pkv_rope_append_e4m3" if e4m3 else "pkv_rope_append"]
+    assert args[14 if e4m3 else 12] == want
