@@ -27,7 +27,7 @@ size_t workspace_size(const pkv_cache_desc *c, int64_t num_tokens, int32_t batch
                       int32_t max_blocks, int32_t flags, bool e4) {
     if (!c || num_tokens <= 0 || batch <= 0 || hq <= 0 || max_blocks < 0 ||
         c->num_kv_heads <= 0 || hq % c->num_kv_heads != 0 || c->num_blocks <= 0 ||
-        num_tokens * hq >= (int64_t(1) << 29) ||
+        num_tokens >= ((int64_t(1) << 29) + hq - 1) / hq ||
         !on_tensor_cores(*c, num_tokens, batch, hq, max_blocks, flags, e4, false))
         return 0;
     return chunk_tc_workspace(*c, num_tokens, batch, hq);
@@ -70,7 +70,7 @@ int prepare(ChunkArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int64
         return PKV_ERR_INVALID_ARG;
     if (hq % c->num_kv_heads != 0 || c->head_dim_k % 8 != 0 || c->head_dim_v % 8 != 0 ||
         c->head_dim_k > 1024 || c->head_dim_v > 1024 || batch > 65535 || hq > 65535 ||
-        num_tokens * hq >= (int64_t(1) << 29))
+        num_tokens >= ((int64_t(1) << 29) + hq - 1) / hq)
         return PKV_ERR_SHAPE;
     if (num_tokens == 0 || batch == 0) {
         *done = true;

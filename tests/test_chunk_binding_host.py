@@ -184,3 +184,15 @@ def test_numbers_past_32_bits(calls, given, want, e4m3):
         m.rope_append(pool, pool, q, k, k, i64, i64, torch.zeros(4), rotary_offset=given)
     args = seen["pkv_rope_append_e4m3" if e4m3 else "pkv_rope_append"]
     assert args[14 if e4m3 else 12] == want
+
+
+@pytest.mark.parametrize("tokens", [1 << 29, 1 << 32, 1 << 59, 1 << 60, (1 << 60) + 4, 1 << 62])
+def test_token_counts_whose_rows_pass_64_bits(built, tokens):
+    """num_tokens * num_q_heads (16) wraps to a small number from 2^60 on."""
+    import ctypes
+    p = ctypes.c_void_p(0x1000)
+    d = built.CacheDesc(16, 16, 8, 128, 128)
+    rc = built.lib.pkv_paged_chunk_attn(ctypes.byref(d), p, tokens, 16, p, 2, p, p, p, 4, p, 1.0,
+                                        0, 0, None, 0, p, p, 0, None)
+    assert rc == -2
+    assert built.lib.pkv_chunk_workspace_size(ctypes.byref(d), tokens, 2, 16, 4, 0) == 0
