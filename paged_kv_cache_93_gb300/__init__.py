@@ -566,6 +566,8 @@ def _chunk_args(desc, size, q, cu_q_lens, block_tables, seq_lens, workspace, out
         raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
     if cu_q_lens.numel() != B + 1 or block_tables.shape[0] != B:
         raise ValueError("cu_q_lens must have one entry more, block_tables one row per seq_len")
+    if workspace is not None:
+        _need(workspace, "workspace", workspace.dtype)
     need = size(ctypes.byref(desc), T, B, Hq, block_tables.shape[1], flags)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if stream is not None and (out is None or lse is None or ws_bytes < need):

@@ -196,3 +196,23 @@ def test_token_counts_whose_rows_pass_64_bits(built, tokens):
                                         0, 0, None, 0, p, p, 0, None)
     assert rc == -2
     assert built.lib.pkv_chunk_workspace_size(ctypes.byref(d), tokens, 2, 16, 4, 0) == 0
+
+
+def test_a_workspace_the_gpu_cannot_write_is_refused(pkv, monkeypatch):
+    """A workspace on the host, or one with gaps: as for every other buffer."""
+    checked = []
+
+    def need(t, name, dtype, dim=None):
+        if name == "workspace":
+            checked.append(name)
+            if not t.is_contiguous():
+                raise ValueError(name)
+            raise TypeError(name)           # every tensor here is on the host
+    monkeypatch.setattr(pkv.m, "_need", need)
+    with pytest.raises(TypeError):
+        scratch(pkv, None, "enough")
+    with pytest.raises(TypeError):
+        scratch(pkv, SIDE, "small", True)
+    assert len(checked) == 2
+    scratch(pkv)                            # none brought: nothing to check
+    assert len(checked) == 2

@@ -106,3 +106,12 @@ def test_cuda_core_rows_that_are_not_numbers(pkv, e4m3):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.isnan(out[20]).all() and torch.isnan(lse[20]).all()
     assert pkv.device_status(reset=True) == 0
+
+
+def test_workspaces_on_the_host_or_with_gaps_are_refused(pkv):  # noqa: F811
+    case = _chunk.make(66, [(300, 20)], 8, 2, 128, 16)
+    with pytest.raises(TypeError):
+        _chunk.run(pkv, case, workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        _chunk.run(pkv, case, workspace=torch.empty(1 << 27, dtype=torch.uint8, device="cuda")[::2])
+    assert pkv.device_status(reset=True) == 0
