@@ -188,13 +188,16 @@ int pkv_copy_blocks_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool
  *                              x2 cos(angle) + x1 sin(angle))
  * where (x1, x2) are elements i and i + rotary_dim / 2 of the part (half
  * layout, the default), or 2i and 2i + 1 (PKV_ROPE_INTERLEAVED).  The other
- * elements pass through (bf16 to bf16 bit by bit, as the values do).  Every query head of q [T][num_q_heads][head_dim_k]
+ * elements pass through (bf16 to bf16 bit by bit, as the values do).  Every
+ * query head of q [T][num_q_heads][head_dim_k]
  * (bf16) goes to q_out (bf16, which may be q itself; fp32 with
  * PKV_ROPE_Q_FP32, as the decode calls take it); every rotated key row of
  * k_new and every (unrotated) value row of v_new goes to the token's slot of
  * the pools, as pkv_kv_append places them.  Arithmetic is fp32, each output
- * rounded once; the angle keeps its fraction of a turn exactly to
- * m * 2^-53 turns, so far positions lose nothing.
+ * rounded once.  The angle's fraction of a turn is taken exactly to
+ * m * 2^-53 turns and then rounded to binary32 for its cosine and sine (2^-26
+ * turns, the larger of the two below m = 2^27): far positions lose no more than
+ * near ones.
  *  - inv_freq: [rotary_dim / 2] binary64 on the device, radians per token
  *    (pkv_rope_frequencies makes the usual tables).
  *  - rotary_dim even, 2 .. head_dim_k; vectors of 16 bytes rotate when
@@ -591,8 +594,8 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  * Head dims 64 or 128 (equal for K and V), query groups up to 128 and
  * power-of-two block sizes 8..256 (E4M3: head dim 128, 16..256) run on the
  * tcgen05 tensor cores while min(batch, num_tokens) * num_kv_heads <= 2^26 - 2048;
- * other shapes (head dims multiples of 8 up to 1024),
- * and flags PKV_DECODE_GENERIC or PKV_DECODE_NO_TCGEN05, on CUDA cores.
+ * other shapes (head dims multiples of 8 up to 1024), and flags
+ * PKV_DECODE_GENERIC or PKV_DECODE_NO_TCGEN05, on CUDA cores.
  * workspace: at least pkv_chunk_workspace_size(...) bytes (0: may be NULL),
  * 16-byte aligned, contents on entry do not matter; calls that may overlap
  * on the GPU need one each.  A row whose kernel gave up on a pipeline wait

@@ -13,12 +13,13 @@
 // fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64, and position * F in
 // wrapping 64-bit integer arithmetic IS the fraction of a turn, off by at most
 // position * 2^-53 turns (F comes from a binary64).  Its upper 32 bits, as a
-// signed number of 2^-32 turns, go to sincospif.
+// signed number of 2^-32 turns, are rounded to binary32 (2^-26 turns) for
+// sincospif.
 //
 // Bound: memory.  Every q, k and v element is read once and written once, as
-// 16-byte vectors; the tokens' cosines and sines are computed once per token
-// into shared memory (rotary_dim / 2 of them against (Hq + Hkv) * head_dim
-// elements) and shared by all heads.
+// 16-byte vectors; cosines and sines (rotary_dim / 2 of them against (Hq + Hkv) *
+// head_dim elements) are computed once for all of a token's heads, or for a part of
+// them: in a warp's registers for the common heads, in shared memory for the others.
 #include <cuda_runtime.h>
 
 #include <algorithm>
