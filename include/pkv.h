@@ -590,6 +590,9 @@ int pkv_paged_decode_attn_cascade(const pkv_cache_desc *cache, const float *q, i
  *    its bits.  A stored key or value of the sequence itself that is infinite
  *    or NaN reaches the rows that see it, and may reach rows of the same
  *    sequence that do not.
+ *  - A row whose every score is -inf counts as one that sees no key: out = 0,
+ *    lse = -inf.  A query that is NaN, or whose scores are, gives a NaN row (E4M3
+ *    caches on the tensor cores: an infinite query too).
  *  - v_pool NULL: values inside the keys, as pkv_paged_decode_attn.
  * Head dims 64 or 128 (equal for K and V), query groups up to 128 and
  * power-of-two block sizes 8..256 (E4M3: head dim 128, 16..256) run on the

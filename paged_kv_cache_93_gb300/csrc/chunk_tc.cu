@@ -14,9 +14,9 @@
 // second the rounding residual of the first (a bf16 element fits them exactly
 // unless it is far below its row's largest), so the stored keys feed the tensor
 // cores as they are, in the time of one bf16 product; the values are widened to
-// fp16, which holds them exactly, and P is rounded to fp16 (two E4M3 terms of P
-// instead cost the softmax threads six conversions for four scores: 650 us for
-// 1,000 tokens over 17K keys, 471 so).
+// fp16, which holds them exactly, and P is rounded to fp16.  (Two E4M3 terms of P cost
+// the softmax threads six conversions for four scores: 1,000 tokens over 17K keys went
+// from 650 to 502 us when only that changed.)
 //
 // Work item = (block of up to 2 tiles' tokens of a sequence, KV head, all of its
 // key tiles or a run of them), given out by plan_kernel:
@@ -95,8 +95,8 @@ struct Cfg {
     static constexpr uint32_t kStage = kKeys * D * kElem;           // a K or V tile
     static constexpr int kStages = E4 ? 6 : kStage == 32768 ? 5 : 10;
     // Who makes the value rows 0 that no row of an item sees.  Head dim 64, whose
-    // softmax bounds a step: the two idle warps (7% of an 8K prompt under a window of
-    // 1,024); head dim 128, where a tile's way to the tensor cores counts: the
+    // softmax bounds a step: the two idle warps (an 8K prompt under a window of 1,024
+    // 250 -> 241 us); head dim 128, where a tile's way to the tensor cores counts: the
     // softmax warps (8K prompt 388 -> 380 us); E4M3: the warps that widen.
     static constexpr bool kTended = D == 64;
     // How a warp that gave up keeps from arriving: by a vote a tile, or by a test before
@@ -653,10 +653,10 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool al
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-// Two of four maxima raised by four scores (two chains in flight).
-__device__ __forceinline__ void raise4(float (&mx)[4], const uint32_t *x) {
+// Two maxima raised by four scores (two chains in flight).
+__device__ __forceinline__ void raise4(float (&mx)[2], const uint32_t *x) {
     mx[0] = max3(mx[0], __uint_as_float(x[0]), __uint_as_float(x[1]));
-    mx[2] = max3(mx[2], __uint_as_float(x[2]), __uint_as_float(x[3]));
+    mx[1] = max3(mx[1], __uint_as_float(x[2]), __uint_as_float(x[3]));
 }
 // Makes what follows depend on registers a TMEM load has filled (their values
 // are there only after the wait that precedes this).
@@ -667,8 +667,8 @@ __device__ __forceinline__ void pin(uint32_t *r) {
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),
                           "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
-// Four probabilities -> their E4M3 codes and those of the rounding residuals.
-// Through fp16 (2^-11 relative, below what two terms resolve).
+// Four query elements, scaled below 256 -> their E4M3 codes and those of the rounding
+// residuals.  Through fp16, which holds a bf16 number of 2^-14 or more exactly.
 __device__ __forceinline__ void e4m3_terms(float p0, float p1, float p2, float p3, uint32_t &t0,
                                            uint32_t &t1) {
     const uint32_t a = pack_f16x2(p0, p1), b = pack_f16x2(p2, p3);
@@ -1392,12 +1392,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
                         const bool rise = total > C::kMost || m == -INFINITY;
                         if (!__any_sync(0xffffffffu, rise && !again)) break;
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                         for (int j = 0; j < 64; j += 4) raise4(mx, x + j);
                         // (a row that need not rise keeps m and, to the bit, its terms:
                         // what a row gives does not depend on its neighbours)
-                        const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[2])) : m;
+                        const float mn = rise ? fmaxf(m, fmaxf(mx[0], mx[1])) : m;
                         const float f = m == -INFINITY ? 0.f : ex2_approx((m - mn) * sc);
                         if (part || i > 0) {
                             // rescale.  These scores were told after the last tile's value
@@ -1783,10 +1783,7 @@ size_t chunk_tc_workspace(const pkv_cache_desc &c, int64_t num_tokens, int32_t b
 
 int launch_chunk_tc(const ChunkArgs &in, void *workspace) {
     ChunkArgs a = in;
-    // a window no sequence outgrows is none; positions stay below 2^30
-    if (a.window >= int64_t(a.max_blocks) * a.cache.block_size) a.window = 0;
-    a.sinks = std::min(a.sinks, 1 << 30);
-    if (a.window == 0) a.sinks = 0;
+    if (a.window == 0) a.sinks = 0;      // (both within the tables' capacity, below 2^30)
     uint8_t *ws = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(workspace) + 255) & ~uintptr_t(255));
     return a.withhold ? launch_shape<true>(a, ws) : launch_shape<false>(a, ws);
