@@ -82,6 +82,10 @@ chunk_generic_kernel(const ChunkArgs a) {
             const int x = a.cu_q_lens[b];
             if (x < 0 || x > a.num_tokens || (b > 0 && a.cu_q_lens[b - 1] > x))
                 raise_status(a.status, PKV_DEV_QUERY_RANGE);
+            // (of a sequence with new tokens its own CTAs tell)
+            const int L = b < a.batch ? a.seq_lens[b] : 0;
+            if (L < 0 || L > int64_t(a.max_blocks) * c.block_size)
+                raise_status(a.status, PKV_DEV_SEQ_LEN);
         }
     const int b = sequence_of(a.cu_q_lens, a.batch, t);
     if (b < 0) return;

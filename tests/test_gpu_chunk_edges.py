@@ -115,3 +115,16 @@ def test_workspaces_on_the_host_or_with_gaps_are_refused(pkv):  # noqa: F811
     with pytest.raises(ValueError):
         _chunk.run(pkv, case, workspace=torch.empty(1 << 27, dtype=torch.uint8, device="cuda")[::2])
     assert pkv.device_status(reset=True) == 0
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 65, 2 ** 31 - 1])
+def test_bad_length_of_a_sequence_without_new_tokens(pkv, flags, length):  # noqa: F811
+    """It sets the status as any other does, in both forms, and changes no row."""
+    case = _chunk.make(67, [(30, 4), (50, 0), (0, 9)], 8, 2, 128, 16)
+    assert case.tables.shape[1] == 4
+    case.lens[1] = length
+    out, lse = _chunk.run(pkv, case, flags=flags)
+    torch.cuda.synchronize()
+    assert pkv.device_status(reset=True) == pkv.DEV_SEQ_LEN
+    _chunk.check(case, out, lse)
