@@ -81,7 +81,10 @@ typedef enum pkv_status {
 #define PKV_DEV_PREFIX        0x40u /* cascade: a table that does not begin with the
                                        shared prefix blocks */
 #define PKV_DEV_QUERY_RANGE   0x80u /* chunk attention: cu_q_lens decreases, or leaves
-                                       [0, num_tokens] */
+                                       [0, num_tokens]; extend_sequences: more new tokens
+                                       than rows */
+#define PKV_DEV_NO_BLOCKS     0x100u /* extend_sequences: not enough free blocks */
+#define PKV_DEV_AXIS          0x200u /* a rotary pair's axis outside [0, num_axes) */
 
 /* Shape of one layer's paged KV cache. */
 typedef struct pkv_cache_desc {
@@ -239,6 +242,133 @@ int pkv_rope_append_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool
                          const int64_t *slot_mapping, int64_t num_tokens, const double *inv_freq,
                          int32_t rotary_dim, int32_t rotary_offset, float amplitude,
                          int32_t flags, void *q_out, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_rope_append_axes -- pkv_rope_append with positions of several axes, as
+ * the tokens of images and videos have them (time, height, width): pair i of a
+ * token t turns by positions[pair_axis[i]][t] * inv_freq[i].  Everything else
+ * is pkv_rope_append's.
+ *  - positions [num_axes][num_tokens] int64, 1 <= num_axes <= 8.  A negative
+ *    position on axis 0 is padding (the token is skipped); on the other axes
+ *    it turns the other way.
+ *  - pair_axis [rotary_dim / 2] int32 on the device.  A value outside
+ *    [0, num_axes) counts as axis 0 and sets PKV_DEV_AXIS.
+ * ------------------------------------------------------------------------- */
+int pkv_rope_append_axes(const pkv_cache_desc *cache, void *k_pool, void *v_pool, const void *q,
+                         int32_t num_q_heads, const void *k_new, const void *v_new,
+                         const int64_t *positions, int32_t num_axes, const int32_t *pair_axis,
+                         const int64_t *slot_mapping, int64_t num_tokens, const double *inv_freq,
+                         int32_t rotary_dim, int32_t rotary_offset, float amplitude,
+                         int32_t flags, void *q_out, pkv_stream_t stream);
+
+int pkv_rope_append_axes_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
+                              const void *q, int32_t num_q_heads, const void *k_new,
+                              const void *v_new, const float *k_scale, const float *v_scale,
+                              const int64_t *positions, int32_t num_axes,
+                              const int32_t *pair_axis, const int64_t *slot_mapping,
+                              int64_t num_tokens, const double *inv_freq, int32_t rotary_dim,
+                              int32_t rotary_offset, float amplitude, int32_t flags, void *q_out,
+                              pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit cache -- [DCP] names storing the KV cache in a low-precision type as
+ * the way to shrink each token's bytes; [PA] "Continuous Batching・prefix
+ * caching・量子化との違い": quantisation's effect on accuracy has to be checked.
+ * The pages fix no format; here a row (one token's key or value of one KV
+ * head, D elements) is D / 2 bytes of codes 0..15, element 2i in the low and
+ * 2i + 1 in the high half of byte i, and a bf16 pair (scale, offset): element d
+ * reads back as scale * code[d] + offset.  At head dim 128 a row takes 68
+ * bytes, 0.27 of bf16's 256.
+ *   k_pool [num_blocks][num_kv_heads][block_size][head_dim_k / 2] uint8,
+ *   k_params [num_blocks][num_kv_heads][block_size][2] bf16, v_pool, v_params
+ *   likewise; all 16-byte aligned.  Head dims: multiples of 32 up to 1024.
+ * With low and high the row's smallest and largest element, and every
+ * operation rounded to binary32 before the next:
+ *   offset = bf16(low), scale = bf16((high - offset) * fl(1/15)) (0 where that
+ *   is negative or below 2^-126), code = the whole number nearest to
+ *   (x - offset) * fl(1 / scale), ties to even, held within 0..15 (0 where
+ *   the scale is 0).
+ * A row with an element that is infinite or NaN, or whose spread is no
+ * binary32, is stored as scale = offset = NaN: it reads as NaN.
+ *
+ * pkv_kv_append_int4: pkv_kv_append into 4-bit pools (k_new, v_new bf16).
+ * pkv_copy_blocks_int4: pkv_copy_blocks for 4-bit pools, parameters with the codes.
+ * pkv_rope_append_int4: pkv_rope_append (pair_axis NULL, num_axes 1) or
+ * pkv_rope_append_axes into 4-bit pools; the rotated key is quantised from
+ * fp32 (no bf16 in between).
+ * Values inside the keys are not offered (v_pool NULL: PKV_ERR_INVALID_ARG).
+ * ------------------------------------------------------------------------- */
+int pkv_kv_append_int4(const pkv_cache_desc *cache, void *k_pool, void *k_params, void *v_pool,
+                       void *v_params, const void *k_new, const void *v_new,
+                       const int64_t *slot_mapping, int64_t num_tokens, pkv_stream_t stream);
+
+int pkv_copy_blocks_int4(const pkv_cache_desc *cache, void *k_pool, void *k_params, void *v_pool,
+                         void *v_params, const int32_t *src, const int32_t *dst,
+                         int32_t num_pairs, pkv_stream_t stream);
+
+int pkv_rope_append_int4(const pkv_cache_desc *cache, void *k_pool, void *k_params, void *v_pool,
+                         void *v_params, const void *q, int32_t num_q_heads, const void *k_new,
+                         const void *v_new, const int64_t *positions, int32_t num_axes,
+                         const int32_t *pair_axis, const int64_t *slot_mapping,
+                         int64_t num_tokens, const double *inv_freq, int32_t rotary_dim,
+                         int32_t rotary_offset, float amplitude, int32_t flags, void *q_out,
+                         pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_extend_sequences, pkv_trim_sequences -- [PA] the block table and the
+ * allocation and reuse of blocks, kept on the device: for steps whose lengths
+ * only the device knows (drafted tokens, some of them refused) and for
+ * captured steps.  The state, all device memory of the caller:
+ *   block_tables [batch][max_blocks] int32, seq_lens [batch] int32;
+ *   free_blocks [num_blocks] int32, a stack of which the first pool_state[0]
+ *   entries are free and the last of those is taken first;
+ *   pool_state [4] int32: the number of free blocks, then three zeros (the
+ *   library counts in them during a call and leaves them zero).
+ *
+ * Extend: sequence b brings new_lens[b] >= 0 tokens.  The blocks it needs beyond
+ * those its length already fills are taken from the stack, sequences in order,
+ * and written to its table row; seq_lens[b] grows; cu_q_lens [batch + 1] int32
+ * gets the running sums of the tokens brought; row cu_q_lens[b] + i of
+ * positions and slot_mapping [num_tokens] int64 (16-byte aligned) gets the
+ * position and the slot of its i-th new token, as pkv_kv_append,
+ * pkv_rope_append and pkv_paged_chunk_attn take them.  Rows from
+ * cu_q_lens[batch] on are padding: position and slot -1.
+ * A sequence that cannot have what it asks for brings nothing and stays as
+ * it is:
+ *   - new_lens[b] or seq_lens[b] negative, or seq_lens[b] past its table row:
+ *     PKV_DEV_SEQ_LEN;
+ *   - more tokens than its table row holds (or a length past 2^31 - 1):
+ *     PKV_DEV_TABLE_RANGE;
+ *   - tokens that end past num_tokens rows, those asked for by the sequences
+ *     before it counted: PKV_DEV_QUERY_RANGE;
+ *   - blocks past the free ones, those asked for by the sequences before it
+ *     (but those of the lines above) counted, so that none overtakes a
+ *     refused one: PKV_DEV_NO_BLOCKS.
+ * A block id outside [0, num_blocks) (in the stack, or in a table where a
+ * token's slot is looked up) gives slot -1 and sets PKV_DEV_BLOCK_ID; so does a
+ * count outside [0, num_blocks], which counts as 0.
+ *
+ * Trim: sequence b keeps its first keep_lens[b] tokens; the blocks past
+ * them go back to the stack, the last sequence's last block first, so that
+ * trimming to the old lengths undoes an extend exactly.  keep_lens[b] negative:
+ * left as it is.  keep_lens[b] > seq_lens[b], or a length past the table row:
+ * left as it is, PKV_DEV_SEQ_LEN.  Blocks that find the stack full (a block
+ * given back twice) are dropped, PKV_DEV_BLOCK_ID.  A block that several
+ * sequences share must not be trimmed away here (the host block manager
+ * counts references).
+ * batch <= 8192, batch * max_blocks < 2^31 (PKV_ERR_SHAPE).  Calls on the same
+ * state follow one another on one stream.
+ * ------------------------------------------------------------------------- */
+int pkv_extend_sequences(int32_t block_size, int32_t num_blocks, int32_t *block_tables,
+                         int32_t *seq_lens, const int32_t *new_lens, int32_t batch,
+                         int32_t max_blocks, int32_t *free_blocks, int32_t *pool_state,
+                         int32_t num_tokens, int32_t *cu_q_lens, int64_t *positions,
+                         int64_t *slot_mapping, pkv_stream_t stream);
+
+int pkv_trim_sequences(int32_t block_size, int32_t num_blocks, const int32_t *block_tables,
+                       int32_t *seq_lens, const int32_t *keep_lens, int32_t batch,
+                       int32_t max_blocks, int32_t *free_blocks, int32_t *pool_state,
+                       pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * pkv_interleave_slot_mapping -- [DCP] interleaved assignment: the KV of token i
@@ -503,6 +633,51 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
                                      const int32_t *seq_lens, float scale, int32_t num_splits,
                                      void *workspace, size_t workspace_bytes, float *out,
                                      float *lse, int32_t flags, pkv_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * pkv_paged_decode_attn_int4 -- pkv_paged_decode_attn over 4-bit pools (the
+ * 4-bit cache above): K_j and V_j are the elements the codes read back as; q,
+ * out, lse, splits, workspace (pkv_decode_workspace_size(batch *
+ * tokens_per_seq, num_q_heads, head_dim_v, S)) and the status bits as there.
+ * _multi_int4: the multi-token step (rows, causal lengths, layouts and the
+ * PKV_DEV_SEQ_LEN rule of pkv_paged_decode_attn_multi; workspace as above).
+ * _partial_int4: the per-chunk partials (pkv_paged_decode_attn_partial).
+ * A token that a row does not see reaches nothing of it, whatever its bits;
+ * one that it sees and that reads as NaN makes the row NaN.
+ * flags: 0, PKV_DECODE_GENERIC (the CUDA-core kernel), PKV_DECODE_NO_TCGEN05
+ * (accepted: no kernel here uses tcgen05).  hq <= 262,140, batch *
+ * tokens_per_seq <= 65535, 1 <= tokens_per_seq <= 64.
+ * pkv_decode_auto_splits_int4: what num_splits = 0 resolves to (tokens_per_seq
+ * 1 for the single-token call; max_seq_len = max_blocks * block_size).
+ * ------------------------------------------------------------------------- */
+int32_t pkv_decode_auto_splits_int4(const pkv_cache_desc *cache, int32_t batch,
+                                    int32_t tokens_per_seq, int32_t num_q_heads,
+                                    int32_t max_seq_len, int32_t flags);
+
+int pkv_paged_decode_attn_int4(const pkv_cache_desc *cache, const float *q, int32_t batch,
+                               int32_t num_q_heads, const void *k_pool, const void *k_params,
+                               const void *v_pool, const void *v_params,
+                               const int32_t *block_tables, int32_t max_blocks,
+                               const int32_t *seq_lens, float scale, int32_t num_splits,
+                               void *workspace, size_t workspace_bytes, float *out, float *lse,
+                               int32_t flags, pkv_stream_t stream);
+
+int pkv_paged_decode_attn_multi_int4(const pkv_cache_desc *cache, const float *q, int32_t batch,
+                                     int32_t tokens_per_seq, int32_t num_q_heads,
+                                     const void *k_pool, const void *k_params,
+                                     const void *v_pool, const void *v_params,
+                                     const int32_t *block_tables, int32_t max_blocks,
+                                     const int32_t *seq_lens, float scale, int32_t num_splits,
+                                     void *workspace, size_t workspace_bytes, float *out,
+                                     float *lse, int32_t flags, pkv_stream_t stream);
+
+int pkv_paged_decode_attn_partial_int4(const pkv_cache_desc *cache, const float *q,
+                                       int32_t batch, int32_t num_q_heads, const void *k_pool,
+                                       const void *k_params, const void *v_pool,
+                                       const void *v_params, const int32_t *block_tables,
+                                       int32_t max_blocks, const int32_t *seq_lens, float scale,
+                                       int32_t num_splits, float *out_part, float *lse_part,
+                                       int32_t flags, pkv_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * pkv_paged_decode_attn_cascade -- decode attention for sequences that share

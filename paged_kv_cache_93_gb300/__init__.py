@@ -10,7 +10,9 @@ v_pool [num_blocks, Hkv, block_size, Dv] bf16, block_tables [B, max_blocks]
 int32, seq_lens [B] int32, q [B, Hq, Dk] fp32, out [B, Hq, Dv] fp32,
 lse [B, Hq] fp32 (natural log).  An FP8 cache holds E4M3 codes in uint8
 pools of the same shapes, with fp32 dequantisation scales per KV head
-(the *_e4m3 functions).
+(the *_e4m3 functions).  A 4-bit cache (the *_int4 functions) holds codes, two
+to a byte, in uint8 pools [num_blocks, Hkv, block_size, D / 2] and a bf16
+(scale, offset) pair per row in params [num_blocks, Hkv, block_size, 2].
 """
 from __future__ import annotations
 
@@ -22,7 +24,7 @@ import torch
 from . import _lib
 from ._lib import (DECODE_GENERIC, DECODE_NO_TCGEN05, DECODE_TEST_WITHHOLD, DEV_BLOCK_ID,
                    DEV_COPY_CONFLICT, DEV_PREFIX, DEV_SEQ_LEN, DEV_SLOT, DEV_TABLE_RANGE,
-                   DEV_QUERY_RANGE, DEV_TIMEOUT, ROPE_INTERLEAVED, ROPE_Q_FP32, CacheDesc,
+                   DEV_AXIS, DEV_NO_BLOCKS, DEV_QUERY_RANGE, DEV_TIMEOUT, ROPE_INTERLEAVED, ROPE_Q_FP32, CacheDesc,
                    PkvError)
 
 __all__ = [
@@ -34,7 +36,10 @@ __all__ = [
     "paged_decode_attn_cascade",
     "decode_cascade_splits", "DEV_PREFIX", "rope_frequencies", "rope_append", "rope_append_e4m3",
     "chunk_workspace_size", "paged_chunk_attn", "paged_chunk_attn_e4m3", "DEV_QUERY_RANGE",
-    "ROPE_INTERLEAVED", "ROPE_Q_FP32",
+    "ROPE_INTERLEAVED", "ROPE_Q_FP32", "DEV_AXIS", "DEV_NO_BLOCKS", "cache_desc_int4",
+    "kv_append_int4", "copy_blocks_int4", "rope_append_int4", "decode_auto_splits_int4",
+    "paged_decode_attn_int4", "paged_decode_attn_multi_int4", "paged_decode_attn_partial_int4",
+    "block_pool", "extend_sequences", "trim_sequences",
     "device_status", "BlockManager", "library_path", "DECODE_GENERIC", "DECODE_NO_TCGEN05",
     "DECODE_TEST_WITHHOLD", "DEV_BLOCK_ID",
     "DEV_SLOT", "DEV_SEQ_LEN", "DEV_COPY_CONFLICT", "DEV_TIMEOUT", "DEV_TABLE_RANGE",
@@ -227,14 +232,20 @@ def rope_frequencies(rotary_dim: int, theta: float = 10000.0, factor: float = 1.
 
 
 def _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq, interleaved, q_dtype,
-               q_out, stream):
+               q_out, stream, pair_axis=None):
     """Checks of the rope_append calls -> (q_out, flags)."""
     _need(q, "q", torch.bfloat16, 3)
     _need(k_new, "k_new", torch.bfloat16, 3)
-    _need(positions, "positions", torch.int64, 1)
+    _need(positions, "positions", torch.int64, 1 if pair_axis is None else 2)
     _need(slots, "slot_mapping", torch.int64, 1)
     _need(inv_freq, "inv_freq", torch.float64, 1)
-    T = positions.numel()
+    T = positions.shape[-1]
+    if pair_axis is not None:
+        _need(pair_axis, "pair_axis", torch.int32, 1)
+        if pair_axis.numel() != inv_freq.numel():
+            raise ValueError("pair_axis must have one entry per rotary pair, as inv_freq")
+        if not 1 <= positions.shape[0] <= 8:
+            raise ValueError("positions must have 1 to 8 axes")
     Tq, Hq, Dk = q.shape
     if slots.numel() != T or Tq != T:
         raise ValueError("q, positions and slots disagree on the number of tokens")
@@ -270,17 +281,26 @@ def _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq, interl
 
 def rope_append(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq,
                 interleaved: bool = False, rotary_offset: int = 0, amplitude: float = 1.0,
-                q_dtype: torch.dtype = torch.bfloat16, q_out=None, stream=None):
+                q_dtype: torch.dtype = torch.bfloat16, q_out=None, stream=None, pair_axis=None):
     """Rotate q [T, Hq, Dk] and k_new [T, Hkv, Dk] (bf16) by their tokens'
     positions [T] (int64; negative: padding, skipped) and write k_new and
     v_new [T, Hkv, Dv] at slots [T] -> the rotated q (bf16, or fp32 as the
     decode calls take it; q_out may be q itself).  inv_freq: [rotary_dim / 2]
     float64 radians per token (see rope_frequencies); pairs are the halves of
     the rotary part, or neighbours with `interleaved`; amplitude multiplies the
-    rotary part."""
+    rotary part.  With pair_axis [rotary_dim / 2] (int32) the positions have
+    several axes, [axes, T] (time, height, width): pair i turns by those of axis
+    pair_axis[i]; negative on axis 0: padding."""
     desc = _bf16_desc(k_pool, v_pool)
     q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
-                              interleaved, q_dtype, q_out, stream)
+                              interleaved, q_dtype, q_out, stream, pair_axis)
+    if pair_axis is not None:
+        _check("pkv_rope_append_axes", lib.pkv_rope_append_axes(
+            ctypes.byref(desc), _ptr(k_pool), _v_ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
+            _ptr(v_new), _ptr(positions), positions.shape[0], _ptr(pair_axis), _ptr(slots),
+            slots.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), _int32(rotary_offset),
+            float(amplitude), flags, _ptr(q_out), _stream(stream)))
+        return q_out
     _check("pkv_rope_append", lib.pkv_rope_append(
         ctypes.byref(desc), _ptr(k_pool), _v_ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(positions), _ptr(slots), positions.numel(), _ptr(inv_freq),
@@ -292,17 +312,158 @@ def rope_append(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq,
 def rope_append_e4m3(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq, k_scale,
                      v_scale, interleaved: bool = False, rotary_offset: int = 0,
                      amplitude: float = 1.0, q_dtype: torch.dtype = torch.bfloat16, q_out=None,
-                     stream=None):
+                     stream=None, pair_axis=None):
     """rope_append into E4M3 pools (uint8 codes, fp32 scales per KV head)."""
     desc = _e4m3_desc(k_pool, v_pool, k_scale, v_scale)
     q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
-                              interleaved, q_dtype, q_out, stream)
+                              interleaved, q_dtype, q_out, stream, pair_axis)
+    if pair_axis is not None:
+        _check("pkv_rope_append_axes_e4m3", lib.pkv_rope_append_axes_e4m3(
+            ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
+            _ptr(v_new), _ptr(k_scale), _ptr(v_scale), _ptr(positions), positions.shape[0],
+            _ptr(pair_axis), _ptr(slots), slots.numel(), _ptr(inv_freq), 2 * inv_freq.numel(),
+            _int32(rotary_offset), float(amplitude), flags, _ptr(q_out), _stream(stream)))
+        return q_out
     _check("pkv_rope_append_e4m3", lib.pkv_rope_append_e4m3(
         ctypes.byref(desc), _ptr(k_pool), _ptr(v_pool), _ptr(q), q.shape[1], _ptr(k_new),
         _ptr(v_new), _ptr(k_scale), _ptr(v_scale), _ptr(positions), _ptr(slots),
         positions.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), _int32(rotary_offset),
         float(amplitude), flags, _ptr(q_out), _stream(stream)))
     return q_out
+
+
+def cache_desc_int4(k_pool, k_params, v_pool, v_params) -> CacheDesc:
+    """Shape of a 4-bit cache: uint8 code pools [num_blocks, Hkv, block_size, D / 2]
+    and bf16 params [num_blocks, Hkv, block_size, 2] (scale, offset)."""
+    for pool, params, name in ((k_pool, k_params, "k"), (v_pool, v_params, "v")):
+        if isinstance(pool, ValuesInKeys):
+            raise ValueError("values inside the keys need a bf16 cache")
+        _need(pool, name + "_pool", torch.uint8, 4)
+        _need(params, name + "_params", torch.bfloat16, 4)
+        if params.shape != (*pool.shape[:3], 2):
+            raise ValueError(f"{name}_params must be [num_blocks, Hkv, block_size, 2] of its pool")
+    nb, hkv, bs, half_k = k_pool.shape
+    if tuple(v_pool.shape[:3]) != (nb, hkv, bs):
+        raise ValueError("k_pool and v_pool disagree on [num_blocks, Hkv, block_size]")
+    return CacheDesc(nb, bs, hkv, 2 * half_k, 2 * v_pool.shape[3])
+
+
+def kv_append_int4(k_pool, k_params, v_pool, v_params, k_new, v_new, slots, stream=None) -> None:
+    """Quantise k_new [T, Hkv, Dk] / v_new [T, Hkv, Dv] (bf16) into the 4-bit pools at
+    slots [T] (int64; negative: skipped), each row with its own scale and offset."""
+    desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
+    _need(k_new, "k_new", torch.bfloat16, 3)
+    _need(v_new, "v_new", torch.bfloat16, 3)
+    _need(slots, "slot_mapping", torch.int64, 1)
+    T = slots.numel()
+    if k_new.shape != (T, desc.num_kv_heads, desc.head_dim_k) or \
+            v_new.shape != (T, desc.num_kv_heads, desc.head_dim_v):
+        raise ValueError("k_new and v_new must be [tokens, Hkv, D] of the cache")
+    _check("pkv_kv_append_int4", lib.pkv_kv_append_int4(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(k_params), _ptr(v_pool), _ptr(v_params),
+        _ptr(k_new), _ptr(v_new), _ptr(slots), T, _stream(stream)))
+
+
+def copy_blocks_int4(k_pool, k_params, v_pool, v_params, src, dst, stream=None) -> None:
+    """copy_blocks for 4-bit pools (codes and params)."""
+    desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
+    _need(src, "src", torch.int32, 1)
+    _need(dst, "dst", torch.int32, 1)
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst lengths differ")
+    _check("pkv_copy_blocks_int4", lib.pkv_copy_blocks_int4(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(k_params), _ptr(v_pool), _ptr(v_params),
+        _ptr(src), _ptr(dst), src.numel(), _stream(stream)))
+
+
+def rope_append_int4(k_pool, k_params, v_pool, v_params, q, k_new, v_new, positions, slots,
+                     inv_freq, interleaved: bool = False, rotary_offset: int = 0,
+                     amplitude: float = 1.0, q_dtype: torch.dtype = torch.bfloat16, q_out=None,
+                     stream=None, pair_axis=None):
+    """rope_append into a 4-bit cache; the rotated keys are quantised from fp32."""
+    desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
+    q_out, flags = _rope_args(desc, v_pool, q, k_new, v_new, positions, slots, inv_freq,
+                              interleaved, q_dtype, q_out, stream, pair_axis)
+    _check("pkv_rope_append_int4", lib.pkv_rope_append_int4(
+        ctypes.byref(desc), _ptr(k_pool), _ptr(k_params), _ptr(v_pool), _ptr(v_params), _ptr(q),
+        q.shape[1], _ptr(k_new), _ptr(v_new), _ptr(positions),
+        1 if pair_axis is None else positions.shape[0], _ptr(pair_axis), _ptr(slots),
+        slots.numel(), _ptr(inv_freq), 2 * inv_freq.numel(), _int32(rotary_offset),
+        float(amplitude), flags, _ptr(q_out), _stream(stream)))
+    return q_out
+
+
+def block_pool(num_blocks: int, device=None, order=None):
+    """The free blocks of extend_sequences and trim_sequences, all of them free ->
+    (free_blocks [num_blocks] int32, pool_state [4] int32).  `order`: the order in
+    which they are first taken (default 0, 1, 2, ...)."""
+    order = range(num_blocks) if order is None else [int(x) for x in order]
+    if sorted(order) != list(range(num_blocks)):
+        raise ValueError("order must be a permutation of 0 .. num_blocks - 1")
+    device = "cuda" if device is None else device
+    free = torch.tensor(list(order)[::-1], dtype=torch.int32, device=device)
+    return free, torch.tensor([num_blocks, 0, 0, 0], dtype=torch.int32, device=device)
+
+
+def _tables_args(block_tables, seq_lens, change, name, free_blocks, pool_state):
+    """Checks of the calls that keep block tables on the device."""
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(change, name, torch.int32, 1)
+    _need(free_blocks, "free_blocks", torch.int32, 1)
+    _need(pool_state, "pool_state", torch.int32, 1)
+    B = seq_lens.numel()
+    if block_tables.shape[0] != B or change.numel() != B:
+        raise ValueError(f"block_tables and {name} must have one row per seq_len")
+    if pool_state.numel() != 4:
+        raise ValueError("pool_state must have 4 entries (see block_pool)")
+
+
+def extend_sequences(block_tables, seq_lens, new_lens, free_blocks, pool_state, block_size: int,
+                     num_tokens: int, cu_q_lens=None, positions=None, slots=None, stream=None):
+    """Give each sequence the blocks of new_lens [B] (int32) more tokens: block_tables
+    [B, max_blocks], seq_lens [B] and the pool (see block_pool) change in place ->
+    (cu_q_lens [B + 1] int32, positions [num_tokens] int64, slots [num_tokens] int64) of
+    the tokens brought, rows past them -1.  A sequence for which rows, table or free
+    blocks do not suffice brings none (device_status says which)."""
+    _tables_args(block_tables, seq_lens, new_lens, "new_lens", free_blocks, pool_state)
+    B, T = seq_lens.numel(), int(num_tokens)
+    if not 0 <= T < 2 ** 31:
+        raise ValueError("num_tokens must be within 0 .. 2^31 - 1")
+    if stream is not None and (cu_q_lens is None or positions is None or slots is None):
+        # what is allocated here is written on that stream: let it belong to it
+        with torch.cuda.stream(stream):
+            return extend_sequences(block_tables, seq_lens, new_lens, free_blocks, pool_state,
+                                    block_size, num_tokens, cu_q_lens, positions, slots)
+    dev = seq_lens.device
+    if cu_q_lens is None:
+        cu_q_lens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int64, device=dev)
+    if slots is None:
+        slots = torch.empty(T, dtype=torch.int64, device=dev)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
+    _need(positions, "positions", torch.int64, 1)
+    _need(slots, "slots", torch.int64, 1)
+    if cu_q_lens.numel() != B + 1 or positions.numel() != T or slots.numel() != T:
+        raise ValueError("cu_q_lens must have B + 1, positions and slots num_tokens entries")
+    _check("pkv_extend_sequences", lib.pkv_extend_sequences(
+        _int32(block_size), free_blocks.numel(), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(new_lens), B, block_tables.shape[1], _ptr(free_blocks), _ptr(pool_state), T,
+        _ptr(cu_q_lens), _ptr(positions), _ptr(slots), _stream(stream)))
+    return cu_q_lens, positions, slots
+
+
+def trim_sequences(block_tables, seq_lens, keep_lens, free_blocks, pool_state, block_size: int,
+                   stream=None) -> None:
+    """Cut each sequence to its first keep_lens [B] (int32; negative: as it is) tokens and
+    give the blocks past them back: seq_lens and the pool change in place.  Trimming to
+    the old lengths undoes an extend exactly."""
+    _tables_args(block_tables, seq_lens, keep_lens, "keep_lens", free_blocks, pool_state)
+    _check("pkv_trim_sequences", lib.pkv_trim_sequences(
+        _int32(block_size), free_blocks.numel(), _ptr(block_tables), _ptr(seq_lens),
+        _ptr(keep_lens), seq_lens.numel(), block_tables.shape[1], _ptr(free_blocks),
+        _ptr(pool_state), _stream(stream)))
 
 
 def interleave_slot_mapping(k_pool, v_pool, first_token: int, num_tokens: int, num_parts: int,
@@ -485,6 +646,115 @@ def paged_decode_attn_multi_e4m3(q, k_pool, v_pool, k_scale, v_scale, block_tabl
         S, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse),
         int(flags), _stream(stream)))
     return out, lse
+
+
+def _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, multi):
+    """Checks of the decode calls over a 4-bit cache -> (desc, batch, tokens, heads)."""
+    desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
+    _need(q, "q", torch.float32, 4 if multi else 3)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B, T, Hq, Dk = q.shape if multi else (q.shape[0], 1, *q.shape[1:])
+    if Dk != desc.head_dim_k:
+        raise ValueError(f"q must have head dim {desc.head_dim_k}, got {Dk}")
+    if seq_lens.numel() != B or block_tables.shape[0] != B:
+        raise ValueError("seq_lens and block_tables must have one row per sequence of q")
+    return desc, B, T, Hq
+
+
+def decode_auto_splits_int4(k_pool, k_params, v_pool, v_params, batch: int, num_q_heads: int,
+                            max_seq_len: int, tokens_per_seq: int = 1, flags: int = 0) -> int:
+    desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
+    return int(lib.pkv_decode_auto_splits_int4(ctypes.byref(desc), batch, tokens_per_seq,
+                                               num_q_heads, _int32(max_seq_len), int(flags)))
+
+
+def _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
+               num_splits, workspace, out, lse, flags, stream, multi):
+    desc, B, T, Hq = _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
+                                multi)
+    shape = (*q.shape[:-1], desc.head_dim_v)
+    if workspace is not None:
+        _need(workspace, "workspace", workspace.dtype)
+    S = _int32(num_splits) or int(lib.pkv_decode_auto_splits_int4(
+        ctypes.byref(desc), B, T, Hq, _int32(block_tables.shape[1] * desc.block_size),
+        int(flags)))
+    # (a split count that the call refuses needs no workspace)
+    need = decode_workspace_size(B * T, Hq, desc.head_dim_v, S) if S <= 256 else 0
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if stream is not None and (out is None or lse is None or ws_bytes < need):
+        # what is allocated here is used on that stream: let it belong to it
+        with torch.cuda.stream(stream):
+            return _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables,
+                              seq_lens, scale, num_splits, workspace, out, lse, flags, None,
+                              multi)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+    _need(out, "out", torch.float32, len(shape))
+    _need(lse, "lse", torch.float32, len(shape) - 1)
+    if out.shape != shape or lse.shape != shape[:-1]:
+        raise ValueError("out and lse must have q's rows (and the cache's value dim)")
+    if ws_bytes < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = need
+    rows = (B, T) if multi else (B,)
+    _check(name, getattr(lib, name)(
+        ctypes.byref(desc), _ptr(q), *rows, Hq, _ptr(k_pool), _ptr(k_params), _ptr(v_pool),
+        _ptr(v_params), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), float(scale),
+        S, _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse), int(flags), _stream(stream)))
+    return out, lse
+
+
+def paged_decode_attn_int4(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
+                           scale: float, num_splits: int = 0, workspace=None, out=None,
+                           lse=None, flags: int = 0, stream=None):
+    """Decode attention of q [B, Hq, Dk] over a 4-bit cache -> (out, lse); num_splits 0
+    lets the library choose."""
+    return _attn_int4("pkv_paged_decode_attn_int4", q, k_pool, k_params, v_pool, v_params,
+                      block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
+                      stream, False)
+
+
+def paged_decode_attn_multi_int4(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
+                                 scale: float, num_splits: int = 0, workspace=None, out=None,
+                                 lse=None, flags: int = 0, stream=None):
+    """The multi-token step (q [B, T, Hq, Dk], causal over the last T tokens) over a
+    4-bit cache -> (out [B, T, Hq, Dv], lse [B, T, Hq])."""
+    return _attn_int4("pkv_paged_decode_attn_multi_int4", q, k_pool, k_params, v_pool, v_params,
+                      block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
+                      stream, True)
+
+
+def paged_decode_attn_partial_int4(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
+                                   scale: float, num_splits: int, out_part=None, lse_part=None,
+                                   flags: int = 0, stream=None):
+    """Per-split partials over a 4-bit cache -> (out_part [S, B, Hq, Dv],
+    lse_part [S, B, Hq])."""
+    desc, B, _, Hq = _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
+                                False)
+    S = _int32(num_splits)
+    if not 1 <= S <= 256:
+        raise ValueError("num_splits must be within 1 .. 256")
+    if stream is not None and (out_part is None or lse_part is None):
+        with torch.cuda.stream(stream):
+            return paged_decode_attn_partial_int4(
+                q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale, num_splits,
+                out_part, lse_part, flags)
+    if out_part is None:
+        out_part = torch.empty(S, B, Hq, desc.head_dim_v, dtype=torch.float32, device=q.device)
+    if lse_part is None:
+        lse_part = torch.empty(S, B, Hq, dtype=torch.float32, device=q.device)
+    _need(out_part, "out_part", torch.float32, 4)
+    _need(lse_part, "lse_part", torch.float32, 3)
+    if out_part.shape != (S, B, Hq, desc.head_dim_v) or lse_part.shape != (S, B, Hq):
+        raise ValueError("out_part must be [S, B, Hq, Dv] and lse_part [S, B, Hq]")
+    _check("pkv_paged_decode_attn_partial_int4", lib.pkv_paged_decode_attn_partial_int4(
+        ctypes.byref(desc), _ptr(q), B, Hq, _ptr(k_pool), _ptr(k_params), _ptr(v_pool),
+        _ptr(v_params), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), float(scale),
+        S, _ptr(out_part), _ptr(lse_part), int(flags), _stream(stream)))
+    return out_part, lse_part
 
 
 def paged_decode_attn_partial(q, k_pool, v_pool, block_tables, seq_lens, scale: float,

@@ -25,6 +25,8 @@ DEV_TIMEOUT = 0x10
 DEV_TABLE_RANGE = 0x20
 DEV_PREFIX = 0x40
 DEV_QUERY_RANGE = 0x80
+DEV_NO_BLOCKS = 0x100
+DEV_AXIS = 0x200
 DECODE_GENERIC = 0x1
 DECODE_NO_TCGEN05 = 0x2
 ROPE_INTERLEAVED = 0x1
@@ -56,6 +58,27 @@ SIGNATURES = {
                                        _i32, _f32, _i32, _P, _P]),
     "pkv_rope_append_e4m3": (ctypes.c_int, [_DESC, _P, _P, _P, _i32, _P, _P, _P, _P, _P, _P,
                                             _i64, _P, _i32, _i32, _f32, _i32, _P, _P]),
+    "pkv_rope_append_axes": (ctypes.c_int, [_DESC, _P, _P, _P, _i32, _P, _P, _P, _i32, _P, _P,
+                                            _i64, _P, _i32, _i32, _f32, _i32, _P, _P]),
+    "pkv_rope_append_axes_e4m3": (ctypes.c_int, [_DESC, _P, _P, _P, _i32, _P, _P, _P, _P, _P,
+                                                 _i32, _P, _P, _i64, _P, _i32, _i32, _f32, _i32,
+                                                 _P, _P]),
+    "pkv_kv_append_int4": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _P, _P, _P, _i64, _P]),
+    "pkv_copy_blocks_int4": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _P, _P, _i32, _P]),
+    "pkv_rope_append_int4": (ctypes.c_int, [_DESC, _P, _P, _P, _P, _P, _i32, _P, _P, _P, _i32, _P,
+                                            _P, _i64, _P, _i32, _i32, _f32, _i32, _P, _P]),
+    "pkv_extend_sequences": (ctypes.c_int, [_i32, _i32, _P, _P, _P, _i32, _i32, _P, _P, _i32, _P,
+                                            _P, _P, _P]),
+    "pkv_trim_sequences": (ctypes.c_int, [_i32, _i32, _P, _P, _P, _i32, _i32, _P, _P, _P]),
+    "pkv_decode_auto_splits_int4": (_i32, [_DESC, _i32, _i32, _i32, _i32, _i32]),
+    "pkv_paged_decode_attn_int4": (ctypes.c_int, [_DESC, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32,
+                                                  _P, _f32, _i32, _P, _sz, _P, _P, _i32, _P]),
+    "pkv_paged_decode_attn_multi_int4": (ctypes.c_int, [_DESC, _P, _i32, _i32, _i32, _P, _P, _P,
+                                                        _P, _P, _i32, _P, _f32, _i32, _P, _sz,
+                                                        _P, _P, _i32, _P]),
+    "pkv_paged_decode_attn_partial_int4": (ctypes.c_int, [_DESC, _P, _i32, _i32, _P, _P, _P, _P,
+                                                          _P, _i32, _P, _f32, _i32, _P, _P, _i32,
+                                                          _P]),
     "pkv_chunk_workspace_size": (_sz, [_DESC, _i64, _i32, _i32, _i32, _i32]),
     "pkv_chunk_workspace_size_e4m3": (_sz, [_DESC, _i64, _i32, _i32, _i32, _i32]),
     "pkv_paged_chunk_attn": (ctypes.c_int, [_DESC, _P, _i64, _i32, _P, _i32, _P, _P, _P, _i32, _P,

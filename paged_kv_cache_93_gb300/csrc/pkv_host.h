@@ -191,6 +191,29 @@ size_t chunk_tc_workspace(const pkv_cache_desc &c, int64_t num_tokens, int32_t b
                           int32_t num_q_heads);
 int launch_chunk_tc(const ChunkArgs &a, void *workspace);
 
+// 4-bit pools: the checks of their shape, and the per-split decode kernels.  Arguments
+// are already validated; out_part / lse_part are [S][batch * q_tokens][Hq][Dv] /
+// [S][batch * q_tokens][Hq].
+int validate_int4_cache(const pkv_cache_desc *c);
+struct Int4DecodeArgs {
+    pkv_cache_desc cache;
+    const float *q;                       // [batch][q_tokens][Hq][Dk]
+    int32_t batch, q_tokens, num_q_heads;
+    const uint8_t *k_pool, *v_pool;
+    const uint32_t *k_params, *v_params;  // bf16 pairs: scale in bits 0-15, offset in 16-31
+    const int32_t *block_tables;
+    int32_t max_blocks;
+    const int32_t *seq_lens;
+    float scale;
+    int32_t num_splits;
+    float *out_part, *lse_part;
+    uint32_t *status;
+    // a sequence shorter than this sets PKV_DEV_SEQ_LEN
+    int32_t flag_below;
+    cudaStream_t stream;
+};
+int launch_decode_int4_generic(const Int4DecodeArgs &a);
+
 int launch_lse_merge(int32_t num_parts, const float *out_part, const float *lse_part,
                      int64_t rows, int32_t head_dim_v, float *out, float *lse,
                      cudaStream_t stream);

@@ -16,6 +16,11 @@
 // signed number of 2^-32 turns, are rounded to binary32 (2^-26 turns) for
 // sincospif.
 //
+// Several axes.  With pair_axis each pair takes its position from its own axis (time,
+// height, width of an image's or a video's tokens): positions is then [axes][tokens].
+// Only the loads of the positions differ; a token's pairs are spread over lanes either
+// way, each lane with the rows of its own pairs' axes.
+//
 // Bound: memory.  Every q, k and v element is read once and written once, as
 // 16-byte vectors; cosines and sines (rotary_dim / 2 of them against (Hq + Hkv) *
 // head_dim elements) are computed once for all of a token's heads, or for a part of
@@ -28,9 +33,13 @@
 #include "pkv.h"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
+#include "pkv_int4.cuh"
 
 namespace pkv {
 namespace {
+
+// How a pool holds its rows.
+constexpr int kBf16 = 0, kE4m3 = 1, kInt4 = 2;
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 512;           // head dims up to 1024
@@ -39,7 +48,9 @@ struct RopeArgs {
     const uint16_t *q, *k_new, *v_new;   // bf16
     const int64_t *positions, *slots;
     const double *inv_freq;
+    const int32_t *pair_axis;            // nullptr: one axis
     const float *k_scale, *v_scale;      // E4M3 pools
+    uint32_t *k_params, *v_params;       // 4-bit pools
     void *k_pool, *v_pool, *q_out;
     uint32_t *status;
     int64_t num_tokens, num_slots;
@@ -52,6 +63,7 @@ struct RopeArgs {
     int32_t group, parts;                // tokens of a work item; items of a token
     float amplitude;
     int32_t q_fp32, in_place;
+    int32_t axes;
 };
 
 // x / n for x * n < 2^32, by multiplication with magic = ceil(2^32 / n).
@@ -101,6 +113,17 @@ __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
     return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
 }
 
+// Where a pair's positions begin: its axis's row of them.
+__device__ __forceinline__ int64_t axis_row(const RopeArgs &a, int pair) {
+    if (!a.pair_axis) return 0;
+    int32_t axis = a.pair_axis[pair];
+    if (axis < 0 || axis >= a.axes) {
+        raise_status(a.status, PKV_DEV_AXIS);
+        axis = 0;
+    }
+    return axis * a.num_tokens;
+}
+
 // VEC: rotary_dim and rotary_offset let whole 16-byte vectors rotate (half
 // layout: both multiples of 16 and 8; interleaved: multiples of 8).  Otherwise
 // a unit is a single pair, or a single element outside the rotary part.
@@ -113,10 +136,12 @@ rope_append_kernel(const RopeArgs a) {
     pdl_launch_dependents();
     // this thread's frequencies (kMaxPairs / kThreads at most)
     uint64_t step[kMaxPairs / kThreads];
+    int64_t arow[kMaxPairs / kThreads];
 #pragma unroll
     for (int i = 0; i < kMaxPairs / kThreads; ++i) {
         const int pr = threadIdx.x + i * kThreads;
         step[i] = pr < npairs ? turn_step(a.inv_freq[pr]) : 0;
+        arow[i] = pr < npairs ? axis_row(a, pr) : 0;
     }
     const int rows_qk = a.hq + a.hkv;
     const int n_qk = rows_qk * a.q_units, n_all = n_qk + a.hkv * a.v_units;
@@ -130,7 +155,8 @@ rope_append_kernel(const RopeArgs a) {
         for (int i = 0; i < kMaxPairs / kThreads; ++i) {
             const int pr = threadIdx.x + i * kThreads;
             if (pr < npairs) {
-                const uint64_t turn = step[i] * uint64_t(pos);
+                const uint64_t turn =
+                    step[i] * uint64_t(a.pair_axis ? a.positions[arow[i] + t] : pos);
                 // signed 2^-32 turns; sincospif takes half turns
                 const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
                 float s, c;
@@ -285,12 +311,16 @@ __global__ void __launch_bounds__(kThreads, kWideCtas)
 rope_append_wide_kernel(const RopeArgs a) {
     __shared__ __align__(16) float2 cs[2][kTable];   // (cos, sin) * amplitude
     __shared__ uint64_t step[kMaxPairs];
+    __shared__ int64_t arow[kMaxPairs];
     __shared__ int64_t s_slot[2][8];             // slot of a token's rows, or -1: not stored
     __shared__ int32_t s_live[2][8];
     const int npairs = a.rot >> 1;
     pdl_wait();
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < npairs; i += kThreads) step[i] = turn_step(a.inv_freq[i]);
+    for (int i = threadIdx.x; i < npairs; i += kThreads) {
+        step[i] = turn_step(a.inv_freq[i]);
+        arow[i] = axis_row(a, i);
+    }
     __syncthreads();
     // this thread's unit of a row, and the row it takes first
     const int r0 = fast_div(threadIdx.x, a.q_magic, a.q_units), c = threadIdx.x - r0 * a.q_units;
@@ -431,7 +461,7 @@ rope_append_wide_kernel(const RopeArgs a) {
         }
         for (int i = threadIdx.x; i < ntok * npairs; i += kThreads) {
             const int tk = a.group > 1 ? i / npairs : 0, pr = i - tk * npairs;
-            const uint64_t turn = step[pr] * uint64_t(a.positions[t0 + tk]);
+            const uint64_t turn = step[pr] * uint64_t(a.positions[arow[pr] + t0 + tk]);
             // signed 2^-32 turns; sincospif takes half turns
             const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
             float s, co;
@@ -470,7 +500,7 @@ rope_append_wide_kernel(const RopeArgs a) {
 constexpr int kWarpAhead = 2;
 constexpr int kWarpCtas = 3;             // per SM
 
-template <bool INTER, bool E4>
+template <bool INTER, int FMT>
 __global__ void __launch_bounds__(kThreads, kWarpCtas)
 rope_append_warp_kernel(const RopeArgs a) {
     pdl_wait();
@@ -494,9 +524,13 @@ rope_append_warp_kernel(const RopeArgs a) {
     }
     // this lane's pairs: lane and lane + 32
     uint64_t step[2];
+    int64_t arow[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        step[i] = lane + 32 * i < npairs ? turn_step(a.inv_freq[lane + 32 * i]) : 0;
+    for (int i = 0; i < 2; ++i) {
+        const bool has = lane + 32 * i < npairs;
+        step[i] = has ? turn_step(a.inv_freq[lane + 32 * i]) : 0;
+        arow[i] = has ? axis_row(a, lane + 32 * i) : 0;
+    }
     const int pq = (a.hq + rpp - 1) >> (5 - shift), pk = (a.hkv + rpp - 1) >> (5 - shift);
     const int passes = pq + pk + (a.dv ? pk : 0), per = (passes + a.parts - 1) / a.parts;
     const int64_t items = a.num_tokens * a.parts;
@@ -540,7 +574,8 @@ rope_append_warp_kernel(const RopeArgs a) {
             float c2[2], s2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint64_t turn = step[i] * uint64_t(pos);
+                const uint64_t turn =
+                    step[i] * uint64_t(a.pair_axis ? a.positions[arow[i] + t] : pos);
                 // signed 2^-32 turns; sincospif takes half turns
                 sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s2[i], &c2[i]);
                 c2[i] *= a.amplitude;
@@ -589,7 +624,7 @@ rope_append_warp_kernel(const RopeArgs a) {
             if (is_q ? a.in_place && !turned : !stored) return;
             const int64_t dst =
                 (is_q ? t * a.hq + row : row0 + int64_t(row) * a.block_size) * a.dk;
-            if (is_q ? !a.q_fp32 : !E4) {
+            if (is_q ? !a.q_fp32 : FMT == kBf16) {
                 // to bf16: copied elements as they came
                 if (turned && (is_q || is_k)) {
                     float x[8], y[8];
@@ -611,6 +646,19 @@ rope_append_warp_kernel(const RopeArgs a) {
             if (is_q) {
                 store8_f32(a.q_out, dst + ea, x);
                 store8_f32(a.q_out, dst + eb, y);
+            } else if constexpr (FMT == kInt4) {
+                // the row's extent over its U lanes, which are all here
+                float low = INFINITY, high = -INFINITY, odd = 0.f;
+                int4_extent8(x, low, high, odd);
+                int4_extent8(y, low, high, odd);
+                const uint32_t group = U == 32 ? 0xffffffffu : ((1u << U) - 1) << (lane & ~(U - 1));
+                const Int4Scale sc = int4_row_scale(low, high, odd, U, group);
+                uint32_t *to = reinterpret_cast<uint32_t *>(
+                    static_cast<uint8_t *>(is_k ? a.k_pool : a.v_pool) + dst / 2);
+                to[(is_k ? ea : 16 * c) / 8] = int4_codes8(x, sc);
+                to[(is_k ? eb : 16 * c + 8) / 8] = int4_codes8(y, sc);
+                if (c == 0)
+                    (is_k ? a.k_params : a.v_params)[row0 + int64_t(row) * a.block_size] = sc.params;
             } else {
                 const float s = (is_k ? a.k_scale : a.v_scale)[row];
                 store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + (is_k ? ea : 16 * c), x, s);
@@ -627,9 +675,128 @@ rope_append_warp_kernel(const RopeArgs a) {
     }
 }
 
+// The form of the 4-bit pools' other shapes: a CTA a token, a warp a row, which stays in
+// the warp's registers because its scale needs all of it (a lane holds up to four
+// vectors of 8 elements).  A rotary element loads its pair's other element by itself,
+// so that any rotary part runs; that load hits the cache.
+template <bool INTER>
+__global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeArgs a) {
+    __shared__ float2 cs[2][kMaxPairs];          // (cos, sin) * amplitude, by token parity
+    const int npairs = a.rot >> 1, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    uint64_t step[kMaxPairs / kThreads];
+    int64_t arow[kMaxPairs / kThreads];
+#pragma unroll
+    for (int i = 0; i < kMaxPairs / kThreads; ++i) {
+        const int pr = threadIdx.x + i * kThreads;
+        step[i] = pr < npairs ? turn_step(a.inv_freq[pr]) : 0;
+        arow[i] = pr < npairs ? axis_row(a, pr) : 0;
+    }
+    int buf = 0;
+    for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
+        if (a.positions[t] < 0) continue;        // padding (uniform in the CTA)
+        const int64_t slot = a.slots[t];
+        float2 *tab = cs[buf];
+#pragma unroll
+        for (int i = 0; i < kMaxPairs / kThreads; ++i) {
+            const int pr = threadIdx.x + i * kThreads;
+            if (pr < npairs) {
+                const uint64_t turn = step[i] * uint64_t(a.positions[arow[i] + t]);
+                // signed 2^-32 turns; sincospif takes half turns
+                float s, c;
+                sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
+                tab[pr] = make_float2(c * a.amplitude, s * a.amplitude);
+            }
+        }
+        const bool stored = slot >= 0 && slot < a.num_slots;
+        if (slot >= a.num_slots && threadIdx.x == 0) raise_status(a.status, PKV_DEV_SLOT);
+        const int64_t block = stored ? slot / a.block_size : 0;
+        const int64_t row0 =
+            block * a.hkv * a.block_size + (stored ? slot - block * a.block_size : 0);
+        __syncthreads();
+        const int rows = a.hq + (stored ? 2 * a.hkv : 0);
+        for (int row = threadIdx.x >> 5; row < rows; row += kThreads / 32) {
+            const bool is_q = row < a.hq, is_k = !is_q && row < a.hq + a.hkv;
+            const int g = is_q ? row : is_k ? row - a.hq : row - a.hq - a.hkv;
+            const int d = is_q || is_k ? a.dk : a.dv;
+            const uint16_t *src = is_q   ? a.q + (t * a.hq + g) * a.dk
+                                  : is_k ? a.k_new + (t * a.hkv + g) * a.dk
+                                         : a.v_new + (t * a.hkv + g) * a.dv;
+            uint4 raw[4];
+            float x[4][8];
+            bool turned[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int e0 = (lane + 32 * n) * 8;
+                turned[n] = false;
+                if (e0 >= d) continue;
+                raw[n] = *reinterpret_cast<const uint4 *>(src + e0);
+                unpack8(raw[n], x[n]);
+                if (!is_q && !is_k) continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rel = e0 + i - a.off;
+                    if (rel < 0 || rel >= a.rot) continue;
+                    const bool first = INTER ? (rel & 1) == 0 : rel < npairs;
+                    const int other = INTER ? (first ? 1 : -1) : (first ? npairs : -npairs);
+                    const float2 r = tab[INTER ? rel >> 1 : first ? rel : rel - npairs];
+                    const float y = __uint_as_float(uint32_t(src[e0 + i + other]) << 16);
+                    x[n][i] = first ? x[n][i] * r.x - y * r.y : x[n][i] * r.x + y * r.y;
+                    turned[n] = true;
+                }
+            }
+            __syncwarp();                        // q_out may be q: all of the row is read
+            if (is_q) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int e0 = (lane + 32 * n) * 8;
+                    if (e0 >= d) continue;
+                    const int64_t at = (t * a.hq + g) * a.dk + e0;
+                    if (a.q_fp32) {
+                        store8_f32(a.q_out, at, x[n]);
+                    } else if (turned[n]) {
+                        // elements outside the rotary part are bf16 and come back as they were
+                        // but for a NaN's bits, which the raw vector keeps
+                        const uint4 y = pack8(x[n]);
+                        const uint32_t was[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+                        const uint32_t now[4] = {y.x, y.y, y.z, y.w};
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int rel = e0 + 2 * i - a.off;
+                            const uint32_t keep =
+                                (rel < 0 || rel >= a.rot ? 0xffffu : 0u) |
+                                (rel + 1 < 0 || rel + 1 >= a.rot ? 0xffff0000u : 0u);
+                            w[i] = (was[i] & keep) | (now[i] & ~keep);
+                        }
+                        store8_raw(a.q_out, at, make_uint4(w[0], w[1], w[2], w[3]));
+                    } else {
+                        store8_raw(a.q_out, at, raw[n]);
+                    }
+                }
+                continue;
+            }
+            float low = INFINITY, high = -INFINITY, odd = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if ((lane + 32 * n) * 8 < d) int4_extent8(x[n], low, high, odd);
+            const Int4Scale sc = int4_row_scale(low, high, odd, 32, 0xffffffffu);
+            const int64_t to = row0 + int64_t(g) * a.block_size;
+            uint32_t *codes = reinterpret_cast<uint32_t *>(
+                static_cast<uint8_t *>(is_k ? a.k_pool : a.v_pool) + to * (d / 2));
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if ((lane + 32 * n) * 8 < d) codes[lane + 32 * n] = int4_codes8(x[n], sc);
+            if (lane == 0) (is_k ? a.k_params : a.v_params)[to] = sc.params;
+        }
+        buf ^= 1;      // the other table: this one may still be read by slower warps
+    }
+}
+
 uint32_t magic_of(int n) { return n > 1 ? uint32_t(((uint64_t(1) << 32) + n - 1) / n) : 0; }
 
-template <bool E4>
+template <int FMT>
 int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     // Parts of a token: the fewest rounds of warps x (passes of a part + 2 for its
     // angles), so that few tokens spread over the device and the last round of
@@ -651,8 +818,25 @@ int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     const int64_t items = a.num_tokens * a.parts;
     const dim3 grid(unsigned(std::min<int64_t>((items + per_cta - 1) / per_cta,
                                                int64_t(sm_count()) * kWarpCtas)));
-    return launch_pdl(interleaved ? rope_append_warp_kernel<true, E4>
-                                  : rope_append_warp_kernel<false, E4>,
+    return launch_pdl(interleaved ? rope_append_warp_kernel<true, FMT>
+                                  : rope_append_warp_kernel<false, FMT>,
+                      grid, dim3(kThreads), 0, stream, a);
+}
+
+// Whether the form of a warp a token takes the shape.
+bool warp_takes(const RopeArgs &a) {
+    const int units = a.dk / 16;
+    return a.dk % 64 == 0 && (units & (units - 1)) == 0 && units <= 32 &&
+           (a.dv == 0 || a.dv == a.dk) && a.rot % 16 == 0 && a.off % 16 == 0 && a.rot <= 128;
+}
+
+int launch_int4(RopeArgs &a, bool interleaved, cudaStream_t stream) {
+    if (warp_takes(a)) {
+        a.q_units = a.dk / 16;
+        return launch_warp<kInt4>(a, interleaved, stream);
+    }
+    const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, int64_t(sm_count()) * 4)));
+    return launch_pdl(interleaved ? rope_append_int4_kernel<true> : rope_append_int4_kernel<false>,
                       grid, dim3(kThreads), 0, stream, a);
 }
 
@@ -660,11 +844,9 @@ template <bool E4>
 int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     const int64_t units16 =
         (int64_t(a.hq) + a.hkv) * (a.dk / 16) + int64_t(a.hkv) * (a.dv / 16);
-    const int units = a.dk / 16;
-    if (a.dk % 64 == 0 && (units & (units - 1)) == 0 && units <= 32 &&
-        (a.dv == 0 || a.dv == a.dk) && a.rot % 16 == 0 && a.off % 16 == 0 && a.rot <= 128) {
-        a.q_units = units;
-        return launch_warp<E4>(a, interleaved, stream);
+    if (warp_takes(a)) {
+        a.q_units = a.dk / 16;
+        return launch_warp<E4 ? kE4m3 : kBf16>(a, interleaved, stream);
     }
     if (a.dk % 16 == 0 && a.dv % 16 == 0 && a.dv <= a.dk && a.rot % 16 == 0 && a.off % 16 == 0) {
         a.q_units = a.dk / 16;
@@ -700,12 +882,14 @@ int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
 }
 
 // The host checks both entry points share; fills everything but the pools'
-// scales.  *done: nothing to launch.
-int prepare(RopeArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int32_t hq,
-            const void *k_new, const void *v_new, const int64_t *positions, const int64_t *slots,
-            int64_t num_tokens, const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
+// scales and the status word.  *done: nothing to launch.
+int prepare(RopeArgs &a, int fmt, const pkv_cache_desc *c, const void *q, int32_t hq,
+            const void *k_new, const void *v_new, const int64_t *positions, int32_t num_axes,
+            const int32_t *pair_axis, const int64_t *slots, int64_t num_tokens, const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
             float amplitude, int32_t flags, void *k_pool, void *v_pool, void *q_out, bool *done) {
     *done = false;
+    const bool e4 = fmt == kE4m3;
+    if (num_axes < 1 || num_axes > 8 || (num_axes > 1 && !pair_axis)) return PKV_ERR_INVALID_ARG;
     if (!c || num_tokens < 0 || hq <= 0 || (flags & ~(PKV_ROPE_INTERLEAVED | PKV_ROPE_Q_FP32)) ||
         !std::isfinite(amplitude))
         return PKV_ERR_INVALID_ARG;
@@ -725,8 +909,8 @@ int prepare(RopeArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int32_
     if (!q || !q_out || !k_new || !k_pool || !positions || !slots || !inv_freq ||
         !v_pool != !v_new)
         return PKV_ERR_INVALID_ARG;
-    if (!v_pool && (e4 || c->head_dim_v > c->head_dim_k))
-        return e4 ? PKV_ERR_INVALID_ARG : PKV_ERR_SHAPE;
+    if (!v_pool && (fmt != kBf16 || c->head_dim_v > c->head_dim_k))
+        return fmt != kBf16 ? PKV_ERR_INVALID_ARG : PKV_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || (v_new && !aligned16(v_new)))
         return PKV_ERR_ALIGNMENT;
     const uintptr_t pool_mask = e4 ? 7 : 15;
@@ -735,14 +919,14 @@ int prepare(RopeArgs &a, bool e4, const pkv_cache_desc *c, const void *q, int32_
         return PKV_ERR_ALIGNMENT;
     const bool fp32 = (flags & PKV_ROPE_Q_FP32) != 0;
     if (fp32 && q_out == q) return PKV_ERR_INVALID_ARG;      // wider than its input
-    a.status = status_word();
-    if (!a.status) return PKV_ERR_CUDA;
     a.q = static_cast<const uint16_t *>(q);
     a.k_new = static_cast<const uint16_t *>(k_new);
     a.v_new = static_cast<const uint16_t *>(v_new);
     a.positions = positions;
     a.slots = slots;
     a.inv_freq = inv_freq;
+    a.pair_axis = pair_axis;
+    a.axes = num_axes;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
     a.q_out = q_out;
@@ -789,19 +973,54 @@ extern "C" int pkv_rope_frequencies(int32_t rotary_dim, double theta, double fac
     return PKV_OK;
 }
 
+namespace {
+int append_bf16(const pkv_cache_desc *cache, void *k_pool, void *v_pool, const void *q,
+                int32_t num_q_heads, const void *k_new, const void *v_new,
+                const int64_t *positions, int32_t num_axes, const int32_t *pair_axis,
+                const int64_t *slot_mapping, int64_t num_tokens, const double *inv_freq,
+                int32_t rotary_dim, int32_t rotary_offset, float amplitude, int32_t flags,
+                void *q_out, pkv_stream_t stream) {
+    RopeArgs a = {};
+    bool done;
+    const int rc = prepare(a, kBf16, cache, q, num_q_heads, k_new, v_new, positions, num_axes,
+                           pair_axis, slot_mapping, num_tokens, inv_freq, rotary_dim,
+                           rotary_offset, amplitude, flags, k_pool, v_pool, q_out, &done);
+    if (rc != PKV_OK || done) return rc;
+    a.status = status_word();
+    if (!a.status) return PKV_ERR_CUDA;
+    return launch<false>(a, flags & PKV_ROPE_INTERLEAVED, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int append_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool, const void *q,
+                int32_t num_q_heads, const void *k_new, const void *v_new, const float *k_scale,
+                const float *v_scale, const int64_t *positions, int32_t num_axes,
+                const int32_t *pair_axis, const int64_t *slot_mapping, int64_t num_tokens,
+                const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
+                float amplitude, int32_t flags, void *q_out, pkv_stream_t stream) {
+    RopeArgs a = {};
+    bool done;
+    const int rc = prepare(a, kE4m3, cache, q, num_q_heads, k_new, v_new, positions, num_axes,
+                           pair_axis, slot_mapping, num_tokens, inv_freq, rotary_dim,
+                           rotary_offset, amplitude, flags, k_pool, v_pool, q_out, &done);
+    if (rc != PKV_OK || done) return rc;
+    if (!k_scale || !v_scale) return PKV_ERR_INVALID_ARG;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.status = status_word();
+    if (!a.status) return PKV_ERR_CUDA;
+    return launch<true>(a, flags & PKV_ROPE_INTERLEAVED, reinterpret_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
 extern "C" int pkv_rope_append(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
                                const void *q, int32_t num_q_heads, const void *k_new,
                                const void *v_new, const int64_t *positions,
                                const int64_t *slot_mapping, int64_t num_tokens,
                                const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
                                float amplitude, int32_t flags, void *q_out, pkv_stream_t stream) {
-    RopeArgs a = {};
-    bool done;
-    const int rc = prepare(a, false, cache, q, num_q_heads, k_new, v_new, positions, slot_mapping,
-                           num_tokens, inv_freq, rotary_dim, rotary_offset, amplitude, flags,
-                           k_pool, v_pool, q_out, &done);
-    if (rc != PKV_OK || done) return rc;
-    return launch<false>(a, flags & PKV_ROPE_INTERLEAVED, reinterpret_cast<cudaStream_t>(stream));
+    return append_bf16(cache, k_pool, v_pool, q, num_q_heads, k_new, v_new, positions, 1, nullptr,
+                       slot_mapping, num_tokens, inv_freq, rotary_dim, rotary_offset, amplitude,
+                       flags, q_out, stream);
 }
 
 extern "C" int pkv_rope_append_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
@@ -812,14 +1031,61 @@ extern "C" int pkv_rope_append_e4m3(const pkv_cache_desc *cache, void *k_pool, v
                                     const double *inv_freq, int32_t rotary_dim,
                                     int32_t rotary_offset, float amplitude, int32_t flags,
                                     void *q_out, pkv_stream_t stream) {
+    return append_e4m3(cache, k_pool, v_pool, q, num_q_heads, k_new, v_new, k_scale, v_scale,
+                       positions, 1, nullptr, slot_mapping, num_tokens, inv_freq, rotary_dim,
+                       rotary_offset, amplitude, flags, q_out, stream);
+}
+
+extern "C" int pkv_rope_append_axes(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
+                                    const void *q, int32_t num_q_heads, const void *k_new,
+                                    const void *v_new, const int64_t *positions,
+                                    int32_t num_axes, const int32_t *pair_axis,
+                                    const int64_t *slot_mapping, int64_t num_tokens,
+                                    const double *inv_freq, int32_t rotary_dim,
+                                    int32_t rotary_offset, float amplitude, int32_t flags,
+                                    void *q_out, pkv_stream_t stream) {
+    if (!pair_axis) return PKV_ERR_INVALID_ARG;
+    return append_bf16(cache, k_pool, v_pool, q, num_q_heads, k_new, v_new, positions, num_axes,
+                       pair_axis, slot_mapping, num_tokens, inv_freq, rotary_dim, rotary_offset,
+                       amplitude, flags, q_out, stream);
+}
+
+extern "C" int pkv_rope_append_axes_e4m3(const pkv_cache_desc *cache, void *k_pool, void *v_pool,
+                                         const void *q, int32_t num_q_heads, const void *k_new,
+                                         const void *v_new, const float *k_scale,
+                                         const float *v_scale, const int64_t *positions,
+                                         int32_t num_axes, const int32_t *pair_axis,
+                                         const int64_t *slot_mapping, int64_t num_tokens,
+                                         const double *inv_freq, int32_t rotary_dim,
+                                         int32_t rotary_offset, float amplitude, int32_t flags,
+                                         void *q_out, pkv_stream_t stream) {
+    if (!pair_axis) return PKV_ERR_INVALID_ARG;
+    return append_e4m3(cache, k_pool, v_pool, q, num_q_heads, k_new, v_new, k_scale, v_scale,
+                       positions, num_axes, pair_axis, slot_mapping, num_tokens, inv_freq,
+                       rotary_dim, rotary_offset, amplitude, flags, q_out, stream);
+}
+
+extern "C" int pkv_rope_append_int4(const pkv_cache_desc *cache, void *k_pool, void *k_params,
+                                    void *v_pool, void *v_params, const void *q,
+                                    int32_t num_q_heads, const void *k_new, const void *v_new,
+                                    const int64_t *positions, int32_t num_axes,
+                                    const int32_t *pair_axis, const int64_t *slot_mapping,
+                                    int64_t num_tokens, const double *inv_freq,
+                                    int32_t rotary_dim, int32_t rotary_offset, float amplitude,
+                                    int32_t flags, void *q_out, pkv_stream_t stream) {
+    const int st = validate_int4_cache(cache);
+    if (st != PKV_OK) return st;
     RopeArgs a = {};
     bool done;
-    const int rc = prepare(a, true, cache, q, num_q_heads, k_new, v_new, positions, slot_mapping,
-                           num_tokens, inv_freq, rotary_dim, rotary_offset, amplitude, flags,
-                           k_pool, v_pool, q_out, &done);
+    const int rc = prepare(a, kInt4, cache, q, num_q_heads, k_new, v_new, positions, num_axes,
+                           pair_axis, slot_mapping, num_tokens, inv_freq, rotary_dim,
+                           rotary_offset, amplitude, flags, k_pool, v_pool, q_out, &done);
     if (rc != PKV_OK || done) return rc;
-    if (!k_scale || !v_scale) return PKV_ERR_INVALID_ARG;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    return launch<true>(a, flags & PKV_ROPE_INTERLEAVED, reinterpret_cast<cudaStream_t>(stream));
+    if (!k_params || !v_params) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_params) || !aligned16(v_params)) return PKV_ERR_ALIGNMENT;
+    a.k_params = static_cast<uint32_t *>(k_params);
+    a.v_params = static_cast<uint32_t *>(v_params);
+    a.status = status_word();
+    if (!a.status) return PKV_ERR_CUDA;
+    return launch_int4(a, flags & PKV_ROPE_INTERLEAVED, reinterpret_cast<cudaStream_t>(stream));
 }
