@@ -1,0 +1,634 @@
+// decode_int4.cu -- decode attention over a 4-bit cache on tensor cores.
+//
+// Element d of token j's key is s_j c_jd + o_j (scale, offset, code), so
+//     q . K_j = s_j (q . c_j) + o_j sum_d q_d,
+//     sum_j p_j V_j = sum_j (p_j s'_j) c'_j + sum_j p_j o'_j
+// and both products run over the codes themselves; scales and offsets are applied to the
+// scores and to the weights, once a token.
+//
+// Bound: memory.  A row of 128 elements is 68 bytes, so an SM at full bandwidth meets
+// 41 elements a clock and cannot afford an instruction for each.  Hence:
+//  - A code needs no conversion.  The bits 0..15 of a code, read as fp16, are the
+//    subnormal code * 2^-24, and shifted left by four code * 2^-20; tensor cores take
+//    subnormals exactly.  A 32-bit word of 8 codes becomes four fp16 pairs with one shift
+//    and four ANDs.  The factors 2^-24 and 16 go into the query and into the result.
+//  - Rows come by cp.async into a ring that belongs to one warp: 16-byte pieces may be
+//    placed anywhere, no barrier couples the warps, and a warp's tiles are on their way
+//    while it computes.  (Warp-level MMAs, because tcgen05 would want the codes expanded
+//    in shared memory first: with both operands' traffic 120 of the 128 bytes a clock
+//    that shared memory moves.)
+//  - Scores: A = 16 tokens x 16 elements, B = the query rows.  The order of the elements
+//    within a product is free, so a lane takes D / 4 of a row in one load and the query
+//    is laid out to match.
+//  - Values: A = 16 elements x 16 tokens.  Again each lane takes whole words: lane group
+//    g's word holds 8 elements, the n-th of which is row g of the n-th product.  Two
+//    tokens' words interleave with two byte permutes into the pairs that the product
+//    wants.
+//  - Weights go from the scores' layout (token, row) to the values' (row, token) by
+//    movmatrix.  Token order within 16 is m -> m ^ bit1(m), with which all reads of
+//    shared memory are free of bank conflicts.
+// Query and weights are carried as two fp16 terms (22 bits): up to 4 rows as 8 columns
+// (row, term), else two products.  The query is scaled by a power of two so that its
+// largest element is 2^12..2^13; a row's weights p_j s'_j likewise, to 2^0..2^15, by a
+// factor that follows their running maximum -- a key that weighs much may have values
+// a millionth of the others'.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "pkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_math.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 32;                 // tokens of a warp's step
+
+// ROWS query rows of an item: 4 (as 8 columns of row and term), 8, or 16 (two tiles of 8).
+template <int D, int ROWS>
+struct Config {
+    static constexpr int kRowBytes = D / 2;
+    static constexpr int kWordsK = D / 32;            // words of a K row a lane takes
+    static constexpr int kWordsV = D / 64;            // words of a V row a lane takes
+    static constexpr int kProducts = 4 * kWordsV;     // products of 16 elements
+    static constexpr bool kPacked = ROWS == 4;
+    static constexpr int kCols = ROWS == 16 ? 2 : 1;  // tiles of 8 columns
+    static constexpr int kTerms = kPacked ? 1 : 2;    // products a tile of columns
+    static constexpr int kLaneRows = kPacked ? 1 : 2 * kCols;
+    static constexpr int kCtas = ROWS == 16 ? 2 : 3;  // per SM
+    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 6 : 4) : (ROWS == 16 ? 10 : 7);
+    static constexpr int kStageBytes = 2 * kTile * (kRowBytes + 4);
+    static constexpr int kWarpBytes = kStages * kStageBytes;
+    // the warps' outputs go over the rings at the end
+    static constexpr int kMergeBytes = kWarps * ROWS * (D + 3) * 4;
+    static constexpr int kSmem =
+        kWarps * kWarpBytes > kMergeBytes ? kWarps * kWarpBytes : kMergeBytes;
+};
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+// N words (1, 2 or 4) from an address aligned to them.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&x)[N]) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
+    else
+        x[0] = lds32(a);
+}
+// D = A (16 x 16, row) * B (16 x 8, col) + D, fp16 inputs, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes the 8 x 8 matrix of 16-bit elements that the warp holds (lane 4 i + k: row
+// i, columns 2 k and 2 k + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// The place of a tile's row in its ring stage, and of a 16-byte piece within the row.
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+    if constexpr (D == 128) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    else return (row ^ ((row >> 2) & 1)) * 32 + (piece << 4);
+}
+
+// 2^n for n clamped to a normal number's range.
+__device__ __forceinline__ float pow2(int n) {
+    return __int_as_float((min(max(n, -126), 126) + 127) << 23);
+}
+// floor(log2 x) of a positive normal x
+__device__ __forceinline__ int exponent(float x) {
+    return ((__float_as_int(x) >> 23) & 255) - 127;
+}
+
+// Over the eight lanes that share lane mod 4.
+__device__ __forceinline__ float group_max(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, Config<D, ROWS>::kCtas)
+decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
+    using C = Config<D, ROWS>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const pkv_cache_desc &c = a.cache;
+    const int group = a.num_q_heads / c.num_kv_heads, rows = group * a.q_tokens;
+    // item: (sequence, KV head, split, tile of rows), the last fastest: CTAs that read
+    // the same tokens run together
+    uint32_t item = blockIdx.x;
+    const int row0 = int(item % row_tiles) * ROWS;
+    item /= row_tiles;
+    const int split = int(item % a.num_splits);
+    item /= a.num_splits;
+    const int head = int(item % c.num_kv_heads), b = int(item / c.num_kv_heads);
+
+    int64_t len = a.seq_lens[b];
+    const bool odd = len < 0 || len > (int64_t(a.max_blocks) << block_shift);
+    if ((odd || len < a.flag_below) && threadIdx.x == 0 && split == 0 && row0 == 0 && head == 0)
+        raise_status(a.status, PKV_DEV_SEQ_LEN);
+    if (odd) len = 0;
+    const int L = int(len);
+    const int64_t chunk = 64 * ((len + 64LL * a.num_splits - 1) / (64LL * a.num_splits));
+    const int begin = int(min(split * chunk, len)), end = int(min((split + 1) * chunk, len));
+    // this warp's share, in whole tiles
+    const int per = (end - begin + kWarps * kTile - 1) / (kWarps * kTile) * kTile;
+    const int first = min(begin + warp * per, end), last = min(first + per, end);
+    const int tiles = (last - first + kTile - 1) / kTile;
+
+    // ---- the ring
+    const uint32_t ring = smem_addr(smem) + warp * C::kWarpBytes;
+    const int32_t *table = a.block_tables + int64_t(b) * a.max_blocks;
+    const int last_block = last > first ? (last - 1) >> block_shift : -1;
+    auto entry = [&](int i) {              // of the table; -1: nothing to read there
+        if (i > last_block) return -1;
+        const int32_t phys = table[i];
+        if (phys >= 0 && phys < c.num_blocks) return int(phys);
+        raise_status(a.status, PKV_DEV_BLOCK_ID);
+        return -1;
+    };
+    // 32 table entries at a time, one a lane, and the next 32 on their way
+    int window = first >> block_shift;
+    int here = entry(window + lane), next = entry(window + 32 + lane);
+    auto load = [&](int tile) {
+        const int j0 = first + tile * kTile;
+        if (((j0 >> block_shift) - window) >= 32) {
+            window += 32;
+            here = next;
+            next = entry(window + 32 + lane);
+        }
+        const uint32_t stage = ring + (tile % C::kStages) * C::kStageBytes;
+        constexpr int kPieces = C::kRowBytes / 16;          // of a row
+        constexpr int kPass = 32 / kPieces;                 // rows a pass of the warp
+#pragma unroll
+        for (int n = 0; n < kTile / kPass; ++n) {
+            const int row = n * kPass + lane / kPieces, piece = lane % kPieces, j = j0 + row;
+            const int phys = __shfl_sync(0xffffffffu, here, ((j >> block_shift) - window) & 31);
+            const bool in = j < last && phys >= 0;
+            const int64_t at =
+                ((int64_t(in ? phys : 0) * c.num_kv_heads + head) << block_shift) +
+                (in ? j & ((1 << block_shift) - 1) : 0);
+            const uint32_t to = stage + piece_at<D>(row, piece), bytes = in ? 16 : 0;
+            cp_async_16(to, a.k_pool + at * C::kRowBytes + piece * 16, bytes);
+            cp_async_16(to + kTile * C::kRowBytes, a.v_pool + at * C::kRowBytes + piece * 16, bytes);
+        }
+        {   // parameters: four tokens a lane, K's by lanes 0-7, V's by lanes 8-15
+            const int j = j0 + (lane & 7) * 4;
+            const int phys = __shfl_sync(0xffffffffu, here, ((j >> block_shift) - window) & 31);
+            const int n = phys >= 0 ? min(max(last - j, 0), 4) : 0;
+            const int64_t at = ((int64_t(n ? phys : 0) * c.num_kv_heads + head) << block_shift) +
+                               (n ? j & ((1 << block_shift) - 1) : 0);
+            if (lane < 16)
+                cp_async_16(stage + 2 * kTile * C::kRowBytes + lane * 16,
+                            (lane < 8 ? a.k_params : a.v_params) + at, n * 4);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) {
+        if (i < tiles) load(i);
+        cp_async_commit();
+    }
+
+    // ---- the query: B fragments of the tile's rows, scaled to 2^12 .. 2^13
+    const auto q_row = [&](int r) {        // the r-th row of the tile
+        r += row0;
+        const int tok = r / group;
+        return a.q + ((int64_t(b) * a.q_tokens + tok) * a.num_q_heads + head * group +
+                      (r - tok * group)) * D;
+    };
+    // word w of a lane, elements 8 (kWordsK t + w) + ..: step 0 takes 0, 4 and 1, 5; step
+    // 1 takes 2, 6 and 3, 7; odd ones' codes come times 16
+    uint32_t qf[C::kCols][C::kTerms][C::kWordsK][2][2];
+    float factor[C::kLaneRows], offset_factor[C::kLaneRows];
+    {
+        float col_factor[C::kCols], col_sum[C::kCols];
+#pragma unroll
+        for (int n = 0; n < C::kCols; ++n) {
+            const int r = C::kPacked ? g >> 1 : 8 * n + g;
+            float x[C::kWordsK][8], sum = 0.f, amax = 0.f;
+            const bool in = row0 + r < rows;
+#pragma unroll
+            for (int w = 0; w < C::kWordsK; ++w) {
+                const float4 *src =
+                    reinterpret_cast<const float4 *>(q_row(in ? r : 0) + 8 * (C::kWordsK * t + w));
+                const float4 lo = in ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 hi = in ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[w][0] = lo.x; x[w][1] = lo.y; x[w][2] = lo.z; x[w][3] = lo.w;
+                x[w][4] = hi.x; x[w][5] = hi.y; x[w][6] = hi.z; x[w][7] = hi.w;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    sum += x[w][e];
+                    amax = fmaxf(amax, fabsf(x[w][e]));
+                }
+            }
+            // a row's elements are in the four lanes of a group
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            }
+            const int e = max(exponent(amax), -100);
+            const float up = pow2(12 - e);
+#pragma unroll
+            for (int w = 0; w < C::kWordsK; ++w)
+#pragma unroll
+                for (int step = 0; step < 2; ++step)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int e0 = 2 * step + half;
+                        const float s = half ? up * 0.0625f : up;
+                        const float u = x[w][e0] * s, v = x[w][e0 + 4] * s;
+                        const uint32_t top = pack_f16x2(u, v);
+                        const uint32_t low = pack_f16x2(u - f16_lo_to_f32(top), v - f16_hi_to_f32(top));
+                        if constexpr (C::kPacked) {
+                            qf[n][0][w][step][half] = g & 1 ? low : top;
+                        } else {
+                            qf[n][0][w][step][half] = top;
+                            qf[n][C::kTerms - 1][w][step][half] = low;
+                        }
+                    }
+            // score = s (sum of products) * col_factor + o * col_sum, in base-2 units
+            const float base = a.scale * kLog2e;
+            col_factor[n] = base * pow2(e - 12) * 16777216.f;
+            col_sum[n] = base * sum;
+        }
+        // to the lanes that hold the rows' scores: lane (g, t) has row t, or rows 2 t, 2 t + 1
+#pragma unroll
+        for (int r = 0; r < C::kLaneRows; ++r) {
+            const int col = C::kPacked ? 2 * t : 2 * t + (r & 1);
+            factor[r] = __shfl_sync(0xffffffffu, col_factor[r >> 1], 4 * col);
+            offset_factor[r] = __shfl_sync(0xffffffffu, col_sum[r >> 1], 4 * col);
+        }
+    }
+    // tokens that each of the lane's rows sees
+    int sees[C::kLaneRows];
+#pragma unroll
+    for (int r = 0; r < C::kLaneRows; ++r) {
+        const int row = row0 + (C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1));
+        sees[r] = L - a.q_tokens + 1 + min(row / group, a.q_tokens - 1);
+    }
+    const int all_see = min(last, L - a.q_tokens + 1);   // every row sees the tokens before
+
+    float m[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
+    float up[C::kLaneRows], most[C::kLaneRows];   // weights' factor, and their largest
+    float acc[C::kProducts][C::kCols][4];
+#pragma unroll
+    for (int r = 0; r < C::kLaneRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = off[r] = most[r] = 0.f;
+        up[r] = 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < C::kProducts; ++i)
+#pragma unroll
+        for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
+    // column x (0 or 1) of a lane's pair in tile n belongs to the lane's row:
+    auto row_of = [](int n, int x) { return C::kPacked ? 0 : 2 * n + x; };
+    auto rescale = [&](const float (&by)[C::kLaneRows]) {
+#pragma unroll
+        for (int i = 0; i < C::kProducts; ++i)
+#pragma unroll
+            for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) acc[i][n][x] *= by[row_of(n, x & 1)];
+    };
+
+    const int tok = g ^ ((g >> 1) & 1);            // the lane's token of the first 8
+    const int pair0 = (2 * t) ^ (t & 1), pair1 = (2 * t + 1) ^ (t & 1);
+    for (int i = 0; i < tiles; ++i) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();                  // the tile is there; the stage before it is free
+        if (i + C::kStages - 1 < tiles) load(i + C::kStages - 1);
+        cp_async_commit();
+        const uint32_t stage = ring + (i % C::kStages) * C::kStageBytes;
+        const uint32_t vstage = stage + kTile * C::kRowBytes;
+        const uint32_t params = vstage + kTile * C::kRowBytes;
+        const int j0 = first + i * kTile;
+
+        // ---- scores of 32 tokens: x[row][k], k: tokens tok + 8 k
+        float x[C::kLaneRows][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float s[C::kCols][4];
+#pragma unroll
+            for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+            uint32_t ka[C::kWordsK], kb[C::kWordsK];
+            const int row = 16 * h + tok;
+            if constexpr (D == 128) {
+                lds_words(stage + piece_at<D>(row, t), ka);
+                lds_words(stage + piece_at<D>(row + 8, t), kb);
+            } else {
+                lds_words(stage + piece_at<D>(row, 0) + 8 * t, ka);
+                lds_words(stage + piece_at<D>(row + 8, 0) + 8 * t, kb);
+            }
+#pragma unroll
+            for (int w = 0; w < C::kWordsK; ++w)
+#pragma unroll
+                for (int step = 0; step < 2; ++step) {
+                    const uint32_t u = step ? ka[w] >> 8 : ka[w], v = step ? kb[w] >> 8 : kb[w];
+                    const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
+                    const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
+#pragma unroll
+                    for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                        for (int term = 0; term < C::kTerms; ++term)
+                            mma_f16(s[n], a0, a1, a2, a3, qf[n][term][w][step][0],
+                                    qf[n][term][w][step][1]);
+                }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t kp = lds32(params + (row + 8 * half) * 4);
+                const float ks = bf16_lo_to_f32(kp), ko = bf16_hi_to_f32(kp);
+#pragma unroll
+                for (int r = 0; r < C::kLaneRows; ++r) {
+                    const float dot = C::kPacked ? s[0][2 * half] + s[0][2 * half + 1]
+                                                 : s[r >> 1][2 * half + (r & 1)];
+                    x[r][2 * h + half] = fmaf(ks, dot * factor[r], ko * offset_factor[r]);
+                }
+            }
+        }
+        // tokens past the end, or past what a row sees
+        uint32_t hidden = 0;           // bit 4 r + k
+        if (j0 + kTile > all_see) {
+#pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (j0 + tok + 8 * k >= min(last, sees[r])) {
+                        x[r][k] = -INFINITY;
+                        hidden |= 1u << (4 * r + k);
+                    }
+        }
+        // ---- the running maximum: it follows once a score is past it by 8 (a factor of
+        // 256, which fp32 sums and the weights' own factor have room for)
+        bool grows = false;
+        float top[C::kLaneRows];
+#pragma unroll
+        for (int r = 0; r < C::kLaneRows; ++r) {
+            top[r] = group_max(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])));
+            grows |= top[r] > m[r] + 8.f || (m[r] == -INFINITY && top[r] > -INFINITY);
+        }
+        if (__any_sync(0xffffffffu, grows)) {
+            float by[C::kLaneRows];
+#pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r) {
+                const float now = fmaxf(m[r], top[r]);
+                by[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - now);
+                m[r] = now;
+                l[r] *= by[r];
+                off[r] *= by[r];
+                most[r] *= by[r];
+            }
+            rescale(by);
+        }
+        // ---- probabilities and the values' weights
+        uint32_t vp[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) vp[k] = lds32(params + (kTile + tok + 8 * k) * 4);
+        bool moves = false;
+#pragma unroll
+        for (int r = 0; r < C::kLaneRows; ++r) {
+            const float base = m[r] == -INFINITY ? 0.f : m[r];
+            float largest = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float p = ex2_approx(x[r][k] - base);
+                l[r] += p;
+                float w = p * bf16_lo_to_f32(vp[k]), o = p * bf16_hi_to_f32(vp[k]);
+                if (hidden >> (4 * r + k) & 1) w = o = 0.f;   // its values may be anything
+                off[r] += o;
+                largest = fmaxf(largest, fabsf(w));
+                x[r][k] = w;
+            }
+            most[r] = fmaxf(most[r], group_max(largest));
+            const float scaled = most[r] * up[r];
+            moves |= scaled > 32768.f || (scaled < 1.f && most[r] > 0.f && up[r] < 1e38f);
+        }
+        if (__any_sync(0xffffffffu, moves)) {
+            float by[C::kLaneRows];
+#pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r) {
+                // (all of a row's lanes have the same `most`)
+                const float now = most[r] > 0.f ? pow2(10 - exponent(most[r])) : up[r];
+                by[r] = fminf(now / up[r], 3.4e38f);      // (a sum of 0 stays 0)
+                up[r] = now;
+            }
+            rescale(by);
+        }
+        // ---- values
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // weights as fp16 terms, in the products' layout: [tile of columns][term][half]
+            uint32_t pb[C::kCols][C::kTerms][2];
+            if constexpr (C::kPacked) {
+                const float u = x[0][2 * h] * up[0], v = x[0][2 * h + 1] * up[0];
+                const uint32_t hi = pack_f16x2(u, v);
+                const uint32_t lo = pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
+                pb[0][0][0] = transpose8(__byte_perm(hi, lo, 0x5410));
+                pb[0][0][1] = transpose8(__byte_perm(hi, lo, 0x7632));
+            } else {
+#pragma unroll
+                for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const float u = x[2 * n][2 * h + half] * up[2 * n];
+                        const float v = x[2 * n + 1][2 * h + half] * up[2 * n + 1];
+                        const uint32_t hi = pack_f16x2(u, v);
+                        const uint32_t lo =
+                            pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
+                        pb[n][0][half] = transpose8(hi);
+                        pb[n][C::kTerms - 1][half] = transpose8(lo);
+                    }
+            }
+            // the four tokens of this lane, and their words
+            uint32_t v0[C::kWordsV], v1[C::kWordsV], v2[C::kWordsV], v3[C::kWordsV];
+            auto word_at = [&](int row) {
+                if constexpr (D == 128)
+                    return vstage + piece_at<D>(row, g >> 1) + (g & 1) * 8;
+                else
+                    return vstage + piece_at<D>(row, 0) + g * 4;
+            };
+            lds_words(word_at(16 * h + pair0), v0);
+            lds_words(word_at(16 * h + pair1), v1);
+            lds_words(word_at(16 * h + 8 + pair0), v2);
+            lds_words(word_at(16 * h + 8 + pair1), v3);
+            // element n of word w, for tokens (0, 1) and (2, 3): [8 w + n]
+            uint32_t lo[C::kWordsV][2][2];        // [word][token pair][low, high half]
+#pragma unroll
+            for (int w = 0; w < C::kWordsV; ++w) {
+                lo[w][0][0] = __byte_perm(v0[w], v1[w], 0x5410);
+                lo[w][0][1] = __byte_perm(v0[w], v1[w], 0x7632);
+                lo[w][1][0] = __byte_perm(v2[w], v3[w], 0x5410);
+                lo[w][1][1] = __byte_perm(v2[w], v3[w], 0x7632);
+            }
+            auto element = [&](int index, int pair) {
+                const int w = index >> 3, n = index & 7;
+                const uint32_t z = lo[w][pair][n >> 2];
+                return ((n & 2) ? z >> 8 : z) & ((n & 1) ? 0x00f000f0u : 0x000f000fu);
+            };
+#pragma unroll
+            for (int p = 0; p < C::kProducts; ++p) {
+                const uint32_t a0 = element(p, 0), a1 = element(p + C::kProducts, 0);
+                const uint32_t a2 = element(p, 1), a3 = element(p + C::kProducts, 1);
+#pragma unroll
+                for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                    for (int term = 0; term < C::kTerms; ++term)
+                        mma_f16(acc[p][n], a0, a1, a2, a3, pb[n][term][0], pb[n][term][1]);
+            }
+        }
+    }
+
+    // ---- the CTA's warps together: outputs, maxima and sums over the rings
+    cp_async_wait<0>();
+    __syncthreads();
+    float *outs = reinterpret_cast<float *>(smem);            // [warp][ROWS][D]
+    float *stats = outs + kWarps * ROWS * D;                  // [warp][ROWS][3]
+#pragma unroll
+    for (int r = 0; r < C::kLaneRows; ++r) {
+        l[r] = group_sum(l[r]);
+        off[r] = group_sum(off[r]);
+        const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
+        if (g == 0) {
+            float *s = stats + (warp * ROWS + row) * 3;
+            s[0] = m[r];
+            s[1] = l[r];
+            s[2] = off[r];
+        }
+        const float down = 1.f / up[r];
+        float *o = outs + (warp * ROWS + row) * D;
+#pragma unroll
+        for (int p = 0; p < C::kProducts; ++p)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int index = p + half * C::kProducts, w = index >> 3, n = index & 7;
+                const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
+                                           : acc[p][r >> 1][2 * half + (r & 1)];
+                o[8 * (C::kWordsV * g + w) + n] = z * (n & 1 ? 1048576.f : 16777216.f) * down;
+            }
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < ROWS * (D / 4); u += kThreads) {
+        const int r = u / (D / 4), e = (u - r * (D / 4)) * 4;
+        if (row0 + r >= rows) break;
+        float top = -INFINITY, sum = 0.f, shift = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * ROWS + r) * 3]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float *s = stats + (w * ROWS + r) * 3;
+            const float by = ex2_approx(s[0] - base);
+            const float4 z = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * D + e);
+            sum = fmaf(by, s[1], sum);
+            shift = fmaf(by, s[2], shift);
+            o.x = fmaf(by, z.x, o.x); o.y = fmaf(by, z.y, o.y);
+            o.z = fmaf(by, z.z, o.z); o.w = fmaf(by, z.w, o.w);
+        }
+        const bool some = sum > 0.f || sum != sum;       // (a NaN score: a NaN row)
+        const float inv = some ? 1.f / sum : 0.f;
+        const int token = (row0 + r) / group;
+        const int64_t to = ((int64_t(split) * a.batch + b) * a.q_tokens + token) * a.num_q_heads +
+                           head * group + (row0 + r - token * group);
+        *reinterpret_cast<float4 *>(a.out_part + to * D + e) =
+            some ? make_float4((o.x + shift) * inv, (o.y + shift) * inv, (o.z + shift) * inv,
+                               (o.w + shift) * inv)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e == 0) a.lse_part[to] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+// Rows of an item for `rows` in all.
+int tile_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
+
+template <int D, int ROWS>
+int launch(const Int4DecodeArgs &a) {
+    using C = Config<D, ROWS>;
+    const cudaError_t e = cudaFuncSetAttribute(
+        decode_int4_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int rows = a.num_q_heads / a.cache.num_kv_heads * a.q_tokens;
+    const int tiles = (rows + ROWS - 1) / ROWS;
+    const int64_t items = int64_t(a.batch) * a.cache.num_kv_heads * tiles * a.num_splits;
+    int shift = 0;
+    while ((1 << shift) < a.cache.block_size) ++shift;
+    return launch_pdl(decode_int4_kernel<D, ROWS>, dim3(unsigned(items)), dim3(kThreads), C::kSmem,
+                      a.stream, a, tiles, shift);
+}
+
+}  // namespace
+
+bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
+                          int32_t q_tokens) {
+    const int32_t bs = c.block_size;
+    if (c.head_dim_k != c.head_dim_v || (c.head_dim_k != 64 && c.head_dim_k != 128) || bs < 8 ||
+        (bs & (bs - 1)) != 0)
+        return false;
+    // items are numbered within 32 bits at any split count
+    const int64_t rows = int64_t(num_q_heads) / c.num_kv_heads * q_tokens;
+    return int64_t(batch) * c.num_kv_heads * ((rows + 3) / 4) * 256 <= INT32_MAX;
+}
+
+// Items per (sequence, KV head, split), and the CTAs that run at once.
+int int4_row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens) {
+    const int rows = num_q_heads / c.num_kv_heads * q_tokens;
+    return (rows + tile_rows(rows) - 1) / tile_rows(rows);
+}
+int int4_resident_ctas(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens) {
+    const int rows = num_q_heads / c.num_kv_heads * q_tokens;
+    return sm_count() * (tile_rows(rows) == 16 ? 2 : 3);
+}
+
+int launch_decode_int4(const Int4DecodeArgs &a) {
+    const int rows = tile_rows(a.num_q_heads / a.cache.num_kv_heads * a.q_tokens);
+    if (a.cache.head_dim_k == 128)
+        return rows == 4 ? launch<128, 4>(a) : rows == 8 ? launch<128, 8>(a) : launch<128, 16>(a);
+    return rows == 4 ? launch<64, 4>(a) : rows == 8 ? launch<64, 8>(a) : launch<64, 16>(a);
+}
+
+}  // namespace pkv

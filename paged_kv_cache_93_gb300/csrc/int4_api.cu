@@ -15,15 +15,39 @@ constexpr int32_t kMaxSplits = 256;
 constexpr int32_t kMaxQueryTokens = 64;
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Enough (row, split) items for the device, each at least 512 tokens long.
+// Whether the tensor-core kernel takes the call.
+bool on_tensor_cores(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
+                     int32_t flags) {
+    return !(flags & PKV_DECODE_GENERIC) && hq % c.num_kv_heads == 0 &&
+           int4_kernel_supports(c, batch, hq, tokens);
+}
+
 int32_t auto_splits(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
                     int64_t max_seq_len, int32_t flags) {
-    (void)c;
-    (void)flags;
+    const int64_t L = std::max<int64_t>(1, max_seq_len);
+    if (on_tensor_cores(c, batch, tokens, hq, flags)) {
+        // The least rounds of resident CTAs x (128-token steps of a CTA's four warps + 2
+        // for its start and end), for sequences of the longest length; a tie goes to
+        // fewer splits (less to merge).
+        const int64_t units =
+            std::max<int64_t>(1, int64_t(batch) * c.num_kv_heads * int4_row_tiles(c, hq, tokens));
+        const int64_t ctas = int4_resident_ctas(c, hq, tokens);
+        const int64_t s_max = std::min<int64_t>(kMaxSplits, (L + 127) / 128);
+        int64_t best = 1, best_cost = INT64_MAX;
+        for (int64_t s = 1; s <= s_max; ++s) {
+            const int64_t chunk = 64 * ((L + 64 * s - 1) / (64 * s));
+            const int64_t cost = (units * s + ctas - 1) / ctas * ((chunk + 127) / 128 + 2);
+            if (cost < best_cost) {
+                best = s;
+                best_cost = cost;
+            }
+        }
+        return int32_t(best);
+    }
+    // Enough (row, split) items for the device, each at least 512 tokens long.
     const int64_t units = std::max<int64_t>(1, int64_t(batch) * tokens * ((hq + 3) / 4));
     const int64_t want = (int64_t(sm_count()) * 8 + units - 1) / units;
-    const int64_t cap = std::max<int64_t>(1, (max_seq_len + 511) / 512);
-    return int32_t(std::max<int64_t>(1, std::min<int64_t>({want, cap, kMaxSplits})));
+    return int32_t(std::max<int64_t>(1, std::min<int64_t>({want, (L + 511) / 512, kMaxSplits})));
 }
 
 int64_t table_tokens(const pkv_cache_desc &c, int32_t max_blocks) {
@@ -31,8 +55,9 @@ int64_t table_tokens(const pkv_cache_desc &c, int32_t max_blocks) {
 }
 
 int run_split_kernel(const Int4DecodeArgs &a, int32_t flags) {
-    (void)flags;
-    return launch_decode_int4_generic(a);
+    return on_tensor_cores(a.cache, a.batch, a.q_tokens, a.num_q_heads, flags)
+               ? launch_decode_int4(a)
+               : launch_decode_int4_generic(a);
 }
 
 // The checks that the entry points share.
