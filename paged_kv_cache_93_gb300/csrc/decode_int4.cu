@@ -25,8 +25,7 @@
 //    tokens' words interleave with two byte permutes into the pairs that the product
 //    wants.
 //  - Weights go from the scores' layout (token, row) to the values' (row, token) by
-//    movmatrix.  Token order within 16 is m -> m ^ bit1(m), with which all reads of
-//    shared memory are free of bank conflicts.
+//    movmatrix.
 // Query and weights are carried as two fp16 terms (22 bits): up to 4 rows as 8 columns
 // (row, term), else two products.  The query is scaled by a power of two so that its
 // largest element is 2^12..2^13; a row's weights p_j s'_j likewise, to 2^0..2^15, by a
@@ -46,6 +45,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -3e38f;           // the running maximum of a row without a score
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens of a warp's step
@@ -61,19 +61,22 @@ struct Config {
     static constexpr int kCols = ROWS == 16 ? 2 : 1;  // tiles of 8 columns
     static constexpr int kTerms = kPacked ? 1 : 2;    // products a tile of columns
     static constexpr int kLaneRows = kPacked ? 1 : 2 * kCols;
-    static constexpr int kCtas = ROWS == 16 ? 2 : 3;  // per SM
-    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 6 : 4) : (ROWS == 16 ? 10 : 7);
+    static constexpr int kCtas = 3;                   // per SM
+    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 3 : 4) : (ROWS == 16 ? 6 : 7);
+    // 16 rows: the query's fragments (the same for all the CTA's warps) in shared memory,
+    // as the registers hold the sums
+    static constexpr bool kSharedQuery = ROWS == 16;
+    static constexpr int kQueryBytes = kSharedQuery ? kWordsK * kCols * kTerms * 512 : 0;
     static constexpr int kStageBytes = 2 * kTile * (kRowBytes + 4);
     static constexpr int kWarpBytes = kStages * kStageBytes;
+    static constexpr int kRings = kWarps * kWarpBytes;
     // the warps' outputs go over the rings at the end
     static constexpr int kMergeBytes = kWarps * ROWS * (D + 3) * 4;
-    static constexpr int kSmem =
-        kWarps * kWarpBytes > kMergeBytes ? kWarps * kWarpBytes : kMergeBytes;
+    static constexpr int kSmem = (kRings > kMergeBytes ? kRings : kMergeBytes) + kQueryBytes;
 };
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -98,11 +101,14 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&x)[N]) {
     else
         x[0] = lds32(a);
 }
+__device__ __forceinline__ void sts_words(uint32_t a, const uint32_t (&x)[4]) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                 ::"r"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
 // D = A (16 x 16, row) * B (16 x 8, col) + D, fp16 inputs, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -115,11 +121,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// The place of a tile's row in its ring stage, and of a 16-byte piece within the row.
+// The place in its ring stage of a 16-byte piece of a tile's row, and the token (of
+// eight) that is row m of a product.  Both are chosen so that the lanes of one pass of
+// shared memory meet different banks: in the keys' reads rows of neighbouring m, whole;
+// in the values' reads the rows of m = 0, 2, 4, 6 (or 1, 3, 5, 7), halves or whole.
 template <int D>
 __device__ __forceinline__ uint32_t piece_at(int row, int piece) {
     if constexpr (D == 128) return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-    else return (row ^ ((row >> 2) & 1)) * 32 + (piece << 4);
+    else return row * 32 + (piece << 4);
+}
+template <int D>
+__device__ __forceinline__ int token_at(int m) {
+    if constexpr (D == 128) return m ^ ((m >> 1) & 1);         // 0 1 3 2 4 5 7 6
+    else return (0x57463120 >> (4 * m)) & 7;                   // 0 2 1 3 6 4 7 5
 }
 
 // 2^n for n clamped to a normal number's range.
@@ -180,48 +194,62 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
     const uint32_t ring = smem_addr(smem) + warp * C::kWarpBytes;
     const int32_t *table = a.block_tables + int64_t(b) * a.max_blocks;
     const int last_block = last > first ? (last - 1) >> block_shift : -1;
-    auto entry = [&](int i) {              // of the table; -1: nothing to read there
-        if (i > last_block) return -1;
-        const int32_t phys = table[i];
-        if (phys >= 0 && phys < c.num_blocks) return int(phys);
-        raise_status(a.status, PKV_DEV_BLOCK_ID);
-        return -1;
+    // The pool row where the i-th block's tokens of this head begin.  Past the last block,
+    // and for a block id out of range, block 0's: its tokens are read and not used, or
+    // the row is unspecified.
+    auto entry = [&](int i) {
+        uint32_t phys = 0;
+        if (i <= last_block) {
+            phys = uint32_t(table[i]);
+            if (phys >= uint32_t(c.num_blocks)) {
+                raise_status(a.status, PKV_DEV_BLOCK_ID);
+                phys = 0;
+            }
+        }
+        return (phys * uint32_t(c.num_kv_heads) + head) << block_shift;
     };
     // 32 table entries at a time, one a lane, and the next 32 on their way
     int window = first >> block_shift;
-    int here = entry(window + lane), next = entry(window + 32 + lane);
+    uint32_t here = entry(window + lane), next = entry(window + 32 + lane);
+    const int block_mask = (1 << block_shift) - 1;
+    constexpr int kPieces = C::kRowBytes / 16;              // of a row
+    constexpr int kPass = 32 / kPieces;                     // rows a pass of the warp
+    const int my_row = lane / kPieces;
+    const uint8_t *k_lane = a.k_pool + (lane % kPieces) * 16;
+    const uint8_t *v_lane = a.v_pool + (lane % kPieces) * 16;
+    const uint32_t my_piece = piece_at<D>(my_row, lane % kPieces);
+    // parameters: four tokens a lane, K's by lanes 0-7, V's by lanes 8-15
+    const int my_four = (lane & 7) * 4;
+    const uint32_t *p_lane = lane < 8 ? a.k_params : a.v_params;
+    uint32_t fill = ring;                                   // the stage that is filled next
     auto load = [&](int tile) {
+        // (a tile begins at a multiple of its size, so its first row's block and place
+        // and a row's own add up)
         const int j0 = first + tile * kTile;
-        if (((j0 >> block_shift) - window) >= 32) {
+        if ((j0 >> block_shift) - window >= 32) {
             window += 32;
             here = next;
             next = entry(window + 32 + lane);
         }
-        const uint32_t stage = ring + (tile % C::kStages) * C::kStageBytes;
-        constexpr int kPieces = C::kRowBytes / 16;          // of a row
-        constexpr int kPass = 32 / kPieces;                 // rows a pass of the warp
+        const int block = (j0 >> block_shift) - window, inner = j0 & block_mask;
 #pragma unroll
         for (int n = 0; n < kTile / kPass; ++n) {
-            const int row = n * kPass + lane / kPieces, piece = lane % kPieces, j = j0 + row;
-            const int phys = __shfl_sync(0xffffffffu, here, ((j >> block_shift) - window) & 31);
-            const bool in = j < last && phys >= 0;
-            const int64_t at =
-                ((int64_t(in ? phys : 0) * c.num_kv_heads + head) << block_shift) +
-                (in ? j & ((1 << block_shift) - 1) : 0);
-            const uint32_t to = stage + piece_at<D>(row, piece), bytes = in ? 16 : 0;
-            cp_async_16(to, a.k_pool + at * C::kRowBytes + piece * 16, bytes);
-            cp_async_16(to + kTile * C::kRowBytes, a.v_pool + at * C::kRowBytes + piece * 16, bytes);
+            uint32_t at;
+            if constexpr (kPass == 8)       // a block has 8 tokens at least: all one block
+                at = __shfl_sync(0xffffffffu, here, block + (n * kPass >> block_shift)) +
+                     (inner + (n * kPass & block_mask)) + my_row;
+            else
+                at = __shfl_sync(0xffffffffu, here, block + ((n * kPass + my_row) >> block_shift)) +
+                     inner + ((n * kPass + my_row) & block_mask);
+            const uint32_t to = fill + my_piece + n * kPass * C::kRowBytes;
+            cp_async_16(to, k_lane + uint64_t(at) * C::kRowBytes);
+            cp_async_16(to + kTile * C::kRowBytes, v_lane + uint64_t(at) * C::kRowBytes);
         }
-        {   // parameters: four tokens a lane, K's by lanes 0-7, V's by lanes 8-15
-            const int j = j0 + (lane & 7) * 4;
-            const int phys = __shfl_sync(0xffffffffu, here, ((j >> block_shift) - window) & 31);
-            const int n = phys >= 0 ? min(max(last - j, 0), 4) : 0;
-            const int64_t at = ((int64_t(n ? phys : 0) * c.num_kv_heads + head) << block_shift) +
-                               (n ? j & ((1 << block_shift) - 1) : 0);
-            if (lane < 16)
-                cp_async_16(stage + 2 * kTile * C::kRowBytes + lane * 16,
-                            (lane < 8 ? a.k_params : a.v_params) + at, n * 4);
-        }
+        const uint32_t at = __shfl_sync(0xffffffffu, here, block + (my_four >> block_shift)) + inner +
+                            (my_four & block_mask);
+        if (lane < 16) cp_async_16(fill + 2 * kTile * C::kRowBytes + lane * 16, p_lane + at);
+        fill += C::kStageBytes;
+        if (fill == ring + C::kWarpBytes) fill = ring;
     };
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) {
@@ -236,9 +264,10 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
         return a.q + ((int64_t(b) * a.q_tokens + tok) * a.num_q_heads + head * group +
                       (r - tok * group)) * D;
     };
-    // word w of a lane, elements 8 (kWordsK t + w) + ..: step 0 takes 0, 4 and 1, 5; step
-    // 1 takes 2, 6 and 3, 7; odd ones' codes come times 16
-    uint32_t qf[C::kCols][C::kTerms][C::kWordsK][2][2];
+    // word w of a lane, elements 8 (kWordsK t + w) + ..: [2 step + half], step 0 takes 0, 4
+    // and 1, 5; step 1 takes 2, 6 and 3, 7; odd ones' codes come times 16
+    uint32_t qf[C::kSharedQuery ? 1 : C::kCols][C::kTerms][C::kWordsK][4];
+    const uint32_t shared_query = smem_addr(smem) + C::kSmem - C::kQueryBytes + lane * 16;
     float factor[C::kLaneRows], offset_factor[C::kLaneRows];
     {
         float col_factor[C::kCols], col_sum[C::kCols];
@@ -270,23 +299,34 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
             const int e = max(exponent(amax), -100);
             const float up = pow2(12 - e);
 #pragma unroll
-            for (int w = 0; w < C::kWordsK; ++w)
+            for (int w = 0; w < C::kWordsK; ++w) {
+                uint32_t top[4], low[4];
 #pragma unroll
-                for (int step = 0; step < 2; ++step)
+                for (int e0 = 0; e0 < 4; ++e0) {
+                    const float s = e0 & 1 ? up * 0.0625f : up;
+                    const float u = x[w][e0] * s, v = x[w][e0 + 4] * s;
+                    top[e0] = pack_f16x2(u, v);
+                    low[e0] = pack_f16x2(u - f16_lo_to_f32(top[e0]), v - f16_hi_to_f32(top[e0]));
+                }
+                if constexpr (C::kSharedQuery) {
+                    // every warp has all of it: warp w writes word w
+                    if (w == warp) {
+                        const uint32_t to = shared_query + (w * C::kCols + n) * C::kTerms * 512;
+                        sts_words(to, top);
+                        sts_words(to + 512, low);
+                    }
+                } else {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int e0 = 2 * step + half;
-                        const float s = half ? up * 0.0625f : up;
-                        const float u = x[w][e0] * s, v = x[w][e0 + 4] * s;
-                        const uint32_t top = pack_f16x2(u, v);
-                        const uint32_t low = pack_f16x2(u - f16_lo_to_f32(top), v - f16_hi_to_f32(top));
+                    for (int e0 = 0; e0 < 4; ++e0) {
                         if constexpr (C::kPacked) {
-                            qf[n][0][w][step][half] = g & 1 ? low : top;
+                            qf[n][0][w][e0] = g & 1 ? low[e0] : top[e0];
                         } else {
-                            qf[n][0][w][step][half] = top;
-                            qf[n][C::kTerms - 1][w][step][half] = low;
+                            qf[n][0][w][e0] = top[e0];
+                            qf[n][C::kTerms - 1][w][e0] = low[e0];
                         }
                     }
+                }
+            }
             // score = s (sum of products) * col_factor + o * col_sum, in base-2 units
             const float base = a.scale * kLog2e;
             col_factor[n] = base * pow2(e - 12) * 16777216.f;
@@ -299,22 +339,24 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
             factor[r] = __shfl_sync(0xffffffffu, col_factor[r >> 1], 4 * col);
             offset_factor[r] = __shfl_sync(0xffffffffu, col_sum[r >> 1], 4 * col);
         }
-    }
-    // tokens that each of the lane's rows sees
-    int sees[C::kLaneRows];
-#pragma unroll
-    for (int r = 0; r < C::kLaneRows; ++r) {
-        const int row = row0 + (C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1));
-        sees[r] = L - a.q_tokens + 1 + min(row / group, a.q_tokens - 1);
+        if constexpr (C::kSharedQuery) __syncthreads();
     }
     const int all_see = min(last, L - a.q_tokens + 1);   // every row sees the tokens before
+    // tokens that the lane's r-th row sees
+    auto sees = [&](int r) {
+        const int row = row0 + (C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1));
+        return min(last, L - a.q_tokens + 1 + min(row / group, a.q_tokens - 1));
+    };
 
+    // A row's running state: m, what is subtracted from its scores; the sums of p and of
+    // p o' (each lane its own tokens'); the weights' factor, and the largest weight of the
+    // lane's tokens.
     float m[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
-    float up[C::kLaneRows], most[C::kLaneRows];   // weights' factor, and their largest
+    float up[C::kLaneRows], most[C::kLaneRows];
     float acc[C::kProducts][C::kCols][4];
 #pragma unroll
     for (int r = 0; r < C::kLaneRows; ++r) {
-        m[r] = -INFINITY;
+        m[r] = kNone;
         l[r] = off[r] = most[r] = 0.f;
         up[r] = 1.f;
     }
@@ -324,136 +366,165 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
         for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
-    // column x (0 or 1) of a lane's pair in tile n belongs to the lane's row:
-    auto row_of = [](int n, int x) { return C::kPacked ? 0 : 2 * n + x; };
     auto rescale = [&](const float (&by)[C::kLaneRows]) {
 #pragma unroll
         for (int i = 0; i < C::kProducts; ++i)
 #pragma unroll
             for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) acc[i][n][x] *= by[row_of(n, x & 1)];
+                for (int x = 0; x < 4; ++x)
+                    acc[i][n][x] *= by[C::kPacked ? 0 : 2 * n + (x & 1)];
     };
 
-    const int tok = g ^ ((g >> 1) & 1);            // the lane's token of the first 8
-    const int pair0 = (2 * t) ^ (t & 1), pair1 = (2 * t + 1) ^ (t & 1);
+    const int tok = token_at<D>(g);                // the lane's token of the first 8
+    const uint32_t my_k = D == 128 ? piece_at<D>(tok, t) : piece_at<D>(tok, 0) + 8 * t;
+    auto word_at = [&](int row) {
+        return kTile * C::kRowBytes +
+               (D == 128 ? piece_at<D>(row, g >> 1) + (g & 1) * 8 : piece_at<D>(row, 0) + g * 4);
+    };
+    const uint32_t my_v0 = word_at(token_at<D>(2 * t)), my_v1 = word_at(token_at<D>(2 * t + 1));
+    uint32_t stage = ring;
     for (int i = 0; i < tiles; ++i) {
         cp_async_wait<C::kStages - 2>();
         __syncwarp();                  // the tile is there; the stage before it is free
         if (i + C::kStages - 1 < tiles) load(i + C::kStages - 1);
         cp_async_commit();
-        const uint32_t stage = ring + (i % C::kStages) * C::kStageBytes;
-        const uint32_t vstage = stage + kTile * C::kRowBytes;
-        const uint32_t params = vstage + kTile * C::kRowBytes;
+        const uint32_t params = stage + 2 * kTile * C::kRowBytes + tok * 4;
         const int j0 = first + i * kTile;
 
-        // ---- scores of 32 tokens: x[row][k], k: tokens tok + 8 k
-        float x[C::kLaneRows][4];
+        // ---- scores of 32 tokens, tok + 8 k: sums over the codes
+        float s[2][C::kCols][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float s[C::kCols][4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-            uint32_t ka[C::kWordsK], kb[C::kWordsK];
-            const int row = 16 * h + tok;
-            if constexpr (D == 128) {
-                lds_words(stage + piece_at<D>(row, t), ka);
-                lds_words(stage + piece_at<D>(row + 8, t), kb);
-            } else {
-                lds_words(stage + piece_at<D>(row, 0) + 8 * t, ka);
-                lds_words(stage + piece_at<D>(row + 8, 0) + 8 * t, kb);
+                for (int e = 0; e < 4; ++e) s[h][n][e] = 0.f;
+        {
+            uint32_t kw[4][C::kWordsK];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) lds_words(stage + my_k + 8 * k * C::kRowBytes, kw[k]);
+#pragma unroll
+            for (int w = 0; w < C::kWordsK; ++w) {
+                uint32_t q[C::kCols][C::kTerms][4];
+#pragma unroll
+                for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                    for (int term = 0; term < C::kTerms; ++term) {
+                        if constexpr (C::kSharedQuery) {
+                            lds_words(shared_query + ((w * C::kCols + n) * C::kTerms + term) * 512,
+                                      q[n][term]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q[n][term][e] = qf[n][term][w][e];
+                        }
+                    }
+#pragma unroll
+                for (int step = 0; step < 2; ++step)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = step ? kw[2 * h][w] >> 8 : kw[2 * h][w];
+                        const uint32_t v = step ? kw[2 * h + 1][w] >> 8 : kw[2 * h + 1][w];
+                        const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
+                        const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
+#pragma unroll
+                        for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                            for (int term = 0; term < C::kTerms; ++term)
+                                mma_f16(s[h][n], a0, a1, a2, a3, q[n][term][2 * step],
+                                        q[n][term][2 * step + 1]);
+                    }
             }
+        }
+        // ---- x[row][k]: the scores, less `from` of their row
+        float x[C::kLaneRows][4];
+        uint32_t hidden = 0;           // bit 4 r + k
+        auto scores = [&](const float (&from)[C::kLaneRows]) {
 #pragma unroll
-            for (int w = 0; w < C::kWordsK; ++w)
-#pragma unroll
-                for (int step = 0; step < 2; ++step) {
-                    const uint32_t u = step ? ka[w] >> 8 : ka[w], v = step ? kb[w] >> 8 : kb[w];
-                    const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
-                    const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
-#pragma unroll
-                    for (int n = 0; n < C::kCols; ++n)
-#pragma unroll
-                        for (int term = 0; term < C::kTerms; ++term)
-                            mma_f16(s[n], a0, a1, a2, a3, qf[n][term][w][step][0],
-                                    qf[n][term][w][step][1]);
-                }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t kp = lds32(params + (row + 8 * half) * 4);
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t kp = lds32(params + 32 * k);
                 const float ks = bf16_lo_to_f32(kp), ko = bf16_hi_to_f32(kp);
 #pragma unroll
                 for (int r = 0; r < C::kLaneRows; ++r) {
-                    const float dot = C::kPacked ? s[0][2 * half] + s[0][2 * half + 1]
-                                                 : s[r >> 1][2 * half + (r & 1)];
-                    x[r][2 * h + half] = fmaf(ks, dot * factor[r], ko * offset_factor[r]);
+                    const float (&z)[4] = s[k >> 1][r >> 1];
+                    const float dot = C::kPacked ? z[2 * (k & 1)] + z[2 * (k & 1) + 1]
+                                                 : z[2 * (k & 1) + (r & 1)];
+                    x[r][k] = fmaf(ks, dot * factor[r], fmaf(ko, offset_factor[r], -from[r]));
                 }
             }
-        }
-        // tokens past the end, or past what a row sees
-        uint32_t hidden = 0;           // bit 4 r + k
-        if (j0 + kTile > all_see) {
+            // tokens past the end, or past what a row sees
+            if (j0 + kTile > all_see) {
 #pragma unroll
-            for (int r = 0; r < C::kLaneRows; ++r)
+                for (int r = 0; r < C::kLaneRows; ++r) {
+                    const int n = sees(r);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (j0 + tok + 8 * k >= min(last, sees[r])) {
-                        x[r][k] = -INFINITY;
-                        hidden |= 1u << (4 * r + k);
-                    }
-        }
-        // ---- the running maximum: it follows once a score is past it by 8 (a factor of
-        // 256, which fp32 sums and the weights' own factor have room for)
-        bool grows = false;
-        float top[C::kLaneRows];
+                    for (int k = 0; k < 4; ++k)
+                        if (j0 + tok + 8 * k >= n) {
+                            x[r][k] = -INFINITY;
+                            hidden |= 1u << (4 * r + k);
+                        }
+                }
+            }
+        };
+        scores(m);
+        float largest = x[0][0];
 #pragma unroll
-        for (int r = 0; r < C::kLaneRows; ++r) {
-            top[r] = group_max(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])));
-            grows |= top[r] > m[r] + 8.f || (m[r] == -INFINITY && top[r] > -INFINITY);
-        }
-        if (__any_sync(0xffffffffu, grows)) {
+        for (int r = 0; r < C::kLaneRows; ++r)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) largest = fmaxf(largest, x[r][k]);
+        // m follows once a score is past it by 8: probabilities to 2^8 are within the sums'
+        // and the terms' reach, and the common tile needs no maximum over lanes
+        const bool grows = __any_sync(0xffffffffu, largest > 8.f);
+        if (grows) {
             float by[C::kLaneRows];
 #pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r) by[r] = 0.f;
+            scores(by);                // (from kNone the differences are only "some")
+#pragma unroll
             for (int r = 0; r < C::kLaneRows; ++r) {
-                const float now = fmaxf(m[r], top[r]);
-                by[r] = m[r] == -INFINITY ? 0.f : ex2_approx(m[r] - now);
+                const float top =
+                    group_max(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])));
+                const float now = fmaxf(m[r], top);
+                by[r] = ex2_approx(m[r] - now);
                 m[r] = now;
                 l[r] *= by[r];
                 off[r] *= by[r];
                 most[r] *= by[r];
             }
             rescale(by);
+            scores(m);
         }
         // ---- probabilities and the values' weights
-        uint32_t vp[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) vp[k] = lds32(params + (kTile + tok + 8 * k) * 4);
-        bool moves = false;
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t vp = lds32(params + (kTile + 8 * k) * 4);
+            float vs = bf16_lo_to_f32(vp), vo = bf16_hi_to_f32(vp);
+#pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r) {
+                const float p = ex2_approx(x[r][k]);
+                l[r] += p;
+                // (what is not seen may be anything)
+                const bool seen = !(hidden >> (4 * r + k) & 1);
+                x[r][k] = seen ? p * vs : 0.f;
+                off[r] = seen ? fmaf(p, vo, off[r]) : off[r];
+            }
+        }
+        float over = 0.f;
 #pragma unroll
         for (int r = 0; r < C::kLaneRows; ++r) {
-            const float base = m[r] == -INFINITY ? 0.f : m[r];
-            float largest = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float p = ex2_approx(x[r][k] - base);
-                l[r] += p;
-                float w = p * bf16_lo_to_f32(vp[k]), o = p * bf16_hi_to_f32(vp[k]);
-                if (hidden >> (4 * r + k) & 1) w = o = 0.f;   // its values may be anything
-                off[r] += o;
-                largest = fmaxf(largest, fabsf(w));
-                x[r][k] = w;
-            }
-            most[r] = fmaxf(most[r], group_max(largest));
-            const float scaled = most[r] * up[r];
-            moves |= scaled > 32768.f || (scaled < 1.f && most[r] > 0.f && up[r] < 1e38f);
+            const float w = fmaxf(fmaxf(fabsf(x[r][0]), fabsf(x[r][1])),
+                                  fmaxf(fabsf(x[r][2]), fabsf(x[r][3])));
+            most[r] = fmaxf(most[r], w);
+            over = fmaxf(over, w * up[r]);
         }
-        if (__any_sync(0xffffffffu, moves)) {
+        // The factor is set where m has moved (the weights before have shrunk) and where a
+        // weight would leave fp16's range; so a row's largest is between 1 and 2^15.
+        if (__any_sync(0xffffffffu, over > 32768.f) || grows) {
             float by[C::kLaneRows];
 #pragma unroll
             for (int r = 0; r < C::kLaneRows; ++r) {
-                // (all of a row's lanes have the same `most`)
-                const float now = most[r] > 0.f ? pow2(10 - exponent(most[r])) : up[r];
+                const float whole = group_max(most[r]);
+                const float now = whole > 0.f ? pow2(10 - exponent(whole)) : up[r];
                 by[r] = fminf(now / up[r], 3.4e38f);      // (a sum of 0 stays 0)
                 up[r] = now;
             }
@@ -486,28 +557,22 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
             }
             // the four tokens of this lane, and their words
             uint32_t v0[C::kWordsV], v1[C::kWordsV], v2[C::kWordsV], v3[C::kWordsV];
-            auto word_at = [&](int row) {
-                if constexpr (D == 128)
-                    return vstage + piece_at<D>(row, g >> 1) + (g & 1) * 8;
-                else
-                    return vstage + piece_at<D>(row, 0) + g * 4;
-            };
-            lds_words(word_at(16 * h + pair0), v0);
-            lds_words(word_at(16 * h + pair1), v1);
-            lds_words(word_at(16 * h + 8 + pair0), v2);
-            lds_words(word_at(16 * h + 8 + pair1), v3);
-            // element n of word w, for tokens (0, 1) and (2, 3): [8 w + n]
-            uint32_t lo[C::kWordsV][2][2];        // [word][token pair][low, high half]
+            lds_words(stage + my_v0 + 16 * h * C::kRowBytes, v0);
+            lds_words(stage + my_v1 + 16 * h * C::kRowBytes, v1);
+            lds_words(stage + my_v0 + (16 * h + 8) * C::kRowBytes, v2);
+            lds_words(stage + my_v1 + (16 * h + 8) * C::kRowBytes, v3);
+            uint32_t both[C::kWordsV][2][2];      // [word][token pair][low, high half]
 #pragma unroll
             for (int w = 0; w < C::kWordsV; ++w) {
-                lo[w][0][0] = __byte_perm(v0[w], v1[w], 0x5410);
-                lo[w][0][1] = __byte_perm(v0[w], v1[w], 0x7632);
-                lo[w][1][0] = __byte_perm(v2[w], v3[w], 0x5410);
-                lo[w][1][1] = __byte_perm(v2[w], v3[w], 0x7632);
+                both[w][0][0] = __byte_perm(v0[w], v1[w], 0x5410);
+                both[w][0][1] = __byte_perm(v0[w], v1[w], 0x7632);
+                both[w][1][0] = __byte_perm(v2[w], v3[w], 0x5410);
+                both[w][1][1] = __byte_perm(v2[w], v3[w], 0x7632);
             }
+            // element n of word w for a pair of tokens: index 8 w + n
             auto element = [&](int index, int pair) {
-                const int w = index >> 3, n = index & 7;
-                const uint32_t z = lo[w][pair][n >> 2];
+                const int n = index & 7;
+                const uint32_t z = both[index >> 3][pair][n >> 2];
                 return ((n & 2) ? z >> 8 : z) & ((n & 1) ? 0x00f000f0u : 0x000f000fu);
             };
 #pragma unroll
@@ -521,6 +586,8 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                         mma_f16(acc[p][n], a0, a1, a2, a3, pb[n][term][0], pb[n][term][1]);
             }
         }
+        stage += C::kStageBytes;
+        if (stage == ring + C::kWarpBytes) stage = ring;
     }
 
     // ---- the CTA's warps together: outputs, maxima and sums over the rings
@@ -534,10 +601,10 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
         off[r] = group_sum(off[r]);
         const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
         if (g == 0) {
-            float *s = stats + (warp * ROWS + row) * 3;
-            s[0] = m[r];
-            s[1] = l[r];
-            s[2] = off[r];
+            float *z = stats + (warp * ROWS + row) * 3;
+            z[0] = m[r];
+            z[1] = l[r];
+            z[2] = off[r];
         }
         const float down = 1.f / up[r];
         float *o = outs + (warp * ROWS + row) * D;
@@ -555,20 +622,19 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
     for (int u = threadIdx.x; u < ROWS * (D / 4); u += kThreads) {
         const int r = u / (D / 4), e = (u - r * (D / 4)) * 4;
         if (row0 + r >= rows) break;
-        float top = -INFINITY, sum = 0.f, shift = 0.f;
+        float top = kNone, sum = 0.f, shift = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * ROWS + r) * 3]);
-        const float base = top == -INFINITY ? 0.f : top;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float *s = stats + (w * ROWS + r) * 3;
-            const float by = ex2_approx(s[0] - base);
-            const float4 z = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * D + e);
-            sum = fmaf(by, s[1], sum);
-            shift = fmaf(by, s[2], shift);
-            o.x = fmaf(by, z.x, o.x); o.y = fmaf(by, z.y, o.y);
-            o.z = fmaf(by, z.z, o.z); o.w = fmaf(by, z.w, o.w);
+            const float *z = stats + (w * ROWS + r) * 3;
+            const float by = ex2_approx(z[0] - top);
+            const float4 y = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * D + e);
+            sum = fmaf(by, z[1], sum);
+            shift = fmaf(by, z[2], shift);
+            o.x = fmaf(by, y.x, o.x); o.y = fmaf(by, y.y, o.y);
+            o.z = fmaf(by, y.z, o.z); o.w = fmaf(by, y.w, o.w);
         }
         const bool some = sum > 0.f || sum != sum;       // (a NaN score: a NaN row)
         const float inv = some ? 1.f / sum : 0.f;
@@ -609,7 +675,8 @@ bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_
     if (c.head_dim_k != c.head_dim_v || (c.head_dim_k != 64 && c.head_dim_k != 128) || bs < 8 ||
         (bs & (bs - 1)) != 0)
         return false;
-    // items are numbered within 32 bits at any split count
+    // pool rows are numbered within 32 bits, items within 31 at any split count
+    if (int64_t(c.num_blocks) * c.num_kv_heads * bs > int64_t(UINT32_MAX)) return false;
     const int64_t rows = int64_t(num_q_heads) / c.num_kv_heads * q_tokens;
     return int64_t(batch) * c.num_kv_heads * ((rows + 3) / 4) * 256 <= INT32_MAX;
 }
@@ -619,10 +686,7 @@ int int4_row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_token
     const int rows = num_q_heads / c.num_kv_heads * q_tokens;
     return (rows + tile_rows(rows) - 1) / tile_rows(rows);
 }
-int int4_resident_ctas(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens) {
-    const int rows = num_q_heads / c.num_kv_heads * q_tokens;
-    return sm_count() * (tile_rows(rows) == 16 ? 2 : 3);
-}
+int int4_resident_ctas() { return sm_count() * 3; }
 
 int launch_decode_int4(const Int4DecodeArgs &a) {
     const int rows = tile_rows(a.num_q_heads / a.cache.num_kv_heads * a.q_tokens);

@@ -31,7 +31,7 @@ int32_t auto_splits(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int3
         // fewer splits (less to merge).
         const int64_t units =
             std::max<int64_t>(1, int64_t(batch) * c.num_kv_heads * int4_row_tiles(c, hq, tokens));
-        const int64_t ctas = int4_resident_ctas(c, hq, tokens);
+        const int64_t ctas = int4_resident_ctas();
         const int64_t s_max = std::min<int64_t>(kMaxSplits, (L + 127) / 128);
         int64_t best = 1, best_cost = INT64_MAX;
         for (int64_t s = 1; s <= s_max; ++s) {

@@ -218,7 +218,7 @@ int launch_decode_int4_generic(const Int4DecodeArgs &a);
 bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
                           int32_t q_tokens);
 int int4_row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens);
-int int4_resident_ctas(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens);
+int int4_resident_ctas();
 int launch_decode_int4(const Int4DecodeArgs &a);
 
 int launch_lse_merge(int32_t num_parts, const float *out_part, const float *lse_part,
