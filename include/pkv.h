@@ -637,22 +637,33 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
 /* ---------------------------------------------------------------------------
  * pkv_paged_decode_attn_int4 -- pkv_paged_decode_attn over 4-bit pools (the
  * 4-bit cache above): K_j and V_j are the elements the codes read back as; q,
- * out, lse, splits, workspace (pkv_decode_workspace_size(batch *
- * tokens_per_seq, num_q_heads, head_dim_v, S)) and the status bits as there.
+ * out, lse, chunks and the status bits as there.
  * _multi_int4: the multi-token step (rows, causal lengths, layouts and the
- * PKV_DEV_SEQ_LEN rule of pkv_paged_decode_attn_multi; workspace as above).
+ * PKV_DEV_SEQ_LEN rule of pkv_paged_decode_attn_multi).
  * _partial_int4: the per-chunk partials (pkv_paged_decode_attn_partial).
  * A token that a row does not see reaches nothing of it, whatever its bits;
- * one that it sees and that reads as NaN makes the row NaN.
- * flags: 0, PKV_DECODE_GENERIC (the CUDA-core kernel), PKV_DECODE_NO_TCGEN05
- * (accepted: no kernel here uses tcgen05).  hq <= 262,140, batch *
+ * one that it sees and that reads as NaN makes the row NaN.  Scales of
+ * magnitude below 2^-100 count as rounded to multiples of about 2^-125, and
+ * those above 2^100 may overflow the sums.
+ * num_splits = S > 0: S chunks of every sequence, merged; 0: the library's own
+ * plan, which shares the tokens of all sequences evenly among the CTAs that
+ * the device holds, from the lengths themselves (where that is not worth it --
+ * tables of 512 tokens or fewer, or many times more (sequence, KV head) pairs
+ * than CTAs -- and for shapes of the CUDA-core kernel an S of its choice).  Either gives the same bits on every run.
+ * workspace: pkv_decode_workspace_size_int4 bytes for the call's arguments
+ * (tokens_per_seq 1 for the single-token call) on the current device, 16-byte
+ * aligned, contents on entry do not matter (0 bytes: may be NULL); calls that
+ * may overlap on the GPU need one each.
+ * Head dims 64 or 128 (equal for K and V), power-of-two block sizes 8..256
+ * and caches of fewer than 2^32 rows (num_blocks * num_kv_heads * block_size)
+ * run on tensor cores; other shapes on CUDA cores.  flags: 0,
+ * PKV_DECODE_GENERIC (the CUDA-core kernel), PKV_DECODE_NO_TCGEN05 (accepted:
+ * no kernel here uses tcgen05).  num_q_heads <= 262,140, batch *
  * tokens_per_seq <= 65535, 1 <= tokens_per_seq <= 64.
- * pkv_decode_auto_splits_int4: what num_splits = 0 resolves to (tokens_per_seq
- * 1 for the single-token call; max_seq_len = max_blocks * block_size).
  * ------------------------------------------------------------------------- */
-int32_t pkv_decode_auto_splits_int4(const pkv_cache_desc *cache, int32_t batch,
-                                    int32_t tokens_per_seq, int32_t num_q_heads,
-                                    int32_t max_seq_len, int32_t flags);
+size_t pkv_decode_workspace_size_int4(const pkv_cache_desc *cache, int32_t batch,
+                                      int32_t tokens_per_seq, int32_t num_q_heads,
+                                      int32_t max_blocks, int32_t num_splits, int32_t flags);
 
 int pkv_paged_decode_attn_int4(const pkv_cache_desc *cache, const float *q, int32_t batch,
                                int32_t num_q_heads, const void *k_pool, const void *k_params,

@@ -37,7 +37,7 @@ __all__ = [
     "decode_cascade_splits", "DEV_PREFIX", "rope_frequencies", "rope_append", "rope_append_e4m3",
     "chunk_workspace_size", "paged_chunk_attn", "paged_chunk_attn_e4m3", "DEV_QUERY_RANGE",
     "ROPE_INTERLEAVED", "ROPE_Q_FP32", "DEV_AXIS", "DEV_NO_BLOCKS", "cache_desc_int4",
-    "kv_append_int4", "copy_blocks_int4", "rope_append_int4", "decode_auto_splits_int4",
+    "kv_append_int4", "copy_blocks_int4", "rope_append_int4", "decode_workspace_size_int4",
     "paged_decode_attn_int4", "paged_decode_attn_multi_int4", "paged_decode_attn_partial_int4",
     "block_pool", "extend_sequences", "trim_sequences",
     "device_status", "BlockManager", "library_path", "DECODE_GENERIC", "DECODE_NO_TCGEN05",
@@ -662,11 +662,14 @@ def _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, mu
     return desc, B, T, Hq
 
 
-def decode_auto_splits_int4(k_pool, k_params, v_pool, v_params, batch: int, num_q_heads: int,
-                            max_seq_len: int, tokens_per_seq: int = 1, flags: int = 0) -> int:
+def decode_workspace_size_int4(k_pool, k_params, v_pool, v_params, batch: int, num_q_heads: int,
+                               max_blocks: int, tokens_per_seq: int = 1, num_splits: int = 0,
+                               flags: int = 0) -> int:
+    """Workspace bytes of the decode calls over a 4-bit cache."""
     desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
-    return int(lib.pkv_decode_auto_splits_int4(ctypes.byref(desc), batch, tokens_per_seq,
-                                               num_q_heads, _int32(max_seq_len), int(flags)))
+    return int(lib.pkv_decode_workspace_size_int4(ctypes.byref(desc), batch, tokens_per_seq,
+                                                  num_q_heads, max_blocks, _int32(num_splits),
+                                                  int(flags)))
 
 
 def _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
@@ -676,11 +679,9 @@ def _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables, seq_le
     shape = (*q.shape[:-1], desc.head_dim_v)
     if workspace is not None:
         _need(workspace, "workspace", workspace.dtype)
-    S = _int32(num_splits) or int(lib.pkv_decode_auto_splits_int4(
-        ctypes.byref(desc), B, T, Hq, _int32(block_tables.shape[1] * desc.block_size),
-        int(flags)))
-    # (a split count that the call refuses needs no workspace)
-    need = decode_workspace_size(B * T, Hq, desc.head_dim_v, S) if S <= 256 else 0
+    S = _int32(num_splits)
+    need = lib.pkv_decode_workspace_size_int4(ctypes.byref(desc), B, T, Hq,
+                                              block_tables.shape[1], S, int(flags))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if stream is not None and (out is None or lse is None or ws_bytes < need):
         # what is allocated here is used on that stream: let it belong to it

@@ -70,7 +70,7 @@ SIGNATURES = {
     "pkv_extend_sequences": (ctypes.c_int, [_i32, _i32, _P, _P, _P, _i32, _i32, _P, _P, _i32, _P,
                                             _P, _P, _P]),
     "pkv_trim_sequences": (ctypes.c_int, [_i32, _i32, _P, _P, _P, _i32, _i32, _P, _P, _P]),
-    "pkv_decode_auto_splits_int4": (_i32, [_DESC, _i32, _i32, _i32, _i32, _i32]),
+    "pkv_decode_workspace_size_int4": (_sz, [_DESC, _i32, _i32, _i32, _i32, _i32, _i32]),
     "pkv_paged_decode_attn_int4": (ctypes.c_int, [_DESC, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32,
                                                   _P, _f32, _i32, _P, _sz, _P, _P, _i32, _P]),
     "pkv_paged_decode_attn_multi_int4": (ctypes.c_int, [_DESC, _P, _i32, _i32, _i32, _P, _P, _P,

@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "pkv.h"
 #include "pkv_device.cuh"
@@ -49,6 +50,7 @@ constexpr float kNone = -3e38f;           // the running maximum of a row withou
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens of a warp's step
+constexpr int kResident = 3;              // CTAs of an SM
 
 // ROWS query rows of an item: 4 (as 8 columns of row and term), 8, or 16 (two tiles of 8).
 template <int D, int ROWS>
@@ -61,8 +63,8 @@ struct Config {
     static constexpr int kCols = ROWS == 16 ? 2 : 1;  // tiles of 8 columns
     static constexpr int kTerms = kPacked ? 1 : 2;    // products a tile of columns
     static constexpr int kLaneRows = kPacked ? 1 : 2 * kCols;
-    static constexpr int kCtas = 3;                   // per SM
-    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 3 : 4) : (ROWS == 16 ? 6 : 7);
+    static constexpr int kCtas = kResident;
+    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 3 : 4) : 7;
     // 16 rows: the query's fragments (the same for all the CTA's warps) in shared memory,
     // as the registers hold the sums
     static constexpr bool kSharedQuery = ROWS == 16;
@@ -71,7 +73,7 @@ struct Config {
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRings = kWarps * kWarpBytes;
     // the warps' outputs go over the rings at the end
-    static constexpr int kMergeBytes = kWarps * ROWS * (D + 3) * 4;
+    static constexpr int kMergeBytes = kWarps * ROWS * (D + 1) * 4;
     static constexpr int kSmem = (kRings > kMergeBytes ? kRings : kMergeBytes) + kQueryBytes;
 };
 
@@ -157,34 +159,26 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kThreads, Config<D, ROWS>::kCtas)
-decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
+// What a CTA works on: the ROWS query rows from row0 on, of KV head `head` of sequence b (of
+// length len), over the tokens begin .. end (begin a multiple of kTile); and where the
+// result goes: chunk `part` of all rows, or (slot >= 0) the workspace's place `slot`.
+struct Segment {
+    int32_t b, head, row0, len, begin, end;
+    int32_t part, slot;
+};
+
+// By the whole CTA.  `segment` says it again whenever it is called: what is wanted only
+// before or after the loop holds no register in it.
+template <int D, int ROWS, typename Say>
+__device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, int block_shift,
+                                       float *parts, float *part_lse, Say segment) {
     using C = Config<D, ROWS>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    pdl_wait();
-    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const pkv_cache_desc &c = a.cache;
     const int group = a.num_q_heads / c.num_kv_heads, rows = group * a.q_tokens;
-    // item: (sequence, KV head, split, tile of rows), the last fastest: CTAs that read
-    // the same tokens run together
-    uint32_t item = blockIdx.x;
-    const int row0 = int(item % row_tiles) * ROWS;
-    item /= row_tiles;
-    const int split = int(item % a.num_splits);
-    item /= a.num_splits;
-    const int head = int(item % c.num_kv_heads), b = int(item / c.num_kv_heads);
-
-    int64_t len = a.seq_lens[b];
-    const bool odd = len < 0 || len > (int64_t(a.max_blocks) << block_shift);
-    if ((odd || len < a.flag_below) && threadIdx.x == 0 && split == 0 && row0 == 0 && head == 0)
-        raise_status(a.status, PKV_DEV_SEQ_LEN);
-    if (odd) len = 0;
-    const int L = int(len);
-    const int64_t chunk = 64 * ((len + 64LL * a.num_splits - 1) / (64LL * a.num_splits));
-    const int begin = int(min(split * chunk, len)), end = int(min((split + 1) * chunk, len));
+    const int head = segment().head, b = segment().b, row0 = segment().row0;
+    const int begin = segment().begin, end = segment().end;
     // this warp's share, in whole tiles
     const int per = (end - begin + kWarps * kTile - 1) / (kWarps * kTile) * kTile;
     const int first = min(begin + warp * per, end), last = min(first + per, end);
@@ -341,24 +335,28 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
         }
         if constexpr (C::kSharedQuery) __syncthreads();
     }
-    const int all_see = min(last, L - a.q_tokens + 1);   // every row sees the tokens before
+    const int all_see = min(last, segment().len - a.q_tokens + 1);   // every row sees the tokens before
     // tokens that the lane's r-th row sees
     auto sees = [&](int r) {
-        const int row = row0 + (C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1));
-        return min(last, L - a.q_tokens + 1 + min(row / group, a.q_tokens - 1));
+        const Segment seg = segment();
+        const int row = seg.row0 + (C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1));
+        return min(last, seg.len - a.q_tokens + 1 + min(row / group, a.q_tokens - 1));
     };
 
-    // A row's running state: m, what is subtracted from its scores; the sums of p and of
-    // p o' (each lane its own tokens'); the weights' factor, and the largest weight of the
-    // lane's tokens.
-    float m[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
-    float up[C::kLaneRows], most[C::kLaneRows];
+    // A row's running state, in base-2 units.  A token of score y has p = 2^(y - from);
+    // l and off are the sums of p and of p o' (each lane its own tokens').  `from` is not
+    // the largest score: it is moved so that the largest weight p s' lies between 1 and
+    // 2^15, which the weights' fp16 terms need, and p stays within 2^110.  It moves when a
+    // weight or a p would leave that (`heaviest` and `top`: the largest y + log2 s' and y
+    // that were met then), in the first tile and seldom after it, so that the common tile
+    // needs no maximum over lanes.
+    float from[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
+    float heaviest[C::kLaneRows], top[C::kLaneRows];
     float acc[C::kProducts][C::kCols][4];
 #pragma unroll
     for (int r = 0; r < C::kLaneRows; ++r) {
-        m[r] = kNone;
-        l[r] = off[r] = most[r] = 0.f;
-        up[r] = 1.f;
+        from[r] = heaviest[r] = top[r] = kNone;
+        l[r] = off[r] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < C::kProducts; ++i)
@@ -366,16 +364,6 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
         for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
-    auto rescale = [&](const float (&by)[C::kLaneRows]) {
-#pragma unroll
-        for (int i = 0; i < C::kProducts; ++i)
-#pragma unroll
-            for (int n = 0; n < C::kCols; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    acc[i][n][x] *= by[C::kPacked ? 0 : 2 * n + (x & 1)];
-    };
-
     const int tok = token_at<D>(g);                // the lane's token of the first 8
     const uint32_t my_k = D == 128 ? piece_at<D>(tok, t) : piece_at<D>(tok, 0) + 8 * t;
     auto word_at = [&](int row) {
@@ -383,63 +371,65 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                (D == 128 ? piece_at<D>(row, g >> 1) + (g & 1) * 8 : piece_at<D>(row, 0) + g * 4);
     };
     const uint32_t my_v0 = word_at(token_at<D>(2 * t)), my_v1 = word_at(token_at<D>(2 * t + 1));
-    uint32_t stage = ring;
-    for (int i = 0; i < tiles; ++i) {
-        cp_async_wait<C::kStages - 2>();
-        __syncwarp();                  // the tile is there; the stage before it is free
-        if (i + C::kStages - 1 < tiles) load(i + C::kStages - 1);
-        cp_async_commit();
-        const uint32_t params = stage + 2 * kTile * C::kRowBytes + tok * 4;
-        const int j0 = first + i * kTile;
-
-        // ---- scores of 32 tokens, tok + 8 k: sums over the codes
-        float s[2][C::kCols][4];
+    // the sums over the codes of a tile's keys: scores of tokens tok + 8 k
+    float s[2][C::kCols][4];
+    auto dot_keys = [&](uint32_t stage) {
+        uint32_t kw[4][C::kWordsK];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) lds_words(stage + my_k + 8 * k * C::kRowBytes, kw[k]);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[h][n][e] = 0.f;
-        {
-            uint32_t kw[4][C::kWordsK];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) lds_words(stage + my_k + 8 * k * C::kRowBytes, kw[k]);
+        for (int w = 0; w < C::kWordsK; ++w) {
+            uint32_t q[C::kCols][C::kTerms][4];
 #pragma unroll
-            for (int w = 0; w < C::kWordsK; ++w) {
-                uint32_t q[C::kCols][C::kTerms][4];
+            for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                for (int n = 0; n < C::kCols; ++n)
+                for (int term = 0; term < C::kTerms; ++term) {
+                    if constexpr (C::kSharedQuery) {
+                        lds_words(shared_query + ((w * C::kCols + n) * C::kTerms + term) * 512,
+                                  q[n][term]);
+                    } else {
 #pragma unroll
-                    for (int term = 0; term < C::kTerms; ++term) {
-                        if constexpr (C::kSharedQuery) {
-                            lds_words(shared_query + ((w * C::kCols + n) * C::kTerms + term) * 512,
-                                      q[n][term]);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) q[n][term][e] = qf[n][term][w][e];
-                        }
+                        for (int e = 0; e < 4; ++e) q[n][term][e] = qf[n][term][w][e];
                     }
+                }
 #pragma unroll
-                for (int step = 0; step < 2; ++step)
+            for (int step = 0; step < 2; ++step)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t u = step ? kw[2 * h][w] >> 8 : kw[2 * h][w];
-                        const uint32_t v = step ? kw[2 * h + 1][w] >> 8 : kw[2 * h + 1][w];
-                        const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
-                        const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = step ? kw[2 * h][w] >> 8 : kw[2 * h][w];
+                    const uint32_t v = step ? kw[2 * h + 1][w] >> 8 : kw[2 * h + 1][w];
+                    const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
+                    const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
 #pragma unroll
-                        for (int n = 0; n < C::kCols; ++n)
+                    for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                            for (int term = 0; term < C::kTerms; ++term)
-                                mma_f16(s[h][n], a0, a1, a2, a3, q[n][term][2 * step],
-                                        q[n][term][2 * step + 1]);
-                    }
-            }
+                        for (int term = 0; term < C::kTerms; ++term)
+                            mma_f16(s[h][n], a0, a1, a2, a3, q[n][term][2 * step],
+                                    q[n][term][2 * step + 1]);
+                }
         }
-        // ---- x[row][k]: the scores, less `from` of their row
+    };
+    uint32_t stage = ring;
+    for (int i = 0; i < tiles; ++i) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();                  // the tile is there; the stage before it is free
+        if (i + C::kStages - 1 < tiles) load(i + C::kStages - 1);
+        cp_async_commit();
+        dot_keys(stage);
+        const uint32_t params = stage + 2 * kTile * C::kRowBytes + tok * 4;
+        const int j0 = first + i * kTile;
+        const bool tail = j0 + kTile > all_see;
+
+        // ---- x[row][k]: the scores, less what is given
         float x[C::kLaneRows][4];
         uint32_t hidden = 0;           // bit 4 r + k
-        auto scores = [&](const float (&from)[C::kLaneRows]) {
+        auto scores = [&](const float (&less)[C::kLaneRows]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t kp = lds32(params + 32 * k);
@@ -449,11 +439,11 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                     const float (&z)[4] = s[k >> 1][r >> 1];
                     const float dot = C::kPacked ? z[2 * (k & 1)] + z[2 * (k & 1) + 1]
                                                  : z[2 * (k & 1) + (r & 1)];
-                    x[r][k] = fmaf(ks, dot * factor[r], fmaf(ko, offset_factor[r], -from[r]));
+                    x[r][k] = fmaf(ks, dot * factor[r], fmaf(ko, offset_factor[r], -less[r]));
                 }
             }
             // tokens past the end, or past what a row sees
-            if (j0 + kTile > all_see) {
+            if (tail) {
 #pragma unroll
                 for (int r = 0; r < C::kLaneRows; ++r) {
                     const int n = sees(r);
@@ -466,69 +456,72 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                 }
             }
         };
-        scores(m);
-        float largest = x[0][0];
+        // ---- the values' weights, over x, and the tile's sums of p and p o'
+        float sum[C::kLaneRows], shift[C::kLaneRows];
+        auto weigh = [&](auto in_tail) {
+            bool leaves = false;       // a weight or a p is out of its range
 #pragma unroll
-        for (int r = 0; r < C::kLaneRows; ++r)
+            for (int r = 0; r < C::kLaneRows; ++r) sum[r] = shift[r] = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) largest = fmaxf(largest, x[r][k]);
-        // m follows once a score is past it by 8: probabilities to 2^8 are within the sums'
-        // and the terms' reach, and the common tile needs no maximum over lanes
-        const bool grows = __any_sync(0xffffffffu, largest > 8.f);
-        if (grows) {
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t vp = lds32(params + (kTile + 8 * k) * 4);
+                const float vs = bf16_lo_to_f32(vp), vo = bf16_hi_to_f32(vp);
+#pragma unroll
+                for (int r = 0; r < C::kLaneRows; ++r) {
+                    const float p = ex2_approx(x[r][k]);
+                    leaves |= p > 1.2e33f;                        // 2^110
+                    sum[r] += p;
+                    // (what is not seen may be anything)
+                    if (decltype(in_tail)::value && (hidden >> (4 * r + k) & 1)) {
+                        x[r][k] = 0.f;
+                    } else {
+                        x[r][k] = p * vs;
+                        shift[r] = fmaf(p, vo, shift[r]);
+                    }
+                    leaves |= !(fabsf(x[r][k]) <= 32768.f);
+                }
+            }
+            return leaves;
+        };
+        scores(from);
+        if (__any_sync(0xffffffffu, tail ? weigh(std::true_type{}) : weigh(std::false_type{}))) {
             float by[C::kLaneRows];
 #pragma unroll
             for (int r = 0; r < C::kLaneRows; ++r) by[r] = 0.f;
-            scores(by);                // (from kNone the differences are only "some")
+            scores(by);
 #pragma unroll
             for (int r = 0; r < C::kLaneRows; ++r) {
-                const float top =
-                    group_max(fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3])));
-                const float now = fmaxf(m[r], top);
-                by[r] = ex2_approx(m[r] - now);
-                m[r] = now;
+                float y = kNone, w = kNone;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float vs = fabsf(bf16_lo_to_f32(lds32(params + (kTile + 8 * k) * 4)));
+                    y = fmaxf(y, x[r][k]);
+                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f) w = fmaxf(w, x[r][k] + log2f(vs));
+                }
+                top[r] = fmaxf(top[r], group_max(y));
+                heaviest[r] = fmaxf(heaviest[r], group_max(w));
+                const float now =
+                    fmaxf(from[r], fminf(fmaxf(heaviest[r] - 10.f, top[r] - 100.f), top[r] + 100.f));
+                by[r] = ex2_approx(from[r] - now);
+                from[r] = now;
                 l[r] *= by[r];
                 off[r] *= by[r];
-                most[r] *= by[r];
             }
-            rescale(by);
-            scores(m);
-        }
-        // ---- probabilities and the values' weights
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t vp = lds32(params + (kTile + 8 * k) * 4);
-            float vs = bf16_lo_to_f32(vp), vo = bf16_hi_to_f32(vp);
+            for (int p = 0; p < C::kProducts; ++p)
 #pragma unroll
-            for (int r = 0; r < C::kLaneRows; ++r) {
-                const float p = ex2_approx(x[r][k]);
-                l[r] += p;
-                // (what is not seen may be anything)
-                const bool seen = !(hidden >> (4 * r + k) & 1);
-                x[r][k] = seen ? p * vs : 0.f;
-                off[r] = seen ? fmaf(p, vo, off[r]) : off[r];
-            }
+                for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[p][n][e] *= by[C::kPacked ? 0 : 2 * n + (e & 1)];
+            scores(from);
+            if (tail) weigh(std::true_type{});
+            else weigh(std::false_type{});
         }
-        float over = 0.f;
 #pragma unroll
         for (int r = 0; r < C::kLaneRows; ++r) {
-            const float w = fmaxf(fmaxf(fabsf(x[r][0]), fabsf(x[r][1])),
-                                  fmaxf(fabsf(x[r][2]), fabsf(x[r][3])));
-            most[r] = fmaxf(most[r], w);
-            over = fmaxf(over, w * up[r]);
-        }
-        // The factor is set where m has moved (the weights before have shrunk) and where a
-        // weight would leave fp16's range; so a row's largest is between 1 and 2^15.
-        if (__any_sync(0xffffffffu, over > 32768.f) || grows) {
-            float by[C::kLaneRows];
-#pragma unroll
-            for (int r = 0; r < C::kLaneRows; ++r) {
-                const float whole = group_max(most[r]);
-                const float now = whole > 0.f ? pow2(10 - exponent(whole)) : up[r];
-                by[r] = fminf(now / up[r], 3.4e38f);      // (a sum of 0 stays 0)
-                up[r] = now;
-            }
-            rescale(by);
+            l[r] += sum[r];
+            off[r] += shift[r];
         }
         // ---- values
 #pragma unroll
@@ -536,7 +529,7 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
             // weights as fp16 terms, in the products' layout: [tile of columns][term][half]
             uint32_t pb[C::kCols][C::kTerms][2];
             if constexpr (C::kPacked) {
-                const float u = x[0][2 * h] * up[0], v = x[0][2 * h + 1] * up[0];
+                const float u = x[0][2 * h], v = x[0][2 * h + 1];
                 const uint32_t hi = pack_f16x2(u, v);
                 const uint32_t lo = pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
                 pb[0][0][0] = transpose8(__byte_perm(hi, lo, 0x5410));
@@ -546,8 +539,7 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                 for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        const float u = x[2 * n][2 * h + half] * up[2 * n];
-                        const float v = x[2 * n + 1][2 * h + half] * up[2 * n + 1];
+                        const float u = x[2 * n][2 * h + half], v = x[2 * n + 1][2 * h + half];
                         const uint32_t hi = pack_f16x2(u, v);
                         const uint32_t lo =
                             pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
@@ -594,19 +586,16 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
     cp_async_wait<0>();
     __syncthreads();
     float *outs = reinterpret_cast<float *>(smem);            // [warp][ROWS][D]
-    float *stats = outs + kWarps * ROWS * D;                  // [warp][ROWS][3]
+    float *stats = outs + kWarps * ROWS * D;                  // [warp][ROWS]
 #pragma unroll
     for (int r = 0; r < C::kLaneRows; ++r) {
+        // each warp's row by itself: its output, and log2 of its sum
         l[r] = group_sum(l[r]);
         off[r] = group_sum(off[r]);
+        const bool some = l[r] > 0.f || l[r] != l[r];         // (a NaN score: a NaN row)
+        const float inv = some ? 1.f / l[r] : 0.f;
         const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
-        if (g == 0) {
-            float *z = stats + (warp * ROWS + row) * 3;
-            z[0] = m[r];
-            z[1] = l[r];
-            z[2] = off[r];
-        }
-        const float down = 1.f / up[r];
+        if (g == 0) stats[warp * ROWS + row] = some ? from[r] + log2f(l[r]) : kNone;
         float *o = outs + (warp * ROWS + row) * D;
 #pragma unroll
         for (int p = 0; p < C::kProducts; ++p)
@@ -615,56 +604,405 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
                 const int index = p + half * C::kProducts, w = index >> 3, n = index & 7;
                 const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
                                            : acc[p][r >> 1][2 * half + (r & 1)];
-                o[8 * (C::kWordsV * g + w) + n] = z * (n & 1 ? 1048576.f : 16777216.f) * down;
+                o[8 * (C::kWordsV * g + w) + n] = fmaf(z, n & 1 ? 1048576.f : 16777216.f, off[r]) * inv;
             }
     }
     __syncthreads();
+    const Segment seg = segment();
+    float *out = seg.slot < 0 ? a.out_part : parts + int64_t(seg.slot) * ROWS * D;
+    float *lse = seg.slot < 0 ? a.lse_part : part_lse + int64_t(seg.slot) * ROWS;
     for (int u = threadIdx.x; u < ROWS * (D / 4); u += kThreads) {
         const int r = u / (D / 4), e = (u - r * (D / 4)) * 4;
-        if (row0 + r >= rows) break;
-        float top = kNone, sum = 0.f, shift = 0.f;
+        if (seg.row0 + r >= rows) break;
+        float most = kNone, all = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * ROWS + r) * 3]);
+        for (int w = 0; w < kWarps; ++w) most = fmaxf(most, stats[w * ROWS + r]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float *z = stats + (w * ROWS + r) * 3;
-            const float by = ex2_approx(z[0] - top);
+            const float z = stats[w * ROWS + r];
+            const float by = z == kNone ? 0.f : ex2_approx(z - most);
             const float4 y = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * D + e);
-            sum = fmaf(by, z[1], sum);
-            shift = fmaf(by, z[2], shift);
+            all += by;
             o.x = fmaf(by, y.x, o.x); o.y = fmaf(by, y.y, o.y);
             o.z = fmaf(by, y.z, o.z); o.w = fmaf(by, y.w, o.w);
         }
-        const bool some = sum > 0.f || sum != sum;       // (a NaN score: a NaN row)
-        const float inv = some ? 1.f / sum : 0.f;
-        const int token = (row0 + r) / group;
-        const int64_t to = ((int64_t(split) * a.batch + b) * a.q_tokens + token) * a.num_q_heads +
-                           head * group + (row0 + r - token * group);
-        *reinterpret_cast<float4 *>(a.out_part + to * D + e) =
-            some ? make_float4((o.x + shift) * inv, (o.y + shift) * inv, (o.z + shift) * inv,
-                               (o.w + shift) * inv)
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e == 0) a.lse_part[to] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
+        const bool some = all != 0.f;
+        const float inv = some ? 1.f / all : 0.f;
+        int64_t to = r;
+        if (seg.slot < 0) {
+            const int token = (seg.row0 + r) / group;
+            to = ((int64_t(seg.part) * a.batch + seg.b) * a.q_tokens + token) * a.num_q_heads +
+                 seg.head * group + (seg.row0 + r - token * group);
+        }
+        *reinterpret_cast<float4 *>(out + to * D + e) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (e == 0)
+            lse[to] = seg.slot >= 0 ? (some ? most + log2f(all) : kNone)
+                      : some        ? (most + log2f(all)) * kLn2
+                                    : -INFINITY;
     }
+}
+
+// The sequence's length; one that is not valid counts as 0.
+__device__ __forceinline__ int length_of(const Int4DecodeArgs &a, int block_shift, int b) {
+    const int32_t len = a.seq_lens[b];
+    return len < 0 || len > (int64_t(a.max_blocks) << block_shift) ? 0 : len;
+}
+__device__ __forceinline__ void check_length(const Int4DecodeArgs &a, int block_shift, int b) {
+    const int32_t len = a.seq_lens[b];
+    if (len < a.flag_below || len < 0 || len > (int64_t(a.max_blocks) << block_shift))
+        raise_status(a.status, PKV_DEV_SEQ_LEN);
+}
+
+// Lengths and tables into L2, a line a thread, while the kernel before this one ends: the
+// first tile waits for a length, then for a table entry, then for its rows.
+__device__ __forceinline__ void prefetch_tables(const Int4DecodeArgs &a) {
+    const int64_t at = (blockIdx.x * int64_t(kThreads) + threadIdx.x) * 128;
+    const int64_t lens = int64_t(a.batch) * 4, tables = lens * a.max_blocks;
+    if (at < lens)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.seq_lens) + at));
+    if (at < tables)
+        asm volatile("prefetch.global.L2 [%0];"
+                     ::"l"(reinterpret_cast<const char *>(a.block_tables) + at));
+}
+
+// ---- a given number of splits: one CTA for each (sequence, KV head, split, tile of rows),
+// the last fastest, so that CTAs that read the same tokens run together
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, Config<D, ROWS>::kCtas)
+decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    prefetch_tables(a);
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t item = blockIdx.x;
+    const int row0 = int(item % row_tiles) * ROWS;
+    item /= row_tiles;
+    const int split = int(item % a.num_splits);
+    item /= a.num_splits;
+    const int head = int(item % a.cache.num_kv_heads), b = int(item / a.cache.num_kv_heads);
+    if (threadIdx.x == 0 && split == 0 && row0 == 0 && head == 0) check_length(a, block_shift, b);
+    const int64_t len = length_of(a, block_shift, b);
+    const int64_t chunk = 64 * ((len + 64LL * a.num_splits - 1) / (64LL * a.num_splits));
+    const int begin = int(min(split * chunk, len)), end = int(min((split + 1) * chunk, len));
+    const Segment seg{b, head, row0, int(len), begin, end, split, -1};
+    attend<D, ROWS>(a, smem, block_shift, nullptr, nullptr, [&]() { return seg; });
+}
+
+// ---- the library's own plan: the CTAs that the device holds at once share the batch's
+// work evenly, whatever the lengths.
+//
+// A unit is a (sequence, KV head, tile of rows): n = ceil(length / 128) steps of a CTA's
+// four warps, and kStart more for the start and end of one more piece of work.  The units lie one after another
+// on a line of T = sum (n + kStart); CTA i of C takes [i T / C, (i + 1) T / C) of it, so
+// it meets the end of one unit, perhaps some whole ones, and the beginning of another.
+// A whole unit goes straight to the output; the parts of others go to the workspace
+// (CTA i's at 2 i, or 2 i + 1 if it is the unit's first) and are merged by the next
+// kernel, from a record that the unit's first CTA leaves.  Where all sequences have the
+// same number of steps, C is a multiple of the units if one is near enough, so that no CTA
+// meets two (8 x 32K, 64 units: 448 of 456 CTAs).
+constexpr int kStep = kWarps * kTile;
+constexpr int kStart = 4;
+constexpr int kMaxPlanned = 2048;          // sequences
+
+struct Record {                            // of a unit: its parts (0: whole) and their first CTA
+    int32_t parts, first;
+};
+// Where CTA i's share of a line of `total` begins, i <= ctas <= total.
+__device__ __forceinline__ int64_t share_at(int i, int64_t total, int ctas) {
+    int64_t q;
+    int r;
+    if (total <= INT32_MAX) {
+        q = int(total) / ctas;
+        r = int(total) - int(q) * ctas;
+    } else {
+        q = total / ctas;
+        r = int(total - q * ctas);
+    }
+    return i * q + i * r / ctas;           // (ctas^2 is far below 2^31)
+}
+struct Share {                             // a CTA's share of the line, and where it stands
+    int64_t at, to, start, total;          // start: of sequence b
+    int32_t ctas, b, len;
+    int32_t extra;                         // what a unit has on the line beside its steps
+};
+
+__device__ __forceinline__ int steps_of(int len) {
+    return int((uint32_t(len) + kStep - 1) / kStep);
+}
+
+// The next part of a unit with something to do (b < 0: none).  Whoever has a unit's beginning writes
+// its record if `writes`.
+__device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int block_shift, int row_tiles,
+                                                int rows, Record *records, Share &share,
+                                                bool writes) {
+    const int heads = a.cache.num_kv_heads * row_tiles;     // units of a sequence
+    Segment seg = {};
+    seg.b = -1;
+    while (share.at < share.to) {
+        const int n = steps_of(share.len), cost = n + share.extra;
+        const int64_t in = share.at - share.start;
+        if (in >= int64_t(cost) * heads) {
+            share.start += int64_t(cost) * heads;
+            share.len = length_of(a, block_shift, ++share.b);
+            continue;
+        }
+        const int unit = in <= INT32_MAX ? int(in) / cost : int(in / cost);
+        const int64_t unit_at = share.start + int64_t(unit) * cost, unit_end = unit_at + cost;
+        const int64_t stop = min(share.to, unit_end);
+        const int s0 = max(0, int(share.at - unit_at) - share.extra);
+        const int s1 = max(0, int(stop - unit_at) - share.extra);
+        const bool empty = n == 0 && share.at == unit_at;
+        share.at = stop;
+        // (a sequence without tokens: whoever has its first place writes its rows)
+        if (s1 > s0 || empty) {
+            const bool whole = s0 == 0 && s1 == n;
+            const int cta = int(blockIdx.x);
+            seg.b = share.b;
+            seg.head = unit / row_tiles;
+            seg.row0 = (unit - seg.head * row_tiles) * rows;
+            seg.len = share.len;
+            seg.begin = s0 * kStep;
+            seg.end = int(min(int64_t(s1) * kStep, int64_t(share.len)));
+            seg.slot = whole ? -1 : 2 * cta + (s0 == 0 ? 1 : 0);
+            if (s0 == 0 && writes) {
+                int parts = 0;
+                if (!whole) {
+                    // the last CTA whose share begins before the unit's end: a guess, put
+                    // right
+                    int last = int(float(unit_end) / float(share.total) * float(share.ctas));
+                    last = max(cta, min(last, share.ctas - 1));
+                    while (last + 1 < share.ctas &&
+                           share_at(last + 1, share.total, share.ctas) < unit_end)
+                        ++last;
+                    while (share_at(last, share.total, share.ctas) >= unit_end) --last;
+                    parts = last - cta + 1;
+                }
+                records[int64_t(share.b) * heads + unit] = {parts, cta};
+            }
+            break;
+        }
+    }
+    return seg;
+}
+
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kThreads, Config<D, ROWS>::kCtas)
+decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift, float *parts,
+                           float *part_lse, Record *records) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    // (in shared memory, as the registers belong to the work itself)
+    __shared__ Share s_share;
+    __shared__ Segment s_seg;
+    prefetch_tables(a);
+    pdl_wait();
+    pdl_launch_dependents();
+    {
+        // Each warp by itself, without a barrier: the line's length, and the sequence in
+        // which this CTA's share begins.
+        const int lane = threadIdx.x & 31, heads = a.cache.num_kv_heads * row_tiles;
+        const int per = (a.batch + 31) / 32;
+        const int b0 = min(lane * per, a.batch), b1 = min(b0 + per, a.batch);
+        int64_t mine = 0;
+        int least = INT32_MAX, most = 0;
+        for (int b = b0; b < b1; ++b) {
+            if (blockIdx.x == 0 && threadIdx.x < 32) check_length(a, block_shift, b);
+            const int n = steps_of(length_of(a, block_shift, b));
+            least = min(least, n);
+            most = max(most, n);
+            mine += n + kStart;
+        }
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        Share share;
+        const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+        const int units = a.batch * heads, ctas = int(gridDim.x), even = ctas / units * units;
+        // (a share that begins with a unit has no more to start than any other)
+        share.extra = least == most && least > 0 && 10 * even >= 9 * ctas ? 0 : kStart;
+        if (share.extra == 0) {
+            mine -= int64_t(kStart) * (b1 - b0);
+            upto -= int64_t(kStart) * b1;
+        }
+        share.total = (all - (share.extra ? 0 : int64_t(kStart) * a.batch)) * heads;
+        // each CTA has a place of the line or more
+        share.ctas = int(min(int64_t(share.extra ? ctas : even), share.total));
+        if (blockIdx.x >= share.ctas) return;
+        share.at = share_at(blockIdx.x, share.total, share.ctas);
+        share.to = share_at(blockIdx.x + 1, share.total, share.ctas);
+        // the lane whose sequences it begins in
+        share.start = (upto - mine) * heads;
+        share.b = b0;
+        share.len = 0;
+        const bool here = share.start <= share.at && share.at < upto * heads;
+        if (here)
+            for (;; ++share.b) {
+                share.len = length_of(a, block_shift, share.b);
+                const int64_t cost = int64_t(steps_of(share.len) + share.extra) * heads;
+                if (share.at < share.start + cost) break;
+                share.start += cost;
+            }
+        const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        share.start = __shfl_sync(0xffffffffu, share.start, owner);
+        share.b = __shfl_sync(0xffffffffu, share.b, owner);
+        share.len = __shfl_sync(0xffffffffu, share.len, owner);
+        if (threadIdx.x < 32) {
+            const Segment seg = next_segment(a, block_shift, row_tiles, ROWS, records, share, lane == 0);
+            if (lane == 0) {
+                s_seg = seg;
+                s_share = share;
+            }
+        }
+    }
+    __syncthreads();
+    while (s_seg.b >= 0) {
+        attend<D, ROWS>(a, smem, block_shift, parts, part_lse,
+                        [&]() { return Segment(*const_cast<const Segment *>(&s_seg)); });
+        __syncthreads();           // nobody wants the segment any more, and the rings are free
+        if (threadIdx.x == 0) {
+            Share share = s_share;
+            s_seg = next_segment(a, block_shift, row_tiles, ROWS, records, share, true);
+            s_share = share;
+        }
+        __syncthreads();
+    }
+}
+
+// Merges the units in parts.  A CTA has a unit's rows RB at a time, each by kThreads / RB
+// threads: D / 4 threads with four elements of the row each, times the groups that take
+// its parts in turn.  Many parts (one row a CTA) want groups, few parts rows.
+template <int D, int ROWS, int RB>
+__global__ void __launch_bounds__(kThreads)
+int4_merge_kernel(const Int4DecodeArgs a, int row_tiles, const float *parts, const float *part_lse,
+                  const Record *records) {
+    constexpr int kLanes = D / 4, kGroups = kThreads / RB / kLanes;
+    __shared__ float4 s_out[RB][kGroups][kLanes];
+    __shared__ float s_top[RB][kGroups], s_sum[RB][kGroups];
+    pdl_wait();
+    pdl_launch_dependents();
+    const Record rec = records[blockIdx.x];
+    if (rec.parts == 0) return;
+    const int rb = threadIdx.x / (kThreads / RB), e = threadIdx.x % kLanes;
+    const int grp = threadIdx.x % (kThreads / RB) / kLanes;
+    const int r = blockIdx.y * RB + rb;                       // of the unit's tile
+    float top = kNone, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 10;
+    for (int p0 = grp; p0 < rec.parts; p0 += kGroups * kAhead) {
+        float z[kAhead];
+        float4 x[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int p = p0 + u * kGroups;
+            const int64_t slot = 2 * (int64_t(rec.first) + p) + (p == 0 ? 1 : 0);
+            const bool in = p < rec.parts;
+            z[u] = in ? part_lse[slot * ROWS + r] : kNone;
+            x[u] = in ? reinterpret_cast<const float4 *>(parts + (slot * ROWS + r) * D)[e]
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float now = top;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) now = fmaxf(now, z[u]);
+        const float by = ex2_approx(top - now);
+        sum *= by;
+        o = make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float w = z[u] == kNone ? 0.f : ex2_approx(z[u] - now);
+            sum += w;
+            o.x = fmaf(w, x[u].x, o.x); o.y = fmaf(w, x[u].y, o.y);
+            o.z = fmaf(w, x[u].z, o.z); o.w = fmaf(w, x[u].w, o.w);
+        }
+        top = now;
+    }
+    if constexpr (kGroups > 1) {
+        s_out[rb][grp][e] = o;
+        if (e == 0) {
+            s_top[rb][grp] = top;
+            s_sum[rb][grp] = sum;
+        }
+        __syncthreads();
+        if (grp != 0) return;
+        float most = kNone, all = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) most = fmaxf(most, s_top[rb][i]);
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const float w = ex2_approx(s_top[rb][i] - most);
+            const float4 x = s_out[rb][i][e];
+            all = fmaf(w, s_sum[rb][i], all);
+            o.x = fmaf(w, x.x, o.x); o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z); o.w = fmaf(w, x.w, o.w);
+        }
+        top = most;
+        sum = all;
+    }
+    const int group = a.num_q_heads / a.cache.num_kv_heads;
+    const int head = int(blockIdx.x) / row_tiles % a.cache.num_kv_heads;
+    const int b = int(blockIdx.x) / (row_tiles * a.cache.num_kv_heads);
+    const int row = int(blockIdx.x) % row_tiles * ROWS + r, token = row / group;
+    if (token >= a.q_tokens) return;
+    const bool some = sum != 0.f;
+    const float inv = some ? 1.f / sum : 0.f;
+    const int64_t to = (int64_t(b) * a.q_tokens + token) * a.num_q_heads + head * group +
+                       (row - token * group);
+    *reinterpret_cast<float4 *>(a.out_part + to * D + 4 * e) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (e == 0) a.lse_part[to] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // Rows of an item for `rows` in all.
 int tile_rows(int rows) { return rows <= 4 ? 4 : rows <= 8 ? 8 : 16; }
 
-template <int D, int ROWS>
-int launch(const Int4DecodeArgs &a) {
-    using C = Config<D, ROWS>;
-    const cudaError_t e = cudaFuncSetAttribute(
-        decode_int4_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return cuda_status(e);
-    const int rows = a.num_q_heads / a.cache.num_kv_heads * a.q_tokens;
-    const int tiles = (rows + ROWS - 1) / ROWS;
-    const int64_t items = int64_t(a.batch) * a.cache.num_kv_heads * tiles * a.num_splits;
+int shift_of(int block_size) {
     int shift = 0;
-    while ((1 << shift) < a.cache.block_size) ++shift;
-    return launch_pdl(decode_int4_kernel<D, ROWS>, dim3(unsigned(items)), dim3(kThreads), C::kSmem,
-                      a.stream, a, tiles, shift);
+    while ((1 << shift) < block_size) ++shift;
+    return shift;
+}
+
+int row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens) {
+    const int rows = num_q_heads / c.num_kv_heads * q_tokens;
+    return (rows + tile_rows(rows) - 1) / tile_rows(rows);
+}
+
+template <int D, int ROWS>
+int launch(const Int4DecodeArgs &a, void *workspace) {
+    using C = Config<D, ROWS>;
+    static_assert(C::kCtas == kResident, "the plan's CTAs are those that run at once");
+    const int tiles = row_tiles(a.cache, a.num_q_heads, a.q_tokens);
+    const int shift = shift_of(a.cache.block_size);
+    if (a.num_splits > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            decode_int4_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return cuda_status(e);
+        const int64_t items = int64_t(a.batch) * a.cache.num_kv_heads * tiles * a.num_splits;
+        return launch_pdl(decode_int4_kernel<D, ROWS>, dim3(unsigned(items)), dim3(kThreads),
+                          C::kSmem, a.stream, a, tiles, shift);
+    }
+    const cudaError_t e = cudaFuncSetAttribute(decode_int4_planned_kernel<D, ROWS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int ctas = sm_count() * kResident, units = a.batch * a.cache.num_kv_heads * tiles;
+    float *parts = static_cast<float *>(workspace);
+    float *part_lse = parts + size_t(2) * ctas * ROWS * D;
+    Record *records = reinterpret_cast<Record *>(part_lse + size_t(2) * ctas * ROWS);
+    const int st = launch_pdl(decode_int4_planned_kernel<D, ROWS>, dim3(ctas), dim3(kThreads), C::kSmem,
+                              a.stream, a, tiles, shift, parts, part_lse, records);
+    if (st != PKV_OK) return st;
+    // more than about nine parts a unit: a row a CTA, its parts in groups
+    constexpr int kRows = 512 / D;
+    const bool many = ctas > 8 * units;
+    return launch_pdl(many ? int4_merge_kernel<D, ROWS, 1> : int4_merge_kernel<D, ROWS, kRows>,
+                      dim3(units, many ? ROWS : (ROWS + kRows - 1) / kRows), dim3(kThreads), 0,
+                      a.stream, a, tiles, static_cast<const float *>(parts),
+                      static_cast<const float *>(part_lse), static_cast<const Record *>(records));
 }
 
 }  // namespace
@@ -681,18 +1019,28 @@ bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_
     return int64_t(batch) * c.num_kv_heads * ((rows + 3) / 4) * 256 <= INT32_MAX;
 }
 
-// Items per (sequence, KV head, split), and the CTAs that run at once.
-int int4_row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens) {
-    const int rows = num_q_heads / c.num_kv_heads * q_tokens;
-    return (rows + tile_rows(rows) - 1) / tile_rows(rows);
+size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
+                           int32_t q_tokens, int32_t max_blocks) {
+    if (batch > kMaxPlanned || !int4_kernel_supports(c, batch, num_q_heads, q_tokens)) return 0;
+    const int64_t ctas = int64_t(sm_count()) * kResident;
+    const int64_t units = int64_t(batch) * c.num_kv_heads * row_tiles(c, num_q_heads, q_tokens);
+    // (many units for each CTA: the device evens them out by itself; sequences of a few
+    // steps at most: a plan costs more than it evens out, 16 of 128 tokens 7.7 us against 4.5)
+    if (units > 4 * ctas || int64_t(max_blocks) * c.block_size <= 4 * kStep) return 0;
+    const int rows = tile_rows(num_q_heads / c.num_kv_heads * q_tokens);
+    return size_t(ctas) * 2 * rows * (c.head_dim_v + 1) * sizeof(float) +
+           size_t(units) * sizeof(Record);
 }
-int int4_resident_ctas() { return sm_count() * 3; }
 
-int launch_decode_int4(const Int4DecodeArgs &a) {
+int launch_decode_int4(const Int4DecodeArgs &a, void *workspace) {
     const int rows = tile_rows(a.num_q_heads / a.cache.num_kv_heads * a.q_tokens);
     if (a.cache.head_dim_k == 128)
-        return rows == 4 ? launch<128, 4>(a) : rows == 8 ? launch<128, 8>(a) : launch<128, 16>(a);
-    return rows == 4 ? launch<64, 4>(a) : rows == 8 ? launch<64, 8>(a) : launch<64, 16>(a);
+        return rows == 4   ? launch<128, 4>(a, workspace)
+               : rows == 8 ? launch<128, 8>(a, workspace)
+                           : launch<128, 16>(a, workspace);
+    return rows == 4   ? launch<64, 4>(a, workspace)
+           : rows == 8 ? launch<64, 8>(a, workspace)
+                       : launch<64, 16>(a, workspace);
 }
 
 }  // namespace pkv

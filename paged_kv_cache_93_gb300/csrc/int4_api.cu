@@ -22,41 +22,34 @@ bool on_tensor_cores(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int
            int4_kernel_supports(c, batch, hq, tokens);
 }
 
-int32_t auto_splits(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
-                    int64_t max_seq_len, int32_t flags) {
-    const int64_t L = std::max<int64_t>(1, max_seq_len);
-    if (on_tensor_cores(c, batch, tokens, hq, flags)) {
-        // The least rounds of resident CTAs x (128-token steps of a CTA's four warps + 2
-        // for its start and end), for sequences of the longest length; a tie goes to
-        // fewer splits (less to merge).
-        const int64_t units =
-            std::max<int64_t>(1, int64_t(batch) * c.num_kv_heads * int4_row_tiles(c, hq, tokens));
-        const int64_t ctas = int4_resident_ctas();
-        const int64_t s_max = std::min<int64_t>(kMaxSplits, (L + 127) / 128);
-        int64_t best = 1, best_cost = INT64_MAX;
-        for (int64_t s = 1; s <= s_max; ++s) {
-            const int64_t chunk = 64 * ((L + 64 * s - 1) / (64 * s));
-            const int64_t cost = (units * s + ctas - 1) / ctas * ((chunk + 127) / 128 + 2);
-            if (cost < best_cost) {
-                best = s;
-                best_cost = cost;
-            }
-        }
-        return int32_t(best);
-    }
-    // Enough (row, split) items for the device, each at least 512 tokens long.
-    const int64_t units = std::max<int64_t>(1, int64_t(batch) * tokens * ((hq + 3) / 4));
-    const int64_t want = (int64_t(sm_count()) * 8 + units - 1) / units;
-    return int32_t(std::max<int64_t>(1, std::min<int64_t>({want, (L + 511) / 512, kMaxSplits})));
-}
+// How a call runs: the library's own plan (S = 0), or S chunks, and its workspace.
+struct Plan {
+    int32_t splits;
+    size_t bytes;
+};
 
-int64_t table_tokens(const pkv_cache_desc &c, int32_t max_blocks) {
-    return std::min<int64_t>(int64_t(max_blocks) * c.block_size, INT32_MAX);
+Plan plan_of(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
+             int32_t max_blocks, int32_t num_splits, int32_t flags) {
+    int32_t S = num_splits;
+    if (S == 0 && on_tensor_cores(c, batch, tokens, hq, flags)) {
+        const size_t bytes = int4_plan_workspace(c, batch, hq, tokens, max_blocks);
+        if (bytes) return {0, bytes};
+        S = 1;
+    }
+    if (S == 0) {
+        // Enough (row, split) items for the device, of sequences as long as their table
+        // rows 512 tokens each.
+        const int64_t units = std::max<int64_t>(1, int64_t(batch) * tokens * ((hq + 3) / 4));
+        const int64_t want = (int64_t(sm_count()) * 8 + units - 1) / units;
+        const int64_t most = (int64_t(max_blocks) * c.block_size + 511) / 512;
+        S = int32_t(std::max<int64_t>(1, std::min<int64_t>({want, most, 64})));
+    }
+    return {S, pkv_decode_workspace_size(batch * tokens, hq, c.head_dim_v, S)};
 }
 
 int run_split_kernel(const Int4DecodeArgs &a, int32_t flags) {
     return on_tensor_cores(a.cache, a.batch, a.q_tokens, a.num_q_heads, flags)
-               ? launch_decode_int4(a)
+               ? launch_decode_int4(a, nullptr)
                : launch_decode_int4_generic(a);
 }
 
@@ -121,19 +114,18 @@ int attend(const pkv_cache_desc *cache, const float *q, int32_t batch, int32_t t
     int st = validate(cache, q, batch, tokens, hq, k_pool, k_params, v_pool, v_params,
                       block_tables, max_blocks, seq_lens, num_splits, flags, out, lse);
     if (st != PKV_OK || batch == 0) return st;
-    const int32_t S = num_splits
-                          ? num_splits
-                          : auto_splits(*cache, batch, tokens, hq,
-                                        table_tokens(*cache, max_blocks), flags);
     const int32_t rows = batch * tokens;
-    const size_t need = pkv_decode_workspace_size(rows, hq, cache->head_dim_v, S);
-    if (S > 1 && (!workspace || workspace_bytes < need)) return PKV_ERR_WORKSPACE_TOO_SMALL;
-    if (S > 1 && !aligned16(workspace)) return PKV_ERR_ALIGNMENT;
+    const Plan plan = plan_of(*cache, batch, tokens, hq, max_blocks, num_splits, flags);
+    const int32_t S = plan.splits;
+    if (plan.bytes && (!workspace || workspace_bytes < plan.bytes))
+        return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (plan.bytes && !aligned16(workspace)) return PKV_ERR_ALIGNMENT;
     Int4DecodeArgs a =
         args_of(cache, q, batch, tokens, hq, k_pool, k_params, v_pool, v_params, block_tables,
                 max_blocks, seq_lens, scale, S, out, lse, flag_below, stream);
     a.status = status_word();
     if (!a.status) return PKV_ERR_CUDA;
+    if (S == 0) return launch_decode_int4(a, workspace);
     if (S == 1) return run_split_kernel(a, flags);
     const size_t parts = size_t(S) * rows * hq;
     char *ws = static_cast<char *>(workspace);
@@ -148,13 +140,16 @@ int attend(const pkv_cache_desc *cache, const float *q, int32_t batch, int32_t t
 
 }  // namespace
 
-extern "C" int32_t pkv_decode_auto_splits_int4(const pkv_cache_desc *cache, int32_t batch,
-                                               int32_t tokens_per_seq, int32_t num_q_heads,
-                                               int32_t max_seq_len, int32_t flags) {
-    if (validate_int4_cache(cache) != PKV_OK || batch <= 0 || tokens_per_seq <= 0 ||
-        num_q_heads <= 0)
-        return 1;
-    return auto_splits(*cache, batch, tokens_per_seq, num_q_heads, max_seq_len, flags);
+extern "C" size_t pkv_decode_workspace_size_int4(const pkv_cache_desc *cache, int32_t batch,
+                                                 int32_t tokens_per_seq, int32_t num_q_heads,
+                                                 int32_t max_blocks, int32_t num_splits,
+                                                 int32_t flags) {
+    if (validate_int4_cache(cache) != PKV_OK || batch <= 0 || tokens_per_seq < 1 ||
+        tokens_per_seq > kMaxQueryTokens || num_q_heads <= 0 || max_blocks < 0 ||
+        num_splits < 0 || num_splits > kMaxSplits || num_q_heads % cache->num_kv_heads != 0 ||
+        int64_t(batch) * tokens_per_seq > 65535)
+        return 0;
+    return plan_of(*cache, batch, tokens_per_seq, num_q_heads, max_blocks, num_splits, flags).bytes;
 }
 
 extern "C" int pkv_paged_decode_attn_int4(

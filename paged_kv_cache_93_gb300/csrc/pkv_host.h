@@ -213,13 +213,14 @@ struct Int4DecodeArgs {
     cudaStream_t stream;
 };
 int launch_decode_int4_generic(const Int4DecodeArgs &a);
-// The tensor-core form: its shapes, items per (sequence, KV head, split), and the CTAs
-// that run at once.
+// The tensor-core form and its shapes.  num_splits > 0: the partials of that many chunks, as
+// above; 0: the library's own plan, the whole result to out_part / lse_part, with a
+// workspace of int4_plan_workspace bytes (0: the shape has no plan).
 bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
                           int32_t q_tokens);
-int int4_row_tiles(const pkv_cache_desc &c, int32_t num_q_heads, int32_t q_tokens);
-int int4_resident_ctas();
-int launch_decode_int4(const Int4DecodeArgs &a);
+size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
+                           int32_t q_tokens, int32_t max_blocks);
+int launch_decode_int4(const Int4DecodeArgs &a, void *workspace);
 
 int launch_lse_merge(int32_t num_parts, const float *out_part, const float *lse_part,
                      int64_t rows, int32_t head_dim_v, float *out, float *lse,

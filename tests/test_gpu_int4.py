@@ -242,8 +242,7 @@ def test_partials_merge_to_the_whole(pkv, dk, bs):
 def test_repeats_exactly_and_reads_nothing_else(pkv):
     c = _int4.make(10, [3000, 17, 900], 32, 8, 128, 128, 16)
     args = (c.q[:, 0].contiguous().cuda(), *c.pools(), c.tables.cuda(), c.lens.cuda(), c.scale)
-    S = pkv.decode_auto_splits_int4(*args[1:5], 3, 32, args[5].shape[1] * 16)
-    need = pkv.decode_workspace_size(3, 32, 128, S)
+    need = pkv.decode_workspace_size_int4(*args[1:5], 3, 32, args[5].shape[1])
     first = pkv.paged_decode_attn_int4(*args)
     for fill in (0, 255):
         ws = torch.full((max(need, 1),), fill, dtype=torch.uint8, device="cuda")

@@ -56,7 +56,7 @@ def test_shapes(pkv, desc, status):
     d = pkv.CacheDesc(*desc)
     assert pkv.lib.pkv_rope_append_int4(ctypes.byref(d), P, P, P, P, P, 32, P, P, P, 1, None, P, 4,
                                         P, 2, 0, 1.0, 0, P, None) == status
-    assert pkv.lib.pkv_decode_auto_splits_int4(ctypes.byref(d), 2, 1, 32, 64, 0) == 1
+    assert pkv.lib.pkv_decode_workspace_size_int4(ctypes.byref(d), 2, 1, 32, 64, 3, 0) == 0
 
 
 def test_append_and_copy_refusals(pkv):
