@@ -335,17 +335,20 @@ def rope_append_e4m3(k_pool, v_pool, q, k_new, v_new, positions, slots, inv_freq
 def cache_desc_int4(k_pool, k_params, v_pool, v_params) -> CacheDesc:
     """Shape of a 4-bit cache: uint8 code pools [num_blocks, Hkv, block_size, D / 2]
     and bf16 params [num_blocks, Hkv, block_size, 2] (scale, offset)."""
-    for pool, params, name in ((k_pool, k_params, "k"), (v_pool, v_params, "v")):
-        if isinstance(pool, ValuesInKeys):
-            raise ValueError("values inside the keys need a bf16 cache")
-        _need(pool, name + "_pool", torch.uint8, 4)
-        _need(params, name + "_params", torch.bfloat16, 4)
-        if params.shape != (*pool.shape[:3], 2):
-            raise ValueError(f"{name}_params must be [num_blocks, Hkv, block_size, 2] of its pool")
+    if isinstance(v_pool, ValuesInKeys):
+        raise ValueError("values inside the keys need a bf16 cache")
+    _need(k_pool, "k_pool", torch.uint8, 4)
+    _need(k_params, "k_params", torch.bfloat16, 4)
+    _need(v_pool, "v_pool", torch.uint8, 4)
+    _need(v_params, "v_params", torch.bfloat16, 4)
     nb, hkv, bs, half_k = k_pool.shape
-    if tuple(v_pool.shape[:3]) != (nb, hkv, bs):
+    half_v = v_pool.shape[3]
+    if v_pool.shape != (nb, hkv, bs, half_v):
         raise ValueError("k_pool and v_pool disagree on [num_blocks, Hkv, block_size]")
-    return CacheDesc(nb, bs, hkv, 2 * half_k, 2 * v_pool.shape[3])
+    params = (nb, hkv, bs, 2)
+    if k_params.shape != params or v_params.shape != params:
+        raise ValueError("k_params and v_params must be [num_blocks, Hkv, block_size, 2]")
+    return CacheDesc(nb, bs, hkv, 2 * half_k, 2 * half_v)
 
 
 def kv_append_int4(k_pool, k_params, v_pool, v_params, k_new, v_new, slots, stream=None) -> None:
@@ -435,18 +438,22 @@ def extend_sequences(block_tables, seq_lens, new_lens, free_blocks, pool_state, 
         with torch.cuda.stream(stream):
             return extend_sequences(block_tables, seq_lens, new_lens, free_blocks, pool_state,
                                     block_size, num_tokens, cu_q_lens, positions, slots)
-    dev = seq_lens.device
     if cu_q_lens is None:
-        cu_q_lens = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        cu_q_lens = seq_lens.new_empty(B + 1)
+    else:
+        _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
+        if cu_q_lens.numel() != B + 1:
+            raise ValueError("cu_q_lens must have one entry more than seq_lens")
     if positions is None:
-        positions = torch.empty(T, dtype=torch.int64, device=dev)
+        positions = seq_lens.new_empty(T, dtype=torch.int64)
+    else:
+        _need(positions, "positions", torch.int64, 1)
     if slots is None:
-        slots = torch.empty(T, dtype=torch.int64, device=dev)
-    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
-    _need(positions, "positions", torch.int64, 1)
-    _need(slots, "slots", torch.int64, 1)
-    if cu_q_lens.numel() != B + 1 or positions.numel() != T or slots.numel() != T:
-        raise ValueError("cu_q_lens must have B + 1, positions and slots num_tokens entries")
+        slots = torch.empty_like(positions)
+    else:
+        _need(slots, "slots", torch.int64, 1)
+    if positions.numel() != T or slots.numel() != T:
+        raise ValueError("positions and slots must have num_tokens entries")
     _check("pkv_extend_sequences", lib.pkv_extend_sequences(
         _int32(block_size), free_blocks.numel(), _ptr(block_tables), _ptr(seq_lens),
         _ptr(new_lens), B, block_tables.shape[1], _ptr(free_blocks), _ptr(pool_state), T,
@@ -672,39 +679,44 @@ def decode_workspace_size_int4(k_pool, k_params, v_pool, v_params, batch: int, n
                                                   int(flags)))
 
 
-def _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
+def _attn_int4(name, call, q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
                num_splits, workspace, out, lse, flags, stream, multi):
     desc, B, T, Hq = _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
                                 multi)
-    shape = (*q.shape[:-1], desc.head_dim_v)
+    ref, mb, S, flags = ctypes.byref(desc), block_tables.shape[1], _int32(num_splits), int(flags)
+    need = lib.pkv_decode_workspace_size_int4(ref, B, T, Hq, mb, S, flags)
+    ws_bytes = 0
     if workspace is not None:
         _need(workspace, "workspace", workspace.dtype)
-    S = _int32(num_splits)
-    need = lib.pkv_decode_workspace_size_int4(ctypes.byref(desc), B, T, Hq,
-                                              block_tables.shape[1], S, int(flags))
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_bytes = workspace.numel() * workspace.element_size()
     if stream is not None and (out is None or lse is None or ws_bytes < need):
         # what is allocated here is used on that stream: let it belong to it
         with torch.cuda.stream(stream):
-            return _attn_int4(name, q, k_pool, k_params, v_pool, v_params, block_tables,
+            return _attn_int4(name, call, q, k_pool, k_params, v_pool, v_params, block_tables,
                               seq_lens, scale, num_splits, workspace, out, lse, flags, None,
                               multi)
+    rows = q.shape[:-1]
+    shape = (*rows, desc.head_dim_v)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        out = q.new_empty(shape)
+    else:
+        _need(out, "out", torch.float32)
+        if out.shape != shape:
+            raise ValueError("out must have q's rows, and the cache's value dim")
     if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.float32, len(shape))
-    _need(lse, "lse", torch.float32, len(shape) - 1)
-    if out.shape != shape or lse.shape != shape[:-1]:
-        raise ValueError("out and lse must have q's rows (and the cache's value dim)")
+        lse = q.new_empty(rows)
+    else:
+        _need(lse, "lse", torch.float32)
+        if lse.shape != rows:
+            raise ValueError("lse must have one entry per row of q")
     if ws_bytes < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty((need + 3) // 4)
         ws_bytes = need
-    rows = (B, T) if multi else (B,)
-    _check(name, getattr(lib, name)(
-        ctypes.byref(desc), _ptr(q), *rows, Hq, _ptr(k_pool), _ptr(k_params), _ptr(v_pool),
-        _ptr(v_params), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), float(scale),
-        S, _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse), int(flags), _stream(stream)))
+    seqs = (B, T, Hq) if multi else (B, Hq)
+    _check(name, call(
+        ref, q.data_ptr(), *seqs, k_pool.data_ptr(), k_params.data_ptr(), v_pool.data_ptr(),
+        v_params.data_ptr(), block_tables.data_ptr(), mb, seq_lens.data_ptr(), scale, S,
+        _ptr(workspace), ws_bytes, out.data_ptr(), lse.data_ptr(), flags, _stream(stream)))
     return out, lse
 
 
@@ -713,7 +725,7 @@ def paged_decode_attn_int4(q, k_pool, k_params, v_pool, v_params, block_tables, 
                            lse=None, flags: int = 0, stream=None):
     """Decode attention of q [B, Hq, Dk] over a 4-bit cache -> (out, lse); num_splits 0
     lets the library choose."""
-    return _attn_int4("pkv_paged_decode_attn_int4", q, k_pool, k_params, v_pool, v_params,
+    return _attn_int4("pkv_paged_decode_attn_int4", lib.pkv_paged_decode_attn_int4, q, k_pool, k_params, v_pool, v_params,
                       block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
                       stream, False)
 
@@ -723,7 +735,7 @@ def paged_decode_attn_multi_int4(q, k_pool, k_params, v_pool, v_params, block_ta
                                  lse=None, flags: int = 0, stream=None):
     """The multi-token step (q [B, T, Hq, Dk], causal over the last T tokens) over a
     4-bit cache -> (out [B, T, Hq, Dv], lse [B, T, Hq])."""
-    return _attn_int4("pkv_paged_decode_attn_multi_int4", q, k_pool, k_params, v_pool, v_params,
+    return _attn_int4("pkv_paged_decode_attn_multi_int4", lib.pkv_paged_decode_attn_multi_int4, q, k_pool, k_params, v_pool, v_params,
                       block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
                       stream, True)
 

@@ -978,17 +978,24 @@ int launch(const Int4DecodeArgs &a, void *workspace) {
     static_assert(C::kCtas == kResident, "the plan's CTAs are those that run at once");
     const int tiles = row_tiles(a.cache, a.num_q_heads, a.q_tokens);
     const int shift = shift_of(a.cache.block_size);
+    // once a device and thread: room for the rings
+    static thread_local int configured = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && configured != dev) {
+        e = cudaFuncSetAttribute(decode_int4_kernel<D, ROWS>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(decode_int4_planned_kernel<D, ROWS>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e == cudaSuccess) configured = dev;
+    }
+    if (e != cudaSuccess) return cuda_status(e);
     if (a.num_splits > 0) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            decode_int4_kernel<D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return cuda_status(e);
         const int64_t items = int64_t(a.batch) * a.cache.num_kv_heads * tiles * a.num_splits;
         return launch_pdl(decode_int4_kernel<D, ROWS>, dim3(unsigned(items)), dim3(kThreads),
                           C::kSmem, a.stream, a, tiles, shift);
     }
-    const cudaError_t e = cudaFuncSetAttribute(decode_int4_planned_kernel<D, ROWS>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return cuda_status(e);
     const int ctas = sm_count() * kResident, units = a.batch * a.cache.num_kv_heads * tiles;
     float *parts = static_cast<float *>(workspace);
     float *part_lse = parts + size_t(2) * ctas * ROWS * D;

@@ -9,11 +9,12 @@
 // the last sequence's last block first.
 //
 // Bound: latency.  A step of 1,000 sequences and 40,000 tokens writes 0.8 MB; what
-// counts is one launch and no round trip.  Every CTA therefore takes the prefix sums
-// of the whole batch by itself (into its shared memory) and then fills its share of the
-// rows, finding a row's sequence by bisection.  What all CTAs read -- the lengths and
-// the stack's height -- is rewritten by the last CTA to finish, which a counter beside
-// the height tells; it wraps back to zero by itself.
+// counts is one launch and few round trips.  Each CTA takes the prefix sums of the whole
+// batch by itself, in its shared memory, and then fills its share of the rows, finding a
+// row's sequence by bisection.  Up to kRowsAlone rows one CTA does it all (and every trim,
+// whose few blocks are copied eight a thread at a time).  With more, what all CTAs read
+// -- the lengths and the stack's height -- is rewritten by the last CTA to finish, which a
+// counter beside the height tells; it wraps back to zero by itself.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -25,8 +26,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kMaxBatch = 8192;             // prefix sums of 64 KB
+constexpr int kThreads = 1024;
+constexpr int kMaxBatch = 8192;             // prefix sums and lengths of 96 KB
+constexpr int kRowsAlone = 4 * kThreads;
 
 struct TablesArgs {
     int32_t *tables, *lens;
@@ -43,39 +45,35 @@ struct Two {
     int64_t a, b;
 };
 
-// Exclusive prefix sums over the CTA of each thread's pair, and the totals.
-__device__ Two cta_scan(Two v, Two &total) {
-    __shared__ int64_t sums[2][kThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t a = v.a, b = v.b;
+// Inclusive prefix sums over the warp.
+__device__ __forceinline__ Two warp_scan(Two v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, a, o);
-        const int64_t y = __shfl_up_sync(0xffffffffu, b, o);
+        const int64_t x = __shfl_up_sync(0xffffffffu, v.a, o);
+        const int64_t y = __shfl_up_sync(0xffffffffu, v.b, o);
         if (lane >= o) {
-            a += x;
-            b += y;
+            v.a += x;
+            v.b += y;
         }
     }
-    if (lane == 31) {
-        sums[0][warp] = a;
-        sums[1][warp] = b;
-    }
+    return v;
+}
+
+// Exclusive prefix sums over the CTA of each thread's pair, and the totals.
+__device__ Two cta_scan(Two v, Two &total) {
+    static_assert(kThreads == 32 * 32, "a warp scans the warps' sums");
+    __shared__ Two sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Two upto = warp_scan(v);
+    if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    Two before = {0, 0};
-    total = {0, 0};
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const int64_t x = sums[0][w], y = sums[1][w];
-        if (w < warp) {
-            before.a += x;
-            before.b += y;
-        }
-        total.a += x;
-        total.b += y;
-    }
+    if (warp == 0) sums[lane] = warp_scan(sums[lane]);
+    __syncthreads();
+    const Two before = warp ? sums[warp - 1] : Two{0, 0};
+    total = sums[31];
     __syncthreads();               // `sums` is free for the next call
-    return {before.a + a - v.a, before.b + b - v.b};
+    return {before.a + upto.a - v.a, before.b + upto.b - v.b};
 }
 
 // The last entry of the rising list first[0 .. n] that is <= x (first[0] <= x < first[n]).
@@ -110,91 +108,83 @@ __device__ __forceinline__ int32_t ceil_div(int32_t x, int32_t n) {
     return int32_t((uint32_t(x) + uint32_t(n) - 1) / uint32_t(n));
 }
 
+// The lengths and changes into L2 while the kernel before this one ends.
+__device__ __forceinline__ void prefetch_lengths(const TablesArgs &a) {
+    const int64_t at = threadIdx.x * 128, bytes = int64_t(a.batch) * 4;
+    if (blockIdx.x == 0 && at < bytes) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.lens) + at));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.change) + at));
+    }
+}
+
+__device__ __forceinline__ int32_t stack_height(const TablesArgs &a) {
+    const int32_t count = a.state[0];
+    if (count >= 0 && count <= a.num_blocks) return count;
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, PKV_DEV_BLOCK_ID);
+    return 0;
+}
+
 __global__ void __launch_bounds__(kThreads) extend_kernel(const TablesArgs a) {
     extern __shared__ int32_t smem[];
-    int32_t *cu = smem, *taken = smem + a.batch + 1;      // [batch + 1] each
+    // [batch + 1] each; first what each sequence brings, then the sums
+    int32_t *cu = smem, *taken = smem + a.batch + 1, *lens = taken + a.batch + 1;
+    prefetch_lengths(a);
     pdl_wait();
     pdl_launch_dependents();
     const bool tells = blockIdx.x == 0;                   // raises the batch's flags
-    int32_t count = a.state[0];
-    if (count < 0 || count > a.num_blocks) {
-        if (tells && threadIdx.x == 0) raise_status(a.status, PKV_DEV_BLOCK_ID);
-        count = 0;
-    }
+    const int32_t count = stack_height(a);
     const int64_t most = min(int64_t(a.max_blocks) * a.block_size, int64_t(INT32_MAX));
     const int per = (a.batch + kThreads - 1) / kThreads;
     const int b0 = min(int(threadIdx.x) * per, a.batch), b1 = min(b0 + per, a.batch);
-    // what sequence b asks for: tokens and blocks (none where its lengths are not valid)
-    auto asked = [&](int b, bool flag) -> Two {
+    // tokens and blocks that each sequence asks for (none where its lengths are not valid)
+    Two mine = {0, 0}, total;
+    for (int b = b0; b < b1; ++b) {
         const int32_t len = a.lens[b], n = a.change[b];
         uint32_t bad = 0;
         if (len < 0 || len > most || n < 0) bad = PKV_DEV_SEQ_LEN;
         else if (n > most - len) bad = PKV_DEV_TABLE_RANGE;
-        if (bad) {
-            if (flag) raise_status(a.status, bad);
-            return {0, 0};
-        }
-        return {n, ceil_div(len + n, a.block_size) - ceil_div(len, a.block_size)};
-    };
-    Two mine = {0, 0}, total;
-    for (int b = b0; b < b1; ++b) {
-        const Two x = asked(b, tells);
-        mine.a += x.a;
-        mine.b += x.b;
+        if (bad && tells) raise_status(a.status, bad);
+        lens[b] = len;
+        cu[b] = bad ? 0 : n;
+        taken[b] = bad ? 0 : ceil_div(len + n, a.block_size) - ceil_div(len, a.block_size);
+        mine.a += cu[b];
+        mine.b += taken[b];
     }
     Two at = cta_scan(mine, total);
-    if (total.a <= a.rows && total.b <= count) {
-        for (int b = b0; b < b1; ++b) {
-            cu[b] = int32_t(at.a);
-            taken[b] = int32_t(at.b);
-            const Two x = asked(b, false);
-            at.a += x.a;
-            at.b += x.b;
-        }
-    } else {
+    if (total.a > a.rows || total.b > count) {
         // Not everything fits.  In order: a sequence whose tokens end past the rows
         // brings none; of the others, one whose blocks end past the free ones.  What is
         // refused keeps its place in the sums, so that nothing later overtakes it.
-        const Two begin = at;
-        int64_t rows_to = begin.a;
         Two again = {0, 0};
         for (int b = b0; b < b1; ++b) {
-            const Two x = asked(b, false);
-            rows_to += x.a;
-            if (x.a > 0 && rows_to > a.rows) {
+            const int32_t n = cu[b];
+            at.a += n;
+            if (n > 0 && at.a > a.rows) {
                 if (tells) raise_status(a.status, PKV_DEV_QUERY_RANGE);
-            } else {
-                again.b += x.b;
+                cu[b] = taken[b] = 0;
             }
+            again.b += taken[b];
         }
-        Two blocks_at = cta_scan(again, total);
+        at = cta_scan(again, total);
         Two granted = {0, 0};
-        // cu / taken first hold each sequence's own counts
-        rows_to = begin.a;
         for (int b = b0; b < b1; ++b) {
-            const Two x = asked(b, false);
-            rows_to += x.a;
-            bool ok = !(x.a > 0 && rows_to > a.rows);
-            if (ok) {
-                blocks_at.b += x.b;
-                if (x.b > 0 && blocks_at.b > count) {
-                    ok = false;
-                    if (tells) raise_status(a.status, PKV_DEV_NO_BLOCKS);
-                }
+            const int32_t k = taken[b];
+            at.b += k;
+            if (k > 0 && at.b > count) {
+                if (tells) raise_status(a.status, PKV_DEV_NO_BLOCKS);
+                cu[b] = taken[b] = 0;
             }
-            cu[b] = ok ? int32_t(x.a) : 0;
-            taken[b] = ok ? int32_t(x.b) : 0;
             granted.a += cu[b];
             granted.b += taken[b];
         }
         at = cta_scan(granted, total);
-        for (int b = b0; b < b1; ++b) {
-            const int32_t n = cu[b], k = taken[b];
-            cu[b] = int32_t(at.a);
-            taken[b] = int32_t(at.b);
-            at.a += n;
-            at.b += k;
-        }
+    }
+    for (int b = b0; b < b1; ++b) {
+        const int32_t n = cu[b], k = taken[b];
+        cu[b] = int32_t(at.a);
+        taken[b] = int32_t(at.b);
+        at.a += n;
+        at.b += k;
     }
     if (threadIdx.x == 0) {
         cu[a.batch] = int32_t(total.a);
@@ -214,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TablesArgs a) {
             const int64_t r = r0 + i;
             if (r >= live) break;
             while (r >= cu[b + 1]) ++b;
-            const int32_t len = a.lens[b], p = len + int32_t(r) - cu[b];
+            const int32_t len = lens[b], p = len + int32_t(r) - cu[b];
             const int32_t lb = p / a.block_size, held = ceil_div(len, a.block_size);
             const int32_t phys = lb < held ? a.tables[int64_t(b) * a.max_blocks + lb]
                                            : stack[-int64_t(taken[b] + lb - held)];
@@ -233,67 +223,70 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TablesArgs a) {
     // ---- the tables' new entries
     for (int64_t k = thread; k < taken[a.batch]; k += threads) {
         const int b = owner(taken, a.batch, int32_t(k));
-        const int32_t held = ceil_div(a.lens[b], a.block_size);
+        const int32_t held = ceil_div(lens[b], a.block_size);
         a.tables[int64_t(b) * a.max_blocks + held + (k - taken[b])] = stack[-k];
     }
     for (int64_t b = thread; b <= a.batch; b += threads) a.cu[b] = cu[b];
     if (!last_cta(a.state)) return;
     for (int b = threadIdx.x; b < a.batch; b += kThreads) {
         const int32_t n = cu[b + 1] - cu[b];
-        if (n) a.lens[b] += n;
+        if (n) a.lens[b] = lens[b] + n;
     }
     if (threadIdx.x == 0) a.state[0] = count - taken[a.batch];
 }
 
+// One CTA.
 __global__ void __launch_bounds__(kThreads) trim_kernel(const TablesArgs a) {
     extern __shared__ int32_t smem[];
-    int32_t *gone = smem;                                  // [batch + 1]
+    // [batch + 1] each: blocks given back, then their sums; the blocks that are kept
+    int32_t *gone = smem, *left = smem + a.batch + 1;
+    prefetch_lengths(a);
     pdl_wait();
     pdl_launch_dependents();
-    const bool tells = blockIdx.x == 0;
-    int32_t count = a.state[0];
-    if (count < 0 || count > a.num_blocks) {
-        if (tells && threadIdx.x == 0) raise_status(a.status, PKV_DEV_BLOCK_ID);
-        count = 0;
-    }
+    const int32_t count = stack_height(a);
     const int64_t most = min(int64_t(a.max_blocks) * a.block_size, int64_t(INT32_MAX));
     const int per = (a.batch + kThreads - 1) / kThreads;
     const int b0 = min(int(threadIdx.x) * per, a.batch), b1 = min(b0 + per, a.batch);
-    // whether sequence b gets shorter
-    auto cut = [&](int b, bool flag) {
-        const int32_t len = a.lens[b], keep = a.change[b];
-        if (keep < 0) return false;
-        if (len < 0 || len > most || keep > len) {
-            if (flag) raise_status(a.status, PKV_DEV_SEQ_LEN);
-            return false;
-        }
-        return keep < len;
-    };
-    auto blocks = [&](int b) {
-        return ceil_div(a.lens[b], a.block_size) - ceil_div(a.change[b], a.block_size);
-    };
     Two mine = {0, 0}, total;
-    for (int b = b0; b < b1; ++b)
-        if (cut(b, tells)) mine.a += blocks(b);
+    for (int b = b0; b < b1; ++b) {
+        const int32_t len = a.lens[b], keep = a.change[b];
+        gone[b] = 0;
+        if (keep < 0) continue;
+        if (len < 0 || len > most || keep > len) {
+            raise_status(a.status, PKV_DEV_SEQ_LEN);
+            continue;
+        }
+        left[b] = ceil_div(keep, a.block_size);
+        gone[b] = ceil_div(len, a.block_size) - left[b];
+        mine.a += gone[b];
+        if (keep < len) a.lens[b] = keep;
+    }
     Two at = cta_scan(mine, total);
     for (int b = b0; b < b1; ++b) {
+        const int32_t k = gone[b];
         gone[b] = int32_t(at.a);
-        if (cut(b, false)) at.a += blocks(b);
+        at.a += k;
     }
     if (threadIdx.x == 0) gone[a.batch] = int32_t(total.a);
     __syncthreads();
-    const int64_t thread = blockIdx.x * int64_t(kThreads) + threadIdx.x;
-    const int64_t threads = int64_t(gridDim.x) * kThreads;
     const int64_t top = count + total.a;
-    for (int64_t k = thread; k < total.a; k += threads) {
-        const int b = owner(gone, a.batch, int32_t(k));
-        const int32_t left = ceil_div(a.change[b], a.block_size);
-        const int32_t phys = a.tables[int64_t(b) * a.max_blocks + left + (k - gone[b])];
-        if (top - 1 - k < a.num_blocks) a.free_blocks[top - 1 - k] = phys;
+    constexpr int kAhead = 8;
+    for (int64_t k0 = threadIdx.x; k0 < total.a; k0 += kThreads * kAhead) {
+        int32_t phys[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t k = k0 + u * kThreads;
+            if (k < total.a) {
+                const int b = owner(gone, a.batch, int32_t(k));
+                phys[u] = a.tables[int64_t(b) * a.max_blocks + left[b] + (k - gone[b])];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t to = top - 1 - (k0 + u * kThreads);
+            if (k0 + u * kThreads < total.a && to < a.num_blocks) a.free_blocks[to] = phys[u];
+        }
     }
-    if (!last_cta(a.state)) return;
-    for (int b = threadIdx.x; b < a.batch; b += kThreads)
-        if (cut(b, false)) a.lens[b] = a.change[b];
     if (threadIdx.x == 0) {
         if (top > a.num_blocks) raise_status(a.status, PKV_DEV_BLOCK_ID);
         a.state[0] = int32_t(min(top, int64_t(a.num_blocks)));
@@ -307,14 +300,21 @@ int check(int32_t block_size, int32_t num_blocks, int32_t batch, int32_t max_blo
     return PKV_OK;
 }
 
-int launch(void (*kernel)(TablesArgs), const TablesArgs &a, int64_t threads, size_t smem,
-           pkv_stream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(2 * (kMaxBatch + 1) * 4));
+int launch(void (*kernel)(TablesArgs), const TablesArgs &a, int64_t ctas, pkv_stream_t stream) {
+    // once a device and thread: room for the longest prefix sums
+    static thread_local int configured = -1;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && configured != dev) {
+        for (auto k : {extend_kernel, trim_kernel})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         int(3 * (kMaxBatch + 1) * 4));
+        if (e == cudaSuccess) configured = dev;
+    }
     if (e != cudaSuccess) return cuda_status(e);
-    const int64_t ctas = (threads + kThreads - 1) / kThreads;
-    return launch_pdl(kernel, dim3(unsigned(std::max<int64_t>(1, std::min<int64_t>(ctas, sm_count())))),
-                      dim3(kThreads), smem, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_pdl(kernel, dim3(unsigned(std::min<int64_t>(ctas, sm_count()))), dim3(kThreads),
+                      3 * size_t(a.batch + 1) * 4, reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 }  // namespace
@@ -351,7 +351,10 @@ extern "C" int pkv_extend_sequences(int32_t block_size, int32_t num_blocks, int3
     a.block_size = block_size;
     a.num_blocks = num_blocks;
     a.rows = num_tokens;
-    return launch(extend_kernel, a, (int64_t(num_tokens) + 1) / 2, 2 * size_t(batch + 1) * 4, stream);
+    // (two rows a thread)
+    const int64_t ctas =
+        num_tokens <= kRowsAlone ? 1 : (int64_t(num_tokens) + 2 * kThreads - 1) / (2 * kThreads);
+    return launch(extend_kernel, a, ctas, stream);
 }
 
 extern "C" int pkv_trim_sequences(int32_t block_size, int32_t num_blocks,
@@ -375,7 +378,5 @@ extern "C" int pkv_trim_sequences(int32_t block_size, int32_t num_blocks,
     a.max_blocks = max_blocks;
     a.block_size = block_size;
     a.num_blocks = num_blocks;
-    // a long sequence's blocks are shared among up to 16 CTAs
-    const int64_t most = std::min<int64_t>(int64_t(batch) * max_blocks / 16, 16 * kThreads);
-    return launch(trim_kernel, a, most, size_t(batch + 1) * 4, stream);
+    return launch(trim_kernel, a, 1, stream);
 }
