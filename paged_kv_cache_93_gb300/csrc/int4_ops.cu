@@ -3,7 +3,10 @@
 // Append.  A row's scale needs the whole row before the first code, so a row stays in
 // the registers of the lanes that loaded it: a lane holds units of 16 elements (two
 // 16-byte vectors in, 8 bytes of codes out), a row's lanes find its extent by shuffles,
-// and nothing is read twice.  Bound: memory, 2 D bytes in and D / 2 + 4 out a row.
+// and nothing is read twice.  A CTA takes one head's rows of neighbouring tokens, whose
+// places in a block are neighbours too, so that codes and parameters are written in whole
+// sectors.  Bound: memory, 2 D bytes in and D / 2 + 4 out a row, with about 7
+// instructions an element close behind.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,6 +29,7 @@ struct AppendArgs {
     uint32_t *status;
     int64_t num_tokens, num_slots;
     int32_t hkv, block_size, dk, dv;
+    int32_t heads;                       // that a CTA takes in turn
 };
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
@@ -36,70 +40,87 @@ __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
 }
 
 // LANES neighbouring lanes a row, UNITS units of 16 elements a lane: unit u of the row
-// is the (u / LANES)-th of lane u mod LANES.
+// is the (u / LANES)-th of lane u mod LANES.  A lane's place in a row and its token's slot
+// serve `heads` heads in turn, the next one's row on its way while one is stored.
 template <int LANES, int UNITS>
 __global__ void __launch_bounds__(kThreads) append_int4_kernel(const AppendArgs a) {
+    constexpr int kRows = kThreads / LANES;              // tokens of a CTA's item
+    const int c = threadIdx.x & (LANES - 1);
     pdl_wait();
     pdl_launch_dependents();
-    constexpr int kRows = kThreads / LANES;
-    const int c = threadIdx.x & (LANES - 1);
-    const int64_t rows = a.num_tokens * a.hkv;
-    // K rows first, then V rows; a whole warp leaves together (its shuffles need all)
-    const int64_t all = 2 * rows, steps = (all + kRows - 1) / kRows;
-    for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
-        int64_t r = step * kRows + threadIdx.x / LANES;
-        const bool is_k = r < rows;
-        const bool in = r < all;
-        if (!is_k) r -= rows;
-        const int d = is_k ? a.dk : a.dv;
-        int64_t t = 0, slot = -1;
-        if (in) {
-            t = r / a.hkv;
-            slot = a.slots[t];
-            if (slot >= a.num_slots) {
-                if (c == 0 && is_k && r == t * a.hkv) raise_status(a.status, PKV_DEV_SLOT);
-                slot = -1;
+    const bool is_k = blockIdx.z == 0;
+    const int d = is_k ? a.dk : a.dv;
+    // grid.x: tokens, grid.y: heads, in strides; a whole warp goes through together (its
+    // shuffles need all lanes)
+    const int64_t tiles = (a.num_tokens + kRows - 1) / kRows;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t t = tile * kRows + threadIdx.x / LANES;
+        const bool in = t < a.num_tokens;
+        const int64_t slot = in ? a.slots[t] : -1;
+        const uint16_t *token = (is_k ? a.k_new : a.v_new) + (in ? t : 0) * a.hkv * d + c * 16;
+        for (int h0 = blockIdx.y * a.heads; h0 < a.hkv; h0 += gridDim.y * a.heads) {
+            const int h1 = min(h0 + a.heads, a.hkv);
+            uint4 raw[UNITS][2];
+            auto load = [&](int h) {
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) {
+                    raw[u][0] = raw[u][1] = make_uint4(0, 0, 0, 0);
+                    if (in && (c + u * LANES) * 16 < d) {
+                        const uint4 *src =
+                            reinterpret_cast<const uint4 *>(token + h * d + u * LANES * 16);
+                        raw[u][0] = src[0];
+                        raw[u][1] = src[1];
+                    }
+                }
+            };
+            load(h0);
+            const bool stored = slot >= 0 && slot < a.num_slots;
+            if (slot >= a.num_slots && c == 0 && is_k && h0 == 0) raise_status(a.status, PKV_DEV_SLOT);
+            // the row of head 0 (rows are numbered within 64 bits, blocks within 32)
+            const uint32_t block = !stored                       ? 0
+                                   : a.num_slots <= UINT32_MAX ? uint32_t(slot) / uint32_t(a.block_size)
+                                                               : uint32_t(slot / a.block_size);
+            const int64_t row0 = int64_t(block) * a.hkv * a.block_size +
+                                 (stored ? slot - int64_t(block) * a.block_size : 0);
+            uint8_t *pool = (is_k ? a.k_pool : a.v_pool) + row0 * (d / 2) + c * 8;
+            uint32_t *params = (is_k ? a.k_params : a.v_params) + row0;
+            for (int h = h0; h < h1; ++h) {
+                // two elements at a time
+                uint32_t low2 = 0x7f807f80u, high2 = 0xff80ff80u;        // +inf, -inf
+                uint4 now[UNITS][2];
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u) {
+                    const uint4 x = now[u][0] = raw[u][0], y = now[u][1] = raw[u][1];
+                    if ((c + u * LANES) * 16 < d) {
+                        low2 = min_nan_bf16x2(low2, min_nan_bf16x2(min_nan_bf16x2(x.x, x.y),
+                                                                   min_nan_bf16x2(x.z, x.w)));
+                        low2 = min_nan_bf16x2(low2, min_nan_bf16x2(min_nan_bf16x2(y.x, y.y),
+                                                                   min_nan_bf16x2(y.z, y.w)));
+                        high2 = max_nan_bf16x2(high2, max_nan_bf16x2(max_nan_bf16x2(x.x, x.y),
+                                                                     max_nan_bf16x2(x.z, x.w)));
+                        high2 = max_nan_bf16x2(high2, max_nan_bf16x2(max_nan_bf16x2(y.x, y.y),
+                                                                     max_nan_bf16x2(y.z, y.w)));
+                    }
+                }
+                if (h + 1 < h1) load(h + 1);
+                const Int4Scale sc = int4_row_scale(
+                    min_nan(bf16_lo_to_f32(low2), bf16_hi_to_f32(low2)),
+                    max_nan(bf16_lo_to_f32(high2), bf16_hi_to_f32(high2)), LANES, 0xffffffffu);
+                if (!stored) continue;
+                const int64_t step = int64_t(h) * a.block_size;
+#pragma unroll
+                for (int u = 0; u < UNITS; ++u)
+                    if ((c + u * LANES) * 16 < d) {
+                        float x[8];
+                        unpack8(now[u][0], x);
+                        const uint32_t w0 = int4_codes8(x, sc);
+                        unpack8(now[u][1], x);
+                        *reinterpret_cast<uint2 *>(pool + step * (d / 2) + u * LANES * 8) =
+                            make_uint2(w0, int4_codes8(x, sc));
+                    }
+                if (c == 0) params[step] = sc.params;
             }
         }
-        uint4 raw[UNITS][2];
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-            const int e = (c + u * LANES) * 16;
-            if (slot >= 0 && e < d) {
-                const uint4 *src =
-                    reinterpret_cast<const uint4 *>((is_k ? a.k_new : a.v_new) + r * d + e);
-                raw[u][0] = src[0];
-                raw[u][1] = src[1];
-            }
-        }
-        float low = INFINITY, high = -INFINITY, odd = 0.f;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-            if (slot >= 0 && (c + u * LANES) * 16 < d) {
-                float x[8];
-                unpack8(raw[u][0], x);
-                int4_extent8(x, low, high, odd);
-                unpack8(raw[u][1], x);
-                int4_extent8(x, low, high, odd);
-            }
-        const Int4Scale sc = int4_row_scale(low, high, odd, LANES, 0xffffffffu);
-        if (slot < 0) continue;
-        const int64_t block = slot / a.block_size;
-        const int64_t row =
-            (block * a.hkv + (r - t * a.hkv)) * a.block_size + (slot - block * a.block_size);
-        uint8_t *pool = (is_k ? a.k_pool : a.v_pool) + row * (d / 2);
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-            const int e = (c + u * LANES) * 16;
-            if (e < d) {
-                float x[8];
-                unpack8(raw[u][0], x);
-                const uint32_t w0 = int4_codes8(x, sc);
-                unpack8(raw[u][1], x);
-                *reinterpret_cast<uint2 *>(pool + e / 2) = make_uint2(w0, int4_codes8(x, sc));
-            }
-        }
-        if (c == 0) (is_k ? a.k_params : a.v_params)[row] = sc.params;
     }
 }
 
@@ -203,8 +224,12 @@ extern "C" int pkv_kv_append_int4(const pkv_cache_desc *cache, void *k_pool, voi
                   : units <= 32 ? append_int4_kernel<32, 1>
                                 : append_int4_kernel<32, 2>;
     const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
-    const int64_t steps = (2 * num_tokens * a.hkv + kThreads / lanes - 1) / (kThreads / lanes);
-    const dim3 grid(unsigned(std::min<int64_t>(steps, int64_t(sm_count()) * 8)));
+    const int rows = kThreads / lanes;
+    const int64_t tiles = (num_tokens + rows - 1) / rows;
+    // four heads a CTA where that leaves enough CTAs (8,191 tokens of 8 heads: 11.3 us, one head a CTA 13.6)
+    a.heads = tiles * 2 * a.hkv >= int64_t(sm_count()) * 16 ? std::min(4, a.hkv) : 1;
+    const dim3 grid(unsigned(std::min<int64_t>(tiles, 1 << 20)),
+                    unsigned(std::min((a.hkv + a.heads - 1) / a.heads, 65535)), 2);
     return launch_pdl(kernel, grid, dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a);
 }
 

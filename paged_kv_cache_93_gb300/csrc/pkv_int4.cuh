@@ -29,13 +29,35 @@ struct Int4Scale {
     uint32_t params;               // bf16 pair: scale in bits 0-15, offset in 16-31
 };
 
-// `low` and `high` of the row; a row that holds an infinite or NaN element comes with
-// low = -inf, high = +inf.
+// min and max that give NaN where an operand is NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float x;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float x;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t x;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(b));
+    return x;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t x;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(a), "r"(b));
+    return x;
+}
+
+// `low` and `high` of the row, NaN if an element is.
 __device__ __forceinline__ Int4Scale int4_scale(float low, float high) {
     Int4Scale r;
     const uint32_t o = f32_to_bf16_bits(low);
     r.offset = __uint_as_float(o << 16);
-    const float range = fmaxf(__fsub_rn(high, r.offset), 0.f);
+    float range = __fsub_rn(high, r.offset);
+    if (range < 0.f) range = 0.f;
     if (!(range <= kFloatMax)) {
         r.offset = r.inverse = 0.f;
         r.params = kInt4NanParams;
@@ -48,43 +70,61 @@ __device__ __forceinline__ Int4Scale int4_scale(float low, float high) {
     return r;
 }
 
-// Eight elements as codes, the first in the low bits.  Adding 2^23 rounds to the nearest
-// whole number (ties to even) and leaves it in the low bits of the sum.
-__device__ __forceinline__ uint32_t int4_codes8(const float (&x)[8], const Int4Scale &r) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 7; i >= 0; --i) {
-        const float v = __fmul_rn(__fsub_rn(x[i], r.offset), r.inverse);
-        // (a NaN element's row has NaN parameters; fmaxf makes its code 0)
-        const float c = __fadd_rn(fminf(fmaxf(v, 0.f), 15.f), 8388608.f);
-        w = (w << 4) | (__float_as_uint(c) & 15u);
-    }
-    return w;
+// Two binary32 operations at a time, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+    return x;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t x;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t x;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
 }
 
-// Takes eight elements into a row's running smallest and largest; `odd` becomes NaN when
-// one of them is infinite or NaN, and stays 0 otherwise.
-__device__ __forceinline__ void int4_extent8(const float (&x)[8], float &low, float &high,
-                                             float &odd) {
+// Eight elements as codes, the first in the low bits.  Adding 2^23 rounds to the nearest
+// whole number (ties to even) and leaves it in the low bits of the sum, whose other bits
+// are 0x4b000000; a word is made by multiplying by 16 and adding, and what those bits add
+// up to is taken off at the end.  (A code cannot pass 15: the scale is short of
+// range / 15 by 2^-9 of it at most.  In a row of NaN parameters max makes codes 0.)
+__device__ __forceinline__ uint32_t int4_codes8(const float (&x)[8], const Int4Scale &r) {
+    const uint64_t less = pair_of(-r.offset, -r.offset), by = pair_of(r.inverse, r.inverse);
+    const uint64_t magic = pair_of(8388608.f, 8388608.f);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 6; i >= 0; i -= 2) {
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;"
+            : "=f"(lo), "=f"(hi) : "l"(mul2(add2(pair_of(x[i], x[i + 1]), less), by)));
+        uint32_t a, b;
+        asm("mov.b64 {%0, %1}, %2;"
+            : "=r"(a), "=r"(b) : "l"(add2(pair_of(fmaxf(lo, 0.f), fmaxf(hi, 0.f)), magic)));
+        w = (w * 16u + b) * 16u + a;
+    }
+    return w - 0x4b000000u * 0x11111111u;
+}
+
+// Takes eight elements into a row's running smallest and largest.
+__device__ __forceinline__ void int4_extent8(const float (&x)[8], float &low, float &high) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        low = fminf(low, x[i]);
-        high = fmaxf(high, x[i]);
-        odd = fmaf(x[i], 0.f, odd);
+        low = min_nan(low, x[i]);
+        high = max_nan(high, x[i]);
     }
 }
 
 // The same over the `lanes` (a power of two) neighbouring lanes that hold a row's
 // elements; the lanes of `mask` call it together.
-__device__ __forceinline__ Int4Scale int4_row_scale(float low, float high, float odd,
-                                                    int lanes, uint32_t mask) {
-    if (odd != 0.f) {
-        low = -INFINITY;
-        high = INFINITY;
-    }
+__device__ __forceinline__ Int4Scale int4_row_scale(float low, float high, int lanes,
+                                                    uint32_t mask) {
     for (int o = lanes >> 1; o > 0; o >>= 1) {
-        low = fminf(low, __shfl_xor_sync(mask, low, o));
-        high = fmaxf(high, __shfl_xor_sync(mask, high, o));
+        low = min_nan(low, __shfl_xor_sync(mask, low, o));
+        high = max_nan(high, __shfl_xor_sync(mask, high, o));
     }
     return int4_scale(low, high);
 }

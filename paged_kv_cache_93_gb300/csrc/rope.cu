@@ -648,11 +648,11 @@ rope_append_warp_kernel(const RopeArgs a) {
                 store8_f32(a.q_out, dst + eb, y);
             } else if constexpr (FMT == kInt4) {
                 // the row's extent over its U lanes, which are all here
-                float low = INFINITY, high = -INFINITY, odd = 0.f;
-                int4_extent8(x, low, high, odd);
-                int4_extent8(y, low, high, odd);
+                float low = INFINITY, high = -INFINITY;
+                int4_extent8(x, low, high);
+                int4_extent8(y, low, high);
                 const uint32_t group = U == 32 ? 0xffffffffu : ((1u << U) - 1) << (lane & ~(U - 1));
-                const Int4Scale sc = int4_row_scale(low, high, odd, U, group);
+                const Int4Scale sc = int4_row_scale(low, high, U, group);
                 uint32_t *to = reinterpret_cast<uint32_t *>(
                     static_cast<uint8_t *>(is_k ? a.k_pool : a.v_pool) + dst / 2);
                 to[(is_k ? ea : 16 * c) / 8] = int4_codes8(x, sc);
@@ -777,11 +777,11 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
                 }
                 continue;
             }
-            float low = INFINITY, high = -INFINITY, odd = 0.f;
+            float low = INFINITY, high = -INFINITY;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-                if ((lane + 32 * n) * 8 < d) int4_extent8(x[n], low, high, odd);
-            const Int4Scale sc = int4_row_scale(low, high, odd, 32, 0xffffffffu);
+                if ((lane + 32 * n) * 8 < d) int4_extent8(x[n], low, high);
+            const Int4Scale sc = int4_row_scale(low, high, 32, 0xffffffffu);
             const int64_t to = row0 + int64_t(g) * a.block_size;
             uint32_t *codes = reinterpret_cast<uint32_t *>(
                 static_cast<uint8_t *>(is_k ? a.k_pool : a.v_pool) + to * (d / 2));
