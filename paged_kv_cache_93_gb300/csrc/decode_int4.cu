@@ -8,10 +8,13 @@
 //
 // Bound: memory.  A row of 128 elements is 68 bytes, so an SM at full bandwidth meets
 // 41 elements a clock and cannot afford an instruction for each.  Hence:
-//  - A code needs no conversion.  The bits 0..15 of a code, read as fp16, are the
-//    subnormal code * 2^-24, and shifted left by four code * 2^-20; tensor cores take
-//    subnormals exactly.  A 32-bit word of 8 codes becomes four fp16 pairs with one shift
-//    and four ANDs.  The factors 2^-24 and 16 go into the query and into the result.
+//  - A code needs no conversion.  Its bits 0..15 at bits 3-6 of an fp16 are the subnormal
+//    code * 2^-21, and at bits 7-10 code * 2^-17 (up to 2047 an fp16's bits count evenly);
+//    tensor cores take subnormals exactly.  A 32-bit word of 8 codes becomes four fp16
+//    pairs with two shifts and four ANDs.  The factors 2^-21 and 16 go into the query and
+//    into the result.  (At bits 0-3 and 4-7 it would be one shift.  But products are lined
+//    up by their operands' exponents, and what a subnormal has in leading zeros is lost
+//    below: scores off by 1e-5 instead of 1e-6.)
 //  - Rows come by cp.async into a ring that belongs to one warp: 16-byte pieces may be
 //    placed anywhere, no barrier couples the warps, and a warp's tiles are on their way
 //    while it computes.  (Warp-level MMAs, because tcgen05 would want the codes expanded
@@ -24,6 +27,13 @@
 //    g's word holds 8 elements, the n-th of which is row g of the n-th product.  Two
 //    tokens' words interleave with two byte permutes into the pairs that the product
 //    wants.
+//  - A code is a positive number, and products' sums are cut off, not rounded, below
+//    fp32's last place: thousands of tokens' values, which nearly cancel, would be lost
+//    in a sum of codes that grows and grows (200,000 tokens: 1e-3 of the output).  So
+//    half of the tokens enter the values' products as -p s' times 15 - code, which is an
+//    exclusive-or in the instruction that masks the codes anyway, and 15 p s' goes to the
+//    offsets' sum.  Which half: those whose place within 16 has an odd number of one
+//    bits, a pattern that no regular spacing of tokens falls in with.
 //  - Weights go from the scores' layout (token, row) to the values' (row, token) by
 //    movmatrix.
 // Query and weights are carried as two fp16 terms (22 bits): up to 4 rows as 8 columns
@@ -51,6 +61,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens of a warp's step
 constexpr int kResident = 3;              // CTAs of an SM
+// Codes' places in a pair of fp16, and 1 / the value of a code of 1 in the first of them.
+constexpr uint32_t kSmall = 0x00780078u, kLarge = 0x07800780u;
+constexpr float kUp = 2097152.f;          // 2^21
 
 // ROWS query rows of an item: 4 (as 8 columns of row and term), 8, or 16 (two tiles of 8).
 template <int D, int ROWS>
@@ -65,6 +78,12 @@ struct Config {
     static constexpr int kLaneRows = kPacked ? 1 : 2 * kCols;
     static constexpr int kCtas = kResident;
     static constexpr int kStages = D == 128 ? (ROWS == 16 ? 3 : 4) : 7;
+    // The scores' sums of the two terms apart, where registers allow: fewer cut-offs on the
+    // large one, and fewer products that wait for one another.
+    static constexpr int kChains = ROWS == 8 ? 2 : 1;
+    static constexpr __host__ __device__ int chain(int term, int step) {
+        return kChains == 1 ? 0 : kChains == 2 ? (kPacked ? step : term) : term ? 2 : step;
+    }
     // 16 rows: the query's fragments (the same for all the CTA's warps) in shared memory,
     // as the registers hold the sums
     static constexpr bool kSharedQuery = ROWS == 16;
@@ -114,6 +133,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with nothing added.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Transposes the 8 x 8 matrix of 16-bit elements that the warp holds (lane 4 i + k: row
 // i, columns 2 k and 2 k + 1).
@@ -323,7 +350,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             }
             // score = s (sum of products) * col_factor + o * col_sum, in base-2 units
             const float base = a.scale * kLog2e;
-            col_factor[n] = base * pow2(e - 12) * 16777216.f;
+            col_factor[n] = base * pow2(e - 12) * kUp;
             col_sum[n] = base * sum;
         }
         // to the lanes that hold the rows' scores: lane (g, t) has row t, or rows 2 t, 2 t + 1
@@ -365,6 +392,10 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[i][n][x] = 0.f;
     const int tok = token_at<D>(g);                // the lane's token of the first 8
+    // complemented tokens (rows 0-7 of a product; rows 8-15 are the other way round): the
+    // lane's own in the scores' layout, and those of its pair in the values'
+    const int odd_row = __popc(g) & 1;
+    const uint32_t flips = t == 0 || t == 3 ? kSmall & 0xffff0000u : kSmall & 0xffffu;
     const uint32_t my_k = D == 128 ? piece_at<D>(tok, t) : piece_at<D>(tok, 0) + 8 * t;
     auto word_at = [&](int row) {
         return kTile * C::kRowBytes +
@@ -372,7 +403,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     };
     const uint32_t my_v0 = word_at(token_at<D>(2 * t)), my_v1 = word_at(token_at<D>(2 * t + 1));
     // the sums over the codes of a tile's keys: scores of tokens tok + 8 k
-    float s[2][C::kCols][4];
+    float s[2][C::kCols][4], more[C::kChains - 1 + (C::kChains == 1)][2][C::kCols][4];
     auto dot_keys = [&](uint32_t stage) {
         uint32_t kw[4][C::kWordsK];
 #pragma unroll
@@ -382,7 +413,11 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
 #pragma unroll
             for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[h][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    s[h][n][e] = 0.f;
+#pragma unroll
+                    for (int z = 1; z < C::kChains; ++z) more[z - 1][h][n][e] = 0.f;
+                }
 #pragma unroll
         for (int w = 0; w < C::kWordsK; ++w) {
             uint32_t q[C::kCols][C::kTerms][4];
@@ -402,18 +437,29 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             for (int step = 0; step < 2; ++step)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = step ? kw[2 * h][w] >> 8 : kw[2 * h][w];
-                    const uint32_t v = step ? kw[2 * h + 1][w] >> 8 : kw[2 * h + 1][w];
-                    const uint32_t a0 = u & 0x000f000fu, a2 = u & 0x00f000f0u;
-                    const uint32_t a1 = v & 0x000f000fu, a3 = v & 0x00f000f0u;
+                    const uint32_t u = step ? kw[2 * h][w] >> 5 : kw[2 * h][w] << 3;
+                    const uint32_t v = step ? kw[2 * h + 1][w] >> 5 : kw[2 * h + 1][w] << 3;
+                    const uint32_t a0 = u & kSmall, a2 = u & kLarge;
+                    const uint32_t a1 = v & kSmall, a3 = v & kLarge;
 #pragma unroll
                     for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
                         for (int term = 0; term < C::kTerms; ++term)
-                            mma_f16(s[h][n], a0, a1, a2, a3, q[n][term][2 * step],
+                        {
+                            const int z = C::chain(term, step);
+                            mma_f16(z ? more[z - 1][h][n] : s[h][n], a0, a1, a2, a3, q[n][term][2 * step],
                                     q[n][term][2 * step + 1]);
+                        }
                 }
         }
+#pragma unroll
+        for (int z = C::kChains - 1; z > 0; --z)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[h][n][e] += more[z - 1][h][n][e];
     };
     uint32_t stage = ring;
     for (int i = 0; i < tiles; ++i) {
@@ -465,7 +511,10 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t vp = lds32(params + (kTile + 8 * k) * 4);
-                const float vs = bf16_lo_to_f32(vp), vo = bf16_hi_to_f32(vp);
+                float vs = bf16_lo_to_f32(vp);
+                const bool flipped = odd_row ^ (k & 1);
+                const float vo = fmaf(vs, flipped ? 15.f : 0.f, bf16_hi_to_f32(vp));
+                vs = flipped ? -vs : vs;
 #pragma unroll
                 for (int r = 0; r < C::kLaneRows; ++r) {
                     const float p = ex2_approx(x[r][k]);
@@ -523,17 +572,19 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             l[r] += sum[r];
             off[r] += shift[r];
         }
-        // ---- values
+        // ---- values: a tile's products by themselves, the small terms first, and added
+        // with rounding to the running sums -- added there by the products they would lose
+        // half a last place each time, always towards zero (1,000 products: 3e-5)
+        uint32_t pb[2][C::kCols][C::kTerms][2];   // weights in the products' layout
+        uint32_t both[2][C::kWordsV][2][2];       // [16 tokens][word][token pair][half]
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            // weights as fp16 terms, in the products' layout: [tile of columns][term][half]
-            uint32_t pb[C::kCols][C::kTerms][2];
             if constexpr (C::kPacked) {
                 const float u = x[0][2 * h], v = x[0][2 * h + 1];
                 const uint32_t hi = pack_f16x2(u, v);
                 const uint32_t lo = pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
-                pb[0][0][0] = transpose8(__byte_perm(hi, lo, 0x5410));
-                pb[0][0][1] = transpose8(__byte_perm(hi, lo, 0x7632));
+                pb[h][0][0][0] = transpose8(__byte_perm(hi, lo, 0x5410));
+                pb[h][0][0][1] = transpose8(__byte_perm(hi, lo, 0x7632));
             } else {
 #pragma unroll
                 for (int n = 0; n < C::kCols; ++n)
@@ -543,8 +594,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                         const uint32_t hi = pack_f16x2(u, v);
                         const uint32_t lo =
                             pack_f16x2(u - f16_lo_to_f32(hi), v - f16_hi_to_f32(hi));
-                        pb[n][0][half] = transpose8(hi);
-                        pb[n][C::kTerms - 1][half] = transpose8(lo);
+                        pb[h][n][0][half] = transpose8(hi);
+                        pb[h][n][C::kTerms - 1][half] = transpose8(lo);
                     }
             }
             // the four tokens of this lane, and their words
@@ -553,29 +604,48 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             lds_words(stage + my_v1 + 16 * h * C::kRowBytes, v1);
             lds_words(stage + my_v0 + (16 * h + 8) * C::kRowBytes, v2);
             lds_words(stage + my_v1 + (16 * h + 8) * C::kRowBytes, v3);
-            uint32_t both[C::kWordsV][2][2];      // [word][token pair][low, high half]
 #pragma unroll
             for (int w = 0; w < C::kWordsV; ++w) {
-                both[w][0][0] = __byte_perm(v0[w], v1[w], 0x5410);
-                both[w][0][1] = __byte_perm(v0[w], v1[w], 0x7632);
-                both[w][1][0] = __byte_perm(v2[w], v3[w], 0x5410);
-                both[w][1][1] = __byte_perm(v2[w], v3[w], 0x7632);
+                both[h][w][0][0] = __byte_perm(v0[w], v1[w], 0x5410);
+                both[h][w][0][1] = __byte_perm(v0[w], v1[w], 0x7632);
+                both[h][w][1][0] = __byte_perm(v2[w], v3[w], 0x5410);
+                both[h][w][1][1] = __byte_perm(v2[w], v3[w], 0x7632);
             }
-            // element n of word w for a pair of tokens: index 8 w + n
-            auto element = [&](int index, int pair) {
-                const int n = index & 7;
-                const uint32_t z = both[index >> 3][pair][n >> 2];
-                return ((n & 2) ? z >> 8 : z) & ((n & 1) ? 0x00f000f0u : 0x000f000fu);
-            };
+        }
+        // element n of word w for a pair of tokens: index 8 w + n
+        auto element = [&](int h, int index, int pair) {
+            const int n = index & 7;
+            const uint32_t z = both[h][index >> 3][pair][n >> 2];
+            const uint32_t flip = pair ? flips ^ kSmall : flips;
+            const uint32_t y = (n & 2) ? z >> 5 : z << 3;
+            return n & 1 ? (y & kLarge) ^ (flip << 4) : (y & kSmall) ^ flip;
+        };
 #pragma unroll
-            for (int p = 0; p < C::kProducts; ++p) {
-                const uint32_t a0 = element(p, 0), a1 = element(p + C::kProducts, 0);
-                const uint32_t a2 = element(p, 1), a3 = element(p + C::kProducts, 1);
+        for (int p = 0; p < C::kProducts; ++p) {
+            uint32_t e[2][4];
 #pragma unroll
-                for (int n = 0; n < C::kCols; ++n)
+            for (int h = 0; h < 2; ++h) {
+                e[h][0] = element(h, p, 0);
+                e[h][1] = element(h, p + C::kProducts, 0);
+                e[h][2] = element(h, p, 1);
+                e[h][3] = element(h, p + C::kProducts, 1);
+            }
 #pragma unroll
-                    for (int term = 0; term < C::kTerms; ++term)
-                        mma_f16(acc[p][n], a0, a1, a2, a3, pb[n][term][0], pb[n][term][1]);
+            for (int n = 0; n < C::kCols; ++n) {
+                float z[4];
+#pragma unroll
+                for (int term = C::kTerms - 1; term >= 0; --term)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (term == C::kTerms - 1 && h == 0)
+                            mma_f16_first(z, e[h][0], e[h][1], e[h][2], e[h][3], pb[h][n][term][0],
+                                          pb[h][n][term][1]);
+                        else
+                            mma_f16(z, e[h][0], e[h][1], e[h][2], e[h][3], pb[h][n][term][0],
+                                    pb[h][n][term][1]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[p][n][i] += z[i];
             }
         }
         stage += C::kStageBytes;
@@ -604,7 +674,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                 const int index = p + half * C::kProducts, w = index >> 3, n = index & 7;
                 const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
                                            : acc[p][r >> 1][2 * half + (r & 1)];
-                o[8 * (C::kWordsV * g + w) + n] = fmaf(z, n & 1 ? 1048576.f : 16777216.f, off[r]) * inv;
+                o[8 * (C::kWordsV * g + w) + n] = fmaf(z, n & 1 ? kUp / 16.f : kUp, off[r]) * inv;
             }
     }
     __syncthreads();

@@ -3,8 +3,9 @@
 // Element d of token j's key is s_j c_jd + o_j with the row's scale s_j and offset o_j, so
 //     q . K_j = s_j (q . c_j) + o_j sum_d q_d
 // and the values' sum splits likewise into sum_j (p_j s_j) c_j and, the same for every
-// element, sum_j p_j o_j: the codes go into the products as whole numbers and scales and
-// offsets are applied once a token.
+// element, sum_j p_j o_j: the codes go into the products as numbers and scales and offsets
+// are applied once a token.  The numbers are c - 7.5 (and the offsets o + 7.5 s): sums of
+// the codes themselves would grow with the context and cancel against the offsets'.
 //
 // One warp per (sequence, query token, query head, split); lanes split a row into words
 // of 8 codes, a token's score is a warp reduction, and the online softmax (running max
@@ -30,6 +31,11 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// The e-th code of a word, less 7.5.
+__device__ __forceinline__ float centred(uint32_t word, int e) {
+    return float((word >> (4 * e)) & 15u) - 7.5f;
 }
 
 // KC / VC: words of a K and of a V row a lane holds (ceil(dim / 256)).
@@ -117,13 +123,14 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_generic_kernel(const 
             for (int i = 0; i < KC; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    part = fmaf(qv[i][e], float((kr[u][i] >> (4 * e)) & 15u), part);
+                    part = fmaf(qv[i][e], centred(kr[u][i], e), part);
             sc[u] = part;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const float dot = warp_sum(sc[u]);
-            sc[u] = live[u] ? fmaf(bf16_lo_to_f32(kp[u]), dot, bf16_hi_to_f32(kp[u]) * qsum)
+            const float ks = bf16_lo_to_f32(kp[u]);
+            sc[u] = live[u] ? fmaf(ks, dot, fmaf(ks, 7.5f, bf16_hi_to_f32(kp[u])) * qsum)
                             : -INFINITY;
         }
         float m_new = m;
@@ -137,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_generic_kernel(const 
             const float p = exp2f(sc[u] - base);
             psum += p;
             w[u] = live[u] ? p * bf16_lo_to_f32(vp[u]) : 0.f;
-            posum += live[u] ? p * bf16_hi_to_f32(vp[u]) : 0.f;
+            posum += live[u] ? p * fmaf(bf16_lo_to_f32(vp[u]), 7.5f, bf16_hi_to_f32(vp[u])) : 0.f;
         }
         l = l * corr + psum;
         off = off * corr + posum;
@@ -159,7 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_int4_generic_kernel(const 
                 acc[i][e] *= corr;
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
-                    acc[i][e] = fmaf(w[u], float((vr[u][i] >> (4 * e)) & 15u), acc[i][e]);
+                    acc[i][e] = fmaf(w[u], centred(vr[u][i], e), acc[i][e]);
             }
     }
 
