@@ -77,7 +77,7 @@ struct Config {
     static constexpr int kTerms = kPacked ? 1 : 2;    // products a tile of columns
     static constexpr int kLaneRows = kPacked ? 1 : 2 * kCols;
     static constexpr int kCtas = kResident;
-    static constexpr int kStages = D == 128 ? (ROWS == 16 ? 3 : 4) : 7;
+    static constexpr int kStages = D == 128 ? 3 : 4;  // (one more or less changes 2%)
     // The scores' sums of the two terms apart, where registers allow: fewer cut-offs on the
     // large one, and fewer products that wait for one another.
     static constexpr int kChains = ROWS == 8 ? 2 : 1;
@@ -86,7 +86,8 @@ struct Config {
     }
     // 16 rows: the query's fragments (the same for all the CTA's warps) in shared memory,
     // as the registers hold the sums
-    static constexpr bool kSharedQuery = ROWS == 16;
+    static constexpr bool kSharedQuery = ROWS == 16 || (ROWS == 8 && D == 128);
+    static_assert(!kSharedQuery || !kPacked, "a packed query is held by its lanes");
     static constexpr int kQueryBytes = kSharedQuery ? kWordsK * kCols * kTerms * 512 : 0;
     static constexpr int kStageBytes = 2 * kTile * (kRowBytes + 4);
     static constexpr int kWarpBytes = kStages * kStageBytes;
@@ -94,6 +95,7 @@ struct Config {
     // the warps' outputs go over the rings at the end
     static constexpr int kMergeBytes = kWarps * ROWS * (D + 1) * 4;
     static constexpr int kSmem = (kRings > kMergeBytes ? kRings : kMergeBytes) + kQueryBytes;
+    static_assert(kResident * (kSmem + 1024 + 256) <= 233472, "an SM's shared memory");
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {

@@ -281,6 +281,52 @@ def test_streams_and_graphs(pkv):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("B,longest,hq,hkv,d,bs,T", [
+    (40, 900, 32, 8, 128, 16, 1), (3, 6000, 64, 8, 128, 32, 1), (97, 700, 8, 1, 128, 8, 4),
+    (33, 1500, 16, 4, 64, 64, 2), (300, 200, 8, 2, 128, 16, 1), (1, 9000, 16, 2, 128, 16, 1),
+    (17, 1, 4, 2, 64, 16, 1), (64, 600, 4, 4, 128, 16, 1), (130, 40, 32, 8, 128, 64, 1)])
+def test_plans_of_ragged_batches(pkv, B, longest, hq, hkv, d, bs, T):
+    """Lengths of every kind, empty ones among them, in tables wide enough for a plan."""
+    g = torch.Generator().manual_seed(B + longest)
+    lens = torch.randint(0, longest + 1, (B,), generator=g)
+    lens[::5] = 0
+    lens[-1] = longest
+    c = _int4.make(B, lens.tolist(), hq, hkv, d, d, bs, T, width=max(640, longest) // bs + 3)
+    out, lse = decode(pkv, c)
+    assert pkv.device_status() == (pkv.DEV_SEQ_LEN if T > 1 else 0)
+    _int4.close(out, lse, _int4.attend(c))
+
+
+@pytest.mark.parametrize("B,L,hq,hkv", [(8, 1024, 8, 2), (2, 3000, 8, 8), (1, 5000, 4, 1),
+                                        (50, 640, 16, 8), (7, 130, 8, 4)])
+def test_plans_of_equal_lengths(pkv, B, L, hq, hkv):
+    c = _int4.make(B, [L] * B, hq, hkv, 128, 128, 16, width=max(640, L) // 16 + 1)
+    ref = _int4.attend(c)
+    out, lse = decode(pkv, c)
+    _int4.close(out, lse, ref)
+    again = decode(pkv, c)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("G,T,kw", [(4, 1, {}), (8, 1, dict(num_splits=1)), (4, 4, {}),
+                                    (2, 1, dict(flags=1))])
+def test_long_sums_keep_their_precision(pkv, G, T, kw):
+    """40,000 tokens of nearly equal weights, whose values cancel to a two-hundredth: off by
+    1e-5 of the result at most, as sums in fp32 would be."""
+    c = _int4.make(21, [40000], 2 * G, 2, 128, 128, 64, T, poison=False)
+    c.q.mul_(0.05)
+    ro = _int4.attend(c)[0]
+    out = decode(pkv, c, **kw)[0].cpu().double().view(ro.shape)
+    assert float((out - ro).norm() / ro.norm()) < 1e-5
+
+
+def test_more_pairs_than_a_plan_takes(pkv):
+    """Thousands of (sequence, KV head) pairs: one CTA each."""
+    c = _int4.make(22, [3 + i % 60 for i in range(700)], 8, 8, 64, 64, 8, width=80)
+    assert pkv.decode_workspace_size_int4(*c.pools(), 700, 8, 80) == 0
+    _int4.close(*decode(pkv, c), _int4.attend(c))
+
+
 def test_far_blocks(pkv):
     """Blocks whose bytes lie past 2^32 in the pool."""
     bs, hkv, d = 16, 8, 128
