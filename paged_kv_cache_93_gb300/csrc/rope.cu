@@ -16,10 +16,11 @@
 // signed number of 2^-32 turns, are rounded to binary32 (2^-26 turns) for
 // sincospif.
 //
-// Several axes.  With pair_axis each pair takes its position from its own axis (time,
-// height, width of an image's or a video's tokens): positions is then [axes][tokens].
-// Only the loads of the positions differ; a token's pairs are spread over lanes either
-// way, each lane with the rows of its own pairs' axes.
+// Several axes.  With AXES each pair takes its position from its own axis (time, height,
+// width of an image's or a video's tokens): positions is then [axes][tokens].  Only the
+// loads of the positions differ; a token's pairs are spread over lanes either way, each
+// lane with the rows of its own pairs' axes.  (A template, not a run-time choice: 8 tokens
+// 3.3 us, which the choice made 3.6, 8,191 tokens 35.9 and 37.1.)
 //
 // Bound: memory.  Every q, k and v element is read once and written once, as
 // 16-byte vectors; cosines and sines (rotary_dim / 2 of them against (Hq + Hkv) *
@@ -29,6 +30,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pkv.h"
 #include "pkv_device.cuh"
@@ -113,21 +115,20 @@ __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
     return __double2ull_rz((turns - floor(turns)) * 18446744073709551616.0);
 }
 
-// Where a pair's positions begin: its axis's row of them.
-__device__ __forceinline__ int64_t axis_row(const RopeArgs &a, int pair) {
-    if (!a.pair_axis) return 0;
+// A pair's axis: the row of `positions` that it reads.
+__device__ __forceinline__ int32_t axis_of(const RopeArgs &a, int pair) {
     int32_t axis = a.pair_axis[pair];
     if (axis < 0 || axis >= a.axes) {
         raise_status(a.status, PKV_DEV_AXIS);
         axis = 0;
     }
-    return axis * a.num_tokens;
+    return axis;
 }
 
 // VEC: rotary_dim and rotary_offset let whole 16-byte vectors rotate (half
 // layout: both multiples of 16 and 8; interleaved: multiples of 8).  Otherwise
 // a unit is a single pair, or a single element outside the rotary part.
-template <bool INTER, bool E4, bool VEC>
+template <bool INTER, bool E4, bool VEC, bool AXES>
 __global__ void __launch_bounds__(kThreads)
 rope_append_kernel(const RopeArgs a) {
     __shared__ float2 cs[2][kMaxPairs];          // (cos, sin) * amplitude, by token parity
@@ -136,12 +137,12 @@ rope_append_kernel(const RopeArgs a) {
     pdl_launch_dependents();
     // this thread's frequencies (kMaxPairs / kThreads at most)
     uint64_t step[kMaxPairs / kThreads];
-    int64_t arow[kMaxPairs / kThreads];
+    int32_t axis[kMaxPairs / kThreads];
 #pragma unroll
     for (int i = 0; i < kMaxPairs / kThreads; ++i) {
         const int pr = threadIdx.x + i * kThreads;
         step[i] = pr < npairs ? turn_step(a.inv_freq[pr]) : 0;
-        arow[i] = pr < npairs ? axis_row(a, pr) : 0;
+        if constexpr (AXES) axis[i] = pr < npairs ? axis_of(a, pr) : 0;
     }
     const int rows_qk = a.hq + a.hkv;
     const int n_qk = rows_qk * a.q_units, n_all = n_qk + a.hkv * a.v_units;
@@ -155,8 +156,7 @@ rope_append_kernel(const RopeArgs a) {
         for (int i = 0; i < kMaxPairs / kThreads; ++i) {
             const int pr = threadIdx.x + i * kThreads;
             if (pr < npairs) {
-                const uint64_t turn =
-                    step[i] * uint64_t(a.pair_axis ? a.positions[arow[i] + t] : pos);
+                const uint64_t turn = step[i] * uint64_t(AXES ? a.positions[axis[i] * a.num_tokens + t] : pos);
                 // signed 2^-32 turns; sincospif takes half turns
                 const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
                 float s, c;
@@ -306,12 +306,12 @@ constexpr int kWideCtas = 3;             // per SM
 constexpr int kItemUnits = 2048;         // units of a work item, about
 constexpr int kTable = 1024;             // entries of a table of cosines and sines
 
-template <bool INTER, bool E4>
+template <bool INTER, bool E4, bool AXES>
 __global__ void __launch_bounds__(kThreads, kWideCtas)
 rope_append_wide_kernel(const RopeArgs a) {
     __shared__ __align__(16) float2 cs[2][kTable];   // (cos, sin) * amplitude
     __shared__ uint64_t step[kMaxPairs];
-    __shared__ int64_t arow[kMaxPairs];
+    __shared__ int32_t axis[AXES ? kMaxPairs : 1];
     __shared__ int64_t s_slot[2][8];             // slot of a token's rows, or -1: not stored
     __shared__ int32_t s_live[2][8];
     const int npairs = a.rot >> 1;
@@ -319,7 +319,7 @@ rope_append_wide_kernel(const RopeArgs a) {
     pdl_launch_dependents();
     for (int i = threadIdx.x; i < npairs; i += kThreads) {
         step[i] = turn_step(a.inv_freq[i]);
-        arow[i] = axis_row(a, i);
+        if constexpr (AXES) axis[i] = axis_of(a, i);
     }
     __syncthreads();
     // this thread's unit of a row, and the row it takes first
@@ -461,7 +461,7 @@ rope_append_wide_kernel(const RopeArgs a) {
         }
         for (int i = threadIdx.x; i < ntok * npairs; i += kThreads) {
             const int tk = a.group > 1 ? i / npairs : 0, pr = i - tk * npairs;
-            const uint64_t turn = step[pr] * uint64_t(a.positions[arow[pr] + t0 + tk]);
+            const uint64_t turn = step[pr] * uint64_t(a.positions[(AXES ? axis[pr] * a.num_tokens : 0) + t0 + tk]);
             // signed 2^-32 turns; sincospif takes half turns
             const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
             float s, co;
@@ -500,7 +500,7 @@ rope_append_wide_kernel(const RopeArgs a) {
 constexpr int kWarpAhead = 2;
 constexpr int kWarpCtas = 3;             // per SM
 
-template <bool INTER, int FMT>
+template <bool INTER, int FMT, bool AXES>
 __global__ void __launch_bounds__(kThreads, kWarpCtas)
 rope_append_warp_kernel(const RopeArgs a) {
     pdl_wait();
@@ -524,12 +524,12 @@ rope_append_warp_kernel(const RopeArgs a) {
     }
     // this lane's pairs: lane and lane + 32
     uint64_t step[2];
-    int64_t arow[2];
+    int32_t axis[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const bool has = lane + 32 * i < npairs;
         step[i] = has ? turn_step(a.inv_freq[lane + 32 * i]) : 0;
-        arow[i] = has ? axis_row(a, lane + 32 * i) : 0;
+        if constexpr (AXES) axis[i] = has ? axis_of(a, lane + 32 * i) : 0;
     }
     const int pq = (a.hq + rpp - 1) >> (5 - shift), pk = (a.hkv + rpp - 1) >> (5 - shift);
     const int passes = pq + pk + (a.dv ? pk : 0), per = (passes + a.parts - 1) / a.parts;
@@ -574,8 +574,7 @@ rope_append_warp_kernel(const RopeArgs a) {
             float c2[2], s2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint64_t turn =
-                    step[i] * uint64_t(a.pair_axis ? a.positions[arow[i] + t] : pos);
+                const uint64_t turn = step[i] * uint64_t(AXES ? a.positions[axis[i] * a.num_tokens + t] : pos);
                 // signed 2^-32 turns; sincospif takes half turns
                 sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s2[i], &c2[i]);
                 c2[i] *= a.amplitude;
@@ -686,12 +685,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
     pdl_wait();
     pdl_launch_dependents();
     uint64_t step[kMaxPairs / kThreads];
-    int64_t arow[kMaxPairs / kThreads];
+    int32_t axis[kMaxPairs / kThreads];
 #pragma unroll
     for (int i = 0; i < kMaxPairs / kThreads; ++i) {
         const int pr = threadIdx.x + i * kThreads;
         step[i] = pr < npairs ? turn_step(a.inv_freq[pr]) : 0;
-        arow[i] = pr < npairs ? axis_row(a, pr) : 0;
+        axis[i] = a.pair_axis && pr < npairs ? axis_of(a, pr) : 0;
     }
     int buf = 0;
     for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
         for (int i = 0; i < kMaxPairs / kThreads; ++i) {
             const int pr = threadIdx.x + i * kThreads;
             if (pr < npairs) {
-                const uint64_t turn = step[i] * uint64_t(a.positions[arow[i] + t]);
+                const uint64_t turn = step[i] * uint64_t(a.positions[axis[i] * a.num_tokens + t]);
                 // signed 2^-32 turns; sincospif takes half turns
                 float s, c;
                 sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
@@ -818,9 +817,11 @@ int launch_warp(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     const int64_t items = a.num_tokens * a.parts;
     const dim3 grid(unsigned(std::min<int64_t>((items + per_cta - 1) / per_cta,
                                                int64_t(sm_count()) * kWarpCtas)));
-    return launch_pdl(interleaved ? rope_append_warp_kernel<true, FMT>
-                                  : rope_append_warp_kernel<false, FMT>,
-                      grid, dim3(kThreads), 0, stream, a);
+    auto kernel = a.pair_axis ? (interleaved ? rope_append_warp_kernel<true, FMT, true>
+                                             : rope_append_warp_kernel<false, FMT, true>)
+                              : (interleaved ? rope_append_warp_kernel<true, FMT, false>
+                                             : rope_append_warp_kernel<false, FMT, false>);
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
 // Whether the form of a warp a token takes the shape.
@@ -861,9 +862,11 @@ int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
         a.parts = a.group > 1 ? 1 : int32_t((units16 + kItemUnits - 1) / kItemUnits);
         const int64_t items = (a.num_tokens + a.group - 1) / a.group * a.parts;
         const dim3 grid(unsigned(std::min(items, ctas)));
-        return launch_pdl(interleaved ? rope_append_wide_kernel<true, E4>
-                                      : rope_append_wide_kernel<false, E4>,
-                          grid, dim3(kThreads), 0, stream, a);
+        auto kernel = a.pair_axis ? (interleaved ? rope_append_wide_kernel<true, E4, true>
+                                                 : rope_append_wide_kernel<false, E4, true>)
+                                  : (interleaved ? rope_append_wide_kernel<true, E4, false>
+                                                 : rope_append_wide_kernel<false, E4, false>);
+        return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a);
     }
     const bool vec = interleaved ? (a.rot % 8 == 0 && a.off % 8 == 0)
                                  : (a.rot % 16 == 0 && a.off % 8 == 0);
@@ -874,10 +877,14 @@ int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
     a.q_magic = magic_of(a.q_units);
     a.v_magic = magic_of(std::max(1, a.v_units));
     const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, int64_t(sm_count()) * 8)));
-    auto kernel = interleaved
-                      ? (vec ? rope_append_kernel<true, E4, true> : rope_append_kernel<true, E4, false>)
-                      : (vec ? rope_append_kernel<false, E4, true>
-                             : rope_append_kernel<false, E4, false>);
+    auto of = [&](auto axes) {
+        constexpr bool A = decltype(axes)::value;
+        return interleaved ? (vec ? rope_append_kernel<true, E4, true, A>
+                                  : rope_append_kernel<true, E4, false, A>)
+                           : (vec ? rope_append_kernel<false, E4, true, A>
+                                  : rope_append_kernel<false, E4, false, A>);
+    };
+    auto kernel = a.pair_axis ? of(std::true_type{}) : of(std::false_type{});
     return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
