@@ -6,8 +6,8 @@
 // and both products run over the codes themselves; scales and offsets are applied to the
 // scores and to the weights, once a token.
 //
-// Bound: memory.  A row of 128 elements is 68 bytes, so an SM at full bandwidth meets
-// 41 elements a clock and cannot afford an instruction for each.  Hence:
+// A row of 128 elements is 68 bytes, so an SM at full bandwidth meets 41 elements a clock
+// and cannot afford an instruction for each.  Hence:
 //  - A code needs no conversion.  Its bits 0..15 at bits 3-6 of an fp16 are the subnormal
 //    code * 2^-21, and at bits 7-10 code * 2^-17 (up to 2047 an fp16's bits count evenly);
 //    tensor cores take subnormals exactly.  A 32-bit word of 8 codes becomes four fp16
@@ -41,6 +41,19 @@
 // largest element is 2^12..2^13; a row's weights p_j s'_j likewise, to 2^0..2^15, by a
 // factor that follows their running maximum -- a key that weighs much may have values
 // a millionth of the others'.
+//
+// Bound: the SM's instruction pipes, not memory.  A warp's tile of 32 tokens takes 32
+// products at 4 rows, 64 at 8 and 128 at 16, 8 clocks of a quarter of the SM each (256,
+// 512 and 1,024 clocks), in which fp32 instructions do not run and others run at about two
+// thirds; about 250 logic instructions, 200 of them to take codes apart; and 130 fp32 ones.
+// A quarter of an SM then takes 800, 1,000 and 1,700 clocks a tile, where memory would bring
+// one in 730; the same batch read from L2 is as slow (8 x 32K of 32 / 8 heads: 58.7 us, from
+// L2 57; memory alone 42.7), and 8, 12 or 16 warps an SM make no difference.
+//   8 x 32K, 32 / 8 heads of 128               58.7 us (0.73 of the copy rate)
+//   48 of up to 16K, 64 / 8                   101.8    (0.56)
+//   8 x 32K, 4 tokens each, 32 / 8            123.6    (0.35)
+//   1 x 200,000, 64 / 8                        62.0    (0.53)
+//   32 x 4,095, 2 tokens each, 32 / 8 of 64    33.9    (0.34)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -82,16 +95,19 @@ struct Config {
     // large one (16 rows of 128, error of small cases: 2e-6 instead of 1e-6, but 124 us
     // instead of 130 for 8 x 32K and 4 tokens a sequence).
     static constexpr int kChains = kPacked || (ROWS == 16 && D == 128) ? 1 : 2;
-    // 16 rows: the query's fragments (the same for all the CTA's warps) in shared memory,
-    // as the registers hold the sums
+    // The query's fragments (the same for all the CTA's warps) in shared memory where the
+    // registers hold more sums (8 rows of 128: 102 us against 105 for the ragged batch).
     static constexpr bool kSharedQuery = ROWS == 16 || (ROWS == 8 && D == 128);
     static_assert(!kSharedQuery || !kPacked, "a packed query is held by its lanes");
-    static constexpr int kQueryBytes = kSharedQuery ? kWordsK * kCols * kTerms * 512 : 0;
+    // the query's fragments, and each row's two factors
+    static constexpr int kFragments = kWordsK * kCols * kTerms * 512;
+    static constexpr int kQueryBytes = kFragments + ROWS * 8;
     static constexpr int kStageBytes = 2 * kTile * (kRowBytes + 4);
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRings = kWarps * kWarpBytes;
-    // the warps' outputs go over the rings at the end
-    static constexpr int kMergeBytes = kWarps * ROWS * (D + 1) * 4;
+    // the warps' outputs go over the rings at the end, a row's floats padded
+    static constexpr int kOutRow = D + (kPacked ? 8 : 4);
+    static constexpr int kMergeBytes = kWarps * ROWS * (kOutRow + 1) * 4;
     static constexpr int kSmem = (kRings > kMergeBytes ? kRings : kMergeBytes) + kQueryBytes;
     static_assert(kResident * (kSmem + 1024 + 256) <= 233472, "an SM's shared memory");
 };
@@ -125,6 +141,12 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&x)[N]) {
 __device__ __forceinline__ void sts_words(uint32_t a, const uint32_t (&x)[4]) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
+__device__ __forceinline__ void sts_pair(uint32_t a, float x, float y) {
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void lds_pair(uint32_t a, float &x, float &y) {
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(a) : "memory");
 }
 // D = A (16 x 16, row) * B (16 x 8, col) + D, fp16 inputs, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -211,6 +233,23 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     const int first = min(begin + warp * per, end), last = min(first + per, end);
     const int tiles = (last - first + kTile - 1) / kTile;
 
+    // ---- the query, on its way: the CTA's threads take 8 neighbouring elements each
+    constexpr int kEights = D / 8, kOctets = (ROWS * kEights + kThreads - 1) / kThreads;
+    float4 octet[kOctets][2];
+#pragma unroll
+    for (int i = 0; i < kOctets; ++i) {
+        const int u = threadIdx.x + i * kThreads, r = row0 + u / kEights;
+        octet[i][0] = octet[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u < ROWS * kEights && r < rows) {
+            const int tok = r / group;
+            const float4 *src = reinterpret_cast<const float4 *>(
+                a.q + ((int64_t(b) * a.q_tokens + tok) * a.num_q_heads + head * group +
+                       (r - tok * group)) * D + u % kEights * 8);
+            octet[i][0] = src[0];
+            octet[i][1] = src[1];
+        }
+    }
+
     // ---- the ring
     const uint32_t ring = smem_addr(smem) + warp * C::kWarpBytes;
     const int32_t *table = a.block_tables + int64_t(b) * a.max_blocks;
@@ -278,91 +317,70 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         cp_async_commit();
     }
 
-    // ---- the query: B fragments of the tile's rows, scaled to 2^12 .. 2^13
-    const auto q_row = [&](int r) {        // the r-th row of the tile
-        r += row0;
-        const int tok = r / group;
-        return a.q + ((int64_t(b) * a.q_tokens + tok) * a.num_q_heads + head * group +
-                      (r - tok * group)) * D;
-    };
-    // word w of a lane, elements 8 (kWordsK t + w) + ..: [2 step + half], step 0 takes 0, 4
-    // and 1, 5; step 1 takes 2, 6 and 3, 7; odd ones' codes come times 16
+    // ---- the query: B fragments of the tile's rows, scaled to 2^12 .. 2^13, in shared
+    // memory and from there to every warp.  Word w of lane (g, t), elements
+    // 8 (kWordsK t + w) + .. of its column's row: [2 step + half], step 0 takes 0, 4 and 1, 5;
+    // step 1 takes 2, 6 and 3, 7; odd ones' codes come times 16.
+    const uint32_t query = smem_addr(smem) + C::kSmem - C::kQueryBytes;
     uint32_t qf[C::kSharedQuery ? 1 : C::kCols][C::kTerms][C::kWordsK][4];
-    const uint32_t shared_query = smem_addr(smem) + C::kSmem - C::kQueryBytes + lane * 16;
+    const uint32_t shared_query = query + lane * 16;
     float factor[C::kLaneRows], offset_factor[C::kLaneRows];
-    {
-        float col_factor[C::kCols], col_sum[C::kCols];
 #pragma unroll
-        for (int n = 0; n < C::kCols; ++n) {
-            const int r = C::kPacked ? g >> 1 : 8 * n + g;
-            float x[C::kWordsK][8], sum = 0.f, amax = 0.f;
-            const bool in = row0 + r < rows;
+    for (int i = 0; i < kOctets; ++i) {
+        const int u = threadIdx.x + i * kThreads, r = u / kEights, piece = u % kEights;
+        if (u >= ROWS * kEights) break;                    // (whole warps)
+        const float x[8] = {octet[i][0].x, octet[i][0].y, octet[i][0].z, octet[i][0].w,
+                            octet[i][1].x, octet[i][1].y, octet[i][1].z, octet[i][1].w};
+        float sum = 0.f, amax = 0.f;
 #pragma unroll
-            for (int w = 0; w < C::kWordsK; ++w) {
-                const float4 *src =
-                    reinterpret_cast<const float4 *>(q_row(in ? r : 0) + 8 * (C::kWordsK * t + w));
-                const float4 lo = in ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 hi = in ? src[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-                x[w][0] = lo.x; x[w][1] = lo.y; x[w][2] = lo.z; x[w][3] = lo.w;
-                x[w][4] = hi.x; x[w][5] = hi.y; x[w][6] = hi.z; x[w][7] = hi.w;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    sum += x[w][e];
-                    amax = fmaxf(amax, fabsf(x[w][e]));
-                }
-            }
-            // a row's elements are in the four lanes of a group
-#pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            }
-            const int e = max(exponent(amax), -100);
-            const float up = pow2(12 - e);
-#pragma unroll
-            for (int w = 0; w < C::kWordsK; ++w) {
-                uint32_t top[4], low[4];
-#pragma unroll
-                for (int e0 = 0; e0 < 4; ++e0) {
-                    const float s = e0 & 1 ? up * 0.0625f : up;
-                    const float u = x[w][e0] * s, v = x[w][e0 + 4] * s;
-                    top[e0] = pack_f16x2(u, v);
-                    low[e0] = pack_f16x2(u - f16_lo_to_f32(top[e0]), v - f16_hi_to_f32(top[e0]));
-                }
-                if constexpr (C::kSharedQuery) {
-                    // every warp has all of it: warp w writes word w
-                    if (w == warp) {
-                        const uint32_t to = shared_query + (w * C::kCols + n) * C::kTerms * 512;
-                        sts_words(to, top);
-                        sts_words(to + 512, low);
-                    }
-                } else {
-#pragma unroll
-                    for (int e0 = 0; e0 < 4; ++e0) {
-                        if constexpr (C::kPacked) {
-                            qf[n][0][w][e0] = g & 1 ? low[e0] : top[e0];
-                        } else {
-                            qf[n][0][w][e0] = top[e0];
-                            qf[n][C::kTerms - 1][w][e0] = low[e0];
-                        }
-                    }
-                }
-            }
-            // score = s (sum of products) * col_factor + o * col_sum, in base-2 units
-            const float base = a.scale * kLog2e;
-            col_factor[n] = base * pow2(e - 12) * kUp;
-            col_sum[n] = base * sum;
+        for (int e = 0; e < 8; ++e) {
+            sum += x[e];
+            amax = fmaxf(amax, fabsf(x[e]));
         }
-        // to the lanes that hold the rows' scores: lane (g, t) has row t, or rows 2 t, 2 t + 1
 #pragma unroll
-        for (int r = 0; r < C::kLaneRows; ++r) {
-            const int col = C::kPacked ? 2 * t : 2 * t + (r & 1);
-            factor[r] = __shfl_sync(0xffffffffu, col_factor[r >> 1], 4 * col);
-            offset_factor[r] = __shfl_sync(0xffffffffu, col_sum[r >> 1], 4 * col);
+        for (int o = 1; o < kEights; o <<= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         }
-        if constexpr (C::kSharedQuery) __syncthreads();
+        const int e = max(exponent(amax), -100);
+        const float up = pow2(12 - e);
+        uint32_t top[4], low[4];
+#pragma unroll
+        for (int e0 = 0; e0 < 4; ++e0) {
+            const float s = e0 & 1 ? up * 0.0625f : up;
+            const float y = x[e0] * s, z = x[e0 + 4] * s;
+            top[e0] = pack_f16x2(y, z);
+            low[e0] = pack_f16x2(y - f16_lo_to_f32(top[e0]), z - f16_hi_to_f32(top[e0]));
+        }
+        const int w = piece % C::kWordsK, column = C::kPacked ? 2 * r : r & 7;
+        const uint32_t to = query + (w * C::kCols + (r >> 3)) * C::kTerms * 512 +
+                            (4 * column + piece / C::kWordsK) * 16;
+        sts_words(to, top);
+        sts_words(to + (C::kPacked ? 64 : 512), low);
+        // score = s (sum of products) * factor + o * offset_factor, in base-2 units
+        if (piece == 0)
+            sts_pair(query + C::kFragments + r * 8, a.scale * kLog2e * pow2(e - 12) * kUp,
+                     a.scale * kLog2e * sum);
     }
-    const int all_see = min(last, segment().len - a.q_tokens + 1);   // every row sees the tokens before
+    __syncthreads();
+    // lane (g, t) has the scores of row t, or of rows 2 t, 2 t + 1
+#pragma unroll
+    for (int r = 0; r < C::kLaneRows; ++r) {
+        const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
+        lds_pair(query + C::kFragments + row * 8, factor[r], offset_factor[r]);
+    }
+    if constexpr (!C::kSharedQuery) {
+#pragma unroll
+        for (int n = 0; n < C::kCols; ++n)
+#pragma unroll
+            for (int term = 0; term < C::kTerms; ++term)
+#pragma unroll
+                for (int w = 0; w < C::kWordsK; ++w)
+                    lds_words(shared_query + ((w * C::kCols + n) * C::kTerms + term) * 512,
+                              qf[n][term][w]);
+    }
+    // every row sees the tokens before
+    const int all_see = min(last, segment().len - a.q_tokens + 1);
     // tokens that the lane's r-th row sees
     auto sees = [&](int r) {
         const Segment seg = segment();
@@ -524,8 +542,12 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             }
             return leaves;
         };
-        scores(from);
-        if (__any_sync(0xffffffffu, tail ? weigh(std::true_type{}) : weigh(std::false_type{}))) {
+        bool move = i == 0;
+        if (!move) {
+            scores(from);
+            move = __any_sync(0xffffffffu, tail ? weigh(std::true_type{}) : weigh(std::false_type{}));
+        }
+        if (move) {
             float by[C::kLaneRows];
 #pragma unroll
             for (int r = 0; r < C::kLaneRows; ++r) by[r] = 0.f;
@@ -537,7 +559,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                 for (int k = 0; k < 4; ++k) {
                     const float vs = fabsf(bf16_lo_to_f32(lds32(params + (kTile + 8 * k) * 4)));
                     y = fmaxf(y, x[r][k]);
-                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f) w = fmaxf(w, x[r][k] + log2f(vs));
+                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f) w = fmaxf(w, x[r][k] + __log2f(vs));
                 }
                 top[r] = fmaxf(top[r], group_max(y));
                 heaviest[r] = fmaxf(heaviest[r], group_max(w));
@@ -647,8 +669,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     // ---- the CTA's warps together: outputs, maxima and sums over the rings
     cp_async_wait<0>();
     __syncthreads();
-    float *outs = reinterpret_cast<float *>(smem);            // [warp][ROWS][D]
-    float *stats = outs + kWarps * ROWS * D;                  // [warp][ROWS]
+    float *outs = reinterpret_cast<float *>(smem);            // [warp][ROWS][kOutRow]
+    float *stats = outs + kWarps * ROWS * C::kOutRow;         // [warp][ROWS]
 #pragma unroll
     for (int r = 0; r < C::kLaneRows; ++r) {
         // each warp's row by itself: its output, and log2 of its sum
@@ -658,16 +680,27 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         const float inv = some ? 1.f / l[r] : 0.f;
         const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
         if (g == 0) stats[warp * ROWS + row] = some ? from[r] + log2f(l[r]) : kNone;
-        float *o = outs + (warp * ROWS + row) * D;
+        // The lane's neighbouring elements of the row, four at a time.  Eight lanes store at
+        // once, two of g and four of t: the rows' padding and the odd g's order of fours
+        // put them in banks of their own (stored one by one, as they are, they met 16 to a
+        // bank: 8 x 4096 tokens XX us instead of 18.1).
+        float4 *o = reinterpret_cast<float4 *>(outs + (warp * ROWS + row) * C::kOutRow) +
+                    2 * C::kWordsV * g;
+        float y[2 * C::kProducts];
 #pragma unroll
-        for (int p = 0; p < C::kProducts; ++p)
+        for (int i = 0; i < 2 * C::kProducts; ++i) {
+            const int p = i % C::kProducts, half = i / C::kProducts;
+            const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
+                                       : acc[p][r >> 1][2 * half + (r & 1)];
+            y[i] = fmaf(z, i & 1 ? kUp / 16.f : kUp, off[r]) * inv;
+        }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int index = p + half * C::kProducts, w = index >> 3, n = index & 7;
-                const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
-                                           : acc[p][r >> 1][2 * half + (r & 1)];
-                o[8 * (C::kWordsV * g + w) + n] = fmaf(z, n & 1 ? kUp / 16.f : kUp, off[r]) * inv;
-            }
+        for (int c = 0; c < C::kProducts / 2; c += 2) {
+            const float4 u = make_float4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+            const float4 v = make_float4(y[4 * c + 4], y[4 * c + 5], y[4 * c + 6], y[4 * c + 7]);
+            o[c + (g & 1)] = g & 1 ? v : u;
+            o[c + 1 - (g & 1)] = g & 1 ? u : v;
+        }
     }
     __syncthreads();
     const Segment seg = segment();
@@ -684,7 +717,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         for (int w = 0; w < kWarps; ++w) {
             const float z = stats[w * ROWS + r];
             const float by = z == kNone ? 0.f : ex2_approx(z - most);
-            const float4 y = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * D + e);
+            const float4 y = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * C::kOutRow + e);
             all += by;
             o.x = fmaf(by, y.x, o.x); o.y = fmaf(by, y.y, o.y);
             o.z = fmaf(by, y.z, o.z); o.w = fmaf(by, y.w, o.w);
@@ -756,8 +789,8 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
 // work evenly, whatever the lengths.
 //
 // A unit is a (sequence, KV head, tile of rows): n = ceil(length / 128) steps of a CTA's
-// four warps, and kStart more for the start and end of one more piece of work.  The units lie one after another
-// on a line of T = sum (n + kStart); CTA i of C takes [i T / C, (i + 1) T / C) of it, so
+// four warps, and kStart more for the start and end of one more piece of work.  The units
+// lie one after another on a line of T = sum (n + kStart); CTA i of C takes [i T / C, (i + 1) T / C) of it, so
 // it meets the end of one unit, perhaps some whole ones, and the beginning of another.
 // A whole unit goes straight to the output; the parts of others go to the workspace
 // (CTA i's at 2 i, or 2 i + 1 if it is the unit's first) and are merged by the next
@@ -767,6 +800,7 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
 constexpr int kStep = kWarps * kTile;
 constexpr int kStart = 4;
 constexpr int kMaxPlanned = 2048;          // sequences
+constexpr int kMaxUnits = 65536;
 
 struct Record {                            // of a unit: its parts (0: whole) and their first CTA
     int32_t parts, first;
@@ -794,8 +828,8 @@ __device__ __forceinline__ int steps_of(int len) {
     return int((uint32_t(len) + kStep - 1) / kStep);
 }
 
-// The next part of a unit with something to do (b < 0: none).  Whoever has a unit's beginning writes
-// its record if `writes`.
+// The next part of a unit with something to do (b < 0: none).  Whoever has a unit's
+// beginning writes its record if `writes`.
 __device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int block_shift, int row_tiles,
                                                 int rows, Record *records, Share &share,
                                                 bool writes) {
@@ -1066,10 +1100,10 @@ int launch(const Int4DecodeArgs &a, void *workspace) {
                               a.stream, a, tiles, shift, parts, part_lse, records);
     if (st != PKV_OK) return st;
     // more than about nine parts a unit: a row a CTA, its parts in groups
-    constexpr int kRows = 512 / D;
+    constexpr int kRows = std::min(ROWS, 512 / D);
     const bool many = ctas > 8 * units;
     return launch_pdl(many ? int4_merge_kernel<D, ROWS, 1> : int4_merge_kernel<D, ROWS, kRows>,
-                      dim3(units, many ? ROWS : (ROWS + kRows - 1) / kRows), dim3(kThreads), 0,
+                      dim3(units, many ? ROWS : ROWS / kRows), dim3(kThreads), 0,
                       a.stream, a, tiles, static_cast<const float *>(parts),
                       static_cast<const float *>(part_lse), static_cast<const Record *>(records));
 }
@@ -1077,25 +1111,27 @@ int launch(const Int4DecodeArgs &a, void *workspace) {
 }  // namespace
 
 bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
-                          int32_t q_tokens) {
+                          int32_t q_tokens, int32_t max_blocks) {
     const int32_t bs = c.block_size;
     if (c.head_dim_k != c.head_dim_v || (c.head_dim_k != 64 && c.head_dim_k != 128) || bs < 8 ||
         (bs & (bs - 1)) != 0)
         return false;
-    // pool rows are numbered within 32 bits, items within 31 at any split count
+    // pool rows are numbered within 32 bits, a sequence's tokens within 30, items within 31
+    // at any split count
     if (int64_t(c.num_blocks) * c.num_kv_heads * bs > int64_t(UINT32_MAX)) return false;
+    if (int64_t(max_blocks) * bs > (1 << 30)) return false;
     const int64_t rows = int64_t(num_q_heads) / c.num_kv_heads * q_tokens;
     return int64_t(batch) * c.num_kv_heads * ((rows + 3) / 4) * 256 <= INT32_MAX;
 }
 
 size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
                            int32_t q_tokens, int32_t max_blocks) {
-    if (batch > kMaxPlanned || !int4_kernel_supports(c, batch, num_q_heads, q_tokens)) return 0;
+    if (batch > kMaxPlanned) return 0;
     const int64_t ctas = int64_t(sm_count()) * kResident;
     const int64_t units = int64_t(batch) * c.num_kv_heads * row_tiles(c, num_q_heads, q_tokens);
-    // (many units for each CTA: the device evens them out by itself; sequences of a few
-    // steps at most: a plan costs more than it evens out, 16 of 128 tokens 7.7 us against 4.5)
-    if (units > 4 * ctas || int64_t(max_blocks) * c.block_size <= 4 * kStep) return 0;
+    // Sequences of a few steps at most: a plan costs more than it evens out (16 of 128 tokens:
+    // 7.7 us against 4.5).  And each unit has a record and a CTA of the merge.
+    if (int64_t(max_blocks) * c.block_size <= 4 * kStep || units > kMaxUnits) return 0;
     const int rows = tile_rows(num_q_heads / c.num_kv_heads * q_tokens);
     return size_t(ctas) * 2 * rows * (c.head_dim_v + 1) * sizeof(float) +
            size_t(units) * sizeof(Record);

@@ -17,9 +17,9 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Whether the tensor-core kernel takes the call.
 bool on_tensor_cores(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
-                     int32_t flags) {
+                     int32_t max_blocks, int32_t flags) {
     return !(flags & PKV_DECODE_GENERIC) && hq % c.num_kv_heads == 0 &&
-           int4_kernel_supports(c, batch, hq, tokens);
+           int4_kernel_supports(c, batch, hq, tokens, max_blocks);
 }
 
 // How a call runs: the library's own plan (S = 0), or S chunks, and its workspace.
@@ -31,7 +31,7 @@ struct Plan {
 Plan plan_of(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
              int32_t max_blocks, int32_t num_splits, int32_t flags) {
     int32_t S = num_splits;
-    if (S == 0 && on_tensor_cores(c, batch, tokens, hq, flags)) {
+    if (S == 0 && on_tensor_cores(c, batch, tokens, hq, max_blocks, flags)) {
         const size_t bytes = int4_plan_workspace(c, batch, hq, tokens, max_blocks);
         if (bytes) return {0, bytes};
         S = 1;
@@ -48,7 +48,7 @@ Plan plan_of(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
 }
 
 int run_split_kernel(const Int4DecodeArgs &a, int32_t flags) {
-    return on_tensor_cores(a.cache, a.batch, a.q_tokens, a.num_q_heads, flags)
+    return on_tensor_cores(a.cache, a.batch, a.q_tokens, a.num_q_heads, a.max_blocks, flags)
                ? launch_decode_int4(a, nullptr)
                : launch_decode_int4_generic(a);
 }

@@ -217,7 +217,7 @@ int launch_decode_int4_generic(const Int4DecodeArgs &a);
 // above; 0: the library's own plan, the whole result to out_part / lse_part, with a
 // workspace of int4_plan_workspace bytes (0: the shape has no plan).
 bool int4_kernel_supports(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
-                          int32_t q_tokens);
+                          int32_t q_tokens, int32_t max_blocks);
 size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
                            int32_t q_tokens, int32_t max_blocks);
 int launch_decode_int4(const Int4DecodeArgs &a, void *workspace);

@@ -320,11 +320,23 @@ def test_long_sums_keep_their_precision(pkv, G, T, kw):
     assert float((out - ro).norm() / ro.norm()) < 1e-5
 
 
-def test_more_pairs_than_a_plan_takes(pkv):
-    """Thousands of (sequence, KV head) pairs: one CTA each."""
-    c = _int4.make(22, [3 + i % 60 for i in range(700)], 8, 8, 64, 64, 8, width=80)
-    assert pkv.decode_workspace_size_int4(*c.pools(), 700, 8, 80) == 0
+@pytest.mark.parametrize("B,plan", [(700, True), (2100, False)])
+def test_thousands_of_pairs(pkv, B, plan):
+    lens = [3 + i % 60 for i in range(B)]
+    lens[B // 2] = 700
+    c = _int4.make(22, lens, 8, 8, 64, 64, 8, width=90)
+    assert (pkv.decode_workspace_size_int4(*c.pools(), B, 8, 90) > 0) == plan
     _int4.close(*decode(pkv, c), _int4.attend(c))
+
+
+def test_tables_too_wide_for_the_tensor_cores(pkv):
+    """2^30 tokens and more a table row: the CUDA-core kernel numbers them."""
+    c = _int4.make(23, [300], 4, 1, 64, 64, 256)
+    wide = torch.full((1, (1 << 22) + 1), -1, dtype=torch.int32, device="cuda")
+    wide[0, :2] = c.tables[0, :2].cuda()
+    out, lse = pkv.paged_decode_attn_int4(c.q[:, 0].contiguous().cuda(), *c.pools(), wide,
+                                          c.lens.cuda(), c.scale, num_splits=2)
+    _int4.close(out, lse, _int4.attend(c))
 
 
 def test_far_blocks(pkv):
