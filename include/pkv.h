@@ -647,18 +647,20 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
  * those above 2^100 may overflow the sums.
  * num_splits = S > 0: S chunks of every sequence, merged; 0: the library's own
  * plan, which shares the tokens of all sequences evenly among the CTAs that
- * the device holds, from the lengths themselves (where that is not worth it --
- * tables of 512 tokens or fewer, more than 2048 sequences -- and for shapes of
- * the CUDA-core kernel an S of its choice).  Either gives the same bits on every run.
+ * the device holds, from the lengths themselves.  Where that is not worth it
+ * (tables of 512 tokens or fewer, more than 512 sequences, or three times as
+ * many pairs of sequence and KV head as CTAs) a CTA takes a pair; shapes of the
+ * CUDA-core kernel run with an S of its choice.  Either gives the same bits on
+ * every run.
  * workspace: pkv_decode_workspace_size_int4 bytes for the call's arguments
  * (tokens_per_seq 1 for the single-token call) on the current device, 16-byte
  * aligned, contents on entry do not matter (0 bytes: may be NULL); calls that
  * may overlap on the GPU need one each.
- * Head dims 64 or 128 (equal for K and V), power-of-two block sizes 8..256
+ * Head dims 64 or 128 (equal for K and V), power-of-two block sizes 8..256,
  * caches of fewer than 2^32 rows (num_blocks * num_kv_heads * block_size) and
- * tables of up to 2^30 tokens run on tensor cores; other shapes on CUDA cores.  flags: 0,
- * PKV_DECODE_GENERIC (the CUDA-core kernel), PKV_DECODE_NO_TCGEN05 (accepted:
- * no kernel here uses tcgen05).  num_q_heads <= 262,140, batch *
+ * tables of up to 2^30 tokens run on tensor cores; other shapes on CUDA
+ * cores.  flags: 0, PKV_DECODE_GENERIC (the CUDA-core kernel),
+ * PKV_DECODE_NO_TCGEN05 (accepted: no kernel here uses tcgen05).  num_q_heads <= 262,140, batch *
  * tokens_per_seq <= 65535, 1 <= tokens_per_seq <= 64.
  * ------------------------------------------------------------------------- */
 size_t pkv_decode_workspace_size_int4(const pkv_cache_desc *cache, int32_t batch,

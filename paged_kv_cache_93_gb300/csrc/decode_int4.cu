@@ -47,13 +47,15 @@
 // 512 and 1,024 clocks), in which fp32 instructions do not run and others run at about two
 // thirds; about 250 logic instructions, 200 of them to take codes apart; and 130 fp32 ones.
 // A quarter of an SM then takes 800, 1,000 and 1,700 clocks a tile, where memory would bring
-// one in 730; the same batch read from L2 is as slow (8 x 32K of 32 / 8 heads: 58.7 us, from
-// L2 57; memory alone 42.7), and 8, 12 or 16 warps an SM make no difference.
-//   8 x 32K, 32 / 8 heads of 128               58.7 us (0.73 of the copy rate)
-//   48 of up to 16K, 64 / 8                   101.8    (0.56)
-//   8 x 32K, 4 tokens each, 32 / 8            123.6    (0.35)
-//   1 x 200,000, 64 / 8                        62.0    (0.53)
-//   32 x 4,095, 2 tokens each, 32 / 8 of 64    33.9    (0.34)
+// one in 730; the same batch read from L2 is as slow, and 8, 12 or 16 warps an SM make no
+// difference.  What does not grow with the tokens -- launches, the chain length, table,
+// rows, the end of the last CTAs and the merge -- is 9 us at 4 rows and 18 at 16.
+//   16 of up to 128, 32 / 8 heads of 128        3.8 us (latency)
+//   8 x 32K, 32 / 8                            54.8    (0.78 of the copy rate)
+//   48 of up to 16K, 64 / 8                    95.4    (0.60)
+//   8 x 32K, 4 tokens each, 32 / 8            117.7    (0.36)
+//   1 x 200,000, 64 / 8                        58.5    (0.56)
+//   32 x 4,095, 2 tokens each, 32 / 8 of 64    30.0    (0.38)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -225,7 +227,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const pkv_cache_desc &c = a.cache;
-    const int group = a.num_q_heads / c.num_kv_heads, rows = group * a.q_tokens;
+    const int group = a.group, rows = group * a.q_tokens;
     const int head = segment().head, b = segment().b, row0 = segment().row0;
     const int begin = segment().begin, end = segment().end;
     // this warp's share, in whole tiles
@@ -682,8 +684,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         if (g == 0) stats[warp * ROWS + row] = some ? from[r] + log2f(l[r]) : kNone;
         // The lane's neighbouring elements of the row, four at a time.  Eight lanes store at
         // once, two of g and four of t: the rows' padding and the odd g's order of fours
-        // put them in banks of their own (stored one by one, as they are, they met 16 to a
-        // bank: 8 x 4096 tokens XX us instead of 18.1).
+        // put them in banks of their own (one at a time they would meet 16 to a bank).
         float4 *o = reinterpret_cast<float4 *>(outs + (warp * ROWS + row) * C::kOutRow) +
                     2 * C::kWordsV * g;
         float y[2 * C::kProducts];
@@ -739,9 +740,11 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     }
 }
 
-// The sequence's length; one that is not valid counts as 0.
+// The sequence's length; one that is not valid counts as 0.  (L2: for reads before the
+// wait for the kernel before, which alone makes an older line of the first cache go.)
+template <bool L2 = false>
 __device__ __forceinline__ int length_of(const Int4DecodeArgs &a, int block_shift, int b) {
-    const int32_t len = a.seq_lens[b];
+    const int32_t len = L2 ? __ldcg(a.seq_lens + b) : a.seq_lens[b];
     return len < 0 || len > (int64_t(a.max_blocks) << block_shift) ? 0 : len;
 }
 __device__ __forceinline__ void check_length(const Int4DecodeArgs &a, int block_shift, int b) {
@@ -790,49 +793,85 @@ decode_int4_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift) {
 //
 // A unit is a (sequence, KV head, tile of rows): n = ceil(length / 128) steps of a CTA's
 // four warps, and kStart more for the start and end of one more piece of work.  The units
-// lie one after another on a line of T = sum (n + kStart); CTA i of C takes [i T / C, (i + 1) T / C) of it, so
-// it meets the end of one unit, perhaps some whole ones, and the beginning of another.
-// A whole unit goes straight to the output; the parts of others go to the workspace
-// (CTA i's at 2 i, or 2 i + 1 if it is the unit's first) and are merged by the next
-// kernel, from a record that the unit's first CTA leaves.  Where all sequences have the
-// same number of steps, C is a multiple of the units if one is near enough, so that no CTA
-// meets two (8 x 32K, 64 units: 448 of 456 CTAs).
+// lie one after another on a line of T = sum (n + kStart); CTA i of C takes
+// [floor(i T / C), floor((i + 1) T / C)) of it, so it meets the end of one unit, perhaps
+// some whole ones, and the beginning of another.  A whole unit goes straight to the
+// output; the parts of others go to the workspace (CTA i's at 2 i, or 2 i + 1 if it is the
+// unit's first) and are merged by the next kernel, which finds them from the lengths by
+// itself.  Where all sequences have the same number of steps, C is a multiple of the units
+// if one is near enough, so that no CTA meets two (8 x 32K, 64 units: 448 of 456 CTAs).
 constexpr int kStep = kWarps * kTile;
-constexpr int kStart = 4;
-constexpr int kMaxPlanned = 2048;          // sequences
-constexpr int kMaxUnits = 65536;
-
-struct Record {                            // of a unit: its parts (0: whole) and their first CTA
-    int32_t parts, first;
-};
-// Where CTA i's share of a line of `total` begins, i <= ctas <= total.
-__device__ __forceinline__ int64_t share_at(int i, int64_t total, int ctas) {
-    int64_t q;
-    int r;
-    if (total <= INT32_MAX) {
-        q = int(total) / ctas;
-        r = int(total) - int(q) * ctas;
-    } else {
-        q = total / ctas;
-        r = int(total - q * ctas);
-    }
-    return i * q + i * r / ctas;           // (ctas^2 is far below 2^31)
-}
-struct Share {                             // a CTA's share of the line, and where it stands
-    int64_t at, to, start, total;          // start: of sequence b
-    int32_t ctas, b, len;
-    int32_t extra;                         // what a unit has on the line beside its steps
-};
+// (1, 2, 3, 4: 48 of up to 16K 105, 97, 97, 98 us; 128 of up to 8K 120, 117, 104, 105)
+constexpr int kStart = 3;
+constexpr int kMaxPlanned = 512;           // sequences
+constexpr int kManyUnits = 3;              // a CTA
 
 __device__ __forceinline__ int steps_of(int len) {
     return int((uint32_t(len) + kStep - 1) / kStep);
 }
 
-// The next part of a unit with something to do (b < 0: none).  Whoever has a unit's
-// beginning writes its record if `writes`.
-__device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int block_shift, int row_tiles,
-                                                int rows, Record *records, Share &share,
-                                                bool writes) {
+// The line, as the lanes of a warp see it: each has the sequences b0 .. b1, the first of
+// which begins at `start`.
+struct Line {
+    int64_t total, start, end;
+    int32_t ctas;                          // that have a share of it
+    int32_t extra;                         // what a unit has on the line beside its steps
+    int32_t b0, b1;
+};
+
+template <bool L2 = false>
+__device__ __forceinline__ Line line_of(const Int4DecodeArgs &a, int block_shift, int heads,
+                                        int ctas, int even) {
+    const int lane = threadIdx.x & 31, per = (a.batch + 31) / 32;
+    Line line;
+    line.b0 = min(lane * per, a.batch);
+    line.b1 = min(line.b0 + per, a.batch);
+    int64_t mine = 0;
+    int least = INT32_MAX, most = 0;
+#pragma unroll 8
+    for (int b = line.b0; b < line.b1; ++b) {
+        const int n = steps_of(length_of<L2>(a, block_shift, b));
+        least = min(least, n);
+        most = max(most, n);
+        mine += n + kStart;
+    }
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+    // (a share that begins with a unit has no more to start than any other; `even` is the
+    // largest multiple of the units within `ctas`)
+    line.extra = least == most && least > 0 && 10 * even >= 9 * ctas ? 0 : kStart;
+    if (line.extra == 0) {
+        mine -= int64_t(kStart) * (line.b1 - line.b0);
+        upto -= int64_t(kStart) * line.b1;
+    }
+    line.total = (all - (line.extra ? 0 : int64_t(kStart) * a.batch)) * heads;
+    // each CTA has a place of the line or more
+    line.ctas = int(min(int64_t(line.extra ? ctas : even), line.total));
+    line.start = (upto - mine) * heads;
+    line.end = upto * heads;
+    return line;
+}
+
+// The CTA whose share has a place of the line: the largest i with i total / ctas < place + 1.
+__device__ __forceinline__ int cta_of(int64_t place, int64_t total, int ctas) {
+    return int(((place + 1) * ctas - 1) / total);
+}
+
+struct Share {                             // a CTA's share of the line, and where it stands
+    int64_t at, to, start;                 // start: of sequence b
+    int32_t b, len, extra;
+};
+
+// The next part of a unit with something to do (b < 0: none).
+__device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int block_shift,
+                                                int row_tiles, int rows, Share &share) {
     const int heads = a.cache.num_kv_heads * row_tiles;     // units of a sequence
     Segment seg = {};
     seg.b = -1;
@@ -845,38 +884,21 @@ __device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int blo
             continue;
         }
         const int unit = in <= INT32_MAX ? int(in) / cost : int(in / cost);
-        const int64_t unit_at = share.start + int64_t(unit) * cost, unit_end = unit_at + cost;
-        const int64_t stop = min(share.to, unit_end);
+        const int64_t unit_at = share.start + int64_t(unit) * cost;
+        const int64_t stop = min(share.to, unit_at + cost);
         const int s0 = max(0, int(share.at - unit_at) - share.extra);
         const int s1 = max(0, int(stop - unit_at) - share.extra);
         const bool empty = n == 0 && share.at == unit_at;
         share.at = stop;
         // (a sequence without tokens: whoever has its first place writes its rows)
         if (s1 > s0 || empty) {
-            const bool whole = s0 == 0 && s1 == n;
-            const int cta = int(blockIdx.x);
             seg.b = share.b;
             seg.head = unit / row_tiles;
             seg.row0 = (unit - seg.head * row_tiles) * rows;
             seg.len = share.len;
             seg.begin = s0 * kStep;
             seg.end = int(min(int64_t(s1) * kStep, int64_t(share.len)));
-            seg.slot = whole ? -1 : 2 * cta + (s0 == 0 ? 1 : 0);
-            if (s0 == 0 && writes) {
-                int parts = 0;
-                if (!whole) {
-                    // the last CTA whose share begins before the unit's end: a guess, put
-                    // right
-                    int last = int(float(unit_end) / float(share.total) * float(share.ctas));
-                    last = max(cta, min(last, share.ctas - 1));
-                    while (last + 1 < share.ctas &&
-                           share_at(last + 1, share.total, share.ctas) < unit_end)
-                        ++last;
-                    while (share_at(last, share.total, share.ctas) >= unit_end) --last;
-                    parts = last - cta + 1;
-                }
-                records[int64_t(share.b) * heads + unit] = {parts, cta};
-            }
+            seg.slot = s0 == 0 && s1 == n ? -1 : 2 * int(blockIdx.x) + (s0 == 0 ? 1 : 0);
             break;
         }
     }
@@ -885,8 +907,8 @@ __device__ __forceinline__ Segment next_segment(const Int4DecodeArgs &a, int blo
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads, Config<D, ROWS>::kCtas)
-decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift, float *parts,
-                           float *part_lse, Record *records) {
+decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift, int even,
+                           float *parts, float *part_lse) {
     extern __shared__ __align__(128) uint8_t smem[];
     // (in shared memory, as the registers belong to the work itself)
     __shared__ Share s_share;
@@ -895,48 +917,27 @@ decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shif
     pdl_wait();
     pdl_launch_dependents();
     {
-        // Each warp by itself, without a barrier: the line's length, and the sequence in
-        // which this CTA's share begins.
+        // Each warp by itself, without a barrier: the sequence in which this CTA's share
+        // begins.
         const int lane = threadIdx.x & 31, heads = a.cache.num_kv_heads * row_tiles;
-        const int per = (a.batch + 31) / 32;
-        const int b0 = min(lane * per, a.batch), b1 = min(b0 + per, a.batch);
-        int64_t mine = 0;
-        int least = INT32_MAX, most = 0;
-        for (int b = b0; b < b1; ++b) {
-            if (blockIdx.x == 0 && threadIdx.x < 32) check_length(a, block_shift, b);
-            const int n = steps_of(length_of(a, block_shift, b));
-            least = min(least, n);
-            most = max(most, n);
-            mine += n + kStart;
-        }
-        int64_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += x;
-        }
-        least = __reduce_min_sync(0xffffffffu, least);
-        most = __reduce_max_sync(0xffffffffu, most);
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b < a.batch; b += kThreads) check_length(a, block_shift, b);
+        const Line line = line_of(a, block_shift, heads, int(gridDim.x), even);
+        if (blockIdx.x >= line.ctas) return;
         Share share;
-        const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
-        const int units = a.batch * heads, ctas = int(gridDim.x), even = ctas / units * units;
-        // (a share that begins with a unit has no more to start than any other)
-        share.extra = least == most && least > 0 && 10 * even >= 9 * ctas ? 0 : kStart;
-        if (share.extra == 0) {
-            mine -= int64_t(kStart) * (b1 - b0);
-            upto -= int64_t(kStart) * b1;
-        }
-        share.total = (all - (share.extra ? 0 : int64_t(kStart) * a.batch)) * heads;
-        // each CTA has a place of the line or more
-        share.ctas = int(min(int64_t(share.extra ? ctas : even), share.total));
-        if (blockIdx.x >= share.ctas) return;
-        share.at = share_at(blockIdx.x, share.total, share.ctas);
-        share.to = share_at(blockIdx.x + 1, share.total, share.ctas);
+        share.extra = line.extra;
+        // floor(i total / ctas) = i q + floor(i r / ctas), and the next (ctas^2 is far below
+        // 2^31)
+        const int cta = int(blockIdx.x), ctas = line.ctas;
+        const int64_t q = line.total <= INT32_MAX ? int(line.total) / ctas : line.total / ctas;
+        const int r = int(line.total - q * ctas), more = cta * r / ctas;
+        share.at = cta * q + more;
+        share.to = share.at + q + (cta * r - more * ctas + r >= ctas ? 1 : 0);
         // the lane whose sequences it begins in
-        share.start = (upto - mine) * heads;
-        share.b = b0;
+        share.start = line.start;
+        share.b = line.b0;
         share.len = 0;
-        const bool here = share.start <= share.at && share.at < upto * heads;
+        const bool here = line.start <= share.at && share.at < line.end;
         if (here)
             for (;; ++share.b) {
                 share.len = length_of(a, block_shift, share.b);
@@ -949,7 +950,7 @@ decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shif
         share.b = __shfl_sync(0xffffffffu, share.b, owner);
         share.len = __shfl_sync(0xffffffffu, share.len, owner);
         if (threadIdx.x < 32) {
-            const Segment seg = next_segment(a, block_shift, row_tiles, ROWS, records, share, lane == 0);
+            const Segment seg = next_segment(a, block_shift, row_tiles, ROWS, share);
             if (lane == 0) {
                 s_seg = seg;
                 s_share = share;
@@ -959,11 +960,11 @@ decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shif
     __syncthreads();
     while (s_seg.b >= 0) {
         attend<D, ROWS>(a, smem, block_shift, parts, part_lse,
-                        [&]() { return Segment(*const_cast<const Segment *>(&s_seg)); });
+                        [&]() { return s_seg; });
         __syncthreads();           // nobody wants the segment any more, and the rings are free
         if (threadIdx.x == 0) {
             Share share = s_share;
-            s_seg = next_segment(a, block_shift, row_tiles, ROWS, records, share, true);
+            s_seg = next_segment(a, block_shift, row_tiles, ROWS, share);
             s_share = share;
         }
         __syncthreads();
@@ -975,33 +976,65 @@ decode_int4_planned_kernel(const Int4DecodeArgs a, int row_tiles, int block_shif
 // its parts in turn.  Many parts (one row a CTA) want groups, few parts rows.
 template <int D, int ROWS, int RB>
 __global__ void __launch_bounds__(kThreads)
-int4_merge_kernel(const Int4DecodeArgs a, int row_tiles, const float *parts, const float *part_lse,
-                  const Record *records) {
+int4_merge_kernel(const Int4DecodeArgs a, int row_tiles, int block_shift, int grid, int even,
+                  const float *parts, const float *part_lse) {
     constexpr int kLanes = D / 4, kGroups = kThreads / RB / kLanes;
     __shared__ float4 s_out[RB][kGroups][kLanes];
     __shared__ float s_top[RB][kGroups], s_sum[RB][kGroups];
-    pdl_wait();
-    pdl_launch_dependents();
-    const Record rec = records[blockIdx.x];
-    if (rec.parts == 0) return;
+    // Which CTAs have the unit's steps.  This goes before the wait: the kernel before this
+    // one lets it begin only after waiting for what came earlier, and does not write lengths.
+    const int heads = a.cache.num_kv_heads * row_tiles;
+    const int b = int(blockIdx.x) / heads, unit = int(blockIdx.x) - b * heads;
+    __shared__ int s_first, s_parts;
+    if (threadIdx.x < 32) {
+        const Line line = line_of<true>(a, block_shift, heads, grid, even);
+        int64_t at = line.start;
+        int steps = 0;
+        if (line.b0 <= b && b < line.b1) {
+#pragma unroll 8
+            for (int i = line.b0; i < b; ++i)
+                at += int64_t(steps_of(length_of<true>(a, block_shift, i)) + line.extra) * heads;
+            steps = steps_of(length_of<true>(a, block_shift, b));
+            at += int64_t(unit) * (steps + line.extra) + line.extra;      // of its first step
+            int first = 0, parts = 0;
+            if (steps) {
+                first = cta_of(at, line.total, line.ctas);
+                parts = cta_of(at + steps - 1, line.total, line.ctas) - first + 1;
+            }
+            s_first = first;
+            s_parts = parts;
+        }
+    }
     const int rb = threadIdx.x / (kThreads / RB), e = threadIdx.x % kLanes;
     const int grp = threadIdx.x % (kThreads / RB) / kLanes;
     const int r = blockIdx.y * RB + rb;                       // of the unit's tile
+    const int group = a.group, head = unit / row_tiles;
+    const int row = (unit - head * row_tiles) * ROWS + r, token = row / group;
+    const int64_t to = (int64_t(b) * a.q_tokens + token) * a.num_q_heads + head * group +
+                       (row - token * group);
+    pdl_wait();
+    pdl_launch_dependents();
+    __syncthreads();
+    const int first = s_first, num_parts = s_parts;
+    if (num_parts < 2) return;                                // (written by the one CTA)
     float top = kNone, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kAhead = 10;
-    for (int p0 = grp; p0 < rec.parts; p0 += kGroups * kAhead) {
+    for (int p0 = grp; p0 < num_parts; p0 += kGroups * kAhead) {
         float z[kAhead];
         float4 x[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int p = p0 + u * kGroups;
-            const int64_t slot = 2 * (int64_t(rec.first) + p) + (p == 0 ? 1 : 0);
-            const bool in = p < rec.parts;
-            z[u] = in ? part_lse[slot * ROWS + r] : kNone;
-            x[u] = in ? reinterpret_cast<const float4 *>(parts + (slot * ROWS + r) * D)[e]
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+            // (past the last part: that one again, without weight -- loads that hang on no
+            // condition go out together)
+            const int p = min(p0 + u * kGroups, num_parts - 1);
+            const int slot = 2 * (first + p) + (p == 0 ? 1 : 0);
+            z[u] = part_lse[slot * ROWS + r];
+            x[u] = reinterpret_cast<const float4 *>(parts)[(slot * ROWS + r) * kLanes + e];
         }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (p0 + u * kGroups >= num_parts) z[u] = kNone;
         float now = top;
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) now = fmaxf(now, z[u]);
@@ -1040,15 +1073,9 @@ int4_merge_kernel(const Int4DecodeArgs a, int row_tiles, const float *parts, con
         top = most;
         sum = all;
     }
-    const int group = a.num_q_heads / a.cache.num_kv_heads;
-    const int head = int(blockIdx.x) / row_tiles % a.cache.num_kv_heads;
-    const int b = int(blockIdx.x) / (row_tiles * a.cache.num_kv_heads);
-    const int row = int(blockIdx.x) % row_tiles * ROWS + r, token = row / group;
     if (token >= a.q_tokens) return;
     const bool some = sum != 0.f;
     const float inv = some ? 1.f / sum : 0.f;
-    const int64_t to = (int64_t(b) * a.q_tokens + token) * a.num_q_heads + head * group +
-                       (row - token * group);
     *reinterpret_cast<float4 *>(a.out_part + to * D + 4 * e) =
         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     if (e == 0) a.lse_part[to] = some ? (top + log2f(sum)) * kLn2 : -INFINITY;
@@ -1093,19 +1120,19 @@ int launch(const Int4DecodeArgs &a, void *workspace) {
                           C::kSmem, a.stream, a, tiles, shift);
     }
     const int ctas = sm_count() * kResident, units = a.batch * a.cache.num_kv_heads * tiles;
+    const int even = ctas / units * units;
     float *parts = static_cast<float *>(workspace);
     float *part_lse = parts + size_t(2) * ctas * ROWS * D;
-    Record *records = reinterpret_cast<Record *>(part_lse + size_t(2) * ctas * ROWS);
-    const int st = launch_pdl(decode_int4_planned_kernel<D, ROWS>, dim3(ctas), dim3(kThreads), C::kSmem,
-                              a.stream, a, tiles, shift, parts, part_lse, records);
+    const int st = launch_pdl(decode_int4_planned_kernel<D, ROWS>, dim3(ctas), dim3(kThreads),
+                              C::kSmem, a.stream, a, tiles, shift, even, parts, part_lse);
     if (st != PKV_OK) return st;
     // more than about nine parts a unit: a row a CTA, its parts in groups
     constexpr int kRows = std::min(ROWS, 512 / D);
     const bool many = ctas > 8 * units;
     return launch_pdl(many ? int4_merge_kernel<D, ROWS, 1> : int4_merge_kernel<D, ROWS, kRows>,
                       dim3(units, many ? ROWS : ROWS / kRows), dim3(kThreads), 0,
-                      a.stream, a, tiles, static_cast<const float *>(parts),
-                      static_cast<const float *>(part_lse), static_cast<const Record *>(records));
+                      a.stream, a, tiles, shift, ctas, even, static_cast<const float *>(parts),
+                      static_cast<const float *>(part_lse));
 }
 
 }  // namespace
@@ -1129,12 +1156,15 @@ size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q
     if (batch > kMaxPlanned) return 0;
     const int64_t ctas = int64_t(sm_count()) * kResident;
     const int64_t units = int64_t(batch) * c.num_kv_heads * row_tiles(c, num_q_heads, q_tokens);
-    // Sequences of a few steps at most: a plan costs more than it evens out (16 of 128 tokens:
-    // 7.7 us against 4.5).  And each unit has a record and a CTA of the merge.
-    if (int64_t(max_blocks) * c.block_size <= 4 * kStep || units > kMaxUnits) return 0;
+    // Where a plan costs more than it evens out, a CTA a unit: sequences of a few steps at
+    // most (16 of up to 128 tokens: 3.8 us, planned 7.7); many units, which even out by
+    // themselves (1,024 of up to 8K tokens 126 us, planned 103; 1,280 of up to 2K 48.7 and
+    // 50.9; 2,048 of up to 2K 69.4 and 82); many sequences, which every CTA adds up (512 of
+    // up to 8K and one KV head 107 us, planned 89; 1,024 of them 172 and 198).
+    const int64_t tokens = int64_t(max_blocks) * c.block_size;
+    if (tokens <= 4 * kStep || units > kManyUnits * ctas) return 0;
     const int rows = tile_rows(num_q_heads / c.num_kv_heads * q_tokens);
-    return size_t(ctas) * 2 * rows * (c.head_dim_v + 1) * sizeof(float) +
-           size_t(units) * sizeof(Record);
+    return size_t(ctas) * 2 * rows * (c.head_dim_v + 1) * sizeof(float);
 }
 
 int launch_decode_int4(const Int4DecodeArgs &a, void *workspace) {

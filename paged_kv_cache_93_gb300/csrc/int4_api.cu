@@ -89,6 +89,7 @@ Int4DecodeArgs args_of(const pkv_cache_desc *c, const float *q, int32_t batch, i
     a.batch = batch;
     a.q_tokens = tokens;
     a.num_q_heads = hq;
+    a.group = hq / c->num_kv_heads;
     a.k_pool = static_cast<const uint8_t *>(k_pool);
     a.v_pool = static_cast<const uint8_t *>(v_pool);
     a.k_params = static_cast<const uint32_t *>(k_params);

@@ -198,7 +198,7 @@ int validate_int4_cache(const pkv_cache_desc *c);
 struct Int4DecodeArgs {
     pkv_cache_desc cache;
     const float *q;                       // [batch][q_tokens][Hq][Dk]
-    int32_t batch, q_tokens, num_q_heads;
+    int32_t batch, q_tokens, num_q_heads, group;   // group: query heads a KV head
     const uint8_t *k_pool, *v_pool;
     const uint32_t *k_params, *v_params;  // bf16 pairs: scale in bits 0-15, offset in 16-31
     const int32_t *block_tables;

@@ -320,11 +320,12 @@ def test_long_sums_keep_their_precision(pkv, G, T, kw):
     assert float((out - ro).norm() / ro.norm()) < 1e-5
 
 
-@pytest.mark.parametrize("B,plan", [(700, True), (2100, False)])
-def test_thousands_of_pairs(pkv, B, plan):
+@pytest.mark.parametrize("B,Hk,plan", [(160, 8, True), (500, 1, True), (700, 1, False),
+                                         (700, 8, False)])
+def test_many_pairs(pkv, B, Hk, plan):
     lens = [3 + i % 60 for i in range(B)]
     lens[B // 2] = 700
-    c = _int4.make(22, lens, 8, 8, 64, 64, 8, width=90)
+    c = _int4.make(22, lens, 8, Hk, 64, 64, 8, width=90)
     assert (pkv.decode_workspace_size_int4(*c.pools(), B, 8, 90) > 0) == plan
     _int4.close(*decode(pkv, c), _int4.attend(c))
 
