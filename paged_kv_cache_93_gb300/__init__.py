@@ -725,9 +725,9 @@ def paged_decode_attn_int4(q, k_pool, k_params, v_pool, v_params, block_tables, 
                            lse=None, flags: int = 0, stream=None):
     """Decode attention of q [B, Hq, Dk] over a 4-bit cache -> (out, lse); num_splits 0
     lets the library choose."""
-    return _attn_int4("pkv_paged_decode_attn_int4", lib.pkv_paged_decode_attn_int4, q, k_pool, k_params, v_pool, v_params,
-                      block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
-                      stream, False)
+    return _attn_int4("pkv_paged_decode_attn_int4", lib.pkv_paged_decode_attn_int4, q, k_pool,
+                      k_params, v_pool, v_params, block_tables, seq_lens, scale, num_splits,
+                      workspace, out, lse, flags, stream, False)
 
 
 def paged_decode_attn_multi_int4(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
@@ -735,9 +735,9 @@ def paged_decode_attn_multi_int4(q, k_pool, k_params, v_pool, v_params, block_ta
                                  lse=None, flags: int = 0, stream=None):
     """The multi-token step (q [B, T, Hq, Dk], causal over the last T tokens) over a
     4-bit cache -> (out [B, T, Hq, Dv], lse [B, T, Hq])."""
-    return _attn_int4("pkv_paged_decode_attn_multi_int4", lib.pkv_paged_decode_attn_multi_int4, q, k_pool, k_params, v_pool, v_params,
-                      block_tables, seq_lens, scale, num_splits, workspace, out, lse, flags,
-                      stream, True)
+    return _attn_int4("pkv_paged_decode_attn_multi_int4", lib.pkv_paged_decode_attn_multi_int4,
+                      q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
+                      num_splits, workspace, out, lse, flags, stream, True)
 
 
 def paged_decode_attn_partial_int4(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,

@@ -136,7 +136,8 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&x)[N]) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(a) : "memory");
     else if constexpr (N == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(x[0]), "=r"(x[1]) : "r"(a) : "memory");
     else
         x[0] = lds32(a);
 }
@@ -307,8 +308,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             cp_async_16(to, k_lane + uint64_t(at) * C::kRowBytes);
             cp_async_16(to + kTile * C::kRowBytes, v_lane + uint64_t(at) * C::kRowBytes);
         }
-        const uint32_t at = __shfl_sync(0xffffffffu, here, block + (my_four >> block_shift)) + inner +
-                            (my_four & block_mask);
+        const uint32_t at = __shfl_sync(0xffffffffu, here, block + (my_four >> block_shift)) +
+                            inner + (my_four & block_mask);
         if (lane < 16) cp_async_16(fill + 2 * kTile * C::kRowBytes + lane * 16, p_lane + at);
         fill += C::kStageBytes;
         if (fill == ring + C::kWarpBytes) fill = ring;
@@ -547,7 +548,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         bool move = i == 0;
         if (!move) {
             scores(from);
-            move = __any_sync(0xffffffffu, tail ? weigh(std::true_type{}) : weigh(std::false_type{}));
+            const bool leaves = tail ? weigh(std::true_type{}) : weigh(std::false_type{});
+            move = __any_sync(0xffffffffu, leaves);
         }
         if (move) {
             float by[C::kLaneRows];
@@ -561,12 +563,13 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                 for (int k = 0; k < 4; ++k) {
                     const float vs = fabsf(bf16_lo_to_f32(lds32(params + (kTile + 8 * k) * 4)));
                     y = fmaxf(y, x[r][k]);
-                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f) w = fmaxf(w, x[r][k] + __log2f(vs));
+                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f)
+                        w = fmaxf(w, x[r][k] + __log2f(vs));
                 }
                 top[r] = fmaxf(top[r], group_max(y));
                 heaviest[r] = fmaxf(heaviest[r], group_max(w));
-                const float now =
-                    fmaxf(from[r], fminf(fmaxf(heaviest[r] - 10.f, top[r] - 100.f), top[r] + 100.f));
+                const float want = fmaxf(heaviest[r] - 10.f, top[r] - 100.f);
+                const float now = fmaxf(from[r], fminf(want, top[r] + 100.f));
                 by[r] = ex2_approx(from[r] - now);
                 from[r] = now;
                 l[r] *= by[r];
@@ -718,7 +721,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         for (int w = 0; w < kWarps; ++w) {
             const float z = stats[w * ROWS + r];
             const float by = z == kNone ? 0.f : ex2_approx(z - most);
-            const float4 y = *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * C::kOutRow + e);
+            const float4 y =
+                *reinterpret_cast<const float4 *>(outs + (w * ROWS + r) * C::kOutRow + e);
             all += by;
             o.x = fmaf(by, y.x, o.x); o.y = fmaf(by, y.y, o.y);
             o.z = fmaf(by, y.z, o.z); o.w = fmaf(by, y.w, o.w);
@@ -759,7 +763,8 @@ __device__ __forceinline__ void prefetch_tables(const Int4DecodeArgs &a) {
     const int64_t at = (blockIdx.x * int64_t(kThreads) + threadIdx.x) * 128;
     const int64_t lens = int64_t(a.batch) * 4, tables = lens * a.max_blocks;
     if (at < lens)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.seq_lens) + at));
+        asm volatile("prefetch.global.L2 [%0];"
+                     ::"l"(reinterpret_cast<const char *>(a.seq_lens) + at));
     if (at < tables)
         asm volatile("prefetch.global.L2 [%0];"
                      ::"l"(reinterpret_cast<const char *>(a.block_tables) + at));

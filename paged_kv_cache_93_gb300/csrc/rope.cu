@@ -156,7 +156,8 @@ rope_append_kernel(const RopeArgs a) {
         for (int i = 0; i < kMaxPairs / kThreads; ++i) {
             const int pr = threadIdx.x + i * kThreads;
             if (pr < npairs) {
-                const uint64_t turn = step[i] * uint64_t(AXES ? a.positions[axis[i] * a.num_tokens + t] : pos);
+                const int64_t p = AXES ? a.positions[axis[i] * a.num_tokens + t] : pos;
+                const uint64_t turn = step[i] * uint64_t(p);
                 // signed 2^-32 turns; sincospif takes half turns
                 const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
                 float s, c;
@@ -461,7 +462,8 @@ rope_append_wide_kernel(const RopeArgs a) {
         }
         for (int i = threadIdx.x; i < ntok * npairs; i += kThreads) {
             const int tk = a.group > 1 ? i / npairs : 0, pr = i - tk * npairs;
-            const uint64_t turn = step[pr] * uint64_t(a.positions[(AXES ? axis[pr] * a.num_tokens : 0) + t0 + tk]);
+            const int64_t row = AXES ? axis[pr] * a.num_tokens : 0;
+            const uint64_t turn = step[pr] * uint64_t(a.positions[row + t0 + tk]);
             // signed 2^-32 turns; sincospif takes half turns
             const float x = float(int32_t(turn >> 32)) * 4.656612873077393e-10f;
             float s, co;
@@ -574,7 +576,8 @@ rope_append_warp_kernel(const RopeArgs a) {
             float c2[2], s2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint64_t turn = step[i] * uint64_t(AXES ? a.positions[axis[i] * a.num_tokens + t] : pos);
+                const int64_t p = AXES ? a.positions[axis[i] * a.num_tokens + t] : pos;
+                const uint64_t turn = step[i] * uint64_t(p);
                 // signed 2^-32 turns; sincospif takes half turns
                 sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f, &s2[i], &c2[i]);
                 c2[i] *= a.amplitude;
@@ -657,7 +660,8 @@ rope_append_warp_kernel(const RopeArgs a) {
                 to[(is_k ? ea : 16 * c) / 8] = int4_codes8(x, sc);
                 to[(is_k ? eb : 16 * c + 8) / 8] = int4_codes8(y, sc);
                 if (c == 0)
-                    (is_k ? a.k_params : a.v_params)[row0 + int64_t(row) * a.block_size] = sc.params;
+                    (is_k ? a.k_params : a.v_params)[row0 + int64_t(row) * a.block_size] =
+                        sc.params;
             } else {
                 const float s = (is_k ? a.k_scale : a.v_scale)[row];
                 store8_e4m3(is_k ? a.k_pool : a.v_pool, dst + (is_k ? ea : 16 * c), x, s);
@@ -892,8 +896,9 @@ int launch(RopeArgs &a, bool interleaved, cudaStream_t stream) {
 // scales and the status word.  *done: nothing to launch.
 int prepare(RopeArgs &a, int fmt, const pkv_cache_desc *c, const void *q, int32_t hq,
             const void *k_new, const void *v_new, const int64_t *positions, int32_t num_axes,
-            const int32_t *pair_axis, const int64_t *slots, int64_t num_tokens, const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset,
-            float amplitude, int32_t flags, void *k_pool, void *v_pool, void *q_out, bool *done) {
+            const int32_t *pair_axis, const int64_t *slots, int64_t num_tokens,
+            const double *inv_freq, int32_t rotary_dim, int32_t rotary_offset, float amplitude,
+            int32_t flags, void *k_pool, void *v_pool, void *q_out, bool *done) {
     *done = false;
     const bool e4 = fmt == kE4m3;
     if (num_axes < 1 || num_axes > 8 || (num_axes > 1 && !pair_axis)) return PKV_ERR_INVALID_ARG;

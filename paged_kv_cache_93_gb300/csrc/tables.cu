@@ -112,8 +112,10 @@ __device__ __forceinline__ int32_t ceil_div(int32_t x, int32_t n) {
 __device__ __forceinline__ void prefetch_lengths(const TablesArgs &a) {
     const int64_t at = threadIdx.x * 128, bytes = int64_t(a.batch) * 4;
     if (blockIdx.x == 0 && at < bytes) {
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.lens) + at));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.change) + at));
+        asm volatile("prefetch.global.L2 [%0];"
+                     ::"l"(reinterpret_cast<const char *>(a.lens) + at));
+        asm volatile("prefetch.global.L2 [%0];"
+                     ::"l"(reinterpret_cast<const char *>(a.change) + at));
     }
 }
 
@@ -213,7 +215,8 @@ __global__ void __launch_bounds__(kThreads) extend_kernel(const TablesArgs a) {
             else slot[i] = int64_t(phys) * a.block_size + (p - lb * a.block_size);
         }
         if (r0 + 1 < a.rows) {
-            *reinterpret_cast<longlong2 *>(a.positions + r0) = make_longlong2(position[0], position[1]);
+            *reinterpret_cast<longlong2 *>(a.positions + r0) =
+                make_longlong2(position[0], position[1]);
             *reinterpret_cast<longlong2 *>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
         } else {
             a.positions[r0] = position[0];
