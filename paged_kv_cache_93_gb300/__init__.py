@@ -17,6 +17,7 @@ to a byte, in uint8 pools [num_blocks, Hkv, block_size, D / 2] and a bf16
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 import torch
@@ -24,8 +25,8 @@ import torch
 from . import _lib
 from ._lib import (DECODE_GENERIC, DECODE_NO_TCGEN05, DECODE_TEST_WITHHOLD, DEV_BLOCK_ID,
                    DEV_COPY_CONFLICT, DEV_PREFIX, DEV_SEQ_LEN, DEV_SLOT, DEV_TABLE_RANGE,
-                   DEV_AXIS, DEV_NO_BLOCKS, DEV_QUERY_RANGE, DEV_TIMEOUT, ROPE_INTERLEAVED, ROPE_Q_FP32, CacheDesc,
-                   PkvError)
+                   DEV_AXIS, DEV_NO_BLOCKS, DEV_QUERY_RANGE, DEV_TIMEOUT, ROPE_INTERLEAVED,
+                   ROPE_Q_FP32, CacheDesc, PkvError)
 
 __all__ = [
     "CacheDesc", "PkvError", "ValuesInKeys", "cache_desc", "kv_append", "slot_mapping", "copy_blocks",
@@ -61,6 +62,7 @@ def _ptr(t: torch.Tensor | None):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream=None):
@@ -69,7 +71,15 @@ def _stream(stream=None):
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
     # the current stream's handle, without the Stream object around it
-    return _raw_stream(torch.cuda.current_device())
+    device = _device()
+    return _raw_stream(torch.cuda.current_device() if device < 0 else device)
+
+
+def _device() -> int:
+    """The current device; -1 where CUDA has not been used yet."""
+    if not torch.cuda.is_initialized():
+        return -1
+    return _get_device() if _get_device else torch.cuda.current_device()
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dim: int | None = None):
@@ -337,18 +347,24 @@ def cache_desc_int4(k_pool, k_params, v_pool, v_params) -> CacheDesc:
     and bf16 params [num_blocks, Hkv, block_size, 2] (scale, offset)."""
     if isinstance(v_pool, ValuesInKeys):
         raise ValueError("values inside the keys need a bf16 cache")
-    _need(k_pool, "k_pool", torch.uint8, 4)
-    _need(k_params, "k_params", torch.bfloat16, 4)
-    _need(v_pool, "v_pool", torch.uint8, 4)
-    _need(v_params, "v_params", torch.bfloat16, 4)
-    nb, hkv, bs, half_k = k_pool.shape
-    half_v = v_pool.shape[3]
-    if v_pool.shape != (nb, hkv, bs, half_v):
+    shape, shape_v = k_pool.shape, v_pool.shape
+    params, params_v = k_params.shape, v_params.shape
+    # (a call's latency is mostly this: each question once, the answers in one line)
+    if not (k_pool.dtype is v_pool.dtype is torch.uint8 and len(shape) == len(shape_v) == 4
+            and k_params.dtype is v_params.dtype is torch.bfloat16 and len(params) == 4
+            and k_pool.is_cuda and v_pool.is_cuda and k_params.is_cuda and v_params.is_cuda
+            and k_pool.is_contiguous() and v_pool.is_contiguous()
+            and k_params.is_contiguous() and v_params.is_contiguous()):
+        _need(k_pool, "k_pool", torch.uint8, 4)
+        _need(k_params, "k_params", torch.bfloat16, 4)
+        _need(v_pool, "v_pool", torch.uint8, 4)
+        _need(v_params, "v_params", torch.bfloat16, 4)
+    nb, hkv, bs, half_k = shape
+    if shape_v[:3] != shape[:3]:
         raise ValueError("k_pool and v_pool disagree on [num_blocks, Hkv, block_size]")
-    params = (nb, hkv, bs, 2)
-    if k_params.shape != params or v_params.shape != params:
+    if params != params_v or params[:3] != shape[:3] or params[3] != 2:
         raise ValueError("k_params and v_params must be [num_blocks, Hkv, block_size, 2]")
-    return CacheDesc(nb, bs, hkv, 2 * half_k, 2 * half_v)
+    return CacheDesc(nb, bs, hkv, 2 * half_k, 2 * shape_v[3])
 
 
 def kv_append_int4(k_pool, k_params, v_pool, v_params, k_new, v_new, slots, stream=None) -> None:
@@ -679,12 +695,20 @@ def decode_workspace_size_int4(k_pool, k_params, v_pool, v_params, batch: int, n
                                                   int(flags)))
 
 
+@functools.lru_cache(maxsize=256)
+def _int4_workspace(nb, bs, hkv, dk, dv, B, T, Hq, mb, S, flags, device) -> int:
+    # (sizes in, a size out: the device counts, as the plan is for its SMs)
+    return lib.pkv_decode_workspace_size_int4(ctypes.byref(CacheDesc(nb, bs, hkv, dk, dv)), B, T,
+                                              Hq, mb, S, flags)
+
+
 def _attn_int4(name, call, q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens, scale,
                num_splits, workspace, out, lse, flags, stream, multi):
     desc, B, T, Hq = _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
                                 multi)
     ref, mb, S, flags = ctypes.byref(desc), block_tables.shape[1], _int32(num_splits), int(flags)
-    need = lib.pkv_decode_workspace_size_int4(ref, B, T, Hq, mb, S, flags)
+    need = _int4_workspace(desc.num_blocks, desc.block_size, desc.num_kv_heads, desc.head_dim_k,
+                           desc.head_dim_v, B, T, Hq, mb, S, flags, _device())
     ws_bytes = 0
     if workspace is not None:
         _need(workspace, "workspace", workspace.dtype)
