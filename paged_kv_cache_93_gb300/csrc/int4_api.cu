@@ -37,10 +37,9 @@ Plan plan_of(const pkv_cache_desc &c, int32_t batch, int32_t tokens, int32_t hq,
         S = 1;
     }
     if (S == 0) {
-        // Enough (row, split) items for the device, of sequences as long as their table
-        // rows 512 tokens each.
-        const int64_t units = std::max<int64_t>(1, int64_t(batch) * tokens * ((hq + 3) / 4));
-        const int64_t want = (int64_t(sm_count()) * 8 + units - 1) / units;
+        // Eight CTAs an SM, of sequences as long as their table rows 512 tokens each.
+        const int64_t ctas = std::max<int64_t>(1, int4_generic_ctas(c, batch, hq, tokens));
+        const int64_t want = (int64_t(sm_count()) * 8 + ctas - 1) / ctas;
         const int64_t most = (int64_t(max_blocks) * c.block_size + 511) / 512;
         S = int32_t(std::max<int64_t>(1, std::min<int64_t>({want, most, 64})));
     }

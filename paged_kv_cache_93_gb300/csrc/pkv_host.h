@@ -213,6 +213,9 @@ struct Int4DecodeArgs {
     cudaStream_t stream;
 };
 int launch_decode_int4_generic(const Int4DecodeArgs &a);
+// Its CTAs for one split.
+int64_t int4_generic_ctas(const pkv_cache_desc &c, int32_t batch, int32_t num_q_heads,
+                          int32_t q_tokens);
 // The tensor-core form and its shapes.  num_splits > 0: the partials of that many chunks, as
 // above; 0: the library's own plan, the whole result to out_part / lse_part, with a
 // workspace of int4_plan_workspace bytes (0: the shape has no plan).
