@@ -369,3 +369,53 @@ def test_far_blocks(pkv):
         assert same_bits(v[slot // bs, :, slot % bs].cpu(), codes[t])
         assert same_bits(vp[slot // bs, :, slot % bs].cpu(), params[t])
     assert pkv.device_status() == 0
+
+
+# lens, hq, hkv, dk, dv, bs, tokens: rows of one to four words a lane, of 8, 16 and 32 lanes;
+# one to nine query heads a KV head
+@pytest.mark.parametrize("lens,hq,hkv,dk,dv,bs,T", [
+    ([0, 1, 2, 31], 3, 3, 32, 32, 1, 1), ([65, 64, 200], 10, 2, 64, 32, 5, 1),
+    ([3, 129, 17], 9, 3, 96, 128, 24, 3), ([300, 7], 9, 1, 160, 64, 256, 1),
+    ([33, 5, 400], 4, 2, 224, 256, 16, 2), ([70, 130], 6, 2, 288, 96, 32, 1),
+    ([40, 1, 0, 90], 2, 2, 512, 544, 16, 4), ([150], 7, 1, 1024, 32, 16, 1),
+    ([1, 640, 63], 14, 2, 128, 128, 16, 5), ([500, 12], 8, 8, 64, 64, 8, 1)])
+@pytest.mark.parametrize("splits", [0, 1, 5])
+def test_cuda_core_shapes(pkv, lens, hq, hkv, dk, dv, bs, T, splits):
+    c = _int4.make(31 + hq + T, lens, hq, hkv, dk, dv, bs, T)
+    got = decode(pkv, c, num_splits=splits, flags=pkv.DECODE_GENERIC)
+    _int4.close(*got, _int4.attend(c))
+    pkv.device_status()
+
+
+def test_lengths_written_just_before(pkv):
+    """Steps that follow one another without a pause, their lengths written by the kernel
+    before (a copy; an extend): the plan and the merge both go by the new ones."""
+    c = _int4.make(41, [2500, 700, 1300, 3000, 90], 8, 2, 128, 128, 16, width=190)
+    args = (c.q[:, 0].contiguous().cuda(), *c.pools(), c.tables.cuda())
+    sets = [c.lens.cuda(), torch.tensor([40, 700, 1100, 129, 90], dtype=torch.int32).cuda(),
+            torch.tensor([2500, 0, 1, 2999, 60], dtype=torch.int32).cuda()]
+    want = []
+    for lens in sets:
+        want.append(pkv.paged_decode_attn_int4(*args, lens, c.scale))
+        torch.cuda.synchronize()
+    now, got = sets[0].clone(), []
+    for i in range(60):
+        now.copy_(sets[i % 3])
+        got.append(pkv.paged_decode_attn_int4(*args, now, c.scale))
+    for i, (out, lse) in enumerate(got):
+        assert torch.equal(out, want[i % 3][0]) and torch.equal(lse, want[i % 3][1])
+    # the tables hold more blocks than the lengths need: an extend within them takes none
+    tables, lens = args[-1].clone(), sets[1].clone()
+    free, state = pkv.block_pool(c.k.shape[0], args[0].device)
+    state[0] = 0
+    one = torch.tensor([1, 0, 1, 0, 1], dtype=torch.int32, device="cuda")
+    lens.copy_(torch.tensor([33, 700, 1090, 129, 81], dtype=torch.int32))
+    got = []
+    for i in range(5):
+        pkv.extend_sequences(tables, lens, one, free, state, 16, 8)
+        got.append(pkv.paged_decode_attn_int4(*args, lens, c.scale))
+    for i in range(5):
+        at = torch.tensor([34 + i, 700, 1091 + i, 129, 82 + i], dtype=torch.int32, device="cuda")
+        out, lse = pkv.paged_decode_attn_int4(*args, at, c.scale)
+        assert torch.equal(out, got[i][0]) and torch.equal(lse, got[i][1])
+    assert pkv.device_status() == 0
