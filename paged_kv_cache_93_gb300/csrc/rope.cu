@@ -679,10 +679,13 @@ rope_append_warp_kernel(const RopeArgs a) {
 }
 
 // The form of the 4-bit pools' other shapes: a CTA a token, a warp a row, which stays in
-// the warp's registers because its scale needs all of it (a lane holds up to four
-// vectors of 8 elements).  A rotary element loads its pair's other element by itself,
-// so that any rotary part runs; that load hits the cache.
-template <bool INTER>
+// the warp's registers because its scale needs all of it (a lane holds C vectors of 8
+// elements: one up to 256 of them, which leaves registers for more CTAs, otherwise four).  VEC: vectors are rotated whole or not at all, with their pairs'
+// vector (half layout) loaded beside them; otherwise each rotary element loads its pair's
+// other element by itself, so that any rotary part runs.  Both loads hit the cache.
+// Bound: latency and instructions (4,999 tokens, 32 + 8 heads: of 96 61 us, of 128 with 72
+// rotary elements, one by one, 146; four vectors a lane for all 246 and 280).
+template <bool INTER, bool VEC, int C>
 __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeArgs a) {
     __shared__ float2 cs[2][kMaxPairs];          // (cos, sin) * amplitude, by token parity
     const int npairs = a.rot >> 1, lane = threadIdx.x & 31;
@@ -726,17 +729,39 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
             const uint16_t *src = is_q   ? a.q + (t * a.hq + g) * a.dk
                                   : is_k ? a.k_new + (t * a.hkv + g) * a.dk
                                          : a.v_new + (t * a.hkv + g) * a.dv;
-            uint4 raw[4];
-            float x[4][8];
-            bool turned[4];
+            uint4 raw[C];
+            float x[C][8];
+            bool turned[C];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < C; ++n) {
                 const int e0 = (lane + 32 * n) * 8;
                 turned[n] = false;
                 if (e0 >= d) continue;
                 raw[n] = *reinterpret_cast<const uint4 *>(src + e0);
                 unpack8(raw[n], x[n]);
                 if (!is_q && !is_k) continue;
+                if constexpr (VEC) {
+                    const int rel = e0 - a.off;
+                    if (rel < 0 || rel >= a.rot) continue;
+                    turned[n] = true;
+                    const bool first = rel < npairs;
+                    float y[8];
+                    if constexpr (INTER) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = x[n][i ^ 1];
+                    } else {
+                        unpack8(*reinterpret_cast<const uint4 *>(src + e0 +
+                                                                 (first ? npairs : -npairs)), y);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 r =
+                            tab[INTER ? (rel + i) >> 1 : first ? rel + i : rel + i - npairs];
+                        const bool lead = INTER ? (i & 1) == 0 : first;
+                        x[n][i] = x[n][i] * r.x + (lead ? -y[i] : y[i]) * r.y;
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int rel = e0 + i - a.off;
@@ -752,7 +777,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
             __syncwarp();                        // q_out may be q: all of the row is read
             if (is_q) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < C; ++n) {
                     const int e0 = (lane + 32 * n) * 8;
                     if (e0 >= d) continue;
                     const int64_t at = (t * a.hq + g) * a.dk + e0;
@@ -782,14 +807,14 @@ __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeAr
             }
             float low = INFINITY, high = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < C; ++n)
                 if ((lane + 32 * n) * 8 < d) int4_extent8(x[n], low, high);
             const Int4Scale sc = int4_row_scale(low, high, 32, 0xffffffffu);
             const int64_t to = row0 + int64_t(g) * a.block_size;
             uint32_t *codes = reinterpret_cast<uint32_t *>(
                 static_cast<uint8_t *>(is_k ? a.k_pool : a.v_pool) + to * (d / 2));
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < C; ++n)
                 if ((lane + 32 * n) * 8 < d) codes[lane + 32 * n] = int4_codes8(x[n], sc);
             if (lane == 0) (is_k ? a.k_params : a.v_params)[to] = sc.params;
         }
@@ -841,8 +866,18 @@ int launch_int4(RopeArgs &a, bool interleaved, cudaStream_t stream) {
         return launch_warp<kInt4>(a, interleaved, stream);
     }
     const dim3 grid(unsigned(std::min<int64_t>(a.num_tokens, int64_t(sm_count()) * 4)));
-    return launch_pdl(interleaved ? rope_append_int4_kernel<true> : rope_append_int4_kernel<false>,
-                      grid, dim3(kThreads), 0, stream, a);
+    const bool vec = interleaved ? (a.rot % 8 == 0 && a.off % 8 == 0)
+                                 : (a.rot % 16 == 0 && a.off % 8 == 0);
+    auto of = [&](auto count) {
+        constexpr int C = decltype(count)::value;
+        return interleaved ? (vec ? rope_append_int4_kernel<true, true, C>
+                                  : rope_append_int4_kernel<true, false, C>)
+                           : (vec ? rope_append_int4_kernel<false, true, C>
+                                  : rope_append_int4_kernel<false, false, C>);
+    };
+    auto kernel = std::max(a.dk, a.dv) <= 256 ? of(std::integral_constant<int, 1>{})
+                                              : of(std::integral_constant<int, 4>{});
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, a);
 }
 
 template <bool E4>
