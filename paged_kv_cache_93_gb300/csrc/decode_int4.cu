@@ -51,11 +51,11 @@
 // difference.  What does not grow with the tokens -- launches, the chain length, table,
 // rows, the end of the last CTAs and the merge -- is 9 us at 4 rows and 18 at 16.
 //   16 of up to 128, 32 / 8 heads of 128        3.8 us (latency)
-//   8 x 32K, 32 / 8                            54.8    (0.78 of the copy rate)
-//   48 of up to 16K, 64 / 8                    95.4    (0.60)
-//   8 x 32K, 4 tokens each, 32 / 8            117.7    (0.36)
-//   1 x 200,000, 64 / 8                        58.5    (0.56)
-//   32 x 4,095, 2 tokens each, 32 / 8 of 64    30.0    (0.38)
+//   8 x 32K, 32 / 8                            55.6    (0.77 of the copy rate)
+//   48 of up to 16K, 64 / 8                    96.6    (0.59)
+//   8 x 32K, 4 tokens each, 32 / 8            118.8    (0.36)
+//   1 x 200,000, 64 / 8                        59.0    (0.55)
+//   32 x 4,095, 2 tokens each, 32 / 8 of 64    30.5    (0.38)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -94,16 +94,15 @@ struct Config {
     static constexpr int kCtas = kResident;
     static constexpr int kStages = D == 128 ? 3 : 4;  // (one more or less changes 2%)
     // The scores' sums of the two terms apart, where registers allow: fewer cut-offs on the
-    // large one (16 rows of 128, error of small cases: 2e-6 instead of 1e-6, but 124 us
-    // instead of 130 for 8 x 32K and 4 tokens a sequence).
+    // large one (16 rows of 128: none, as it takes 5% more time at 4 tokens a sequence).
     static constexpr int kChains = kPacked || (ROWS == 16 && D == 128) ? 1 : 2;
     // The query's fragments (the same for all the CTA's warps) in shared memory where the
     // registers hold more sums (8 rows of 128: 102 us against 105 for the ragged batch).
     static constexpr bool kSharedQuery = ROWS == 16 || (ROWS == 8 && D == 128);
     static_assert(!kSharedQuery || !kPacked, "a packed query is held by its lanes");
-    // the query's fragments, and each row's two factors
+    // the query's fragments, each row's two factors, and what its scores' sums begin with
     static constexpr int kFragments = kWordsK * kCols * kTerms * 512;
-    static constexpr int kQueryBytes = kFragments + ROWS * 8;
+    static constexpr int kQueryBytes = kFragments + ROWS * 12;
     static constexpr int kStageBytes = 2 * kTile * (kRowBytes + 4);
     static constexpr int kWarpBytes = kStages * kStageBytes;
     static constexpr int kRings = kWarps * kWarpBytes;
@@ -147,6 +146,9 @@ __device__ __forceinline__ void sts_words(uint32_t a, const uint32_t (&x)[4]) {
 }
 __device__ __forceinline__ void sts_pair(uint32_t a, float x, float y) {
     asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 __device__ __forceinline__ void lds_pair(uint32_t a, float &x, float &y) {
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x), "=f"(y) : "r"(a) : "memory");
@@ -360,10 +362,15 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                             (4 * column + piece / C::kWordsK) * 16;
         sts_words(to, top);
         sts_words(to + (C::kPacked ? 64 : 512), low);
-        // score = s (sum of products) * factor + o * offset_factor, in base-2 units
-        if (piece == 0)
+        // score = s (sum of products) * factor + o * offset_factor, in base-2 units; the
+        // sum over the codes less 4, so that it passes through zero on its way: what products
+        // cut off goes by the sum's size (errors 6% smaller over 45 shapes, in the larger ones
+        // by up to a third, for 1% of the time)
+        if (piece == 0) {
             sts_pair(query + C::kFragments + r * 8, a.scale * kLog2e * pow2(e - 12) * kUp,
                      a.scale * kLog2e * sum);
+            sts32(query + C::kFragments + ROWS * 8 + r * 4, -4.f / kUp * up * sum);
+        }
     }
     __syncthreads();
     // lane (g, t) has the scores of row t, or of rows 2 t, 2 t + 1
@@ -429,12 +436,22 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         uint32_t kw[4][C::kWordsK];
 #pragma unroll
         for (int k = 0; k < 4; ++k) lds_words(stage + my_k + 8 * k * C::kRowBytes, kw[k]);
+        float start[C::kLaneRows];
+#pragma unroll
+        for (int r = 0; r < C::kLaneRows; ++r) {
+            const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
+            start[r] = __uint_as_float(lds32(query + C::kFragments + ROWS * 8 + row * 4));
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < C::kCols; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[h][n][e] = low[h][n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    low[h][n][e] = 0.f;
+                    if constexpr (C::kPacked) s[h][n][e] = e & 1 ? 0.f : start[0];
+                    else s[h][n][e] = start[2 * n + (e & 1)];
+                }
 #pragma unroll
         for (int w = 0; w < C::kWordsK; ++w) {
             uint32_t q[C::kCols][C::kTerms][4];
@@ -492,7 +509,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t kp = lds32(params + 32 * k);
-                const float ks = bf16_lo_to_f32(kp), ko = bf16_hi_to_f32(kp);
+                const float ks = bf16_lo_to_f32(kp), ko = fmaf(ks, 4.f, bf16_hi_to_f32(kp));
 #pragma unroll
                 for (int r = 0; r < C::kLaneRows; ++r) {
                     const float (&z)[4] = s[k >> 1][r >> 1];
