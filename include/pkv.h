@@ -643,8 +643,8 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
  * _partial_int4: the per-chunk partials (pkv_paged_decode_attn_partial).
  * A token that a row does not see reaches nothing of it, whatever its bits;
  * one that it sees and that reads as NaN makes the row NaN.  Scales of
- * magnitude below 2^-100 count as rounded to multiples of about 2^-125, and
- * those above 2^100 may overflow the sums.
+ * magnitude below 2^-100 count as rounded to multiples of about 2^-125;
+ * scales and offsets above 2^100 may overflow the sums.
  * num_splits = S > 0: S chunks of every sequence, merged; 0: the library's own
  * plan, which shares the tokens of all sequences evenly among the CTAs that
  * the device holds, from the lengths themselves.  Where that is not worth it

@@ -401,10 +401,14 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     // A row's running state, in base-2 units.  A token of score y has p = 2^(y - from);
     // l and off are the sums of p and of p o' (each lane its own tokens').  `from` is not
     // the largest score: it is moved so that the largest weight p s' lies between 1 and
-    // 2^15, which the weights' fp16 terms need, and p stays within 2^110.  It moves when a
-    // weight or a p would leave that (`heaviest` and `top`: the largest y + log2 s' and y
-    // that were met then), in the first tile and seldom after it, so that the common tile
-    // needs no maximum over lanes.
+    // 2^15, which the weights' fp16 terms need, a tile's sum of p o' within 2^24, and one of
+    // p within 2^110.  It moves when one of them would leave that (`heaviest` and `top`: the
+    // largest y + log2 max(s', |o'| / 32) and y that were met then), in the first tile and
+    // seldom after it, so that the common tile needs no maximum over lanes.
+    // Offsets count because rows of one value have scale 0, and then nothing but `top` held
+    // p down: p o' had no bound.  At |o'| <= 32 s', as rows of many values have it, they
+    // change nothing; beyond, weights below 2^10 lose nothing that p o' would not hide
+    // (fp16's last place, 2^-25, against 2^15).  In 2^30 tokens off stays within 2^50.
     float from[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
     float heaviest[C::kLaneRows], top[C::kLaneRows];
     float acc[C::kProducts][C::kCols][4];
@@ -548,7 +552,6 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
 #pragma unroll
                 for (int r = 0; r < C::kLaneRows; ++r) {
                     const float p = ex2_approx(x[r][k]);
-                    leaves |= p > 1.2e33f;                        // 2^110
                     sum[r] += p;
                     // (what is not seen may be anything)
                     if (decltype(in_tail)::value && (hidden >> (4 * r + k) & 1)) {
@@ -560,6 +563,9 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                     leaves |= !(fabsf(x[r][k]) <= 32768.f);
                 }
             }
+#pragma unroll
+            for (int r = 0; r < C::kLaneRows; ++r)
+                leaves |= !(sum[r] <= 0x1p110f) || !(fabsf(shift[r]) <= 0x1p24f);
             return leaves;
         };
         bool move = i == 0;
@@ -578,10 +584,12 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
                 float y = kNone, w = kNone;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float vs = fabsf(bf16_lo_to_f32(lds32(params + (kTile + 8 * k) * 4)));
+                    const uint32_t vp = lds32(params + (kTile + 8 * k) * 4);
+                    const float size = fmaxf(fabsf(bf16_lo_to_f32(vp)),
+                                             fabsf(bf16_hi_to_f32(vp)) * 0.03125f);
                     y = fmaxf(y, x[r][k]);
-                    if (!(hidden >> (4 * r + k) & 1) && vs > 0.f)
-                        w = fmaxf(w, x[r][k] + __log2f(vs));
+                    if (!(hidden >> (4 * r + k) & 1) && size > 0.f)
+                        w = fmaxf(w, x[r][k] + __log2f(size));
                 }
                 top[r] = fmaxf(top[r], group_max(y));
                 heaviest[r] = fmaxf(heaviest[r], group_max(w));
