@@ -408,7 +408,8 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
     // Offsets count because rows of one value have scale 0, and then nothing but `top` held
     // p down: p o' had no bound.  At |o'| <= 32 s', as rows of many values have it, they
     // change nothing; beyond, weights below 2^10 lose nothing that p o' would not hide
-    // (fp16's last place, 2^-25, against 2^15).  In 2^30 tokens off stays within 2^50.
+    // (fp16's last place, 2^-25, against 2^15).  In 2^30 tokens off stays within 2^50; l,
+    // which may get 2^110 a tile where all values are zero, is kept times 2^-16.
     float from[C::kLaneRows], l[C::kLaneRows], off[C::kLaneRows];
     float heaviest[C::kLaneRows], top[C::kLaneRows];
     float acc[C::kProducts][C::kCols][4];
@@ -613,7 +614,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         }
 #pragma unroll
         for (int r = 0; r < C::kLaneRows; ++r) {
-            l[r] += sum[r];
+            l[r] = fmaf(sum[r], 0x1p-16f, l[r]);
             off[r] += shift[r];
         }
         // ---- values: a tile's products by themselves, the small terms first, and added
@@ -707,9 +708,13 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         l[r] = group_sum(l[r]);
         off[r] = group_sum(off[r]);
         const bool some = l[r] > 0.f || l[r] != l[r];         // (a NaN score: a NaN row)
-        const float inv = some ? 1.f / l[r] : 0.f;
+        // the whole sum where fp32 holds it, as nearly always
+        const bool whole = !(l[r] > 0x1p100f);
+        const float sum = whole ? l[r] * 65536.f : l[r];
+        const float inv = some ? (whole ? 1.f : 0x1p-16f) / sum : 0.f;
         const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
-        if (g == 0) stats[warp * ROWS + row] = some ? from[r] + log2f(l[r]) : kNone;
+        if (g == 0)
+            stats[warp * ROWS + row] = some ? from[r] + (log2f(sum) + (whole ? 0.f : 16.f)) : kNone;
         // The lane's neighbouring elements of the row, four at a time.  Eight lanes store at
         // once, two of g and four of t: the rows' padding and the odd g's order of fours
         // put them in banks of their own (one at a time they would meet 16 to a bank).

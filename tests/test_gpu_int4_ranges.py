@@ -1,6 +1,8 @@
 """Decode over a 4-bit cache where its sums have least room: value rows that are constant
-(scale 0, the offset alone), offsets of any size, scores that rise."""
+(scale 0, the offset alone), offsets of any size, scores that rise, very long sequences."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -97,3 +99,31 @@ def test_constant_rows_keep_the_scores_bits(pkv, G, d):
     for kw in (dict(), dict(num_splits=1)):
         out = decode(pkv, c, **kw)[0].cpu().double().view(ro.shape)
         assert float((out - ro).abs().max()) <= 2.0 ** -20 + 2.0 ** -23
+
+
+@pytest.mark.parametrize("value", [0.0, 1.0])
+@pytest.mark.parametrize("G,d", [(4, 128), (16, 64)])
+def test_the_weights_of_many_million_tokens(pkv, G, d, value):
+    """9 million tokens (a few blocks, again and again), the same in all but the first tile of
+    each warp, whose scores are lower by 7.89 base-2 units.  The sum of weights has room for
+    all of them; lse by arithmetic."""
+    bs, blocks = 256, 36000
+    L = bs * blocks
+    zero = torch.zeros(2, 1, bs, d // 2, dtype=torch.uint8, device="cuda")
+    k_params = torch.zeros(2, 1, bs, 2, dtype=torch.bfloat16, device="cuda")
+    v_params = torch.zeros_like(k_params)
+    k_params[1, :, :, 1] = 5.46875
+    v_params[..., 1] = value
+    tables = torch.ones(1, blocks, dtype=torch.int32, device="cuda")
+    tables[0, ::blocks // 4] = 0                # a warp's first block, low
+    q = torch.full((1, G, d), 1.0 / d, device="cuda")
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    out, lse = pkv.paged_decode_attn_int4(q, zero, k_params, zero, v_params, tables, lens, 1.0,
+                                          num_splits=1)
+    want = math.log(4 * bs + (L - 4 * bs) * math.exp(5.46875))
+    assert pkv.device_status() == 0
+    # lse: 72,000 tiles' sums in a chain a lane, each off by half a step at most, 72,000 * 2^-24
+    # of the sum together; scores and the result itself round by 2^-20 and less
+    assert float((lse.double() - want).abs().max()) < 72000 * 2.0 ** -24 + 2.0 ** -18
+    # out: the same sums above and below the line
+    assert float((out.double() - value).abs().max()) <= 2.0 ** -18 * value
