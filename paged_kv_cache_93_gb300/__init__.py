@@ -690,9 +690,9 @@ def decode_workspace_size_int4(k_pool, k_params, v_pool, v_params, batch: int, n
                                flags: int = 0) -> int:
     """Workspace bytes of the decode calls over a 4-bit cache."""
     desc = cache_desc_int4(k_pool, k_params, v_pool, v_params)
-    return int(lib.pkv_decode_workspace_size_int4(ctypes.byref(desc), batch, tokens_per_seq,
-                                                  num_q_heads, max_blocks, _int32(num_splits),
-                                                  int(flags)))
+    return int(lib.pkv_decode_workspace_size_int4(
+        ctypes.byref(desc), _int32(batch), _int32(tokens_per_seq), _int32(num_q_heads),
+        _int32(max_blocks), _int32(num_splits), _int32(flags)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -706,7 +706,8 @@ def _attn_int4(name, call, q, k_pool, k_params, v_pool, v_params, block_tables, 
                num_splits, workspace, out, lse, flags, stream, multi):
     desc, B, T, Hq = _int4_args(q, k_pool, k_params, v_pool, v_params, block_tables, seq_lens,
                                 multi)
-    ref, mb, S, flags = ctypes.byref(desc), block_tables.shape[1], _int32(num_splits), int(flags)
+    ref, mb, S = ctypes.byref(desc), block_tables.shape[1], _int32(num_splits)
+    flags = _int32(flags)
     need = _int4_workspace(desc.num_blocks, desc.block_size, desc.num_kv_heads, desc.head_dim_k,
                            desc.head_dim_v, B, T, Hq, mb, S, flags, _device())
     ws_bytes = 0
@@ -790,7 +791,7 @@ def paged_decode_attn_partial_int4(q, k_pool, k_params, v_pool, v_params, block_
     _check("pkv_paged_decode_attn_partial_int4", lib.pkv_paged_decode_attn_partial_int4(
         ctypes.byref(desc), _ptr(q), B, Hq, _ptr(k_pool), _ptr(k_params), _ptr(v_pool),
         _ptr(v_params), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), float(scale),
-        S, _ptr(out_part), _ptr(lse_part), int(flags), _stream(stream)))
+        S, _ptr(out_part), _ptr(lse_part), _int32(flags), _stream(stream)))
     return out_part, lse_part
 
 
