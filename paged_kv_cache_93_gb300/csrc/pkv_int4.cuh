@@ -9,10 +9,11 @@
 //            held within 0..15
 // each operation rounded to binary32.  The offset is the row's own smallest value and
 // not a whole number of steps, so that rows far from zero keep their spread, and in
-// bf16 because the values are: from bf16 rows it is exact.  A scale rounded to bf16 is
-// off by 2^-9 at most, 0.03 of a step at the row's far end.  A spread below 15 * 2^-126
-// is stored as none (scale 0, codes 0).  A row with an element that is infinite or NaN,
-// or whose spread is no binary32, is stored as scale = offset = NaN and reads as NaN.
+// bf16 because the values are: from bf16 rows it is exact.  A scale rounded to bf16 (8
+// significant bits) is off by 2^-8 of itself at most, 0.06 of a step at the row's far end.
+// A spread below 15 * 2^-126 is stored as none (scale 0, codes 0).  A row with an element
+// that is infinite or NaN, or whose spread is no binary32, is stored as scale = offset =
+// NaN and reads as NaN.
 #pragma once
 
 #include <cstdint>
@@ -91,7 +92,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // whole number (ties to even) and leaves it in the low bits of the sum, whose other bits
 // are 0x4b000000; a word is made by multiplying by 16 and adding, and what those bits add
 // up to is taken off at the end.  (A code cannot pass 15: the scale is short of
-// range / 15 by 2^-9 of it at most.  In a row of NaN parameters max makes codes 0.)
+// range / 15 by 2^-8 of it at most, so that the largest quotient, 15.06 with binary32's
+// own roundings, is below 15.5.  In a row of NaN parameters max makes codes 0.)
 __device__ __forceinline__ uint32_t int4_codes8(const float (&x)[8], const Int4Scale &r) {
     const uint64_t less = pair_of(-r.offset, -r.offset), by = pair_of(r.inverse, r.inverse);
     const uint64_t magic = pair_of(8388608.f, 8388608.f);
