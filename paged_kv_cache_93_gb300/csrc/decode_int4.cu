@@ -708,13 +708,15 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
         l[r] = group_sum(l[r]);
         off[r] = group_sum(off[r]);
         const bool some = l[r] > 0.f || l[r] != l[r];         // (a NaN score: a NaN row)
-        // the whole sum where fp32 holds it, as nearly always
-        const bool whole = !(l[r] > 0x1p100f);
-        const float sum = whole ? l[r] * 65536.f : l[r];
-        const float inv = some ? (whole ? 1.f : 0x1p-16f) / sum : 0.f;
+        // (l is the sum times 2^-16: so are off and the products)
+        const float inv = some ? 1.f / l[r] : 0.f;
+        off[r] *= 0x1p-16f;
         const int row = C::kPacked ? t : 8 * (r >> 1) + 2 * t + (r & 1);
+        // the whole sum's logarithm; past what fp32 holds in two parts
         if (g == 0)
-            stats[warp * ROWS + row] = some ? from[r] + (log2f(sum) + (whole ? 0.f : 16.f)) : kNone;
+            stats[warp * ROWS + row] = !some               ? kNone
+                                       : l[r] <= 0x1p100f ? from[r] + log2f(l[r] * 65536.f)
+                                                          : from[r] + (log2f(l[r]) + 16.f);
         // The lane's neighbouring elements of the row, four at a time.  Eight lanes store at
         // once, two of g and four of t: the rows' padding and the odd g's order of fours
         // put them in banks of their own (one at a time they would meet 16 to a bank).
@@ -726,7 +728,7 @@ __device__ __forceinline__ void attend(const Int4DecodeArgs &a, uint8_t *smem, i
             const int p = i % C::kProducts, half = i / C::kProducts;
             const float z = C::kPacked ? acc[p][0][2 * half] + acc[p][0][2 * half + 1]
                                        : acc[p][r >> 1][2 * half + (r & 1)];
-            y[i] = fmaf(z, i & 1 ? kUp / 16.f : kUp, off[r]) * inv;
+            y[i] = fmaf(z, i & 1 ? kUp * 0x1p-20f : kUp * 0x1p-16f, off[r]) * inv;
         }
 #pragma unroll
         for (int c = 0; c < C::kProducts / 2; c += 2) {
