@@ -644,7 +644,12 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
  * A token that a row does not see reaches nothing of it, whatever its bits;
  * one that it sees and that reads as NaN makes the row NaN.  Scales of
  * magnitude below 2^-100 count as rounded to multiples of about 2^-125;
- * scales and offsets above 2^100 may overflow the sums.
+ * scales and offsets above 2^100 may overflow the sums.  Sums are fp32; the
+ * query, and the weights with the values' scales, enter the tensor cores'
+ * products with 22 significant bits (results within about 1e-6 of themselves;
+ * the CUDA-core kernel keeps 24).  With 16 query rows a KV head and more (4
+ * tokens at 4 heads a KV head) the products and not the cache's bytes decide:
+ * 8 x 32K tokens, 32 / 8 heads, 4 tokens each take 118 us, over an E4M3 cache 103.
  * num_splits = S > 0: S chunks of every sequence, merged; 0: the library's own
  * plan, which shares the tokens of all sequences evenly among the CTAs that
  * the device holds, from the lengths themselves.  Where that is not worth it

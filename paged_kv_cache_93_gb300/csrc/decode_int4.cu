@@ -17,9 +17,13 @@
 //    below: scores off by 1e-5 instead of 1e-6.)
 //  - Rows come by cp.async into a ring that belongs to one warp: 16-byte pieces may be
 //    placed anywhere, no barrier couples the warps, and a warp's tiles are on their way
-//    while it computes.  (Warp-level MMAs, because tcgen05 would want the codes expanded
-//    in shared memory first: with both operands' traffic 120 of the 128 bytes a clock
-//    that shared memory moves.)
+//    while it computes.
+//  - Warp-level MMAs, which take the codes from registers as they come.  tcgen05 takes
+//    operands from shared memory or tensor memory, where codes would be written first, as
+//    fp16 in four times their bytes (120 of the 128 bytes a clock that shared memory moves,
+//    with the reads).  As bytes they would be E4M3 numbers, code * 2^-9 exactly, in twice
+//    their bytes, with query and weights as terms of E4M3; that form is not built, and at 8
+//    and 16 rows, where the warps' products are the bound, it is what may be faster.
 //  - Scores: A = 16 tokens x 16 elements, B = the query rows.  The order of the elements
 //    within a product is free, so a lane takes D / 4 of a row in one load and the query
 //    is laid out to match.
@@ -37,7 +41,10 @@
 //  - Weights go from the scores' layout (token, row) to the values' (row, token) by
 //    movmatrix.
 // Query and weights are carried as two fp16 terms (22 bits): up to 4 rows as 8 columns
-// (row, term), else two products.  The query is scaled by a power of two so that its
+// (row, term), else two products.  A third term would be half as many products again; two
+// leave errors of 2e-7 to 1.6e-6 of the result against 64 bits (45 shapes; the same in fp32
+// throughout: 6e-8 to 3.3e-6), with ex2.approx (2^-22) for p.  One term would leave 2e-4
+// to 6e-4.  The query is scaled by a power of two so that its
 // largest element is 2^12..2^13; a row's weights p_j s'_j likewise, to 2^0..2^15, by a
 // factor that follows their running maximum -- a key that weighs much may have values
 // a millionth of the others'.
@@ -52,10 +59,10 @@
 // rows, the end of the last CTAs and the merge -- is 9 us at 4 rows and 18 at 16.
 //   16 of up to 128, 32 / 8 heads of 128        3.8 us (latency)
 //   8 x 32K, 32 / 8                            55.6    (0.77 of the copy rate)
-//   48 of up to 16K, 64 / 8                    96.6    (0.59)
-//   8 x 32K, 4 tokens each, 32 / 8            118.8    (0.36)
-//   1 x 200,000, 64 / 8                        59.0    (0.55)
-//   32 x 4,095, 2 tokens each, 32 / 8 of 64    30.5    (0.38)
+//   48 of up to 16K, 64 / 8                    96.1    (0.60)
+//   8 x 32K, 4 tokens each, 32 / 8            117.9    (0.36; over an E4M3 cache 103.2)
+//   1 x 200,000, 64 / 8                        58.5    (0.56)
+//   32 x 4,095, 2 tokens each, 32 / 8 of 64    30.8    (0.37)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -1194,10 +1201,11 @@ size_t int4_plan_workspace(const pkv_cache_desc &c, int32_t batch, int32_t num_q
     const int64_t ctas = int64_t(sm_count()) * kResident;
     const int64_t units = int64_t(batch) * c.num_kv_heads * row_tiles(c, num_q_heads, q_tokens);
     // Where a plan costs more than it evens out, a CTA a unit: sequences of a few steps at
-    // most (16 of up to 128 tokens: 3.8 us, planned 7.7); many units, which even out by
-    // themselves (1,024 of up to 8K tokens 126 us, planned 103; 1,280 of up to 2K 48.7 and
-    // 50.9; 2,048 of up to 2K 69.4 and 82); many sequences, which every CTA adds up (512 of
-    // up to 8K and one KV head 107 us, planned 89; 1,024 of them 172 and 198).
+    // most (16 of up to 128 tokens: 3.8 us, planned 7.1; the host knows the tables' width and
+    // not the lengths, so short sequences in wide tables are planned); many units, which even
+    // out by themselves (1,024 of up to 8K tokens 126 us, planned 103; 1,280 of up to 2K 48.7
+    // and 50.9; 2,048 of up to 2K 69.4 and 82); many sequences, which every CTA adds up (512
+    // of up to 8K and one KV head 107 us, planned 89; 1,024 of them 172 and 198).
     const int64_t tokens = int64_t(max_blocks) * c.block_size;
     if (tokens <= 4 * kStep || units > kManyUnits * ctas) return 0;
     const int rows = tile_rows(num_q_heads / c.num_kv_heads * q_tokens);

@@ -680,11 +680,12 @@ rope_append_warp_kernel(const RopeArgs a) {
 
 // The form of the 4-bit pools' other shapes: a CTA a token, a warp a row, which stays in
 // the warp's registers because its scale needs all of it (a lane holds C vectors of 8
-// elements: one up to 256 of them, which leaves registers for more CTAs, otherwise four).  VEC: vectors are rotated whole or not at all, with their pairs'
-// vector (half layout) loaded beside them; otherwise each rotary element loads its pair's
-// other element by itself, so that any rotary part runs.  Both loads hit the cache.
-// Bound: latency and instructions (4,999 tokens, 32 + 8 heads: of 96 61 us, of 128 with 72
-// rotary elements, one by one, 146; four vectors a lane for all 246 and 280).
+// elements: one up to 256 of them, which leaves registers for more CTAs, otherwise four).
+// VEC: vectors are rotated whole or not at all, with their pairs' vector (half layout)
+// loaded beside them; otherwise each rotary element loads its pair's other element by
+// itself, so that any rotary part runs.  Both loads hit the cache.
+// Bound: latency and instructions (4,999 tokens, 32 + 8 heads: of 96 64 us, of 128 with 72
+// rotary elements, one by one, 145; four vectors a lane for all 246 and 280).
 template <bool INTER, bool VEC, int C>
 __global__ void __launch_bounds__(kThreads) rope_append_int4_kernel(const RopeArgs a) {
     __shared__ float2 cs[2][kMaxPairs];          // (cos, sin) * amplitude, by token parity

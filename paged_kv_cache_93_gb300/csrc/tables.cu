@@ -10,12 +10,14 @@
 //
 // Bound: latency.  A step of 1,000 sequences and 40,000 tokens writes 0.8 MB; what
 // counts is one launch and few round trips (an extend and the trim that undoes it: 256
-// sequences of a token each 7.4 us, 1,000 of up to 512 each 13.5).  Each CTA takes the prefix sums of the whole
-// batch by itself, in its shared memory, and then fills its share of the rows, finding a
-// row's sequence by bisection.  Up to kRowsAlone rows one CTA does it all (and every trim,
-// whose few blocks are copied eight a thread at a time).  With more, what all CTAs read
-// -- the lengths and the stack's height -- is rewritten by the last CTA to finish, which a
-// counter beside the height tells; it wraps back to zero by itself.
+// sequences of a token each 7.5 us, 1,000 of up to 512 each 13.5).  Each CTA takes the
+// prefix sums of the whole batch by itself, in its shared memory, and then fills its share
+// of the rows, finding a row's sequence by bisection.  Up to kRowsAlone rows one CTA does
+// it all, and every trim, whose blocks are copied eight a thread at a time: few, as a rule
+// (256 sequences of 32K tokens cut to none, 524,288 blocks, take that CTA 309 us).  With
+// more rows, what all CTAs read -- the lengths and the stack's height -- is rewritten by
+// the last CTA to finish, which a counter beside the height tells; it wraps back to zero by
+// itself.
 #include <cuda_runtime.h>
 
 #include <algorithm>
