@@ -647,7 +647,10 @@ int pkv_paged_decode_attn_multi_e4m3(const pkv_cache_desc *cache, const float *q
  * scales and offsets above 2^100 may overflow the sums.  Sums are fp32; the
  * query, and the weights with the values' scales, enter the tensor cores'
  * products with 22 significant bits (results within about 1e-6 of themselves;
- * the CUDA-core kernel keeps 24).  With 16 query rows a KV head and more (4
+ * the CUDA-core kernel keeps 24).  There a softmax weight is held together with
+ * its value's size: where a row sees only values (scales and offsets) below
+ * 2^-20 or above 2^20, zeros among them, its weights and lse are within 2^-17
+ * instead.  With 16 query rows a KV head and more (4
  * tokens at 4 heads a KV head) the products and not the cache's bytes decide:
  * 8 x 32K tokens, 32 / 8 heads, 4 tokens each take 118 us, over an E4M3 cache 103.
  * num_splits = S > 0: S chunks of every sequence, merged; 0: the library's own
