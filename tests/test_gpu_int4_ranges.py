@@ -127,3 +127,21 @@ def test_the_weights_of_many_million_tokens(pkv, G, d, value):
     assert float((lse.double() - want).abs().max()) < 72000 * 2.0 ** -24 + 2.0 ** -18
     # out: the same sums above and below the line
     assert float((out.double() - value).abs().max()) <= 2.0 ** -18 * value
+
+
+@pytest.mark.parametrize("G,T,d", [(4, 1, 128), (8, 1, 64), (4, 4, 128)])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -90, 2.0 ** -30, 2.0 ** 30, 2.0 ** 90])
+def test_values_of_unusual_sizes(pkv, size, G, T, d):
+    """Weights and lse within 2^-17 where all values are tiny, huge or zero; and what the
+    products' 22 bits and the scores' sums add, as elsewhere (2^-18 each)."""
+    c = _int4.make(56, [300, 5, 40], 2 * G, 2, d, d, 16, T)
+    c.v_params = (c.v_params.float() * size).to(torch.bfloat16)
+    c.q.mul_(0.1)
+    ro, rl, tol, _ = _int4.attend(c)
+    for kw in (dict(), dict(num_splits=2)):
+        out, lse = decode(pkv, c, **kw)
+        out, lse = out.cpu().double().view(ro.shape), lse.cpu().double().view(rl.shape)
+        # (tol is 2^-18 of the sum of weights times values' sizes, and more)
+        assert torch.all((out - ro).abs() <= 3 * tol)
+        assert float((lse - rl).abs().max()) <= 2.0 ** -17 + 2.0 ** -18
+    assert pkv.device_status() == 0
